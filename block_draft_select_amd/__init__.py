@@ -19,11 +19,13 @@ F32 = 0
 BF16 = 1
 K_MAX, L_MAX, R_MAX, V_MAX, CHUNK = 16, 16, 256, 2097152, 4096
 STATIC_SCRATCH_BYTES = 8 << 20
+ROWS_MAX, DISTILL_K_MAX = 4194304, 1024
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = 0, 1, 2, 3, 4
 
 KERNELS = ("topk", "gate", "scores", "trace", "stats", "finalize", "cycle_stream", "cycle_scores",
-           "cycle_finalize", "conv2tap", "trace_viterbi", "topk_merge", "shard_stats", "shard_finalize")
+           "cycle_finalize", "conv2tap", "trace_viterbi", "topk_merge", "shard_stats", "shard_finalize", "sample",
+           "filter", "distill", "distill_grad")
 
 
 class dflash_dims(ctypes.Structure):
@@ -32,6 +34,15 @@ class dflash_dims(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class dflash_rows(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("stride", ctypes.c_int64), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class dflash_filters(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("group", ctypes.c_int32)]
 
 
 class DFlashError(RuntimeError):
@@ -45,7 +56,8 @@ def _load():
         raise ImportError(f"{LIB_PATH} is missing: build it with `python block_draft_select_amd/build.py`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, U64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64, ctypes.c_size_t
-    D = ctypes.POINTER(dflash_dims)
+    I64, F64 = ctypes.c_int64, ctypes.c_double
+    D, W, F = ctypes.POINTER(dflash_dims), ctypes.POINTER(dflash_rows), ctypes.POINTER(dflash_filters)
     sig = {
         "dflash_abi_version": (I32, []),
         "dflash_status_string": (ctypes.c_char_p, [I32]),
@@ -66,6 +78,11 @@ def _load():
         "dflash_shard_stats": (I32, [D, I32, ctypes.POINTER(I32), I32, P, P, P, P]),
         "dflash_verify_shards": (I32, [D, I32, ctypes.POINTER(I32), ctypes.POINTER(P), P, P, P, P, P, P, U64, P, P,
                                        P]),
+        "dflash_rows_workspace_bytes": (I32, [W, ctypes.POINTER(SZ)]),
+        "dflash_sample": (I32, [W, P, F, P, P, P, P, P, SZ, P]),
+        "dflash_filter": (I32, [W, P, F, ctypes.c_float, P, I64, P, P, SZ, P]),
+        "dflash_distill": (I32, [W, P, I32, F64, P, P, P, P, P, P, P, P, SZ, P]),
+        "dflash_distill_grad": (I32, [W, P, I32, F64, P, P, P, P, P, P, P, P, I64, P]),
         "dflash_read_probe": (I32, [P, SZ, P, P]),
         "dflash_copy_probe": (I32, [P, P, SZ, P]),
         "dflash_kernel_name": (ctypes.c_char_p, [I32]),
@@ -299,6 +316,158 @@ def dflash_conv2tap(d, x, x0, Wt, y, stream=None):
     _check(lib.dflash_conv2tap(ctypes.byref(d), _ptr(x, "x", pt, R * d.hidden), _ptr(x0, "x0", pt, d.B * d.hidden),
                                _ptr(Wt, "Wt", pt, 2 * d.hidden * d.hidden),
                                _ptr(y, "y", torch.float32, R * d.hidden), _stream(stream)))
+
+
+# ------------------------------------------------------------------ rows of vocabulary logits
+
+_ROWS_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def rows(t):
+    """A ``dflash_rows`` value describing a tensor of logits [..., V]: the
+    leading dimensions must step evenly (any stride), the last one by 1."""
+    if t.dtype not in _ROWS_DTYPE:
+        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    if t.dim() < 1:
+        raise ValueError("logits must have at least one dimension")
+    V, R, stride = t.shape[-1], 1, None
+    if V > 1 and t.stride(-1) != 1:
+        raise ValueError("the elements of a logit row must be adjacent")
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * R and R != 0:
+            raise ValueError("the rows of the logits must step evenly")
+        R *= n
+    return dflash_rows(R, V if stride is None else stride, V, _ROWS_DTYPE[t.dtype])
+
+
+def rows_workspace_bytes(r):
+    n = ctypes.c_size_t(0)
+    _check(lib.dflash_rows_workspace_bytes(ctypes.byref(r), ctypes.byref(n)))
+    return n.value
+
+
+def rows_workspace(r, device="cuda"):
+    """A workspace tensor large enough for any operator on these rows."""
+    return torch.empty(max(rows_workspace_bytes(r), 16), dtype=torch.uint8, device=device)
+
+
+def _row_tensor(t, name, r, device, stride=None):
+    """Pointer of a tensor of rows ``r`` (``stride``: None takes its own, and
+    the row stride is returned with it)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    own = rows(t)
+    if (own.R, own.V, own.dtype) != (r.R, r.V, r.dtype):
+        raise ValueError(f"{name} must hold {r.R} rows of {r.V} logits of the rows' dtype")
+    if stride is not None and own.R > 1 and own.stride != stride:
+        raise ValueError(f"{name} must have the row stride {stride}, got {own.stride}")
+    _on(t, name, device)
+    return ctypes.c_void_p(t.data_ptr()), own.stride
+
+
+def _on(t, name, device):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the rows are on {device}")
+
+
+def _vec(t, name, dtype, numel, device, optional=False):
+    p = _ptr(t, name, dtype, numel, optional)
+    if t is not None:
+        _on(t, name, device)
+    return p
+
+
+def _stream_on(device, stream):
+    """The stream to launch on: the given one, or the current one of the tensors' device."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the rows are on {device}")
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _filters(r, device, T, top_k, top_p, min_p, group):
+    n = -(-r.R // group) if group >= 1 else 0
+    return dflash_filters(_vec(T, "T", torch.float32, n, device, True), _vec(top_k, "top_k", torch.int32, n, device, True),
+                          _vec(top_p, "top_p", torch.float32, n, device, True),
+                          _vec(min_p, "min_p", torch.float32, n, device, True), int(group))
+
+
+def dflash_sample(r, Z, u, token, ws, T=None, top_k=None, top_p=None, min_p=None, group=1, prob=None, kept=None,
+                  stream=None):
+    """One token per row of ``Z`` (described by ``r = rows(Z)``) into
+    ``token``, by the uniforms ``u`` [R] (float64) under the settings T,
+    top_k, top_p, min_p (one value per ``group`` rows; None: off)."""
+    dev = Z.device
+    f = _filters(r, dev, T, top_k, top_p, min_p, group)
+    with torch.cuda.device(dev):
+        _check(lib.dflash_sample(ctypes.byref(r), _row_tensor(Z, "Z", r, dev, r.stride)[0], ctypes.byref(f),
+                                 _vec(u, "u", torch.float64, r.R, dev), _vec(token, "token", torch.int32, r.R, dev),
+                                 _vec(prob, "prob", torch.float32, r.R, dev, True),
+                                 _vec(kept, "kept", torch.int32, r.R, dev, True), _vec(ws, "ws", torch.uint8, None, dev),
+                                 ws.numel(), _stream_on(dev, stream)))
+
+
+def dflash_filter(r, Z, out, ws, fill=None, T=None, top_k=None, top_p=None, min_p=None, group=1, kept=None, stream=None):
+    """``out`` = the rows ``Z`` with the tokens that the settings remove set
+    to ``fill`` (None: the lowest finite value of Z's type); ``out`` may be
+    ``Z``."""
+    dev = Z.device
+    if fill is None:
+        fill = torch.finfo(Z.dtype).min
+    f = _filters(r, dev, T, top_k, top_p, min_p, group)
+    po, so = _row_tensor(out, "out", r, dev)
+    with torch.cuda.device(dev):
+        _check(lib.dflash_filter(ctypes.byref(r), _row_tensor(Z, "Z", r, dev, r.stride)[0], ctypes.byref(f), float(fill),
+                                 po, so, _vec(kept, "kept", torch.int32, r.R, dev, True),
+                                 _vec(ws, "ws", torch.uint8, None, dev), ws.numel(), _stream_on(dev, stream)))
+
+
+def _distill_list(r, t_idx, t_logit, device):
+    if t_idx is None and t_logit is None:
+        return 0, None, None
+    if t_idx is None or t_logit is None or t_idx.shape != t_logit.shape:
+        raise ValueError("t_idx and t_logit must be given together, with one shape [R, K]")
+    K = t_idx.shape[-1]
+    return K, _vec(t_idx, "t_idx", torch.int32, r.R * K, device), _vec(t_logit, "t_logit", torch.float32, r.R * K, device)
+
+
+def dflash_distill(r, S, t_idx, t_logit, loss, lse, ws, tau=1.0, t_lse=None, weight=None, lse_rest=None, stream=None):
+    """The loss of each student row against the teacher's listed logits
+    (``t_idx``, ``t_logit`` [R, K]; both None: K = 0, ``lse`` alone)."""
+    dev = S.device
+    K, pi, pt = _distill_list(r, t_idx, t_logit, dev)
+    with torch.cuda.device(dev):
+        _check(lib.dflash_distill(ctypes.byref(r), _row_tensor(S, "S", r, dev, r.stride)[0], K, float(tau), pi, pt,
+                                  _vec(t_lse, "t_lse", torch.float64, r.R, dev, True),
+                                  _vec(weight, "weight", torch.float32, r.R, dev, True),
+                                  _vec(loss, "loss", torch.float32, r.R, dev, True),
+                                  _vec(lse, "lse", torch.float64, r.R, dev),
+                                  _vec(lse_rest, "lse_rest", torch.float64, r.R, dev, True),
+                                  _vec(ws, "ws", torch.uint8, None, dev), ws.numel(), _stream_on(dev, stream)))
+
+
+def dflash_distill_grad(r, S, t_idx, t_logit, lse, dS, tau=1.0, t_lse=None, weight=None, grad_loss=None, lse_rest=None,
+                        stream=None):
+    """The gradient of dflash_distill's loss with respect to ``S`` into
+    ``dS`` (may be ``S``)."""
+    dev = S.device
+    K, pi, pt = _distill_list(r, t_idx, t_logit, dev)
+    pd, sd = _row_tensor(dS, "dS", r, dev)
+    with torch.cuda.device(dev):
+        _check(lib.dflash_distill_grad(ctypes.byref(r), _row_tensor(S, "S", r, dev, r.stride)[0], K, float(tau), pi, pt,
+                                       _vec(t_lse, "t_lse", torch.float64, r.R, dev, True),
+                                       _vec(weight, "weight", torch.float32, r.R, dev, True),
+                                       _vec(grad_loss, "grad_loss", torch.float32, r.R, dev, True),
+                                       _vec(lse, "lse", torch.float64, r.R, dev),
+                                       _vec(lse_rest, "lse_rest", torch.float64, r.R, dev, True), pd, sd,
+                                       _stream_on(dev, stream)))
 
 
 def dflash_workspace_init(ws, stream=None):

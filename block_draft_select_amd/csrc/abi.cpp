@@ -3,7 +3,9 @@
 // Nothing here allocates device memory; all work goes to the caller's stream.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdlib>
+#include <cstring>
 #include <mutex>
 #include <new>
 #include <string>
@@ -94,8 +96,8 @@ Profiler& prof() {
 
 // Run `f` (which enqueues on `st`), timed when the timer is on.  Entry
 // points of a single launch hand the events to that launch, which records
-// them at the kernel's own start and end; the two-launch top-K entry point
-// brackets its launches with events on the stream.
+// them at the kernel's own start and end; the entry points of several
+// launches under one name bracket them with events on the stream.
 template <class F>
 hipError_t timed(int kernel, hipStream_t st, F f) {
   Profiler& P = prof();
@@ -107,7 +109,8 @@ hipError_t timed(int kernel, hipStream_t st, F f) {
       b = P.take();
     }
   }
-  const bool on_stream = kernel == DFLASH_KERNEL_TOPK;
+  const bool on_stream = kernel == DFLASH_KERNEL_TOPK || kernel == DFLASH_KERNEL_SAMPLE ||
+                         kernel == DFLASH_KERNEL_FILTER || kernel == DFLASH_KERNEL_DISTILL;
   if (a && b) {
     if (on_stream) {
       hipEventRecord(a, st);
@@ -203,7 +206,128 @@ WsLayout ws_layout(const dflash_dims& d) {
   return w;
 }
 
+// 16-byte slots a row can take, at any alignment
+static int row_slots(const dflash_rows& r) {
+  const int ve = r.dtype == DFLASH_BF16 ? 8 : 4;
+  return (r.V + ve - 1 + ve - 1) / ve;
+}
+
+// Slots per thread: the most whose grid still has 1024 blocks (four per CU),
+// so that few rows spread over the GPU and many amortise their bins.
+SamplePlan sample_plan(const dflash_rows& r) {
+  SamplePlan p{};
+  const int slots = row_slots(r);
+  for (p.loads = kSampleMaxLoads;; p.loads /= 2) {
+    p.n_seg = (slots + kSampleThreads * p.loads - 1) / (kSampleThreads * p.loads);
+    if (p.loads == 1 || r.R * p.n_seg >= 1024) break;
+  }
+  p.batch = 4096 / p.n_seg > 1 ? 4096 / p.n_seg : 1;
+  const size_t rows = (size_t)(r.R < p.batch ? r.R : p.batch);
+  p.parts = 0;
+  p.cuts = align256(rows * p.n_seg * sizeof(SamplePart));
+  p.total = align256(p.cuts + rows * sizeof(uint64_t));
+  return p;
+}
+
+DistillPlan distill_plan(const dflash_rows& r) {
+  DistillPlan p{};
+  const int slots = row_slots(r);
+  for (p.loads = 8;; p.loads = 2) {
+    p.n_seg = (slots + kDistillThreads * p.loads - 1) / (kDistillThreads * p.loads);
+    if (p.loads == 2 || r.R * p.n_seg >= 2048) break;
+  }
+  p.total = align256((size_t)r.R * p.n_seg * sizeof(DistillPart));
+  return p;
+}
+
 }  // namespace dfk
+
+namespace {
+
+dflash_status check_rows(const dflash_rows* r) {
+  if (!r) return fail(DFLASH_ERR_INVALID_ARG, "rows is NULL");
+  if (r->R < 0) return fail(DFLASH_ERR_INVALID_ARG, "R must not be negative");
+  if (r->V < 1) return fail(DFLASH_ERR_INVALID_ARG, "V must be >= 1");
+  if (r->dtype != DFLASH_F32 && r->dtype != DFLASH_BF16) return fail(DFLASH_ERR_INVALID_ARG, "unknown dtype");
+  if (r->R > 1 && r->stride < r->V) return fail(DFLASH_ERR_INVALID_ARG, "stride must be at least V");
+  if (r->R > DFLASH_ROWS_MAX) return fail(DFLASH_ERR_UNSUPPORTED, "R above DFLASH_ROWS_MAX");
+  if (r->V > DFLASH_V_MAX) return fail(DFLASH_ERR_UNSUPPORTED, "V above DFLASH_V_MAX");
+  if (r->stride > (INT64_C(1) << 40)) return fail(DFLASH_ERR_UNSUPPORTED, "stride above 2^40 elements");
+  // a launch holds fewer than 2^32 threads
+  if (r->R * dfk::distill_plan(*r).n_seg >= (INT64_C(1) << 32) / dfk::kDistillThreads)
+    return fail(DFLASH_ERR_UNSUPPORTED, "R * V too large for one launch");
+  return DFLASH_OK;
+}
+
+dflash_status check_elem(const dflash_rows& r, const void* p, const char* name) {
+  if (!p) return fail(DFLASH_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % logit_bytes(r.dtype))
+    return fail(DFLASH_ERR_INVALID_ARG, std::string(name) + " is not aligned to its elements");
+  return DFLASH_OK;
+}
+
+// a second tensor of the same rows: the same address and stride, or no overlap
+dflash_status check_out(const dflash_rows& r, const void* in, const void* out, int64_t stride, const char* name) {
+  if (dflash_status s = check_elem(r, out, name)) return s;
+  if (r.R > 1 && stride < r.V) return fail(DFLASH_ERR_INVALID_ARG, std::string(name) + "'s stride must be at least V");
+  if (stride > (INT64_C(1) << 40)) return fail(DFLASH_ERR_UNSUPPORTED, std::string(name) + "'s stride is above 2^40 elements");
+  const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t es = logit_bytes(r.dtype);
+  if (a == b && (r.R <= 1 || stride == r.stride)) return DFLASH_OK;
+  const uintptr_t na = ((uintptr_t)(r.R - 1) * (r.R > 1 ? r.stride : 0) + r.V) * es;
+  const uintptr_t nb = ((uintptr_t)(r.R - 1) * (r.R > 1 ? stride : 0) + r.V) * es;
+  if (a < b + nb && b < a + na) {
+    // rows side by side in one allocation do not meet if the strides agree
+    // and one tensor's rows lie in the other's gaps
+    const uintptr_t row = (uintptr_t)r.stride * es, d = (a < b ? b - a : a - b) % row, v = (uintptr_t)r.V * es;
+    if (r.R <= 1 || stride != r.stride || d < v || row - d < v)
+      return fail(DFLASH_ERR_INVALID_ARG, std::string(name) + " overlaps its input (equal address and stride are allowed)");
+  }
+  return DFLASH_OK;
+}
+
+dflash_status check_rows_ws(size_t need, void* ws, size_t ws_bytes) {
+  if (!ws) return fail(DFLASH_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned16(ws)) return fail(DFLASH_ERR_WORKSPACE, "workspace is not 16-byte aligned");
+  if (ws_bytes < need) return fail(DFLASH_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+  return DFLASH_OK;
+}
+
+dflash_status check_filters(const dflash_filters* f) {
+  if (!f) return fail(DFLASH_ERR_INVALID_ARG, "filters is NULL");
+  if (f->group < 1) return fail(DFLASH_ERR_INVALID_ARG, "filters' group must be >= 1");
+  return DFLASH_OK;
+}
+
+dfk::SampleArgs sample_args(const dflash_rows& r, const void* Z, const dflash_filters& f) {
+  return dfk::SampleArgs{Z, r.R, r.stride, r.V, f.group, f.T, f.top_k, f.top_p, f.min_p};
+}
+
+dflash_status check_distill(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
+                            const float* t_logit, const double* t_lse, const double* lse, const double* lse_rest) {
+  if (K < 0 || K > DFLASH_DISTILL_K_MAX) return fail(DFLASH_ERR_INVALID_ARG, "K must be in [0, DFLASH_DISTILL_K_MAX]");
+  if (!(tau > 0.0) || tau > 1e30 || tau < 1e-30) return fail(DFLASH_ERR_INVALID_ARG, "tau must lie in [1e-30, 1e30]");
+  if (r->R == 0) return DFLASH_OK;
+  if (dflash_status s = check_elem(*r, S, "S")) return s;
+  if (K > 0)
+    if (dflash_status s = check_ptrs({{t_idx, "t_idx", false}, {t_logit, "t_logit", false}})) return s;
+  if (!lse) return fail(DFLASH_ERR_INVALID_ARG, "lse is NULL");
+  if ((t_lse != nullptr) != (lse_rest != nullptr))
+    return fail(DFLASH_ERR_INVALID_ARG, "lse_rest must be given exactly if t_lse is");
+  return DFLASH_OK;
+}
+
+// the fill value in the element type (bf16: nearest even)
+uint32_t fill_bits(int32_t dtype, float v) {
+  uint32_t u;
+  static_assert(sizeof(u) == sizeof(v), "");
+  std::memcpy(&u, &v, 4);
+  if (dtype == DFLASH_F32) return u;
+  if (v != v) return 0x7FC0u;
+  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -563,6 +687,101 @@ dflash_status dflash_conv2tap(const dflash_dims* d, const void* x, const void* x
   }
 }
 
+dflash_status dflash_rows_workspace_bytes(const dflash_rows* r, size_t* bytes) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_rows(r)) return s;
+    if (!bytes) return fail(DFLASH_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = r->R ? std::max(dfk::sample_plan(*r).total, dfk::distill_plan(*r).total) : 0;
+    return DFLASH_OK;
+  } catch (...) {
+    return fail(DFLASH_ERR_INVALID_ARG, "internal error");
+  }
+}
+
+dflash_status dflash_sample(const dflash_rows* r, const void* Z, const dflash_filters* f, const double* u, int32_t* token,
+                            float* prob_opt, int32_t* kept_opt, void* ws, size_t ws_bytes, void* stream) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_rows(r)) return s;
+    if (dflash_status s = check_filters(f)) return s;
+    if (r->R == 0) return DFLASH_OK;
+    if (dflash_status s = check_elem(*r, Z, "Z")) return s;
+    if (dflash_status s = check_ptrs({{u, "u", false}, {token, "token", false}})) return s;
+    const dfk::SamplePlan p = dfk::sample_plan(*r);
+    if (dflash_status s = check_rows_ws(p.total, ws, ws_bytes)) return s;
+    hipStream_t st = (hipStream_t)stream;
+    const dfk::SampleOut o{u, token, prob_opt, kept_opt, nullptr, 0, 0};
+    return hip_status(timed(DFLASH_KERNEL_SAMPLE, st, [&] {
+      return dfk::launch_sample(r->dtype, sample_args(*r, Z, *f), o, static_cast<char*>(ws), p, st);
+    }), "sample launch");
+  } catch (...) {
+    return fail(DFLASH_ERR_HIP, "internal error");
+  }
+}
+
+dflash_status dflash_filter(const dflash_rows* r, const void* Z, const dflash_filters* f, float fill, void* out,
+                            int64_t out_stride, int32_t* kept_opt, void* ws, size_t ws_bytes, void* stream) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_rows(r)) return s;
+    if (dflash_status s = check_filters(f)) return s;
+    if (r->R == 0) return DFLASH_OK;
+    if (dflash_status s = check_elem(*r, Z, "Z")) return s;
+    if (dflash_status s = check_out(*r, Z, out, out_stride, "out")) return s;
+    const dfk::SamplePlan p = dfk::sample_plan(*r);
+    if (dflash_status s = check_rows_ws(p.total, ws, ws_bytes)) return s;
+    hipStream_t st = (hipStream_t)stream;
+    const dfk::SampleOut o{nullptr, nullptr, nullptr, kept_opt, out, out_stride, fill_bits(r->dtype, fill)};
+    return hip_status(timed(DFLASH_KERNEL_FILTER, st, [&] {
+      return dfk::launch_sample(r->dtype, sample_args(*r, Z, *f), o, static_cast<char*>(ws), p, st);
+    }), "filter launch");
+  } catch (...) {
+    return fail(DFLASH_ERR_HIP, "internal error");
+  }
+}
+
+dflash_status dflash_distill(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
+                             const float* t_logit, const double* t_lse_opt, const float* weight_opt, float* loss_opt,
+                             double* lse, double* lse_rest_opt, void* ws, size_t ws_bytes, void* stream) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_rows(r)) return s;
+    if (dflash_status s = check_distill(r, S, K, tau, t_idx, t_logit, t_lse_opt, lse, lse_rest_opt)) return s;
+    if (r->R == 0) return DFLASH_OK;
+    const dfk::DistillPlan p = dfk::distill_plan(*r);
+    if (dflash_status s = check_rows_ws(p.total, ws, ws_bytes)) return s;
+    hipStream_t st = (hipStream_t)stream;
+    const dfk::DistillArgs a{S, r->R, r->stride, r->V, K, tau, t_idx, t_logit, t_lse_opt, weight_opt};
+    return hip_status(timed(DFLASH_KERNEL_DISTILL, st, [&] {
+      return dfk::launch_distill(r->dtype, a, loss_opt, lse, lse_rest_opt, static_cast<char*>(ws), p, st);
+    }), "distill launch");
+  } catch (...) {
+    return fail(DFLASH_ERR_HIP, "internal error");
+  }
+}
+
+dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
+                                  const float* t_logit, const double* t_lse_opt, const float* weight_opt,
+                                  const float* grad_loss_opt, const double* lse, const double* lse_rest_opt, void* dS,
+                                  int64_t ds_stride, void* stream) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_rows(r)) return s;
+    if (dflash_status s = check_distill(r, S, K, tau, t_idx, t_logit, t_lse_opt, lse, lse_rest_opt)) return s;
+    if (r->R == 0) return DFLASH_OK;
+    if (dflash_status s = check_out(*r, S, dS, ds_stride, "dS")) return s;
+    hipStream_t st = (hipStream_t)stream;
+    const dfk::DistillArgs a{S, r->R, r->stride, r->V, K, tau, t_idx, t_logit, t_lse_opt, weight_opt};
+    return hip_status(timed(DFLASH_KERNEL_DISTILL_GRAD, st, [&] {
+      return dfk::launch_distill_grad(r->dtype, a, grad_loss_opt, lse, lse_rest_opt, dS, ds_stride, dfk::distill_plan(*r),
+                                      st);
+    }), "distill gradient launch");
+  } catch (...) {
+    return fail(DFLASH_ERR_HIP, "internal error");
+  }
+}
+
 dflash_status dflash_read_probe(const void* buf, size_t bytes, uint32_t* sink, void* stream) {
   try {
     g_err.clear();
@@ -589,7 +808,8 @@ const char* dflash_kernel_name(int32_t kernel) {
   static const char* names[DFLASH_KERNEL_COUNT] = {"topk", "gate", "scores", "trace", "stats", "finalize",
                                                    "cycle_stream", "cycle_scores", "cycle_finalize", "conv2tap",
                                                    "trace_viterbi", "topk_merge", "shard_stats",
-                                                   "shard_finalize"};
+                                                   "shard_finalize", "sample", "filter", "distill",
+                                                   "distill_grad"};
   return (kernel >= 0 && kernel < DFLASH_KERNEL_COUNT) ? names[kernel] : "";
 }
 

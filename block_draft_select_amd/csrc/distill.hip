@@ -1,0 +1,416 @@
+// dflash_distill and dflash_distill_grad: the divergence of a student's row
+// of logits from a teacher known by its K top logits, and its gradient.
+//
+// With x_j = s_j / tau, lse = log sum_j e^x_j, and the teacher's listed
+// probabilities p_k = e^(t_k / tau - c) (c: the teacher's log-sum-exp over its
+// whole vocabulary if given, else over the list),
+//   D = sum_k p_k (log p_k - x_{i_k} + lse)
+//     + p_rest (log p_rest - lse_rest + lse)     p_rest = 1 - sum p_k,
+// where the second line (teacher's log-sum-exp given) treats all unlisted
+// tokens as one class and lse_rest is their log-sum-exp.  It is summed over
+// the unlisted tokens directly, never as total minus listed: a student that
+// puts nearly everything on the list leaves a rest far below the total's
+// rounding.  The gradient, with A = sum p + p_rest, is
+//   dD/dx_j = A e^(x_j - lse) - p_j                      listed,
+//           = e^(x_j - lse_rest) (A e^(lse_rest - lse) - p_rest)  unlisted,
+// which stays finite for any gap between the two sums.
+//
+// distill_sum_kernel streams a row segment once into (maximum, sum);
+// distill_loss_kernel, one block per row, joins the segments and the list.
+// distill_grad_kernel recomputes the exponentials from lse (one read, one
+// write), treats every token as unlisted, then rewrites the listed ones of its
+// segment after a barrier.
+//
+// Sums are fp64: lse is returned in fp64 and the two passes must agree.
+#include "rows_blocks.hpp"
+
+namespace dfk {
+
+namespace {
+
+constexpr int kThreads = kDistillThreads;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kMaskWords = kThreads * 8 * 8 / 32;  // one bit per element of a segment
+constexpr double kLog2e64 = 1.4426950408889634;
+constexpr double kLn2 = 0.6931471805599453;
+
+// 2^x for x <= 0.5: the integer part by ldexp, the rest (|f| <= 1/2) by the
+// Taylor series of e^(f ln 2) to degree 9 (truncation below 7e-12)
+__device__ __forceinline__ double exp2_sum(double x) {
+  x = fmax(x, -1100.0);
+  const double n = rint(x), f = (x - n) * kLn2;
+  double p = 1.0 / 362880.0;
+  p = fma(p, f, 1.0 / 40320.0);
+  p = fma(p, f, 1.0 / 5040.0);
+  p = fma(p, f, 1.0 / 720.0);
+  p = fma(p, f, 1.0 / 120.0);
+  p = fma(p, f, 1.0 / 24.0);
+  p = fma(p, f, 1.0 / 6.0);
+  p = fma(p, f, 0.5);
+  p = fma(p, f, 1.0);
+  p = fma(p, f, 1.0);
+  return ldexp(p, (int)n);
+}
+
+struct Red {
+  double d[kWaves];
+};
+
+__device__ __forceinline__ double block_sum(Red& s, double v) {
+  v = wave_sum_f64(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s.d[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double r = s.d[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) r += s.d[w];
+  return r;
+}
+
+__device__ __forceinline__ double block_max(Red& s, double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s.d[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double r = s.d[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) r = fmax(r, s.d[w]);
+  return r;
+}
+
+// a list entry counts unless its index lies outside the vocabulary (padding)
+__device__ __forceinline__ bool listed(const DistillArgs& a, int64_t row, int k, int& idx) {
+  idx = a.t_idx[row * a.K + k];
+  return idx >= 0 && idx < a.V;
+}
+
+// the teacher's normaliser c (natural log); -inf: the teacher's row is empty
+__device__ __forceinline__ double teacher_lse(Red& red, const DistillArgs& a, int64_t row) {
+  if (a.t_lse) {
+    const double c = a.t_lse[row];
+    return c < INFINITY ? c : (c != c ? c : -INFINITY);
+  }
+  double m = -INFINITY;
+  int idx;
+  for (int k = threadIdx.x; k < a.K; k += kThreads)
+    if (listed(a, row, k, idx)) {
+      const double t = (double)a.t_logit[row * a.K + k] / a.tau;
+      m = t != t ? INFINITY : fmax(m, t);
+    }
+  m = block_max(red, m);
+  if (m == -INFINITY) return m;
+  double s = 0.0;
+  for (int k = threadIdx.x; k < a.K; k += kThreads)
+    if (listed(a, row, k, idx)) s += exp((double)a.t_logit[row * a.K + k] / a.tau - m);
+  return m + log(block_sum(red, s));
+}
+
+// ---------------------------------------------------------------- forward
+
+template <int DT, int NL, bool REST>
+__global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, int n_seg, DistillPart* __restrict__ parts) {
+  constexpr int VE = RowType<DT>::VE;
+  __shared__ Red red;
+  __shared__ uint32_t mask[REST ? kMaskWords : 1];
+  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
+  const int64_t row = blockIdx.x / n_seg;
+  if (a.weight && a.weight[row] == 0.0f) return;
+  const RowRef<DT> z(a.S, row, a.stride, a.V);
+  const int s0 = seg * (kThreads * NL);
+  Slot x[NL];
+#pragma unroll
+  for (int l = 0; l < NL; ++l) x[l] = z.template load<true>(s0 + l * kThreads + tid);
+  if constexpr (REST) {
+    for (int i = tid; i < kMaskWords; i += kThreads) mask[i] = 0;
+    __syncthreads();
+    const int e0 = z.first(s0);
+    int idx;
+    for (int k = tid; k < a.K; k += kThreads)
+      if (listed(a, row, k, idx) && idx >= e0 && idx < e0 + kThreads * NL * VE)
+        atomicOr(&mask[(idx - e0) >> 5], 1u << ((idx - e0) & 31));
+    __syncthreads();
+#pragma unroll
+    for (int l = 0; l < NL; ++l) {  // listed tokens leave the sums
+      const int bit = (l * kThreads + tid) * VE;
+      const uint32_t mk = (mask[bit >> 5] >> (bit & 31)) & ((1u << VE) - 1u);
+      if (mk) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if ((mk >> i) & 1u) {
+            if constexpr (DT == DFLASH_BF16)
+              x[l].w[i >> 1] = (i & 1) ? (x[l].w[i >> 1] & 0x0000FFFFu) | 0xFF800000u : (x[l].w[i >> 1] & 0xFFFF0000u) | 0x0000FF80u;
+            else
+              x[l].w[i] = 0xFF800000u;
+          }
+      }
+    }
+  }
+  float m = kNegInf;
+#pragma unroll
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[l], i));
+  const double c = kLog2e64 / a.tau;
+  const double M = rint(block_max(red, (double)m) * c);  // -inf: nothing here; +inf ends in NaN below
+  double s = 0.0;
+#pragma unroll
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DT>(x[l], i);
+      // -inf adds nothing; NaN and +inf make the sum NaN
+      if (v != kNegInf) s += v < INFINITY ? exp2_sum(fma((double)v, c, -M)) : (double)NAN;
+    }
+  s = block_sum(red, s);
+  if (tid == 0) parts[blockIdx.x] = DistillPart{M, s};
+}
+
+// log-sum-exp (natural) of terms s * 2^m
+__device__ __forceinline__ double join_log(double m, double s) {
+  if (s == 0.0) return -INFINITY;
+  return (m + log2(s)) * kLn2;
+}
+
+template <int DT, bool REST>
+__global__ __launch_bounds__(kThreads) void distill_loss_kernel(DistillArgs a, int n_seg, const DistillPart* __restrict__ parts,
+                                                                float* __restrict__ loss, double* __restrict__ lse_out,
+                                                                double* __restrict__ rest_out) {
+  __shared__ Red red;
+  __shared__ int seen[DFLASH_DISTILL_K_MAX];
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const float w = a.weight ? a.weight[row] : 1.0f;
+  if (w == 0.0f) {
+    if (tid == 0) {
+      if (loss) loss[row] = 0.0f;
+      lse_out[row] = 0.0;
+      if (REST) rest_out[row] = 0.0;
+    }
+    return;
+  }
+  const RowRef<DT> z(a.S, row, a.stride, a.V);
+  const double c2 = kLog2e64 / a.tau;
+  const double c = teacher_lse(red, a, row);
+
+  // the segments' sums: maxima first, then the terms in segment order
+  const DistillPart* part = parts + row * n_seg;
+  double M = -INFINITY;
+  for (int g = tid; g < n_seg; g += kThreads)
+    if (part[g].s != 0.0) M = fmax(M, part[g].m);
+  M = block_max(red, M);
+  double s = 0.0;
+  for (int g = tid; g < n_seg; g += kThreads)
+    if (part[g].s != 0.0) s += part[g].s == part[g].s ? ldexp(part[g].s, (int)fmax(part[g].m - M, -4000.0)) : (double)NAN;
+  s = block_sum(red, s);
+  const double rest = join_log(M, s);  // natural
+  double lse = rest;
+
+  if constexpr (REST) {
+    // the listed tokens' own terms, each token once
+    for (int k = tid; k < a.K; k += kThreads) {
+      int idx;
+      seen[k] = listed(a, row, k, idx) ? idx : -1;
+    }
+    __syncthreads();
+    double lm = -INFINITY;
+    for (int k = tid; k < a.K; k += kThreads) {
+      const int idx = seen[k];
+      bool first = idx >= 0;
+      for (int q = 0; q < k && first; ++q) first = seen[q] != idx;
+      if (first) {
+        const float v = row_value<DT>(z, idx);
+        lm = v != v ? INFINITY : fmax(lm, (double)v);
+      }
+    }
+    lm = block_max(red, lm);
+    if (lm > -INFINITY) {
+      const double LM = rint(lm * c2);
+      double ls = 0.0;
+      for (int k = tid; k < a.K; k += kThreads) {
+        const int idx = seen[k];
+        bool first = idx >= 0;
+        for (int q = 0; q < k && first; ++q) first = seen[q] != idx;
+        if (first) {
+          const float v = row_value<DT>(z, idx);
+          if (v != kNegInf) ls += v < INFINITY ? exp2(fma((double)v, c2, -LM)) : (double)NAN;
+        }
+      }
+      ls = block_sum(red, ls);
+      const double T = s > 0.0 ? fmax(M, LM) : LM;
+      const double all = (s == 0.0 ? 0.0 : ldexp(s, (int)fmax(M - T, -4000.0))) + ldexp(ls, (int)fmax(LM - T, -4000.0));
+      lse = s != s ? s : join_log(T, all);
+    }
+  }
+
+  // D over the listed entries
+  double d = 0.0, p_sum = 0.0;
+  if (c > -INFINITY || c != c)
+    for (int k = tid; k < a.K; k += kThreads) {
+      int idx;
+      if (!listed(a, row, k, idx)) continue;
+      const double logp = (double)a.t_logit[row * a.K + k] / a.tau - c;
+      const double p = exp(logp);
+      p_sum += p;
+      if (p != 0.0) d += p * (logp - (double)row_value<DT>(z, idx) / a.tau + lse);
+    }
+  d = block_sum(red, d);
+  p_sum = block_sum(red, p_sum);
+  if constexpr (REST) {
+    const double p_rest = 1.0 - p_sum;
+    if (c > -INFINITY && rest > -INFINITY && p_rest > 0.0) d += p_rest * (log(p_rest) - rest + lse);
+    if (rest != rest) d = rest;
+  }
+  if (c == -INFINITY || lse == -INFINITY) d = 0.0;  // an empty row on either side
+  if (tid == 0) {
+    if (loss) loss[row] = (float)((double)w * d);
+    lse_out[row] = lse;
+    if (REST) rest_out[row] = rest;
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+template <int DT, int NL, bool REST>
+__global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, int n_seg, const float* __restrict__ grad_loss,
+                                                                const double* __restrict__ lse_in,
+                                                                const double* __restrict__ rest_in, void* dS,
+                                                                int64_t d_stride) {
+  using E = typename RowType<DT>::elem;
+  constexpr int VE = RowType<DT>::VE;
+  constexpr int kPerThread = DFLASH_DISTILL_K_MAX / kThreads;
+  __shared__ Red red;
+  __shared__ int seen[DFLASH_DISTILL_K_MAX];
+  __shared__ double prob[DFLASH_DISTILL_K_MAX];
+  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
+  const int64_t row = blockIdx.x / n_seg;
+  const RowRef<DT> z(a.S, row, a.stride, a.V);
+  E* o = static_cast<E*>(dS) + row * d_stride;
+  const bool same = (reinterpret_cast<uintptr_t>(o) & 15u) == (reinterpret_cast<uintptr_t>(z.p) & 15u);
+  const int s0 = seg * (kThreads * NL), e0 = z.first(s0), e1 = e0 + kThreads * NL * VE;
+  double f = (a.weight ? (double)a.weight[row] : 1.0) * (grad_loss ? (double)grad_loss[row] : 1.0);
+  const bool off = (a.weight && a.weight[row] == 0.0f) || (grad_loss && grad_loss[row] == 0.0f);
+  f /= a.tau;
+  const double lse = off ? 0.0 : lse_in[row];
+  const double rest = REST && !off ? rest_in[row] : 0.0;
+
+  Slot x[NL];
+  if (!off) {
+#pragma unroll
+    for (int l = 0; l < NL; ++l) x[l] = z.template load<true>(s0 + l * kThreads + tid);
+  }
+  double c = -INFINITY, p_sum = 0.0;
+  float own[kPerThread];  // the listed tokens' logits of this segment, read before anything is stored (dS may be S)
+  if (!off) {
+    c = teacher_lse(red, a, row);
+    if (c != -INFINITY) {
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j) {
+        const int k = j * kThreads + tid;
+        if (k < a.K) {
+          int idx;
+          const bool in = listed(a, row, k, idx);
+          const double p = in ? exp((double)a.t_logit[row * a.K + k] / a.tau - c) : 0.0;
+          p_sum += p;
+          seen[k] = in ? idx : -1;
+          prob[k] = p;
+          if (in && idx >= e0 && idx < e1) own[j] = row_value<DT>(z, idx);
+        }
+      }
+    }
+    p_sum = block_sum(red, p_sum);
+  }
+  if (off || c == -INFINITY || lse == -INFINITY) {  // no gradient: weight zero, or an empty row on either side
+#pragma unroll
+    for (int l = 0; l < NL; ++l) store_slot<DT>(o, z, s0 + l * kThreads + tid, Slot{{0, 0, 0, 0}}, same);
+    return;
+  }
+  const bool with_rest = REST && rest != -INFINITY;
+  const double p_rest = with_rest ? fmax(1.0 - p_sum, 0.0) : 0.0;
+  const double A = p_sum + p_rest;
+  const double base = with_rest ? rest : lse;
+  const float G = (float)(f * (with_rest ? A * exp(rest - lse) - p_rest : A));
+  // x_j - base in two pieces of fp32: the product s c and its difference from
+  // the base are rounded once (fma), the low halves are added after
+  const double c2 = kLog2e64 / a.tau, b2 = base * kLog2e64;
+  const float ch = (float)c2, cl = (float)(c2 - (double)ch), bh = (float)b2, bl = (float)(b2 - (double)bh);
+#pragma unroll
+  for (int l = 0; l < NL; ++l) {
+    Slot y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y.w[k] = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DT>(x[l], i);
+      const float t = fmaf(v, ch, -bh) + fmaf(v, cl, -bl);
+      const float g = v == kNegInf ? 0.0f : G * __builtin_amdgcn_exp2f(t);
+      if constexpr (DT == DFLASH_BF16)
+        y.w[i >> 1] |= bf16_round(g) << ((i & 1) * 16);
+      else
+        y.w[i] = __float_as_uint(g);
+    }
+    store_slot<DT>(o, z, s0 + l * kThreads + tid, y, same);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int k = j * kThreads + tid;
+    if (k < a.K && seen[k] >= 0 && seen[k] >= e0 && seen[k] < e1) {  // e0 < 0 in a row that starts inside a slot
+      double p = 0.0;  // every entry of this token, in list order
+      for (int q = 0; q < a.K; ++q)
+        if (seen[q] == seen[k]) p += prob[q];
+      const double sm = own[j] == kNegInf ? 0.0 : exp((double)own[j] / a.tau - lse);
+      o[seen[k]] = to_elem<DT>((float)(f * (A * sm - p)));
+    }
+  }
+}
+
+template <int DT, int NL>
+hipError_t run_forward(const DistillArgs& a, float* loss, double* lse, double* rest, char* ws, const DistillPlan& pl,
+                       hipStream_t st) {
+  DistillPart* parts = reinterpret_cast<DistillPart*>(ws);
+  const dim3 grid((unsigned)(a.R * pl.n_seg)), rows((unsigned)a.R), block(kThreads);
+  if (rest) {
+    launch(distill_sum_kernel<DT, NL, true>, grid, block, st, a, pl.n_seg, parts);
+    launch(distill_loss_kernel<DT, true>, rows, block, st, a, pl.n_seg, (const DistillPart*)parts, loss, lse, rest);
+  } else {
+    launch(distill_sum_kernel<DT, NL, false>, grid, block, st, a, pl.n_seg, parts);
+    launch(distill_loss_kernel<DT, false>, rows, block, st, a, pl.n_seg, (const DistillPart*)parts, loss, lse, rest);
+  }
+  return hipGetLastError();
+}
+
+template <int DT, int NL>
+hipError_t run_grad(const DistillArgs& a, const float* grad_loss, const double* lse, const double* rest, void* dS,
+                    int64_t d_stride, const DistillPlan& pl, hipStream_t st) {
+  const dim3 grid((unsigned)(a.R * pl.n_seg)), block(kThreads);
+  if (rest)
+    launch(distill_grad_kernel<DT, NL, true>, grid, block, st, a, pl.n_seg, grad_loss, lse, rest, dS, d_stride);
+  else
+    launch(distill_grad_kernel<DT, NL, false>, grid, block, st, a, pl.n_seg, grad_loss, lse, rest, dS, d_stride);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_distill(int32_t dtype, const DistillArgs& a, float* loss, double* lse, double* rest, char* ws,
+                          const DistillPlan& pl, hipStream_t st) {
+  if (dtype == DFLASH_BF16) {
+    return pl.loads == 2 ? run_forward<DFLASH_BF16, 2>(a, loss, lse, rest, ws, pl, st)
+                         : run_forward<DFLASH_BF16, 8>(a, loss, lse, rest, ws, pl, st);
+  }
+  return pl.loads == 2 ? run_forward<DFLASH_F32, 2>(a, loss, lse, rest, ws, pl, st)
+                       : run_forward<DFLASH_F32, 8>(a, loss, lse, rest, ws, pl, st);
+}
+
+hipError_t launch_distill_grad(int32_t dtype, const DistillArgs& a, const float* grad_loss, const double* lse,
+                               const double* rest, void* dS, int64_t d_stride, const DistillPlan& pl, hipStream_t st) {
+  if (dtype == DFLASH_BF16) {
+    return pl.loads == 2 ? run_grad<DFLASH_BF16, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st)
+                         : run_grad<DFLASH_BF16, 8>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
+  }
+  return pl.loads == 2 ? run_grad<DFLASH_F32, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st)
+                       : run_grad<DFLASH_F32, 8>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
+}
+
+}  // namespace dfk

@@ -167,6 +167,75 @@ hipError_t launch_cycle_finalize(const dflash_dims& d, const WsLayout& w, const 
                                  int32_t* out_tok, hipStream_t st, bool advance_epoch = false);
 hipError_t launch_conv2tap(const dflash_dims& d, const void* x, const void* x0, const void* Wt, float* y,
                            hipStream_t st);
+// ---- rows of vocabulary logits (dflash_rows) ----
+
+// dflash_sample / dflash_filter: a block takes kSampleThreads * loads 16-byte
+// slots of a row; its bins go to one SamplePart
+constexpr int kSampleThreads = 512;
+constexpr int kSampleBins = 512;
+constexpr int kSampleMaxLoads = 8;  // at most 32768 elements a block, what its 64-bit bin sums hold
+struct SamplePart {
+  double J;      // floor of the segment's maximum in eighths of an octave; -inf: nothing unmasked
+  float max;     // the maximum
+  uint32_t n;    // unmasked tokens
+  int32_t nb;    // bins in use
+  int32_t pad;
+  double mass[kSampleBins];   // bin b: weights over 2^((J - b) / 8)
+  uint32_t cnt[kSampleBins];  // and tokens
+};
+struct SampleArgs {
+  const void* Z;
+  int64_t R, stride;
+  int32_t V, group;
+  const float* T;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+};
+struct SampleOut {
+  const double* u;
+  int32_t* token;
+  float* prob;
+  int32_t* kept;
+  void* out;  // the filtered rows (dflash_filter)
+  int64_t out_stride;
+  uint32_t fill;  // fill value in the element type
+};
+struct SamplePlan {
+  int loads;      // slots per thread of the bin kernel
+  int n_seg;      // blocks per row
+  int64_t batch;  // rows per pass over the workspace
+  size_t parts, cuts, total;
+};
+SamplePlan sample_plan(const dflash_rows& r);
+hipError_t launch_sample(int32_t dtype, const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl,
+                         hipStream_t st);
+
+// dflash_distill / dflash_distill_grad: a block takes kDistillThreads *
+// loads slots of a row
+constexpr int kDistillThreads = 256;
+struct DistillPart {
+  double m, s;  // log2 of the largest term (rounded) and sum of 2^(x - m) over the segment's tokens
+};
+struct DistillArgs {
+  const void* S;
+  int64_t R, stride;
+  int32_t V, K;
+  double tau;
+  const int32_t* t_idx;
+  const float* t_logit;
+  const double* t_lse;   // or null: the list alone is the teacher
+  const float* weight;   // or null
+};
+struct DistillPlan {
+  int loads, n_seg;
+  size_t total;
+};
+DistillPlan distill_plan(const dflash_rows& r);
+hipError_t launch_distill(int32_t dtype, const DistillArgs& a, float* loss, double* lse, double* lse_rest, char* ws,
+                          const DistillPlan& pl, hipStream_t st);
+hipError_t launch_distill_grad(int32_t dtype, const DistillArgs& a, const float* grad_loss, const double* lse,
+                               const double* lse_rest, void* dS, int64_t d_stride, const DistillPlan& pl, hipStream_t st);
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
 // device address and size of the library's static scratch on the current
 // device (looked up once per device)

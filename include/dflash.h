@@ -26,7 +26,9 @@
  * one.  Beside them: dflash_trace_viterbi and dflash_cycle_maxsum take the
  * path of largest summed score instead of the greedy/sampled walk, and
  * dflash_conv2tap is the drafter's two-tap dynamic convolution, upstream of
- * the context vectors h.
+ * the context vectors h.  Around the cycle: dflash_sample and dflash_filter
+ * (top-k, top-p, min-p on any logit rows), dflash_distill and
+ * dflash_distill_grad (the drafter's loss against a teacher's top logits).
  *
  * Conventions for every entry point:
  *   - Every array argument is a DEVICE pointer owned by the caller; the
@@ -81,6 +83,8 @@ extern "C" {
 #define DFLASH_R_MAX 256     /* embedding rank */
 #define DFLASH_V_MAX 2097152 /* vocabulary size */
 #define DFLASH_CHUNK 4096    /* tokens per first-level item of the residual draw */
+#define DFLASH_ROWS_MAX 4194304  /* rows of one call on a dflash_rows */
+#define DFLASH_DISTILL_K_MAX 1024 /* listed teacher tokens per row */
 #define DFLASH_STATIC_SCRATCH_BYTES (8u << 20) /* the library's own scratch per GPU (dflash_cycle_static) */
 
 typedef int32_t dflash_status;
@@ -355,6 +359,125 @@ dflash_status dflash_trace_viterbi(const dflash_dims* d, const float* S, const i
 dflash_status dflash_conv2tap(const dflash_dims* d, const void* x, const void* x0, const void* Wt, float* y,
                               void* stream);
 
+/* ---- rows of vocabulary logits ------------------------------------------
+ * Four operators around the cycle that take any set of logit rows: the
+ * filters a serving request asks for (dflash_sample, dflash_filter) and the
+ * drafter's training loss (dflash_distill, dflash_distill_grad).  The
+ * conventions above hold except that
+ *   - rows may have any length, any stride and any element-aligned address
+ *     (16-byte aligned rows whose stride is a multiple of 16 bytes are the
+ *     fastest);
+ *   - -inf logits are allowed and mean a masked token; what NaN and +inf mean
+ *     stands with each operator;
+ *   - R = 0 is an empty call: DFLASH_OK, nothing is launched, pointers may be
+ *     NULL.
+ * The calls enqueue kernels only, so they may be captured into a HIP graph. */
+typedef struct dflash_rows {
+  int64_t R;      /* rows, 0..DFLASH_ROWS_MAX */
+  int64_t stride; /* elements from one row's start to the next one's, >= V (any value if R <= 1) */
+  int32_t V;      /* logits per row, 1..DFLASH_V_MAX */
+  int32_t dtype;  /* DFLASH_F32 | DFLASH_BF16 */
+} dflash_rows;
+
+/* Bytes of workspace any of the four needs for these rows (host only, pure).
+ * The contents need no initialisation; calls that overlap in time, and
+ * captured graphs whose replays may, must not share a workspace. */
+dflash_status dflash_rows_workspace_bytes(const dflash_rows* r, size_t* bytes);
+
+/* What a request asks of its distribution: DEVICE arrays with one value for
+ * every `group` consecutive rows (value i serves rows i * group ..
+ * (i + 1) * group - 1; group = L + 1 for target rows [B, L + 1]).  A NULL
+ * array leaves its setting off (T: 1).
+ * With w_i = exp((z_i - max z) / T) and a row's tokens ordered by logit
+ * descending, then index ascending (-0 equal to +0), each filter keeps the
+ * first tokens of that order, and the shortest of the three is kept:
+ *   top_k  the first top_k tokens; off if <= 0
+ *   top_p  the fewest tokens whose weights sum to at least top_p times the
+ *          sum over those top_k leaves; off if >= 1 or NaN; <= 0 keeps one
+ *   min_p  the tokens with w_i >= min_p (above 1: as 1); off if <= 0 or NaN
+ * T <= 0 or NaN is greedy: the first token of the order alone (the other
+ * settings of that row are ignored); T = +inf weighs unmasked tokens alike.
+ * Masked tokens (-inf, NaN) are never kept; +inf counts as the type's largest
+ * finite value.  Weights, sums and their comparisons are fp64. */
+typedef struct dflash_filters {
+  const float* T;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t group; /* >= 1 */
+} dflash_filters;
+
+/* One token per row, drawn from the kept tokens' renormalised weights by
+ * inverse CDF along the order above: the first token whose running sum
+ * exceeds u[row] times the kept tokens' sum.
+ *   Z      [R, V] logits;  u [R] double, uniform in [0, 1) (clamped into it;
+ *          NaN: 0)
+ *   token  [R] int32 out;  -1 for a row with nothing unmasked
+ *   prob   [R] float out or NULL: the token's probability among the kept (0
+ *          with token -1)
+ *   kept   [R] int32 out or NULL: how many tokens were kept */
+dflash_status dflash_sample(const dflash_rows* r, const void* Z, const dflash_filters* f, const double* u,
+                            int32_t* token, float* prob_opt, int32_t* kept_opt, void* ws, size_t ws_bytes, void* stream);
+
+/* The rows with every token that the filters remove set to `fill`, so that
+ * dflash_verify and the cycles, given these rows as Z (and the same T),
+ * accept and draw from the filtered distribution.  They need finite logits:
+ * fill with a finite value so low that exp((fill - max z) / T) is 0 (the
+ * element type's lowest finite value always is).
+ *   out    [R, V] in Z's type with its own row stride; out may be Z itself
+ *          (same address and stride), and must not overlap it otherwise
+ *   fill   rounded to Z's type
+ *   kept   [R] int32 out or NULL */
+dflash_status dflash_filter(const dflash_rows* r, const void* Z, const dflash_filters* f, float fill, void* out,
+                            int64_t out_stride, int32_t* kept_opt, void* ws, size_t ws_bytes, void* stream);
+
+/* Distillation from a teacher's top logits: the divergence of the student's
+ * distribution from the teacher's at temperature tau, a row at a time.  The
+ * teacher is known by K listed tokens (dflash_topk over its rows writes such
+ * lists) and, if t_lse is given, by its log-sum-exp over the whole
+ * vocabulary.  With x_j = S_j / tau, lse = log sum_j e^x_j and
+ * p_k = e^(t_k / tau - c):
+ *   without t_lse, c is the list's own log-sum-exp and
+ *     D = sum_k p_k (log p_k - x_{i_k} + lse);
+ *   with t_lse, c = t_lse and all unlisted tokens form one class more:
+ *     D += p_rest (log p_rest - lse_rest + lse),
+ *     p_rest = max(0, 1 - sum_k p_k), lse_rest the unlisted tokens'
+ *     log-sum-exp (the term is left out if none of them is unmasked).
+ *   S        [R, V] student logits;  K in 0..DFLASH_DISTILL_K_MAX
+ *   tau      HOST value, finite, > 0
+ *   t_idx    [R, K] int32 token ids; an id outside [0, V) is padding and
+ *            counts for nothing; a repeated id's entries add up
+ *   t_logit  [R, K] float (-inf: probability 0)
+ *   t_lse    [R] double log sum_j e^(t_j / tau), or NULL
+ *   weight   [R] float or NULL (ones); a row of weight 0 is not read
+ *   loss     [R] float out or NULL: weight * D
+ *   lse      [R] double out
+ *   lse_rest [R] double out, given exactly if t_lse is
+ * K = 0 with loss NULL computes lse alone (a teacher's t_lse).  Weight 0 gives
+ * 0 in all outputs.  A row in which no listed token has mass (and t_lse is
+ * absent or not finite), or no student logit is unmasked, has D = 0.  NaN or
+ * +inf logits make the row's outputs NaN; a masked student token with p > 0
+ * makes D +inf. */
+dflash_status dflash_distill(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
+                             const float* t_logit, const double* t_lse_opt, const float* weight_opt, float* loss_opt,
+                             double* lse, double* lse_rest_opt, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient: dS_j = weight * grad_loss * dD/dS_j, with the arguments of the
+ * forward call and what it wrote (lse, lse_rest).  With A = sum_k p_k (+
+ * p_rest):  tau dD/dS_j = A e^(x_j - lse) - (p of j) for a listed token,
+ * A e^(x_j - lse) - p_rest e^(x_j - lse_rest) for an unlisted one.
+ *   grad_loss [R] float or NULL (ones); where it or weight is 0 the row of
+ *             dS is zeros and S is not read, and so is a row with D = 0 by
+ *             the rule above
+ *   dS        [R, V] in S's type with its own row stride, written whole; may
+ *             be S itself (same address and stride), and must not overlap it
+ *             otherwise
+ * One launch, no workspace, no atomics: repeated calls give the same bits. */
+dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
+                                  const float* t_logit, const double* t_lse_opt, const float* weight_opt,
+                                  const float* grad_loss_opt, const double* lse, const double* lse_rest_opt, void* dS,
+                                  int64_t ds_stride, void* stream);
+
 /* ---- measurement helpers (not part of the method) ---------------------- */
 
 /* Stream-read `bytes` (multiple of 16, 16-byte aligned) of `buf` once: the
@@ -386,7 +509,11 @@ enum {
   DFLASH_KERNEL_TOPK_MERGE = 11,    /* dflash_topk_merge */
   DFLASH_KERNEL_SHARD_STATS = 12,   /* dflash_shard_stats */
   DFLASH_KERNEL_SHARD_FINALIZE = 13, /* dflash_verify_shards */
-  DFLASH_KERNEL_COUNT = 14
+  DFLASH_KERNEL_SAMPLE = 14,        /* dflash_sample (all of its launches) */
+  DFLASH_KERNEL_FILTER = 15,        /* dflash_filter (all of its launches) */
+  DFLASH_KERNEL_DISTILL = 16,       /* dflash_distill (both launches) */
+  DFLASH_KERNEL_DISTILL_GRAD = 17,  /* dflash_distill_grad */
+  DFLASH_KERNEL_COUNT = 18
 };
 
 /* Name of a kernel identifier ("" if out of range). */
