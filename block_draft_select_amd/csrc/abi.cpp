@@ -219,7 +219,7 @@ SamplePlan sample_plan(const dflash_rows& r) {
   const int slots = row_slots(r);
   for (p.loads = kSampleMaxLoads;; p.loads /= 2) {
     p.n_seg = (slots + kSampleThreads * p.loads - 1) / (kSampleThreads * p.loads);
-    if (p.loads == 1 || r.R * p.n_seg >= 1024) break;
+    if (p.loads == 1 || r.R * p.n_seg >= 1024 || p.n_seg * 2 + 1 > kSampleMaxSeg) break;
   }
   p.batch = 4096 / p.n_seg > 1 ? 4096 / p.n_seg : 1;
   const size_t rows = (size_t)(r.R < p.batch ? r.R : p.batch);

@@ -173,15 +173,20 @@ hipError_t launch_conv2tap(const dflash_dims& d, const void* x, const void* x0, 
 // slots of a row; its bins go to one SamplePart
 constexpr int kSampleThreads = 512;
 constexpr int kSampleBins = 512;
+constexpr int kSampleList = 256;
+constexpr int kSampleMaxSeg = 512;  // blocks per row
 constexpr int kSampleMaxLoads = 8;  // at most 32768 elements a block, what its 64-bit bin sums hold
 struct SamplePart {
   double J;      // floor of the segment's maximum in eighths of an octave; -inf: nothing unmasked
   float max;     // the maximum
   uint32_t n;    // unmasked tokens
   int32_t nb;    // bins in use
+  int32_t listed;  // the tokens of bins 0 .. listed - 1 are in `list`
+  int32_t n_list;
   int32_t pad;
   double mass[kSampleBins];   // bin b: weights over 2^((J - b) / 8)
   uint32_t cnt[kSampleBins];  // and tokens
+  uint64_t list[kSampleList];  // (~key, index) of the segment's largest tokens, in any order
 };
 struct SampleArgs {
   const void* Z;

@@ -39,8 +39,7 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kBins = kSampleBins;  // 64 octaves; the last bin collects everything below (weight under 2^-63.9)
 constexpr int kTail = kBins - 1;
 constexpr int kCols = 4;            // copies of the bins a wave's lanes spread over
-constexpr int kCap = 4096;          // tokens the sorted list holds
-constexpr int kPer = kCap / kThreads;
+constexpr int kCap = 4096;          // tokens of one bin held in LDS
 static_assert(kThreads == kBins, "one thread per bin");
 
 constexpr uint32_t kKeyLowest = 0x00800000u;  // ordered key of the lowest finite fp32
@@ -96,66 +95,107 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
 
 // ---------------------------------------------------------------- block helpers (kThreads threads)
 
+// Reductions over the block with one barrier each: successive calls alternate
+// between two buffers, so a buffer is rewritten only after the barrier of the
+// call between, which every thread reaches after it has read the buffer.
 struct Red {
-  double d[kWaves];
-  uint32_t u[kWaves];
-  int first;
+  double d[2][kWaves];
+  uint32_t u[2][kWaves];
 };
 
-// smallest thread index whose predicate holds (kThreads if none)
-__device__ __forceinline__ int block_first(Red& s, bool pred) {
-  const int tid = threadIdx.x;
-  __syncthreads();
-  if (tid == 0) s.first = kThreads;
-  __syncthreads();
-  const int f = first_lane(pred);
-  if ((tid & 63) == 0 && f < 64) atomicMin(&s.first, tid + f);
-  __syncthreads();
-  return s.first;
-}
+struct BlockOps {
+  Red& s;
+  int flip;
+  __device__ explicit BlockOps(Red& r) : s(r), flip(0) {}
 
-__device__ __forceinline__ int block_min(Red& s, int v) {
-  const int tid = threadIdx.x;
-  v = wave_min_i32(v);
-  __syncthreads();
-  if (tid == 0) s.first = 0x7FFFFFFF;
-  __syncthreads();
-  if ((tid & 63) == 0) atomicMin(&s.first, v);
-  __syncthreads();
-  return s.first;
-}
-
-__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
-  const int lane = lane_id();
+  // smallest thread index whose predicate holds (kThreads if none)
+  __device__ __forceinline__ int first(bool pred) {
+    const int tid = threadIdx.x, f = first_lane(pred);
+    flip ^= 1;
+    if ((tid & 63) == 0) s.u[flip][tid >> 6] = f < 64 ? (uint32_t)(tid + f) : (uint32_t)kThreads;
+    __syncthreads();
+    uint32_t r = s.u[flip][0];
 #pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const uint32_t w = __shfl_up(v, o);
-    v += lane >= o ? w : 0u;
+    for (int w = 1; w < kWaves; ++w) r = min(r, s.u[flip][w]);
+    return (int)r;
   }
-  return v;
-}
+  // inclusive scans, in fixed order
+  __device__ __forceinline__ uint32_t scan(uint32_t v) {
+    const int w = threadIdx.x >> 6;
+    v = wave_scan_u32(v);
+    flip ^= 1;
+    if ((threadIdx.x & 63) == 63) s.u[flip][w] = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i) v += i < w ? s.u[flip][i] : 0u;
+    return v;
+  }
+  __device__ __forceinline__ double scan(double v) {
+    const int w = threadIdx.x >> 6;
+    v = wave_scan_f64(v);
+    flip ^= 1;
+    if ((threadIdx.x & 63) == 63) s.d[flip][w] = v;
+    __syncthreads();
+    double off = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i) off += i < w ? s.d[flip][i] : 0.0;
+    return v + off;
+  }
+  __device__ __forceinline__ double max(double v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
+    flip ^= 1;
+    if ((threadIdx.x & 63) == 0) s.d[flip][threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = s.d[flip][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v = fmax(v, s.d[flip][w]);
+    return v;
+  }
+  __device__ __forceinline__ uint32_t sum(uint32_t v) {
+    v = wave_sum_u32(v);
+    flip ^= 1;
+    if ((threadIdx.x & 63) == 0) s.u[flip][threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += s.u[flip][w];
+    return v;
+  }
 
-// inclusive scans over the block, in fixed order
-__device__ __forceinline__ uint32_t block_scan_u32(Red& s, uint32_t v) {
-  const int w = threadIdx.x >> 6;
-  v = wave_scan_u32(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 63) s.u[w] = v;
-  __syncthreads();
-  uint32_t off = 0;
-  for (int i = 0; i < w; ++i) off += s.u[i];
-  return v + off;
-}
+ private:
+  static __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
+    v += dpp_u32<kDppRowShr1>(v, 0u);
+    v += dpp_u32<kDppRowShr2>(v, 0u);
+    v += dpp_u32<kDppRowShr4>(v, 0u);
+    v += dpp_u32<kDppRowShr8>(v, 0u);
+    v += dpp_u32<kDppRowBcast15, 0xA>(v, 0u);
+    v += dpp_u32<kDppRowBcast31, 0xC>(v, 0u);
+    return v;
+  }
+};
 
-__device__ __forceinline__ double block_scan_f64(Red& s, double v) {
-  const int w = threadIdx.x >> 6;
-  v = wave_scan_f64(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 63) s.d[w] = v;
-  __syncthreads();
-  double off = 0.0;
-  for (int i = 0; i < w; ++i) off += s.d[i];
-  return v + off;
+__device__ __forceinline__ uint32_t key_of(float v, float max_finite) {
+  return ord32_canon(__float_as_uint(fminf(v, max_finite)));
+}
+__device__ __forceinline__ double key_value(uint32_t key) { return (double)__uint_as_float(unord32(key)); }
+
+// smallest ordered key >= kKeyLowest whose t = z c8 reaches `j` (0xFF800000,
+// above every finite key, if none does).  One round of the wave's 64 lanes
+// around j / c8, which rounding moves by a few keys; a search where that
+// guess does not bracket it (j or c8 extreme).
+__device__ __forceinline__ uint32_t lowest_key(double j, double c8) {
+  const double z = fmin(fmax(j / c8, -3.4028234663852886e38), 3.4028234663852886e38);  // 0/0: some finite value
+  const uint32_t g = max(ord32_canon(__float_as_uint((float)z)), kKeyLowest + 32u);
+  const uint32_t cand = min(g - 32u + (uint32_t)lane_id(), 0xFF7FFFFFu);
+  const uint64_t hit = __ballot(key_value(cand) * c8 >= j);
+  if (hit && !(hit & 1)) return __shfl(cand, __builtin_ctzll(hit));
+  uint32_t l = kKeyLowest, h = 0xFF800000u;
+  while (l < h) {
+    const uint32_t mid = l + ((h - l) >> 1);
+    if (key_value(mid) * c8 >= j) h = mid; else l = mid + 1;
+  }
+  return l;
 }
 
 // ---------------------------------------------------------------- (1) bins of a segment
@@ -166,8 +206,9 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
   constexpr int VE = RowType<DT>::VE;
   __shared__ uint64_t mass[kBins * kCols];
   __shared__ uint32_t cnt[kBins * kCols];
-  __shared__ float wmax[kWaves];
   __shared__ Red red;
+  __shared__ uint32_t n_list;
+  BlockOps ops(red);
   const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
   const int64_t row = row0 + blockIdx.x / n_seg;
   const RowRef<DT> z(a.Z, row, a.stride, a.V);
@@ -183,17 +224,13 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
     mass[c * kBins + tid] = 0;
     cnt[c * kBins + tid] = 0;
   }
+  if (tid == 0) n_list = 0;
   float m = kNegInf;
 #pragma unroll
   for (int l = 0; l < NL; ++l)
 #pragma unroll
     for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[l], i));  // NaN drops out
-  m = wave_max_f32(fminf(m, RowType<DT>::kMax));
-  if ((tid & 63) == 0) wmax[tid >> 6] = m;
-  __syncthreads();
-  m = wmax[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, wmax[w]);
+  m = (float)ops.max((double)fminf(m, RowType<DT>::kMax));
 
   SamplePart& out = parts[blockIdx.x];
   if (m == kNegInf) {
@@ -202,6 +239,8 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
       out.max = kNegInf;
       out.n = 0;
       out.nb = 0;
+      out.listed = kBins;
+      out.n_list = 0;
     }
     return;
   }
@@ -221,28 +260,47 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
       }
     }
   __syncthreads();
-  uint32_t c = 0;
+  uint32_t c = 0, mirror = 0;  // mirror: the bin counted from the far end
   uint64_t f = 0;
 #pragma unroll
   for (int k = 0; k < kCols; ++k) {
     c += cnt[tid * kCols + k];
     f += mass[tid * kCols + k];
+    mirror += cnt[(kBins - 1 - tid) * kCols + k];
   }
   f -= (uint64_t)c * kOneBits;  // modulo 2^64: the fraction bits' sum
-  const uint32_t n = block_scan_u32(red, c);
-  uint32_t mirror = 0;  // the bin counted from the far end: the bins in use end where the first of these is not empty
-#pragma unroll
-  for (int k = 0; k < kCols; ++k) mirror += cnt[(kBins - 1 - tid) * kCols + k];
-  const int nb = kBins - block_first(red, mirror != 0);
+  const uint32_t upto = ops.scan(c);
+  const int nb = kBins - ops.first(mirror != 0);  // bins in use
+  // the first bins with at most kSampleList tokens together are listed
+  const int listed = ops.first(upto > (uint32_t)kSampleList);
   if (tid < nb) {
     out.cnt[tid] = c;
     out.mass[tid] = tid < kTail ? (double)c + (double)f * 0x1p-52 : 0.0;
   }
+  if (listed > 0) {
+    const uint32_t least = listed >= kBins ? kKeyLowest : lowest_key(J - (double)(listed - 1), c8);
+#pragma unroll
+    for (int l = 0; l < NL; ++l) {
+      const int e = z.first(s0 + l * kThreads);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float v = slot_value<DT>(x[l], i);
+        const uint32_t key = key_of(v, RowType<DT>::kMax);
+        if (v > kNegInf && key >= least) {
+          const uint32_t at = atomicAdd(&n_list, 1u);
+          if (at < (uint32_t)kSampleList) out.list[at] = ((uint64_t)~key << 32) | (uint32_t)(e + i);
+        }
+      }
+    }
+  }
+  __syncthreads();
   if (tid == kThreads - 1) {
     out.J = J;
     out.max = m;
-    out.n = n;
+    out.n = upto;
     out.nb = nb;
+    out.listed = listed;
+    out.n_list = (int32_t)min(n_list, (uint32_t)kSampleList);
   }
 }
 
@@ -250,17 +308,23 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
 
 enum { kByCount, kByMassGe, kByMassGt, kByWeight };
 
+constexpr int kMaxSeg = kSampleMaxSeg;
+
 struct FinLds {
-  uint64_t comp[kCap];    // the list: (~key, index), ascending = the row's order
-  uint64_t mass[kBins];   // bins of a split
+  uint64_t big[kCap];       // tokens of one bin as (~key, index), in any order
+  uint64_t win[kThreads];   // the window: sorted, ascending = the row's order
+  double wcum[kThreads];    // and the running sums at its tokens
+  uint64_t mass[kBins];     // bins of a split
   uint32_t cnt[kBins];
-  uint32_t cc[kBins + 1];  // tokens before each bin
-  double cm[kBins + 1];    // their weight
-  uint32_t rc[kBins + 1];  // the same inside a split
+  uint32_t cc[kBins + 1];   // tokens before each bin
+  double cm[kBins + 1];     // their weight
+  uint32_t rc[kBins + 1];   // the same inside a split
   double rm[kBins + 1];
+  int16_t shift[kMaxSeg];   // a segment's first bin on the row's grid
+  int16_t len[kMaxSeg];     // its bins and its listed tokens
+  int16_t n_list[kMaxSeg];
   Red red;
-  uint32_t n_list;
-  double cum;
+  uint32_t n;
   uint64_t at;
 };
 
@@ -272,166 +336,192 @@ struct Cross {
   uint64_t at;   // (~key, index) of the last of them (not for kByWeight)
 };
 
+__device__ __forceinline__ uint32_t comp_key(uint64_t c) { return ~(uint32_t)(c >> 32); }
+
 template <int DT>
 struct Finalize {
   static constexpr int VE = RowType<DT>::VE;
   FinLds& s;
+  BlockOps& ops;
   const RowRef<DT> z;
+  const SamplePart* part;
+  const int n_seg;
   const double c8, J;
   const int tid;
   const uint32_t kmax;  // the row's largest key
-  // the list's tokens: rank base + 1 .. base + n, of bins b0 .. b1 (b0 > b1: part of a bin)
+  const int listed;     // bins 0 .. listed - 1 are in the segments' lists
+  // the window's tokens: rank base + 1 .. base + n, of bins b0 .. b1 (b0 > b1: part of a bin)
   uint32_t base, n;
   double bmass;
   int b0, b1;
   uint32_t lo;
-  double cum[kPer];
 
-  __device__ Finalize(FinLds& s_, const RowRef<DT>& z_, double c8_, double J_, uint32_t kmax_)
-      : s(s_), z(z_), c8(c8_), J(J_), tid(threadIdx.x), kmax(kmax_), base(0), n(0), bmass(0.0), b0(1), b1(0), lo(0) {}
+  __device__ Finalize(FinLds& s_, BlockOps& o, const RowRef<DT>& z_, const SamplePart* part_, int n_seg_, double c8_, double J_,
+                      uint32_t kmax_, int listed_)
+      : s(s_), ops(o), z(z_), part(part_), n_seg(n_seg_), c8(c8_), J(J_), tid(threadIdx.x), kmax(kmax_), listed(listed_), base(0),
+        n(0), bmass(0.0), b0(1), b1(0), lo(0) {}
 
   // weight of a key relative to 2^(J / 8)
   __device__ double weight(uint32_t key) const {
-    const double t = (double)__uint_as_float(unord32(key)) * c8, fl = floor(t);
+    const double t = key_value(key) * c8, fl = floor(t);
     return exp2_eighth(t - fl) * pow2_eighth((int)fmax(fl - J, -16000.0));
   }
-  // smallest key whose t reaches `j` (a floor value)
-  __device__ uint32_t lowest_key(double j) const {
-    uint32_t l = kKeyLowest, h = 0xFF800000u;  // t(h) >= j or no finite key reaches it
-    while (l < h) {
-      const uint32_t mid = l + ((h - l) >> 1);
-      if ((double)__uint_as_float(unord32(mid)) * c8 >= j) h = mid; else l = mid + 1;
-    }
-    return l;
-  }
 
+  // f((~key, index)) of every token of the row with klo <= key <= khi; eight slots in flight per thread
   template <class F>
-  __device__ void each(F f) const {  // f(key, index) of every unmasked token of the row
+  __device__ void each_in_row(uint32_t klo, uint32_t khi, F f) const {
     const int n_slots = (z.V + z.phase + VE - 1) / VE;
-    for (int sl = tid; sl < n_slots; sl += kThreads) {
-      const Slot x = z.load(sl);
-      const int e = z.first(sl);
+    for (int s0 = tid; s0 < n_slots; s0 += 8 * kThreads) {
+      Slot x[8];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float v = slot_value<DT>(x, i);
-        if (v > kNegInf) f(ord32_canon(__float_as_uint(fminf(v, RowType<DT>::kMax))), (uint32_t)(e + i));
+      for (int l = 0; l < 8; ++l) x[l] = z.load(s0 + l * kThreads);
+#pragma unroll
+      for (int l = 0; l < 8; ++l) {
+        const int e = z.first(s0 + l * kThreads);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          const float v = slot_value<DT>(x[l], i);
+          const uint32_t key = key_of(v, RowType<DT>::kMax);
+          if (v > kNegInf && key >= klo && key <= khi) f(((uint64_t)~key << 32) | (uint32_t)(e + i));
+        }
       }
     }
   }
+  // the same over the segments' lists (whole only for listed bins) and over `big`
+  template <class F>
+  __device__ void each_in_lists(uint32_t klo, uint32_t khi, F f) const {
+    for (int i = tid; i < n_seg * kSampleList; i += kThreads) {
+      const int g = i / kSampleList, j = i % kSampleList;
+      if (j < s.n_list[g]) {
+        const uint64_t c = part[g].list[j];
+        const uint32_t key = comp_key(c);
+        if (key >= klo && key <= khi) f(c);
+      }
+    }
+  }
+  template <class F>
+  __device__ void each_in_big(uint32_t nbig, uint32_t klo, uint32_t khi, F f) const {
+    for (uint32_t i = tid; i < nbig; i += kThreads) {
+      const uint64_t c = s.big[i];
+      const uint32_t key = comp_key(c);
+      if (key >= klo && key <= khi) f(c);
+    }
+  }
 
-  // gather the tokens with lo <= key <= hi (at most kCap) into the list, sort
-  // it and sum its weights
-  __device__ void load(uint32_t lo_, uint32_t hi, uint32_t base_, double bmass_, int b0_, int b1_) {
+  // append to an LDS array through s.n
+  __device__ void start_append() {
+    __syncthreads();
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+  }
+
+  // s.win[0 .. s.n - 1] holds the window's tokens in any order: sort them (each
+  // thread ranks one token against the others) and sum their weights
+  __device__ void open_window(uint32_t lo_, uint32_t base_, double bmass_, int b0_, int b1_) {
     lo = lo_, base = base_, bmass = bmass_, b0 = b0_, b1 = b1_;
     __syncthreads();
-    if (tid == 0) s.n_list = 0;
-    __syncthreads();
-    each([&](uint32_t key, uint32_t idx) {
-      if (key >= lo && key <= hi) {
-        const uint32_t i = atomicAdd(&s.n_list, 1u);
-        if (i < kCap) s.comp[i] = ((uint64_t)~key << 32) | idx;
+    n = min(s.n, (uint32_t)kThreads);
+    const bool in = tid < (int)n;
+    const uint64_t mine = in ? s.win[tid] : 0;
+    uint32_t rank = 0;
+    if ((tid & ~63) < (int)n) {
+      uint32_t j = 0;
+      for (; j + 4 <= n; j += 4) {
+        const uint64_t a = s.win[j], b = s.win[j + 1], c = s.win[j + 2], d = s.win[j + 3];
+        rank += (uint32_t)(a < mine) + (uint32_t)(b < mine) + (uint32_t)(c < mine) + (uint32_t)(d < mine);
       }
-    });
-    sort();
+      for (; j < n; ++j) rank += s.win[j] < mine;
+    }
+    __syncthreads();
+    if (in) s.win[rank] = mine;
+    __syncthreads();
+    const double w = in ? weight(comp_key(s.win[tid])) : 0.0;
+    const double c = bmass + ops.scan(w);
+    if (in) s.wcum[tid] = c;
+    __syncthreads();
   }
 
-  __device__ void sort() {
-    __syncthreads();
-    n = min(s.n_list, (uint32_t)kCap);
-    int P = 2;
-    while (P < (int)n) P *= 2;
-    for (int i = (int)n + tid; i < P; i += kThreads) s.comp[i] = ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= P; k *= 2)
-      for (int j = k / 2; j > 0; j /= 2) {
-        for (int q = tid; q < P / 2; q += kThreads) {
-          const int i = ((q & ~(j - 1)) << 1) | (q & (j - 1)), l = i | j;
-          const uint64_t x = s.comp[i], y = s.comp[l];
-          if ((x > y) == ((i & k) == 0)) {
-            s.comp[i] = y;
-            s.comp[l] = x;
-          }
-        }
-        __syncthreads();
-      }
-    double carry = bmass;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (e * kThreads >= (int)n) break;
-      const int i = e * kThreads + tid;
-      const double w = i < (int)n ? weight(~(uint32_t)(s.comp[i] >> 32)) : 0.0;
-      cum[e] = carry + block_scan_f64(s.red, w);
-      __syncthreads();
-      if (tid == kThreads - 1) s.cum = cum[e];
-      __syncthreads();
-      carry = s.cum;
-    }
-  }
-
-  __device__ Cross from_list(int kind, double amount) {
-    int pos = (int)n;
-#pragma unroll
-    for (int e = kPer - 1; e >= 0; --e) {
-      const int i = e * kThreads + tid;
-      if (i < (int)n) {
-        const bool hit = kind == kByCount    ? (double)(base + i + 1) >= amount
-                         : kind == kByMassGe ? cum[e] >= amount
-                         : kind == kByMassGt ? cum[e] > amount
-                                             : weight(~(uint32_t)(s.comp[i] >> 32)) < amount;
-        if (hit) pos = i;
-      }
-    }
-    pos = block_min(s.red, pos);
-    if (kind != kByWeight) pos = min(pos, (int)n - 1) + 1;  // pos tokens of the list are in
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (pos > 0 && e * kThreads + tid == pos - 1) s.cum = cum[e];
-    __syncthreads();
+  __device__ Cross from_window(int kind, double amount) {
+    const bool in = tid < (int)n;
+    const bool hit = in && (kind == kByCount    ? (double)(base + tid + 1) >= amount
+                            : kind == kByMassGe ? s.wcum[tid] >= amount
+                            : kind == kByMassGt ? s.wcum[tid] > amount
+                                                : weight(comp_key(s.win[tid])) < amount);
+    int pos = min(ops.first(hit), (int)n);
+    if (kind != kByWeight) pos = min(pos + 1, (int)n);  // pos tokens of the window are in
     Cross r;
     r.n = base + pos;
-    r.cum = pos > 0 ? s.cum : bmass;
-    r.at = pos > 0 ? s.comp[pos - 1] : 0;
-    r.cut = pos < (int)n ? s.comp[pos] : ((uint64_t)~lo + 1) << 32;
+    r.cum = pos > 0 ? s.wcum[pos - 1] : bmass;
+    r.at = pos > 0 ? s.win[pos - 1] : 0;
+    r.cut = pos < (int)n ? s.win[pos] : ((uint64_t)~lo + 1) << 32;
     return r;
   }
 
-  // index of the r-th (from 1) token with this key, in index order: the waves
+  // index of the r-th (from 1) token with this key in `big`
+  __device__ uint32_t tie_in_big(uint32_t nbig, uint32_t key, uint32_t r) {
+    uint32_t ilo = 0, ihi = (uint32_t)z.V - 1;
+    for (;;) {
+      const uint32_t range = ihi - ilo;
+      const int sh = max(0, 32 - (range ? __builtin_clz(range) : 32) - 9);
+      __syncthreads();
+      s.cnt[tid] = 0;
+      __syncthreads();
+      each_in_big(nbig, key, key, [&](uint64_t c) {
+        const uint32_t i = (uint32_t)c;
+        if (i >= ilo && i <= ihi) atomicAdd(&s.cnt[(i - ilo) >> sh], 1u);
+      });
+      __syncthreads();
+      const uint32_t c = s.cnt[tid], upto = ops.scan(c);
+      const int b = min(ops.first(upto >= r), kThreads - 1);
+      if (tid == b) s.at = upto - c;
+      __syncthreads();
+      r -= (uint32_t)s.at;
+      ilo += (uint32_t)b << sh;
+      if (sh == 0) return ilo;
+      ihi = min(ihi, ilo + ((1u << sh) - 1u));
+    }
+  }
+
+  // the same over the row, for more equal tokens than `big` holds: the waves
   // count contiguous pieces, the one that holds it walks its piece again
-  __device__ uint32_t tie_index(uint32_t key, uint32_t r) {
+  __device__ uint32_t tie_in_row(uint32_t key, uint32_t r) {
     const int n_slots = (z.V + z.phase + VE - 1) / VE, lane = tid & 63, w = tid >> 6;
     const int per = ((n_slots + kWaves - 1) / kWaves + 63) / 64 * 64;
     const int sb = w * per, se = min(n_slots, sb + per);
     auto count = [&](int sl, uint32_t* mask) {
       const Slot x = z.load(sl);
-      uint32_t c = 0, mk = 0;
+      uint32_t mk = 0;
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
         const float v = slot_value<DT>(x, i);
-        const bool hit = v > kNegInf && ord32_canon(__float_as_uint(fminf(v, RowType<DT>::kMax))) == key;
-        c += hit;
-        mk |= (uint32_t)hit << i;
+        mk |= (uint32_t)(v > kNegInf && key_of(v, RowType<DT>::kMax) == key) << i;
       }
       *mask = mk;
-      return c;
+      return (uint32_t)__popc(mk);
     };
-    uint32_t c = 0, mk;
+    uint32_t c = 0, mk = 0;
     for (int sl = sb + lane; sl < se; sl += 64) c += count(sl, &mk);
     c = wave_sum_u32(c);
     __syncthreads();
-    if (lane == 0) s.red.u[w] = c;
+    if (lane == 0) s.cnt[w] = c;
     if (tid == 0) s.at = 0;
     __syncthreads();
     uint32_t before = 0;
-    for (int i = 0; i < w; ++i) before += s.red.u[i];
-    if (r > before && r <= before + s.red.u[w]) {
+    for (int i = 0; i < w; ++i) before += s.cnt[i];
+    if (r > before && r <= before + s.cnt[w]) {
       uint32_t left = r - before;
       for (int b = sb; b < se; b += 64) {
         const uint32_t cl = b + lane < se ? count(b + lane, &mk) : 0;
-        const uint32_t sc = wave_scan_u32(cl), total = __shfl(sc, 63);
+        uint32_t sc = cl;  // inclusive scan over the wave
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+          const uint32_t t = __shfl_up(sc, o);
+          sc += lane >= o ? t : 0u;
+        }
+        const uint32_t total = __shfl(sc, 63);
         if (left <= total) {
-          uint32_t k = left - (sc - cl);  // from 1 inside this lane's slot, if it is here
           if (left > sc - cl && left <= sc) {
+            uint32_t k = left - (sc - cl);  // from 1 inside this lane's slot
             int i = -1;
             do {
               ++i;
@@ -448,53 +538,101 @@ struct Finalize {
     return (uint32_t)s.at;
   }
 
-  // a bin (keys lo..hi, more tokens than the list holds): split its key range
-  // until the part with the crossing fits, or is one value
-  __device__ Cross split(int kind, double amount, uint32_t klo, uint32_t khi, uint32_t cb, double mb, bool tail) {
+  // A bin (keys klo .. khi) of more tokens than a window holds: split its key
+  // range until the part with the crossing fits one, or is a single value.
+  // The first rounds read the row where the bin does not fit `big` either.
+  __device__ Cross split(int kind, double amount, uint32_t klo, uint32_t khi, uint32_t cb, uint32_t nc, double mb, bool tail,
+                         bool from_lists) {
+    uint32_t nbig = 0;
     for (;;) {
+      if (nbig == 0 && nc <= (uint32_t)kCap) {
+        start_append();
+        auto put = [&](uint64_t c) {
+          const uint32_t i = atomicAdd(&s.n, 1u);
+          if (i < (uint32_t)kCap) s.big[i] = c;
+        };
+        if (from_lists)
+          each_in_lists(klo, khi, put);
+        else
+          each_in_row(klo, khi, put);
+        __syncthreads();
+        nbig = min(s.n, (uint32_t)kCap);
+      }
+      if (nc <= (uint32_t)kThreads) {
+        start_append();
+        each_in_big(nbig, klo, khi, [&](uint64_t c) {
+          const uint32_t i = atomicAdd(&s.n, 1u);
+          if (i < (uint32_t)kThreads) s.win[i] = c;
+        });
+        open_window(klo, cb, mb, 1, 0);
+        return from_window(kind, amount);
+      }
+      if (klo == khi) {  // one value: every token weighs w
+        const double w = tail ? 0.0 : weight(klo);
+        double r = (double)nc;
+        if (kind == kByCount) r = amount - cb;
+        if (kind == kByMassGe || kind == kByMassGt) {
+          r = fmin(fmax(floor((amount - mb) / w), 0.0), (double)nc);
+          // the quotient is off by rounding only: settle it on the sums themselves
+          if (r > 0.0 && (kind == kByMassGe ? fma(r - 1.0, w, mb) >= amount : fma(r - 1.0, w, mb) > amount)) r -= 1.0;
+          if (r < (double)nc && !(kind == kByMassGe ? fma(r, w, mb) >= amount : fma(r, w, mb) > amount)) r += 1.0;
+          r = fmax(r, 1.0);
+        }
+        if (kind == kByWeight) r = weight(klo) < amount ? 0.0 : (double)nc;
+        Cross x;
+        x.n = cb + (uint32_t)r;
+        x.cum = fma(r, w, mb);
+        x.at = 0;
+        x.cut = ((uint64_t)~klo) << 32;
+        if (r > 0.0) {
+          const uint32_t i = nbig ? tie_in_big(nbig, klo, (uint32_t)r) : tie_in_row(klo, (uint32_t)r);
+          x.at = ((uint64_t)~klo << 32) | i;
+          x.cut = x.at + 1;
+        }
+        return x;
+      }
       const uint32_t range = khi - klo;
-      const int sh = max(0, 32 - (range ? __builtin_clz(range) : 32) - 9);
+      const int sh = max(0, 32 - __builtin_clz(range) - 9);
       __syncthreads();
       s.cnt[tid] = 0;
       s.mass[tid] = 0;
       __syncthreads();
-      each([&](uint32_t key, uint32_t) {
-        if (key >= klo && key <= khi) {
-          const uint32_t b = (khi - key) >> sh;
-          atomicAdd(&s.cnt[b], 1u);
-          if (!tail) {
-            const double t = (double)__uint_as_float(unord32(key)) * c8;
-            // 46 bits of the mantissa: sums of 2^21 tokens fit 64 bits
-            atomicAdd((unsigned long long*)&s.mass[b],
-                      (unsigned long long)((__double_as_longlong(exp2_eighth(t - floor(t))) - kOneBits) >> 6));
-          }
+      auto add = [&](uint64_t cp) {
+        const uint32_t key = comp_key(cp), b = (khi - key) >> sh;
+        atomicAdd(&s.cnt[b], 1u);
+        if (!tail) {
+          const double t = key_value(key) * c8;
+          // 46 bits of the mantissa: sums of 2^21 tokens fit 64 bits
+          atomicAdd((unsigned long long*)&s.mass[b],
+                    (unsigned long long)((__double_as_longlong(exp2_eighth(t - floor(t))) - kOneBits) >> 6));
         }
-      });
+      };
+      if (nbig)
+        each_in_big(nbig, klo, khi, add);
+      else
+        each_in_row(klo, khi, add);
       __syncthreads();
       // one bin holds one eighth of an octave: its unit is that of its lowest key
-      const double unit = tail ? 0.0 : pow2_eighth((int)fmax(floor((double)__uint_as_float(unord32(klo)) * c8) - J, -16000.0));
+      const double unit = tail ? 0.0 : pow2_eighth((int)fmax(floor(key_value(klo) * c8) - J, -16000.0));
       const uint32_t c = s.cnt[tid];
-      const double mass = unit * ((double)c + (double)s.mass[tid] * 0x1p-46);
-      const uint32_t c1 = cb + block_scan_u32(s.red, c);
-      const double m1 = mb + block_scan_f64(s.red, mass);
-      __syncthreads();
+      const uint32_t c1 = cb + ops.scan(c);
+      const double m1 = mb + ops.scan(unit * ((double)c + (double)s.mass[tid] * 0x1p-46));
       s.rc[tid + 1] = c1;
       s.rm[tid + 1] = m1;
       if (tid == 0) {
         s.rc[0] = cb;
         s.rm[0] = mb;
       }
-      const uint32_t top = khi - ((uint32_t)tid << sh);  // highest key of part tid (if it exists)
-      const uint32_t n_part = (range >> sh) + 1;
-      const uint32_t low = (uint32_t)tid + 1 >= n_part ? klo : top - ((1u << sh) - 1u);
+      const uint32_t n_part = (range >> sh) + 1;  // parts, from the highest key down
+      const uint32_t low = (uint32_t)tid + 1 >= n_part ? klo : khi - ((uint32_t)tid << sh) - ((1u << sh) - 1u);
       const bool hit = (uint32_t)tid < n_part &&
                        (kind == kByCount    ? (double)c1 >= amount
                         : kind == kByMassGe ? m1 >= amount
                         : kind == kByMassGt ? m1 > amount
                                             : weight(low) < amount);
-      int b = block_first(s.red, hit);
+      int b = ops.first(hit);
       if (b >= (int)n_part) {
-        // by rounding past the last token, or every key passes
+        // every key passes, or rounding left the sum short of the last token
         if (kind == kByWeight) {
           Cross r;
           r.n = s.rc[n_part];
@@ -505,42 +643,20 @@ struct Finalize {
         }
         kind = kByCount;
         amount = (double)s.rc[n_part];
-        b = block_first(s.red, (uint32_t)tid < n_part && (double)c1 >= amount);
+        b = ops.first((uint32_t)tid < n_part && (double)c1 >= amount);
       }
-      const uint32_t nc = s.rc[b + 1] - s.rc[b];
-      const uint32_t nhi = khi - ((uint32_t)b << sh);
-      const uint32_t nlo = (uint32_t)b + 1 >= n_part ? klo : nhi - ((1u << sh) - 1u);
+      nc = s.rc[b + 1] - s.rc[b];
       cb = s.rc[b];
       mb = s.rm[b];
-      klo = nlo;
-      khi = nhi;
-      __syncthreads();
-      if (nc <= kCap) {
-        load(klo, khi, cb, mb, 1, 0);
-        return from_list(kind, amount);
-      }
-      if (klo == khi) {  // one value: every token weighs w
-        const double w = tail ? 0.0 : weight(klo);
-        double r = (double)nc;
-        if (kind == kByCount) r = amount - cb;
-        if (kind == kByMassGe || kind == kByMassGt) {
-          r = fmin(fmax(floor((amount - mb) / w), 0.0), (double)nc);
-          // the quotient is off by rounding only: settle it on the sums themselves
-          while (r > 0.0 && (kind == kByMassGe ? fma(r, w, mb) >= amount : fma(r, w, mb) > amount)) r -= 1.0;
-          while (r < (double)nc && !(kind == kByMassGe ? fma(r, w, mb) >= amount : fma(r, w, mb) > amount)) r += 1.0;
-          r = fmax(r, 1.0);
-        }
-        if (kind == kByWeight) r = weight(klo) < amount ? 0.0 : (double)nc;
-        Cross x;
-        x.n = cb + (uint32_t)r;
-        x.cum = fma(r, w, mb);
-        x.at = 0;
-        x.cut = ((uint64_t)~klo) << 32;
-        if (r > 0.0) {
-          x.at = ((uint64_t)~klo << 32) | tie_index(klo, (uint32_t)r);
-          x.cut = x.at + 1;
-        }
-        return x;
+      khi -= (uint32_t)b << sh;
+      if ((uint32_t)b + 1 < n_part) klo = khi - ((1u << sh) - 1u);
+      if (nc == 0) {  // kByWeight: the threshold falls between tokens
+        Cross r;
+        r.n = cb;
+        r.cum = mb;
+        r.cut = ((uint64_t)~khi) << 32;
+        r.at = 0;
+        return r;
       }
     }
   }
@@ -554,31 +670,49 @@ struct Finalize {
                      : kind == kByMassGe ? s.cm[tid + 1] >= amount
                      : kind == kByMassGt ? s.cm[tid + 1] > amount
                                          : pow2_eighth(-tid) <= amount;
-    int b = block_first(s.red, hit);
+    int b = ops.first(hit);
     if (b >= kBins) {
       b = kTail;
       if (kind != kByWeight) {  // a sum that rounding left short: the last token above the tail
         kind = kByCount;
         amount = (double)s.cc[kTail];
-        b = block_first(s.red, (double)s.cc[tid + 1] >= amount);
+        b = ops.first((double)s.cc[tid + 1] >= amount);
       }
     }
+    if (b >= b0 && b <= b1) return from_window(kind, amount);
     const uint32_t c = s.cc[b + 1] - s.cc[b];
-    if (!(b >= b0 && b <= b1)) {
-      const uint32_t klo = b == kTail ? kKeyLowest : lowest_key(J - b);
-      const uint32_t khi = b == 0 ? kmax : lowest_key(J - b + 1.0) - 1u;
-      if (c == 0) {  // kByWeight only: nothing in the threshold's own bin
-        Cross r;
-        r.n = s.cc[b];
-        r.cum = s.cm[b];
-        r.cut = ((uint64_t)~(khi + 1u) + 1) << 32;
-        r.at = 0;
-        return r;
-      }
-      if (c > kCap) return split(kind, amount, klo, khi, s.cc[b], s.cm[b], b == kTail);
-      load(klo, khi, s.cc[b], s.cm[b], b, b);
+    const uint32_t klo = b == kTail ? kKeyLowest : lowest_key(J - b, c8);
+    if (b < listed && s.cc[b + 1] <= (uint32_t)kThreads) {
+      // everything down to this bin fits a window and is in the lists
+      start_append();
+      each_in_lists(klo, kmax, [&](uint64_t cp) {
+        const uint32_t i = atomicAdd(&s.n, 1u);
+        if (i < (uint32_t)kThreads) s.win[i] = cp;
+      });
+      open_window(klo, 0, 0.0, 0, b);
+      return from_window(kind, amount);
     }
-    return from_list(kind, amount);
+    const uint32_t khi = b == 0 ? kmax : lowest_key(J - b + 1.0, c8) - 1u;
+    if (c == 0) {  // kByWeight only: nothing in the threshold's own bin
+      Cross r;
+      r.n = s.cc[b];
+      r.cum = s.cm[b];
+      r.cut = ((uint64_t)~khi) << 32;
+      r.at = 0;
+      return r;
+    }
+    if (c > (uint32_t)kThreads) return split(kind, amount, klo, khi, s.cc[b], c, s.cm[b], b == kTail, b < listed);
+    start_append();
+    auto put = [&](uint64_t cp) {
+      const uint32_t i = atomicAdd(&s.n, 1u);
+      if (i < (uint32_t)kThreads) s.win[i] = cp;
+    };
+    if (b < listed)
+      each_in_lists(klo, khi, put);
+    else
+      each_in_row(klo, khi, put);
+    open_window(klo, s.cc[b], s.cm[b], b, b);
+    return from_window(kind, amount);
   }
 };
 
@@ -589,19 +723,21 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
                                                                    float* __restrict__ prob, int32_t* __restrict__ kept,
                                                                    uint64_t* __restrict__ cuts) {
   __shared__ FinLds s;
+  BlockOps ops(s.red);
   const int tid = threadIdx.x;
   const int64_t row = row0 + blockIdx.x;
   const RowParams rp = row_params(a, row);
   const SamplePart* part = parts + (size_t)blockIdx.x * n_seg;
 
-  double J = -INFINITY;
-  float m = kNegInf;
-  uint32_t N = 0;
-  for (int g = 0; g < n_seg; ++g) {
-    J = fmax(J, part[g].J);
-    m = fmaxf(m, part[g].max);
-    N += part[g].n;
-  }
+  // the segments' headers, one thread each (n_seg <= kMaxSeg = kThreads)
+  const bool have = tid < n_seg;
+  const double Js = have ? part[tid].J : -INFINITY;
+  const uint32_t ns = have ? part[tid].n : 0;
+  const int nbs = have ? part[tid].nb : 0, ls = have ? part[tid].listed : kBins, nl = have ? part[tid].n_list : 0;
+  const double ms = have ? (double)part[tid].max : -INFINITY;
+  const double J = ops.max(Js);
+  const float m = (float)ops.max(ms);
+  const uint32_t N = ops.sum(ns);
   if (N == 0) {  // every token masked
     if (tid == 0) {
       if (token) token[row] = -1;
@@ -611,31 +747,37 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
     }
     return;
   }
+  const int shift = ns ? (int)fmin(J - Js, (double)kBins) : kBins;
+  if (have) {
+    s.shift[tid] = (int16_t)shift;
+    s.len[tid] = (int16_t)min(nbs, kTail);
+    s.n_list[tid] = (int16_t)nl;
+  }
+  // bins whose tokens are all listed: as far as every segment's list reaches
+  const int listed = kBins - (int)ops.max((double)(kBins - (ls >= kBins ? kBins : min(kBins, ls + shift))));
   // the segments' bins on the row's grid, in segment order
   uint32_t c = 0;
   double mass = 0.0;
+#pragma unroll 8
   for (int g = 0; g < n_seg; ++g) {
-    if (part[g].n == 0) continue;
-    const int shift = (int)fmin(J - part[g].J, (double)kBins), b = tid - shift;
-    if (tid < kTail && b >= 0 && b < min(part[g].nb, kTail)) {
-      c += part[g].cnt[b];
-      mass += part[g].mass[b];
-    }
+    const int b = tid - s.shift[g];
+    const bool in = tid < kTail && b >= 0 && b < s.len[g];
+    c += in ? part[g].cnt[b] : 0u;
+    mass += in ? part[g].mass[b] : 0.0;
   }
-  uint32_t cs = block_scan_u32(s.red, c);
-  const double ms = block_scan_f64(s.red, mass * pow2_eighth(-tid));
+  uint32_t cs = ops.scan(c);
+  const double cum = ops.scan(mass * pow2_eighth(-tid));
   if (tid == kTail) cs = N;  // the tail bin: whatever is left
-  __syncthreads();
   s.cc[tid + 1] = cs;
-  s.cm[tid + 1] = ms;
+  s.cm[tid + 1] = cum;
   if (tid == 0) {
     s.cc[0] = 0;
     s.cm[0] = 0.0;
   }
   __syncthreads();
 
-  const uint32_t kmax = ord32_canon(__float_as_uint(m));
-  Finalize<DT> f(s, RowRef<DT>(a.Z, row, a.stride, a.V), rp.c8, J, kmax);
+  const uint32_t kmax = key_of(m, RowType<DT>::kMax);
+  Finalize<DT> f(s, ops, RowRef<DT>(a.Z, row, a.stride, a.V), part, n_seg, rp.c8, J, kmax, listed);
   uint32_t n = N;
   double Z = s.cm[kBins];
   uint64_t cut = ~0ull;
@@ -658,7 +800,7 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
   if (d.n > n) d = f.locate(kByCount, (double)n);
   if (tid == 0) {
     token[row] = (int32_t)(uint32_t)d.at;
-    if (prob) prob[row] = (float)(f.weight(~(uint32_t)(d.at >> 32)) / Z);
+    if (prob) prob[row] = (float)(f.weight(comp_key(d.at)) / Z);
   }
 }
 
@@ -689,7 +831,7 @@ __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, in
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
       const float v = slot_value<DT>(x[l], i);
-      const uint32_t key = ord32_canon(__float_as_uint(fminf(v, RowType<DT>::kMax)));
+      const uint32_t key = key_of(v, RowType<DT>::kMax);
       const bool in = v > kNegInf && (((uint64_t)~key << 32) | (uint32_t)(e + i)) < cut;
       if constexpr (DT == DFLASH_BF16) {
         const uint32_t raw = (i & 1) ? x[l].w[i >> 1] >> 16 : x[l].w[i >> 1] & 0xFFFFu;
