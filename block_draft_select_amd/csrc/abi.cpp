@@ -206,10 +206,9 @@ WsLayout ws_layout(const dflash_dims& d) {
   return w;
 }
 
-// 16-byte slots a row can take, at any alignment
 static int row_slots(const dflash_rows& r) {
   const int ve = r.dtype == DFLASH_BF16 ? 8 : 4;
-  return (r.V + ve - 1 + ve - 1) / ve;
+  return (r.V + ve - 1) / ve;
 }
 
 // Slots per thread: the most whose grid still has 1024 blocks (four per CU),
@@ -219,13 +218,22 @@ SamplePlan sample_plan(const dflash_rows& r) {
   const int slots = row_slots(r);
   for (p.loads = kSampleMaxLoads;; p.loads /= 2) {
     p.n_seg = (slots + kSampleThreads * p.loads - 1) / (kSampleThreads * p.loads);
-    if (p.loads == 1 || r.R * p.n_seg >= 1024 || p.n_seg * 2 + 1 > kSampleMaxSeg) break;
+    if (p.loads == 1 || r.R * p.n_seg >= 1024 || p.n_seg * 2 > kSampleMaxSeg) break;
   }
-  p.batch = 4096 / p.n_seg > 1 ? 4096 / p.n_seg : 1;
-  const size_t rows = (size_t)(r.R < p.batch ? r.R : p.batch);
+  const bool all = p.loads == 1;
+  // One slot per thread: few rows, and the whole segment is listed, so that
+  // the one block that finishes a row needs no other.  Longer segments list
+  // what ordinary cuts take (top-k of 50, peaked rows).
+  p.cap = all ? kSampleThreads * (r.dtype == DFLASH_BF16 ? 8 : 4) : p.loads == 2 ? 256 : 64;
+  p.batch = std::max(1, 4096 / p.n_seg);
+  if (!all) p.batch = std::min<int64_t>(p.batch, 1024);
+  const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);
   p.parts = 0;
-  p.cuts = align256(rows * p.n_seg * sizeof(SamplePart));
-  p.total = align256(p.cuts + rows * sizeof(uint64_t));
+  p.lists = align256(rows * p.n_seg * sizeof(SamplePart));
+  p.cuts = p.lists + align256(rows * p.n_seg * p.cap * (r.dtype == DFLASH_BF16 ? sizeof(uint32_t) : sizeof(uint64_t)));
+  p.asks = p.cuts + align256(rows * sizeof(uint64_t));
+  p.asked = p.asks + (all ? 0 : align256(rows * sizeof(SampleAsk)));
+  p.total = p.asked + (all ? 0 : align256(rows * kSampleAsk * sizeof(uint64_t)));
   return p;
 }
 

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, in
   if constexpr (REST) {
     for (int i = tid; i < kMaskWords; i += kThreads) mask[i] = 0;
     __syncthreads();
-    const int e0 = z.first(s0);
+    const int e0 = s0 * VE;
     int idx;
     for (int k = tid; k < a.K; k += kThreads)
       if (listed(a, row, k, idx) && idx >= e0 && idx < e0 + kThreads * NL * VE)
@@ -286,8 +286,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   const int64_t row = blockIdx.x / n_seg;
   const RowRef<DT> z(a.S, row, a.stride, a.V);
   E* o = static_cast<E*>(dS) + row * d_stride;
-  const bool same = (reinterpret_cast<uintptr_t>(o) & 15u) == (reinterpret_cast<uintptr_t>(z.p) & 15u);
-  const int s0 = seg * (kThreads * NL), e0 = z.first(s0), e1 = e0 + kThreads * NL * VE;
+  const int s0 = seg * (kThreads * NL), e0 = s0 * VE, e1 = e0 + kThreads * NL * VE;
   double f = (a.weight ? (double)a.weight[row] : 1.0) * (grad_loss ? (double)grad_loss[row] : 1.0);
   const bool off = (a.weight && a.weight[row] == 0.0f) || (grad_loss && grad_loss[row] == 0.0f);
   f /= a.tau;
@@ -322,7 +321,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   }
   if (off || c == -INFINITY || lse == -INFINITY) {  // no gradient: weight zero, or an empty row on either side
 #pragma unroll
-    for (int l = 0; l < NL; ++l) store_slot<DT>(o, z, s0 + l * kThreads + tid, Slot{{0, 0, 0, 0}}, same);
+    for (int l = 0; l < NL; ++l) store_slot<DT>(o, a.V, s0 + l * kThreads + tid, Slot{{0, 0, 0, 0}});
     return;
   }
   const bool with_rest = REST && rest != -INFINITY;
@@ -349,13 +348,13 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
       else
         y.w[i] = __float_as_uint(g);
     }
-    store_slot<DT>(o, z, s0 + l * kThreads + tid, y, same);
+    store_slot<DT>(o, a.V, s0 + l * kThreads + tid, y);
   }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
     const int k = j * kThreads + tid;
-    if (k < a.K && seen[k] >= 0 && seen[k] >= e0 && seen[k] < e1) {  // e0 < 0 in a row that starts inside a slot
+    if (k < a.K && seen[k] >= e0 && seen[k] < e1) {
       double p = 0.0;  // every entry of this token, in list order
       for (int q = 0; q < a.K; ++q)
         if (seen[q] == seen[k]) p += prob[q];

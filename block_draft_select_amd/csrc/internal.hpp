@@ -173,20 +173,26 @@ hipError_t launch_conv2tap(const dflash_dims& d, const void* x, const void* x0, 
 // slots of a row; its bins go to one SamplePart
 constexpr int kSampleThreads = 512;
 constexpr int kSampleBins = 512;
-constexpr int kSampleList = 256;
-constexpr int kSampleMaxSeg = 512;  // blocks per row
-constexpr int kSampleMaxLoads = 8;  // at most 32768 elements a block, what its 64-bit bin sums hold
+constexpr int kSampleMaxSeg = 512;   // blocks per row
+constexpr int kSampleMaxLoads = 8;
+constexpr int kSamplePick = 1024;    // tokens a block picks out of a segment
+constexpr int kSampleAsk = 8192;     // tokens outside the lists that a row can ask for
 struct SamplePart {
   double J;      // floor of the segment's maximum in eighths of an octave; -inf: nothing unmasked
   float max;     // the maximum
   uint32_t n;    // unmasked tokens
   int32_t nb;    // bins in use
-  int32_t listed;  // the tokens of bins 0 .. listed - 1 are in `list`
-  int32_t n_list;
-  int32_t pad;
-  double mass[kSampleBins];   // bin b: weights over 2^((J - b) / 8)
-  uint32_t cnt[kSampleBins];  // and tokens
-  uint64_t list[kSampleList];  // (~key, index) of the segment's largest tokens, in any order
+  int32_t listed;  // the tokens of bins 0 .. listed - 1 are in the segment's list
+  double mass[kSampleBins];    // bin b: weights over 2^((J - b) / 8)
+  uint32_t upto[kSampleBins];  // tokens of bins 0 .. b
+};
+// bins whose tokens a row needs beyond the lists: up to two ranges
+enum { kSampleAskNone = 0, kSampleAskBins = 1, kSampleAskRow = 2 /* more tokens than kSampleAsk: the row is read again */ };
+struct SampleAsk {
+  int32_t kind;
+  uint32_t n;  // tokens collected
+  int32_t b0[2], b1[2];
+  uint32_t klo[2], khi[2];
 };
 struct SampleArgs {
   const void* Z;
@@ -209,8 +215,9 @@ struct SampleOut {
 struct SamplePlan {
   int loads;      // slots per thread of the bin kernel
   int n_seg;      // blocks per row
+  int cap;        // tokens a block lists
   int64_t batch;  // rows per pass over the workspace
-  size_t parts, cuts, total;
+  size_t parts, lists, cuts, asks, asked, total;
 };
 SamplePlan sample_plan(const dflash_rows& r);
 hipError_t launch_sample(int32_t dtype, const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl,

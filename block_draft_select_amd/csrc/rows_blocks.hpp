@@ -1,13 +1,12 @@
 // Device building blocks of the operators on rows of vocabulary logits
 // (dflash_sample, dflash_filter, dflash_distill, dflash_distill_grad): 16-byte
-// access to rows of any length, stride and alignment, and fp64 weights.
+// access to rows of any length, stride and alignment.
 //
-// A row starts at any element-aligned address.  Its 16-byte aligned slots
-// are numbered from the one holding its first element, so slot s covers
-// elements s * VE - phase .. s * VE - phase + VE - 1 (VE elements of 16
-// bytes; phase: elements between the slot's start and the row's).  Whole
-// slots move as one 16-byte access; the partial first and last ones element
-// by element, so nothing outside the row is read or written.
+// A row is cut into slots of 16 bytes from its first element on (VE elements
+// each), wherever that element lies: global memory instructions take any
+// alignment here, and a wave's 1 KB touches at most one cache line more.  Only
+// the last slot of a row can be short; it is read through the 16 bytes that
+// end with the row, so nothing outside the row is read or written.
 #pragma once
 
 #include "device_util.hpp"
@@ -48,49 +47,63 @@ __device__ __forceinline__ float slot_value(const Slot& s, int i) {
     return __uint_as_float(s.w[i]);
 }
 
+// 16 bytes at an address aligned to two bytes only
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 template <int DT>
 struct RowRef {
   using E = typename RowType<DT>::elem;
   static constexpr int VE = RowType<DT>::VE;
-  const E* p;    // first element
-  int phase;     // elements of slot 0 before the row's first
+  const E* p;
   int V;
 
   __device__ __forceinline__ RowRef(const void* base, int64_t row, int64_t stride, int V_)
-      : p(static_cast<const E*>(base) + row * stride), V(V_) {
-    phase = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(E));
-  }
-  __device__ __forceinline__ int first(int slot) const { return slot * VE - phase; }  // first element of a slot
-  __device__ __forceinline__ bool whole(int slot) const {
-    const int e = first(slot);
-    return e >= 0 && e + VE <= V;
-  }
-  // the slot's elements; those outside the row read as masked (-inf)
+      : p(static_cast<const E*>(base) + row * stride), V(V_) {}
+  __device__ __forceinline__ int slots() const { return (V + VE - 1) / VE; }
+
+  // the slot's elements; those past the row's end read as masked (-inf)
   template <bool STREAM = false>
   __device__ __forceinline__ Slot load(int slot) const {
+    const int e = slot * VE;
     Slot s;
-    const int e = first(slot);
-    if (e >= 0 && e + VE <= V) {
-      uint4 v;
+    if (e + VE <= V) {
+      const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p + e);
+      u32x4_any v;
       if constexpr (STREAM)
-        v = load_stream16(p + e);
+        v = __builtin_nontemporal_load(q);
       else
-        v = *reinterpret_cast<const uint4*>(p + e);
+        v = *q;
       s.w[0] = v.x, s.w[1] = v.y, s.w[2] = v.z, s.w[3] = v.w;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s.w[k] = RowType<DT>::kMasked;
-#pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (e + i >= 0 && e + i < V) {
-          if constexpr (DT == DFLASH_BF16) {
-            const uint32_t b = p[e + i];
-            s.w[i >> 1] = (i & 1) ? ((s.w[i >> 1] & 0x0000FFFFu) | (b << 16)) : ((s.w[i >> 1] & 0xFFFF0000u) | b);
-          } else {
-            s.w[i] = p[e + i];
-          }
-        }
+      return s;
     }
+    constexpr uint64_t kFill = (uint64_t)RowType<DT>::kMasked << 32 | RowType<DT>::kMasked;
+    uint64_t lo = kFill, hi = kFill;
+    if (e < V) {
+      const int bits = (V - e) * (int)sizeof(E) * 8;  // valid bits, below 128
+      uint64_t a = 0, b = 0;
+      if (V >= VE) {
+        const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p + V - VE);
+        a = (uint64_t)v.y << 32 | v.x;
+        b = (uint64_t)v.w << 32 | v.z;
+        const int sh = 128 - bits;  // move the row's last elements to the slot's start
+        if (sh < 64) {
+          a = a >> sh | b << (64 - sh);
+          b >>= sh;
+        } else {
+          a = b >> (sh - 64);
+          b = 0;
+        }
+      } else {  // the whole row is shorter than a slot
+#pragma unroll 1
+        for (int i = 0; i < V; ++i) {
+          const int at = i * (int)sizeof(E) * 8;
+          if (at < 64) a |= (uint64_t)p[i] << at; else b |= (uint64_t)p[i] << (at - 64);
+        }
+      }
+      lo = bits < 64 ? a | kFill << bits : a;
+      hi = bits <= 64 ? kFill : b | kFill << (bits - 64);
+    }
+    s.w[0] = (uint32_t)lo, s.w[1] = (uint32_t)(lo >> 32), s.w[2] = (uint32_t)hi, s.w[3] = (uint32_t)(hi >> 32);
     return s;
   }
 };
@@ -103,8 +116,6 @@ __device__ __forceinline__ float row_value(const RowRef<DT>& z, int i) {
   else
     return __uint_as_float(z.p[i]);
 }
-
-// ---------------------------------------------------------------- stores
 
 // fp32 -> bf16, nearest even (NaN stays NaN)
 __device__ __forceinline__ uint32_t bf16_round(float x) {
@@ -121,25 +132,24 @@ __device__ __forceinline__ typename RowType<DT>::elem to_elem(float x) {
     return __float_as_uint(x);
 }
 
-// Store a slot that was numbered by `in` to the row `out` of another tensor
-// (element for element).  One 16-byte store where the slot is whole and the
-// output row has the same alignment, else element by element.
+// a slot to a row of V elements
 template <int DT>
-__device__ __forceinline__ void store_slot(typename RowType<DT>::elem* out, const RowRef<DT>& in, int slot,
-                                           const Slot& s, bool same_phase) {
+__device__ __forceinline__ void store_slot(typename RowType<DT>::elem* out, int V, int slot, const Slot& s) {
+  using E = typename RowType<DT>::elem;
   constexpr int VE = RowType<DT>::VE;
-  const int e = in.first(slot);
-  if (same_phase && in.whole(slot)) {
-    *reinterpret_cast<uint4*>(out + e) = make_uint4(s.w[0], s.w[1], s.w[2], s.w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VE; ++i)
-      if (e + i >= 0 && e + i < in.V) {
-        if constexpr (DT == DFLASH_BF16)
-          out[e + i] = (uint16_t)((i & 1) ? s.w[i >> 1] >> 16 : s.w[i >> 1]);
-        else
-          out[e + i] = s.w[i];
-      }
+  const int e = slot * VE;
+  if (e + VE <= V) {
+    u32x4_any v;
+    v.x = s.w[0], v.y = s.w[1], v.z = s.w[2], v.w = s.w[3];
+    *reinterpret_cast<u32x4_any*>(out + e) = v;
+  } else if (e < V) {
+    uint64_t a = (uint64_t)s.w[1] << 32 | s.w[0], b = (uint64_t)s.w[3] << 32 | s.w[2];
+#pragma unroll 1
+    for (int i = e; i < V; ++i) {
+      out[i] = (E)a;
+      a = a >> (sizeof(E) * 8) | b << (64 - sizeof(E) * 8);
+      b >>= sizeof(E) * 8;
+    }
   }
 }
 

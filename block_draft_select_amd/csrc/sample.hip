@@ -11,18 +11,25 @@
 //
 // It is answered without sorting the row.  In units of an eighth of an octave
 // a weight is 2^(t / 8), t = z 8 log2(e) / T, and floor(t) bins the tokens in
-// their order: (1) sample_hist_kernel counts the tokens and sums the weights
-// of each bin of a row segment; (2) sample_finalize_kernel, one block per
-// row, adds the segments' bins, scans them, finds the bin of the crossing
-// and gathers and sorts that bin's tokens alone, from the row.  A bin of more tokens
-// than the list holds is split again by key ranges first; if one value alone
-// has that many tokens, its tokens share one weight and the crossing is a
-// division.  (3) sample_apply_kernel (dflash_filter) copies the kept tokens.
+// their order.
+// (1) sample_hist_kernel (sample_count_kernel for long bf16 segments) counts the
+//     tokens and sums the weights of each bin of a row segment, and lists the
+//     segment's largest tokens in the order of their bins.
+// (2) sample_finalize_kernel, one block per row, adds the segments' bins,
+//     scans them, finds the bin of the crossing and ranks that bin's tokens
+//     alone: a window of at most 512 tokens; a fuller bin is narrowed by key
+//     ranges first, and tokens of one value share one weight, so that their
+//     crossing is a division.
+// (3) Short segments list all their tokens.  Rows in long ones whose cut or
+//     draw falls outside the lists ask for the bins they need;
+//     sample_gather_kernel collects those from all segments at once, and
+//     the row is finished by a second run of (2).
+// (4) sample_apply_kernel (dflash_filter) copies the kept tokens.
 //
 // Counts are exact and sums do not depend on the order of the atomics: a bin
-// adds the mantissas of 2^frac(t / 8) as 64-bit integers (the fraction bits of
-// a double in [1, 1.0906) stay below 2^48.6, so 32768 of them fit), which keeps
-// 52 bits below each token's own weight.  Decisions next to a border need
+// adds the mantissas of 2^frac(t / 8) as 64-bit integers (the upper 51 fraction
+// bits of a double in [1, 1.0906) stay below 2^47.6, so 65536 of them fit),
+// which keeps 51 bits below each token's own weight.  Decisions next to a border need
 // such sums: they compare running sums over the whole vocabulary.
 #include "rows_blocks.hpp"
 
@@ -39,7 +46,6 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kBins = kSampleBins;  // 64 octaves; the last bin collects everything below (weight under 2^-63.9)
 constexpr int kTail = kBins - 1;
 constexpr int kCols = 4;            // copies of the bins a wave's lanes spread over
-constexpr int kCap = 4096;          // tokens of one bin held in LDS
 static_assert(kThreads == kBins, "one thread per bin");
 
 constexpr uint32_t kKeyLowest = 0x00800000u;  // ordered key of the lowest finite fp32
@@ -79,7 +85,7 @@ struct RowParams {
 };
 
 __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row) {
-  const int64_t g = row / a.group;
+  const uint32_t g = (uint32_t)row / (uint32_t)a.group;  // rows fit 23 bits
   const float T = a.T ? a.T[g] : 1.0f;
   const bool greedy = !(T > 0.0f);
   RowParams r;
@@ -198,134 +204,362 @@ __device__ __forceinline__ uint32_t lowest_key(double j, double c8) {
   return l;
 }
 
+// ---------------------------------------------------------------- list entries
+// A listed token: bf16 rows in 32 bits (~key of 16 bits, place in the
+// segment), fp32 rows in 64 (~key, index in the row).
+
+template <int DT>
+struct Entry;
+template <>
+struct Entry<DFLASH_BF16> {
+  using T = uint32_t;
+  static __device__ __forceinline__ T make(uint32_t key, int place, int) { return ((~key >> 16) << 16) | (uint32_t)place; }
+  static __device__ __forceinline__ uint64_t comp(T e, int first) {
+    return ((uint64_t)~ord32_of_k16((~e >> 16) & 0xFFFFu) << 32) | (uint32_t)(first + (int)(e & 0xFFFFu));
+  }
+};
+template <>
+struct Entry<DFLASH_F32> {
+  using T = uint64_t;
+  static __device__ __forceinline__ T make(uint32_t key, int place, int first) {
+    return ((uint64_t)~key << 32) | (uint32_t)(first + place);
+  }
+  static __device__ __forceinline__ uint64_t comp(T e, int) { return e; }
+};
+__device__ __forceinline__ uint32_t comp_key(uint64_t c) { return ~(uint32_t)(c >> 32); }
+
 // ---------------------------------------------------------------- (1) bins of a segment
 
-template <int DT, int NL>
-__global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int64_t row0, int n_seg,
-                                                               SamplePart* __restrict__ parts) {
-  constexpr int VE = RowType<DT>::VE;
-  __shared__ uint64_t mass[kBins * kCols];
-  __shared__ uint32_t cnt[kBins * kCols];
-  __shared__ Red red;
-  __shared__ uint32_t n_list;
-  BlockOps ops(red);
-  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
-  const int64_t row = row0 + blockIdx.x / n_seg;
-  const RowRef<DT> z(a.Z, row, a.stride, a.V);
-  const double c8 = row_params(a, row).c8;
+template <int COLS>
+struct HistLds {
+  uint64_t mass[kBins * COLS];
+  uint32_t cnt[kBins * COLS];
+  uint32_t key[kSamplePick];    // tokens to be listed
+  uint32_t place[kSamplePick];
+  uint32_t n_pick;
+  Red red;
+};
 
-  Slot x[NL];
-  const int s0 = seg * (kThreads * NL) + tid;
-#pragma unroll
-  for (int l = 0; l < NL; ++l) x[l] = z.template load<true>(s0 + l * kThreads);
+// `times` equal tokens into their bin
+template <int COLS>
+__device__ __forceinline__ void bin_token(HistLds<COLS>& s, double c8, double J, float v, uint32_t times) {
+  const double t = (double)v * c8, fl = floor(t);
+  const int b = (int)fmin(J - fl, (double)kTail), at = b * COLS + (threadIdx.x & (COLS - 1));
+  atomicAdd(&s.cnt[at], times);
+  if (b < kTail)
+    atomicAdd((unsigned long long*)&s.mass[at],
+              (unsigned long long)(__double_as_longlong(exp2_eighth(t - fl)) >> 1) * times);
+}
 
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    mass[c * kBins + tid] = 0;
-    cnt[c * kBins + tid] = 0;
-  }
-  if (tid == 0) n_list = 0;
-  float m = kNegInf;
-#pragma unroll
-  for (int l = 0; l < NL; ++l)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[l], i));  // NaN drops out
-  m = (float)ops.max((double)fminf(m, RowType<DT>::kMax));
-
-  SamplePart& out = parts[blockIdx.x];
-  if (m == kNegInf) {
-    if (tid == 0) {
-      out.J = -INFINITY;
-      out.max = kNegInf;
-      out.n = 0;
-      out.nb = 0;
-      out.listed = kBins;
-      out.n_list = 0;
-    }
-    return;
-  }
-  const double J = floor((double)m * c8);
-  const int col = tid & (kCols - 1);
-#pragma unroll
-  for (int l = 0; l < NL; ++l)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float v = slot_value<DT>(x[l], i);
-      if (v > kNegInf) {
-        const double t = (double)fminf(v, RowType<DT>::kMax) * c8, fl = floor(t);
-        const int b = (int)fmin(J - fl, (double)kTail);
-        atomicAdd(&cnt[b * kCols + col], 1u);
-        if (b < kTail)
-          atomicAdd((unsigned long long*)&mass[b * kCols + col], (unsigned long long)__double_as_longlong(exp2_eighth(t - fl)));
-      }
-    }
-  __syncthreads();
+// after a barrier: the bins to memory; returns the number of leading bins that
+// are listed (at most `cap` tokens together) and leaves in cnt[b * COLS]
+// where bin b's list starts
+template <int COLS>
+__device__ __forceinline__ int write_bins(HistLds<COLS>& s, BlockOps& ops, SamplePart& out, double J, float m, int cap) {
+  const int tid = threadIdx.x;
   uint32_t c = 0, mirror = 0;  // mirror: the bin counted from the far end
   uint64_t f = 0;
 #pragma unroll
-  for (int k = 0; k < kCols; ++k) {
-    c += cnt[tid * kCols + k];
-    f += mass[tid * kCols + k];
-    mirror += cnt[(kBins - 1 - tid) * kCols + k];
+  for (int k = 0; k < COLS; ++k) {
+    c += s.cnt[tid * COLS + k];
+    f += s.mass[tid * COLS + k];
+    mirror += s.cnt[(kBins - 1 - tid) * COLS + k];
   }
-  f -= (uint64_t)c * kOneBits;  // modulo 2^64: the fraction bits' sum
+  f -= (uint64_t)c * (kOneBits >> 1);  // modulo 2^64: the fraction bits' sum
   const uint32_t upto = ops.scan(c);
-  const int nb = kBins - ops.first(mirror != 0);  // bins in use
-  // the first bins with at most kSampleList tokens together are listed
-  const int listed = ops.first(upto > (uint32_t)kSampleList);
+  const int nb = kBins - ops.first(mirror != 0);       // bins in use
+  const int listed = ops.first(upto > (uint32_t)cap);
+  s.cnt[tid * COLS] = upto - c;
   if (tid < nb) {
-    out.cnt[tid] = c;
-    out.mass[tid] = tid < kTail ? (double)c + (double)f * 0x1p-52 : 0.0;
+    out.upto[tid] = upto;
+    out.mass[tid] = tid < kTail ? (double)c + (double)f * 0x1p-51 : 0.0;
   }
-  if (listed > 0) {
-    const uint32_t least = listed >= kBins ? kKeyLowest : lowest_key(J - (double)(listed - 1), c8);
-#pragma unroll
-    for (int l = 0; l < NL; ++l) {
-      const int e = z.first(s0 + l * kThreads);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float v = slot_value<DT>(x[l], i);
-        const uint32_t key = key_of(v, RowType<DT>::kMax);
-        if (v > kNegInf && key >= least) {
-          const uint32_t at = atomicAdd(&n_list, 1u);
-          if (at < (uint32_t)kSampleList) out.list[at] = ((uint64_t)~key << 32) | (uint32_t)(e + i);
-        }
-      }
-    }
-  }
-  __syncthreads();
   if (tid == kThreads - 1) {
     out.J = J;
     out.max = m;
     out.n = upto;
     out.nb = nb;
     out.listed = listed;
-    out.n_list = (int32_t)min(n_list, (uint32_t)kSampleList);
   }
+  __syncthreads();
+  return listed;
+}
+
+__device__ __forceinline__ void empty_part(SamplePart& out) {
+  if (threadIdx.x == 0) {
+    out.J = -INFINITY;
+    out.max = kNegInf;
+    out.n = 0;
+    out.nb = 0;
+    out.listed = kBins;
+  }
+}
+
+// a token into the list, which is in the order of its bins
+template <int DT, int COLS>
+__device__ __forceinline__ void list_token(HistLds<COLS>& s, typename Entry<DT>::T* list, double c8, double J, uint32_t key,
+                                           int place, int first) {
+  const int b = (int)fmin(J - floor(key_value(key) * c8), (double)kTail);
+  list[atomicAdd(&s.cnt[b * COLS], 1u)] = Entry<DT>::make(key, place, first);
+}
+
+// a token among those to be listed (few: picked first, then listed densely)
+template <int COLS>
+__device__ __forceinline__ void pick(HistLds<COLS>& s, uint32_t key, int place) {
+  const uint32_t i = atomicAdd(&s.n_pick, 1u);
+  if (i < (uint32_t)kSamplePick) {
+    s.key[i] = key;
+    s.place[i] = (uint32_t)place;
+  }
+}
+template <int DT, int COLS>
+__device__ __forceinline__ void list_picked(HistLds<COLS>& s, typename Entry<DT>::T* list, double c8, double J, int first) {
+  __syncthreads();
+  const int n = (int)min(s.n_pick, (uint32_t)kSamplePick);
+  for (int i = threadIdx.x; i < n; i += kThreads) list_token<DT>(s, list, c8, J, s.key[i], (int)s.place[i], first);
+}
+
+// every token through the fp64 weight
+template <int DT, int NL>
+__global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
+                                                               SamplePart* __restrict__ parts,
+                                                               typename Entry<DT>::T* __restrict__ lists) {
+  constexpr int VE = RowType<DT>::VE, COLS = kCols;
+  constexpr float kMax = RowType<DT>::kMax;
+  __shared__ HistLds<COLS> s;
+  BlockOps ops(s.red);
+  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
+  const int64_t row = row0 + blockIdx.x / n_seg;
+  const RowRef<DT> z(a.Z, row, a.stride, a.V);
+  const double c8 = row_params(a, row).c8;
+  const int s0 = seg * (kThreads * NL) + tid;
+  Slot x[NL];
+#pragma unroll
+  for (int l = 0; l < NL; ++l) x[l] = z.template load<true>(s0 + l * kThreads);
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) {
+    s.mass[c * kBins + tid] = 0;
+    s.cnt[c * kBins + tid] = 0;
+  }
+  if (tid == 0) s.n_pick = 0;
+  float m = kNegInf;
+#pragma unroll
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[l], i));  // NaN drops out
+  m = (float)ops.max((double)fminf(m, kMax));
+  SamplePart& out = parts[blockIdx.x];
+  if (m == kNegInf) return empty_part(out);
+  const double J = floor((double)m * c8);
+#pragma unroll
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DT>(x[l], i);
+      if (v > kNegInf) bin_token(s, c8, J, fminf(v, kMax), 1u);
+    }
+  __syncthreads();
+  const int listed = write_bins(s, ops, out, J, m, cap);
+  if (listed == 0) return;
+  typename Entry<DT>::T* list = lists + (size_t)blockIdx.x * cap;
+  const int first = seg * (kThreads * NL) * VE;
+  if constexpr (NL == 1) {  // cap holds the whole segment
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DT>(x[0], i);
+      if (v > kNegInf) list_token<DT>(s, list, c8, J, key_of(v, kMax), tid * VE + i, first);
+    }
+  } else {
+    const uint32_t least = listed >= kBins ? kKeyLowest : lowest_key(J - (double)(listed - 1), c8);
+#pragma unroll
+    for (int l = 0; l < NL; ++l)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float v = slot_value<DT>(x[l], i);
+        const uint32_t key = key_of(v, kMax);
+        if (v > kNegInf && key >= least) pick(s, key, (tid + l * kThreads) * VE + i);
+      }
+    list_picked<DT>(s, list, c8, J, first);
+  }
+}
+
+// Long segments of bf16 rows: a token is one of few values, so values are
+// counted first and each value present is weighed once (the same sums, bit for
+// bit).  Counted directly are kMags magnitudes of either sign, up to the
+// largest that can matter (that of the maximum, or of the lowest logit that
+// still has weight); their ordered keys, packed two to a register, map to
+// counters without a branch: counter 0 takes all lower keys (masked, or below
+// every bin), 1 .. kMags the negative ones, kMags + 1 everything nearer to
+// zero, then the positive ones.  The few tokens nearer to zero are picked out
+// and weighed one by one.
+constexpr int kMags = 1920;  // 15 binades
+constexpr int kCounters = 2 * kMags + 2;
+
+template <int NL>
+__global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
+                                                                SamplePart* __restrict__ parts, uint32_t* __restrict__ lists) {
+  constexpr int VE = 8, ND = NL * 4;
+  constexpr float kMax = RowType<DFLASH_BF16>::kMax;
+  constexpr uint32_t kMaskedKey = 0x007Fu, kInfKey = 0xFF80u;  // 16-bit keys of -inf and +inf
+  __shared__ HistLds<1> s;
+  __shared__ uint32_t count[kCounters];
+  __shared__ uint32_t n_masked;
+  BlockOps ops(s.red);
+  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
+  const int64_t row = row0 + blockIdx.x / n_seg;
+  const RowRef<DFLASH_BF16> z(a.Z, row, a.stride, a.V);
+  const double c8 = row_params(a, row).c8;
+  const int s0 = seg * (kThreads * NL) + tid;
+  Slot x[NL];
+#pragma unroll
+  for (int l = 0; l < NL; ++l) x[l] = z.load<true>(s0 + l * kThreads);
+  for (int i = tid; i < kCounters; i += kThreads) count[i] = 0;
+  s.mass[tid] = 0;
+  s.cnt[tid] = 0;
+  if (tid == 0) {
+    s.n_pick = 0;
+    n_masked = 0;
+  }
+  uint32_t o[ND];  // ordered 16-bit keys, two a word
+  uint32_t top = 0;
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+    o[d] = ord16x2(x[d >> 2].w[d & 3]);
+    top = max_u16x2(top, o[d]);
+  }
+  const uint32_t kmax16 = (uint32_t)ops.max((double)max(top & 0xFFFFu, top >> 16));
+  SamplePart& out = parts[blockIdx.x];
+  const bool odd_values = kmax16 >= kInfKey;  // +inf or NaN: every token one by one
+  float m;
+  if (!odd_values) {
+    m = kmax16 <= kMaskedKey ? kNegInf : __uint_as_float(unord32(ord32_of_k16(kmax16)));
+  } else {
+    m = kNegInf;
+#pragma unroll 1
+    for (int l = 0; l < NL; ++l) {
+      const Slot y = z.load(s0 + l * kThreads);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DFLASH_BF16>(y, i));
+    }
+    m = (float)ops.max((double)fminf(m, kMax));
+  }
+  if (m == kNegInf) return empty_part(out);
+  const double J = floor((double)m * c8);
+  // the largest magnitude with a counter: m's, or that of the logit 512 eighths of an octave below it
+  const double reach = fmin(fmax(fabs((double)m), fabs((double)m - 512.0 / c8)), (double)kMax);
+  const int top_mag = min((int)(__float_as_uint((float)reach) >> 16) + 1, 0x7F7F);
+  const uint32_t base = (uint32_t)max(1, top_mag + 1 - kMags);  // smallest magnitude with a counter
+  const uint32_t below = 0x7FFFu - base - kMags;                // the key under the lowest counted one
+  bool one_by_one = odd_values;
+  if (!odd_values) {
+    const uint32_t below2 = below * 0x10001u, mid2 = (kMags + 1) * 0x10001u, pos2 = (kMags + 2 * base) * 0x10001u;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      const uint32_t r = subsat_u16x2(o[d], below2);
+      const u16x2 i2 = __builtin_bit_cast(u16x2, min_u16x2(r, mid2)) + __builtin_bit_cast(u16x2, subsat_u16x2(r, pos2));
+      const uint32_t i = __builtin_bit_cast(uint32_t, i2);
+      atomicAdd(&count[i & 0xFFFFu], 1u);
+      atomicAdd(&count[i >> 16], 1u);
+    }
+    __syncthreads();
+    const uint32_t n_mid = count[kMags + 1];
+    one_by_one = n_mid > (uint32_t)kSamplePick;
+    if (!one_by_one && n_mid) {  // the tokens near zero: keys within `base` of either zero
+      const uint32_t from2 = (0x8000u - base) * 0x10001u, width2 = 2 * base * 0x10001u;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const u16x2 r2 = __builtin_bit_cast(u16x2, o[d]) - __builtin_bit_cast(u16x2, from2);
+        const uint32_t near = subsat_u16x2(width2, __builtin_bit_cast(uint32_t, r2));
+        if (near) {
+          if (near & 0xFFFFu) s.key[atomicAdd(&s.n_pick, 1u)] = o[d] & 0xFFFFu;
+          if (near >> 16) s.key[atomicAdd(&s.n_pick, 1u)] = o[d] >> 16;
+        }
+      }
+    }
+    if (!one_by_one && count[0]) {  // of the low ones, how many are masked
+      u16x2 k2 = {0, 0};
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        k2 += __builtin_bit_cast(u16x2, min_u16x2(subsat_u16x2((kMaskedKey + 1) * 0x10001u, o[d]), 0x10001u));
+      const uint32_t k = wave_sum_u32((uint32_t)k2.x + (uint32_t)k2.y);
+      if ((tid & 63) == 0) atomicAdd(&n_masked, k);
+    }
+    __syncthreads();
+    if (!one_by_one) {
+      // the counted values, then the picked tokens (counter 0 and the middle one are not values)
+#pragma unroll 1
+      for (int i = tid; i < kCounters + (int)n_mid; i += kThreads) {
+        uint32_t c = 1, k16;
+        if (i < kCounters) {
+          c = i != 0 && i != kMags + 1 ? count[i] : 0u;
+          k16 = i <= kMags ? below + (uint32_t)i : 0x8000u + base + (uint32_t)(i - kMags - 2);
+        } else {
+          k16 = s.key[i - kCounters];
+        }
+        if (c) bin_token(s, c8, J, __uint_as_float(unord32(ord32_of_k16(k16))), c);
+      }
+      if (tid == 0) atomicAdd(&s.cnt[kTail], count[0] - n_masked);
+    }
+  }
+  if (one_by_one) {  // a NaN or infinity, or many values near zero: every token through the fp64 weight
+#pragma unroll 1
+    for (int l = 0; l < NL; ++l) {
+      const Slot y = z.load(s0 + l * kThreads);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float v = slot_value<DFLASH_BF16>(y, i);
+        if (v > kNegInf) bin_token(s, c8, J, fminf(v, kMax), 1u);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) s.n_pick = 0;
+  const int listed = write_bins(s, ops, out, J, m, cap);
+  if (listed == 0) return;
+  const uint32_t least = listed >= kBins ? kKeyLowest : lowest_key(J - (double)(listed - 1), c8);
+  // the smallest 16-bit key whose value reaches it; -0 counts as +0
+  uint32_t least16 = least >= 0x80000000u ? (least + 0xFFFFu) >> 16 : least >> 16;
+  if (least16 == 0x8000u) least16 = 0x7FFFu;
+  const uint32_t under2 = (least16 - 1u) * 0x10001u;
+  auto put = [&](uint32_t k16, int place) {
+    if (k16 <= kInfKey) pick(s, k16 == kInfKey ? key_of(kMax, kMax) : ord32_of_k16(k16), place);  // above: NaN
+  };
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+    const uint32_t in = subsat_u16x2(o[d], under2);
+    if (in) {
+      const int place = (tid + (d >> 2) * kThreads) * VE + 2 * (d & 3);
+      if (in & 0xFFFFu) put(o[d] & 0xFFFFu, place);
+      if (in >> 16) put(o[d] >> 16, place + 1);
+    }
+  }
+  list_picked<DFLASH_BF16>(s, lists + (size_t)blockIdx.x * cap, c8, J, 0);
 }
 
 // ---------------------------------------------------------------- (2) cuts and draw of a row
 
 enum { kByCount, kByMassGe, kByMassGt, kByWeight };
-
+// kAll: the lists hold every token.  kFirst: they hold the largest; rows that
+// need others ask for them.  kSecond: the rows that asked.
+enum { kAll, kFirst, kSecond };
 constexpr int kMaxSeg = kSampleMaxSeg;
 
 struct FinLds {
-  uint64_t big[kCap];       // tokens of one bin as (~key, index), in any order
-  uint64_t win[kThreads];   // the window: sorted, ascending = the row's order
+  uint64_t win[kThreads];   // the window: sorted (~key, index), ascending = the row's order
   double wcum[kThreads];    // and the running sums at its tokens
-  uint64_t mass[kBins];     // bins of a split
+  uint64_t mass[kBins];     // parts of a key range
   uint32_t cnt[kBins];
   uint32_t cc[kBins + 1];   // tokens before each bin
   double cm[kBins + 1];     // their weight
-  uint32_t rc[kBins + 1];   // the same inside a split
-  double rm[kBins + 1];
   int16_t shift[kMaxSeg];   // a segment's first bin on the row's grid
-  int16_t len[kMaxSeg];     // its bins and its listed tokens
-  int16_t n_list[kMaxSeg];
+  int16_t nb[kMaxSeg];      // its bins
+  uint32_t n_seg[kMaxSeg];  // its unmasked tokens
+  uint32_t from[kMaxSeg];   // its listed tokens of some bins: from .. to - 1
+  uint32_t to[kMaxSeg];
   Red red;
   uint32_t n;
-  uint64_t at;
+  uint32_t before_n;
+  double before_m;
 };
 
 // where a running count or sum crosses a value
@@ -336,16 +570,18 @@ struct Cross {
   uint64_t at;   // (~key, index) of the last of them (not for kByWeight)
 };
 
-__device__ __forceinline__ uint32_t comp_key(uint64_t c) { return ~(uint32_t)(c >> 32); }
-
-template <int DT>
+template <int DT, int MODE>
 struct Finalize {
+  using T = typename Entry<DT>::T;
   static constexpr int VE = RowType<DT>::VE;
   FinLds& s;
   BlockOps& ops;
   const RowRef<DT> z;
   const SamplePart* part;
-  const int n_seg;
+  const T* lists;
+  const uint64_t* asked;  // the row's asked-for tokens
+  const SampleAsk* ask;
+  const int n_seg, cap, seg_elems;
   const double c8, J;
   const int tid;
   const uint32_t kmax;  // the row's largest key
@@ -356,92 +592,105 @@ struct Finalize {
   int b0, b1;
   uint32_t lo;
 
-  __device__ Finalize(FinLds& s_, BlockOps& o, const RowRef<DT>& z_, const SamplePart* part_, int n_seg_, double c8_, double J_,
-                      uint32_t kmax_, int listed_)
-      : s(s_), ops(o), z(z_), part(part_), n_seg(n_seg_), c8(c8_), J(J_), tid(threadIdx.x), kmax(kmax_), listed(listed_), base(0),
-        n(0), bmass(0.0), b0(1), b1(0), lo(0) {}
-
   // weight of a key relative to 2^(J / 8)
-  __device__ double weight(uint32_t key) const {
+  __device__ __forceinline__ double weight(uint32_t key) const {
     const double t = key_value(key) * c8, fl = floor(t);
     return exp2_eighth(t - fl) * pow2_eighth((int)fmax(fl - J, -16000.0));
   }
 
-  // f((~key, index)) of every token of the row with klo <= key <= khi; eight slots in flight per thread
+  // f((~key, index)) of every token of bins B0 .. B1, and of others
   template <class F>
-  __device__ void each_in_row(uint32_t klo, uint32_t khi, F f) const {
-    const int n_slots = (z.V + z.phase + VE - 1) / VE;
-    for (int s0 = tid; s0 < n_slots; s0 += 8 * kThreads) {
-      Slot x[8];
+  __device__ __forceinline__ void each(int B0, int B1, F f) {
+    if (MODE == kAll || B1 < listed) {
+      // a segment's list is in the order of its bins, so its part is one run; 16 threads a segment
+      __syncthreads();
+      if (tid < n_seg) {
+        const int l0 = B0 - s.shift[tid], l1 = B1 - s.shift[tid], nb = s.nb[tid];
+        const uint32_t* upto = part[tid].upto;
+        const uint32_t n_all = s.n_seg[tid];
+        s.from[tid] = l0 <= 0 ? 0u : l0 > nb ? n_all : upto[l0 - 1];
+        s.to[tid] = B1 == kTail || l1 >= nb ? n_all : l1 < 0 ? 0u : upto[l1];  // the last bin: all that is left
+      }
+      __syncthreads();
+      for (int g = tid >> 4; g < n_seg; g += kThreads / 16) {
+        const T* list = lists + (size_t)g * cap;
+        const int first = g * seg_elems, end = (int)s.to[g];
+#pragma unroll 4
+        for (int j = (int)s.from[g] + (tid & 15); j < end; j += 16) f(Entry<DT>::comp(list[j], first));
+      }
+    } else if constexpr (MODE == kSecond) {
+      if (ask->kind == kSampleAskBins && ((B0 >= ask->b0[0] && B1 <= ask->b1[0]) || (B0 >= ask->b0[1] && B1 <= ask->b1[1]))) {
+        const int end = (int)min(ask->n, (uint32_t)kSampleAsk);
+#pragma unroll 4
+        for (int j = tid; j < end; j += kThreads) f(asked[j]);
+      } else {
+        const int n_slots = z.slots();
+#pragma unroll 2
+        for (int sl = tid; sl < n_slots; sl += kThreads) {
+          const Slot x = z.load(sl);
 #pragma unroll
-      for (int l = 0; l < 8; ++l) x[l] = z.load(s0 + l * kThreads);
-#pragma unroll
-      for (int l = 0; l < 8; ++l) {
-        const int e = z.first(s0 + l * kThreads);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          const float v = slot_value<DT>(x[l], i);
-          const uint32_t key = key_of(v, RowType<DT>::kMax);
-          if (v > kNegInf && key >= klo && key <= khi) f(((uint64_t)~key << 32) | (uint32_t)(e + i));
+          for (int i = 0; i < VE; ++i) {
+            const float v = slot_value<DT>(x, i);
+            if (v > kNegInf) f(((uint64_t)~key_of(v, RowType<DT>::kMax) << 32) | (uint32_t)(sl * VE + i));
+          }
         }
       }
     }
   }
-  // the same over the segments' lists (whole only for listed bins) and over `big`
-  template <class F>
-  __device__ void each_in_lists(uint32_t klo, uint32_t khi, F f) const {
-    for (int i = tid; i < n_seg * kSampleList; i += kThreads) {
-      const int g = i / kSampleList, j = i % kSampleList;
-      if (j < s.n_list[g]) {
-        const uint64_t c = part[g].list[j];
-        const uint32_t key = comp_key(c);
-        if (key >= klo && key <= khi) f(c);
-      }
-    }
-  }
-  template <class F>
-  __device__ void each_in_big(uint32_t nbig, uint32_t klo, uint32_t khi, F f) const {
-    for (uint32_t i = tid; i < nbig; i += kThreads) {
-      const uint64_t c = s.big[i];
-      const uint32_t key = comp_key(c);
-      if (key >= klo && key <= khi) f(c);
-    }
-  }
 
-  // append to an LDS array through s.n
-  __device__ void start_append() {
+  // One pass over bins B0 .. B1: the tokens with klo <= key <= khi and ilo <=
+  // index <= ihi go into the window (sh < 0), or are counted and weighed in
+  // parts of 2^sh keys from the highest down (of 2^sh indices if by_index)
+  __device__ __forceinline__ void pass(int B0, int B1, uint32_t klo, uint32_t khi, uint32_t ilo, uint32_t ihi, int sh, bool by_index) {
     __syncthreads();
+    s.cnt[tid] = 0;
+    s.mass[tid] = 0;
     if (tid == 0) s.n = 0;
+    __syncthreads();
+    const bool weigh = !by_index && B1 != kTail;
+    each(B0, B1, [&](uint64_t c) {
+      const uint32_t key = comp_key(c), idx = (uint32_t)c;
+      if (key < klo || key > khi || idx < ilo || idx > ihi) return;
+      if (sh < 0) {
+        const uint32_t i = atomicAdd(&s.n, 1u);
+        if (i < (uint32_t)kThreads) s.win[i] = c;
+      } else {
+        const uint32_t b = (by_index ? idx - ilo : khi - key) >> sh;
+        atomicAdd(&s.cnt[b], 1u);
+        if (weigh) {
+          const double t = key_value(key) * c8;
+          // 46 bits of the mantissa: sums of 2^21 tokens fit 64 bits
+          atomicAdd((unsigned long long*)&s.mass[b],
+                    (unsigned long long)((__double_as_longlong(exp2_eighth(t - floor(t))) - kOneBits) >> 6));
+        }
+      }
+    });
     __syncthreads();
   }
 
   // s.win[0 .. s.n - 1] holds the window's tokens in any order: sort them (each
   // thread ranks one token against the others) and sum their weights
-  __device__ void open_window(uint32_t lo_, uint32_t base_, double bmass_, int b0_, int b1_) {
+  __device__ __forceinline__ void open_window(uint32_t lo_, uint32_t base_, double bmass_, int b0_, int b1_) {
     lo = lo_, base = base_, bmass = bmass_, b0 = b0_, b1 = b1_;
-    __syncthreads();
     n = min(s.n, (uint32_t)kThreads);
     const bool in = tid < (int)n;
     const uint64_t mine = in ? s.win[tid] : 0;
     uint32_t rank = 0;
     if ((tid & ~63) < (int)n) {
-      uint32_t j = 0;
-      for (; j + 4 <= n; j += 4) {
-        const uint64_t a = s.win[j], b = s.win[j + 1], c = s.win[j + 2], d = s.win[j + 3];
-        rank += (uint32_t)(a < mine) + (uint32_t)(b < mine) + (uint32_t)(c < mine) + (uint32_t)(d < mine);
-      }
-      for (; j < n; ++j) rank += s.win[j] < mine;
+#pragma unroll 8
+      for (uint32_t j = 0; j < n; ++j) rank += s.win[j] < mine;
     }
     __syncthreads();
     if (in) s.win[rank] = mine;
-    __syncthreads();
-    const double w = in ? weight(comp_key(s.win[tid])) : 0.0;
-    const double c = bmass + ops.scan(w);
+    const double c = bmass + [&] {  // the scan's barrier also closes the writes above
+      __syncthreads();
+      return ops.scan(in ? weight(comp_key(s.win[tid])) : 0.0);
+    }();
     if (in) s.wcum[tid] = c;
     __syncthreads();
   }
 
-  __device__ Cross from_window(int kind, double amount) {
+  __device__ __forceinline__ Cross from_window(int kind, double amount) {
     const bool in = tid < (int)n;
     const bool hit = in && (kind == kByCount    ? (double)(base + tid + 1) >= amount
                             : kind == kByMassGe ? s.wcum[tid] >= amount
@@ -457,211 +706,18 @@ struct Finalize {
     return r;
   }
 
-  // index of the r-th (from 1) token with this key in `big`
-  __device__ uint32_t tie_in_big(uint32_t nbig, uint32_t key, uint32_t r) {
-    uint32_t ilo = 0, ihi = (uint32_t)z.V - 1;
-    for (;;) {
-      const uint32_t range = ihi - ilo;
-      const int sh = max(0, 32 - (range ? __builtin_clz(range) : 32) - 9);
-      __syncthreads();
-      s.cnt[tid] = 0;
-      __syncthreads();
-      each_in_big(nbig, key, key, [&](uint64_t c) {
-        const uint32_t i = (uint32_t)c;
-        if (i >= ilo && i <= ihi) atomicAdd(&s.cnt[(i - ilo) >> sh], 1u);
-      });
-      __syncthreads();
-      const uint32_t c = s.cnt[tid], upto = ops.scan(c);
-      const int b = min(ops.first(upto >= r), kThreads - 1);
-      if (tid == b) s.at = upto - c;
-      __syncthreads();
-      r -= (uint32_t)s.at;
-      ilo += (uint32_t)b << sh;
-      if (sh == 0) return ilo;
-      ihi = min(ihi, ilo + ((1u << sh) - 1u));
-    }
-  }
-
-  // the same over the row, for more equal tokens than `big` holds: the waves
-  // count contiguous pieces, the one that holds it walks its piece again
-  __device__ uint32_t tie_in_row(uint32_t key, uint32_t r) {
-    const int n_slots = (z.V + z.phase + VE - 1) / VE, lane = tid & 63, w = tid >> 6;
-    const int per = ((n_slots + kWaves - 1) / kWaves + 63) / 64 * 64;
-    const int sb = w * per, se = min(n_slots, sb + per);
-    auto count = [&](int sl, uint32_t* mask) {
-      const Slot x = z.load(sl);
-      uint32_t mk = 0;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float v = slot_value<DT>(x, i);
-        mk |= (uint32_t)(v > kNegInf && key_of(v, RowType<DT>::kMax) == key) << i;
-      }
-      *mask = mk;
-      return (uint32_t)__popc(mk);
-    };
-    uint32_t c = 0, mk = 0;
-    for (int sl = sb + lane; sl < se; sl += 64) c += count(sl, &mk);
-    c = wave_sum_u32(c);
-    __syncthreads();
-    if (lane == 0) s.cnt[w] = c;
-    if (tid == 0) s.at = 0;
-    __syncthreads();
-    uint32_t before = 0;
-    for (int i = 0; i < w; ++i) before += s.cnt[i];
-    if (r > before && r <= before + s.cnt[w]) {
-      uint32_t left = r - before;
-      for (int b = sb; b < se; b += 64) {
-        const uint32_t cl = b + lane < se ? count(b + lane, &mk) : 0;
-        uint32_t sc = cl;  // inclusive scan over the wave
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-          const uint32_t t = __shfl_up(sc, o);
-          sc += lane >= o ? t : 0u;
-        }
-        const uint32_t total = __shfl(sc, 63);
-        if (left <= total) {
-          if (left > sc - cl && left <= sc) {
-            uint32_t k = left - (sc - cl);  // from 1 inside this lane's slot
-            int i = -1;
-            do {
-              ++i;
-              if ((mk >> i) & 1u) --k;
-            } while (k);
-            s.at = (uint64_t)(z.first(b + lane) + i);
-          }
-          break;
-        }
-        left -= total;
-      }
+  // part `b` of a pass: (tokens, weight) before it, and its own tokens
+  __device__ __forceinline__ uint32_t part_of(int b, uint32_t upto, double mass_upto, uint32_t c, double mass) {
+    if (tid == b) {
+      s.before_n = upto - c;
+      s.before_m = mass_upto - mass;
+      s.n = c;
     }
     __syncthreads();
-    return (uint32_t)s.at;
+    return s.n;
   }
 
-  // A bin (keys klo .. khi) of more tokens than a window holds: split its key
-  // range until the part with the crossing fits one, or is a single value.
-  // The first rounds read the row where the bin does not fit `big` either.
-  __device__ Cross split(int kind, double amount, uint32_t klo, uint32_t khi, uint32_t cb, uint32_t nc, double mb, bool tail,
-                         bool from_lists) {
-    uint32_t nbig = 0;
-    for (;;) {
-      if (nbig == 0 && nc <= (uint32_t)kCap) {
-        start_append();
-        auto put = [&](uint64_t c) {
-          const uint32_t i = atomicAdd(&s.n, 1u);
-          if (i < (uint32_t)kCap) s.big[i] = c;
-        };
-        if (from_lists)
-          each_in_lists(klo, khi, put);
-        else
-          each_in_row(klo, khi, put);
-        __syncthreads();
-        nbig = min(s.n, (uint32_t)kCap);
-      }
-      if (nc <= (uint32_t)kThreads) {
-        start_append();
-        each_in_big(nbig, klo, khi, [&](uint64_t c) {
-          const uint32_t i = atomicAdd(&s.n, 1u);
-          if (i < (uint32_t)kThreads) s.win[i] = c;
-        });
-        open_window(klo, cb, mb, 1, 0);
-        return from_window(kind, amount);
-      }
-      if (klo == khi) {  // one value: every token weighs w
-        const double w = tail ? 0.0 : weight(klo);
-        double r = (double)nc;
-        if (kind == kByCount) r = amount - cb;
-        if (kind == kByMassGe || kind == kByMassGt) {
-          r = fmin(fmax(floor((amount - mb) / w), 0.0), (double)nc);
-          // the quotient is off by rounding only: settle it on the sums themselves
-          if (r > 0.0 && (kind == kByMassGe ? fma(r - 1.0, w, mb) >= amount : fma(r - 1.0, w, mb) > amount)) r -= 1.0;
-          if (r < (double)nc && !(kind == kByMassGe ? fma(r, w, mb) >= amount : fma(r, w, mb) > amount)) r += 1.0;
-          r = fmax(r, 1.0);
-        }
-        if (kind == kByWeight) r = weight(klo) < amount ? 0.0 : (double)nc;
-        Cross x;
-        x.n = cb + (uint32_t)r;
-        x.cum = fma(r, w, mb);
-        x.at = 0;
-        x.cut = ((uint64_t)~klo) << 32;
-        if (r > 0.0) {
-          const uint32_t i = nbig ? tie_in_big(nbig, klo, (uint32_t)r) : tie_in_row(klo, (uint32_t)r);
-          x.at = ((uint64_t)~klo << 32) | i;
-          x.cut = x.at + 1;
-        }
-        return x;
-      }
-      const uint32_t range = khi - klo;
-      const int sh = max(0, 32 - __builtin_clz(range) - 9);
-      __syncthreads();
-      s.cnt[tid] = 0;
-      s.mass[tid] = 0;
-      __syncthreads();
-      auto add = [&](uint64_t cp) {
-        const uint32_t key = comp_key(cp), b = (khi - key) >> sh;
-        atomicAdd(&s.cnt[b], 1u);
-        if (!tail) {
-          const double t = key_value(key) * c8;
-          // 46 bits of the mantissa: sums of 2^21 tokens fit 64 bits
-          atomicAdd((unsigned long long*)&s.mass[b],
-                    (unsigned long long)((__double_as_longlong(exp2_eighth(t - floor(t))) - kOneBits) >> 6));
-        }
-      };
-      if (nbig)
-        each_in_big(nbig, klo, khi, add);
-      else
-        each_in_row(klo, khi, add);
-      __syncthreads();
-      // one bin holds one eighth of an octave: its unit is that of its lowest key
-      const double unit = tail ? 0.0 : pow2_eighth((int)fmax(floor(key_value(klo) * c8) - J, -16000.0));
-      const uint32_t c = s.cnt[tid];
-      const uint32_t c1 = cb + ops.scan(c);
-      const double m1 = mb + ops.scan(unit * ((double)c + (double)s.mass[tid] * 0x1p-46));
-      s.rc[tid + 1] = c1;
-      s.rm[tid + 1] = m1;
-      if (tid == 0) {
-        s.rc[0] = cb;
-        s.rm[0] = mb;
-      }
-      const uint32_t n_part = (range >> sh) + 1;  // parts, from the highest key down
-      const uint32_t low = (uint32_t)tid + 1 >= n_part ? klo : khi - ((uint32_t)tid << sh) - ((1u << sh) - 1u);
-      const bool hit = (uint32_t)tid < n_part &&
-                       (kind == kByCount    ? (double)c1 >= amount
-                        : kind == kByMassGe ? m1 >= amount
-                        : kind == kByMassGt ? m1 > amount
-                                            : weight(low) < amount);
-      int b = ops.first(hit);
-      if (b >= (int)n_part) {
-        // every key passes, or rounding left the sum short of the last token
-        if (kind == kByWeight) {
-          Cross r;
-          r.n = s.rc[n_part];
-          r.cum = s.rm[n_part];
-          r.cut = ((uint64_t)~klo + 1) << 32;
-          r.at = 0;
-          return r;
-        }
-        kind = kByCount;
-        amount = (double)s.rc[n_part];
-        b = ops.first((uint32_t)tid < n_part && (double)c1 >= amount);
-      }
-      nc = s.rc[b + 1] - s.rc[b];
-      cb = s.rc[b];
-      mb = s.rm[b];
-      khi -= (uint32_t)b << sh;
-      if ((uint32_t)b + 1 < n_part) klo = khi - ((1u << sh) - 1u);
-      if (nc == 0) {  // kByWeight: the threshold falls between tokens
-        Cross r;
-        r.n = cb;
-        r.cum = mb;
-        r.cut = ((uint64_t)~khi) << 32;
-        r.at = 0;
-        return r;
-      }
-    }
-  }
-
-  __device__ Cross locate(int kind, double amount) {
+  __device__ __forceinline__ Cross locate(int kind, double amount) {
     // a sum within 2^-44 of the value counts as equal to it: rows of equal
     // logits meet dyadic settings exactly, and the sums round (below 2^-47)
     if (kind == kByMassGe) amount *= 1.0 - 0x1p-44;
@@ -679,93 +735,220 @@ struct Finalize {
         b = ops.first((double)s.cc[tid + 1] >= amount);
       }
     }
-    if (b >= b0 && b <= b1) return from_window(kind, amount);
-    const uint32_t c = s.cc[b + 1] - s.cc[b];
-    const uint32_t klo = b == kTail ? kKeyLowest : lowest_key(J - b, c8);
-    if (b < listed && s.cc[b + 1] <= (uint32_t)kThreads) {
-      // everything down to this bin fits a window and is in the lists
-      start_append();
-      each_in_lists(klo, kmax, [&](uint64_t cp) {
-        const uint32_t i = atomicAdd(&s.n, 1u);
-        if (i < (uint32_t)kThreads) s.win[i] = cp;
-      });
-      open_window(klo, 0, 0.0, 0, b);
-      return from_window(kind, amount);
+    if (b < b0 || b > b1) {
+      uint32_t klo = b == kTail ? kKeyLowest : lowest_key(J - b, c8);
+      uint32_t khi = b == 0 ? kmax : lowest_key(J - b + 1.0, c8) - 1u;
+      uint32_t cb = s.cc[b], nc = s.cc[b + 1] - cb;
+      double mb = s.cm[b];
+      if (nc == 0) return Cross{cb, mb, ((uint64_t)~khi) << 32, 0};  // kByWeight: nothing in the threshold's own bin
+      int B0 = b;
+      bool whole = true;
+      if ((MODE == kAll || b < listed) && s.cc[b + 1] <= (uint32_t)kThreads) {  // everything down to this bin fits a window
+        B0 = 0;
+        khi = kmax;
+        nc += cb;
+        cb = 0;
+        mb = 0.0;
+      }
+      while (nc > (uint32_t)kThreads) {
+        whole = false;
+        if (klo == khi) {  // one value: every token weighs w
+          const double w = b == kTail ? 0.0 : weight(klo);
+          double r = (double)nc;
+          if (kind == kByCount) r = amount - cb;
+          if (kind == kByMassGe || kind == kByMassGt) {
+            r = fmin(fmax(floor((amount - mb) / w), 0.0), (double)nc);
+            // the quotient is off by rounding only: settle it on the sums themselves
+            if (r > 0.0 && (kind == kByMassGe ? fma(r - 1.0, w, mb) >= amount : fma(r - 1.0, w, mb) > amount)) r -= 1.0;
+            if (r < (double)nc && !(kind == kByMassGe ? fma(r, w, mb) >= amount : fma(r, w, mb) > amount)) r += 1.0;
+            r = fmax(r, 1.0);
+          }
+          if (kind == kByWeight && weight(klo) < amount) return Cross{cb, mb, ((uint64_t)~klo) << 32, 0};
+          const Cross x{cb + (uint32_t)r, fma(r, w, mb), 0, 0};
+          // the index of the r-th of them
+          uint32_t left = (uint32_t)r, ilo = 0, ihi = (uint32_t)z.V - 1;
+          for (;;) {
+            const uint32_t range = ihi - ilo;
+            const int sh = max(0, 32 - (range ? __builtin_clz(range) : 32) - 9);
+            pass(B0, b, klo, khi, ilo, ihi, sh, true);
+            const uint32_t c = s.cnt[tid], upto = ops.scan(c);
+            const int q = min(ops.first(upto >= left), kThreads - 1);
+            part_of(q, upto, 0.0, c, 0.0);
+            left -= s.before_n;
+            ilo += (uint32_t)q << sh;
+            if (sh == 0) break;
+            ihi = min(ihi, ilo + ((1u << sh) - 1u));
+          }
+          const uint64_t at = ((uint64_t)~klo << 32) | ilo;
+          return Cross{x.n, x.cum, at + 1, at};
+        }
+        const uint32_t range = khi - klo;
+        const int sh = max(0, 32 - __builtin_clz(range) - 9);
+        pass(B0, b, klo, khi, 0, 0xFFFFFFFFu, sh, false);
+        // one bin holds one eighth of an octave: its unit is that of its lowest key
+        const double unit = b == kTail ? 0.0 : pow2_eighth((int)fmax(floor(key_value(klo) * c8) - J, -16000.0));
+        const uint32_t c = s.cnt[tid];
+        const double mass = unit * ((double)c + (double)s.mass[tid] * 0x1p-46);
+        const uint32_t c1 = cb + ops.scan(c);
+        const double m1 = mb + ops.scan(mass);
+        const uint32_t n_part = (range >> sh) + 1;  // parts, from the highest key down
+        const uint32_t low = (uint32_t)tid + 1 >= n_part ? klo : khi - ((uint32_t)tid << sh) - ((1u << sh) - 1u);
+        const bool part_hit = (uint32_t)tid < n_part &&
+                              (kind == kByCount    ? (double)c1 >= amount
+                               : kind == kByMassGe ? m1 >= amount
+                               : kind == kByMassGt ? m1 > amount
+                                                   : weight(low) < amount);
+        int q = ops.first(part_hit);
+        if (q >= (int)n_part) {  // every key passes, or rounding left the sum short of the last token
+          part_of((int)n_part - 1, c1, m1, c, mass);
+          if (kind == kByWeight) return Cross{s.before_n + s.n, s.before_m, ((uint64_t)~klo + 1) << 32, 0};
+          kind = kByCount;
+          amount = (double)(s.before_n + s.n);
+          q = ops.first((uint32_t)tid < n_part && (double)c1 >= amount);
+        }
+        nc = part_of(q, c1, m1, c, mass);
+        cb = s.before_n;
+        mb = s.before_m;
+        khi -= (uint32_t)q << sh;
+        if ((uint32_t)q + 1 < n_part) klo = khi - ((1u << sh) - 1u);
+        if (nc == 0) return Cross{cb, mb, ((uint64_t)~khi) << 32, 0};  // kByWeight: the threshold falls between tokens
+      }
+      pass(B0, b, klo, khi, 0, 0xFFFFFFFFu, -1, false);
+      open_window(klo, cb, mb, whole ? B0 : 1, whole ? b : 0);
     }
-    const uint32_t khi = b == 0 ? kmax : lowest_key(J - b + 1.0, c8) - 1u;
-    if (c == 0) {  // kByWeight only: nothing in the threshold's own bin
-      Cross r;
-      r.n = s.cc[b];
-      r.cum = s.cm[b];
-      r.cut = ((uint64_t)~khi) << 32;
-      r.at = 0;
-      return r;
-    }
-    if (c > (uint32_t)kThreads) return split(kind, amount, klo, khi, s.cc[b], c, s.cm[b], b == kTail, b < listed);
-    start_append();
-    auto put = [&](uint64_t cp) {
-      const uint32_t i = atomicAdd(&s.n, 1u);
-      if (i < (uint32_t)kThreads) s.win[i] = cp;
-    };
-    if (b < listed)
-      each_in_lists(klo, khi, put);
-    else
-      each_in_row(klo, khi, put);
-    open_window(klo, s.cc[b], s.cm[b], b, b);
     return from_window(kind, amount);
   }
 };
 
-template <int DT>
-__global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg,
+// The bins that a row's cuts and draw can need, from the bins' sums alone: a
+// cut or draw whose amount depends on an earlier cut inside a bin takes the
+// bins of that amount's bounds.  True if all are listed; else asks for them.
+__device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowParams& rp, uint32_t N, double wmax, bool draw,
+                                            double u, double J, double c8, uint32_t kmax, int listed, SampleAsk& ask) {
+  constexpr double kLess = 1.0 - 0x1p-40, kMore = 1.0 + 0x1p-40;
+  const int tid = threadIdx.x;
+  const double total = s.cm[kBins], after = s.cm[tid + 1];
+  int need0 = kBins, need1 = -1, cut1 = kTail;  // bins of cuts; the latest bin the kept tokens can end in
+  double zlo = total, zhi = total;
+  bool any = false;
+  int bk = -1;
+  if (rp.k < (int64_t)N) {
+    bk = ops.first(s.cc[tid + 1] >= (uint32_t)rp.k);
+    cut1 = bk;
+    zlo = s.cm[bk];
+    zhi = s.cm[bk + 1];
+    need0 = need1 = bk;
+    any = true;
+  }
+  if (rp.p < 1.0) {
+    const int p0 = min(ops.first(after >= rp.p * zlo * kLess), kTail);
+    const int p1 = min(ops.first(after >= rp.p * zhi * kMore), kTail);
+    need0 = min(need0, p0);
+    need1 = max(need1, min(p1, cut1));
+    cut1 = min(cut1, p1);
+    zlo = fmin(zlo, s.cm[p0]);
+    zhi = s.cm[cut1 + 1];
+    any = true;
+  }
+  if (rp.m > 0.0) {
+    const int bm = min(ops.first(pow2_eighth(-tid) <= rp.m * wmax), kTail);
+    if (bm <= cut1) {
+      need0 = min(need0, bm);
+      need1 = max(need1, bm);
+      cut1 = bm;
+      zlo = fmin(zlo, s.cm[bm]);
+      zhi = s.cm[cut1 + 1];
+      any = true;
+    }
+  }
+  int d0 = kBins, d1 = -1;
+  if (draw) {
+    d0 = min(ops.first(after > u * zlo * kLess), cut1);
+    d1 = min(ops.first(after > u * zhi * kMore), cut1);
+  }
+  if (need1 < listed && d1 < listed) return true;
+  if (!any) {
+    need0 = d0;
+    need1 = d1;
+  } else if (draw && d1 >= need0 && d0 <= need1) {
+    need0 = min(need0, d0);
+    need1 = max(need1, d1);
+    d1 = -1;
+  }
+  if (!any) d1 = -1;
+  const uint32_t count = s.cc[need1 + 1] - s.cc[need0] + (d1 >= 0 ? s.cc[d1 + 1] - s.cc[d0] : 0u);
+  if (d1 < 0) d0 = kBins;
+  // keys of the two ranges of bins (an empty second one: none)
+  const uint32_t l0 = need1 == kTail ? kKeyLowest : lowest_key(J - need1, c8), h0 = need0 == 0 ? kmax : lowest_key(J - need0 + 1.0, c8) - 1u;
+  uint32_t l1 = 1, h1 = 0;
+  if (d1 >= 0) {
+    l1 = d1 == kTail ? kKeyLowest : lowest_key(J - d1, c8);
+    h1 = d0 == 0 ? kmax : lowest_key(J - d0 + 1.0, c8) - 1u;
+  }
+  if (tid == 0) {
+    ask.kind = count <= (uint32_t)kSampleAsk ? kSampleAskBins : kSampleAskRow;
+    ask.n = 0;
+    ask.b0[0] = need0, ask.b1[0] = need1, ask.klo[0] = l0, ask.khi[0] = h0;
+    ask.b0[1] = d0, ask.b1[1] = d1, ask.klo[1] = l1, ask.khi[1] = h1;
+  }
+  return false;
+}
+
+template <int DT, int MODE>
+__global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap, int seg_elems,
                                                                    const SamplePart* __restrict__ parts,
-                                                                   const double* __restrict__ u, int32_t* __restrict__ token,
-                                                                   float* __restrict__ prob, int32_t* __restrict__ kept,
-                                                                   uint64_t* __restrict__ cuts) {
+                                                                   const typename Entry<DT>::T* __restrict__ lists,
+                                                                   SampleAsk* __restrict__ asks, const uint64_t* __restrict__ asked,
+                                                                   SampleOut o, uint64_t* __restrict__ cuts) {
+  if constexpr (MODE == kSecond) {
+    if (asks[blockIdx.x].kind == kSampleAskNone) return;
+  }
   __shared__ FinLds s;
   BlockOps ops(s.red);
   const int tid = threadIdx.x;
   const int64_t row = row0 + blockIdx.x;
   const RowParams rp = row_params(a, row);
   const SamplePart* part = parts + (size_t)blockIdx.x * n_seg;
+  if (MODE == kFirst && tid == 0) asks[blockIdx.x].kind = kSampleAskNone;
 
   // the segments' headers, one thread each (n_seg <= kMaxSeg = kThreads)
   const bool have = tid < n_seg;
   const double Js = have ? part[tid].J : -INFINITY;
   const uint32_t ns = have ? part[tid].n : 0;
-  const int nbs = have ? part[tid].nb : 0, ls = have ? part[tid].listed : kBins, nl = have ? part[tid].n_list : 0;
+  const int nbs = have ? part[tid].nb : 0, ls = have ? part[tid].listed : kBins;
   const double ms = have ? (double)part[tid].max : -INFINITY;
+  double u = o.token ? o.u[row] : 0.0;
+  u = u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;  // NaN: 0
   const double J = ops.max(Js);
   const float m = (float)ops.max(ms);
   const uint32_t N = ops.sum(ns);
   if (N == 0) {  // every token masked
     if (tid == 0) {
-      if (token) token[row] = -1;
-      if (prob) prob[row] = 0.0f;
-      if (kept) kept[row] = 0;
-      if (cuts) cuts[blockIdx.x] = 0;
+      if (o.token) o.token[row] = -1;
+      if (o.prob) o.prob[row] = 0.0f;
+      if (o.kept) o.kept[row] = 0;
+      if (o.out) cuts[blockIdx.x] = 0;
     }
     return;
   }
   const int shift = ns ? (int)fmin(J - Js, (double)kBins) : kBins;
   if (have) {
     s.shift[tid] = (int16_t)shift;
-    s.len[tid] = (int16_t)min(nbs, kTail);
-    s.n_list[tid] = (int16_t)nl;
+    s.nb[tid] = (int16_t)nbs;
+    s.n_seg[tid] = ns;
   }
   // bins whose tokens are all listed: as far as every segment's list reaches
   const int listed = kBins - (int)ops.max((double)(kBins - (ls >= kBins ? kBins : min(kBins, ls + shift))));
   // the segments' bins on the row's grid, in segment order
-  uint32_t c = 0;
+  uint32_t cs = 0;
   double mass = 0.0;
 #pragma unroll 8
   for (int g = 0; g < n_seg; ++g) {
     const int b = tid - s.shift[g];
-    const bool in = tid < kTail && b >= 0 && b < s.len[g];
-    c += in ? part[g].cnt[b] : 0u;
+    const bool in = tid < kTail && b >= 0 && b < s.nb[g];
+    cs += in ? part[g].upto[b] : b < 0 ? 0u : s.n_seg[g];
     mass += in ? part[g].mass[b] : 0.0;
   }
-  uint32_t cs = ops.scan(c);
   const double cum = ops.scan(mass * pow2_eighth(-tid));
   if (tid == kTail) cs = N;  // the tail bin: whatever is left
   s.cc[tid + 1] = cs;
@@ -777,34 +960,109 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
   __syncthreads();
 
   const uint32_t kmax = key_of(m, RowType<DT>::kMax);
-  Finalize<DT> f(s, ops, RowRef<DT>(a.Z, row, a.stride, a.V), part, n_seg, rp.c8, J, kmax, listed);
+  Finalize<DT, MODE> f{s, ops, RowRef<DT>(a.Z, row, a.stride, a.V), part, lists + (size_t)blockIdx.x * n_seg * cap,
+                       MODE == kSecond ? asked + (size_t)blockIdx.x * kSampleAsk : nullptr,
+                       MODE == kSecond ? asks + blockIdx.x : nullptr, n_seg, cap, seg_elems, rp.c8, J, tid, kmax, listed,
+                       0, 0, 0.0, 1, 0, 0};
+  const double wmax = f.weight(kmax);
+  if constexpr (MODE == kFirst) {
+    if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, rp.c8, kmax, listed, asks[blockIdx.x])) return;
+  }
   uint32_t n = N;
   double Z = s.cm[kBins];
   uint64_t cut = ~0ull;
-  auto take = [&](const Cross& x) {
-    if (x.n < n) {
-      n = x.n;
-      Z = x.cum;
-      cut = x.cut;
+  // the cuts (0: top-k, 1: top-p, 2: min-p), the draw (3), and the last kept
+  // token if rounding drew one behind it (4)
+#pragma unroll 1
+  for (int q = 0; q < 5; ++q) {
+    int kind;
+    double amount;
+    if (q == 0) {
+      if (rp.k >= (int64_t)N) continue;
+      kind = kByCount, amount = (double)rp.k;
+    } else if (q == 1) {
+      if (!(rp.p < 1.0)) continue;
+      kind = kByMassGe, amount = rp.p * Z;
+    } else if (q == 2) {
+      if (!(rp.m > 0.0)) continue;
+      kind = kByWeight, amount = rp.m * wmax;
+    } else if (q == 3) {
+      if (tid == 0) {
+        if (o.kept) o.kept[row] = (int32_t)n;
+        if (o.out) cuts[blockIdx.x] = cut;
+      }
+      if (!o.token) break;
+      kind = kByMassGt, amount = u * Z;
+    } else {
+      kind = kByCount, amount = (double)n;
     }
-  };
-  if (rp.k < (int64_t)N) take(f.locate(kByCount, (double)rp.k));
-  if (rp.p < 1.0) take(f.locate(kByMassGe, rp.p * Z));
-  if (rp.m > 0.0) take(f.locate(kByWeight, rp.m * f.weight(kmax)));
-  if (kept && tid == 0) kept[row] = (int32_t)n;
-  if (cuts && tid == 0) cuts[blockIdx.x] = cut;
-  if (!token) return;
-  double x = u[row];
-  x = x > 0.0 ? fmin(x, 1.0 - 0x1p-53) : 0.0;  // NaN: 0
-  Cross d = f.locate(kByMassGt, x * Z);
-  if (d.n > n) d = f.locate(kByCount, (double)n);
-  if (tid == 0) {
-    token[row] = (int32_t)(uint32_t)d.at;
-    if (prob) prob[row] = (float)(f.weight(comp_key(d.at)) / Z);
+    const Cross x = f.locate(kind, amount);
+    if (q < 3) {
+      if (x.n < n) {
+        n = x.n;
+        Z = x.cum;
+        cut = x.cut;
+      }
+    } else if (q == 4 || x.n <= n) {
+      if (tid == 0) {
+        o.token[row] = (int32_t)(uint32_t)x.at;
+        if (o.prob) o.prob[row] = (float)(f.weight(comp_key(x.at)) / Z);
+      }
+      break;
+    }
   }
 }
 
-// ---------------------------------------------------------------- (3) the filtered row
+// ---------------------------------------------------------------- (3) the tokens that rows asked for
+
+template <int DT, int NL>
+__global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, int64_t row0, int n_seg, SampleAsk* __restrict__ asks,
+                                                                 uint64_t* __restrict__ asked) {
+  constexpr int VE = RowType<DT>::VE;
+  const int r = blockIdx.x / n_seg, seg = blockIdx.x % n_seg, tid = threadIdx.x;
+  SampleAsk& ask = asks[r];
+  if (ask.kind != kSampleAskBins) return;
+  __shared__ uint32_t place[kSampleAsk];
+  __shared__ uint32_t n, at;
+  if (tid == 0) n = 0;
+  __syncthreads();
+  const RowRef<DT> z(a.Z, row0 + r, a.stride, a.V);
+  const int s0 = seg * (kThreads * NL) + tid;
+  const uint32_t l0 = ask.klo[0], w0 = ask.khi[0] - l0, l1 = ask.klo[1], w1 = ask.khi[1] - l1;
+  const bool two = ask.b1[1] >= 0;
+  Slot x[NL];
+#pragma unroll
+  for (int l = 0; l < NL; ++l) x[l] = z.load(s0 + l * kThreads);
+#pragma unroll
+  for (int l = 0; l < NL; ++l) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DT>(x[l], i);
+      const uint32_t key = key_of(v, RowType<DT>::kMax);
+      hits |= (uint32_t)(v > kNegInf && (key - l0 <= w0 || (two && key - l1 <= w1))) << i;
+    }
+    if (hits) {
+      uint32_t i = atomicAdd(&n, (uint32_t)__popc(hits));
+      do {
+        if (i < (uint32_t)kSampleAsk) place[i] = (uint32_t)((s0 + l * kThreads) * VE + __builtin_ctz(hits));
+        ++i;
+        hits &= hits - 1;
+      } while (hits);
+    }
+  }
+  __syncthreads();
+  const uint32_t c = min(n, (uint32_t)kSampleAsk);
+  if (tid == 0) at = atomicAdd(&ask.n, c);  // the tokens' order in the row's buffer does not matter
+  __syncthreads();
+  uint64_t* out = asked + (size_t)r * kSampleAsk;
+  for (uint32_t i = tid; i < c && at + i < (uint32_t)kSampleAsk; i += kThreads) {
+    const uint32_t idx = place[i];
+    out[at + i] = ((uint64_t)~key_of(row_value<DT>(z, (int)idx), RowType<DT>::kMax) << 32) | idx;
+  }
+}
+
+// ---------------------------------------------------------------- (4) the filtered row
 
 template <int DT, int NL>
 __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, int64_t row0, int n_seg,
@@ -816,7 +1074,6 @@ __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, in
   const int64_t r = blockIdx.x / n_seg, row = row0 + r;
   const RowRef<DT> z(a.Z, row, a.stride, a.V);
   E* o = static_cast<E*>(out) + row * out_stride;
-  const bool same = (reinterpret_cast<uintptr_t>(o) & 15u) == (reinterpret_cast<uintptr_t>(z.p) & 15u);
   const uint64_t cut = cuts[r];
   const int s0 = seg * (kThreads * NL) + tid;
   Slot x[NL];
@@ -824,7 +1081,7 @@ __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, in
   for (int l = 0; l < NL; ++l) x[l] = z.load(s0 + l * kThreads);
 #pragma unroll
   for (int l = 0; l < NL; ++l) {
-    const int e = z.first(s0 + l * kThreads);
+    const int e = (s0 + l * kThreads) * VE;
     Slot y;
 #pragma unroll
     for (int k = 0; k < 4; ++k) y.w[k] = 0;
@@ -840,22 +1097,39 @@ __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, in
         y.w[i] = in ? x[l].w[i] : fill;
       }
     }
-    store_slot<DT>(o, z, s0 + l * kThreads, y, same);
+    store_slot<DT>(o, a.V, s0 + l * kThreads, y);
   }
 }
 
 template <int DT, int NL>
 hipError_t run(const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl, hipStream_t st) {
+  using T = typename Entry<DT>::T;
   SamplePart* parts = reinterpret_cast<SamplePart*>(ws + pl.parts);
+  T* lists = reinterpret_cast<T*>(ws + pl.lists);
   uint64_t* cuts = reinterpret_cast<uint64_t*>(ws + pl.cuts);
+  SampleAsk* asks = reinterpret_cast<SampleAsk*>(ws + pl.asks);
+  uint64_t* asked = reinterpret_cast<uint64_t*>(ws + pl.asked);
+  const dim3 block(kThreads);
+  const int seg_elems = kThreads * NL * RowType<DT>::VE;
   for (int64_t r0 = 0; r0 < a.R; r0 += pl.batch) {
-    const unsigned nr = (unsigned)(a.R - r0 < pl.batch ? a.R - r0 : pl.batch), nb = nr * (unsigned)pl.n_seg;
-    launch(sample_hist_kernel<DT, NL>, dim3(nb), dim3(kThreads), st, a, r0, pl.n_seg, parts);
-    launch(sample_finalize_kernel<DT>, dim3(nr), dim3(kThreads), st, a, r0, pl.n_seg, (const SamplePart*)parts, o.u,
-                 o.token, o.prob, o.kept, o.out ? cuts : (uint64_t*)nullptr);
+    const unsigned nr = (unsigned)(a.R - r0 < pl.batch ? a.R - r0 : pl.batch);
+    const dim3 rows(nr), segs(nr * (unsigned)pl.n_seg);
+    if constexpr (DT == DFLASH_BF16 && NL >= 4)
+      launch(sample_count_kernel<NL>, segs, block, st, a, r0, pl.n_seg, pl.cap, parts, lists);
+    else
+      launch(sample_hist_kernel<DT, NL>, segs, block, st, a, r0, pl.n_seg, pl.cap, parts, lists);
+    if constexpr (NL == 1) {
+      launch(sample_finalize_kernel<DT, kAll>, rows, block, st, a, r0, pl.n_seg, pl.cap, seg_elems, (const SamplePart*)parts,
+             (const T*)lists, asks, (const uint64_t*)asked, o, cuts);
+    } else {
+      launch(sample_finalize_kernel<DT, kFirst>, rows, block, st, a, r0, pl.n_seg, pl.cap, seg_elems, (const SamplePart*)parts,
+             (const T*)lists, asks, (const uint64_t*)asked, o, cuts);
+      launch(sample_gather_kernel<DT, NL>, segs, block, st, a, r0, pl.n_seg, asks, asked);
+      launch(sample_finalize_kernel<DT, kSecond>, rows, block, st, a, r0, pl.n_seg, pl.cap, seg_elems, (const SamplePart*)parts,
+             (const T*)lists, asks, (const uint64_t*)asked, o, cuts);
+    }
     if (o.out)
-      launch(sample_apply_kernel<DT, NL>, dim3(nb), dim3(kThreads), st, a, r0, pl.n_seg, (const uint64_t*)cuts, o.fill,
-                   o.out, o.out_stride);
+      launch(sample_apply_kernel<DT, NL>, segs, block, st, a, r0, pl.n_seg, (const uint64_t*)cuts, o.fill, o.out, o.out_stride);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
