@@ -211,26 +211,40 @@ static int row_slots(const dflash_rows& r) {
   return (r.V + ve - 1) / ve;
 }
 
-// Slots per thread: the most whose grid still has 1024 blocks (four per CU),
-// so that few rows spread over the GPU and many amortise their bins.
 SamplePlan sample_plan(const dflash_rows& r) {
   SamplePlan p{};
   const int slots = row_slots(r);
+  if (r.dtype == DFLASH_BF16) {
+    // A block costs its counters (12 KB written, read again and scanned) beside
+    // its slots: the longest segments that still give four blocks per CU,
+    // but no shorter ones than four slots a thread.
+    const int least = (slots + kSampleMaxSegSlots - 1) / kSampleMaxSegSlots;
+    const int most = std::max(least, slots / (4 * kSampleThreads));
+    p.n_seg = (int)std::min<int64_t>(std::max<int64_t>(least, (1024 + r.R - 1) / std::max<int64_t>(r.R, 1)), most);
+    p.n_seg = std::min(std::max(p.n_seg, 1), kSampleMaxSeg);
+    p.seg_slots = (slots + p.n_seg - 1) / p.n_seg;
+    p.batch = std::max(1, 4096 / p.n_seg);
+    const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);
+    p.cuts = align256(rows * p.n_seg * sizeof(SampleValues));
+    p.total = p.cuts + align256(rows * sizeof(uint64_t));
+    return p;
+  }
+  // Slots per thread: the most whose grid still has 1024 blocks (four per CU),
+  // so that few rows spread over the GPU and many amortise their bins.
   for (p.loads = kSampleMaxLoads;; p.loads /= 2) {
     p.n_seg = (slots + kSampleThreads * p.loads - 1) / (kSampleThreads * p.loads);
     if (p.loads == 1 || r.R * p.n_seg >= 1024 || p.n_seg * 2 > kSampleMaxSeg) break;
   }
-  const bool all = p.loads == 1;
   // One slot per thread: few rows, and the whole segment is listed, so that
   // the one block that finishes a row needs no other.  Longer segments list
   // what ordinary cuts take (top-k of 50, peaked rows).
-  p.cap = all ? kSampleThreads * (r.dtype == DFLASH_BF16 ? 8 : 4) : p.loads == 2 ? 256 : 64;
+  const bool all = p.loads == 1;
+  p.cap = all ? kSampleThreads * 4 : p.loads == 2 ? 256 : 64;
   p.batch = std::max(1, 4096 / p.n_seg);
   if (!all) p.batch = std::min<int64_t>(p.batch, 1024);
   const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);
-  p.parts = 0;
   p.lists = align256(rows * p.n_seg * sizeof(SamplePart));
-  p.cuts = p.lists + align256(rows * p.n_seg * p.cap * (r.dtype == DFLASH_BF16 ? sizeof(uint32_t) : sizeof(uint64_t)));
+  p.cuts = p.lists + align256(rows * p.n_seg * p.cap * sizeof(uint64_t));
   p.asks = p.cuts + align256(rows * sizeof(uint64_t));
   p.asked = p.asks + (all ? 0 : align256(rows * sizeof(SampleAsk)));
   p.total = p.asked + (all ? 0 : align256(rows * kSampleAsk * sizeof(uint64_t)));

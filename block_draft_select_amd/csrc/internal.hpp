@@ -169,14 +169,14 @@ hipError_t launch_conv2tap(const dflash_dims& d, const void* x, const void* x0, 
                            hipStream_t st);
 // ---- rows of vocabulary logits (dflash_rows) ----
 
-// dflash_sample / dflash_filter: a block takes kSampleThreads * loads 16-byte
-// slots of a row; its bins go to one SamplePart
+// dflash_sample / dflash_filter
 constexpr int kSampleThreads = 512;
 constexpr int kSampleBins = 512;
 constexpr int kSampleMaxSeg = 512;   // blocks per row
 constexpr int kSampleMaxLoads = 8;
 constexpr int kSamplePick = 1024;    // tokens a block picks out of a segment
 constexpr int kSampleAsk = 8192;     // tokens outside the lists that a row can ask for
+// a segment of an fp32 row: kSampleThreads * loads slots
 struct SamplePart {
   double J;      // floor of the segment's maximum in eighths of an octave; -inf: nothing unmasked
   float max;     // the maximum
@@ -185,6 +185,14 @@ struct SamplePart {
   int32_t listed;  // the tokens of bins 0 .. listed - 1 are in the segment's list
   double mass[kSampleBins];    // bin b: weights over 2^((J - b) / 8)
   uint32_t upto[kSampleBins];  // tokens of bins 0 .. b
+};
+// a segment of a bf16 row: seg_slots slots, at most 65528 elements (a count fits 16 bits)
+constexpr int kSampleItems = 6144;
+constexpr int kSampleOdd = 64;
+constexpr int kSampleMaxSegSlots = 8191;
+struct SampleValues {
+  uint16_t items[kSampleItems];  // counts of values, in the order of the row's tokens
+  uint32_t odd[kSampleOdd];      // tokens near zero: value << 16 | place in the segment
 };
 // bins whose tokens a row needs beyond the lists: up to two ranges
 enum { kSampleAskNone = 0, kSampleAskBins = 1, kSampleAskRow = 2 /* more tokens than kSampleAsk: the row is read again */ };
@@ -213,9 +221,10 @@ struct SampleOut {
   uint32_t fill;  // fill value in the element type
 };
 struct SamplePlan {
-  int loads;      // slots per thread of the bin kernel
   int n_seg;      // blocks per row
-  int cap;        // tokens a block lists
+  int seg_slots;  // bf16: slots of a block
+  int loads;      // fp32: slots of a thread
+  int cap;        // fp32: tokens a block lists
   int64_t batch;  // rows per pass over the workspace
   size_t parts, lists, cuts, asks, asked, total;
 };

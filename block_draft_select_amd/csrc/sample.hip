@@ -9,12 +9,19 @@
 // u W(kept) along the same order.  So a cut and a draw are the same question:
 // at which token does a running count or sum cross a value.
 //
-// It is answered without sorting the row.  In units of an eighth of an octave
-// a weight is 2^(t / 8), t = z 8 log2(e) / T, and floor(t) bins the tokens in
-// their order.
-// (1) sample_hist_kernel (sample_count_kernel for long bf16 segments) counts the
-//     tokens and sums the weights of each bin of a row segment, and lists the
-//     segment's largest tokens in the order of their bins.
+// It is answered without sorting the row, in two ways.
+//
+// bf16 rows (few distinct values): sample_values_kernel counts each value of a
+// row segment in LDS; sample_finalize_values_kernel, one block per row, adds
+// the segments' counts in the row's order, weighs each value present once and
+// scans.  A crossing is a value and a place among its equal tokens, which
+// share one weight; that token's index is looked up in its own segment.
+//
+// fp32 rows: in units of an eighth of an octave a weight is 2^(t / 8), t = z
+// 8 log2(e) / T, and floor(t) bins the tokens in their order.
+// (1) sample_hist_kernel counts the tokens and sums the weights of each bin of
+//     a row segment, and lists the segment's largest tokens in the order of
+//     their bins.
 // (2) sample_finalize_kernel, one block per row, adds the segments' bins,
 //     scans them, finds the bin of the crossing and ranks that bin's tokens
 //     alone: a window of at most 512 tokens; a fuller bin is narrowed by key
@@ -24,7 +31,10 @@
 //     draw falls outside the lists ask for the bins they need;
 //     sample_gather_kernel collects those from all segments at once, and
 //     the row is finished by a second run of (2).
-// (4) sample_apply_kernel (dflash_filter) copies the kept tokens.
+// A bf16 row with values out of the counters' range goes the second way, in
+// one block that reads the row as often as it needs.
+//
+// sample_apply_kernel (dflash_filter) copies the kept tokens.
 //
 // Counts are exact and sums do not depend on the order of the atomics: a bin
 // adds the mantissas of 2^frac(t / 8) as 64-bit integers (the upper 51 fraction
@@ -101,6 +111,17 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
 
 // ---------------------------------------------------------------- block helpers (kThreads threads)
 
+// inclusive prefix sum over the 64 lanes
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
+  v += dpp_u32<kDppRowShr1>(v, 0u);
+  v += dpp_u32<kDppRowShr2>(v, 0u);
+  v += dpp_u32<kDppRowShr4>(v, 0u);
+  v += dpp_u32<kDppRowShr8>(v, 0u);
+  v += dpp_u32<kDppRowBcast15, 0xA>(v, 0u);
+  v += dpp_u32<kDppRowBcast31, 0xC>(v, 0u);
+  return v;
+}
+
 // Reductions over the block with one barrier each: successive calls alternate
 // between two buffers, so a buffer is rewritten only after the barrier of the
 // call between, which every thread reaches after it has read the buffer.
@@ -169,16 +190,6 @@ struct BlockOps {
     return v;
   }
 
- private:
-  static __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
-    v += dpp_u32<kDppRowShr1>(v, 0u);
-    v += dpp_u32<kDppRowShr2>(v, 0u);
-    v += dpp_u32<kDppRowShr4>(v, 0u);
-    v += dpp_u32<kDppRowShr8>(v, 0u);
-    v += dpp_u32<kDppRowBcast15, 0xA>(v, 0u);
-    v += dpp_u32<kDppRowBcast31, 0xC>(v, 0u);
-    return v;
-  }
 };
 
 __device__ __forceinline__ uint32_t key_of(float v, float max_finite) {
@@ -204,72 +215,96 @@ __device__ __forceinline__ uint32_t lowest_key(double j, double c8) {
   return l;
 }
 
-// ---------------------------------------------------------------- list entries
-// A listed token: bf16 rows in 32 bits (~key of 16 bits, place in the
-// segment), fp32 rows in 64 (~key, index in the row).
-
-template <int DT>
-struct Entry;
-template <>
-struct Entry<DFLASH_BF16> {
-  using T = uint32_t;
-  static __device__ __forceinline__ T make(uint32_t key, int place, int) { return ((~key >> 16) << 16) | (uint32_t)place; }
-  static __device__ __forceinline__ uint64_t comp(T e, int first) {
-    return ((uint64_t)~ord32_of_k16((~e >> 16) & 0xFFFFu) << 32) | (uint32_t)(first + (int)(e & 0xFFFFu));
-  }
-};
-template <>
-struct Entry<DFLASH_F32> {
-  using T = uint64_t;
-  static __device__ __forceinline__ T make(uint32_t key, int place, int first) {
-    return ((uint64_t)~key << 32) | (uint32_t)(first + place);
-  }
-  static __device__ __forceinline__ uint64_t comp(T e, int) { return e; }
-};
 __device__ __forceinline__ uint32_t comp_key(uint64_t c) { return ~(uint32_t)(c >> 32); }
+__device__ __forceinline__ uint64_t comp_of(uint32_t key, uint32_t index) { return ((uint64_t)~key << 32) | index; }
 
 // ---------------------------------------------------------------- (1) bins of a segment
 
-template <int COLS>
 struct HistLds {
-  uint64_t mass[kBins * COLS];
-  uint32_t cnt[kBins * COLS];
-  uint32_t key[kSamplePick];    // tokens to be listed
-  uint32_t place[kSamplePick];
+  uint64_t mass[kBins * kCols];
+  uint32_t cnt[kBins * kCols];
+  uint32_t pick[kSamplePick];  // tokens to be listed: places in the segment
   uint32_t n_pick;
   Red red;
 };
 
-// `times` equal tokens into their bin
-template <int COLS>
-__device__ __forceinline__ void bin_token(HistLds<COLS>& s, double c8, double J, float v, uint32_t times) {
-  const double t = (double)v * c8, fl = floor(t);
-  const int b = (int)fmin(J - fl, (double)kTail), at = b * COLS + (threadIdx.x & (COLS - 1));
-  atomicAdd(&s.cnt[at], times);
-  if (b < kTail)
-    atomicAdd((unsigned long long*)&s.mass[at],
-              (unsigned long long)(__double_as_longlong(exp2_eighth(t - fl)) >> 1) * times);
+// the upper 51 fraction bits of 2^frac(t / 8), as an integer
+__device__ __forceinline__ unsigned long long weight_bits(double t, double fl) {
+  return (unsigned long long)(__double_as_longlong(exp2_eighth(t - fl)) >> 1);
 }
 
-// after a barrier: the bins to memory; returns the number of leading bins that
-// are listed (at most `cap` tokens together) and leaves in cnt[b * COLS]
-// where bin b's list starts
-template <int COLS>
-__device__ __forceinline__ int write_bins(HistLds<COLS>& s, BlockOps& ops, SamplePart& out, double J, float m, int cap) {
-  const int tid = threadIdx.x;
+// a token into the list, which is in the order of its bins (cnt[b * kCols]: bin b's next place)
+__device__ __forceinline__ void list_token(HistLds& s, uint64_t* list, double c8, double J, uint32_t key, uint32_t index) {
+  const int b = (int)fmin(J - floor(key_value(key) * c8), (double)kTail);
+  list[atomicAdd(&s.cnt[b * kCols], 1u)] = comp_of(key, index);
+}
+
+template <int NL>
+__global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
+                                                               SamplePart* __restrict__ parts, uint64_t* __restrict__ lists) {
+  constexpr int VE = RowType<DFLASH_F32>::VE;
+  constexpr float kMax = RowType<DFLASH_F32>::kMax;
+  __shared__ HistLds s;
+  BlockOps ops(s.red);
+  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
+  const int64_t row = row0 + blockIdx.x / n_seg;
+  const RowRef<DFLASH_F32> z(a.Z, row, a.stride, a.V);
+  const double c8 = row_params(a, row).c8;
+  const int s0 = seg * (kThreads * NL) + tid;
+  Slot x[NL];
+#pragma unroll
+  for (int l = 0; l < NL; ++l) x[l] = z.load<true>(s0 + l * kThreads);
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    s.mass[c * kBins + tid] = 0;
+    s.cnt[c * kBins + tid] = 0;
+  }
+  if (tid == 0) s.n_pick = 0;
+  float m = kNegInf;
+#pragma unroll
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DFLASH_F32>(x[l], i));  // NaN drops out
+  m = (float)ops.max((double)fminf(m, kMax));
+  SamplePart& out = parts[blockIdx.x];
+  if (m == kNegInf) {
+    if (tid == 0) {
+      out.J = -INFINITY;
+      out.max = kNegInf;
+      out.n = 0;
+      out.nb = 0;
+      out.listed = kBins;
+    }
+    return;
+  }
+  const double J = floor((double)m * c8);
+  const int col = tid & (kCols - 1);
+#pragma unroll
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DFLASH_F32>(x[l], i);
+      if (v > kNegInf) {
+        const double t = (double)fminf(v, kMax) * c8, fl = floor(t);
+        const int b = (int)fmin(J - fl, (double)kTail);
+        atomicAdd(&s.cnt[b * kCols + col], 1u);
+        if (b < kTail) atomicAdd((unsigned long long*)&s.mass[b * kCols + col], weight_bits(t, fl));
+      }
+    }
+  __syncthreads();
   uint32_t c = 0, mirror = 0;  // mirror: the bin counted from the far end
   uint64_t f = 0;
 #pragma unroll
-  for (int k = 0; k < COLS; ++k) {
-    c += s.cnt[tid * COLS + k];
-    f += s.mass[tid * COLS + k];
-    mirror += s.cnt[(kBins - 1 - tid) * COLS + k];
+  for (int k = 0; k < kCols; ++k) {
+    c += s.cnt[tid * kCols + k];
+    f += s.mass[tid * kCols + k];
+    mirror += s.cnt[(kBins - 1 - tid) * kCols + k];
   }
   f -= (uint64_t)c * (kOneBits >> 1);  // modulo 2^64: the fraction bits' sum
   const uint32_t upto = ops.scan(c);
   const int nb = kBins - ops.first(mirror != 0);       // bins in use
-  const int listed = ops.first(upto > (uint32_t)cap);
-  s.cnt[tid * COLS] = upto - c;
+  const int listed = ops.first(upto > (uint32_t)cap);  // leading bins with at most `cap` tokens together
+  s.cnt[tid * kCols] = upto - c;
   if (tid < nb) {
     out.upto[tid] = upto;
     out.mass[tid] = tid < kTail ? (double)c + (double)f * 0x1p-51 : 0.0;
@@ -282,266 +317,44 @@ __device__ __forceinline__ int write_bins(HistLds<COLS>& s, BlockOps& ops, Sampl
     out.listed = listed;
   }
   __syncthreads();
-  return listed;
-}
-
-__device__ __forceinline__ void empty_part(SamplePart& out) {
-  if (threadIdx.x == 0) {
-    out.J = -INFINITY;
-    out.max = kNegInf;
-    out.n = 0;
-    out.nb = 0;
-    out.listed = kBins;
-  }
-}
-
-// a token into the list, which is in the order of its bins
-template <int DT, int COLS>
-__device__ __forceinline__ void list_token(HistLds<COLS>& s, typename Entry<DT>::T* list, double c8, double J, uint32_t key,
-                                           int place, int first) {
-  const int b = (int)fmin(J - floor(key_value(key) * c8), (double)kTail);
-  list[atomicAdd(&s.cnt[b * COLS], 1u)] = Entry<DT>::make(key, place, first);
-}
-
-// a token among those to be listed (few: picked first, then listed densely)
-template <int COLS>
-__device__ __forceinline__ void pick(HistLds<COLS>& s, uint32_t key, int place) {
-  const uint32_t i = atomicAdd(&s.n_pick, 1u);
-  if (i < (uint32_t)kSamplePick) {
-    s.key[i] = key;
-    s.place[i] = (uint32_t)place;
-  }
-}
-template <int DT, int COLS>
-__device__ __forceinline__ void list_picked(HistLds<COLS>& s, typename Entry<DT>::T* list, double c8, double J, int first) {
-  __syncthreads();
-  const int n = (int)min(s.n_pick, (uint32_t)kSamplePick);
-  for (int i = threadIdx.x; i < n; i += kThreads) list_token<DT>(s, list, c8, J, s.key[i], (int)s.place[i], first);
-}
-
-// every token through the fp64 weight
-template <int DT, int NL>
-__global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
-                                                               SamplePart* __restrict__ parts,
-                                                               typename Entry<DT>::T* __restrict__ lists) {
-  constexpr int VE = RowType<DT>::VE, COLS = kCols;
-  constexpr float kMax = RowType<DT>::kMax;
-  __shared__ HistLds<COLS> s;
-  BlockOps ops(s.red);
-  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
-  const int64_t row = row0 + blockIdx.x / n_seg;
-  const RowRef<DT> z(a.Z, row, a.stride, a.V);
-  const double c8 = row_params(a, row).c8;
-  const int s0 = seg * (kThreads * NL) + tid;
-  Slot x[NL];
-#pragma unroll
-  for (int l = 0; l < NL; ++l) x[l] = z.template load<true>(s0 + l * kThreads);
-#pragma unroll
-  for (int c = 0; c < COLS; ++c) {
-    s.mass[c * kBins + tid] = 0;
-    s.cnt[c * kBins + tid] = 0;
-  }
-  if (tid == 0) s.n_pick = 0;
-  float m = kNegInf;
-#pragma unroll
-  for (int l = 0; l < NL; ++l)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[l], i));  // NaN drops out
-  m = (float)ops.max((double)fminf(m, kMax));
-  SamplePart& out = parts[blockIdx.x];
-  if (m == kNegInf) return empty_part(out);
-  const double J = floor((double)m * c8);
-#pragma unroll
-  for (int l = 0; l < NL; ++l)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float v = slot_value<DT>(x[l], i);
-      if (v > kNegInf) bin_token(s, c8, J, fminf(v, kMax), 1u);
-    }
-  __syncthreads();
-  const int listed = write_bins(s, ops, out, J, m, cap);
   if (listed == 0) return;
-  typename Entry<DT>::T* list = lists + (size_t)blockIdx.x * cap;
+  uint64_t* list = lists + (size_t)blockIdx.x * cap;
   const int first = seg * (kThreads * NL) * VE;
   if constexpr (NL == 1) {  // cap holds the whole segment
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
-      const float v = slot_value<DT>(x[0], i);
-      if (v > kNegInf) list_token<DT>(s, list, c8, J, key_of(v, kMax), tid * VE + i, first);
+      const float v = slot_value<DFLASH_F32>(x[0], i);
+      if (v > kNegInf) list_token(s, list, c8, J, key_of(v, kMax), (uint32_t)(first + tid * VE + i));
     }
   } else {
+    // few tokens: picked first, worked on densely afterwards
     const uint32_t least = listed >= kBins ? kKeyLowest : lowest_key(J - (double)(listed - 1), c8);
 #pragma unroll
     for (int l = 0; l < NL; ++l)
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        const float v = slot_value<DT>(x[l], i);
-        const uint32_t key = key_of(v, kMax);
-        if (v > kNegInf && key >= least) pick(s, key, (tid + l * kThreads) * VE + i);
-      }
-    list_picked<DT>(s, list, c8, J, first);
-  }
-}
-
-// Long segments of bf16 rows: a token is one of few values, so values are
-// counted first and each value present is weighed once (the same sums, bit for
-// bit).  Counted directly are kMags magnitudes of either sign, up to the
-// largest that can matter (that of the maximum, or of the lowest logit that
-// still has weight); their ordered keys, packed two to a register, map to
-// counters without a branch: counter 0 takes all lower keys (masked, or below
-// every bin), 1 .. kMags the negative ones, kMags + 1 everything nearer to
-// zero, then the positive ones.  The few tokens nearer to zero are picked out
-// and weighed one by one.
-constexpr int kMags = 1920;  // 15 binades
-constexpr int kCounters = 2 * kMags + 2;
-
-template <int NL>
-__global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
-                                                                SamplePart* __restrict__ parts, uint32_t* __restrict__ lists) {
-  constexpr int VE = 8, ND = NL * 4;
-  constexpr float kMax = RowType<DFLASH_BF16>::kMax;
-  constexpr uint32_t kMaskedKey = 0x007Fu, kInfKey = 0xFF80u;  // 16-bit keys of -inf and +inf
-  __shared__ HistLds<1> s;
-  __shared__ uint32_t count[kCounters];
-  __shared__ uint32_t n_masked;
-  BlockOps ops(s.red);
-  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
-  const int64_t row = row0 + blockIdx.x / n_seg;
-  const RowRef<DFLASH_BF16> z(a.Z, row, a.stride, a.V);
-  const double c8 = row_params(a, row).c8;
-  const int s0 = seg * (kThreads * NL) + tid;
-  Slot x[NL];
-#pragma unroll
-  for (int l = 0; l < NL; ++l) x[l] = z.load<true>(s0 + l * kThreads);
-  for (int i = tid; i < kCounters; i += kThreads) count[i] = 0;
-  s.mass[tid] = 0;
-  s.cnt[tid] = 0;
-  if (tid == 0) {
-    s.n_pick = 0;
-    n_masked = 0;
-  }
-  uint32_t o[ND];  // ordered 16-bit keys, two a word
-  uint32_t top = 0;
-#pragma unroll
-  for (int d = 0; d < ND; ++d) {
-    o[d] = ord16x2(x[d >> 2].w[d & 3]);
-    top = max_u16x2(top, o[d]);
-  }
-  const uint32_t kmax16 = (uint32_t)ops.max((double)max(top & 0xFFFFu, top >> 16));
-  SamplePart& out = parts[blockIdx.x];
-  const bool odd_values = kmax16 >= kInfKey;  // +inf or NaN: every token one by one
-  float m;
-  if (!odd_values) {
-    m = kmax16 <= kMaskedKey ? kNegInf : __uint_as_float(unord32(ord32_of_k16(kmax16)));
-  } else {
-    m = kNegInf;
-#pragma unroll 1
-    for (int l = 0; l < NL; ++l) {
-      const Slot y = z.load(s0 + l * kThreads);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DFLASH_BF16>(y, i));
-    }
-    m = (float)ops.max((double)fminf(m, kMax));
-  }
-  if (m == kNegInf) return empty_part(out);
-  const double J = floor((double)m * c8);
-  // the largest magnitude with a counter: m's, or that of the logit 512 eighths of an octave below it
-  const double reach = fmin(fmax(fabs((double)m), fabs((double)m - 512.0 / c8)), (double)kMax);
-  const int top_mag = min((int)(__float_as_uint((float)reach) >> 16) + 1, 0x7F7F);
-  const uint32_t base = (uint32_t)max(1, top_mag + 1 - kMags);  // smallest magnitude with a counter
-  const uint32_t below = 0x7FFFu - base - kMags;                // the key under the lowest counted one
-  bool one_by_one = odd_values;
-  if (!odd_values) {
-    const uint32_t below2 = below * 0x10001u, mid2 = (kMags + 1) * 0x10001u, pos2 = (kMags + 2 * base) * 0x10001u;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      const uint32_t r = subsat_u16x2(o[d], below2);
-      const u16x2 i2 = __builtin_bit_cast(u16x2, min_u16x2(r, mid2)) + __builtin_bit_cast(u16x2, subsat_u16x2(r, pos2));
-      const uint32_t i = __builtin_bit_cast(uint32_t, i2);
-      atomicAdd(&count[i & 0xFFFFu], 1u);
-      atomicAdd(&count[i >> 16], 1u);
-    }
-    __syncthreads();
-    const uint32_t n_mid = count[kMags + 1];
-    one_by_one = n_mid > (uint32_t)kSamplePick;
-    if (!one_by_one && n_mid) {  // the tokens near zero: keys within `base` of either zero
-      const uint32_t from2 = (0x8000u - base) * 0x10001u, width2 = 2 * base * 0x10001u;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const u16x2 r2 = __builtin_bit_cast(u16x2, o[d]) - __builtin_bit_cast(u16x2, from2);
-        const uint32_t near = subsat_u16x2(width2, __builtin_bit_cast(uint32_t, r2));
-        if (near) {
-          if (near & 0xFFFFu) s.key[atomicAdd(&s.n_pick, 1u)] = o[d] & 0xFFFFu;
-          if (near >> 16) s.key[atomicAdd(&s.n_pick, 1u)] = o[d] >> 16;
+        const float v = slot_value<DFLASH_F32>(x[l], i);
+        if (v > kNegInf && key_of(v, kMax) >= least) {
+          const uint32_t at = atomicAdd(&s.n_pick, 1u);
+          if (at < (uint32_t)kSamplePick) s.pick[at] = (uint32_t)((tid + l * kThreads) * VE + i);
         }
       }
-    }
-    if (!one_by_one && count[0]) {  // of the low ones, how many are masked
-      u16x2 k2 = {0, 0};
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-        k2 += __builtin_bit_cast(u16x2, min_u16x2(subsat_u16x2((kMaskedKey + 1) * 0x10001u, o[d]), 0x10001u));
-      const uint32_t k = wave_sum_u32((uint32_t)k2.x + (uint32_t)k2.y);
-      if ((tid & 63) == 0) atomicAdd(&n_masked, k);
-    }
     __syncthreads();
-    if (!one_by_one) {
-      // the counted values, then the picked tokens (counter 0 and the middle one are not values)
-#pragma unroll 1
-      for (int i = tid; i < kCounters + (int)n_mid; i += kThreads) {
-        uint32_t c = 1, k16;
-        if (i < kCounters) {
-          c = i != 0 && i != kMags + 1 ? count[i] : 0u;
-          k16 = i <= kMags ? below + (uint32_t)i : 0x8000u + base + (uint32_t)(i - kMags - 2);
-        } else {
-          k16 = s.key[i - kCounters];
-        }
-        if (c) bin_token(s, c8, J, __uint_as_float(unord32(ord32_of_k16(k16))), c);
-      }
-      if (tid == 0) atomicAdd(&s.cnt[kTail], count[0] - n_masked);
+    const int n = (int)min(s.n_pick, (uint32_t)kSamplePick);
+    for (int i = tid; i < n; i += kThreads) {
+      const int e = first + (int)s.pick[i];
+      list_token(s, list, c8, J, key_of(row_value<DFLASH_F32>(z, e), kMax), (uint32_t)e);
     }
   }
-  if (one_by_one) {  // a NaN or infinity, or many values near zero: every token through the fp64 weight
-#pragma unroll 1
-    for (int l = 0; l < NL; ++l) {
-      const Slot y = z.load(s0 + l * kThreads);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float v = slot_value<DFLASH_BF16>(y, i);
-        if (v > kNegInf) bin_token(s, c8, J, fminf(v, kMax), 1u);
-      }
-    }
-  }
-  __syncthreads();
-  if (tid == 0) s.n_pick = 0;
-  const int listed = write_bins(s, ops, out, J, m, cap);
-  if (listed == 0) return;
-  const uint32_t least = listed >= kBins ? kKeyLowest : lowest_key(J - (double)(listed - 1), c8);
-  // the smallest 16-bit key whose value reaches it; -0 counts as +0
-  uint32_t least16 = least >= 0x80000000u ? (least + 0xFFFFu) >> 16 : least >> 16;
-  if (least16 == 0x8000u) least16 = 0x7FFFu;
-  const uint32_t under2 = (least16 - 1u) * 0x10001u;
-  auto put = [&](uint32_t k16, int place) {
-    if (k16 <= kInfKey) pick(s, k16 == kInfKey ? key_of(kMax, kMax) : ord32_of_k16(k16), place);  // above: NaN
-  };
-#pragma unroll
-  for (int d = 0; d < ND; ++d) {
-    const uint32_t in = subsat_u16x2(o[d], under2);
-    if (in) {
-      const int place = (tid + (d >> 2) * kThreads) * VE + 2 * (d & 3);
-      if (in & 0xFFFFu) put(o[d] & 0xFFFFu, place);
-      if (in >> 16) put(o[d] >> 16, place + 1);
-    }
-  }
-  list_picked<DFLASH_BF16>(s, lists + (size_t)blockIdx.x * cap, c8, J, 0);
 }
 
 // ---------------------------------------------------------------- (2) cuts and draw of a row
 
 enum { kByCount, kByMassGe, kByMassGt, kByWeight };
 // kAll: the lists hold every token.  kFirst: they hold the largest; rows that
-// need others ask for them.  kSecond: the rows that asked.
-enum { kAll, kFirst, kSecond };
+// need others ask for them.  kSecond: the rows that asked.  kSelf: no lists,
+// the row itself is read.
+enum { kAll, kFirst, kSecond, kSelf };
 constexpr int kMaxSeg = kSampleMaxSeg;
 
 struct FinLds {
@@ -572,16 +385,15 @@ struct Cross {
 
 template <int DT, int MODE>
 struct Finalize {
-  using T = typename Entry<DT>::T;
   static constexpr int VE = RowType<DT>::VE;
   FinLds& s;
   BlockOps& ops;
   const RowRef<DT> z;
   const SamplePart* part;
-  const T* lists;
+  const uint64_t* lists;
   const uint64_t* asked;  // the row's asked-for tokens
   const SampleAsk* ask;
-  const int n_seg, cap, seg_elems;
+  const int n_seg, cap;
   const double c8, J;
   const int tid;
   const uint32_t kmax;  // the row's largest key
@@ -601,7 +413,7 @@ struct Finalize {
   // f((~key, index)) of every token of bins B0 .. B1, and of others
   template <class F>
   __device__ __forceinline__ void each(int B0, int B1, F f) {
-    if (MODE == kAll || B1 < listed) {
+    if (MODE != kSelf && (MODE == kAll || B1 < listed)) {
       // a segment's list is in the order of its bins, so its part is one run; 16 threads a segment
       __syncthreads();
       if (tid < n_seg) {
@@ -613,13 +425,13 @@ struct Finalize {
       }
       __syncthreads();
       for (int g = tid >> 4; g < n_seg; g += kThreads / 16) {
-        const T* list = lists + (size_t)g * cap;
-        const int first = g * seg_elems, end = (int)s.to[g];
+        const uint64_t* list = lists + (size_t)g * cap;
+        const int end = (int)s.to[g];
 #pragma unroll 4
-        for (int j = (int)s.from[g] + (tid & 15); j < end; j += 16) f(Entry<DT>::comp(list[j], first));
+        for (int j = (int)s.from[g] + (tid & 15); j < end; j += 16) f(list[j]);
       }
-    } else if constexpr (MODE == kSecond) {
-      if (ask->kind == kSampleAskBins && ((B0 >= ask->b0[0] && B1 <= ask->b1[0]) || (B0 >= ask->b0[1] && B1 <= ask->b1[1]))) {
+    } else if constexpr (MODE == kSecond || MODE == kSelf) {
+      if (MODE == kSecond && ask->kind == kSampleAskBins && ((B0 >= ask->b0[0] && B1 <= ask->b1[0]) || (B0 >= ask->b0[1] && B1 <= ask->b1[1]))) {
         const int end = (int)min(ask->n, (uint32_t)kSampleAsk);
 #pragma unroll 4
         for (int j = tid; j < end; j += kThreads) f(asked[j]);
@@ -631,7 +443,7 @@ struct Finalize {
 #pragma unroll
           for (int i = 0; i < VE; ++i) {
             const float v = slot_value<DT>(x, i);
-            if (v > kNegInf) f(((uint64_t)~key_of(v, RowType<DT>::kMax) << 32) | (uint32_t)(sl * VE + i));
+            if (v > kNegInf) f(comp_of(key_of(v, RowType<DT>::kMax), (uint32_t)(sl * VE + i)));
           }
         }
       }
@@ -743,7 +555,7 @@ struct Finalize {
       if (nc == 0) return Cross{cb, mb, ((uint64_t)~khi) << 32, 0};  // kByWeight: nothing in the threshold's own bin
       int B0 = b;
       bool whole = true;
-      if ((MODE == kAll || b < listed) && s.cc[b + 1] <= (uint32_t)kThreads) {  // everything down to this bin fits a window
+      if (MODE != kSelf && (MODE == kAll || b < listed) && s.cc[b + 1] <= (uint32_t)kThreads) {  // everything down to this bin fits a window
         B0 = 0;
         khi = kmax;
         nc += cb;
@@ -817,6 +629,54 @@ struct Finalize {
       open_window(klo, cb, mb, whole ? B0 : 1, whole ? b : 0);
     }
     return from_window(kind, amount);
+  }
+
+  // the row's cuts and draw, once s.cc and s.cm hold its bins
+  __device__ __forceinline__ void answer(const RowParams& rp, uint32_t N, double wmax, double u, int64_t row, const SampleOut& o,
+                                         uint64_t* cut_out) {
+    uint32_t kept = N;
+    double Z = s.cm[kBins];
+    uint64_t cut = ~0ull;
+    // the cuts (0: top-k, 1: top-p, 2: min-p), the draw (3), and the last kept
+    // token if rounding drew one behind it (4)
+#pragma unroll 1
+    for (int q = 0; q < 5; ++q) {
+      int kind;
+      double amount;
+      if (q == 0) {
+        if (rp.k >= (int64_t)N) continue;
+        kind = kByCount, amount = (double)rp.k;
+      } else if (q == 1) {
+        if (!(rp.p < 1.0)) continue;
+        kind = kByMassGe, amount = rp.p * Z;
+      } else if (q == 2) {
+        if (!(rp.m > 0.0)) continue;
+        kind = kByWeight, amount = rp.m * wmax;
+      } else if (q == 3) {
+        if (tid == 0) {
+          if (o.kept) o.kept[row] = (int32_t)kept;
+          if (o.out) *cut_out = cut;
+        }
+        if (!o.token) break;
+        kind = kByMassGt, amount = u * Z;
+      } else {
+        kind = kByCount, amount = (double)kept;
+      }
+      const Cross x = locate(kind, amount);
+      if (q < 3) {
+        if (x.n < kept) {
+          kept = x.n;
+          Z = x.cum;
+          cut = x.cut;
+        }
+      } else if (q == 4 || x.n <= kept) {
+        if (tid == 0) {
+          o.token[row] = (int32_t)(uint32_t)x.at;
+          if (o.prob) o.prob[row] = (float)(weight(comp_key(x.at)) / Z);
+        }
+        break;
+      }
+    }
   }
 };
 
@@ -894,10 +754,23 @@ __device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowP
   return false;
 }
 
-template <int DT, int MODE>
-__global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap, int seg_elems,
+__device__ __forceinline__ void empty_row(int64_t row, const SampleOut& o, uint64_t* cut_out) {
+  if (threadIdx.x == 0) {
+    if (o.token) o.token[row] = -1;
+    if (o.prob) o.prob[row] = 0.0f;
+    if (o.kept) o.kept[row] = 0;
+    if (o.out) *cut_out = 0;
+  }
+}
+__device__ __forceinline__ double row_uniform(const SampleOut& o, int64_t row) {
+  const double u = o.token ? o.u[row] : 0.0;
+  return u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;  // NaN: 0
+}
+
+template <int MODE>
+__global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
                                                                    const SamplePart* __restrict__ parts,
-                                                                   const typename Entry<DT>::T* __restrict__ lists,
+                                                                   const uint64_t* __restrict__ lists,
                                                                    SampleAsk* __restrict__ asks, const uint64_t* __restrict__ asked,
                                                                    SampleOut o, uint64_t* __restrict__ cuts) {
   if constexpr (MODE == kSecond) {
@@ -917,20 +790,11 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
   const uint32_t ns = have ? part[tid].n : 0;
   const int nbs = have ? part[tid].nb : 0, ls = have ? part[tid].listed : kBins;
   const double ms = have ? (double)part[tid].max : -INFINITY;
-  double u = o.token ? o.u[row] : 0.0;
-  u = u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;  // NaN: 0
+  const double u = row_uniform(o, row);
   const double J = ops.max(Js);
   const float m = (float)ops.max(ms);
   const uint32_t N = ops.sum(ns);
-  if (N == 0) {  // every token masked
-    if (tid == 0) {
-      if (o.token) o.token[row] = -1;
-      if (o.prob) o.prob[row] = 0.0f;
-      if (o.kept) o.kept[row] = 0;
-      if (o.out) cuts[blockIdx.x] = 0;
-    }
-    return;
-  }
+  if (N == 0) return empty_row(row, o, cuts + blockIdx.x);  // every token masked
   const int shift = ns ? (int)fmin(J - Js, (double)kBins) : kBins;
   if (have) {
     s.shift[tid] = (int16_t)shift;
@@ -959,66 +823,24 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
   }
   __syncthreads();
 
-  const uint32_t kmax = key_of(m, RowType<DT>::kMax);
-  Finalize<DT, MODE> f{s, ops, RowRef<DT>(a.Z, row, a.stride, a.V), part, lists + (size_t)blockIdx.x * n_seg * cap,
-                       MODE == kSecond ? asked + (size_t)blockIdx.x * kSampleAsk : nullptr,
-                       MODE == kSecond ? asks + blockIdx.x : nullptr, n_seg, cap, seg_elems, rp.c8, J, tid, kmax, listed,
-                       0, 0, 0.0, 1, 0, 0};
+  const uint32_t kmax = key_of(m, RowType<DFLASH_F32>::kMax);
+  Finalize<DFLASH_F32, MODE> f{s, ops, RowRef<DFLASH_F32>(a.Z, row, a.stride, a.V), part, lists + (size_t)blockIdx.x * n_seg * cap,
+                               MODE == kSecond ? asked + (size_t)blockIdx.x * kSampleAsk : nullptr,
+                               MODE == kSecond ? asks + blockIdx.x : nullptr, n_seg, cap, rp.c8, J, tid, kmax, listed,
+                               0, 0, 0.0, 1, 0, 0};
   const double wmax = f.weight(kmax);
   if constexpr (MODE == kFirst) {
     if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, rp.c8, kmax, listed, asks[blockIdx.x])) return;
   }
-  uint32_t n = N;
-  double Z = s.cm[kBins];
-  uint64_t cut = ~0ull;
-  // the cuts (0: top-k, 1: top-p, 2: min-p), the draw (3), and the last kept
-  // token if rounding drew one behind it (4)
-#pragma unroll 1
-  for (int q = 0; q < 5; ++q) {
-    int kind;
-    double amount;
-    if (q == 0) {
-      if (rp.k >= (int64_t)N) continue;
-      kind = kByCount, amount = (double)rp.k;
-    } else if (q == 1) {
-      if (!(rp.p < 1.0)) continue;
-      kind = kByMassGe, amount = rp.p * Z;
-    } else if (q == 2) {
-      if (!(rp.m > 0.0)) continue;
-      kind = kByWeight, amount = rp.m * wmax;
-    } else if (q == 3) {
-      if (tid == 0) {
-        if (o.kept) o.kept[row] = (int32_t)n;
-        if (o.out) cuts[blockIdx.x] = cut;
-      }
-      if (!o.token) break;
-      kind = kByMassGt, amount = u * Z;
-    } else {
-      kind = kByCount, amount = (double)n;
-    }
-    const Cross x = f.locate(kind, amount);
-    if (q < 3) {
-      if (x.n < n) {
-        n = x.n;
-        Z = x.cum;
-        cut = x.cut;
-      }
-    } else if (q == 4 || x.n <= n) {
-      if (tid == 0) {
-        o.token[row] = (int32_t)(uint32_t)x.at;
-        if (o.prob) o.prob[row] = (float)(f.weight(comp_key(x.at)) / Z);
-      }
-      break;
-    }
-  }
+  f.answer(rp, N, wmax, u, row, o, cuts + blockIdx.x);
 }
 
 // ---------------------------------------------------------------- (3) the tokens that rows asked for
 
-template <int DT, int NL>
+template <int NL>
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, int64_t row0, int n_seg, SampleAsk* __restrict__ asks,
                                                                  uint64_t* __restrict__ asked) {
-  constexpr int VE = RowType<DT>::VE;
+  constexpr int DT = DFLASH_F32, VE = RowType<DT>::VE;
   const int r = blockIdx.x / n_seg, seg = blockIdx.x % n_seg, tid = threadIdx.x;
   SampleAsk& ask = asks[r];
   if (ask.kind != kSampleAskBins) return;
@@ -1058,11 +880,524 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, i
   uint64_t* out = asked + (size_t)r * kSampleAsk;
   for (uint32_t i = tid; i < c && at + i < (uint32_t)kSampleAsk; i += kThreads) {
     const uint32_t idx = place[i];
-    out[at + i] = ((uint64_t)~key_of(row_value<DT>(z, (int)idx), RowType<DT>::kMax) << 32) | idx;
+    out[at + i] = comp_of(key_of(row_value<DT>(z, (int)idx), RowType<DT>::kMax), idx);
   }
 }
 
-// ---------------------------------------------------------------- (4) the filtered row
+// ---------------------------------------------------------------- bf16 rows: counts of values
+// The items of a segment, in the order of the row's tokens: item 0 counts
+// positive values over the range (and NaN), 1 .. kMags the positive values
+// downwards, kMid all that lie nearer to zero, then the negative values, kLow
+// the finite values under the range; masked tokens are not counted.  The range
+// depends on T alone, so that a row's segments agree: kMags magnitudes (23
+// binades) below a power of two over 100 T, at least 128.  A row whose
+// largest logit lies over it, or that has logits under it which still weigh
+// (within 512 eighths of an octave of the largest), is not counted but binned.
+constexpr int kMags = 2944;
+constexpr int kMid = kMags + 1, kLow = 2 * kMags + 2, kItems = kLow + 1;
+constexpr int kGroups = (kItems + 63) / 64;  // groups of 64 items
+static_assert(kGroups * 64 <= kSampleItems && kGroups <= kThreads, "");
+
+// smallest magnitude (bit pattern) with a counter of its own
+__device__ __forceinline__ uint32_t value_base(double c8) {
+  const double T = 8.0 * 1.4426950408889634 / c8;  // c8 = 0: inf
+  const uint32_t e = (__float_as_uint((float)fmin(fmax(100.0 * T, 64.0), 1.7e38)) >> 23) + 1u;
+  return min(e << 7, 0x7F80u) - (uint32_t)kMags;
+}
+
+__global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, int64_t row0, int n_seg, int seg_slots,
+                                                                 SampleValues* __restrict__ parts) {
+  constexpr int VE = 8, U = 4;
+  // counters: 64 that take the masked tokens (one a lane: equal addresses
+  // would queue up) and are not read, 64 for those under the range, then by
+  // ascending value the items kLow - 1 .. 0
+  constexpr int kUnder = 64, kFirst = 128, kCounters = kFirst + kLow;
+  __shared__ uint32_t count[kCounters];
+  __shared__ uint32_t n_odd;
+  const int tid = threadIdx.x, lane = tid & 63, seg = blockIdx.x % n_seg;
+  const int64_t row = row0 + blockIdx.x / n_seg;
+  const RowRef<DFLASH_BF16> z(a.Z, row, a.stride, a.V);
+  const int begin = seg * seg_slots, end = min(begin + seg_slots, z.slots());
+  const uint32_t base = value_base(row_params(a, row).c8);
+  for (int i = tid; i < kCounters; i += kThreads) count[i] = 0;
+  if (tid == 0) n_odd = 0;
+  __syncthreads();
+  // ordered 16-bit keys, two a word, to counters without a branch: with r the
+  // key over the lowest counted one's (0 if it is lower), min(r, kMags + 1)
+  // plus what r exceeds the values nearer to zero by
+  const u16x2 lane2 = (u16x2)((unsigned short)lane), to_under2 = (u16x2)((unsigned short)kUnder),
+              to_first2 = (u16x2)((unsigned short)(kFirst - 1 - kUnder - lane));
+  const uint32_t masked2 = 0x007F007Fu, one2 = 0x00010001u, below2 = (0x7FFFu - base - kMags) * 0x10001u,
+                 mid2 = (kMags + 1) * 0x10001u, pos2 = (kMags + 2 * base) * 0x10001u;
+  auto add = [&](const Slot& x) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t o = ord16x2(x.w[d]), r = subsat_u16x2(o, below2);
+      const u16x2 live = __builtin_bit_cast(u16x2, min_u16x2(subsat_u16x2(o, masked2), one2));
+      const u16x2 in = __builtin_bit_cast(u16x2, min_u16x2(r, one2));
+      u16x2 i2 = __builtin_bit_cast(u16x2, min_u16x2(r, mid2)) +
+                 __builtin_bit_cast(u16x2, min_u16x2(subsat_u16x2(r, pos2), mid2)) + (live * to_under2 + (in * to_first2 + lane2));
+      i2 <<= (u16x2)(2);  // byte offsets
+      const uint32_t i = __builtin_bit_cast(uint32_t, i2);
+      atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(count) + (i & 0xFFFFu)), 1u);
+      atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(count) + (i >> 16)), 1u);
+    }
+  };
+#pragma unroll 1
+  for (int sl = begin + tid; sl < end; sl += U * kThreads) {
+    Slot x[U];
+#pragma unroll
+    for (int l = 0; l < U; ++l) x[l] = z.load<true>(min(sl + l * kThreads, end));
+#pragma unroll
+    for (int l = 0; l < U; ++l)
+      if (sl + l * kThreads < end) add(x[l]);
+  }
+  __syncthreads();
+  SampleValues& out = parts[blockIdx.x];
+  const uint32_t n_mid = count[kFirst + kLow - 1 - kMid];
+  if (n_mid != 0 && n_mid <= (uint32_t)kSampleOdd) {  // the few tokens near zero: find them again
+#pragma unroll 1
+    for (int sl = begin + tid; sl < end; sl += kThreads) {
+      const Slot x = z.load(sl);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const uint32_t w = (i & 1) ? x.w[i >> 1] >> 16 : x.w[i >> 1] & 0xFFFFu;
+        if ((w & 0x7FFFu) < base) out.odd[atomicAdd(&n_odd, 1u)] = w << 16 | (uint32_t)((sl - begin) * VE + i);
+      }
+    }
+  }
+  uint32_t* items = reinterpret_cast<uint32_t*>(out.items);
+  for (int j = tid; j < kLow / 2; j += kThreads)
+    items[j] = count[kFirst + kLow - 1 - 2 * j] | count[kFirst + kLow - 2 - 2 * j] << 16;
+  if (tid < 64) {
+    const uint32_t under = wave_sum_u32(count[kUnder + tid]);
+    if (tid == 0) items[kLow / 2] = under;
+  }
+}
+
+struct ValLds {
+  uint32_t c[kGroups * 64];  // tokens of each item
+  uint32_t gc[kGroups + 1];  // tokens before each group of 64 items
+  double gm[kGroups + 1];    // and their weight
+  uint64_t win[kThreads];    // the tokens near zero, sorted
+  double wcum[kThreads];     // their running weight
+  Red red;
+  uint32_t n;
+  uint32_t at, idx;
+};
+union RowLds {
+  ValLds v;
+  FinLds f;
+  __device__ RowLds() {}
+};
+
+// where a running count or sum crosses a value: an item and a place in it
+struct ValueCross {
+  uint32_t n;   // tokens up to and including the crossing one (kByWeight: tokens that pass)
+  double cum;   // their weight
+  int item;
+  uint32_t r;   // tokens of this item among them
+};
+
+struct Values {
+  ValLds& s;
+  BlockOps& ops;
+  const RowRef<DFLASH_BF16> z;
+  const SampleValues* part;
+  const int n_seg, seg_slots, tid;
+  const double c8;
+  const uint32_t base;
+  double tm;             // c8 times the largest logit
+  uint32_t n_mid, n_in;  // tokens near zero, tokens in the range
+
+  // the logit of a counted value
+  __device__ __forceinline__ float value(int item) const {
+    const int mag = (int)base + (item < kMid ? kMags - item : item - kMid - 1);
+    const float v = __uint_as_float((uint32_t)mag << 16);
+    return item < kMid ? v : -v;
+  }
+  // relative to the row's largest token, whose weight is exactly 1
+  __device__ __forceinline__ double weight(double v) const {
+    const double t = v * c8 - tm, fl = floor(t);
+    return exp2_eighth(t - fl) * pow2_eighth((int)fmax(fl, -16000.0));
+  }
+  __device__ __forceinline__ double near_value(uint32_t i) const { return key_value(comp_key(s.win[i])); }
+
+  // group g on a wave: this lane's item, its tokens, the weight of one of
+  // them (of all for kMid) and the running count and sum inside the group
+  __device__ __forceinline__ void group(int g, uint32_t& c, double& w, uint32_t& upto, double& cum) const {
+    const int item = g * 64 + lane_id();
+    c = item >= 1 && item < kLow ? s.c[item] : 0u;
+    w = c && item != kMid ? weight((double)value(item)) : 0.0;
+    double all = (double)c * w;
+    if (item == kMid && c) all = w = s.wcum[n_mid - 1];
+    upto = wave_scan_u32(c);
+    cum = wave_scan_f64(all);
+  }
+
+  __device__ __forceinline__ ValueCross locate(int kind, double amount) {
+    // a sum within 2^-44 of the value counts as equal to it: rows of equal
+    // logits meet dyadic settings exactly, and the sums round (below 2^-47)
+    if (kind == kByMassGe) amount *= 1.0 - 0x1p-44;
+    if (kind == kByMassGt) amount *= 1.0 + 0x1p-44;
+    bool hit = false;
+    if (tid < kGroups) {
+      const bool some = s.gc[tid + 1] != s.gc[tid];
+      if (kind == kByCount) hit = (double)s.gc[tid + 1] >= amount;
+      else if (kind == kByMassGe) hit = some && s.gm[tid + 1] >= amount;
+      else if (kind == kByMassGt) hit = some && s.gm[tid + 1] > amount;
+      else {  // the group's last value passes or not, present or not
+        const int item = min(tid * 64 + 63, kLow - 1);
+        hit = weight(item == kMid ? (n_mid ? near_value(n_mid - 1) : 0.0) : (double)value(item)) < amount;
+      }
+    }
+    int g = ops.first(hit);
+    const bool none = g >= kGroups;
+    if (none) {
+      if (kind == kByWeight) return ValueCross{n_in, s.gm[kGroups], -1, 0};
+      g = ops.first(tid < kGroups && s.gc[tid + 1] >= n_in);  // rounding left the sum short: the last token
+    }
+    // every wave works the group out for itself
+    const int lane = lane_id(), item = g * 64 + lane;
+    const uint32_t n0 = s.gc[g];
+    const double m0 = s.gm[g];
+    uint32_t c, upto;
+    double w, cum;
+    group(g, c, w, upto, cum);
+    const uint32_t in_group = s.gc[g + 1] - n0;
+    bool cross;
+    if (kind == kByWeight) {
+      cross = item >= 1 && item < kLow &&
+              (item == kMid ? (n_mid ? weight(near_value(n_mid - 1)) : weight(0.0)) : weight((double)value(item))) < amount;
+    } else {
+      const bool last = upto == in_group;
+      cross = c != 0 && (none ? last
+                         : kind == kByCount    ? (double)(n0 + upto) >= amount
+                         : kind == kByMassGe ? m0 + cum >= amount || last
+                                             : m0 + cum > amount || last);
+    }
+    const int l = min(first_lane(cross), 63);
+    const uint32_t lc = __shfl(c, l), n1 = n0 + __shfl(upto, l) - lc;  // before the item
+    const double lw = __shfl(w, l), before = m0 + (l > 0 ? __shfl(cum, max(l - 1, 0)) : 0.0);
+    const int li = g * 64 + l;
+    if (li == kMid && lc) {  // among the tokens near zero, one by one
+      const bool in = tid < (int)n_mid;
+      const bool h = in && (kind == kByCount    ? (double)(n1 + tid + 1) >= amount
+                            : kind == kByMassGe ? before + s.wcum[tid] >= amount
+                            : kind == kByMassGt ? before + s.wcum[tid] > amount
+                                                : weight(near_value(tid)) < amount);
+      int pos = min(ops.first(h), (int)n_mid);
+      if (kind != kByWeight) pos = none ? (int)n_mid : min(pos + 1, (int)n_mid);
+      return ValueCross{n1 + pos, pos ? before + s.wcum[pos - 1] : before, kMid, (uint32_t)pos};
+    }
+    if (kind == kByWeight) return ValueCross{n1, before, li, 0};
+    double r = (double)lc;
+    if (!none) {
+      if (kind == kByCount) {
+        r = amount - (double)n1;
+      } else {
+        r = fmin(fmax(floor((amount - before) / lw), 0.0), (double)lc);
+        // the quotient is off by rounding only: settle it on the sums themselves
+        if (r > 0.0 && (kind == kByMassGe ? fma(r - 1.0, lw, before) >= amount : fma(r - 1.0, lw, before) > amount)) r -= 1.0;
+        if (r < (double)lc && !(kind == kByMassGe ? fma(r, lw, before) >= amount : fma(r, lw, before) > amount)) r += 1.0;
+        r = fmax(r, 1.0);
+      }
+    }
+    return ValueCross{n1 + (uint32_t)r, fma(r, lw, before), li, (uint32_t)r};
+  }
+
+  __device__ __forceinline__ uint32_t item_key(const ValueCross& x) const {
+    return x.item == kMid ? comp_key(s.win[min(max(x.r, 1u), max(n_mid, 1u)) - 1]) : ord32(__float_as_uint(value(x.item)));
+  }
+
+  // index of the r-th (from 1) token of an item, in index order
+  __device__ __forceinline__ uint32_t index_of(int item, uint32_t r) {
+    if (item == kMid) return (uint32_t)s.win[r - 1];
+    // its segment, by the segments' own counts (n_seg <= kThreads)
+    const uint32_t has = tid < n_seg ? part[tid].items[item] : 0u, sc = ops.scan(has);
+    const int g = min(ops.first(sc >= r), n_seg - 1);
+    if (tid == g) s.n = sc - has;
+    __syncthreads();
+    r -= s.n;
+    const uint32_t want = __float_as_uint(value(item)) >> 16;
+    // its thread's piece of the segment (at most 16 slots)
+    const int begin = g * seg_slots, end = min(begin + seg_slots, z.slots()), per = (seg_slots + kThreads - 1) / kThreads;
+    const int sb = min(begin + tid * per, end), se = min(sb + per, end);
+    uint32_t found = 0;
+#pragma unroll 1
+    for (int sl = sb; sl < se; sl += 4) {
+      Slot x[4];
+#pragma unroll
+      for (int l = 0; l < 4; ++l) x[l] = z.load(min(sl + l, z.slots()));
+#pragma unroll
+      for (int l = 0; l < 4; ++l)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          if (sl + l < se) found += (uint32_t)((x[l].w[d] & 0xFFFFu) == want) + (uint32_t)(x[l].w[d] >> 16 == want);
+    }
+    const uint32_t upto = ops.scan(found);
+    const int t = min(ops.first(upto >= r), kThreads - 1);
+    if (tid == t) {
+      s.n = upto - found;
+      s.at = (uint32_t)sb;
+    }
+    __syncthreads();
+    // its place in the piece, an element a thread
+    r -= s.n;
+    const int e = (int)s.at * 8 + tid;
+    const bool here = tid < per * 8 && e < z.V && z.p[min(e, z.V - 1)] == (uint16_t)want;
+    const uint32_t rank = ops.scan((uint32_t)here);
+    if (here && rank == r) s.idx = (uint32_t)e;
+    __syncthreads();
+    return s.idx;
+  }
+};
+
+// one bf16 row from its segments' counts; false if the row has to be binned
+__device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, int64_t row, int n_seg, int seg_slots,
+                                                const SampleValues* __restrict__ part, const SampleOut& o, uint64_t* cut_out) {
+  constexpr int VE = 8, kPairs = kGroups * 32, kMine = (kPairs + kThreads - 1) / kThreads;
+  BlockOps ops(s.red);
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const RowParams rp = row_params(a, row);
+  const double c8 = rp.c8, u = row_uniform(o, row);
+  const uint32_t base = value_base(c8);
+  // the segments' counts, added two a word where no sum of 16 bits can carry
+  uint32_t c0[kMine], c1[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) c0[j] = c1[j] = 0;
+#pragma unroll 2
+  for (int g = 0; g < n_seg; ++g) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(part[g].items);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int i = tid + j * kThreads;
+      const uint32_t v = 2 * i < kItems ? p[i] : 0u;
+      c0[j] += v & 0xFFFFu;
+      c1[j] += v >> 16;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int i = tid + j * kThreads;
+    if (i < kPairs) {
+      s.c[2 * i] = c0[j];
+      s.c[2 * i + 1] = 2 * i + 1 < kItems ? c1[j] : 0u;
+    }
+  }
+  if (tid == 0) s.n = 0;
+  __syncthreads();
+  const uint32_t n_over = s.c[0], n_mid = s.c[kMid], n_low = s.c[kLow];
+  if (n_over || n_mid > (uint32_t)kThreads) return false;
+  if (n_mid) {
+    // the tokens near zero, from the segments' lists; too many in one segment: not listed
+    bool full = false;
+    for (int g = tid; g < n_seg; g += kThreads) {
+      const uint32_t k = part[g].items[kMid];
+      full |= k > (uint32_t)kSampleOdd;
+      if (k && k <= (uint32_t)kSampleOdd) {
+        uint32_t at = atomicAdd(&s.n, k);
+#pragma unroll 1
+        for (uint32_t j = 0; j < k && at < (uint32_t)kThreads; ++j, ++at) {
+          const uint32_t e = part[g].odd[j];
+          s.win[at] = comp_of(ord32_canon(e & 0xFFFF0000u), (uint32_t)(g * seg_slots * VE) + (e & 0xFFFFu));
+        }
+      }
+    }
+    if (ops.first(full) < kThreads) return false;
+    __syncthreads();
+    const bool in = tid < (int)n_mid;
+    const uint64_t me = in ? s.win[tid] : 0;
+    uint32_t rank = 0;
+    if ((tid & ~63) < (int)n_mid) {
+#pragma unroll 4
+      for (uint32_t j = 0; j < n_mid; ++j) rank += s.win[j] < me;
+    }
+    __syncthreads();
+    if (in) s.win[rank] = me;
+    __syncthreads();
+  }
+  Values f{s, ops, RowRef<DFLASH_BF16>(a.Z, row, a.stride, a.V), part, n_seg, seg_slots, tid, c8, base, 0.0, n_mid, 0};
+  // the largest token: the first item with any
+  int top = kItems;
+#pragma unroll 1
+  for (int g = wave; g < kGroups; g += kWaves) {
+    const int item = g * 64 + lane;
+    const int l = first_lane(item >= 1 && item < kLow && s.c[item] != 0);
+    if (l < 64) {
+      top = g * 64 + l;
+      break;
+    }
+  }
+  top = kItems - (int)ops.max((double)(kItems - top));
+  if (top >= kItems) {
+    if (n_low) return false;
+    empty_row(row, o, cut_out);
+    return true;
+  }
+  const double m = top == kMid ? f.near_value(0) : (double)f.value(top);
+  if (n_low && m - 512.0 / c8 < -(double)__uint_as_float(min((base + (uint32_t)kMags) << 16, 0x7F7F0000u))) return false;
+  f.tm = m * c8;
+  if (n_mid) {
+    const double sc = ops.scan(tid < (int)n_mid ? f.weight(f.near_value(tid)) : 0.0);
+    if (tid < (int)n_mid) s.wcum[tid] = sc;
+    __syncthreads();
+  }
+  // each group's tokens and weight, then before each group
+#pragma unroll 1
+  for (int g = wave; g < kGroups; g += kWaves) {
+    const int item = g * 64 + lane;
+    uint32_t c = 0, upto = 0;
+    double w, cum = 0.0;
+    if (__ballot(item >= 1 && item < kLow && s.c[item] != 0)) f.group(g, c, w, upto, cum);
+    if (lane == 63) {
+      s.gc[g + 1] = upto;
+      s.gm[g + 1] = cum;
+    }
+  }
+  __syncthreads();
+  {
+    const uint32_t gc = ops.scan(tid < kGroups ? s.gc[tid + 1] : 0u);
+    const double gm = ops.scan(tid < kGroups ? s.gm[tid + 1] : 0.0);
+    if (tid < kGroups) {
+      s.gc[tid + 1] = gc;
+      s.gm[tid + 1] = gm;
+    }
+    if (tid == 0) {
+      s.gc[0] = 0;
+      s.gm[0] = 0.0;
+    }
+    __syncthreads();
+  }
+  const uint32_t n_in = s.gc[kGroups], N = n_in + n_low;
+  f.n_in = n_in;
+  const double total = s.gm[kGroups];
+
+  uint32_t kept = N;
+  double Z = total;
+  ValueCross cut{N, total, -1, 0}, draw{0, 0.0, -1, 0};
+  bool in_low = false;  // a cut among the tokens under the range
+#pragma unroll 1
+  for (int q = 0; q < 5; ++q) {
+    int kind;
+    double amount;
+    if (q == 0) {
+      if (rp.k >= (int64_t)N) continue;
+      if (rp.k > (int64_t)n_in) {
+        in_low = true;
+        kept = (uint32_t)rp.k;
+        continue;
+      }
+      kind = kByCount, amount = (double)rp.k;
+    } else if (q == 1) {
+      if (!(rp.p < 1.0)) continue;
+      kind = kByMassGe, amount = rp.p * Z;
+    } else if (q == 2) {
+      if (!(rp.m > 0.0)) continue;
+      kind = kByWeight, amount = rp.m;
+    } else if (q == 3) {
+      if (in_low && o.out) return false;  // the cut itself is needed
+      if (!o.token) break;
+      kind = kByMassGt, amount = u * Z;
+    } else {
+      kind = kByCount, amount = (double)min(kept, n_in);
+    }
+    const ValueCross x = f.locate(kind, amount);
+    if (q < 3) {
+      if (x.item < 0) {  // all tokens of the range pass min-p
+        if (n_low) return false;
+      } else if (x.n < kept) {
+        kept = x.n;
+        Z = x.cum;
+        cut = x;
+        in_low = false;
+      }
+    } else {
+      draw = x;
+      if (q == 4 || x.n <= min(kept, n_in)) break;
+    }
+  }
+  if (tid == 0 && o.kept) o.kept[row] = (int32_t)kept;
+  // the index of the cut's or the drawn token (a call has one or the other)
+  const ValueCross x = o.out ? cut : draw;
+  uint32_t idx = 0;
+  if (x.item >= 0 && (x.r > 0 || o.token)) idx = f.index_of(x.item, max(x.r, 1u));
+  if (tid == 0) {
+    if (o.out) *cut_out = x.item < 0 ? ~0ull : x.r == 0 ? (uint64_t)~(x.item != kMid ? f.item_key(x) : n_mid ? comp_key(s.win[0]) : 0x80000000u) << 32
+                                                        : comp_of(f.item_key(x), idx) + 1;
+    if (o.token) {
+      o.token[row] = (int32_t)idx;
+      if (o.prob) o.prob[row] = (float)(f.weight(key_value(f.item_key(x))) / Z);
+    }
+  }
+  return true;
+}
+
+// a bf16 row by bins, in one block: maximum, bins, then passes over the row
+__device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, int64_t row, const SampleOut& o, uint64_t* cut_out) {
+  constexpr int DT = DFLASH_BF16, VE = 8;
+  constexpr float kMax = RowType<DT>::kMax;
+  BlockOps ops(s.red);
+  const int tid = threadIdx.x;
+  const RowParams rp = row_params(a, row);
+  const RowRef<DT> z(a.Z, row, a.stride, a.V);
+  const int n_slots = z.slots();
+  float m = kNegInf;
+#pragma unroll 2
+  for (int sl = tid; sl < n_slots; sl += kThreads) {
+    const Slot x = z.load(sl);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x, i));
+  }
+  m = (float)ops.max((double)fminf(m, kMax));
+  if (m == kNegInf) return empty_row(row, o, cut_out);
+  const double c8 = rp.c8, J = floor((double)m * c8);
+  s.mass[tid] = 0;
+  s.cnt[tid] = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int sl = tid; sl < n_slots; sl += kThreads) {
+    const Slot x = z.load(sl);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DT>(x, i);
+      if (v > kNegInf) {
+        const double t = (double)fminf(v, kMax) * c8, fl = floor(t);
+        const int b = (int)fmin(J - fl, (double)kTail);
+        atomicAdd(&s.cnt[b], 1u);
+        // 46 bits of the mantissa: sums of 2^21 tokens fit 64 bits
+        if (b < kTail)
+          atomicAdd((unsigned long long*)&s.mass[b],
+                    (unsigned long long)((__double_as_longlong(exp2_eighth(t - fl)) - kOneBits) >> 6));
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t c = s.cnt[tid], cs = ops.scan(c);
+  const double cum = ops.scan(tid < kTail ? ((double)c + (double)s.mass[tid] * 0x1p-46) * pow2_eighth(-tid) : 0.0);
+  s.cc[tid + 1] = cs;
+  s.cm[tid + 1] = cum;
+  if (tid == 0) {
+    s.cc[0] = 0;
+    s.cm[0] = 0.0;
+  }
+  __syncthreads();
+  const uint32_t kmax = key_of(m, kMax);
+  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, c8, J, tid, kmax, 0, 0, 0, 0.0, 1, 0, 0};
+  f.answer(rp, s.cc[kBins], f.weight(kmax), row_uniform(o, row), row, o, cut_out);
+}
+
+__global__ __launch_bounds__(kThreads, 4) void sample_finalize_values_kernel(SampleArgs a, int64_t row0, int n_seg, int seg_slots,
+                                                                          const SampleValues* __restrict__ parts, SampleOut o,
+                                                                          uint64_t* __restrict__ cuts) {
+  __shared__ RowLds s;
+  const int64_t row = row0 + blockIdx.x;
+  if (finalize_values(s.v, a, row, n_seg, seg_slots, parts + (size_t)blockIdx.x * n_seg, o, cuts + blockIdx.x)) return;
+  __syncthreads();
+  finalize_self(s.f, a, row, o, cuts + blockIdx.x);
+}
+
+// ---------------------------------------------------------------- the filtered row
 
 template <int DT, int NL>
 __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, int64_t row0, int n_seg,
@@ -1101,56 +1436,71 @@ __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, in
   }
 }
 
-template <int DT, int NL>
-hipError_t run(const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl, hipStream_t st) {
-  using T = typename Entry<DT>::T;
-  SamplePart* parts = reinterpret_cast<SamplePart*>(ws + pl.parts);
-  T* lists = reinterpret_cast<T*>(ws + pl.lists);
+template <int DT>
+void apply(const SampleArgs& a, const SampleOut& o, int64_t r0, unsigned nr, const uint64_t* cuts, hipStream_t st) {
+  const int slots = (a.V + RowType<DT>::VE - 1) / RowType<DT>::VE;
+  const unsigned n8 = (unsigned)((slots + kThreads * 8 - 1) / (kThreads * 8)), n1 = (unsigned)((slots + kThreads - 1) / kThreads);
+  if ((uint64_t)nr * n8 >= 1024)  // four blocks per CU and more
+    launch(sample_apply_kernel<DT, 8>, dim3(nr * n8), dim3(kThreads), st, a, r0, (int)n8, cuts, o.fill, o.out, o.out_stride);
+  else
+    launch(sample_apply_kernel<DT, 1>, dim3(nr * n1), dim3(kThreads), st, a, r0, (int)n1, cuts, o.fill, o.out, o.out_stride);
+}
+
+hipError_t run_bf16(const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl, hipStream_t st) {
+  SampleValues* parts = reinterpret_cast<SampleValues*>(ws + pl.parts);
   uint64_t* cuts = reinterpret_cast<uint64_t*>(ws + pl.cuts);
-  SampleAsk* asks = reinterpret_cast<SampleAsk*>(ws + pl.asks);
-  uint64_t* asked = reinterpret_cast<uint64_t*>(ws + pl.asked);
-  const dim3 block(kThreads);
-  const int seg_elems = kThreads * NL * RowType<DT>::VE;
   for (int64_t r0 = 0; r0 < a.R; r0 += pl.batch) {
     const unsigned nr = (unsigned)(a.R - r0 < pl.batch ? a.R - r0 : pl.batch);
-    const dim3 rows(nr), segs(nr * (unsigned)pl.n_seg);
-    if constexpr (DT == DFLASH_BF16 && NL >= 4)
-      launch(sample_count_kernel<NL>, segs, block, st, a, r0, pl.n_seg, pl.cap, parts, lists);
-    else
-      launch(sample_hist_kernel<DT, NL>, segs, block, st, a, r0, pl.n_seg, pl.cap, parts, lists);
-    if constexpr (NL == 1) {
-      launch(sample_finalize_kernel<DT, kAll>, rows, block, st, a, r0, pl.n_seg, pl.cap, seg_elems, (const SamplePart*)parts,
-             (const T*)lists, asks, (const uint64_t*)asked, o, cuts);
-    } else {
-      launch(sample_finalize_kernel<DT, kFirst>, rows, block, st, a, r0, pl.n_seg, pl.cap, seg_elems, (const SamplePart*)parts,
-             (const T*)lists, asks, (const uint64_t*)asked, o, cuts);
-      launch(sample_gather_kernel<DT, NL>, segs, block, st, a, r0, pl.n_seg, asks, asked);
-      launch(sample_finalize_kernel<DT, kSecond>, rows, block, st, a, r0, pl.n_seg, pl.cap, seg_elems, (const SamplePart*)parts,
-             (const T*)lists, asks, (const uint64_t*)asked, o, cuts);
-    }
-    if (o.out)
-      launch(sample_apply_kernel<DT, NL>, segs, block, st, a, r0, pl.n_seg, (const uint64_t*)cuts, o.fill, o.out, o.out_stride);
+    launch(sample_values_kernel, dim3(nr * (unsigned)pl.n_seg), dim3(kThreads), st, a, r0, pl.n_seg, pl.seg_slots, parts);
+    launch(sample_finalize_values_kernel, dim3(nr), dim3(kThreads), st, a, r0, pl.n_seg, pl.seg_slots, (const SampleValues*)parts,
+           o, cuts);
+    if (o.out) apply<DFLASH_BF16>(a, o, r0, nr, cuts, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <int DT>
-hipError_t run_nl(const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl, hipStream_t st) {
-  switch (pl.loads) {
-    case 1: return run<DT, 1>(a, o, ws, pl, st);
-    case 2: return run<DT, 2>(a, o, ws, pl, st);
-    case 4: return run<DT, 4>(a, o, ws, pl, st);
-    default: return run<DT, 8>(a, o, ws, pl, st);
+template <int NL>
+hipError_t run_f32(const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl, hipStream_t st) {
+  SamplePart* parts = reinterpret_cast<SamplePart*>(ws + pl.parts);
+  uint64_t* lists = reinterpret_cast<uint64_t*>(ws + pl.lists);
+  uint64_t* cuts = reinterpret_cast<uint64_t*>(ws + pl.cuts);
+  SampleAsk* asks = reinterpret_cast<SampleAsk*>(ws + pl.asks);
+  uint64_t* asked = reinterpret_cast<uint64_t*>(ws + pl.asked);
+  const dim3 block(kThreads);
+  for (int64_t r0 = 0; r0 < a.R; r0 += pl.batch) {
+    const unsigned nr = (unsigned)(a.R - r0 < pl.batch ? a.R - r0 : pl.batch);
+    const dim3 rows(nr), segs(nr * (unsigned)pl.n_seg);
+    launch(sample_hist_kernel<NL>, segs, block, st, a, r0, pl.n_seg, pl.cap, parts, lists);
+    if constexpr (NL == 1) {
+      launch(sample_finalize_kernel<kAll>, rows, block, st, a, r0, pl.n_seg, pl.cap, (const SamplePart*)parts,
+             (const uint64_t*)lists, asks, (const uint64_t*)asked, o, cuts);
+    } else {
+      launch(sample_finalize_kernel<kFirst>, rows, block, st, a, r0, pl.n_seg, pl.cap, (const SamplePart*)parts,
+             (const uint64_t*)lists, asks, (const uint64_t*)asked, o, cuts);
+      launch(sample_gather_kernel<NL>, segs, block, st, a, r0, pl.n_seg, asks, asked);
+      launch(sample_finalize_kernel<kSecond>, rows, block, st, a, r0, pl.n_seg, pl.cap, (const SamplePart*)parts,
+             (const uint64_t*)lists, asks, (const uint64_t*)asked, o, cuts);
+    }
+    if (o.out) apply<DFLASH_F32>(a, o, r0, nr, cuts, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t launch_sample(int32_t dtype, const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl,
                          hipStream_t st) {
-  return dtype == DFLASH_BF16 ? run_nl<DFLASH_BF16>(a, o, ws, pl, st) : run_nl<DFLASH_F32>(a, o, ws, pl, st);
+  if (dtype == DFLASH_BF16) return run_bf16(a, o, ws, pl, st);
+  switch (pl.loads) {
+    case 1: return run_f32<1>(a, o, ws, pl, st);
+    case 2: return run_f32<2>(a, o, ws, pl, st);
+    case 4: return run_f32<4>(a, o, ws, pl, st);
+    default: return run_f32<8>(a, o, ws, pl, st);
+  }
 }
 
 }  // namespace dfk
