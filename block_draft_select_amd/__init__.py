@@ -356,40 +356,53 @@ def rows_workspace(r, device="cuda"):
 
 
 def _row_tensor(t, name, r, device, stride=None):
-    """Pointer of a tensor of rows ``r`` (``stride``: None takes its own, and
-    the row stride is returned with it)."""
+    """Pointer and row stride of a tensor of rows ``r`` (``stride``: the row
+    stride it must have)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    own = rows(t)
-    if (own.R, own.V, own.dtype) != (r.R, r.V, r.dtype):
+    if t.dim() == 2 and t.stride(1) == 1 and t.shape[0] > 1:  # the usual case without the walk over dimensions
+        own_R, own_V, own_stride, own_dtype = t.shape[0], t.shape[1], t.stride(0), _ROWS_DTYPE.get(t.dtype)
+    else:
+        own = rows(t)
+        own_R, own_V, own_stride, own_dtype = own.R, own.V, own.stride, own.dtype
+    if own_R != r.R or own_V != r.V or own_dtype != r.dtype:
         raise ValueError(f"{name} must hold {r.R} rows of {r.V} logits of the rows' dtype")
-    if stride is not None and own.R > 1 and own.stride != stride:
-        raise ValueError(f"{name} must have the row stride {stride}, got {own.stride}")
-    _on(t, name, device)
-    return ctypes.c_void_p(t.data_ptr()), own.stride
+    if stride is not None and own_R > 1 and own_stride != stride:
+        raise ValueError(f"{name} must have the row stride {stride}, got {own_stride}")
+    if t.device != device or not t.is_cuda:
+        _on(t, name, device)
+    return t.data_ptr(), own_stride
 
 
 def _on(t, name, device):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the rows are on {device}")
 
 
 def _vec(t, name, dtype, numel, device, optional=False):
-    p = _ptr(t, name, dtype, numel, optional)
-    if t is not None:
-        _on(t, name, device)
-    return p
+    if t is None and optional:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and (numel is None or t.numel() == numel)
+            and t.device == device and t.is_cuda and t.is_contiguous()):
+        return t.data_ptr()
+    _ptr(t, name, dtype, numel, optional)  # raises what is wrong with it
+    _on(t, name, device)
 
 
-def _stream_on(device, stream):
-    """The stream to launch on: the given one, or the current one of the tensors' device."""
+def _call(fn, device, stream, *args):
+    """Call an entry point on ``stream`` (None: the current stream of the
+    tensors' device), with that device current."""
     if stream is None:
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the rows are on {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream.cuda_stream))
 
 
 def _filters(r, device, T, top_k, top_p, min_p, group):
@@ -406,12 +419,10 @@ def dflash_sample(r, Z, u, token, ws, T=None, top_k=None, top_p=None, min_p=None
     top_k, top_p, min_p (one value per ``group`` rows; None: off)."""
     dev = Z.device
     f = _filters(r, dev, T, top_k, top_p, min_p, group)
-    with torch.cuda.device(dev):
-        _check(lib.dflash_sample(ctypes.byref(r), _row_tensor(Z, "Z", r, dev, r.stride)[0], ctypes.byref(f),
-                                 _vec(u, "u", torch.float64, r.R, dev), _vec(token, "token", torch.int32, r.R, dev),
-                                 _vec(prob, "prob", torch.float32, r.R, dev, True),
-                                 _vec(kept, "kept", torch.int32, r.R, dev, True), _vec(ws, "ws", torch.uint8, None, dev),
-                                 ws.numel(), _stream_on(dev, stream)))
+    _call(lib.dflash_sample, dev, stream, r, _row_tensor(Z, "Z", r, dev, r.stride)[0], f,
+          _vec(u, "u", torch.float64, r.R, dev), _vec(token, "token", torch.int32, r.R, dev),
+          _vec(prob, "prob", torch.float32, r.R, dev, True), _vec(kept, "kept", torch.int32, r.R, dev, True),
+          _vec(ws, "ws", torch.uint8, None, dev), ws.numel())
 
 
 def dflash_filter(r, Z, out, ws, fill=None, T=None, top_k=None, top_p=None, min_p=None, group=1, kept=None, stream=None):
@@ -423,10 +434,8 @@ def dflash_filter(r, Z, out, ws, fill=None, T=None, top_k=None, top_p=None, min_
         fill = torch.finfo(Z.dtype).min
     f = _filters(r, dev, T, top_k, top_p, min_p, group)
     po, so = _row_tensor(out, "out", r, dev)
-    with torch.cuda.device(dev):
-        _check(lib.dflash_filter(ctypes.byref(r), _row_tensor(Z, "Z", r, dev, r.stride)[0], ctypes.byref(f), float(fill),
-                                 po, so, _vec(kept, "kept", torch.int32, r.R, dev, True),
-                                 _vec(ws, "ws", torch.uint8, None, dev), ws.numel(), _stream_on(dev, stream)))
+    _call(lib.dflash_filter, dev, stream, r, _row_tensor(Z, "Z", r, dev, r.stride)[0], f, float(fill), po, so,
+          _vec(kept, "kept", torch.int32, r.R, dev, True), _vec(ws, "ws", torch.uint8, None, dev), ws.numel())
 
 
 def _distill_list(r, t_idx, t_logit, device):
@@ -443,14 +452,10 @@ def dflash_distill(r, S, t_idx, t_logit, loss, lse, ws, tau=1.0, t_lse=None, wei
     (``t_idx``, ``t_logit`` [R, K]; both None: K = 0, ``lse`` alone)."""
     dev = S.device
     K, pi, pt = _distill_list(r, t_idx, t_logit, dev)
-    with torch.cuda.device(dev):
-        _check(lib.dflash_distill(ctypes.byref(r), _row_tensor(S, "S", r, dev, r.stride)[0], K, float(tau), pi, pt,
-                                  _vec(t_lse, "t_lse", torch.float64, r.R, dev, True),
-                                  _vec(weight, "weight", torch.float32, r.R, dev, True),
-                                  _vec(loss, "loss", torch.float32, r.R, dev, True),
-                                  _vec(lse, "lse", torch.float64, r.R, dev),
-                                  _vec(lse_rest, "lse_rest", torch.float64, r.R, dev, True),
-                                  _vec(ws, "ws", torch.uint8, None, dev), ws.numel(), _stream_on(dev, stream)))
+    _call(lib.dflash_distill, dev, stream, r, _row_tensor(S, "S", r, dev, r.stride)[0], K, float(tau), pi, pt,
+          _vec(t_lse, "t_lse", torch.float64, r.R, dev, True), _vec(weight, "weight", torch.float32, r.R, dev, True),
+          _vec(loss, "loss", torch.float32, r.R, dev, True), _vec(lse, "lse", torch.float64, r.R, dev),
+          _vec(lse_rest, "lse_rest", torch.float64, r.R, dev, True), _vec(ws, "ws", torch.uint8, None, dev), ws.numel())
 
 
 def dflash_distill_grad(r, S, t_idx, t_logit, lse, dS, tau=1.0, t_lse=None, weight=None, grad_loss=None, lse_rest=None,
@@ -460,14 +465,10 @@ def dflash_distill_grad(r, S, t_idx, t_logit, lse, dS, tau=1.0, t_lse=None, weig
     dev = S.device
     K, pi, pt = _distill_list(r, t_idx, t_logit, dev)
     pd, sd = _row_tensor(dS, "dS", r, dev)
-    with torch.cuda.device(dev):
-        _check(lib.dflash_distill_grad(ctypes.byref(r), _row_tensor(S, "S", r, dev, r.stride)[0], K, float(tau), pi, pt,
-                                       _vec(t_lse, "t_lse", torch.float64, r.R, dev, True),
-                                       _vec(weight, "weight", torch.float32, r.R, dev, True),
-                                       _vec(grad_loss, "grad_loss", torch.float32, r.R, dev, True),
-                                       _vec(lse, "lse", torch.float64, r.R, dev),
-                                       _vec(lse_rest, "lse_rest", torch.float64, r.R, dev, True), pd, sd,
-                                       _stream_on(dev, stream)))
+    _call(lib.dflash_distill_grad, dev, stream, r, _row_tensor(S, "S", r, dev, r.stride)[0], K, float(tau), pi, pt,
+          _vec(t_lse, "t_lse", torch.float64, r.R, dev, True), _vec(weight, "weight", torch.float32, r.R, dev, True),
+          _vec(grad_loss, "grad_loss", torch.float32, r.R, dev, True), _vec(lse, "lse", torch.float64, r.R, dev),
+          _vec(lse_rest, "lse_rest", torch.float64, r.R, dev, True), pd, sd)
 
 
 def dflash_workspace_init(ws, stream=None):

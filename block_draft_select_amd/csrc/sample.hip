@@ -64,18 +64,13 @@ constexpr uint64_t kOneBits = 0x3FF0000000000000ull;
 constexpr double kLn2Eighth = 0.08664339756999316;  // ln 2 / 8
 
 // 2^(f / 8) for f in [0, 1): Taylor series to degree 8, truncation below
-// 8e-16; exactly 1 at f = 0 and never below 1
+// 8e-16, its upper terms in pairs (a short chain: a row's finish waits for few
+// weights, one after the other); exactly 1 at f = 0 and never below 1
 __device__ __forceinline__ double exp2_eighth(double f) {
-  const double x = f * kLn2Eighth;
-  double p = 1.0 / 40320.0;
-  p = fma(p, x, 1.0 / 5040.0);
-  p = fma(p, x, 1.0 / 720.0);
-  p = fma(p, x, 1.0 / 120.0);
-  p = fma(p, x, 1.0 / 24.0);
-  p = fma(p, x, 1.0 / 6.0);
-  p = fma(p, x, 0.5);
-  p = fma(p, x, 1.0);
-  return fma(p, x, 1.0);
+  const double x = f * kLn2Eighth, x2 = x * x;
+  const double a = fma(x, 1.0 / 6.0, 0.5), b = fma(x, 1.0 / 120.0, 1.0 / 24.0), c = fma(x, 1.0 / 5040.0, 1.0 / 720.0);
+  const double d = fma(x2, fma(x2, fma(x2, 1.0 / 40320.0, c), b), a);
+  return 1.0 + fma(x2, d, x);
 }
 
 // 2^(e / 8), e <= 0 an integer
@@ -179,10 +174,25 @@ struct BlockOps {
     for (int w = 1; w < kWaves; ++w) v = fmax(v, s.d[flip][w]);
     return v;
   }
-  __device__ __forceinline__ uint32_t sum(uint32_t v) {
-    v = wave_sum_u32(v);
+  __device__ __forceinline__ uint32_t max(uint32_t v) {
+    v = ::max(v, dpp_u32<kDppRowShr1>(v, 0u));
+    v = ::max(v, dpp_u32<kDppRowShr2>(v, 0u));
+    v = ::max(v, dpp_u32<kDppRowShr4>(v, 0u));
+    v = ::max(v, dpp_u32<kDppRowShr8>(v, 0u));
+    v = ::max(v, dpp_u32<kDppRowBcast15, 0xA>(v, 0u));
+    v = ::max(v, dpp_u32<kDppRowBcast31, 0xC>(v, 0u));
     flip ^= 1;
-    if ((threadIdx.x & 63) == 0) s.u[flip][threadIdx.x >> 6] = v;
+    if ((threadIdx.x & 63) == 63) s.u[flip][threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = s.u[flip][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v = ::max(v, s.u[flip][w]);
+    return v;
+  }
+  __device__ __forceinline__ uint32_t sum(uint32_t v) {
+    v = wave_scan_u32(v);
+    flip ^= 1;
+    if ((threadIdx.x & 63) == 63) s.u[flip][threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0;
 #pragma unroll
@@ -886,7 +896,7 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, i
 
 // ---------------------------------------------------------------- bf16 rows: counts of values
 // The items of a segment, in the order of the row's tokens: item 0 counts
-// positive values over the range (and NaN), 1 .. kMags the positive values
+// positive values over the range (+inf too), 1 .. kMags the positive values
 // downwards, kMid all that lie nearer to zero, then the negative values, kLow
 // the finite values under the range; masked tokens are not counted.  The range
 // depends on T alone, so that a row's segments agree: kMags magnitudes (23
@@ -908,10 +918,10 @@ __device__ __forceinline__ uint32_t value_base(double c8) {
 __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, int64_t row0, int n_seg, int seg_slots,
                                                                  SampleValues* __restrict__ parts) {
   constexpr int VE = 8, U = 4;
-  // counters: 64 that take the masked tokens (one a lane: equal addresses
-  // would queue up) and are not read, 64 for those under the range, then by
-  // ascending value the items kLow - 1 .. 0
-  constexpr int kUnder = 64, kFirst = 128, kCounters = kFirst + kLow;
+  // counters: for either sign kMags + 2 by magnitude (0: nearer to zero, kMags
+  // + 1: over the range), then one a lane for the tokens under the range
+  // (equal addresses queue up)
+  constexpr int kSide = kMags + 2, kUnder = 2 * kSide, kCounters = kUnder + 64;
   __shared__ uint32_t count[kCounters];
   __shared__ uint32_t n_odd;
   const int tid = threadIdx.x, lane = tid & 63, seg = blockIdx.x % n_seg;
@@ -922,39 +932,42 @@ __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, i
   for (int i = tid; i < kCounters; i += kThreads) count[i] = 0;
   if (tid == 0) n_odd = 0;
   __syncthreads();
-  // ordered 16-bit keys, two a word, to counters without a branch: with r the
-  // key over the lowest counted one's (0 if it is lower), min(r, kMags + 1)
-  // plus what r exceeds the values nearer to zero by
-  const u16x2 lane2 = (u16x2)((unsigned short)lane), to_under2 = (u16x2)((unsigned short)kUnder),
-              to_first2 = (u16x2)((unsigned short)(kFirst - 1 - kUnder - lane));
-  const uint32_t masked2 = 0x007F007Fu, one2 = 0x00010001u, below2 = (0x7FFFu - base - kMags) * 0x10001u,
-                 mid2 = (kMags + 1) * 0x10001u, pos2 = (kMags + 2 * base) * 0x10001u;
+  const uint32_t near2 = (base - 1u) * 0x10001u, over2 = (uint32_t)(kMags + 1) * 0x10001u, side2 = (uint32_t)kSide * 0x10001u;
   auto add = [&](const Slot& x) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const uint32_t o = ord16x2(x.w[d]), r = subsat_u16x2(o, below2);
-      const u16x2 live = __builtin_bit_cast(u16x2, min_u16x2(subsat_u16x2(o, masked2), one2));
-      const u16x2 in = __builtin_bit_cast(u16x2, min_u16x2(r, one2));
-      u16x2 i2 = __builtin_bit_cast(u16x2, min_u16x2(r, mid2)) +
-                 __builtin_bit_cast(u16x2, min_u16x2(subsat_u16x2(r, pos2), mid2)) + (live * to_under2 + (in * to_first2 + lane2));
-      i2 <<= (u16x2)(2);  // byte offsets
-      const uint32_t i = __builtin_bit_cast(uint32_t, i2);
-      atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(count) + (i & 0xFFFFu)), 1u);
-      atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(count) + (i >> 16)), 1u);
+      const uint32_t w = x.w[d];
+      const uint32_t mag = subsat_u16x2(w & 0x7FFF7FFFu, near2), e = min_u16x2(mag, over2);
+      const uint32_t neg = __builtin_bit_cast(uint32_t, __builtin_bit_cast(s16x2, w) >> (s16x2)(15));
+      uint32_t i = __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, e) + __builtin_bit_cast(u16x2, neg & side2));
+      if (subsat_u16x2(mag, over2 - 0x10001u)) {
+        // a token out of the range: masked ones (-inf, NaN) are not counted,
+        // those under the range go to the lane's counter
+        const uint32_t lo = w & 0xFFFFu, hi = w >> 16;
+        const bool ol = (e & 0xFFFFu) > (uint32_t)kMags, oh = (e >> 16) > (uint32_t)kMags;
+        const auto masked = [](uint32_t h) { return h == 0xFF80u || (h & 0x7FFFu) > 0x7F80u; };
+        if (ol && (lo >> 15)) i = (i & 0xFFFF0000u) | (uint32_t)(kUnder + lane);
+        if (oh && (hi >> 15)) i = (i & 0xFFFFu) | (uint32_t)(kUnder + lane) << 16;
+        if (!(ol && masked(lo))) atomicAdd(&count[i & 0xFFFFu], 1u);
+        if (!(oh && masked(hi))) atomicAdd(&count[i >> 16], 1u);
+      } else {
+        atomicAdd(&count[i & 0xFFFFu], 1u);
+        atomicAdd(&count[i >> 16], 1u);
+      }
     }
   };
 #pragma unroll 1
   for (int sl = begin + tid; sl < end; sl += U * kThreads) {
     Slot x[U];
 #pragma unroll
-    for (int l = 0; l < U; ++l) x[l] = z.load<true>(min(sl + l * kThreads, end));
+    for (int l = 0; l < U; ++l) x[l] = z.load(min(sl + l * kThreads, end));
 #pragma unroll
     for (int l = 0; l < U; ++l)
       if (sl + l * kThreads < end) add(x[l]);
   }
   __syncthreads();
   SampleValues& out = parts[blockIdx.x];
-  const uint32_t n_mid = count[kFirst + kLow - 1 - kMid];
+  const uint32_t n_mid = count[0] + count[kSide];
   if (n_mid != 0 && n_mid <= (uint32_t)kSampleOdd) {  // the few tokens near zero: find them again
 #pragma unroll 1
     for (int sl = begin + tid; sl < end; sl += kThreads) {
@@ -966,9 +979,10 @@ __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, i
       }
     }
   }
+  // item 0 and the positive values from the largest down, kMid, the negative ones
+  auto item = [&](int i) { return i < kMid ? count[kMags + 1 - i] : i == kMid ? n_mid : count[kSide + i - kMid]; };
   uint32_t* items = reinterpret_cast<uint32_t*>(out.items);
-  for (int j = tid; j < kLow / 2; j += kThreads)
-    items[j] = count[kFirst + kLow - 1 - 2 * j] | count[kFirst + kLow - 2 - 2 * j] << 16;
+  for (int j = tid; j < kLow / 2; j += kThreads) items[j] = item(2 * j) | item(2 * j + 1) << 16;
   if (tid < 64) {
     const uint32_t under = wave_sum_u32(count[kUnder + tid]);
     if (tid == 0) items[kLow / 2] = under;
@@ -983,7 +997,7 @@ struct ValLds {
   double wcum[kThreads];     // their running weight
   Red red;
   uint32_t n;
-  uint32_t at, idx;
+  uint32_t idx;
 };
 union RowLds {
   ValLds v;
@@ -1005,9 +1019,9 @@ struct Values {
   const RowRef<DFLASH_BF16> z;
   const SampleValues* part;
   const int n_seg, seg_slots, tid;
-  const double c8;
+  const double c;        // log2(e) / T
   const uint32_t base;
-  double tm;             // c8 times the largest logit
+  double tm;             // c times the largest logit
   uint32_t n_mid, n_in;  // tokens near zero, tokens in the range
 
   // the logit of a counted value
@@ -1016,22 +1030,31 @@ struct Values {
     const float v = __uint_as_float((uint32_t)mag << 16);
     return item < kMid ? v : -v;
   }
-  // relative to the row's largest token, whose weight is exactly 1
+  // relative to the row's largest token, whose weight is exactly 1: 2^t by
+  // its nearest integer and the Taylor series of e^(f ln 2), |f| <= 1/2, to
+  // degree 12 (truncation below 2e-16)
   __device__ __forceinline__ double weight(double v) const {
-    const double t = v * c8 - tm, fl = floor(t);
-    return exp2_eighth(t - fl) * pow2_eighth((int)fmax(fl, -16000.0));
+    const double t = fmax(v * c - tm, -1100.0), n = rint(t), x = (t - n) * 0.6931471805599453, x2 = x * x, x4 = x2 * x2;
+    const double p3 = fma(x, 1.0 / 6.0, 0.5), p5 = fma(x, 1.0 / 120.0, 1.0 / 24.0), p7 = fma(x, 1.0 / 5040.0, 1.0 / 720.0),
+                 p9 = fma(x, 1.0 / 362880.0, 1.0 / 40320.0), p11 = fma(x, 1.0 / 39916800.0, 1.0 / 3628800.0);
+    const double hi = fma(x4, fma(x2, 1.0 / 479001600.0, p11), fma(x2, p9, p7)), lo = fma(x2, p5, p3);
+    return ldexp(1.0 + fma(x2, fma(x4, hi, lo), x), (int)n);
   }
   __device__ __forceinline__ double near_value(uint32_t i) const { return key_value(comp_key(s.win[i])); }
 
+  __device__ __forceinline__ uint32_t tokens(int g) const {
+    const int item = g * 64 + lane_id();
+    return item >= 1 && item < kLow ? s.c[item] : 0u;
+  }
   // group g on a wave: this lane's item, its tokens, the weight of one of
   // them (of all for kMid) and the running count and sum inside the group
-  __device__ __forceinline__ void group(int g, uint32_t& c, double& w, uint32_t& upto, double& cum) const {
+  __device__ __forceinline__ void group(int g, uint32_t& n, double& w, uint32_t& upto, double& cum) const {
     const int item = g * 64 + lane_id();
-    c = item >= 1 && item < kLow ? s.c[item] : 0u;
-    w = c && item != kMid ? weight((double)value(item)) : 0.0;
-    double all = (double)c * w;
-    if (item == kMid && c) all = w = s.wcum[n_mid - 1];
-    upto = wave_scan_u32(c);
+    n = tokens(g);
+    w = n && item != kMid ? weight((double)value(item)) : 0.0;
+    double all = (double)n * w;
+    if (item == kMid && n) all = w = s.wcum[n_mid - 1];
+    upto = wave_scan_u32(n);
     cum = wave_scan_f64(all);
   }
 
@@ -1120,34 +1143,32 @@ struct Values {
     __syncthreads();
     r -= s.n;
     const uint32_t want = __float_as_uint(value(item)) >> 16;
-    // its thread's piece of the segment (at most 16 slots)
-    const int begin = g * seg_slots, end = min(begin + seg_slots, z.slots()), per = (seg_slots + kThreads - 1) / kThreads;
-    const int sb = min(begin + tid * per, end), se = min(sb + per, end);
-    uint32_t found = 0;
+    // the segment in order, four slots a thread at a time, up to the r-th
+    const int end = min((g + 1) * seg_slots, z.slots());
 #pragma unroll 1
-    for (int sl = sb; sl < se; sl += 4) {
+    for (int s0 = g * seg_slots; s0 < end; s0 += 4 * kThreads) {
+      const int sl = s0 + 4 * tid;
+      uint32_t mask = 0;
       Slot x[4];
 #pragma unroll
-      for (int l = 0; l < 4; ++l) x[l] = z.load(min(sl + l, z.slots()));
+      for (int l = 0; l < 4; ++l) x[l] = z.load(min(sl + l, end));
 #pragma unroll
       for (int l = 0; l < 4; ++l)
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          if (sl + l < se) found += (uint32_t)((x[l].w[d] & 0xFFFFu) == want) + (uint32_t)(x[l].w[d] >> 16 == want);
+          mask |= ((uint32_t)((x[l].w[d] & 0xFFFFu) == want) | (uint32_t)(x[l].w[d] >> 16 == want) << 1) << (8 * l + 2 * d);
+      if (sl + 4 > end) mask &= sl < end ? (1u << 8 * (end - sl)) - 1u : 0u;
+      const uint32_t found = (uint32_t)__popc(mask), upto = ops.scan(found);
+      const int t = ops.first(upto >= r);
+      if (t < kThreads) {
+        if (tid == t) {
+          for (uint32_t left = r - (upto - found); left > 1; --left) mask &= mask - 1u;
+          s.idx = (uint32_t)(sl * 8 + __builtin_ctz(mask));
+        }
+        break;
+      }
+      r -= ops.sum(found);
     }
-    const uint32_t upto = ops.scan(found);
-    const int t = min(ops.first(upto >= r), kThreads - 1);
-    if (tid == t) {
-      s.n = upto - found;
-      s.at = (uint32_t)sb;
-    }
-    __syncthreads();
-    // its place in the piece, an element a thread
-    r -= s.n;
-    const int e = (int)s.at * 8 + tid;
-    const bool here = tid < per * 8 && e < z.V && z.p[min(e, z.V - 1)] == (uint16_t)want;
-    const uint32_t rank = ops.scan((uint32_t)here);
-    if (here && rank == r) s.idx = (uint32_t)e;
     __syncthreads();
     return s.idx;
   }
@@ -1166,7 +1187,7 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
   uint32_t c0[kMine], c1[kMine];
 #pragma unroll
   for (int j = 0; j < kMine; ++j) c0[j] = c1[j] = 0;
-#pragma unroll 2
+#pragma unroll 4
   for (int g = 0; g < n_seg; ++g) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(part[g].items);
 #pragma unroll
@@ -1177,9 +1198,12 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
       c1[j] += v >> 16;
     }
   }
+  int top = kItems;  // the first item with a token: the row's largest
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) {
+  for (int j = kMine - 1; j >= 0; --j) {
     const int i = tid + j * kThreads;
+    if (c1[j] && 2 * i + 1 < kLow) top = 2 * i + 1;
+    if (c0[j] && i > 0 && 2 * i < kLow) top = 2 * i;
     if (i < kPairs) {
       s.c[2 * i] = c0[j];
       s.c[2 * i + 1] = 2 * i + 1 < kItems ? c1[j] : 0u;
@@ -1217,19 +1241,8 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
     if (in) s.win[rank] = me;
     __syncthreads();
   }
-  Values f{s, ops, RowRef<DFLASH_BF16>(a.Z, row, a.stride, a.V), part, n_seg, seg_slots, tid, c8, base, 0.0, n_mid, 0};
-  // the largest token: the first item with any
-  int top = kItems;
-#pragma unroll 1
-  for (int g = wave; g < kGroups; g += kWaves) {
-    const int item = g * 64 + lane;
-    const int l = first_lane(item >= 1 && item < kLow && s.c[item] != 0);
-    if (l < 64) {
-      top = g * 64 + l;
-      break;
-    }
-  }
-  top = kItems - (int)ops.max((double)(kItems - top));
+  Values f{s, ops, RowRef<DFLASH_BF16>(a.Z, row, a.stride, a.V), part, n_seg, seg_slots, tid, c8 * 0.125, base, 0.0, n_mid, 0};
+  top = kItems - (int)ops.max((uint32_t)(kItems - top));
   if (top >= kItems) {
     if (n_low) return false;
     empty_row(row, o, cut_out);
@@ -1237,22 +1250,29 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
   }
   const double m = top == kMid ? f.near_value(0) : (double)f.value(top);
   if (n_low && m - 512.0 / c8 < -(double)__uint_as_float(min((base + (uint32_t)kMags) << 16, 0x7F7F0000u))) return false;
-  f.tm = m * c8;
+  f.tm = m * f.c;
   if (n_mid) {
     const double sc = ops.scan(tid < (int)n_mid ? f.weight(f.near_value(tid)) : 0.0);
     if (tid < (int)n_mid) s.wcum[tid] = sc;
     __syncthreads();
   }
-  // each group's tokens and weight, then before each group
+  // each group's tokens and weight, two groups at a time, then before each group
 #pragma unroll 1
-  for (int g = wave; g < kGroups; g += kWaves) {
-    const int item = g * 64 + lane;
-    uint32_t c = 0, upto = 0;
-    double w, cum = 0.0;
-    if (__ballot(item >= 1 && item < kLow && s.c[item] != 0)) f.group(g, c, w, upto, cum);
+  for (int g = wave; g < kGroups; g += 2 * kWaves) {
+    const int g1 = g + kWaves;  // past the last group: no items
+    uint32_t c, upto[2] = {0, 0};
+    double w, cum[2] = {0.0, 0.0};
+    if (__ballot(f.tokens(g) != 0 || f.tokens(g1) != 0)) {
+      f.group(g, c, w, upto[0], cum[0]);
+      f.group(g1, c, w, upto[1], cum[1]);
+    }
     if (lane == 63) {
-      s.gc[g + 1] = upto;
-      s.gm[g + 1] = cum;
+      s.gc[g + 1] = upto[0];
+      s.gm[g + 1] = cum[0];
+      if (g1 < kGroups) {
+        s.gc[g1 + 1] = upto[1];
+        s.gm[g1 + 1] = cum[1];
+      }
     }
   }
   __syncthreads();
