@@ -34,22 +34,40 @@ constexpr int kMaskWords = kThreads * 8 * 8 / 32;  // one bit per element of a s
 constexpr double kLog2e64 = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
 
-// 2^x for x <= 0.5: the integer part by ldexp, the rest (|f| <= 1/2) by the
-// Taylor series of e^(f ln 2) to degree 9 (truncation below 7e-12)
-__device__ __forceinline__ double exp2_sum(double x) {
-  x = fmax(x, -1100.0);
-  const double n = rint(x), f = (x - n) * kLn2;
-  double p = 1.0 / 362880.0;
-  p = fma(p, f, 1.0 / 40320.0);
-  p = fma(p, f, 1.0 / 5040.0);
-  p = fma(p, f, 1.0 / 720.0);
-  p = fma(p, f, 1.0 / 120.0);
-  p = fma(p, f, 1.0 / 24.0);
-  p = fma(p, f, 1.0 / 6.0);
-  p = fma(p, f, 0.5);
-  p = fma(p, f, 1.0);
-  p = fma(p, f, 1.0);
-  return ldexp(p, (int)n);
+// The forward pass sums 2^t, t = (x - m) log2 e, in fp64 for every logit, so its
+// time is that of the fp64 instructions a term takes.  With n = floor(32 t)
+// and g the rest, 2^t = 2^(n >> 5) 2^((n & 31 + 1/2) / 32) e^((g - 1/2) ln 2 / 32):
+// the middle factor from a table in LDS (32 entries cover the 64 banks once,
+// so no read conflicts), the last by a polynomial in g of degree 4 (the Taylor
+// series about 1/2, |.| <= 0.0109: truncation below 1.3e-12), the first added
+// to the table entry's exponent.  32 t is shifted by kShift so that truncation
+// is the floor and everything below 2^-960 (and -inf) ends at the range's foot.
+constexpr int kTab = 32;
+constexpr double kShift = 32.0 * 960.0;
+
+// c, k in p(g) = sum k_i g^i = e^((g - 1/2) L) to degree 4, L = ln 2 / 32
+constexpr double kL = 0.021660849392498290;
+constexpr double kU = -0.5 * kL;  // the expansion's value at g = 0
+constexpr double kP4 = kL * kL * kL * kL / 24.0;
+constexpr double kP3 = kL * kL * kL * (1.0 / 6.0 + kU / 6.0);
+constexpr double kP2 = kL * kL * (0.5 + kU * (0.5 + kU * 0.25));
+constexpr double kP1 = kL * (1.0 + kU * (1.0 + kU * (0.5 + kU / 6.0)));
+constexpr double kP0 = 1.0 + kU * (1.0 + kU * (0.5 + kU * (1.0 / 6.0 + kU / 24.0)));
+
+// entry k of the table: 2^((k + 1/2) / 32 - 960)
+__device__ __forceinline__ double table_entry(int k) { return exp2(((double)k + 0.5) / 32.0 - 960.0); }
+
+// adds 2^(ts / 32 - 960) to the sum (ts = 32 t + kShift)
+__device__ __forceinline__ double add_term(double sum, double ts, const double* tab) {
+  ts = fmax(ts, 0.0);
+  const uint32_t n = (uint32_t)ts;
+  const double g = __builtin_amdgcn_fract(ts);
+  const uint64_t e = __double_as_longlong(tab[n & 31u]) + ((uint64_t)(n & ~31u) << 47);
+  double p = fma(g, kP4, kP3);
+  p = fma(p, g, kP2);
+  p = fma(p, g, kP1);
+  p = fma(p, g, kP0);
+  return fma(__longlong_as_double(e), p, sum);
 }
 
 struct Red {
@@ -112,6 +130,7 @@ template <int DT, int NL, bool REST>
 __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, int n_seg, DistillPart* __restrict__ parts) {
   constexpr int VE = RowType<DT>::VE;
   __shared__ Red red;
+  __shared__ double tab[kTab];
   __shared__ uint32_t mask[REST ? kMaskWords : 1];
   const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
   const int64_t row = blockIdx.x / n_seg;
@@ -121,6 +140,7 @@ __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, in
   Slot x[NL];
 #pragma unroll
   for (int l = 0; l < NL; ++l) x[l] = z.template load<true>(s0 + l * kThreads + tid);
+  if (tid < kTab) tab[tid] = table_entry(tid);
   if constexpr (REST) {
     for (int i = tid; i < kMaskWords; i += kThreads) mask[i] = 0;
     __syncthreads();
@@ -146,22 +166,47 @@ __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, in
       }
     }
   }
+  // the largest logit; whether one is NaN or +inf (then the sum is NaN)
   float m = kNegInf;
+  bool odd = false;
+  if constexpr (DT == DFLASH_BF16) {
+    // signed and unsigned maxima of the raw patterns, two a word: the signed one
+    // is the largest logit unless all are negative (then the unsigned minimum
+    // is), and a NaN of either sign stands over its infinity
+    uint32_t hi = 0x80008000u, up = 0, lo = 0xFFFFFFFFu;
 #pragma unroll
-  for (int l = 0; l < NL; ++l)
+    for (int l = 0; l < NL; ++l)
 #pragma unroll
-    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[l], i));
+      for (int d = 0; d < 4; ++d) {
+        hi = smax_i16x2(hi, x[l].w[d]);
+        up = max_u16x2(up, x[l].w[d]);
+        lo = min_u16x2(lo, x[l].w[d]);
+      }
+    const int h = max((int)(int16_t)(hi & 0xFFFFu), (int)(int16_t)(hi >> 16));
+    odd = h >= 0x7F80 || max(up & 0xFFFFu, up >> 16) > 0xFF80u;
+    m = __uint_as_float((h >= 0 ? (uint32_t)h : min(lo & 0xFFFFu, lo >> 16)) << 16);
+  } else {
+#pragma unroll
+    for (int l = 0; l < NL; ++l)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float v = slot_value<DT>(x[l], i);
+        m = fmaxf(m, v);
+        odd |= !(v < INFINITY);
+      }
+  }
   const double c = kLog2e64 / a.tau;
-  const double M = rint(block_max(red, (double)m) * c);  // -inf: nothing here; +inf ends in NaN below
+  const double M = rint(block_max(red, odd ? INFINITY : (double)m) * c);  // -inf: nothing here
   double s = 0.0;
+  if (M == INFINITY) {
+    s = NAN;
+  } else if (M > -INFINITY) {
+    const double c32 = 32.0 * c, off = kShift - 32.0 * M;
 #pragma unroll
-  for (int l = 0; l < NL; ++l)
+    for (int l = 0; l < NL; ++l)
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float v = slot_value<DT>(x[l], i);
-      // -inf adds nothing; NaN and +inf make the sum NaN
-      if (v != kNegInf) s += v < INFINITY ? exp2_sum(fma((double)v, c, -M)) : (double)NAN;
-    }
+      for (int i = 0; i < VE; ++i) s = add_term(s, fma((double)slot_value<DT>(x[l], i), c32, off), tab);
+  }
   s = block_sum(red, s);
   if (tid == 0) parts[blockIdx.x] = DistillPart{M, s};
 }

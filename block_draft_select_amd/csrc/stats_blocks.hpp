@@ -31,11 +31,6 @@ namespace dfk {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ uint32_t smax_i16x2(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(s16x2, a),
-                                                                __builtin_bit_cast(s16x2, b)));
-}
-
 // One chunk of a target row in a wave's registers: 64 raw values per lane
 // (bf16 pairs or fp32 words), lane l holding 16-byte unit j * 64 + l.
 template <int DT>
