@@ -35,39 +35,37 @@ constexpr double kLog2e64 = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
 
 // The forward pass sums 2^t, t = (x - m) log2 e, in fp64 for every logit, so its
-// time is that of the fp64 instructions a term takes.  With n = floor(32 t)
-// and g the rest, 2^t = 2^(n >> 5) 2^((n & 31 + 1/2) / 32) e^((g - 1/2) ln 2 / 32):
-// the middle factor from a table in LDS (32 entries cover the 64 banks once,
-// so no read conflicts), the last by a polynomial in g of degree 4 (the Taylor
-// series about 1/2, |.| <= 0.0109: truncation below 1.3e-12), the first added
-// to the table entry's exponent.  32 t is shifted by kShift so that truncation
-// is the floor and everything below 2^-960 (and -inf) ends at the range's foot.
-constexpr int kTab = 32;
-constexpr double kShift = 32.0 * 960.0;
+// time is that of the instructions a term takes.  With n = floor(64 t) and g
+// the rest, 2^t = 2^(n >> 6) 2^((n & 63 + 1/2) / 64) e^v, v = (g - 1/2) ln 2 / 64:
+// the middle factor comes from a table in LDS, the last from a polynomial of
+// degree 3 (the Taylor series with its fourth term spread over the lower ones,
+// v^4 ~ h^2 v^2 - h^4 / 8 on |v| <= h = 0.00542: within 5e-12), the first is
+// added to the table entry's exponent.  64 t is shifted by kShift so that
+// truncation is the floor and everything below 2^-960 (and -inf) ends at the
+// range's foot.
+constexpr int kTab = 64;
+constexpr double kShift = 64.0 * 960.0;
 
-// c, k in p(g) = sum k_i g^i = e^((g - 1/2) L) to degree 4, L = ln 2 / 32
-constexpr double kL = 0.021660849392498290;
-constexpr double kU = -0.5 * kL;  // the expansion's value at g = 0
-constexpr double kP4 = kL * kL * kL * kL / 24.0;
-constexpr double kP3 = kL * kL * kL * (1.0 / 6.0 + kU / 6.0);
-constexpr double kP2 = kL * kL * (0.5 + kU * (0.5 + kU * 0.25));
-constexpr double kP1 = kL * (1.0 + kU * (1.0 + kU * (0.5 + kU / 6.0)));
-constexpr double kP0 = 1.0 + kU * (1.0 + kU * (0.5 + kU * (1.0 / 6.0 + kU / 24.0)));
+// k0 + k1 g + k2 g^2 + k3 g^3 = e^v as above
+constexpr double kL = 0.010830424696249145;  // ln 2 / 64
+constexpr double kU = -0.5 * kL;             // v at g = 0
+constexpr double kA0 = 1.0 - kU * kU * kU * kU / 192.0, kA2 = 0.5 + kU * kU / 24.0, kA3 = 1.0 / 6.0;
+constexpr double kP3 = kA3 * kL * kL * kL;
+constexpr double kP2 = kL * kL * (kA2 + 3.0 * kA3 * kU);
+constexpr double kP1 = kL * (1.0 + 2.0 * kA2 * kU + 3.0 * kA3 * kU * kU);
+constexpr double kP0 = kA0 + kU + kA2 * kU * kU + kA3 * kU * kU * kU;
 
-// entry k of the table: 2^((k + 1/2) / 32 - 960)
-__device__ __forceinline__ double table_entry(int k) { return exp2(((double)k + 0.5) / 32.0 - 960.0); }
+// entry k of the table: 2^((k + 1/2) / 64 - 960)
+__device__ __forceinline__ double table_entry(int k) { return exp2(((double)k + 0.5) / 64.0 - 960.0); }
 
-// adds 2^(ts / 32 - 960) to the sum (ts = 32 t + kShift)
+// adds 2^(ts / 64 - 960) to the sum (ts = 64 t + kShift)
 __device__ __forceinline__ double add_term(double sum, double ts, const double* tab) {
   ts = fmax(ts, 0.0);
   const uint32_t n = (uint32_t)ts;
   const double g = __builtin_amdgcn_fract(ts);
-  const uint64_t e = __double_as_longlong(tab[n & 31u]) + ((uint64_t)(n & ~31u) << 47);
-  double p = fma(g, kP4, kP3);
-  p = fma(p, g, kP2);
-  p = fma(p, g, kP1);
-  p = fma(p, g, kP0);
-  return fma(__longlong_as_double(e), p, sum);
+  const double e = tab[n & 63u];
+  const double f = __hiloint2double(__double2hiint(e) + (int)((n & ~63u) << 14), __double2loint(e));
+  return fma(f, fma(fma(fma(g, kP3, kP2), g, kP1), g, kP0), sum);
 }
 
 struct Red {
@@ -173,18 +171,26 @@ __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, in
     // signed and unsigned maxima of the raw patterns, two a word: the signed one
     // is the largest logit unless all are negative (then the unsigned minimum
     // is), and a NaN of either sign stands over its infinity
-    uint32_t hi = 0x80008000u, up = 0, lo = 0xFFFFFFFFu;
+    uint32_t hi = 0x80008000u, up = 0;
 #pragma unroll
     for (int l = 0; l < NL; ++l)
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         hi = smax_i16x2(hi, x[l].w[d]);
         up = max_u16x2(up, x[l].w[d]);
-        lo = min_u16x2(lo, x[l].w[d]);
       }
     const int h = max((int)(int16_t)(hi & 0xFFFFu), (int)(int16_t)(hi >> 16));
     odd = h >= 0x7F80 || max(up & 0xFFFFu, up >> 16) > 0xFF80u;
-    m = __uint_as_float((h >= 0 ? (uint32_t)h : min(lo & 0xFFFFu, lo >> 16)) << 16);
+    uint32_t best = (uint32_t)h;
+    if (h < 0) {
+      uint32_t lo = 0xFFFFFFFFu;
+#pragma unroll
+      for (int l = 0; l < NL; ++l)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) lo = min_u16x2(lo, x[l].w[d]);
+      best = min(lo & 0xFFFFu, lo >> 16);
+    }
+    m = __uint_as_float(best << 16);
   } else {
 #pragma unroll
     for (int l = 0; l < NL; ++l)
@@ -201,11 +207,11 @@ __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, in
   if (M == INFINITY) {
     s = NAN;
   } else if (M > -INFINITY) {
-    const double c32 = 32.0 * c, off = kShift - 32.0 * M;
+    const double c64 = 64.0 * c, off = kShift - 64.0 * M;
 #pragma unroll
     for (int l = 0; l < NL; ++l)
 #pragma unroll
-      for (int i = 0; i < VE; ++i) s = add_term(s, fma((double)slot_value<DT>(x[l], i), c32, off), tab);
+      for (int i = 0; i < VE; ++i) s = add_term(s, fma((double)slot_value<DT>(x[l], i), c64, off), tab);
   }
   s = block_sum(red, s);
   if (tid == 0) parts[blockIdx.x] = DistillPart{M, s};
