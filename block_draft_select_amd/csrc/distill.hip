@@ -30,42 +30,61 @@ namespace {
 
 constexpr int kThreads = kDistillThreads;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kMaskWords = kThreads * 8 * 8 / 32;  // one bit per element of a segment
 constexpr double kLog2e64 = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
 
 // The forward pass sums 2^t, t = (x - m) log2 e, in fp64 for every logit, so its
-// time is that of the instructions a term takes.  With n = floor(64 t) and g
-// the rest, 2^t = 2^(n >> 6) 2^((n & 63 + 1/2) / 64) e^v, v = (g - 1/2) ln 2 / 64:
-// the middle factor comes from a table in LDS, the last from a polynomial of
-// degree 3 (the Taylor series with its fourth term spread over the lower ones,
-// v^4 ~ h^2 v^2 - h^4 / 8 on |v| <= h = 0.00542: within 5e-12), the first is
-// added to the table entry's exponent.  64 t is shifted by kShift so that
-// truncation is the floor and everything below 2^-960 (and -inf) ends at the
-// range's foot.
-constexpr int kTab = 64;
-constexpr double kShift = 64.0 * 960.0;
+// time is that of the instructions a term takes (16; fp64 and fp32 issue
+// alike here).  With n = floor(512 t) and g the rest,
+// 2^t = 2^(n >> 9) 2^((n & 511 + 1/2) / 512) e^v, v = (g - 1/2) ln 2 / 512: the middle
+// factor comes from a table in LDS, the last from a parabola (the Taylor
+// series with its third term spread over the first, v^3 ~ 3/4 h^2 v on
+// |v| <= h = 6.8e-4: within 1.3e-11), the first is added to the table entry's
+// exponent.  512 t is shifted by kShift so that truncation is the floor and
+// everything below 2^-960 (and -inf) ends at the range's foot.  Measured on
+// 2048 x 151936 against 64 entries and degree 3: 148 us to 160.
+constexpr int kTabBits = 9, kTab = 1 << kTabBits;
+constexpr double kShift = (double)kTab * 960.0;
 
-// k0 + k1 g + k2 g^2 + k3 g^3 = e^v as above
-constexpr double kL = 0.010830424696249145;  // ln 2 / 64
-constexpr double kU = -0.5 * kL;             // v at g = 0
-constexpr double kA0 = 1.0 - kU * kU * kU * kU / 192.0, kA2 = 0.5 + kU * kU / 24.0, kA3 = 1.0 / 6.0;
-constexpr double kP3 = kA3 * kL * kL * kL;
-constexpr double kP2 = kL * kL * (kA2 + 3.0 * kA3 * kU);
-constexpr double kP1 = kL * (1.0 + 2.0 * kA2 * kU + 3.0 * kA3 * kU * kU);
-constexpr double kP0 = kA0 + kU + kA2 * kU * kU + kA3 * kU * kU * kU;
+// k0 + k1 g + k2 g^2 = e^v as above
+constexpr double kL = 0.6931471805599453 / kTab;
+constexpr double kU = -0.5 * kL;  // v at g = 0
+constexpr double kA1 = 1.0 + kU * kU / 8.0;
+constexpr double kP2 = 0.5 * kL * kL;
+constexpr double kP1 = kL * (kA1 + kU);
+constexpr double kP0 = 1.0 + kA1 * kU + 0.5 * kU * kU;
 
-// entry k of the table: 2^((k + 1/2) / 64 - 960)
-__device__ __forceinline__ double table_entry(int k) { return exp2(((double)k + 0.5) / 64.0 - 960.0); }
+// entry k of the table: 2^((k + 1/2) / 512 - 960), by the Taylor series of e^x, |x| <= 0.3466, to degree 13
+__device__ __forceinline__ double table_entry(int k) {
+  const double x = ((double)k + 0.5 - 0.5 * kTab) * kL;
+  double p = 1.0 / 6227020800.0;
+  p = fma(p, x, 1.0 / 479001600.0);
+  p = fma(p, x, 1.0 / 39916800.0);
+  p = fma(p, x, 1.0 / 3628800.0);
+  p = fma(p, x, 1.0 / 362880.0);
+  p = fma(p, x, 1.0 / 40320.0);
+  p = fma(p, x, 1.0 / 5040.0);
+  p = fma(p, x, 1.0 / 720.0);
+  p = fma(p, x, 1.0 / 120.0);
+  p = fma(p, x, 1.0 / 24.0);
+  p = fma(p, x, 1.0 / 6.0);
+  p = fma(p, x, 0.5);
+  p = fma(p, x, 1.0);
+  p = fma(p, x, 1.0);
+  return ldexp(p * 1.4142135623730951, -960);
+}
 
-// adds 2^(ts / 64 - 960) to the sum (ts = 64 t + kShift)
-__device__ __forceinline__ double add_term(double sum, double ts, const double* tab) {
+// adds 2^(ts / 512 - 960) to the sum (ts = 512 t + kShift).  exp_unit is 2^20, an
+// exponent's last bit in the upper word; it is a kernel argument because the
+// compiler turns the product with a constant back into a shift, a mask and an
+// addition (one instruction of 17 more, 8 per cent)
+__device__ __forceinline__ double add_term(double sum, double ts, const double* tab, uint32_t exp_unit) {
   ts = fmax(ts, 0.0);
   const uint32_t n = (uint32_t)ts;
   const double g = __builtin_amdgcn_fract(ts);
-  const double e = tab[n & 63u];
-  const double f = __hiloint2double(__double2hiint(e) + (int)((n & ~63u) << 14), __double2loint(e));
-  return fma(f, fma(fma(fma(g, kP3, kP2), g, kP1), g, kP0), sum);
+  const double e = tab[n & (uint32_t)(kTab - 1)];
+  const double f = __hiloint2double((int)(__umul24(n >> kTabBits, exp_unit) + (uint32_t)__double2hiint(e)), __double2loint(e));
+  return fma(f, fma(fma(g, kP2, kP1), g, kP0), sum);
 }
 
 struct Red {
@@ -124,56 +143,18 @@ __device__ __forceinline__ double teacher_lse(Red& red, const DistillArgs& a, in
 
 // ---------------------------------------------------------------- forward
 
-template <int DT, int NL, bool REST>
-__global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, int n_seg, DistillPart* __restrict__ parts) {
-  constexpr int VE = RowType<DT>::VE;
-  __shared__ Red red;
-  __shared__ double tab[kTab];
-  __shared__ uint32_t mask[REST ? kMaskWords : 1];
-  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
-  const int64_t row = blockIdx.x / n_seg;
-  if (a.weight && a.weight[row] == 0.0f) return;
-  const RowRef<DT> z(a.S, row, a.stride, a.V);
-  const int s0 = seg * (kThreads * NL);
-  Slot x[NL];
-#pragma unroll
-  for (int l = 0; l < NL; ++l) x[l] = z.template load<true>(s0 + l * kThreads + tid);
-  if (tid < kTab) tab[tid] = table_entry(tid);
-  if constexpr (REST) {
-    for (int i = tid; i < kMaskWords; i += kThreads) mask[i] = 0;
-    __syncthreads();
-    const int e0 = s0 * VE;
-    int idx;
-    for (int k = tid; k < a.K; k += kThreads)
-      if (listed(a, row, k, idx) && idx >= e0 && idx < e0 + kThreads * NL * VE)
-        atomicOr(&mask[(idx - e0) >> 5], 1u << ((idx - e0) & 31));
-    __syncthreads();
-#pragma unroll
-    for (int l = 0; l < NL; ++l) {  // listed tokens leave the sums
-      const int bit = (l * kThreads + tid) * VE;
-      const uint32_t mk = (mask[bit >> 5] >> (bit & 31)) & ((1u << VE) - 1u);
-      if (mk) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if ((mk >> i) & 1u) {
-            if constexpr (DT == DFLASH_BF16)
-              x[l].w[i >> 1] = (i & 1) ? (x[l].w[i >> 1] & 0x0000FFFFu) | 0xFF800000u : (x[l].w[i >> 1] & 0xFFFF0000u) | 0x0000FF80u;
-            else
-              x[l].w[i] = 0xFF800000u;
-          }
-      }
-    }
-  }
-  // the largest logit; whether one is NaN or +inf (then the sum is NaN)
+// a thread's largest logit; whether one is NaN or +inf
+template <int DT, int N>
+__device__ __forceinline__ float largest(const Slot (&x)[N], bool& odd) {
   float m = kNegInf;
-  bool odd = false;
+  odd = false;
   if constexpr (DT == DFLASH_BF16) {
     // signed and unsigned maxima of the raw patterns, two a word: the signed one
     // is the largest logit unless all are negative (then the unsigned minimum
     // is), and a NaN of either sign stands over its infinity
     uint32_t hi = 0x80008000u, up = 0;
 #pragma unroll
-    for (int l = 0; l < NL; ++l)
+    for (int l = 0; l < N; ++l)
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         hi = smax_i16x2(hi, x[l].w[d]);
@@ -185,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, in
     if (h < 0) {
       uint32_t lo = 0xFFFFFFFFu;
 #pragma unroll
-      for (int l = 0; l < NL; ++l)
+      for (int l = 0; l < N; ++l)
 #pragma unroll
         for (int d = 0; d < 4; ++d) lo = min_u16x2(lo, x[l].w[d]);
       best = min(lo & 0xFFFFu, lo >> 16);
@@ -193,28 +174,103 @@ __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, in
     m = __uint_as_float(best << 16);
   } else {
 #pragma unroll
-    for (int l = 0; l < NL; ++l)
+    for (int l = 0; l < N; ++l)
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
+      for (int i = 0; i < RowType<DT>::VE; ++i) {
         const float v = slot_value<DT>(x[l], i);
         m = fmaxf(m, v);
         odd |= !(v < INFINITY);
       }
   }
-  const double c = kLog2e64 / a.tau;
-  const double M = rint(block_max(red, odd ? INFINITY : (double)m) * c);  // -inf: nothing here
-  double s = 0.0;
-  if (M == INFINITY) {
-    s = NAN;
-  } else if (M > -INFINITY) {
-    const double c64 = 64.0 * c, off = kShift - 64.0 * M;
-#pragma unroll
-    for (int l = 0; l < NL; ++l)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) s = add_term(s, fma((double)slot_value<DT>(x[l], i), c64, off), tab);
+  return m;
+}
+
+// A block sums a row segment of `units` times kDistillUnit slots; each of its
+// waves on its own, four slots a lane at a time, relative to the largest logit
+// so far (rounded to a power of two, so that a new one only moves exponents).
+template <int DT, bool REST>
+__global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, int n_seg, int units, uint32_t exp_unit,
+                                                               DistillPart* __restrict__ parts) {
+  constexpr int VE = RowType<DT>::VE, U = kDistillUnit / kThreads;
+  __shared__ double tab[kTab];
+  __shared__ double wave_m[kWaves], wave_s[kWaves];
+  __shared__ uint32_t mask[REST ? kDistillMaxUnits * kDistillUnit * VE / 32 : 1];
+  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
+  const int64_t row = blockIdx.x / n_seg;
+  if (a.weight && a.weight[row] == 0.0f) return;
+  const RowRef<DT> z(a.S, row, a.stride, a.V);
+  const int s0 = seg * units * kDistillUnit, s1 = min(s0 + units * kDistillUnit, z.slots());
+  for (int i = tid; i < kTab; i += kThreads) tab[i] = table_entry(i);
+  if constexpr (REST) {
+    for (int i = tid; i < units * kDistillUnit * VE / 32; i += kThreads) mask[i] = 0;
+    __syncthreads();
+    const int e0 = s0 * VE, e1 = s1 * VE;
+    int idx;
+    for (int k = tid; k < a.K; k += kThreads)
+      if (listed(a, row, k, idx) && idx >= e0 && idx < e1) atomicOr(&mask[(idx - e0) >> 5], 1u << ((idx - e0) & 31));
   }
-  s = block_sum(red, s);
-  if (tid == 0) parts[blockIdx.x] = DistillPart{M, s};
+  __syncthreads();
+  const double c = kLog2e64 / a.tau;
+  double M = -INFINITY, s = 0.0;
+  bool any_odd = false;
+#pragma unroll 1
+  for (int u0 = s0; u0 < s1; u0 += kDistillUnit) {
+    Slot x[U];
+#pragma unroll
+    for (int l = 0; l < U; ++l) x[l] = z.template load<true>(min(u0 + l * kThreads + tid, z.slots()));
+    if constexpr (REST) {
+#pragma unroll
+      for (int l = 0; l < U; ++l) {  // listed tokens leave the sums
+        const int bit = (u0 - s0 + l * kThreads + tid) * VE;
+        const uint32_t mk = (mask[bit >> 5] >> (bit & 31)) & ((1u << VE) - 1u);
+        if (mk) {
+#pragma unroll
+          for (int i = 0; i < VE; ++i)
+            if ((mk >> i) & 1u) {
+              if constexpr (DT == DFLASH_BF16)
+                x[l].w[i >> 1] = (i & 1) ? (x[l].w[i >> 1] & 0x0000FFFFu) | 0xFF800000u : (x[l].w[i >> 1] & 0xFFFF0000u) | 0x0000FF80u;
+              else
+                x[l].w[i] = 0xFF800000u;
+            }
+        }
+      }
+    }
+    bool odd;
+    const float m = wave_max_dpp_f32(largest<DT>(x, odd));
+    any_odd |= __ballot(odd) != 0;
+    const double Mu = rint((double)m * c);
+    if (Mu > M && Mu < INFINITY) {
+      s = M > -INFINITY ? ldexp(s, (int)fmax(M - Mu, -4000.0)) : 0.0;
+      M = Mu;
+    }
+    if (M > -INFINITY) {
+      const double ct = (double)kTab * c, off = kShift - (double)kTab * M;
+#pragma unroll
+      for (int l = 0; l < U; ++l)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) s = add_term(s, fma((double)slot_value<DT>(x[l], i), ct, off), tab, exp_unit);
+    }
+  }
+  s = wave_sum_dpp_f64(s);
+  if ((tid & 63) == 0) {
+    wave_m[tid >> 6] = any_odd ? INFINITY : M;
+    wave_s[tid >> 6] = s;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    double BM = wave_m[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) BM = fmax(BM, wave_m[w]);
+    double sum = 0.0;
+    if (BM == INFINITY) {
+      sum = NAN;
+    } else {
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        if (wave_m[w] > -INFINITY) sum += ldexp(wave_s[w], (int)fmax(wave_m[w] - BM, -4000.0));
+    }
+    parts[blockIdx.x] = DistillPart{BM, sum};
+  }
 }
 
 // log-sum-exp (natural) of terms s * 2^m
@@ -415,16 +471,16 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   }
 }
 
-template <int DT, int NL>
+template <int DT>
 hipError_t run_forward(const DistillArgs& a, float* loss, double* lse, double* rest, char* ws, const DistillPlan& pl,
                        hipStream_t st) {
   DistillPart* parts = reinterpret_cast<DistillPart*>(ws);
   const dim3 grid((unsigned)(a.R * pl.n_seg)), rows((unsigned)a.R), block(kThreads);
   if (rest) {
-    launch(distill_sum_kernel<DT, NL, true>, grid, block, st, a, pl.n_seg, parts);
+    launch(distill_sum_kernel<DT, true>, grid, block, st, a, pl.n_seg, pl.units, 0x100000u, parts);
     launch(distill_loss_kernel<DT, true>, rows, block, st, a, pl.n_seg, (const DistillPart*)parts, loss, lse, rest);
   } else {
-    launch(distill_sum_kernel<DT, NL, false>, grid, block, st, a, pl.n_seg, parts);
+    launch(distill_sum_kernel<DT, false>, grid, block, st, a, pl.n_seg, pl.units, 0x100000u, parts);
     launch(distill_loss_kernel<DT, false>, rows, block, st, a, pl.n_seg, (const DistillPart*)parts, loss, lse, rest);
   }
   return hipGetLastError();
@@ -433,11 +489,11 @@ hipError_t run_forward(const DistillArgs& a, float* loss, double* lse, double* r
 template <int DT, int NL>
 hipError_t run_grad(const DistillArgs& a, const float* grad_loss, const double* lse, const double* rest, void* dS,
                     int64_t d_stride, const DistillPlan& pl, hipStream_t st) {
-  const dim3 grid((unsigned)(a.R * pl.n_seg)), block(kThreads);
+  const dim3 grid((unsigned)(a.R * pl.grad_seg)), block(kThreads);
   if (rest)
-    launch(distill_grad_kernel<DT, NL, true>, grid, block, st, a, pl.n_seg, grad_loss, lse, rest, dS, d_stride);
+    launch(distill_grad_kernel<DT, NL, true>, grid, block, st, a, pl.grad_seg, grad_loss, lse, rest, dS, d_stride);
   else
-    launch(distill_grad_kernel<DT, NL, false>, grid, block, st, a, pl.n_seg, grad_loss, lse, rest, dS, d_stride);
+    launch(distill_grad_kernel<DT, NL, false>, grid, block, st, a, pl.grad_seg, grad_loss, lse, rest, dS, d_stride);
   return hipGetLastError();
 }
 
@@ -445,21 +501,17 @@ hipError_t run_grad(const DistillArgs& a, const float* grad_loss, const double* 
 
 hipError_t launch_distill(int32_t dtype, const DistillArgs& a, float* loss, double* lse, double* rest, char* ws,
                           const DistillPlan& pl, hipStream_t st) {
-  if (dtype == DFLASH_BF16) {
-    return pl.loads == 2 ? run_forward<DFLASH_BF16, 2>(a, loss, lse, rest, ws, pl, st)
-                         : run_forward<DFLASH_BF16, 8>(a, loss, lse, rest, ws, pl, st);
-  }
-  return pl.loads == 2 ? run_forward<DFLASH_F32, 2>(a, loss, lse, rest, ws, pl, st)
-                       : run_forward<DFLASH_F32, 8>(a, loss, lse, rest, ws, pl, st);
+  return dtype == DFLASH_BF16 ? run_forward<DFLASH_BF16>(a, loss, lse, rest, ws, pl, st)
+                              : run_forward<DFLASH_F32>(a, loss, lse, rest, ws, pl, st);
 }
 
 hipError_t launch_distill_grad(int32_t dtype, const DistillArgs& a, const float* grad_loss, const double* lse,
                                const double* rest, void* dS, int64_t d_stride, const DistillPlan& pl, hipStream_t st) {
   if (dtype == DFLASH_BF16) {
-    return pl.loads == 2 ? run_grad<DFLASH_BF16, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st)
+    return pl.grad_loads == 2 ? run_grad<DFLASH_BF16, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st)
                          : run_grad<DFLASH_BF16, 8>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
   }
-  return pl.loads == 2 ? run_grad<DFLASH_F32, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st)
+  return pl.grad_loads == 2 ? run_grad<DFLASH_F32, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st)
                        : run_grad<DFLASH_F32, 8>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
 }
 

@@ -232,9 +232,11 @@ SamplePlan sample_plan(const dflash_rows& r);
 hipError_t launch_sample(int32_t dtype, const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl,
                          hipStream_t st);
 
-// dflash_distill / dflash_distill_grad: a block takes kDistillThreads *
-// loads slots of a row
+// dflash_distill: a block sums `units` times kDistillUnit slots of a row;
+// dflash_distill_grad: a block writes kDistillThreads * grad_loads slots
 constexpr int kDistillThreads = 256;
+constexpr int kDistillUnit = 1024;
+constexpr int kDistillMaxUnits = 8;
 struct DistillPart {
   double m, s;  // log2 of the largest term (rounded) and sum of 2^(x - m) over the segment's tokens
 };
@@ -249,7 +251,8 @@ struct DistillArgs {
   const float* weight;   // or null
 };
 struct DistillPlan {
-  int loads, n_seg;
+  int units, n_seg;
+  int grad_loads, grad_seg;
   size_t total;
 };
 DistillPlan distill_plan(const dflash_rows& r);

@@ -3,7 +3,7 @@ dflash_distill, dflash_distill_grad) with the float64 oracle (oracle.rows).
 
 Bars.  Tokens, kept counts and filtered rows: equal.  prob: half a step of
 fp32 (2^-24 relative) plus 2^-40 for the fp64 sums.  lse: the library's
-exponential is off by at most 7e-12 relative, so a log-sum-exp by 2e-11
+exponential is off by at most 1.4e-11 relative, so a log-sum-exp by 2e-11
 absolute, plus 2^-49 of its own size.  loss: half a step of fp32 plus what lse
 and 1 - sum p bring in (1e-10 of the terms' size).  Gradients: half a step of
 the type, plus (|t| + 4) 2^-23 relative for the fp32 exponent t (|t| <= 126:
