@@ -91,27 +91,39 @@ struct Red {
   double d[kWaves];
 };
 
+// over the block's T threads
+template <int T>
 __device__ __forceinline__ double block_sum(Red& s, double v) {
-  v = wave_sum_f64(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s.d[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double r = s.d[0];
+  v = wave_sum_dpp_f64(v);
+  if constexpr (T > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s.d[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = s.d[0];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) r += s.d[w];
-  return r;
+    for (int w = 1; w < T / 64; ++w) v += s.d[w];
+  }
+  return v;
 }
 
+template <int T>
 __device__ __forceinline__ double block_max(Red& s, double v) {
+  v = fmax(v, dpp_f64<kDppRowShr1>(v, -INFINITY));
+  v = fmax(v, dpp_f64<kDppRowShr2>(v, -INFINITY));
+  v = fmax(v, dpp_f64<kDppRowShr4>(v, -INFINITY));
+  v = fmax(v, dpp_f64<kDppRowShr8>(v, -INFINITY));
+  v = fmax(v, dpp_f64<kDppRowBcast15, 0xA>(v, -INFINITY));
+  v = fmax(v, dpp_f64<kDppRowBcast31, 0xC>(v, -INFINITY));
+  v = readlane_f64(v, 63);
+  if constexpr (T > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s.d[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = s.d[0];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s.d[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double r = s.d[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) r = fmax(r, s.d[w]);
-  return r;
+    for (int w = 1; w < T / 64; ++w) v = fmax(v, s.d[w]);
+  }
+  return v;
 }
 
 // a list entry counts unless its index lies outside the vocabulary (padding)
@@ -121,6 +133,7 @@ __device__ __forceinline__ bool listed(const DistillArgs& a, int64_t row, int k,
 }
 
 // the teacher's normaliser c (natural log); -inf: the teacher's row is empty
+template <int T>
 __device__ __forceinline__ double teacher_lse(Red& red, const DistillArgs& a, int64_t row) {
   if (a.t_lse) {
     const double c = a.t_lse[row];
@@ -128,17 +141,17 @@ __device__ __forceinline__ double teacher_lse(Red& red, const DistillArgs& a, in
   }
   double m = -INFINITY;
   int idx;
-  for (int k = threadIdx.x; k < a.K; k += kThreads)
+  for (int k = threadIdx.x; k < a.K; k += T)
     if (listed(a, row, k, idx)) {
       const double t = (double)a.t_logit[row * a.K + k] / a.tau;
       m = t != t ? INFINITY : fmax(m, t);
     }
-  m = block_max(red, m);
+  m = block_max<T>(red, m);
   if (m == -INFINITY) return m;
   double s = 0.0;
-  for (int k = threadIdx.x; k < a.K; k += kThreads)
+  for (int k = threadIdx.x; k < a.K; k += T)
     if (listed(a, row, k, idx)) s += exp((double)a.t_logit[row * a.K + k] / a.tau - m);
-  return m + log(block_sum(red, s));
+  return m + log(block_sum<T>(red, s));
 }
 
 // ---------------------------------------------------------------- forward
@@ -279,8 +292,10 @@ __device__ __forceinline__ double join_log(double m, double s) {
   return (m + log2(s)) * kLn2;
 }
 
-template <int DT, bool REST>
-__global__ __launch_bounds__(kThreads) void distill_loss_kernel(DistillArgs a, int n_seg, const DistillPart* __restrict__ parts,
+// T threads a row: a wave for short lists (no barriers), a block for long ones,
+// whose repeated entries are searched for pair by pair
+template <int DT, int T, bool REST>
+__global__ __launch_bounds__(T) void distill_loss_kernel(DistillArgs a, int n_seg, const DistillPart* __restrict__ parts,
                                                                 float* __restrict__ loss, double* __restrict__ lse_out,
                                                                 double* __restrict__ rest_out) {
   __shared__ Red red;
@@ -298,30 +313,30 @@ __global__ __launch_bounds__(kThreads) void distill_loss_kernel(DistillArgs a, i
   }
   const RowRef<DT> z(a.S, row, a.stride, a.V);
   const double c2 = kLog2e64 / a.tau;
-  const double c = teacher_lse(red, a, row);
+  const double c = teacher_lse<T>(red, a, row);
 
   // the segments' sums: maxima first, then the terms in segment order
   const DistillPart* part = parts + row * n_seg;
   double M = -INFINITY;
-  for (int g = tid; g < n_seg; g += kThreads)
+  for (int g = tid; g < n_seg; g += T)
     if (part[g].s != 0.0) M = fmax(M, part[g].m);
-  M = block_max(red, M);
+  M = block_max<T>(red, M);
   double s = 0.0;
-  for (int g = tid; g < n_seg; g += kThreads)
+  for (int g = tid; g < n_seg; g += T)
     if (part[g].s != 0.0) s += part[g].s == part[g].s ? ldexp(part[g].s, (int)fmax(part[g].m - M, -4000.0)) : (double)NAN;
-  s = block_sum(red, s);
+  s = block_sum<T>(red, s);
   const double rest = join_log(M, s);  // natural
   double lse = rest;
 
   if constexpr (REST) {
     // the listed tokens' own terms, each token once
-    for (int k = tid; k < a.K; k += kThreads) {
+    for (int k = tid; k < a.K; k += T) {
       int idx;
       seen[k] = listed(a, row, k, idx) ? idx : -1;
     }
     __syncthreads();
     double lm = -INFINITY;
-    for (int k = tid; k < a.K; k += kThreads) {
+    for (int k = tid; k < a.K; k += T) {
       const int idx = seen[k];
       bool first = idx >= 0;
       for (int q = 0; q < k && first; ++q) first = seen[q] != idx;
@@ -330,11 +345,11 @@ __global__ __launch_bounds__(kThreads) void distill_loss_kernel(DistillArgs a, i
         lm = v != v ? INFINITY : fmax(lm, (double)v);
       }
     }
-    lm = block_max(red, lm);
+    lm = block_max<T>(red, lm);
     if (lm > -INFINITY) {
       const double LM = rint(lm * c2);
       double ls = 0.0;
-      for (int k = tid; k < a.K; k += kThreads) {
+      for (int k = tid; k < a.K; k += T) {
         const int idx = seen[k];
         bool first = idx >= 0;
         for (int q = 0; q < k && first; ++q) first = seen[q] != idx;
@@ -343,17 +358,17 @@ __global__ __launch_bounds__(kThreads) void distill_loss_kernel(DistillArgs a, i
           if (v != kNegInf) ls += v < INFINITY ? exp2(fma((double)v, c2, -LM)) : (double)NAN;
         }
       }
-      ls = block_sum(red, ls);
-      const double T = s > 0.0 ? fmax(M, LM) : LM;
-      const double all = (s == 0.0 ? 0.0 : ldexp(s, (int)fmax(M - T, -4000.0))) + ldexp(ls, (int)fmax(LM - T, -4000.0));
-      lse = s != s ? s : join_log(T, all);
+      ls = block_sum<T>(red, ls);
+      const double top = s > 0.0 ? fmax(M, LM) : LM;
+      const double all = (s == 0.0 ? 0.0 : ldexp(s, (int)fmax(M - top, -4000.0))) + ldexp(ls, (int)fmax(LM - top, -4000.0));
+      lse = s != s ? s : join_log(top, all);
     }
   }
 
   // D over the listed entries
   double d = 0.0, p_sum = 0.0;
   if (c > -INFINITY || c != c)
-    for (int k = tid; k < a.K; k += kThreads) {
+    for (int k = tid; k < a.K; k += T) {
       int idx;
       if (!listed(a, row, k, idx)) continue;
       const double logp = (double)a.t_logit[row * a.K + k] / a.tau - c;
@@ -361,8 +376,8 @@ __global__ __launch_bounds__(kThreads) void distill_loss_kernel(DistillArgs a, i
       p_sum += p;
       if (p != 0.0) d += p * (logp - (double)row_value<DT>(z, idx) / a.tau + lse);
     }
-  d = block_sum(red, d);
-  p_sum = block_sum(red, p_sum);
+  d = block_sum<T>(red, d);
+  p_sum = block_sum<T>(red, p_sum);
   if constexpr (REST) {
     const double p_rest = 1.0 - p_sum;
     if (c > -INFINITY && rest > -INFINITY && p_rest > 0.0) d += p_rest * (log(p_rest) - rest + lse);
@@ -408,7 +423,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   double c = -INFINITY, p_sum = 0.0;
   float own[kPerThread];  // the listed tokens' logits of this segment, read before anything is stored (dS may be S)
   if (!off) {
-    c = teacher_lse(red, a, row);
+    c = teacher_lse<kThreads>(red, a, row);
     if (c != -INFINITY) {
 #pragma unroll
       for (int j = 0; j < kPerThread; ++j) {
@@ -424,7 +439,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
         }
       }
     }
-    p_sum = block_sum(red, p_sum);
+    p_sum = block_sum<kThreads>(red, p_sum);
   }
   if (off || c == -INFINITY || lse == -INFINITY) {  // no gradient: weight zero, or an empty row on either side
 #pragma unroll
@@ -471,18 +486,18 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   }
 }
 
-template <int DT>
+template <int DT, bool REST>
 hipError_t run_forward(const DistillArgs& a, float* loss, double* lse, double* rest, char* ws, const DistillPlan& pl,
                        hipStream_t st) {
   DistillPart* parts = reinterpret_cast<DistillPart*>(ws);
-  const dim3 grid((unsigned)(a.R * pl.n_seg)), rows((unsigned)a.R), block(kThreads);
-  if (rest) {
-    launch(distill_sum_kernel<DT, true>, grid, block, st, a, pl.n_seg, pl.units, 0x100000u, parts);
-    launch(distill_loss_kernel<DT, true>, rows, block, st, a, pl.n_seg, (const DistillPart*)parts, loss, lse, rest);
-  } else {
-    launch(distill_sum_kernel<DT, false>, grid, block, st, a, pl.n_seg, pl.units, 0x100000u, parts);
-    launch(distill_loss_kernel<DT, false>, rows, block, st, a, pl.n_seg, (const DistillPart*)parts, loss, lse, rest);
-  }
+  const dim3 rows((unsigned)a.R);
+  launch(distill_sum_kernel<DT, REST>, dim3((unsigned)(a.R * pl.n_seg)), dim3(kThreads), st, a, pl.n_seg, pl.units, 0x100000u,
+         parts);
+  if (a.K <= 128)
+    launch(distill_loss_kernel<DT, 64, REST>, rows, dim3(64), st, a, pl.n_seg, (const DistillPart*)parts, loss, lse, rest);
+  else
+    launch(distill_loss_kernel<DT, kThreads, REST>, rows, dim3(kThreads), st, a, pl.n_seg, (const DistillPart*)parts, loss, lse,
+           rest);
   return hipGetLastError();
 }
 
@@ -501,8 +516,11 @@ hipError_t run_grad(const DistillArgs& a, const float* grad_loss, const double* 
 
 hipError_t launch_distill(int32_t dtype, const DistillArgs& a, float* loss, double* lse, double* rest, char* ws,
                           const DistillPlan& pl, hipStream_t st) {
-  return dtype == DFLASH_BF16 ? run_forward<DFLASH_BF16>(a, loss, lse, rest, ws, pl, st)
-                              : run_forward<DFLASH_F32>(a, loss, lse, rest, ws, pl, st);
+  if (dtype == DFLASH_BF16)
+    return rest ? run_forward<DFLASH_BF16, true>(a, loss, lse, rest, ws, pl, st)
+                : run_forward<DFLASH_BF16, false>(a, loss, lse, rest, ws, pl, st);
+  return rest ? run_forward<DFLASH_F32, true>(a, loss, lse, rest, ws, pl, st)
+              : run_forward<DFLASH_F32, false>(a, loss, lse, rest, ws, pl, st);
 }
 
 hipError_t launch_distill_grad(int32_t dtype, const DistillArgs& a, const float* grad_loss, const double* lse,
