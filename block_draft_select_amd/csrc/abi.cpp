@@ -253,8 +253,9 @@ SamplePlan sample_plan(const dflash_rows& r) {
 
 // The forward pass: 2048 blocks (eight per CU) if the rows have that much, and
 // more only because a block's segment is bounded.  The gradient: eight slots
-// a thread in flight (7 per cent faster than two on 2048 rows) unless the
-// grid then has too few blocks.
+// a thread (213 us against 278 with two at 2048 x 151936 bf16, 13.3 against
+// 14.5 at 427 blocks) unless the grid then leaves CUs idle (80 blocks: 9.0
+// against 6.4).
 DistillPlan distill_plan(const dflash_rows& r) {
   DistillPlan p{};
   const int slots = row_slots(r), units = (slots + kDistillUnit - 1) / kDistillUnit;
@@ -265,7 +266,7 @@ DistillPlan distill_plan(const dflash_rows& r) {
   p.n_seg = (units + p.units - 1) / p.units;
   for (p.grad_loads = 8;; p.grad_loads = 2) {
     p.grad_seg = (slots + kDistillThreads * p.grad_loads - 1) / (kDistillThreads * p.grad_loads);
-    if (p.grad_loads == 2 || r.R * p.grad_seg >= 2048) break;
+    if (p.grad_loads == 2 || r.R * p.grad_seg >= 256) break;
   }
   p.total = align256((size_t)r.R * p.n_seg * sizeof(DistillPart));
   return p;

@@ -191,7 +191,7 @@ constexpr int kSampleItems = 6144;
 constexpr int kSampleOdd = 64;
 constexpr int kSampleMaxSegSlots = 8191;
 struct SampleValues {
-  uint16_t items[kSampleItems];  // counts of values, in the order of the row's tokens
+  uint16_t counts[kSampleItems];
   uint32_t odd[kSampleOdd];      // tokens near zero: value << 16 | place in the segment
 };
 // bins whose tokens a row needs beyond the lists: up to two ranges

@@ -908,6 +908,18 @@ constexpr int kMid = kMags + 1, kLow = 2 * kMags + 2, kItems = kLow + 1;
 constexpr int kGroups = (kItems + 63) / 64;  // groups of 64 items
 static_assert(kGroups * 64 <= kSampleItems && kGroups <= kThreads, "");
 
+// A segment's counters in memory: for either sign kSide by magnitude (0: nearer
+// to zero, kMags + 1: over the range), then the tokens under the range
+constexpr int kSide = kMags + 2, kUnder = 2 * kSide;
+static_assert(kUnder % 4 == 0 && kUnder + 2 <= kSampleItems, "");
+__device__ __forceinline__ int item_of(int counter) {  // -1: none, or part of kMid
+  const int q = counter < kSide ? counter : counter - kSide;
+  if (counter >= kUnder) return counter == kUnder ? kLow : -1;
+  if (q == 0) return -1;
+  return counter < kSide ? kMags + 1 - q : q <= kMags ? kMid + q : -1;
+}
+__device__ __forceinline__ int counter_of(int item) { return item < kMid ? kMags + 1 - item : kSide + item - kMid; }
+
 // smallest magnitude (bit pattern) with a counter of its own
 __device__ __forceinline__ uint32_t value_base(double c8) {
   const double T = 8.0 * 1.4426950408889634 / c8;  // c8 = 0: inf
@@ -918,11 +930,9 @@ __device__ __forceinline__ uint32_t value_base(double c8) {
 __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, int64_t row0, int n_seg, int seg_slots,
                                                                  SampleValues* __restrict__ parts) {
   constexpr int VE = 8, U = 4;
-  // counters: for either sign kMags + 2 by magnitude (0: nearer to zero, kMags
-  // + 1: over the range), then one a lane for the tokens under the range
-  // (equal addresses queue up)
-  constexpr int kSide = kMags + 2, kUnder = 2 * kSide, kCounters = kUnder + 64;
-  __shared__ uint32_t count[kCounters];
+  // the tokens under the range have a counter a lane (equal addresses queue up)
+  constexpr int kCounters = kUnder + 64;
+  __shared__ __align__(16) uint32_t count[kCounters];
   __shared__ uint32_t n_odd;
   const int tid = threadIdx.x, lane = tid & 63, seg = blockIdx.x % n_seg;
   const int64_t row = row0 + blockIdx.x / n_seg;
@@ -979,13 +989,14 @@ __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, i
       }
     }
   }
-  // item 0 and the positive values from the largest down, kMid, the negative ones
-  auto item = [&](int i) { return i < kMid ? count[kMags + 1 - i] : i == kMid ? n_mid : count[kSide + i - kMid]; };
-  uint32_t* items = reinterpret_cast<uint32_t*>(out.items);
-  for (int j = tid; j < kLow / 2; j += kThreads) items[j] = item(2 * j) | item(2 * j + 1) << 16;
+  uint2* counts = reinterpret_cast<uint2*>(out.counts);
+  for (int j = tid; j < kUnder / 4; j += kThreads) {
+    const uint4 c = reinterpret_cast<const uint4*>(count)[j];
+    counts[j] = make_uint2(c.x | c.y << 16, c.z | c.w << 16);
+  }
   if (tid < 64) {
     const uint32_t under = wave_sum_u32(count[kUnder + tid]);
-    if (tid == 0) items[kLow / 2] = under;
+    if (tid == 0) counts[kUnder / 4] = make_uint2(under, 0);
   }
 }
 
@@ -996,6 +1007,7 @@ struct ValLds {
   uint64_t win[kThreads];    // the tokens near zero, sorted
   double wcum[kThreads];     // their running weight
   Red red;
+  uint32_t near[2];
   uint32_t n;
   uint32_t idx;
 };
@@ -1137,7 +1149,7 @@ struct Values {
   __device__ __forceinline__ uint32_t index_of(int item, uint32_t r) {
     if (item == kMid) return (uint32_t)s.win[r - 1];
     // its segment, by the segments' own counts (n_seg <= kThreads)
-    const uint32_t has = tid < n_seg ? part[tid].items[item] : 0u, sc = ops.scan(has);
+    const uint32_t has = tid < n_seg ? part[tid].counts[counter_of(item)] : 0u, sc = ops.scan(has);
     const int g = min(ops.first(sc >= r), n_seg - 1);
     if (tid == g) s.n = sc - has;
     __syncthreads();
@@ -1177,39 +1189,49 @@ struct Values {
 // one bf16 row from its segments' counts; false if the row has to be binned
 __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, int64_t row, int n_seg, int seg_slots,
                                                 const SampleValues* __restrict__ part, const SampleOut& o, uint64_t* cut_out) {
-  constexpr int VE = 8, kPairs = kGroups * 32, kMine = (kPairs + kThreads - 1) / kThreads;
+  constexpr int VE = 8, kPairs = kUnder / 2 + 1, kMine = (kPairs + kThreads - 1) / kThreads;
   BlockOps ops(s.red);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const RowParams rp = row_params(a, row);
   const double c8 = rp.c8, u = row_uniform(o, row);
   const uint32_t base = value_base(c8);
-  // the segments' counts, added two a word where no sum of 16 bits can carry
+  // the segments' counts
   uint32_t c0[kMine], c1[kMine];
 #pragma unroll
   for (int j = 0; j < kMine; ++j) c0[j] = c1[j] = 0;
 #pragma unroll 4
   for (int g = 0; g < n_seg; ++g) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(part[g].items);
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(part[g].counts);
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
       const int i = tid + j * kThreads;
-      const uint32_t v = 2 * i < kItems ? p[i] : 0u;
+      const uint32_t v = i < kPairs ? p[i] : 0u;
       c0[j] += v & 0xFFFFu;
       c1[j] += v >> 16;
     }
   }
   int top = kItems;  // the first item with a token: the row's largest
 #pragma unroll
-  for (int j = kMine - 1; j >= 0; --j) {
+  for (int j = 0; j < kMine; ++j) {
     const int i = tid + j * kThreads;
-    if (c1[j] && 2 * i + 1 < kLow) top = 2 * i + 1;
-    if (c0[j] && i > 0 && 2 * i < kLow) top = 2 * i;
-    if (i < kPairs) {
-      s.c[2 * i] = c0[j];
-      s.c[2 * i + 1] = 2 * i + 1 < kItems ? c1[j] : 0u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int item = item_of(2 * i + h);
+      const uint32_t c = h ? c1[j] : c0[j];
+      if (i < kPairs && item >= 0) {
+        s.c[item] = c;
+        if (c && item > 0 && item < kLow) top = min(top, item);
+      }
     }
   }
+  if (tid == 0) s.near[0] = c0[0];                                           // counter 0
+  if (tid == (kSide / 2) % kThreads) s.near[1] = c0[kSide / 2 / kThreads];  // counter kSide
+  static_assert(kSide % 2 == 0, "");
+  if (tid < kGroups * 64 - kItems) s.c[kItems + tid] = 0;
   if (tid == 0) s.n = 0;
+  __syncthreads();
+  if (tid == 0) s.c[kMid] = s.near[0] + s.near[1];
+  if (s.near[0] + s.near[1]) top = min(top, kMid);
   __syncthreads();
   const uint32_t n_over = s.c[0], n_mid = s.c[kMid], n_low = s.c[kLow];
   if (n_over || n_mid > (uint32_t)kThreads) return false;
@@ -1217,7 +1239,7 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
     // the tokens near zero, from the segments' lists; too many in one segment: not listed
     bool full = false;
     for (int g = tid; g < n_seg; g += kThreads) {
-      const uint32_t k = part[g].items[kMid];
+      const uint32_t k = (uint32_t)part[g].counts[0] + part[g].counts[kSide];
       full |= k > (uint32_t)kSampleOdd;
       if (k && k <= (uint32_t)kSampleOdd) {
         uint32_t at = atomicAdd(&s.n, k);
