@@ -59,6 +59,7 @@ constexpr int kCols = 4;            // copies of the bins a wave's lanes spread 
 static_assert(kThreads == kBins, "one thread per bin");
 
 constexpr uint32_t kKeyLowest = 0x00800000u;  // ordered key of the lowest finite fp32
+constexpr uint32_t kKeyZero = 0x80000000u;    // of zero
 constexpr uint64_t kOneBits = 0x3FF0000000000000ull;
 
 constexpr double kLn2Eighth = 0.08664339756999316;  // ln 2 / 8
@@ -897,7 +898,8 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, i
 // ---------------------------------------------------------------- bf16 rows: counts of values
 // The items of a segment, in the order of the row's tokens: item 0 counts
 // positive values over the range (+inf too), 1 .. kMags the positive values
-// downwards, kMid all that lie nearer to zero, then the negative values, kLow
+// downwards, kMid all that lie nearer to zero (zeros are counted, the others
+// listed one by one), then the negative values, kLow
 // the finite values under the range; masked tokens are not counted.  The range
 // depends on T alone, so that a row's segments agree: kMags magnitudes (23
 // binades) below a power of two over 100 T, at least 128.  A row whose
@@ -909,7 +911,8 @@ constexpr int kGroups = (kItems + 63) / 64;  // groups of 64 items
 static_assert(kGroups * 64 <= kSampleItems && kGroups <= kThreads, "");
 
 // A segment's counters in memory: for either sign kSide by magnitude (0: nearer
-// to zero, kMags + 1: over the range), then the tokens under the range
+// to zero, kMags + 1: over the range), then the tokens under the range.  In
+// memory the two near zero hold the listed tokens and the zeros.
 constexpr int kSide = kMags + 2, kUnder = 2 * kSide;
 static_assert(kUnder % 4 == 0 && kUnder + 2 <= kSampleItems, "");
 __device__ __forceinline__ int item_of(int counter) {  // -1: none, or part of kMid
@@ -933,14 +936,14 @@ __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, i
   // the tokens under the range have a counter a lane (equal addresses queue up)
   constexpr int kCounters = kUnder + 64;
   __shared__ __align__(16) uint32_t count[kCounters];
-  __shared__ uint32_t n_odd;
+  __shared__ uint32_t n_odd, n_zero;
   const int tid = threadIdx.x, lane = tid & 63, seg = blockIdx.x % n_seg;
   const int64_t row = row0 + blockIdx.x / n_seg;
   const RowRef<DFLASH_BF16> z(a.Z, row, a.stride, a.V);
   const int begin = seg * seg_slots, end = min(begin + seg_slots, z.slots());
   const uint32_t base = value_base(row_params(a, row).c8);
   for (int i = tid; i < kCounters; i += kThreads) count[i] = 0;
-  if (tid == 0) n_odd = 0;
+  if (tid == 0) n_odd = n_zero = 0;
   __syncthreads();
   const uint32_t near2 = (base - 1u) * 0x10001u, over2 = (uint32_t)(kMags + 1) * 0x10001u, side2 = (uint32_t)kSide * 0x10001u;
   auto add = [&](const Slot& x) {
@@ -977,17 +980,36 @@ __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, i
   }
   __syncthreads();
   SampleValues& out = parts[blockIdx.x];
-  const uint32_t n_mid = count[0] + count[kSide];
-  if (n_mid != 0 && n_mid <= (uint32_t)kSampleOdd) {  // the few tokens near zero: find them again
+  if (count[0] + count[kSide] != 0) {  // tokens near zero: find them again
+    uint32_t zeros = 0;
 #pragma unroll 1
-    for (int sl = begin + tid; sl < end; sl += kThreads) {
-      const Slot x = z.load(sl);
+    for (int sl = begin + tid; sl < end; sl += U * kThreads) {
+      Slot x[U];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const uint32_t w = (i & 1) ? x.w[i >> 1] >> 16 : x.w[i >> 1] & 0xFFFFu;
-        if ((w & 0x7FFFu) < base) out.odd[atomicAdd(&n_odd, 1u)] = w << 16 | (uint32_t)((sl - begin) * VE + i);
-      }
+      for (int l = 0; l < U; ++l) x[l] = z.load(min(sl + l * kThreads, end));
+#pragma unroll
+      for (int l = 0; l < U; ++l)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          const uint32_t w = (i & 1) ? x[l].w[i >> 1] >> 16 : x[l].w[i >> 1] & 0xFFFFu;
+          if ((w & 0x7FFFu) < base && sl + l * kThreads < end) {
+            if ((w & 0x7FFFu) == 0) {
+              ++zeros;
+            } else {
+              const uint32_t at = atomicAdd(&n_odd, 1u);
+              if (at < (uint32_t)kSampleOdd) out.odd[at] = w << 16 | (uint32_t)((sl + l * kThreads - begin) * VE + i);
+            }
+          }
+        }
     }
+    zeros = wave_sum_u32(zeros);
+    if (lane == 0 && zeros) atomicAdd(&n_zero, zeros);
+    __syncthreads();  // every thread has read the two counters, too
+    if (tid == 0) {
+      count[0] = n_odd;
+      count[kSide] = n_zero;
+    }
+    __syncthreads();
   }
   uint2* counts = reinterpret_cast<uint2*>(out.counts);
   for (int j = tid; j < kUnder / 4; j += kThreads) {
@@ -1004,8 +1026,9 @@ struct ValLds {
   uint32_t c[kGroups * 64];  // tokens of each item
   uint32_t gc[kGroups + 1];  // tokens before each group of 64 items
   double gm[kGroups + 1];    // and their weight
-  uint64_t win[kThreads];    // the tokens near zero, sorted
-  double wcum[kThreads];     // their running weight
+  uint64_t win[kThreads];    // the tokens near zero, sorted; the zeros are one entry
+  uint32_t ncum[kThreads];   // their running count
+  double wcum[kThreads];     // and weight
   Red red;
   uint32_t near[2];
   uint32_t n;
@@ -1022,7 +1045,8 @@ struct ValueCross {
   uint32_t n;   // tokens up to and including the crossing one (kByWeight: tokens that pass)
   double cum;   // their weight
   int item;
-  uint32_t r;   // tokens of this item among them
+  uint32_t r;   // tokens of this item (kMid: of this entry) among them
+  int e;        // kMid: the entry
 };
 
 struct Values {
@@ -1034,7 +1058,8 @@ struct Values {
   const double c;        // log2(e) / T
   const uint32_t base;
   double tm;             // c times the largest logit
-  uint32_t n_mid, n_in;  // tokens near zero, tokens in the range
+  int n_mid;             // entries near zero
+  uint32_t n_in;         // tokens in the range
 
   // the logit of a counted value
   __device__ __forceinline__ float value(int item) const {
@@ -1089,7 +1114,7 @@ struct Values {
     int g = ops.first(hit);
     const bool none = g >= kGroups;
     if (none) {
-      if (kind == kByWeight) return ValueCross{n_in, s.gm[kGroups], -1, 0};
+      if (kind == kByWeight) return ValueCross{n_in, s.gm[kGroups], -1, 0, 0};
       g = ops.first(tid < kGroups && s.gc[tid + 1] >= n_in);  // rounding left the sum short: the last token
     }
     // every wave works the group out for itself
@@ -1115,60 +1140,69 @@ struct Values {
     const uint32_t lc = __shfl(c, l), n1 = n0 + __shfl(upto, l) - lc;  // before the item
     const double lw = __shfl(w, l), before = m0 + (l > 0 ? __shfl(cum, max(l - 1, 0)) : 0.0);
     const int li = g * 64 + l;
-    if (li == kMid && lc) {  // among the tokens near zero, one by one
-      const bool in = tid < (int)n_mid;
-      const bool h = in && (kind == kByCount    ? (double)(n1 + tid + 1) >= amount
-                            : kind == kByMassGe ? before + s.wcum[tid] >= amount
-                            : kind == kByMassGt ? before + s.wcum[tid] > amount
-                                                : weight(near_value(tid)) < amount);
-      int pos = min(ops.first(h), (int)n_mid);
-      if (kind != kByWeight) pos = none ? (int)n_mid : min(pos + 1, (int)n_mid);
-      return ValueCross{n1 + pos, pos ? before + s.wcum[pos - 1] : before, kMid, (uint32_t)pos};
-    }
-    if (kind == kByWeight) return ValueCross{n1, before, li, 0};
-    double r = (double)lc;
-    if (!none) {
-      if (kind == kByCount) {
-        r = amount - (double)n1;
-      } else {
-        r = fmin(fmax(floor((amount - before) / lw), 0.0), (double)lc);
-        // the quotient is off by rounding only: settle it on the sums themselves
-        if (r > 0.0 && (kind == kByMassGe ? fma(r - 1.0, lw, before) >= amount : fma(r - 1.0, lw, before) > amount)) r -= 1.0;
-        if (r < (double)lc && !(kind == kByMassGe ? fma(r, lw, before) >= amount : fma(r, lw, before) > amount)) r += 1.0;
-        r = fmax(r, 1.0);
+    if (li == kMid && lc) {  // among the entries near zero
+      const bool h = tid < n_mid && (kind == kByCount    ? (double)(n1 + s.ncum[tid]) >= amount
+                                     : kind == kByMassGe ? before + s.wcum[tid] >= amount
+                                     : kind == kByMassGt ? before + s.wcum[tid] > amount
+                                                         : weight(near_value(tid)) < amount);
+      int e = ops.first(h);
+      if (kind == kByWeight) {  // up to the last entry that passes
+        e = min(e, n_mid);
+        const uint32_t n = e ? s.ncum[e - 1] : 0u;
+        return ValueCross{n1 + n, e ? before + s.wcum[e - 1] : before, kMid, e > 1 ? n - s.ncum[e - 2] : n, max(e - 1, 0)};
       }
+      e = none ? n_mid - 1 : min(e, n_mid - 1);
+      const uint32_t n = e ? s.ncum[e - 1] : 0u, c1 = s.ncum[e] - n;
+      const double b = e ? before + s.wcum[e - 1] : before;
+      const double w1 = weight(near_value(e)), r = none ? (double)c1 : place(kind, amount, n1 + n, b, w1, c1);
+      return ValueCross{n1 + n + (uint32_t)r, fma(r, w1, b), kMid, (uint32_t)r, e};
     }
-    return ValueCross{n1 + (uint32_t)r, fma(r, lw, before), li, (uint32_t)r};
+    if (kind == kByWeight) return ValueCross{n1, before, li, 0, 0};
+    const double r = none ? (double)lc : place(kind, amount, n1, before, lw, lc);
+    return ValueCross{n1 + (uint32_t)r, fma(r, lw, before), li, (uint32_t)r, 0};
+  }
+
+  // the first of c tokens of weight w, behind n tokens of the weight `before`,
+  // at which the crossing falls (from 1)
+  __device__ __forceinline__ double place(int kind, double amount, uint32_t n, double before, double w, uint32_t c) const {
+    if (kind == kByCount) return amount - (double)n;
+    double r = fmin(fmax(floor((amount - before) / w), 0.0), (double)c);
+    // the quotient is off by rounding only: settle it on the sums themselves
+    if (r > 0.0 && (kind == kByMassGe ? fma(r - 1.0, w, before) >= amount : fma(r - 1.0, w, before) > amount)) r -= 1.0;
+    if (r < (double)c && !(kind == kByMassGe ? fma(r, w, before) >= amount : fma(r, w, before) > amount)) r += 1.0;
+    return fmax(r, 1.0);
   }
 
   __device__ __forceinline__ uint32_t item_key(const ValueCross& x) const {
-    return x.item == kMid ? comp_key(s.win[min(max(x.r, 1u), max(n_mid, 1u)) - 1]) : ord32(__float_as_uint(value(x.item)));
+    if (x.item == kMid) return n_mid ? comp_key(s.win[x.e]) : kKeyZero;
+    return ord32(__float_as_uint(value(x.item)));
   }
 
-  // index of the r-th (from 1) token of an item, in index order
-  __device__ __forceinline__ uint32_t index_of(int item, uint32_t r) {
-    if (item == kMid) return (uint32_t)s.win[r - 1];
+  // index of the r-th (from 1) token of x's item, in index order
+  __device__ __forceinline__ uint32_t index_of(const ValueCross& x, uint32_t r) {
+    const bool zero = x.item == kMid;
+    if (zero && comp_key(s.win[x.e]) != kKeyZero) return (uint32_t)s.win[x.e];
     // its segment, by the segments' own counts (n_seg <= kThreads)
-    const uint32_t has = tid < n_seg ? part[tid].counts[counter_of(item)] : 0u, sc = ops.scan(has);
+    const uint32_t has = tid < n_seg ? part[tid].counts[zero ? kSide : counter_of(x.item)] : 0u, sc = ops.scan(has);
     const int g = min(ops.first(sc >= r), n_seg - 1);
     if (tid == g) s.n = sc - has;
     __syncthreads();
     r -= s.n;
-    const uint32_t want = __float_as_uint(value(item)) >> 16;
+    const uint32_t want = zero ? 0u : __float_as_uint(value(x.item)) >> 16, bits = zero ? 0x7FFFu : 0xFFFFu;
     // the segment in order, four slots a thread at a time, up to the r-th
     const int end = min((g + 1) * seg_slots, z.slots());
 #pragma unroll 1
     for (int s0 = g * seg_slots; s0 < end; s0 += 4 * kThreads) {
       const int sl = s0 + 4 * tid;
       uint32_t mask = 0;
-      Slot x[4];
+      Slot y[4];
 #pragma unroll
-      for (int l = 0; l < 4; ++l) x[l] = z.load(min(sl + l, end));
+      for (int l = 0; l < 4; ++l) y[l] = z.load(min(sl + l, end));
 #pragma unroll
       for (int l = 0; l < 4; ++l)
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          mask |= ((uint32_t)((x[l].w[d] & 0xFFFFu) == want) | (uint32_t)(x[l].w[d] >> 16 == want) << 1) << (8 * l + 2 * d);
+          mask |= ((uint32_t)((y[l].w[d] & bits) == want) | (uint32_t)((y[l].w[d] >> 16 & bits) == want) << 1) << (8 * l + 2 * d);
       if (sl + 4 > end) mask &= sl < end ? (1u << 8 * (end - sl)) - 1u : 0u;
       const uint32_t found = (uint32_t)__popc(mask), upto = ops.scan(found);
       const int t = ops.first(upto >= r);
@@ -1224,8 +1258,8 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
       }
     }
   }
-  if (tid == 0) s.near[0] = c0[0];                                           // counter 0
-  if (tid == (kSide / 2) % kThreads) s.near[1] = c0[kSide / 2 / kThreads];  // counter kSide
+  if (tid == 0) s.near[0] = c0[0];                                           // counter 0: listed tokens
+  if (tid == (kSide / 2) % kThreads) s.near[1] = c0[kSide / 2 / kThreads];  // counter kSide: zeros
   static_assert(kSide % 2 == 0, "");
   if (tid < kGroups * 64 - kItems) s.c[kItems + tid] = 0;
   if (tid == 0) s.n = 0;
@@ -1233,13 +1267,14 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
   if (tid == 0) s.c[kMid] = s.near[0] + s.near[1];
   if (s.near[0] + s.near[1]) top = min(top, kMid);
   __syncthreads();
-  const uint32_t n_over = s.c[0], n_mid = s.c[kMid], n_low = s.c[kLow];
+  const uint32_t n_over = s.c[0], n_low = s.c[kLow], n_zero = s.near[1];
+  const uint32_t n_mid = s.near[0] + (n_zero != 0);  // entries
   if (n_over || n_mid > (uint32_t)kThreads) return false;
   if (n_mid) {
-    // the tokens near zero, from the segments' lists; too many in one segment: not listed
+    // from the segments' lists; too many in one segment: not listed
     bool full = false;
     for (int g = tid; g < n_seg; g += kThreads) {
-      const uint32_t k = (uint32_t)part[g].counts[0] + part[g].counts[kSide];
+      const uint32_t k = part[g].counts[0];
       full |= k > (uint32_t)kSampleOdd;
       if (k && k <= (uint32_t)kSampleOdd) {
         uint32_t at = atomicAdd(&s.n, k);
@@ -1250,6 +1285,7 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
         }
       }
     }
+    if (tid == 0 && n_zero) s.win[n_mid - 1] = comp_of(kKeyZero, 0);
     if (ops.first(full) < kThreads) return false;
     __syncthreads();
     const bool in = tid < (int)n_mid;
@@ -1263,7 +1299,7 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
     if (in) s.win[rank] = me;
     __syncthreads();
   }
-  Values f{s, ops, RowRef<DFLASH_BF16>(a.Z, row, a.stride, a.V), part, n_seg, seg_slots, tid, c8 * 0.125, base, 0.0, n_mid, 0};
+  Values f{s, ops, RowRef<DFLASH_BF16>(a.Z, row, a.stride, a.V), part, n_seg, seg_slots, tid, c8 * 0.125, base, 0.0, (int)n_mid, 0};
   top = kItems - (int)ops.max((uint32_t)(kItems - top));
   if (top >= kItems) {
     if (n_low) return false;
@@ -1274,8 +1310,12 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
   if (n_low && m - 512.0 / c8 < -(double)__uint_as_float(min((base + (uint32_t)kMags) << 16, 0x7F7F0000u))) return false;
   f.tm = m * f.c;
   if (n_mid) {
-    const double sc = ops.scan(tid < (int)n_mid ? f.weight(f.near_value(tid)) : 0.0);
-    if (tid < (int)n_mid) s.wcum[tid] = sc;
+    const uint32_t c = tid >= (int)n_mid ? 0u : comp_key(s.win[tid]) == kKeyZero ? n_zero : 1u, nc = ops.scan(c);
+    const double wc = ops.scan(c ? (double)c * f.weight(f.near_value(tid)) : 0.0);
+    if (c) {
+      s.ncum[tid] = nc;
+      s.wcum[tid] = wc;
+    }
     __syncthreads();
   }
   // each group's tokens and weight, two groups at a time, then before each group
@@ -1317,7 +1357,7 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
 
   uint32_t kept = N;
   double Z = total;
-  ValueCross cut{N, total, -1, 0}, draw{0, 0.0, -1, 0};
+  ValueCross cut{N, total, -1, 0, 0}, draw{0, 0.0, -1, 0, 0};
   bool in_low = false;  // a cut among the tokens under the range
 #pragma unroll 1
   for (int q = 0; q < 5; ++q) {
@@ -1363,10 +1403,9 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
   // the index of the cut's or the drawn token (a call has one or the other)
   const ValueCross x = o.out ? cut : draw;
   uint32_t idx = 0;
-  if (x.item >= 0 && (x.r > 0 || o.token)) idx = f.index_of(x.item, max(x.r, 1u));
+  if (x.item >= 0 && (x.r > 0 || o.token)) idx = f.index_of(x, max(x.r, 1u));
   if (tid == 0) {
-    if (o.out) *cut_out = x.item < 0 ? ~0ull : x.r == 0 ? (uint64_t)~(x.item != kMid ? f.item_key(x) : n_mid ? comp_key(s.win[0]) : 0x80000000u) << 32
-                                                        : comp_of(f.item_key(x), idx) + 1;
+    if (o.out) *cut_out = x.item < 0 ? ~0ull : x.r == 0 ? comp_of(f.item_key(x), 0) : comp_of(f.item_key(x), idx) + 1;
     if (o.token) {
       o.token[row] = (int32_t)idx;
       if (o.prob) o.prob[row] = (float)(f.weight(key_value(f.item_key(x))) / Z);

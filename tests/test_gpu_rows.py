@@ -209,6 +209,120 @@ def test_sample_longest_vocabulary():
     _check_sample(np.zeros((1, 2097152), dtype=np.float32), torch.float32, [dict(top_p=0.5)], np.array([0.75]))
 
 
+@pytest.mark.parametrize("kind", ["flat", "peaked", "ties", "masked", "shifted"])
+@pytest.mark.parametrize("R,V", [(260, 16003), (520, 15998), (1030, 5003), (345, 40009)])
+def test_sample_f32_rows_in_long_segments(kind, R, V):
+    # many fp32 rows: segments of 2, 4 and 8 slots a thread list only their
+    # largest tokens, and deep cuts ask for more
+    import torch
+    rng = np.random.default_rng(R + V + len(kind))
+    z = _logits(rng, R, V, kind)
+    _say(f"[rows] sample f32 R={R} V={V} {kind}")
+    _check_sample(z, torch.float32, [MIX[i % len(MIX)] for i in range(R)], rng.random(R), pad=V % 2)
+
+
+def test_filter_f32_rows_in_long_segments():
+    import torch
+    import block_draft_select_amd as dfl
+    rng = np.random.default_rng(41)
+    for R, V, kind in ((260, 16003, "ties"), (1030, 5003, "flat"), (520, 15998, "peaked")):
+        z = _logits(rng, R, V, kind)
+        st = [MIX[i % len(MIX)] for i in range(R)]
+        v, _ = _tensor(z, torch.float32)
+        r = dfl.rows(v)
+        dfl.dflash_filter(r, v, v, dfl.rows_workspace(r), **_filters(st))
+        torch.cuda.synchronize()
+        got, zz = _f64(v), z.astype(np.float64)
+        for i, s in enumerate(st):
+            assert np.array_equal(got[i], O.filtered(zz[i], torch.finfo(torch.float32).min, **_as_used(s))), (R, i, s)
+
+
+DEEP = [dict(), dict(top_k=5000), dict(top_k=9000, T=0.5), dict(top_p=0.6, T=8.0), dict(min_p=0.9, T=30.0), dict(top_p=0.99, T=50.0),
+        dict(min_p=0.999999, T=300.0), dict(top_p=0.5, T=float("inf")), dict(T=1e-3, top_p=0.9)]
+
+
+@pytest.mark.parametrize("kind", ["zeros", "half zeros", "positive and zeros", "near zero", "near zero, few", "mixed", "over", "under",
+                                  "over and masked"])
+def test_bf16_values_at_the_ends_of_the_counters(kind):
+    # exact zeros of both signs, magnitudes below the counters' range (listed
+    # one by one, or too many for that), values over and under it
+    import torch
+    rng = np.random.default_rng(42 + len(kind))
+    R, V = len(DEEP), 12007
+    z = (rng.normal(size=(R, V)) * 2).astype(np.float32)
+    if kind == "zeros":
+        z[:] = 0.0
+        z[:, ::3] = -0.0
+    if kind == "half zeros":
+        z[:, ::2] = 0.0
+        z[:, ::6] = -0.0
+    if kind == "positive and zeros":
+        z = np.maximum(z, 0.0)
+        z[:, 5:9] = 1e-7
+    if kind == "near zero":
+        z *= 1e-7
+    if kind == "near zero, few":
+        z[:, 100:140] *= 1e-8
+        z[:, 11000:11012] *= 1e-12
+        z[:, 7000:7300] = 0.0
+    if kind == "mixed":
+        z[:, ::5] = 0.0
+        z[:, 1::700] = 1e-38
+        z[:, 2::900] = -1e-30
+        z[:, 3::800] = 1e-42  # subnormal
+    if kind == "over":
+        z += 900.0
+    if kind == "under":
+        z -= 90000.0
+        z[:, 6000:] += 89000.0
+    if kind == "over and masked":
+        z[:, ::4] = -np.inf
+        z[:, 1::4] = np.nan
+        z[:, 2::4] *= 1e4
+    v, _ = _tensor(z, torch.bfloat16)
+    _say(f"[rows] bf16 {kind}")
+    for u in (rng.random(R), 1.0 - rng.random(R) * 1e-3):
+        _check_sample(z, torch.bfloat16, DEEP, u, pad=1)
+    import block_draft_select_amd as dfl
+    r = dfl.rows(v)
+    zz = _f64(v)
+    kept = torch.full((R,), -7, dtype=torch.int32, device="cuda")
+    dfl.dflash_filter(r, v, v, dfl.rows_workspace(r), kept=kept, **_filters(DEEP))
+    torch.cuda.synchronize()
+    got = _f64(v)
+    for i, s in enumerate(DEEP):
+        assert np.array_equal(got[i], O.filtered(zz[i], torch.finfo(torch.bfloat16).min, **_as_used(s))), (i, s)
+        assert int(kept[i]) == O.keep(zz[i], **_as_used(s))[0].size
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_sample_does_not_depend_on_the_other_rows(dt):
+    # the same rows alone and among many, which are split differently and pass
+    # through the workspace in batches
+    import torch
+    import block_draft_select_amd as dfl
+    t = dict(bf16=torch.bfloat16, f32=torch.float32)[dt]
+    rng = np.random.default_rng(43)
+    n, reps, V = len(MIX), 80, 150001
+    z = torch.from_numpy(_logits(rng, n, V, "peaked")).cuda().to(t)
+    u = torch.from_numpy(rng.random(n)).cuda()
+    f = _filters(MIX)
+
+    def run(z, u, f):
+        R = z.shape[0]
+        r = dfl.rows(z)
+        token = torch.full((R,), -7, dtype=torch.int32, device="cuda")
+        kept, prob = torch.full_like(token, -7), torch.full((R,), -7.0, device="cuda")
+        dfl.dflash_sample(r, z, u, token, dfl.rows_workspace(r), prob=prob, kept=kept, **f)
+        torch.cuda.synchronize()
+        return token, kept, prob
+
+    one = run(z, u, f)
+    many = run(z.repeat(reps, 1), u.repeat(reps), {k: v.repeat(reps) for k, v in f.items()})
+    assert torch.equal(one[0].repeat(reps), many[0]) and torch.equal(one[1].repeat(reps), many[1])
+    assert ((one[2].repeat(reps) - many[2]).abs() <= many[2] * 2.0 ** -23).all()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("kind,V,pad,shift,opad,oshift", [
     ("peaked", 1000, 0, 0, 0, 0), ("masked", 1003, 5, 3, 2, 1), ("ties", 50021, 3, 0, 3, 0), ("flat", 7, 1, 1, 0, 2),
