@@ -239,7 +239,7 @@ SamplePlan sample_plan(const dflash_rows& r) {
   // the one block that finishes a row needs no other.  Longer segments list
   // what ordinary cuts take (top-k of 50, peaked rows).
   const bool all = p.loads == 1;
-  p.cap = all ? kSampleThreads * 4 : p.loads == 2 ? 256 : 64;
+  p.cap = sample_cap(p.loads);
   p.batch = std::max(1, 4096 / p.n_seg);
   if (!all) p.batch = std::min<int64_t>(p.batch, 1024);
   const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);

@@ -174,11 +174,12 @@ constexpr int kSampleThreads = 512;
 constexpr int kSampleBins = 512;
 constexpr int kSampleMaxSeg = 512;   // blocks per row
 constexpr int kSampleMaxLoads = 8;
-constexpr int kSamplePick = 1024;    // tokens a block picks out of a segment
+// tokens that a segment of `loads` slots a thread lists
+constexpr int sample_cap(int loads) { return loads == 1 ? kSampleThreads * 4 : loads == 2 ? 256 : 64; }
 constexpr int kSampleAsk = 8192;     // tokens outside the lists that a row can ask for
 // a segment of an fp32 row: kSampleThreads * loads slots
 struct SamplePart {
-  double J;      // floor of the segment's maximum in eighths of an octave; -inf: nothing unmasked
+  double J;      // the segment's maximum in eighths of an octave, rounded; -inf: nothing unmasked
   float max;     // the maximum
   uint32_t n;    // unmasked tokens
   int32_t nb;    // bins in use

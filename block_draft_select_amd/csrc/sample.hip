@@ -18,7 +18,7 @@
 // share one weight; that token's index is looked up in its own segment.
 //
 // fp32 rows: in units of an eighth of an octave a weight is 2^(t / 8), t = z
-// 8 log2(e) / T, and floor(t) bins the tokens in their order.
+// 8 log2(e) / T, and rint(t) bins the tokens in their order.
 // (1) sample_hist_kernel counts the tokens and sums the weights of each bin of
 //     a row segment, and lists the segment's largest tokens in the order of
 //     their bins.
@@ -36,15 +36,14 @@
 //
 // sample_apply_kernel (dflash_filter) copies the kept tokens.
 //
-// Counts are exact and sums do not depend on the order of the atomics: a bin
-// adds the mantissas of 2^frac(t / 8) as 64-bit integers (the upper 51 fraction
-// bits of a double in [1, 1.0906) stay below 2^47.6, so 65536 of them fit),
-// which keeps 51 bits below each token's own weight.  Decisions next to a border need
-// such sums: they compare running sums over the whole vocabulary.
+// Counts are exact and sums do not depend on the order of the atomics: every
+// 2^((t - rint(t)) / 8) is rounded to a multiple of 2^-42 (off by 2^-43 of
+// itself) wherever it is used, and summed as an integer.  Decisions next to a
+// border need such sums: they compare running sums over the whole vocabulary.
 #include "rows_blocks.hpp"
 
 // t = z c8 is one rounded product wherever it is formed: fused into the
-// subtraction of its own floor it would differ from the value that was binned
+// subtraction of rint(t) it would differ from the value that was binned
 #pragma clang fp contract(off)
 
 namespace dfk {
@@ -55,23 +54,36 @@ constexpr int kThreads = kSampleThreads;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kBins = kSampleBins;  // 64 octaves; the last bin collects everything below (weight under 2^-63.9)
 constexpr int kTail = kBins - 1;
-constexpr int kCols = 4;            // copies of the bins a wave's lanes spread over
+constexpr int kCols = 4;            // copies of the bins that lanes spread over
 static_assert(kThreads == kBins, "one thread per bin");
 
 constexpr uint32_t kKeyLowest = 0x00800000u;  // ordered key of the lowest finite fp32
 constexpr uint32_t kKeyZero = 0x80000000u;    // of zero
-constexpr uint64_t kOneBits = 0x3FF0000000000000ull;
 
 constexpr double kLn2Eighth = 0.08664339756999316;  // ln 2 / 8
 
-// 2^(f / 8) for f in [0, 1): Taylor series to degree 8, truncation below
-// 8e-16, its upper terms in pairs (a short chain: a row's finish waits for few
-// weights, one after the other); exactly 1 at f = 0 and never below 1
-__device__ __forceinline__ double exp2_eighth(double f) {
-  const double x = f * kLn2Eighth, x2 = x * x;
-  const double a = fma(x, 1.0 / 6.0, 0.5), b = fma(x, 1.0 / 120.0, 1.0 / 24.0), c = fma(x, 1.0 / 5040.0, 1.0 / 720.0);
-  const double d = fma(x2, fma(x2, fma(x2, 1.0 / 40320.0, c), b), a);
-  return 1.0 + fma(x2, d, x);
+// an fp64 constant in scalar registers: an fma takes one as its addend, where a
+// literal would be moved into the vector registers that it accumulates in
+__device__ __forceinline__ double scalar(double c) {
+  asm("" : "+s"(c));
+  return c;
+}
+
+// 2^(f / 8), |f| <= 1/2, plus 1024: the Taylor series to degree 6 (truncation
+// below 2^-43.9), rounded to a multiple of 2^-42
+__device__ __forceinline__ double exp2_eighth_1024(double f) {
+  constexpr double L = kLn2Eighth, L2 = L * L, L3 = L2 * L;
+  double p = fma(f, scalar(L3 * L3 / 720.0), L3 * L2 / 120.0);
+  p = fma(p, f, scalar(L2 * L2 / 24.0));
+  p = fma(p, f, scalar(L3 / 6.0));
+  p = fma(p, f, scalar(L2 / 2.0));
+  p = fma(p, f, scalar(L));
+  return fma(p, f, scalar(1025.0));
+}
+__device__ __forceinline__ double exp2_eighth(double f) { return exp2_eighth_1024(f) - 1024.0; }
+// in units of 2^-42
+__device__ __forceinline__ unsigned long long exp2_eighth_units(double f) {
+  return (unsigned long long)__double_as_longlong(exp2_eighth_1024(f)) & ((1ull << 52) - 1);
 }
 
 // 2^(e / 8), e <= 0 an integer
@@ -85,6 +97,7 @@ __device__ __forceinline__ double pow2_eighth(int e) {
 
 struct RowParams {
   double c8;  // 8 log2(e) / T
+  double t8;  // T ln(2) / 8
   int64_t k;  // top-k; INT64_MAX: off
   double p;   // top-p; >= 1: off
   double m;   // min-p; <= 0: off
@@ -96,6 +109,7 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
   const bool greedy = !(T > 0.0f);
   RowParams r;
   r.c8 = 8.0 * 1.4426950408889634 / (greedy ? 1.0 : (double)T);
+  r.t8 = kLn2Eighth * (greedy ? 1.0 : (double)T);
   const int32_t k = a.top_k ? a.top_k[g] : 0;
   r.k = greedy ? 1 : (k > 0 ? (int64_t)k : INT64_MAX);
   const float p = a.top_p ? a.top_p[g] : 1.0f;
@@ -208,20 +222,20 @@ __device__ __forceinline__ uint32_t key_of(float v, float max_finite) {
 }
 __device__ __forceinline__ double key_value(uint32_t key) { return (double)__uint_as_float(unord32(key)); }
 
-// smallest ordered key >= kKeyLowest whose t = z c8 reaches `j` (0xFF800000,
-// above every finite key, if none does).  One round of the wave's 64 lanes
-// around j / c8, which rounding moves by a few keys; a search where that
-// guess does not bracket it (j or c8 extreme).
-__device__ __forceinline__ uint32_t lowest_key(double j, double c8) {
-  const double z = fmin(fmax(j / c8, -3.4028234663852886e38), 3.4028234663852886e38);  // 0/0: some finite value
+// smallest ordered key >= kKeyLowest whose t = z c8 rounds to `j` or more
+// (0xFF800000, above every finite key, if none does).  One round of the wave's
+// 64 lanes around (j - 1/2) t8, t8 = 1 / c8, which rounding moves by a few
+// keys; a search where that guess does not bracket it (j or c8 extreme).
+__device__ __forceinline__ uint32_t lowest_key(double j, double c8, double t8) {
+  const double z = fmin(fmax((j - 0.5) * t8, -3.4028234663852886e38), 3.4028234663852886e38);
   const uint32_t g = max(ord32_canon(__float_as_uint((float)z)), kKeyLowest + 32u);
   const uint32_t cand = min(g - 32u + (uint32_t)lane_id(), 0xFF7FFFFFu);
-  const uint64_t hit = __ballot(key_value(cand) * c8 >= j);
+  const uint64_t hit = __ballot(rint(key_value(cand) * c8) >= j);
   if (hit && !(hit & 1)) return __shfl(cand, __builtin_ctzll(hit));
   uint32_t l = kKeyLowest, h = 0xFF800000u;
   while (l < h) {
     const uint32_t mid = l + ((h - l) >> 1);
-    if (key_value(mid) * c8 >= j) h = mid; else l = mid + 1;
+    if (rint(key_value(mid) * c8) >= j) h = mid; else l = mid + 1;
   }
   return l;
 }
@@ -231,23 +245,34 @@ __device__ __forceinline__ uint64_t comp_of(uint32_t key, uint32_t index) { retu
 
 // ---------------------------------------------------------------- (1) bins of a segment
 
+// A bin's cell takes a token in one 64-bit atomic: 1 from bit 51 on, and below
+// it the token's weight over 15/16, in units of 2^-42 (0.02 to 0.107).  Four
+// cells a bin, so one takes at most 128 threads' 32 tokens: 2^12, whose sum
+// stays below 2^50.8.  Beside a separate count this saves a third of the LDS
+// work.
+constexpr int kCellCount = 51;
+constexpr unsigned long long kCellLess = 15ull << 38;  // 15/16 in units of 2^-42
+static_assert(kThreads / kCols * kSampleMaxLoads * 4 <= 4096, "");
+
+template <int NL>
 struct HistLds {
-  uint64_t mass[kBins * kCols];
-  uint32_t cnt[kBins * kCols];
-  uint32_t pick[kSamplePick];  // tokens to be listed: places in the segment
-  uint32_t n_pick;
+  unsigned long long cell[kBins * kCols];
+  uint32_t next[kBins];                                 // the list's next place for each bin
+  uint16_t pick[kWaves][NL == 1 ? 1 : sample_cap(NL)];  // a wave's slots with tokens to be listed
   Red red;
 };
 
-// the upper 51 fraction bits of 2^frac(t / 8), as an integer
-__device__ __forceinline__ unsigned long long weight_bits(double t, double fl) {
-  return (unsigned long long)(__double_as_longlong(exp2_eighth(t - fl)) >> 1);
+__device__ __forceinline__ unsigned long long cell_of(double f) {
+  // the constants touch the upper word alone
+  constexpr uint32_t kUpper = (uint32_t)((((1ull << kCellCount) - kCellLess) >> 32) - 0x40900000u);
+  const unsigned long long w = (unsigned long long)__double_as_longlong(exp2_eighth_1024(f));
+  return (unsigned long long)((uint32_t)(w >> 32) + kUpper) << 32 | (uint32_t)w;
 }
 
-// a token into the list, which is in the order of its bins (cnt[b * kCols]: bin b's next place)
-__device__ __forceinline__ void list_token(HistLds& s, uint64_t* list, double c8, double J, uint32_t key, uint32_t index) {
-  const int b = (int)fmin(J - floor(key_value(key) * c8), (double)kTail);
-  list[atomicAdd(&s.cnt[b * kCols], 1u)] = comp_of(key, index);
+// a token into the list, which is in the order of its bins
+__device__ __forceinline__ void list_token(uint32_t* next, uint64_t* list, double c8, double J, uint64_t c) {
+  const int b = (int)fmin(J - rint(key_value(comp_key(c)) * c8), (double)kTail);
+  list[atomicAdd(&next[b], 1u)] = c;
 }
 
 template <int NL>
@@ -255,27 +280,27 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
                                                                SamplePart* __restrict__ parts, uint64_t* __restrict__ lists) {
   constexpr int VE = RowType<DFLASH_F32>::VE;
   constexpr float kMax = RowType<DFLASH_F32>::kMax;
-  __shared__ HistLds s;
+  __shared__ HistLds<NL> s;
   BlockOps ops(s.red);
   const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
   const int64_t row = row0 + blockIdx.x / n_seg;
   const RowRef<DFLASH_F32> z(a.Z, row, a.stride, a.V);
-  const double c8 = row_params(a, row).c8;
+  const RowParams rp = row_params(a, row);
+  const double c8 = rp.c8;
   const int s0 = seg * (kThreads * NL) + tid;
   Slot x[NL];
 #pragma unroll
   for (int l = 0; l < NL; ++l) x[l] = z.load<true>(s0 + l * kThreads);
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    s.mass[c * kBins + tid] = 0;
-    s.cnt[c * kBins + tid] = 0;
+  for (int c = 0; c < kCols; ++c) s.cell[c * kBins + tid] = 0;
+  float m = kNegInf, most[NL];  // the slots' largest
+#pragma unroll
+  for (int l = 0; l < NL; ++l) {
+    most[l] = kNegInf;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) most[l] = fmaxf(most[l], slot_value<DFLASH_F32>(x[l], i));  // NaN drops out
+    m = fmaxf(m, most[l]);
   }
-  if (tid == 0) s.n_pick = 0;
-  float m = kNegInf;
-#pragma unroll
-  for (int l = 0; l < NL; ++l)
-#pragma unroll
-    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DFLASH_F32>(x[l], i));  // NaN drops out
   m = (float)ops.max((double)fminf(m, kMax));
   SamplePart& out = parts[blockIdx.x];
   if (m == kNegInf) {
@@ -288,37 +313,56 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
     }
     return;
   }
-  const double J = floor((double)m * c8);
-  const int col = tid & (kCols - 1);
+  const double J = rint((double)m * c8);
+  unsigned long long* cell = s.cell + (tid & (kCols - 1));
+  if (fabs(J) <= 0x1p20) {
+    // rint by adding 3 2^51, whose sum's lower word is the integer.  Tokens far
+    // below the maximum are raised to 1000 bins below it: the tail all the same
+    constexpr double kMagic = 0x1.8p52;
+    const float lowest = (float)((J - 1000.0) * rp.t8);
+    const int j = (int)J;
 #pragma unroll
-  for (int l = 0; l < NL; ++l)
+    for (int l = 0; l < NL; ++l)
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float v = slot_value<DFLASH_F32>(x[l], i);
+      for (int i = 0; i < VE; ++i) {
+        const float v = slot_value<DFLASH_F32>(x[l], i);
+        if (v > kNegInf) {
+          const double t = (double)__builtin_amdgcn_fmed3f(v, lowest, kMax) * c8, r = t + kMagic;
+          const uint32_t b = min((uint32_t)(j - (int)(uint32_t)__double_as_longlong(r)), (uint32_t)kTail);
+          atomicAdd(&cell[b * kCols], cell_of(t - (r - kMagic)));
+        }
+      }
+  } else {
+#pragma unroll 1
+    for (int e = 0; e < NL * VE; ++e) {
+      float v = kNegInf;
+#pragma unroll
+      for (int k = 0; k < NL * VE; ++k)
+        if (k == e) v = slot_value<DFLASH_F32>(x[k / VE], k % VE);
       if (v > kNegInf) {
-        const double t = (double)fminf(v, kMax) * c8, fl = floor(t);
-        const int b = (int)fmin(J - fl, (double)kTail);
-        atomicAdd(&s.cnt[b * kCols + col], 1u);
-        if (b < kTail) atomicAdd((unsigned long long*)&s.mass[b * kCols + col], weight_bits(t, fl));
+        const double t = (double)fminf(v, kMax) * c8, n = rint(t);
+        atomicAdd(&cell[(int)fmin(J - n, (double)kTail) * kCols], cell_of(t - n));
       }
     }
+  }
   __syncthreads();
   uint32_t c = 0, mirror = 0;  // mirror: the bin counted from the far end
-  uint64_t f = 0;
+  unsigned long long f = 0;
 #pragma unroll
   for (int k = 0; k < kCols; ++k) {
-    c += s.cnt[tid * kCols + k];
-    f += s.mass[tid * kCols + k];
-    mirror += s.cnt[(kBins - 1 - tid) * kCols + k];
+    const unsigned long long w = s.cell[tid * kCols + k];
+    c += (uint32_t)(w >> kCellCount);
+    f += w & ((1ull << kCellCount) - 1);
+    mirror |= (uint32_t)(s.cell[(kBins - 1 - tid) * kCols + k] >> kCellCount);
   }
-  f -= (uint64_t)c * (kOneBits >> 1);  // modulo 2^64: the fraction bits' sum
+  f += (unsigned long long)c * kCellLess;
   const uint32_t upto = ops.scan(c);
   const int nb = kBins - ops.first(mirror != 0);       // bins in use
   const int listed = ops.first(upto > (uint32_t)cap);  // leading bins with at most `cap` tokens together
-  s.cnt[tid * kCols] = upto - c;
+  s.next[tid] = upto - c;
   if (tid < nb) {
     out.upto[tid] = upto;
-    out.mass[tid] = tid < kTail ? (double)c + (double)f * 0x1p-51 : 0.0;
+    out.mass[tid] = tid < kTail ? (double)f * 0x1p-42 : 0.0;
   }
   if (tid == kThreads - 1) {
     out.J = J;
@@ -335,26 +379,31 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
       const float v = slot_value<DFLASH_F32>(x[0], i);
-      if (v > kNegInf) list_token(s, list, c8, J, key_of(v, kMax), (uint32_t)(first + tid * VE + i));
+      if (v > kNegInf) list_token(s.next, list, c8, J, comp_of(key_of(v, kMax), (uint32_t)(first + tid * VE + i)));
     }
   } else {
-    // few tokens: picked first, worked on densely afterwards
-    const uint32_t least = listed >= kBins ? kKeyLowest : lowest_key(J - (double)(listed - 1), c8);
+    // few tokens: a wave picks the slots that hold one, then reads them again,
+    // four lanes a slot
+    const float least = listed >= kBins ? -kMax : __uint_as_float(unord32(lowest_key(J - (double)(listed - 1), c8, rp.t8)));
+    uint16_t* pick = s.pick[tid >> 6];
+    int n = 0;
 #pragma unroll
-    for (int l = 0; l < NL; ++l)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float v = slot_value<DFLASH_F32>(x[l], i);
-        if (v > kNegInf && key_of(v, kMax) >= least) {
-          const uint32_t at = atomicAdd(&s.n_pick, 1u);
-          if (at < (uint32_t)kSamplePick) s.pick[at] = (uint32_t)((tid + l * kThreads) * VE + i);
-        }
+    for (int l = 0; l < NL; ++l) {
+      const uint64_t hits = __ballot(most[l] >= least);
+      if (hits) {
+        const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hits >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hits, 0));
+        if (most[l] >= least && at < sample_cap(NL)) pick[at] = (uint16_t)(tid + l * kThreads);
+        n += __popcll(hits);
       }
-    __syncthreads();
-    const int n = (int)min(s.n_pick, (uint32_t)kSamplePick);
-    for (int i = tid; i < n; i += kThreads) {
-      const int e = first + (int)s.pick[i];
-      list_token(s, list, c8, J, key_of(row_value<DFLASH_F32>(z, e), kMax), (uint32_t)e);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    n = min(n, sample_cap(NL));
+    for (int i = lane_id(); i < n * VE; i += kWave) {
+      const int slot = pick[i / VE];
+      const Slot y = z.load(seg * (kThreads * NL) + slot);
+      const int k = i % VE;
+      const float v = __uint_as_float(k == 0 ? y.w[0] : k == 1 ? y.w[1] : k == 2 ? y.w[2] : y.w[3]);
+      if (v >= least) list_token(s.next, list, c8, J, comp_of(key_of(v, kMax), (uint32_t)(first + slot * VE + k)));  // not NaN, not masked
     }
   }
 }
@@ -405,7 +454,7 @@ struct Finalize {
   const uint64_t* asked;  // the row's asked-for tokens
   const SampleAsk* ask;
   const int n_seg, cap;
-  const double c8, J;
+  const double c8, t8, J;
   const int tid;
   const uint32_t kmax;  // the row's largest key
   const int listed;     // bins 0 .. listed - 1 are in the segments' lists
@@ -417,8 +466,8 @@ struct Finalize {
 
   // weight of a key relative to 2^(J / 8)
   __device__ __forceinline__ double weight(uint32_t key) const {
-    const double t = key_value(key) * c8, fl = floor(t);
-    return exp2_eighth(t - fl) * pow2_eighth((int)fmax(fl - J, -16000.0));
+    const double t = key_value(key) * c8, n = rint(t);
+    return exp2_eighth(t - n) * pow2_eighth((int)fmax(n - J, -16000.0));
   }
 
   // f((~key, index)) of every token of bins B0 .. B1, and of others
@@ -482,9 +531,7 @@ struct Finalize {
         atomicAdd(&s.cnt[b], 1u);
         if (weigh) {
           const double t = key_value(key) * c8;
-          // 46 bits of the mantissa: sums of 2^21 tokens fit 64 bits
-          atomicAdd((unsigned long long*)&s.mass[b],
-                    (unsigned long long)((__double_as_longlong(exp2_eighth(t - floor(t))) - kOneBits) >> 6));
+          atomicAdd((unsigned long long*)&s.mass[b], exp2_eighth_units(t - rint(t)));  // sums of 2^21 tokens fit 64 bits
         }
       }
     });
@@ -548,7 +595,7 @@ struct Finalize {
     const bool hit = kind == kByCount    ? (double)s.cc[tid + 1] >= amount
                      : kind == kByMassGe ? s.cm[tid + 1] >= amount
                      : kind == kByMassGt ? s.cm[tid + 1] > amount
-                                         : pow2_eighth(-tid) <= amount;
+                                         : pow2_eighth(-tid) * exp2_eighth(-0.5) <= amount;  // the bin's lowest weight
     int b = ops.first(hit);
     if (b >= kBins) {
       b = kTail;
@@ -559,8 +606,8 @@ struct Finalize {
       }
     }
     if (b < b0 || b > b1) {
-      uint32_t klo = b == kTail ? kKeyLowest : lowest_key(J - b, c8);
-      uint32_t khi = b == 0 ? kmax : lowest_key(J - b + 1.0, c8) - 1u;
+      uint32_t klo = b == kTail ? kKeyLowest : lowest_key(J - b, c8, t8);
+      uint32_t khi = b == 0 ? kmax : lowest_key(J - b + 1.0, c8, t8) - 1u;
       uint32_t cb = s.cc[b], nc = s.cc[b + 1] - cb;
       double mb = s.cm[b];
       if (nc == 0) return Cross{cb, mb, ((uint64_t)~khi) << 32, 0};  // kByWeight: nothing in the threshold's own bin
@@ -609,9 +656,9 @@ struct Finalize {
         const int sh = max(0, 32 - __builtin_clz(range) - 9);
         pass(B0, b, klo, khi, 0, 0xFFFFFFFFu, sh, false);
         // one bin holds one eighth of an octave: its unit is that of its lowest key
-        const double unit = b == kTail ? 0.0 : pow2_eighth((int)fmax(floor(key_value(klo) * c8) - J, -16000.0));
+        const double unit = b == kTail ? 0.0 : pow2_eighth((int)fmax(rint(key_value(klo) * c8) - J, -16000.0)) * 0x1p-42;
         const uint32_t c = s.cnt[tid];
-        const double mass = unit * ((double)c + (double)s.mass[tid] * 0x1p-46);
+        const double mass = unit * (double)s.mass[tid];
         const uint32_t c1 = cb + ops.scan(c);
         const double m1 = mb + ops.scan(mass);
         const uint32_t n_part = (range >> sh) + 1;  // parts, from the highest key down
@@ -695,7 +742,8 @@ struct Finalize {
 // cut or draw whose amount depends on an earlier cut inside a bin takes the
 // bins of that amount's bounds.  True if all are listed; else asks for them.
 __device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowParams& rp, uint32_t N, double wmax, bool draw,
-                                            double u, double J, double c8, uint32_t kmax, int listed, SampleAsk& ask) {
+                                            double u, double J, uint32_t kmax, int listed, SampleAsk& ask) {
+  const double c8 = rp.c8, t8 = rp.t8;
   constexpr double kLess = 1.0 - 0x1p-40, kMore = 1.0 + 0x1p-40;
   const int tid = threadIdx.x;
   const double total = s.cm[kBins], after = s.cm[tid + 1];
@@ -722,7 +770,7 @@ __device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowP
     any = true;
   }
   if (rp.m > 0.0) {
-    const int bm = min(ops.first(pow2_eighth(-tid) <= rp.m * wmax), kTail);
+    const int bm = min(ops.first(pow2_eighth(-tid) * exp2_eighth(-0.5) <= rp.m * wmax), kTail);
     if (bm <= cut1) {
       need0 = min(need0, bm);
       need1 = max(need1, bm);
@@ -750,11 +798,11 @@ __device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowP
   const uint32_t count = s.cc[need1 + 1] - s.cc[need0] + (d1 >= 0 ? s.cc[d1 + 1] - s.cc[d0] : 0u);
   if (d1 < 0) d0 = kBins;
   // keys of the two ranges of bins (an empty second one: none)
-  const uint32_t l0 = need1 == kTail ? kKeyLowest : lowest_key(J - need1, c8), h0 = need0 == 0 ? kmax : lowest_key(J - need0 + 1.0, c8) - 1u;
+  const uint32_t l0 = need1 == kTail ? kKeyLowest : lowest_key(J - need1, c8, t8), h0 = need0 == 0 ? kmax : lowest_key(J - need0 + 1.0, c8, t8) - 1u;
   uint32_t l1 = 1, h1 = 0;
   if (d1 >= 0) {
-    l1 = d1 == kTail ? kKeyLowest : lowest_key(J - d1, c8);
-    h1 = d0 == 0 ? kmax : lowest_key(J - d0 + 1.0, c8) - 1u;
+    l1 = d1 == kTail ? kKeyLowest : lowest_key(J - d1, c8, t8);
+    h1 = d0 == 0 ? kmax : lowest_key(J - d0 + 1.0, c8, t8) - 1u;
   }
   if (tid == 0) {
     ask.kind = count <= (uint32_t)kSampleAsk ? kSampleAskBins : kSampleAskRow;
@@ -837,11 +885,11 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
   const uint32_t kmax = key_of(m, RowType<DFLASH_F32>::kMax);
   Finalize<DFLASH_F32, MODE> f{s, ops, RowRef<DFLASH_F32>(a.Z, row, a.stride, a.V), part, lists + (size_t)blockIdx.x * n_seg * cap,
                                MODE == kSecond ? asked + (size_t)blockIdx.x * kSampleAsk : nullptr,
-                               MODE == kSecond ? asks + blockIdx.x : nullptr, n_seg, cap, rp.c8, J, tid, kmax, listed,
+                               MODE == kSecond ? asks + blockIdx.x : nullptr, n_seg, cap, rp.c8, rp.t8, J, tid, kmax, listed,
                                0, 0, 0.0, 1, 0, 0};
   const double wmax = f.weight(kmax);
   if constexpr (MODE == kFirst) {
-    if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, rp.c8, kmax, listed, asks[blockIdx.x])) return;
+    if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, kmax, listed, asks[blockIdx.x])) return;
   }
   f.answer(rp, N, wmax, u, row, o, cuts + blockIdx.x);
 }
@@ -1432,7 +1480,7 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
   }
   m = (float)ops.max((double)fminf(m, kMax));
   if (m == kNegInf) return empty_row(row, o, cut_out);
-  const double c8 = rp.c8, J = floor((double)m * c8);
+  const double c8 = rp.c8, J = rint((double)m * c8);
   s.mass[tid] = 0;
   s.cnt[tid] = 0;
   __syncthreads();
@@ -1443,19 +1491,16 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
     for (int i = 0; i < VE; ++i) {
       const float v = slot_value<DT>(x, i);
       if (v > kNegInf) {
-        const double t = (double)fminf(v, kMax) * c8, fl = floor(t);
-        const int b = (int)fmin(J - fl, (double)kTail);
+        const double t = (double)fminf(v, kMax) * c8, n = rint(t);
+        const int b = (int)fmin(J - n, (double)kTail);
         atomicAdd(&s.cnt[b], 1u);
-        // 46 bits of the mantissa: sums of 2^21 tokens fit 64 bits
-        if (b < kTail)
-          atomicAdd((unsigned long long*)&s.mass[b],
-                    (unsigned long long)((__double_as_longlong(exp2_eighth(t - fl)) - kOneBits) >> 6));
+        if (b < kTail) atomicAdd((unsigned long long*)&s.mass[b], exp2_eighth_units(t - n));  // sums of 2^21 tokens fit 64 bits
       }
     }
   }
   __syncthreads();
   const uint32_t c = s.cnt[tid], cs = ops.scan(c);
-  const double cum = ops.scan(tid < kTail ? ((double)c + (double)s.mass[tid] * 0x1p-46) * pow2_eighth(-tid) : 0.0);
+  const double cum = ops.scan(tid < kTail ? (double)s.mass[tid] * 0x1p-42 * pow2_eighth(-tid) : 0.0);
   s.cc[tid + 1] = cs;
   s.cm[tid + 1] = cum;
   if (tid == 0) {
@@ -1464,7 +1509,7 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
   }
   __syncthreads();
   const uint32_t kmax = key_of(m, kMax);
-  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, c8, J, tid, kmax, 0, 0, 0, 0.0, 1, 0, 0};
+  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, c8, rp.t8, J, tid, kmax, 0, 0, 0, 0.0, 1, 0, 0};
   f.answer(rp, s.cc[kBins], f.weight(kmax), row_uniform(o, row), row, o, cut_out);
 }
 
