@@ -229,25 +229,35 @@ SamplePlan sample_plan(const dflash_rows& r) {
     p.total = p.cuts + align256(rows * sizeof(uint64_t));
     return p;
   }
-  // Slots per thread: the most whose grid still has 1024 blocks (four per CU),
-  // so that few rows spread over the GPU and many amortise their bins.
-  for (p.loads = kSampleMaxLoads;; p.loads /= 2) {
+  // Up to about six million tokens every token is listed, so that the one block
+  // that finishes a row needs no other and no row is read twice; beyond, lists
+  // of 8 bytes a token cost more than they save (top-p, 32 x 151936: 56 us
+  // against 90 without; 64 rows: 82 against 80; 512 x 32000: 108 against 78).
+  p.all = r.R * (int64_t)r.V < (INT64_C(3) << 21);
+  if (p.all) {
+    // The finish adds the segments one after another and a segment works its
+    // tokens off so: one, two, four slots a thread take 42, 34, 26 us on one row
+    // of 151936, 17, 16, 22 on 32000 and 14.5, 15, 18 on 8192
+    p.loads = slots <= 4 * kSampleThreads ? 1 : slots <= 16 * kSampleThreads ? 2 : 4;
     p.n_seg = (slots + kSampleThreads * p.loads - 1) / (kSampleThreads * p.loads);
-    if (p.loads == 1 || r.R * p.n_seg >= 1024 || p.n_seg * 2 > kSampleMaxSeg) break;
+  } else {
+    // the most slots a thread whose grid still has 1024 blocks (four per CU), so
+    // that many rows amortise their bins
+    for (p.loads = kSampleMaxLoads;; p.loads /= 2) {
+      p.n_seg = (slots + kSampleThreads * p.loads - 1) / (kSampleThreads * p.loads);
+      if (p.loads == 2 || r.R * p.n_seg >= 1024) break;
+    }
   }
-  // One slot per thread: few rows, and the whole segment is listed, so that
-  // the one block that finishes a row needs no other.  Longer segments list
-  // what ordinary cuts take (top-k of 50, peaked rows).
-  const bool all = p.loads == 1;
-  p.cap = sample_cap(p.loads);
+  // a short list holds what ordinary cuts take (top-k of 50, peaked rows)
+  p.cap = sample_cap(p.loads, p.all);
   p.batch = std::max(1, 4096 / p.n_seg);
-  if (!all) p.batch = std::min<int64_t>(p.batch, 1024);
+  if (!p.all) p.batch = std::min<int64_t>(p.batch, 1024);
   const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);
   p.lists = align256(rows * p.n_seg * sizeof(SamplePart));
   p.cuts = p.lists + align256(rows * p.n_seg * p.cap * sizeof(uint64_t));
   p.asks = p.cuts + align256(rows * sizeof(uint64_t));
-  p.asked = p.asks + (all ? 0 : align256(rows * sizeof(SampleAsk)));
-  p.total = p.asked + (all ? 0 : align256(rows * kSampleAsk * sizeof(uint64_t)));
+  p.asked = p.asks + (p.all ? 0 : align256(rows * sizeof(SampleAsk)));
+  p.total = p.asked + (p.all ? 0 : align256(rows * kSampleAsk * sizeof(uint64_t)));
   return p;
 }
 

@@ -175,7 +175,7 @@ constexpr int kSampleBins = 512;
 constexpr int kSampleMaxSeg = 512;   // blocks per row
 constexpr int kSampleMaxLoads = 8;
 // tokens that a segment of `loads` slots a thread lists
-constexpr int sample_cap(int loads) { return loads == 1 ? kSampleThreads * 4 : loads == 2 ? 256 : 64; }
+constexpr int sample_cap(int loads, bool all) { return all ? kSampleThreads * 4 * loads : loads == 2 ? 256 : 64; }
 constexpr int kSampleAsk = 8192;     // tokens outside the lists that a row can ask for
 // a segment of an fp32 row: kSampleThreads * loads slots
 struct SamplePart {
@@ -225,6 +225,7 @@ struct SamplePlan {
   int n_seg;      // blocks per row
   int seg_slots;  // bf16: slots of a block
   int loads;      // fp32: slots of a thread
+  bool all;       // fp32: every token is listed
   int cap;        // fp32: tokens a block lists
   int64_t batch;  // rows per pass over the workspace
   size_t parts, lists, cuts, asks, asked, total;

@@ -27,8 +27,8 @@
 //     alone: a window of at most 512 tokens; a fuller bin is narrowed by key
 //     ranges first, and tokens of one value share one weight, so that their
 //     crossing is a division.
-// (3) Short segments list all their tokens.  Rows in long ones whose cut or
-//     draw falls outside the lists ask for the bins they need;
+// (3) Of few tokens all are listed.  Else rows whose cut or draw falls outside
+//     the lists ask for the bins they need;
 //     sample_gather_kernel collects those from all segments at once, and
 //     the row is finished by a second run of (2).
 // A bf16 row with values out of the counters' range goes the second way, in
@@ -254,11 +254,11 @@ constexpr int kCellCount = 51;
 constexpr unsigned long long kCellLess = 15ull << 38;  // 15/16 in units of 2^-42
 static_assert(kThreads / kCols * kSampleMaxLoads * 4 <= 4096, "");
 
-template <int NL>
+template <int NL, bool ALL>
 struct HistLds {
   unsigned long long cell[kBins * kCols];
   uint32_t next[kBins];                                 // the list's next place for each bin
-  uint16_t pick[kWaves][NL == 1 ? 1 : sample_cap(NL)];  // a wave's slots with tokens to be listed
+  uint16_t pick[kWaves][ALL ? 1 : sample_cap(NL, false)];  // a wave's slots with tokens to be listed
   Red red;
 };
 
@@ -275,12 +275,12 @@ __device__ __forceinline__ void list_token(uint32_t* next, uint64_t* list, doubl
   list[atomicAdd(&next[b], 1u)] = c;
 }
 
-template <int NL>
+template <int NL, bool ALL>
 __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
                                                                SamplePart* __restrict__ parts, uint64_t* __restrict__ lists) {
   constexpr int VE = RowType<DFLASH_F32>::VE;
   constexpr float kMax = RowType<DFLASH_F32>::kMax;
-  __shared__ HistLds<NL> s;
+  __shared__ HistLds<NL, ALL> s;
   BlockOps ops(s.red);
   const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
   const int64_t row = row0 + blockIdx.x / n_seg;
@@ -375,12 +375,14 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
   if (listed == 0) return;
   uint64_t* list = lists + (size_t)blockIdx.x * cap;
   const int first = seg * (kThreads * NL) * VE;
-  if constexpr (NL == 1) {  // cap holds the whole segment
+  if constexpr (ALL) {  // cap holds the whole segment
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float v = slot_value<DFLASH_F32>(x[0], i);
-      if (v > kNegInf) list_token(s.next, list, c8, J, comp_of(key_of(v, kMax), (uint32_t)(first + tid * VE + i)));
-    }
+    for (int l = 0; l < NL; ++l)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float v = slot_value<DFLASH_F32>(x[l], i);
+        if (v > kNegInf) list_token(s.next, list, c8, J, comp_of(key_of(v, kMax), (uint32_t)(first + (tid + l * kThreads) * VE + i)));
+      }
   } else {
     // few tokens: a wave picks the slots that hold one, then reads them again,
     // four lanes a slot
@@ -392,12 +394,12 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
       const uint64_t hits = __ballot(most[l] >= least);
       if (hits) {
         const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(hits >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hits, 0));
-        if (most[l] >= least && at < sample_cap(NL)) pick[at] = (uint16_t)(tid + l * kThreads);
+        if (most[l] >= least && at < sample_cap(NL, false)) pick[at] = (uint16_t)(tid + l * kThreads);
         n += __popcll(hits);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    n = min(n, sample_cap(NL));
+    n = min(n, sample_cap(NL, false));
     for (int i = lane_id(); i < n * VE; i += kWave) {
       const int slot = pick[i / VE];
       const Slot y = z.load(seg * (kThreads * NL) + slot);
@@ -474,7 +476,7 @@ struct Finalize {
   template <class F>
   __device__ __forceinline__ void each(int B0, int B1, F f) {
     if (MODE != kSelf && (MODE == kAll || B1 < listed)) {
-      // a segment's list is in the order of its bins, so its part is one run; 16 threads a segment
+      // a segment's list is in the order of its bins, so its part is one run
       __syncthreads();
       if (tid < n_seg) {
         const int l0 = B0 - s.shift[tid], l1 = B1 - s.shift[tid], nb = s.nb[tid];
@@ -484,11 +486,12 @@ struct Finalize {
         s.to[tid] = B1 == kTail || l1 >= nb ? n_all : l1 < 0 ? 0u : upto[l1];  // the last bin: all that is left
       }
       __syncthreads();
-      for (int g = tid >> 4; g < n_seg; g += kThreads / 16) {
+      const int per = n_seg <= 16 ? 5 : 4;  // log2 of the threads a segment
+      for (int g = tid >> per; g < n_seg; g += kThreads >> per) {
         const uint64_t* list = lists + (size_t)g * cap;
         const int end = (int)s.to[g];
 #pragma unroll 4
-        for (int j = (int)s.from[g] + (tid & 15); j < end; j += 16) f(list[j]);
+        for (int j = (int)s.from[g] + (tid & ((1 << per) - 1)); j < end; j += 1 << per) f(list[j]);
       }
     } else if constexpr (MODE == kSecond || MODE == kSelf) {
       if (MODE == kSecond && ask->kind == kSampleAskBins && ((B0 >= ask->b0[0] && B1 <= ask->b1[0]) || (B0 >= ask->b0[1] && B1 <= ask->b1[1]))) {
@@ -1587,7 +1590,7 @@ hipError_t run_bf16(const SampleArgs& a, const SampleOut& o, char* ws, const Sam
   return hipSuccess;
 }
 
-template <int NL>
+template <int NL, bool ALL>
 hipError_t run_f32(const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl, hipStream_t st) {
   SamplePart* parts = reinterpret_cast<SamplePart*>(ws + pl.parts);
   uint64_t* lists = reinterpret_cast<uint64_t*>(ws + pl.lists);
@@ -1598,8 +1601,8 @@ hipError_t run_f32(const SampleArgs& a, const SampleOut& o, char* ws, const Samp
   for (int64_t r0 = 0; r0 < a.R; r0 += pl.batch) {
     const unsigned nr = (unsigned)(a.R - r0 < pl.batch ? a.R - r0 : pl.batch);
     const dim3 rows(nr), segs(nr * (unsigned)pl.n_seg);
-    launch(sample_hist_kernel<NL>, segs, block, st, a, r0, pl.n_seg, pl.cap, parts, lists);
-    if constexpr (NL == 1) {
+    launch(sample_hist_kernel<NL, ALL>, segs, block, st, a, r0, pl.n_seg, pl.cap, parts, lists);
+    if constexpr (ALL) {
       launch(sample_finalize_kernel<kAll>, rows, block, st, a, r0, pl.n_seg, pl.cap, (const SamplePart*)parts,
              (const uint64_t*)lists, asks, (const uint64_t*)asked, o, cuts);
     } else {
@@ -1622,10 +1625,10 @@ hipError_t launch_sample(int32_t dtype, const SampleArgs& a, const SampleOut& o,
                          hipStream_t st) {
   if (dtype == DFLASH_BF16) return run_bf16(a, o, ws, pl, st);
   switch (pl.loads) {
-    case 1: return run_f32<1>(a, o, ws, pl, st);
-    case 2: return run_f32<2>(a, o, ws, pl, st);
-    case 4: return run_f32<4>(a, o, ws, pl, st);
-    default: return run_f32<8>(a, o, ws, pl, st);
+    case 1: return run_f32<1, true>(a, o, ws, pl, st);
+    case 2: return pl.all ? run_f32<2, true>(a, o, ws, pl, st) : run_f32<2, false>(a, o, ws, pl, st);
+    case 4: return pl.all ? run_f32<4, true>(a, o, ws, pl, st) : run_f32<4, false>(a, o, ws, pl, st);
+    default: return run_f32<8, false>(a, o, ws, pl, st);
   }
 }
 

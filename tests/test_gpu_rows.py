@@ -210,7 +210,7 @@ def test_sample_longest_vocabulary():
 
 
 @pytest.mark.parametrize("kind", ["flat", "peaked", "ties", "masked", "shifted"])
-@pytest.mark.parametrize("R,V", [(260, 16003), (520, 15998), (1030, 5003), (345, 40009)])
+@pytest.mark.parametrize("R,V", [(260, 16003), (420, 16003), (520, 15998), (1030, 5003), (1300, 5003), (345, 40009)])
 def test_sample_f32_rows_in_long_segments(kind, R, V):
     # many fp32 rows: segments of 2, 4 and 8 slots a thread list only their
     # largest tokens, and deep cuts ask for more
@@ -225,7 +225,7 @@ def test_filter_f32_rows_in_long_segments():
     import torch
     import block_draft_select_amd as dfl
     rng = np.random.default_rng(41)
-    for R, V, kind in ((260, 16003, "ties"), (1030, 5003, "flat"), (520, 15998, "peaked")):
+    for R, V, kind in ((420, 16003, "ties"), (1300, 5003, "flat"), (520, 15998, "peaked")):
         z = _logits(rng, R, V, kind)
         st = [MIX[i % len(MIX)] for i in range(R)]
         v, _ = _tensor(z, torch.float32)
