@@ -217,9 +217,10 @@ SamplePlan sample_plan(const dflash_rows& r) {
   if (r.dtype == DFLASH_BF16) {
     // A block costs its counters (12 KB written, read again and scanned) beside
     // its slots: the longest segments that still give four blocks per CU,
-    // but no shorter ones than four slots a thread.
+    // but none shorter than four slots a thread (which the search for a token's
+    // index reads at once).
     const int least = (slots + kSampleMaxSegSlots - 1) / kSampleMaxSegSlots;
-    const int most = std::max(least, slots / (4 * kSampleThreads));
+    const int most = std::max(least, (slots + 4 * kSampleThreads - 1) / (4 * kSampleThreads));
     p.n_seg = (int)std::min<int64_t>(std::max<int64_t>(least, (1024 + r.R - 1) / std::max<int64_t>(r.R, 1)), most);
     p.n_seg = std::min(std::max(p.n_seg, 1), kSampleMaxSeg);
     p.seg_slots = (slots + p.n_seg - 1) / p.n_seg;

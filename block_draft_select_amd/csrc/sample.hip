@@ -121,12 +121,16 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
 
 // ---------------------------------------------------------------- block helpers (kThreads threads)
 
-// inclusive prefix sum over the 64 lanes
-__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
+// inclusive prefix sums, over the 16 lanes of a row and over all 64
+__device__ __forceinline__ uint32_t row16_scan_u32(uint32_t v) {
   v += dpp_u32<kDppRowShr1>(v, 0u);
   v += dpp_u32<kDppRowShr2>(v, 0u);
   v += dpp_u32<kDppRowShr4>(v, 0u);
   v += dpp_u32<kDppRowShr8>(v, 0u);
+  return v;
+}
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
+  v = row16_scan_u32(v);
   v += dpp_u32<kDppRowBcast15, 0xA>(v, 0u);
   v += dpp_u32<kDppRowBcast31, 0xC>(v, 0u);
   return v;
@@ -957,22 +961,19 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, i
 // largest logit lies over it, or that has logits under it which still weigh
 // (within 512 eighths of an octave of the largest), is not counted but binned.
 constexpr int kMags = 2944;
-constexpr int kMid = kMags + 1, kLow = 2 * kMags + 2, kItems = kLow + 1;
-constexpr int kGroups = (kItems + 63) / 64;  // groups of 64 items
-static_assert(kGroups * 64 <= kSampleItems && kGroups <= kThreads, "");
+constexpr int kMid = kMags + 1, kLow = 2 * kMags + 2;
 
-// A segment's counters in memory: for either sign kSide by magnitude (0: nearer
-// to zero, kMags + 1: over the range), then the tokens under the range.  In
-// memory the two near zero hold the listed tokens and the zeros.
-constexpr int kSide = kMags + 2, kUnder = 2 * kSide;
-static_assert(kUnder % 4 == 0 && kUnder + 2 <= kSampleItems, "");
-__device__ __forceinline__ int item_of(int counter) {  // -1: none, or part of kMid
-  const int q = counter < kSide ? counter : counter - kSide;
-  if (counter >= kUnder) return counter == kUnder ? kLow : -1;
-  if (q == 0) return -1;
-  return counter < kSide ? kMags + 1 - q : q <= kMags ? kMid + q : -1;
-}
-__device__ __forceinline__ int counter_of(int item) { return item < kMid ? kMags + 1 - item : kSide + item - kMid; }
+// A segment's counters: for either sign kSide by magnitude (0: nearer to zero,
+// kMags + 1: over the range), then the tokens under the range.  In memory the
+// two near zero hold the listed tokens and the zeros, and added up for a row
+// the first of them holds both.
+constexpr int kSide = (kMags + 2 + 3) / 4 * 4, kUnder = 2 * kSide;
+static_assert(kUnder + 4 <= kSampleItems, "");
+__device__ __forceinline__ int counter_of(int item) { return item <= kMid ? kMid - item : kSide + item - kMid; }
+
+// The finish adds up the items in runs, one a thread
+constexpr int kRun = 12;
+static_assert(kLow < kRun * kThreads && kRun <= 16, "");
 
 // smallest magnitude (bit pattern) with a counter of its own
 __device__ __forceinline__ uint32_t value_base(double c8) {
@@ -1074,14 +1075,13 @@ __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, i
 }
 
 struct ValLds {
-  uint32_t c[kGroups * 64];  // tokens of each item
-  uint32_t gc[kGroups + 1];  // tokens before each group of 64 items
-  double gm[kGroups + 1];    // and their weight
-  uint64_t win[kThreads];    // the tokens near zero, sorted; the zeros are one entry
-  uint32_t ncum[kThreads];   // their running count
-  double wcum[kThreads];     // and weight
+  __align__(16) uint32_t c[kSampleItems];  // the row's counters
+  uint32_t rc[kThreads + 1];  // tokens before each run
+  double rm[kThreads + 1];    // and their weight
+  uint64_t win[kThreads];     // the tokens near zero, sorted; the zeros are one entry
+  uint32_t ncum[kThreads];    // their running count
+  double wcum[kThreads];      // and weight
   Red red;
-  uint32_t near[2];
   uint32_t n;
   uint32_t idx;
 };
@@ -1130,21 +1130,8 @@ struct Values {
   }
   __device__ __forceinline__ double near_value(uint32_t i) const { return key_value(comp_key(s.win[i])); }
 
-  __device__ __forceinline__ uint32_t tokens(int g) const {
-    const int item = g * 64 + lane_id();
-    return item >= 1 && item < kLow ? s.c[item] : 0u;
-  }
-  // group g on a wave: this lane's item, its tokens, the weight of one of
-  // them (of all for kMid) and the running count and sum inside the group
-  __device__ __forceinline__ void group(int g, uint32_t& n, double& w, uint32_t& upto, double& cum) const {
-    const int item = g * 64 + lane_id();
-    n = tokens(g);
-    w = n && item != kMid ? weight((double)value(item)) : 0.0;
-    double all = (double)n * w;
-    if (item == kMid && n) all = w = s.wcum[n_mid - 1];
-    upto = wave_scan_u32(n);
-    cum = wave_scan_f64(all);
-  }
+  // tokens of an item
+  __device__ __forceinline__ uint32_t tokens(int item) const { return s.c[counter_of(item)]; }
 
   __device__ __forceinline__ ValueCross locate(int kind, double amount) {
     // a sum within 2^-44 of the value counts as equal to it: rows of equal
@@ -1152,45 +1139,44 @@ struct Values {
     if (kind == kByMassGe) amount *= 1.0 - 0x1p-44;
     if (kind == kByMassGt) amount *= 1.0 + 0x1p-44;
     bool hit = false;
-    if (tid < kGroups) {
-      const bool some = s.gc[tid + 1] != s.gc[tid];
-      if (kind == kByCount) hit = (double)s.gc[tid + 1] >= amount;
-      else if (kind == kByMassGe) hit = some && s.gm[tid + 1] >= amount;
-      else if (kind == kByMassGt) hit = some && s.gm[tid + 1] > amount;
-      else {  // the group's last value passes or not, present or not
-        const int item = min(tid * 64 + 63, kLow - 1);
+    if (tid <= kLow / kRun) {
+      const bool some = s.rc[tid + 1] != s.rc[tid];
+      if (kind == kByCount) hit = (double)s.rc[tid + 1] >= amount;
+      else if (kind == kByMassGe) hit = some && s.rm[tid + 1] >= amount;
+      else if (kind == kByMassGt) hit = some && s.rm[tid + 1] > amount;
+      else {  // the run's last value passes or not, present or not
+        const int item = min(tid * kRun + kRun - 1, kLow - 1);
         hit = weight(item == kMid ? (n_mid ? near_value(n_mid - 1) : 0.0) : (double)value(item)) < amount;
       }
     }
     int g = ops.first(hit);
-    const bool none = g >= kGroups;
+    const bool none = g >= kThreads;
     if (none) {
-      if (kind == kByWeight) return ValueCross{n_in, s.gm[kGroups], -1, 0, 0};
-      g = ops.first(tid < kGroups && s.gc[tid + 1] >= n_in);  // rounding left the sum short: the last token
+      if (kind == kByWeight) return ValueCross{n_in, s.rm[kThreads], -1, 0, 0};
+      g = ops.first(s.rc[tid + 1] >= n_in);  // rounding left the sum short: the last token
     }
-    // every wave works the group out for itself
-    const int lane = lane_id(), item = g * 64 + lane;
-    const uint32_t n0 = s.gc[g];
-    const double m0 = s.gm[g];
-    uint32_t c, upto;
-    double w, cum;
-    group(g, c, w, upto, cum);
-    const uint32_t in_group = s.gc[g + 1] - n0;
+    // every wave works the run out for itself, an item a lane
+    const int lane = lane_id(), item = g * kRun + lane;
+    const uint32_t n0 = s.rc[g], in_run = s.rc[g + 1] - n0;
+    const double m0 = s.rm[g];
+    const bool own = lane < kRun && item < kLow;
+    const uint32_t c = own ? tokens(item) : 0u;
+    const double w = item != kMid ? weight((double)value(item)) : weight(n_mid ? near_value(n_mid - 1) : 0.0);
+    const uint32_t upto = row16_scan_u32(c);
+    const double cum = row16_scan_f64(c ? (item != kMid ? (double)c * w : s.wcum[n_mid - 1]) : 0.0);
     bool cross;
     if (kind == kByWeight) {
-      cross = item >= 1 && item < kLow &&
-              (item == kMid ? (n_mid ? weight(near_value(n_mid - 1)) : weight(0.0)) : weight((double)value(item))) < amount;
+      cross = own && item > 0 && w < amount;
     } else {
-      const bool last = upto == in_group;
+      const bool last = upto == in_run;
       cross = c != 0 && (none ? last
                          : kind == kByCount    ? (double)(n0 + upto) >= amount
                          : kind == kByMassGe ? m0 + cum >= amount || last
                                              : m0 + cum > amount || last);
     }
-    const int l = min(first_lane(cross), 63);
-    const uint32_t lc = __shfl(c, l), n1 = n0 + __shfl(upto, l) - lc;  // before the item
-    const double lw = __shfl(w, l), before = m0 + (l > 0 ? __shfl(cum, max(l - 1, 0)) : 0.0);
-    const int li = g * 64 + l;
+    const int l = min(first_lane(cross), kRun - 1), li = g * kRun + l;
+    const uint32_t lc = __builtin_amdgcn_readlane(c, l), n1 = n0 + __builtin_amdgcn_readlane(upto, l) - lc;  // before the item
+    const double lw = readlane_f64(w, l), before = m0 + (l > 0 ? readlane_f64(cum, max(l - 1, 0)) : 0.0);
     if (li == kMid && lc) {  // among the entries near zero
       const bool h = tid < n_mid && (kind == kByCount    ? (double)(n1 + s.ncum[tid]) >= amount
                                      : kind == kByMassGe ? before + s.wcum[tid] >= amount
@@ -1274,52 +1260,49 @@ struct Values {
 // one bf16 row from its segments' counts; false if the row has to be binned
 __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, int64_t row, int n_seg, int seg_slots,
                                                 const SampleValues* __restrict__ part, const SampleOut& o, uint64_t* cut_out) {
-  constexpr int VE = 8, kPairs = kUnder / 2 + 1, kMine = (kPairs + kThreads - 1) / kThreads;
+  constexpr int VE = 8, kMine = kSampleItems / 4 / kThreads;
+  static_assert(kSampleItems == kMine * 4 * kThreads, "");
   BlockOps ops(s.red);
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x;
   const RowParams rp = row_params(a, row);
   const double c8 = rp.c8, u = row_uniform(o, row);
   const uint32_t base = value_base(c8);
-  // the segments' counts
-  uint32_t c0[kMine], c1[kMine];
+  // the segments' counts, four counters a thread at a time (what lies behind
+  // the last counter is not used)
+  uint4 c[kMine];
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) c0[j] = c1[j] = 0;
-#pragma unroll 4
+  for (int j = 0; j < kMine; ++j) c[j] = make_uint4(0, 0, 0, 0);
+#pragma unroll 8
   for (int g = 0; g < n_seg; ++g) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(part[g].counts);
+    const uint2* p = reinterpret_cast<const uint2*>(part[g].counts);
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
-      const int i = tid + j * kThreads;
-      const uint32_t v = i < kPairs ? p[i] : 0u;
-      c0[j] += v & 0xFFFFu;
-      c1[j] += v >> 16;
+      const uint2 v = p[tid + j * kThreads];
+      c[j].x += v.x & 0xFFFFu;
+      c[j].y += v.x >> 16;
+      c[j].z += v.y & 0xFFFFu;
+      c[j].w += v.y >> 16;
     }
   }
-  int top = kItems;  // the first item with a token: the row's largest
+  int top = kLow;  // the first item with a token: the row's largest
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
-    const int i = tid + j * kThreads;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int item = item_of(2 * i + h);
-      const uint32_t c = h ? c1[j] : c0[j];
-      if (i < kPairs && item >= 0) {
-        s.c[item] = c;
-        if (c && item > 0 && item < kLow) top = min(top, item);
-      }
+    const int q = 4 * (tid + j * kThreads);
+    reinterpret_cast<uint4*>(s.c)[tid + j * kThreads] = c[j];
+    if (q < kUnder) {
+      const int sign = q < kSide ? -1 : 1, item = q < kSide ? kMid - q : kMid + q - kSide;
+      top = min(top, c[j].x ? item : kLow);
+      top = min(top, c[j].y ? item + sign : kLow);
+      top = min(top, c[j].z ? item + 2 * sign : kLow);
+      top = min(top, c[j].w ? item + 3 * sign : kLow);
     }
   }
-  if (tid == 0) s.near[0] = c0[0];                                           // counter 0: listed tokens
-  if (tid == (kSide / 2) % kThreads) s.near[1] = c0[kSide / 2 / kThreads];  // counter kSide: zeros
-  static_assert(kSide % 2 == 0, "");
-  if (tid < kGroups * 64 - kItems) s.c[kItems + tid] = 0;
   if (tid == 0) s.n = 0;
+  top = kLow - (int)ops.max((uint32_t)(kLow - top));
+  const uint32_t n_near = s.c[0], n_zero = s.c[kSide], n_low = s.c[kUnder], n_over = s.c[kMags + 1];
+  const uint32_t n_mid = n_near + (n_zero != 0);  // entries
   __syncthreads();
-  if (tid == 0) s.c[kMid] = s.near[0] + s.near[1];
-  if (s.near[0] + s.near[1]) top = min(top, kMid);
-  __syncthreads();
-  const uint32_t n_over = s.c[0], n_low = s.c[kLow], n_zero = s.near[1];
-  const uint32_t n_mid = s.near[0] + (n_zero != 0);  // entries
+  if (tid == 0) s.c[0] = n_near + n_zero;
   if (n_over || n_mid > (uint32_t)kThreads) return false;
   if (n_mid) {
     // from the segments' lists; too many in one segment: not listed
@@ -1351,8 +1334,7 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
     __syncthreads();
   }
   Values f{s, ops, RowRef<DFLASH_BF16>(a.Z, row, a.stride, a.V), part, n_seg, seg_slots, tid, c8 * 0.125, base, 0.0, (int)n_mid, 0};
-  top = kItems - (int)ops.max((uint32_t)(kItems - top));
-  if (top >= kItems) {
+  if (top >= kLow) {
     if (n_low) return false;
     empty_row(row, o, cut_out);
     return true;
@@ -1369,42 +1351,32 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
     }
     __syncthreads();
   }
-  // each group's tokens and weight, two groups at a time, then before each group
-#pragma unroll 1
-  for (int g = wave; g < kGroups; g += 2 * kWaves) {
-    const int g1 = g + kWaves;  // past the last group: no items
-    uint32_t c, upto[2] = {0, 0};
-    double w, cum[2] = {0.0, 0.0};
-    if (__ballot(f.tokens(g) != 0 || f.tokens(g1) != 0)) {
-      f.group(g, c, w, upto[0], cum[0]);
-      f.group(g1, c, w, upto[1], cum[1]);
+  // each run's tokens and weight, then before each run
+  uint32_t n = 0;
+  double sum = 0.0;
+  if (tid <= kLow / kRun) {
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const int item = tid * kRun + k;
+      const uint32_t c = f.tokens(item);
+      double all = (double)c * f.weight((double)f.value(item));
+      if (k == kMid % kRun && item == kMid && n_mid) all = s.wcum[n_mid - 1];
+      n += c;
+      sum += c ? all : 0.0;  // the weight of a value over the row's largest may be infinite
     }
-    if (lane == 63) {
-      s.gc[g + 1] = upto[0];
-      s.gm[g + 1] = cum[0];
-      if (g1 < kGroups) {
-        s.gc[g1 + 1] = upto[1];
-        s.gm[g1 + 1] = cum[1];
-      }
-    }
+  }
+  n = ops.scan(n);
+  sum = ops.scan(sum);
+  s.rc[tid + 1] = n;
+  s.rm[tid + 1] = sum;
+  if (tid == 0) {
+    s.rc[0] = 0;
+    s.rm[0] = 0.0;
   }
   __syncthreads();
-  {
-    const uint32_t gc = ops.scan(tid < kGroups ? s.gc[tid + 1] : 0u);
-    const double gm = ops.scan(tid < kGroups ? s.gm[tid + 1] : 0.0);
-    if (tid < kGroups) {
-      s.gc[tid + 1] = gc;
-      s.gm[tid + 1] = gm;
-    }
-    if (tid == 0) {
-      s.gc[0] = 0;
-      s.gm[0] = 0.0;
-    }
-    __syncthreads();
-  }
-  const uint32_t n_in = s.gc[kGroups], N = n_in + n_low;
+  const uint32_t n_in = s.rc[kThreads], N = n_in + n_low;
   f.n_in = n_in;
-  const double total = s.gm[kGroups];
+  const double total = s.rm[kThreads];
 
   uint32_t kept = N;
   double Z = total;
