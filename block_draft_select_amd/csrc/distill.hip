@@ -33,6 +33,11 @@ constexpr int kWaves = kThreads / kWave;
 constexpr double kLog2e64 = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
 
+// Where |x_j| log2 e reaches this, fp64 no longer holds lse beside x_j: a row
+// that lies below (all of it the type's lowest value) is empty, a logit above
+// counts as +inf
+constexpr double kRange = 0x1p40;
+
 // The forward pass sums 2^t, t = (x - m) log2 e, in fp64 for every logit, so its
 // time is that of the instructions a term takes (16; fp64 and fp32 issue
 // alike here).  With n = floor(512 t) and g the rest,
@@ -250,9 +255,9 @@ __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, in
     }
     bool odd;
     const float m = wave_max_dpp_f32(largest<DT>(x, odd));
-    any_odd |= __ballot(odd) != 0;
     const double Mu = rint((double)m * c);
-    if (Mu > M && Mu < INFINITY) {
+    any_odd |= __ballot(odd) != 0 || Mu >= kRange;
+    if (Mu > M && fabs(Mu) < kRange) {
       s = M > -INFINITY ? ldexp(s, (int)fmax(M - Mu, -4000.0)) : 0.0;
       M = Mu;
     }
@@ -346,8 +351,8 @@ __global__ __launch_bounds__(T) void distill_loss_kernel(DistillArgs a, int n_se
       }
     }
     lm = block_max<T>(red, lm);
-    if (lm > -INFINITY) {
-      const double LM = rint(lm * c2);
+    const double LM = rint(lm * c2);
+    if (LM > -kRange) {
       double ls = 0.0;
       for (int k = tid; k < a.K; k += T) {
         const int idx = seen[k];
@@ -355,7 +360,7 @@ __global__ __launch_bounds__(T) void distill_loss_kernel(DistillArgs a, int n_se
         for (int q = 0; q < k && first; ++q) first = seen[q] != idx;
         if (first) {
           const float v = row_value<DT>(z, idx);
-          if (v != kNegInf) ls += v < INFINITY ? exp2(fma((double)v, c2, -LM)) : (double)NAN;
+          if (v != kNegInf) ls += LM < kRange ? exp2(fma((double)v, c2, -LM)) : (double)NAN;
         }
       }
       ls = block_sum<T>(red, ls);

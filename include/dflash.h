@@ -444,7 +444,7 @@ dflash_status dflash_filter(const dflash_rows* r, const void* Z, const dflash_fi
  *     p_rest = max(0, 1 - sum_k p_k), lse_rest the unlisted tokens'
  *     log-sum-exp (the term is left out if none of them is unmasked).
  *   S        [R, V] student logits;  K in 0..DFLASH_DISTILL_K_MAX
- *   tau      HOST value, finite, > 0
+ *   tau      HOST value in [1e-30, 1e30]
  *   t_idx    [R, K] int32 token ids; an id outside [0, V) is padding and
  *            counts for nothing; a repeated id's entries add up
  *   t_logit  [R, K] float (-inf: probability 0)
@@ -457,7 +457,9 @@ dflash_status dflash_filter(const dflash_rows* r, const void* Z, const dflash_fi
  * 0 in all outputs.  A row in which no listed token has mass (and t_lse is
  * absent or not finite), or no student logit is unmasked, has D = 0.  NaN or
  * +inf logits make the row's outputs NaN; a masked student token with p > 0
- * makes D +inf. */
+ * makes D +inf.  x_j beyond 2^40 ln 2 are out of fp64's reach: a row whose
+ * largest x_j lies below -2^40 ln 2 (every logit the type's lowest value) has
+ * nothing unmasked, and an x_j above 2^40 ln 2 counts as +inf. */
 dflash_status dflash_distill(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
                              const float* t_logit, const double* t_lse_opt, const float* weight_opt, float* loss_opt,
                              double* lse, double* lse_rest_opt, void* ws, size_t ws_bytes, void* stream);

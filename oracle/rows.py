@@ -61,11 +61,18 @@ def filtered(z, fill, **filters):
     return out
 
 
+RANGE = 2.0 ** 40 * np.log(2.0)  # beyond it float64 does not hold a log-sum-exp beside its largest term
+
+
 def log_sum_exp(x):
     x = np.asarray(x, dtype=np.float64)
     if x.size == 0:
         return -np.inf
     m = x.max()
+    if m <= -RANGE:
+        return -np.inf
+    if m >= RANGE:
+        return np.nan
     if not np.isfinite(m):
         return -np.inf if m == -np.inf else np.nan
     return float(m + np.log(np.exp(x - m).sum()))

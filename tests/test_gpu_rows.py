@@ -488,6 +488,95 @@ def test_distill_masked_and_empty_rows(with_lse):
         _check_distill(s, idx, tl, t, 1.0, lse, None, None)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_of_the_types_lowest_value(dt):
+    # a mask of finite lowest values that leaves nothing, some, or only listed
+    # tokens; and logits beyond fp64's reach on the other side
+    import torch
+    t = dict(bf16=torch.bfloat16, f32=torch.float32)[dt]
+    low = float(torch.finfo(t).min)
+    rng = np.random.default_rng(61)
+    V = 20005
+    s = np.full((6, V), low, dtype=np.float32)
+    idx = np.tile(np.array([[3, 19000, 7]], dtype=np.int32), (6, 1))
+    tl = np.ones((6, 3), dtype=np.float32)
+    s[1, 100:200] = rng.normal(size=100)      # only unlisted tokens remain (the listed ones are unlikely beyond fp32)
+    s[2, [3, 19000, 7]] = rng.normal(size=3)  # only listed ones
+    s[3] = rng.normal(size=V)
+    s[3, ::2] = low
+    s[3, [3, 19000, 7]] = rng.normal(size=3)
+    s[4, 20004] = 0.5
+    _say(f"[rows] lowest values {dt}")
+    for with_lse in (False, True):
+        lse = np.full(6, 2.5) if with_lse else None
+        keep = [0, 2, 3, 5]
+        _check_distill(s[keep], idx[keep], tl[keep], t, 0.8, None if lse is None else lse[keep], None, None)
+    z = s.copy()
+    z[5] = low
+    st = [dict(top_p=0.5), dict(), dict(top_k=2), dict(min_p=0.1), dict(), dict(top_k=7, T=0.01)]
+    _check_sample(z, t, st, rng.random(6))
+    import block_draft_select_amd as dfl
+    big = np.full((1, 3000), -1.0, dtype=np.float32)
+    big[0, 5] = 3e38
+    v, _ = _tensor(big, t)
+    lse = torch.zeros(1, dtype=torch.float64, device="cuda")
+    r = dfl.rows(v)
+    dfl.dflash_distill(r, v, None, None, None, lse, dfl.rows_workspace(r))
+    assert torch.isnan(lse).all()
+
+
+def test_rows_past_32_bit_offsets():
+    # two rows 2^31 elements apart
+    import torch
+    import block_draft_select_amd as dfl
+    rng = np.random.default_rng(62)
+    V, stride = 4999, 2 ** 31 + 3
+    flat = torch.empty(stride + V + 8, dtype=torch.bfloat16, device="cuda")
+    v = flat.as_strided((2, V), (stride, 1), 1)
+    z = _logits(rng, 2, V, "peaked")
+    v.copy_(torch.from_numpy(z))
+    zz = _f64(v)
+    r = dfl.rows(v)
+    assert r.stride == stride
+    ws = dfl.rows_workspace(r)
+    u = torch.rand(2, dtype=torch.float64, device="cuda")
+    token = torch.empty(2, dtype=torch.int32, device="cuda")
+    p = _arr([0.9, 0.9], torch.float32)
+    dfl.dflash_sample(r, v, u, token, ws, top_p=p)
+    for i in range(2):
+        assert int(token[i]) == O.sample(zz[i], float(u[i]), top_p=float(np.float32(0.9)))[0]
+    idx = torch.from_numpy(np.argsort(-zz, axis=1)[:, :8].astype(np.int32)).cuda()
+    tl = torch.gather(v.float(), 1, idx.long())
+    loss, lse, _, dS = _run_distill(v, idx, tl, 1.0, None, None, None, flat.as_strided((2, V), (stride, 1), 1))
+    for i in range(2):
+        ref = O.distill(zz[i], idx[i].cpu().numpy(), tl[i].cpu().numpy())
+        assert abs(float(lse[i]) - ref["lse"]) <= 2e-11 + 1e-13
+        err = np.abs(_f64(dS)[i] - ref["grad"])
+        assert (err <= _grad_tol(ref, zz[i], 1.0, 1.0, torch.bfloat16)).all()
+    v.copy_(torch.from_numpy(z))
+    dfl.dflash_filter(r, v, v, ws, top_p=p)
+    got = _f64(v)
+    for i in range(2):
+        assert np.array_equal(got[i], O.filtered(zz[i], torch.finfo(torch.bfloat16).min, top_p=float(np.float32(0.9))))
+
+
+def test_settings_and_outputs_left_out():
+    import torch
+    import block_draft_select_amd as dfl
+    rng = np.random.default_rng(63)
+    for t in (torch.bfloat16, torch.float32):
+        z = _logits(rng, 5, 3000, "peaked")
+        v, _ = _tensor(z, t)
+        zz, u = _f64(v), rng.random(5)
+        r = dfl.rows(v)
+        token = torch.empty(5, dtype=torch.int32, device="cuda")
+        dfl.dflash_sample(r, v, _arr(list(u), torch.float64), token, dfl.rows_workspace(r))
+        assert [int(x) for x in token] == [O.sample(zz[i], u[i])[0] for i in range(5)]
+        out = torch.empty_like(v)
+        dfl.dflash_filter(r, v, out, dfl.rows_workspace(r))
+        assert np.array_equal(_f64(out), zz)
+
+
 def test_distill_whole_vocabulary_listed():
     # no unlisted token: the rest class is left out
     import torch

@@ -89,3 +89,10 @@ def test_distill_padding_duplicates_and_empty_rows():
         assert e["loss"] == 0 and not e["grad"].any()
     f = R.distill(np.full(4, -np.inf), np.array([1]), np.zeros(1))
     assert f["loss"] == 0 and not f["grad"].any()
+
+
+def test_log_sum_exp_out_of_range():
+    # every logit the type's lowest value: nothing unmasked; far above: no result
+    assert R.log_sum_exp(np.full(5, -3.4e38)) == -np.inf and np.isnan(R.log_sum_exp(np.array([1.0, 3e38])))
+    d = R.distill(np.full(6, -3.4e38), np.array([1, 4]), np.array([0.0, 1.0]))
+    assert d["loss"] == 0 and d["lse"] == -np.inf and not d["grad"].any()
