@@ -211,6 +211,28 @@ static int row_slots(const dflash_rows& r) {
   return (r.V + ve - 1) / ve;
 }
 
+// most rows of this length that are listed in full (fp32)
+static int64_t all_listed_rows(const dflash_rows& r) { return ((INT64_C(3) << 21) - 1) / r.V; }
+
+// fp32 rows
+static SamplePlan sample_layout(const dflash_rows& r, bool all, int loads) {
+  SamplePlan p{};
+  p.all = all;
+  p.loads = loads;
+  p.n_seg = (row_slots(r) + kSampleThreads * loads - 1) / (kSampleThreads * loads);
+  // in full, or what ordinary cuts take (top-k of 50, peaked rows)
+  p.cap = sample_cap(loads, all);
+  p.batch = std::max(1, 4096 / p.n_seg);
+  if (!all) p.batch = std::min<int64_t>(p.batch, 1024);
+  const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);
+  p.lists = align256(rows * p.n_seg * sizeof(SamplePart));
+  p.cuts = p.lists + align256(rows * p.n_seg * p.cap * sizeof(uint64_t));
+  p.asks = p.cuts + align256(rows * sizeof(uint64_t));
+  p.asked = p.asks + (all ? 0 : align256(rows * sizeof(SampleAsk)));
+  p.total = p.asked + (all ? 0 : align256(rows * kSampleAsk * sizeof(uint64_t)));
+  return p;
+}
+
 SamplePlan sample_plan(const dflash_rows& r) {
   SamplePlan p{};
   const int slots = row_slots(r);
@@ -234,32 +256,18 @@ SamplePlan sample_plan(const dflash_rows& r) {
   // that finishes a row needs no other and no row is read twice; beyond, lists
   // of 8 bytes a token cost more than they save (top-p, 32 x 151936: 56 us
   // against 90 without; 64 rows: 82 against 80; 512 x 32000: 108 against 78).
-  p.all = r.R * (int64_t)r.V < (INT64_C(3) << 21);
-  if (p.all) {
+  if (r.R <= all_listed_rows(r)) {
     // The finish adds the segments one after another and a segment works its
     // tokens off so: one, two, four slots a thread take 42, 34, 26 us on one row
     // of 151936, 17, 16, 22 on 32000 and 14.5, 15, 18 on 8192
-    p.loads = slots <= 4 * kSampleThreads ? 1 : slots <= 16 * kSampleThreads ? 2 : 4;
-    p.n_seg = (slots + kSampleThreads * p.loads - 1) / (kSampleThreads * p.loads);
-  } else {
-    // the most slots a thread whose grid still has 1024 blocks (four per CU), so
-    // that many rows amortise their bins
-    for (p.loads = kSampleMaxLoads;; p.loads /= 2) {
-      p.n_seg = (slots + kSampleThreads * p.loads - 1) / (kSampleThreads * p.loads);
-      if (p.loads == 2 || r.R * p.n_seg >= 1024) break;
-    }
+    return sample_layout(r, true, slots <= 4 * kSampleThreads ? 1 : slots <= 16 * kSampleThreads ? 2 : 4);
   }
-  // a short list holds what ordinary cuts take (top-k of 50, peaked rows)
-  p.cap = sample_cap(p.loads, p.all);
-  p.batch = std::max(1, 4096 / p.n_seg);
-  if (!p.all) p.batch = std::min<int64_t>(p.batch, 1024);
-  const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);
-  p.lists = align256(rows * p.n_seg * sizeof(SamplePart));
-  p.cuts = p.lists + align256(rows * p.n_seg * p.cap * sizeof(uint64_t));
-  p.asks = p.cuts + align256(rows * sizeof(uint64_t));
-  p.asked = p.asks + (p.all ? 0 : align256(rows * sizeof(SampleAsk)));
-  p.total = p.asked + (p.all ? 0 : align256(rows * kSampleAsk * sizeof(uint64_t)));
-  return p;
+  // the most slots a thread whose grid still has 1024 blocks (four per CU), so
+  // that many rows amortise their bins
+  for (int loads = kSampleMaxLoads;; loads /= 2) {
+    p = sample_layout(r, false, loads);
+    if (loads == 2 || r.R * p.n_seg >= 1024) return p;
+  }
 }
 
 // The forward pass: 2048 blocks (eight per CU) if the rows have that much, and
@@ -281,6 +289,27 @@ DistillPlan distill_plan(const dflash_rows& r) {
   }
   p.total = align256((size_t)r.R * p.n_seg * sizeof(DistillPart));
   return p;
+}
+
+// Workspace for these rows, or fewer of their length: plans of fewer rows split
+// them further, so this is a bound over all of them that grows with R
+size_t rows_workspace(const dflash_rows& r) {
+  if (r.R == 0) return 0;
+  const int slots = row_slots(r), units = (slots + kDistillUnit - 1) / kDistillUnit;
+  const int64_t least_units = (units + kDistillMaxUnits - 1) / kDistillMaxUnits;
+  size_t total = align256((size_t)std::min(r.R * units, std::max(r.R * least_units, 2048 + r.R)) * sizeof(DistillPart));
+  if (r.dtype == DFLASH_BF16) {
+    const int64_t least = (slots + kSampleMaxSegSlots - 1) / kSampleMaxSegSlots;
+    const int64_t most = std::max<int64_t>(least, (slots + 4 * kSampleThreads - 1) / (4 * kSampleThreads));
+    const int64_t segs = std::min<int64_t>(std::min(r.R * most, std::max(r.R * least, 1024 + r.R)), 4096);
+    return std::max(total, align256(segs * sizeof(SampleValues)) + align256(std::min<int64_t>(r.R, 4096) * sizeof(uint64_t)));
+  }
+  dflash_rows few = r;
+  few.R = std::min(r.R, all_listed_rows(r));
+  if (few.R) total = std::max(total, sample_plan(few).total);
+  if (r.R > few.R)
+    for (int loads = 2; loads <= kSampleMaxLoads; loads *= 2) total = std::max(total, sample_layout(r, false, loads).total);
+  return total;
 }
 
 }  // namespace dfk
@@ -735,7 +764,7 @@ dflash_status dflash_rows_workspace_bytes(const dflash_rows* r, size_t* bytes) {
     g_err.clear();
     if (dflash_status s = check_rows(r)) return s;
     if (!bytes) return fail(DFLASH_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = r->R ? std::max(dfk::sample_plan(*r).total, dfk::distill_plan(*r).total) : 0;
+    *bytes = dfk::rows_workspace(*r);
     return DFLASH_OK;
   } catch (...) {
     return fail(DFLASH_ERR_INVALID_ARG, "internal error");

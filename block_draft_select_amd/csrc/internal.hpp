@@ -231,6 +231,7 @@ struct SamplePlan {
   size_t parts, lists, cuts, asks, asked, total;
 };
 SamplePlan sample_plan(const dflash_rows& r);
+size_t rows_workspace(const dflash_rows& r);
 hipError_t launch_sample(int32_t dtype, const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl,
                          hipStream_t st);
 

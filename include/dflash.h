@@ -379,9 +379,10 @@ typedef struct dflash_rows {
   int32_t dtype;  /* DFLASH_F32 | DFLASH_BF16 */
 } dflash_rows;
 
-/* Bytes of workspace any of the four needs for these rows (host only, pure).
- * The contents need no initialisation; calls that overlap in time, and
- * captured graphs whose replays may, must not share a workspace. */
+/* Bytes of workspace any of the four needs for these rows, or for fewer of the
+ * same V and dtype (host only, pure; grows with R).  The contents need no
+ * initialisation; calls that overlap in time, and captured graphs whose
+ * replays may, must not share a workspace. */
 dflash_status dflash_rows_workspace_bytes(const dflash_rows* r, size_t* bytes);
 
 /* What a request asks of its distribution: DEVICE arrays with one value for

@@ -99,6 +99,22 @@ def test_pointers_and_workspaces(dfl):
     assert need > 16
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("V", [1, 33, 5000, 16384, 32000, 151936, 262144, 2097152])
+def test_a_workspace_serves_fewer_rows_too(dfl, dtype, V):
+    # what a call asks for (its refusal says so) stays within the workspace of
+    # as many rows or more
+    last = 0
+    for R in sorted({1, 2, 3, 7, 8, 31, 41, 42, 64, 100, 128, 195, 196, 341, 342, 512, 513, 1023, 1024, 1025, 2048, 4097}):
+        r = _rows(dfl, R=R, stride=V, V=V, dtype=dtype)
+        status, n = _ws(dfl, r)
+        assert status == 0 and n >= last
+        last = n
+        for call in (_sample, _distill):
+            assert call(dfl, r, n=0) == 3
+            assert int(dfl.lib.dflash_last_error().split(b"need ")[1].split()[0]) <= n, (R, V)
+
+
 @pytest.mark.parametrize("kw", [dict(K=-1), dict(K=1025), dict(tau=0.0), dict(tau=-1.0), dict(tau=float("nan")),
                                 dict(tau=float("inf")), dict(tau=1e-40), dict(t_lse=FAKE), dict(rest=FAKE)])
 def test_bad_distill_arguments(dfl, kw):
