@@ -279,6 +279,10 @@ __device__ __forceinline__ void list_token(uint32_t* next, uint64_t* list, doubl
   list[atomicAdd(&next[b], 1u)] = c;
 }
 
+// Bound by instructions, about twenty a token, eleven of them fp64 (t, its bin,
+// the weight): 256 x 262144 fp32 in 74 us, 3.6 TB/s; without the weight 53,
+// loads and the integer part alone 46; the one atomic a token hides behind them,
+// the list takes 10.
 template <int NL, bool ALL>
 __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
                                                                SamplePart* __restrict__ parts, uint64_t* __restrict__ lists) {
@@ -833,6 +837,9 @@ __device__ __forceinline__ double row_uniform(const SampleOut& o, int64_t row) {
   return u > 0.0 ? fmin(u, 1.0 - 0x1p-53) : 0.0;  // NaN: 0
 }
 
+// One block a row: bound by the latency of its steps (the segments' bins as
+// other blocks left them in memory, then scans, windows and searches).  One row
+// of 151936 fp32 takes 16 us, 256 of 262144 23 and 31 (kFirst and kSecond).
 template <int MODE>
 __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
                                                                    const SamplePart* __restrict__ parts,
@@ -903,6 +910,8 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
 
 // ---------------------------------------------------------------- (3) the tokens that rows asked for
 
+// Reads the rows a second time at the memory's rate (256 x 262144 fp32: 44 us,
+// 6.1 TB/s); rows that asked for nothing are not read.
 template <int NL>
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, int64_t row0, int n_seg, SampleAsk* __restrict__ asks,
                                                                  uint64_t* __restrict__ asked) {
@@ -982,6 +991,11 @@ __device__ __forceinline__ uint32_t value_base(double c8) {
   return min(e << 7, 0x7F80u) - (uint32_t)kMags;
 }
 
+// One LDS atomic a token, two tokens a word formed side by side in 16-bit
+// halves.  512 x 262144 bf16 take 68 us, 3.9 TB/s; the loads alone 53, without
+// the atomics 65, the atomics alone (random addresses) 28: issue slots and LDS
+// share the time.  Not faster: nontemporal loads (81), 8 loads in flight (86
+// against 84 then), 16.
 __global__ __launch_bounds__(kThreads) void sample_values_kernel(SampleArgs a, int64_t row0, int n_seg, int seg_slots,
                                                                  SampleValues* __restrict__ parts) {
   constexpr int VE = 8, U = 4;
@@ -1488,6 +1502,12 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
   f.answer(rp, s.cc[kBins], f.weight(kmax), row_uniform(o, row), row, o, cut_out);
 }
 
+// One row takes 13 us, 512 rows 30: a chain of steps whose latency counts.  Of
+// 29 thousand cycles for a row of 151936 the segments' counters take 9.5, the
+// weights 2.5, scans 3.7, a query 3 to 5 and the token's index 6 (in another
+// block's segment).  Runs of items a thread took the weights there from 11; a
+// separate kernel for rows that have to be binned costs the others a launch (5
+// us).
 __global__ __launch_bounds__(kThreads, 4) void sample_finalize_values_kernel(SampleArgs a, int64_t row0, int n_seg, int seg_slots,
                                                                           const SampleValues* __restrict__ parts, SampleOut o,
                                                                           uint64_t* __restrict__ cuts) {
@@ -1500,6 +1520,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_finalize_values_kernel(Sam
 
 // ---------------------------------------------------------------- the filtered row
 
+// A copy with a comparison: 819 x 262144 bf16 in 138 us, 6.2 TB/s read and written.
 template <int DT, int NL>
 __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, int64_t row0, int n_seg,
                                                                 const uint64_t* __restrict__ cuts, uint32_t fill,

@@ -670,11 +670,12 @@ def test_gradient_against_differences():
 
 # ---------------------------------------------------------------- streams, graphs, the operators together
 
-def test_sample_and_filter_replayed_from_a_graph():
+@pytest.mark.parametrize("dt,V", [("bf16", 50021), ("f32", 50021), ("f32", 400007)])
+def test_sample_and_filter_replayed_from_a_graph(dt, V):
     import torch
     import block_draft_select_amd as dfl
     rng = np.random.default_rng(31)
-    z = torch.from_numpy(_logits(rng, 18, 50021, "peaked")).cuda().to(torch.bfloat16)
+    z = torch.from_numpy(_logits(rng, 18, V, "peaked")).cuda().to(dict(bf16=torch.bfloat16, f32=torch.float32)[dt])
     st = _filters(MIX)
     u = torch.rand(18, dtype=torch.float64, device="cuda")
     r = dfl.rows(z)
@@ -697,7 +698,7 @@ def test_sample_and_filter_replayed_from_a_graph():
         graphs.append(g)
     for rep in range(4):
         # new inputs in place, other eager work between the replays
-        z.copy_(torch.from_numpy(_logits(rng, 18, 50021, "peaked" if rep % 2 else "ties")).cuda())
+        z.copy_(torch.from_numpy(_logits(rng, 18, V, "peaked" if rep % 2 else "ties")).cuda())
         u.copy_(torch.rand(18, dtype=torch.float64, device="cuda"))
         call(0)
         torch.cuda.synchronize()
