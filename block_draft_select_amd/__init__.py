@@ -369,7 +369,7 @@ def _row_tensor(t, name, r, device, stride=None):
         raise ValueError(f"{name} must hold {r.R} rows of {r.V} logits of the rows' dtype")
     if stride is not None and own_R > 1 and own_stride != stride:
         raise ValueError(f"{name} must have the row stride {stride}, got {own_stride}")
-    if t.device != device or not t.is_cuda:
+    if t.get_device() != device.index:
         _on(t, name, device)
     return t.data_ptr(), own_stride
 
@@ -385,7 +385,7 @@ def _vec(t, name, dtype, numel, device, optional=False):
     if t is None and optional:
         return None
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and (numel is None or t.numel() == numel)
-            and t.device == device and t.is_cuda and t.is_contiguous()):
+            and t.get_device() == device.index and t.is_contiguous()):
         return t.data_ptr()
     _ptr(t, name, dtype, numel, optional)  # raises what is wrong with it
     _on(t, name, device)
@@ -395,7 +395,7 @@ def _call(fn, device, stream, *args):
     """Call an entry point on ``stream`` (None: the current stream of the
     tensors' device), with that device current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        stream = torch.cuda.current_stream(device.index)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the rows are on {device}")
     if torch.cuda.current_device() == device.index:
