@@ -171,6 +171,25 @@ struct BlockOps {
     for (int i = 0; i < kWaves - 1; ++i) v += i < w ? s.u[flip][i] : 0u;
     return v;
   }
+  // both, with one barrier
+  __device__ __forceinline__ void scan(uint32_t& n, double& v) {
+    const int w = threadIdx.x >> 6;
+    n = wave_scan_u32(n);
+    v = wave_scan_f64(v);
+    flip ^= 1;
+    if ((threadIdx.x & 63) == 63) {
+      s.u[flip][w] = n;
+      s.d[flip][w] = v;
+    }
+    __syncthreads();
+    double off = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i) {
+      n += i < w ? s.u[flip][i] : 0u;
+      off += i < w ? s.d[flip][i] : 0.0;
+    }
+    v += off;
+  }
   __device__ __forceinline__ double scan(double v) {
     const int w = threadIdx.x >> 6;
     v = wave_scan_f64(v);
@@ -1136,11 +1155,19 @@ struct Values {
   // its nearest integer and the Taylor series of e^(f ln 2), |f| <= 1/2, to
   // degree 12 (truncation below 2e-16)
   __device__ __forceinline__ double weight(double v) const {
-    const double t = fmax(v * c - tm, -1100.0), n = rint(t), x = (t - n) * 0.6931471805599453, x2 = x * x, x4 = x2 * x2;
-    const double p3 = fma(x, 1.0 / 6.0, 0.5), p5 = fma(x, 1.0 / 120.0, 1.0 / 24.0), p7 = fma(x, 1.0 / 5040.0, 1.0 / 720.0),
-                 p9 = fma(x, 1.0 / 362880.0, 1.0 / 40320.0), p11 = fma(x, 1.0 / 39916800.0, 1.0 / 3628800.0);
-    const double hi = fma(x4, fma(x2, 1.0 / 479001600.0, p11), fma(x2, p9, p7)), lo = fma(x2, p5, p3);
-    return ldexp(1.0 + fma(x2, fma(x4, hi, lo), x), (int)n);
+    const double t = fmax(v * c - tm, -1100.0), n = rint(t), x = (t - n) * 0.6931471805599453;
+    double p = fma(x, scalar(1.0 / 479001600.0), 1.0 / 39916800.0);
+    p = fma(p, x, scalar(1.0 / 3628800.0));
+    p = fma(p, x, scalar(1.0 / 362880.0));
+    p = fma(p, x, scalar(1.0 / 40320.0));
+    p = fma(p, x, scalar(1.0 / 5040.0));
+    p = fma(p, x, scalar(1.0 / 720.0));
+    p = fma(p, x, scalar(1.0 / 120.0));
+    p = fma(p, x, scalar(1.0 / 24.0));
+    p = fma(p, x, scalar(1.0 / 6.0));
+    p = fma(p, x, 0.5);
+    p = fma(p, x, 1.0);
+    return ldexp(fma(p, x, 1.0), (int)n);
   }
   __device__ __forceinline__ double near_value(uint32_t i) const { return key_value(comp_key(s.win[i])); }
 
@@ -1286,17 +1313,24 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
   uint4 c[kMine];
 #pragma unroll
   for (int j = 0; j < kMine; ++j) c[j] = make_uint4(0, 0, 0, 0);
-#pragma unroll 8
-  for (int g = 0; g < n_seg; ++g) {
-    const uint2* p = reinterpret_cast<const uint2*>(part[g].counts);
+  constexpr int kBatch = 5;  // segments whose loads are on their way together
+#pragma unroll 1
+  for (int g0 = 0; g0 < n_seg; g0 += kBatch) {
+    uint2 v[kBatch][kMine];
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const uint2 v = p[tid + j * kThreads];
-      c[j].x += v.x & 0xFFFFu;
-      c[j].y += v.x >> 16;
-      c[j].z += v.y & 0xFFFFu;
-      c[j].w += v.y >> 16;
-    }
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int j = 0; j < kMine; ++j)
+        v[b][j] = g0 + b < n_seg ? reinterpret_cast<const uint2*>(part[g0 + b].counts)[tid + j * kThreads] : make_uint2(0, 0);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        c[j].x += v[b][j].x & 0xFFFFu;
+        c[j].y += v[b][j].x >> 16;
+        c[j].z += v[b][j].y & 0xFFFFu;
+        c[j].w += v[b][j].y >> 16;
+      }
   }
   int top = kLow;  // the first item with a token: the row's largest
 #pragma unroll
@@ -1379,8 +1413,7 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
       sum += c ? all : 0.0;  // the weight of a value over the row's largest may be infinite
     }
   }
-  n = ops.scan(n);
-  sum = ops.scan(sum);
+  ops.scan(n, sum);
   s.rc[tid + 1] = n;
   s.rm[tid + 1] = sum;
   if (tid == 0) {
