@@ -222,6 +222,8 @@ static SamplePlan sample_layout(const dflash_rows& r, bool all, int loads) {
   p.n_seg = (row_slots(r) + kSampleThreads * loads - 1) / (kSampleThreads * loads);
   // in full, or what ordinary cuts take (top-k of 50, peaked rows)
   p.cap = sample_cap(loads, all);
+  // a flat row's cut and draw may need a bin or two each, of a few per cent of its tokens
+  p.ask = (uint32_t)std::max(kSampleAsk, r.V / 8);
   p.batch = std::max(1, 4096 / p.n_seg);
   if (!all) p.batch = std::min<int64_t>(p.batch, 1024);
   const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);
@@ -229,7 +231,7 @@ static SamplePlan sample_layout(const dflash_rows& r, bool all, int loads) {
   p.cuts = p.lists + align256(rows * p.n_seg * p.cap * sizeof(uint64_t));
   p.asks = p.cuts + align256(rows * sizeof(uint64_t));
   p.asked = p.asks + (all ? 0 : align256(rows * sizeof(SampleAsk)));
-  p.total = p.asked + (all ? 0 : align256(rows * kSampleAsk * sizeof(uint64_t)));
+  p.total = p.asked + (all ? 0 : align256(rows * p.ask * sizeof(uint64_t)));
   return p;
 }
 

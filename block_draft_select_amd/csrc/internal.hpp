@@ -176,7 +176,7 @@ constexpr int kSampleMaxSeg = 512;   // blocks per row
 constexpr int kSampleMaxLoads = 8;
 // tokens that a segment of `loads` slots a thread lists
 constexpr int sample_cap(int loads, bool all) { return all ? kSampleThreads * 4 * loads : loads == 2 ? 256 : 64; }
-constexpr int kSampleAsk = 8192;     // tokens outside the lists that a row can ask for
+constexpr int kSampleAsk = 8192;     // tokens outside the lists that a row can ask for: these or an eighth
 // a segment of an fp32 row: kSampleThreads * loads slots
 struct SamplePart {
   double J;      // the segment's maximum in eighths of an octave, rounded; -inf: nothing unmasked
@@ -196,7 +196,7 @@ struct SampleValues {
   uint32_t odd[kSampleOdd];      // tokens near zero: value << 16 | place in the segment
 };
 // bins whose tokens a row needs beyond the lists: up to two ranges
-enum { kSampleAskNone = 0, kSampleAskBins = 1, kSampleAskRow = 2 /* more tokens than kSampleAsk: the row is read again */ };
+enum { kSampleAskNone = 0, kSampleAskBins = 1, kSampleAskRow = 2 /* more tokens than a row can ask for: it is read again */ };
 struct SampleAsk {
   int32_t kind;
   uint32_t n;  // tokens collected
@@ -227,6 +227,7 @@ struct SamplePlan {
   int loads;      // fp32: slots of a thread
   bool all;       // fp32: every token is listed
   int cap;        // fp32: tokens a block lists
+  uint32_t ask;   // fp32: tokens outside the lists that a row can ask for
   int64_t batch;  // rows per pass over the workspace
   size_t parts, lists, cuts, asks, asked, total;
 };

@@ -482,6 +482,7 @@ struct Finalize {
   const uint64_t* lists;
   const uint64_t* asked;  // the row's asked-for tokens
   const SampleAsk* ask;
+  const uint32_t ask_cap;
   const int n_seg, cap;
   const double c8, t8, J;
   const int tid;
@@ -522,7 +523,7 @@ struct Finalize {
       }
     } else if constexpr (MODE == kSecond || MODE == kSelf) {
       if (MODE == kSecond && ask->kind == kSampleAskBins && ((B0 >= ask->b0[0] && B1 <= ask->b1[0]) || (B0 >= ask->b0[1] && B1 <= ask->b1[1]))) {
-        const int end = (int)min(ask->n, (uint32_t)kSampleAsk);
+        const int end = (int)min(ask->n, ask_cap);
 #pragma unroll 4
         for (int j = tid; j < end; j += kThreads) f(asked[j]);
       } else {
@@ -772,7 +773,7 @@ struct Finalize {
 // cut or draw whose amount depends on an earlier cut inside a bin takes the
 // bins of that amount's bounds.  True if all are listed; else asks for them.
 __device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowParams& rp, uint32_t N, double wmax, bool draw,
-                                            double u, double J, uint32_t kmax, int listed, SampleAsk& ask) {
+                                            double u, double J, uint32_t kmax, int listed, uint32_t ask_cap, SampleAsk& ask) {
   const double c8 = rp.c8, t8 = rp.t8;
   constexpr double kLess = 1.0 - 0x1p-40, kMore = 1.0 + 0x1p-40;
   const int tid = threadIdx.x;
@@ -835,7 +836,7 @@ __device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowP
     h1 = d0 == 0 ? kmax : lowest_key(J - d0 + 1.0, c8, t8) - 1u;
   }
   if (tid == 0) {
-    ask.kind = count <= (uint32_t)kSampleAsk ? kSampleAskBins : kSampleAskRow;
+    ask.kind = count <= ask_cap ? kSampleAskBins : kSampleAskRow;
     ask.n = 0;
     ask.b0[0] = need0, ask.b1[0] = need1, ask.klo[0] = l0, ask.khi[0] = h0;
     ask.b0[1] = d0, ask.b1[1] = d1, ask.klo[1] = l1, ask.khi[1] = h1;
@@ -860,7 +861,7 @@ __device__ __forceinline__ double row_uniform(const SampleOut& o, int64_t row) {
 // other blocks left them in memory, then scans, windows and searches).  One row
 // of 151936 fp32 takes 16 us, 256 of 262144 23 and 31 (kFirst and kSecond).
 template <int MODE>
-__global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
+__global__ __launch_bounds__(kThreads, 4) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap, uint32_t ask_cap,
                                                                    const SamplePart* __restrict__ parts,
                                                                    const uint64_t* __restrict__ lists,
                                                                    SampleAsk* __restrict__ asks, const uint64_t* __restrict__ asked,
@@ -917,12 +918,12 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
 
   const uint32_t kmax = key_of(m, RowType<DFLASH_F32>::kMax);
   Finalize<DFLASH_F32, MODE> f{s, ops, RowRef<DFLASH_F32>(a.Z, row, a.stride, a.V), part, lists + (size_t)blockIdx.x * n_seg * cap,
-                               MODE == kSecond ? asked + (size_t)blockIdx.x * kSampleAsk : nullptr,
-                               MODE == kSecond ? asks + blockIdx.x : nullptr, n_seg, cap, rp.c8, rp.t8, J, tid, kmax, listed,
+                               MODE == kSecond ? asked + (size_t)blockIdx.x * ask_cap : nullptr,
+                               MODE == kSecond ? asks + blockIdx.x : nullptr, ask_cap, n_seg, cap, rp.c8, rp.t8, J, tid, kmax, listed,
                                0, 0, 0.0, 1, 0, 0};
   const double wmax = f.weight(kmax);
   if constexpr (MODE == kFirst) {
-    if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, kmax, listed, asks[blockIdx.x])) return;
+    if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, kmax, listed, ask_cap, asks[blockIdx.x])) return;
   }
   f.answer(rp, N, wmax, u, row, o, cuts + blockIdx.x);
 }
@@ -932,13 +933,13 @@ __global__ __launch_bounds__(kThreads) void sample_finalize_kernel(SampleArgs a,
 // Reads the rows a second time at the memory's rate (256 x 262144 fp32: 44 us,
 // 6.1 TB/s); rows that asked for nothing are not read.
 template <int NL>
-__global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, int64_t row0, int n_seg, SampleAsk* __restrict__ asks,
-                                                                 uint64_t* __restrict__ asked) {
+__global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, int64_t row0, int n_seg, uint32_t ask_cap,
+                                                                 SampleAsk* __restrict__ asks, uint64_t* __restrict__ asked) {
   constexpr int DT = DFLASH_F32, VE = RowType<DT>::VE;
   const int r = blockIdx.x / n_seg, seg = blockIdx.x % n_seg, tid = threadIdx.x;
   SampleAsk& ask = asks[r];
   if (ask.kind != kSampleAskBins) return;
-  __shared__ uint32_t place[kSampleAsk];
+  __shared__ uint16_t place[kThreads * NL * VE];  // in the segment
   __shared__ uint32_t n, at;
   if (tid == 0) n = 0;
   __syncthreads();
@@ -961,19 +962,18 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, i
     if (hits) {
       uint32_t i = atomicAdd(&n, (uint32_t)__popc(hits));
       do {
-        if (i < (uint32_t)kSampleAsk) place[i] = (uint32_t)((s0 + l * kThreads) * VE + __builtin_ctz(hits));
-        ++i;
+        place[i++] = (uint16_t)((tid + l * kThreads) * VE + __builtin_ctz(hits));
         hits &= hits - 1;
       } while (hits);
     }
   }
   __syncthreads();
-  const uint32_t c = min(n, (uint32_t)kSampleAsk);
+  const uint32_t c = n;
   if (tid == 0) at = atomicAdd(&ask.n, c);  // the tokens' order in the row's buffer does not matter
   __syncthreads();
-  uint64_t* out = asked + (size_t)r * kSampleAsk;
-  for (uint32_t i = tid; i < c && at + i < (uint32_t)kSampleAsk; i += kThreads) {
-    const uint32_t idx = place[i];
+  uint64_t* out = asked + (size_t)r * ask_cap;
+  for (uint32_t i = tid; i < c && at + i < ask_cap; i += kThreads) {
+    const uint32_t idx = (uint32_t)(seg * (kThreads * NL * VE)) + place[i];
     out[at + i] = comp_of(key_of(row_value<DT>(z, (int)idx), RowType<DT>::kMax), idx);
   }
 }
@@ -1531,7 +1531,7 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
   }
   __syncthreads();
   const uint32_t kmax = key_of(m, kMax);
-  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, c8, rp.t8, J, tid, kmax, 0, 0, 0, 0.0, 1, 0, 0};
+  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, 0, c8, rp.t8, J, tid, kmax, 0, 0, 0, 0.0, 1, 0, 0};
   f.answer(rp, s.cc[kBins], f.weight(kmax), row_uniform(o, row), row, o, cut_out);
 }
 
@@ -1629,13 +1629,13 @@ hipError_t run_f32(const SampleArgs& a, const SampleOut& o, char* ws, const Samp
     const dim3 rows(nr), segs(nr * (unsigned)pl.n_seg);
     launch(sample_hist_kernel<NL, ALL>, segs, block, st, a, r0, pl.n_seg, pl.cap, parts, lists);
     if constexpr (ALL) {
-      launch(sample_finalize_kernel<kAll>, rows, block, st, a, r0, pl.n_seg, pl.cap, (const SamplePart*)parts,
+      launch(sample_finalize_kernel<kAll>, rows, block, st, a, r0, pl.n_seg, pl.cap, pl.ask, (const SamplePart*)parts,
              (const uint64_t*)lists, asks, (const uint64_t*)asked, o, cuts);
     } else {
-      launch(sample_finalize_kernel<kFirst>, rows, block, st, a, r0, pl.n_seg, pl.cap, (const SamplePart*)parts,
+      launch(sample_finalize_kernel<kFirst>, rows, block, st, a, r0, pl.n_seg, pl.cap, pl.ask, (const SamplePart*)parts,
              (const uint64_t*)lists, asks, (const uint64_t*)asked, o, cuts);
-      launch(sample_gather_kernel<NL>, segs, block, st, a, r0, pl.n_seg, asks, asked);
-      launch(sample_finalize_kernel<kSecond>, rows, block, st, a, r0, pl.n_seg, pl.cap, (const SamplePart*)parts,
+      launch(sample_gather_kernel<NL>, segs, block, st, a, r0, pl.n_seg, pl.ask, asks, asked);
+      launch(sample_finalize_kernel<kSecond>, rows, block, st, a, r0, pl.n_seg, pl.cap, pl.ask, (const SamplePart*)parts,
              (const uint64_t*)lists, asks, (const uint64_t*)asked, o, cuts);
     }
     if (o.out) apply<DFLASH_F32>(a, o, r0, nr, cuts, st);
