@@ -238,6 +238,11 @@ static SamplePlan sample_layout(const dflash_rows& r, bool all, int loads) {
 SamplePlan sample_plan(const dflash_rows& r) {
   SamplePlan p{};
   const int slots = row_slots(r);
+  if (slots <= kSampleThreads) {  // in one launch
+    p.one = true;
+    p.total = align256(1);
+    return p;
+  }
   if (r.dtype == DFLASH_BF16) {
     // A block costs its counters (12 KB written, read again and scanned) beside
     // its slots: the longest segments that still give four blocks per CU,

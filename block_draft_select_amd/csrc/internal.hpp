@@ -222,6 +222,7 @@ struct SampleOut {
   uint32_t fill;  // fill value in the element type
 };
 struct SamplePlan {
+  bool one;       // one launch, a block a row
   int n_seg;      // blocks per row
   int seg_slots;  // bf16: slots of a block
   int loads;      // fp32: slots of a thread

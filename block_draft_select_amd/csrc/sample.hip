@@ -292,6 +292,58 @@ __device__ __forceinline__ unsigned long long cell_of(double f) {
   return (unsigned long long)((uint32_t)(w >> 32) + kUpper) << 32 | (uint32_t)w;
 }
 
+// a thread's tokens into the bins' cells; J: the maximum's bin
+template <int DT, int NL>
+__device__ __forceinline__ void add_cells(unsigned long long* cells, const Slot (&x)[NL], double J, const RowParams& rp) {
+  constexpr int VE = RowType<DT>::VE;
+  constexpr float kMax = RowType<DT>::kMax;
+  const double c8 = rp.c8;
+  unsigned long long* cell = cells + (threadIdx.x & (kCols - 1));
+  if (fabs(J) <= 0x1p20) {
+    // rint by adding 3 2^51, whose sum's lower word is the integer.  Tokens far
+    // below the maximum are raised to 1000 bins below it: the tail all the same
+    constexpr double kMagic = 0x1.8p52;
+    const float lowest = (float)((J - 1000.0) * rp.t8);
+    const int j = (int)J;
+#pragma unroll
+    for (int l = 0; l < NL; ++l)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float v = slot_value<DT>(x[l], i);
+        if (v > kNegInf) {
+          const double t = (double)__builtin_amdgcn_fmed3f(v, lowest, kMax) * c8, r = t + kMagic;
+          const uint32_t b = min((uint32_t)(j - (int)(uint32_t)__double_as_longlong(r)), (uint32_t)kTail);
+          atomicAdd(&cell[b * kCols], cell_of(t - (r - kMagic)));
+        }
+      }
+  } else {
+#pragma unroll 1
+    for (int e = 0; e < NL * VE; ++e) {
+      float v = kNegInf;
+#pragma unroll
+      for (int k = 0; k < NL * VE; ++k)
+        if (k == e) v = slot_value<DT>(x[k / VE], k % VE);
+      if (v > kNegInf) {
+        const double t = (double)fminf(v, kMax) * c8, n = rint(t);
+        atomicAdd(&cell[(int)fmin(J - n, (double)kTail) * kCols], cell_of(t - n));
+      }
+    }
+  }
+}
+
+// a bin's tokens c, and their weight in units of 2^-42
+__device__ __forceinline__ unsigned long long read_cells(const unsigned long long* cells, int bin, uint32_t& c) {
+  c = 0;
+  unsigned long long f = 0;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    const unsigned long long w = cells[bin * kCols + k];
+    c += (uint32_t)(w >> kCellCount);
+    f += w & ((1ull << kCellCount) - 1);
+  }
+  return f + (unsigned long long)c * kCellLess;
+}
+
 // a token into the list, which is in the order of its bins
 __device__ __forceinline__ void list_token(uint32_t* next, uint64_t* list, double c8, double J, uint64_t c) {
   const int b = (int)fmin(J - rint(key_value(comp_key(c)) * c8), (double)kTail);
@@ -341,50 +393,13 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
     return;
   }
   const double J = rint((double)m * c8);
-  unsigned long long* cell = s.cell + (tid & (kCols - 1));
-  if (fabs(J) <= 0x1p20) {
-    // rint by adding 3 2^51, whose sum's lower word is the integer.  Tokens far
-    // below the maximum are raised to 1000 bins below it: the tail all the same
-    constexpr double kMagic = 0x1.8p52;
-    const float lowest = (float)((J - 1000.0) * rp.t8);
-    const int j = (int)J;
-#pragma unroll
-    for (int l = 0; l < NL; ++l)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float v = slot_value<DFLASH_F32>(x[l], i);
-        if (v > kNegInf) {
-          const double t = (double)__builtin_amdgcn_fmed3f(v, lowest, kMax) * c8, r = t + kMagic;
-          const uint32_t b = min((uint32_t)(j - (int)(uint32_t)__double_as_longlong(r)), (uint32_t)kTail);
-          atomicAdd(&cell[b * kCols], cell_of(t - (r - kMagic)));
-        }
-      }
-  } else {
-#pragma unroll 1
-    for (int e = 0; e < NL * VE; ++e) {
-      float v = kNegInf;
-#pragma unroll
-      for (int k = 0; k < NL * VE; ++k)
-        if (k == e) v = slot_value<DFLASH_F32>(x[k / VE], k % VE);
-      if (v > kNegInf) {
-        const double t = (double)fminf(v, kMax) * c8, n = rint(t);
-        atomicAdd(&cell[(int)fmin(J - n, (double)kTail) * kCols], cell_of(t - n));
-      }
-    }
-  }
+  add_cells<DFLASH_F32>(s.cell, x, J, rp);
   __syncthreads();
-  uint32_t c = 0, mirror = 0;  // mirror: the bin counted from the far end
-  unsigned long long f = 0;
-#pragma unroll
-  for (int k = 0; k < kCols; ++k) {
-    const unsigned long long w = s.cell[tid * kCols + k];
-    c += (uint32_t)(w >> kCellCount);
-    f += w & ((1ull << kCellCount) - 1);
-    mirror |= (uint32_t)(s.cell[(kBins - 1 - tid) * kCols + k] >> kCellCount);
-  }
-  f += (unsigned long long)c * kCellLess;
+  uint32_t c, far;  // far: the bin counted from the other end
+  const unsigned long long f = read_cells(s.cell, tid, c);
+  read_cells(s.cell, kBins - 1 - tid, far);
   const uint32_t upto = ops.scan(c);
-  const int nb = kBins - ops.first(mirror != 0);       // bins in use
+  const int nb = kBins - ops.first(far != 0);       // bins in use
   const int listed = ops.first(upto > (uint32_t)cap);  // leading bins with at most `cap` tokens together
   s.next[tid] = upto - c;
   if (tid < nb) {
@@ -442,8 +457,9 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int
 enum { kByCount, kByMassGe, kByMassGt, kByWeight };
 // kAll: the lists hold every token.  kFirst: they hold the largest; rows that
 // need others ask for them.  kSecond: the rows that asked.  kSelf: no lists,
-// the row itself is read.
-enum { kAll, kFirst, kSecond, kSelf };
+// the row itself is read.  kOne: a row of one block, which holds the list of
+// all its tokens.
+enum { kAll, kFirst, kSecond, kSelf, kOne };
 constexpr int kMaxSeg = kSampleMaxSeg;
 
 struct FinLds {
@@ -503,7 +519,10 @@ struct Finalize {
   // f((~key, index)) of every token of bins B0 .. B1, and of others
   template <class F>
   __device__ __forceinline__ void each(int B0, int B1, F f) {
-    if (MODE != kSelf && (MODE == kAll || B1 < listed)) {
+    if constexpr (MODE == kOne) {
+      const int end = (int)s.cc[B1 + 1];
+      for (int j = (int)s.cc[B0] + tid; j < end; j += kThreads) f(lists[j]);
+    } else if (MODE != kSelf && (MODE == kAll || B1 < listed)) {
       // a segment's list is in the order of its bins, so its part is one run
       __syncthreads();
       if (tid < n_seg) {
@@ -591,6 +610,28 @@ struct Finalize {
     __syncthreads();
   }
 
+  // kOne: bins b0 .. b1 into the window; a token's rank is its bin's place in
+  // the list and its rank among the bin's own tokens
+  __device__ __forceinline__ void open_bins(uint32_t lo_, uint32_t base_, double bmass_, int b0_, int b1_, uint32_t n_) {
+    lo = lo_, base = base_, bmass = bmass_, b0 = b0_, b1 = b1_, n = n_;
+    __syncthreads();  // the last window's readers
+    const uint64_t* list = lists + s.cc[b0];
+    const bool in = tid < (int)n;
+    double w = 0.0;
+    if (in) {
+      const uint64_t mine = list[tid];
+      const int bin = (int)fmin(J - rint(key_value(comp_key(mine)) * c8), (double)kTail);
+      uint32_t rank = s.cc[bin] - s.cc[b0];
+      for (uint32_t j = rank, end = s.cc[bin + 1] - s.cc[b0]; j < end; ++j) rank += list[j] < mine;
+      s.win[rank] = mine;
+    }
+    __syncthreads();
+    if (in) w = weight(comp_key(s.win[tid]));
+    w = bmass + ops.scan(w);
+    if (in) s.wcum[tid] = w;
+    __syncthreads();
+  }
+
   __device__ __forceinline__ Cross from_window(int kind, double amount) {
     const bool in = tid < (int)n;
     const bool hit = in && (kind == kByCount    ? (double)(base + tid + 1) >= amount
@@ -644,7 +685,7 @@ struct Finalize {
       if (nc == 0) return Cross{cb, mb, ((uint64_t)~khi) << 32, 0};  // kByWeight: nothing in the threshold's own bin
       int B0 = b;
       bool whole = true;
-      if (MODE != kSelf && (MODE == kAll || b < listed) && s.cc[b + 1] <= (uint32_t)kThreads) {  // everything down to this bin fits a window
+      if (MODE != kSelf && (MODE == kAll || MODE == kOne || b < listed) && s.cc[b + 1] <= (uint32_t)kThreads) {  // everything down to this bin fits a window
         B0 = 0;
         khi = kmax;
         nc += cb;
@@ -714,8 +755,12 @@ struct Finalize {
         if ((uint32_t)q + 1 < n_part) klo = khi - ((1u << sh) - 1u);
         if (nc == 0) return Cross{cb, mb, ((uint64_t)~khi) << 32, 0};  // kByWeight: the threshold falls between tokens
       }
-      pass(B0, b, klo, khi, 0, 0xFFFFFFFFu, -1, false);
-      open_window(klo, cb, mb, whole ? B0 : 1, whole ? b : 0);
+      if (MODE == kOne && whole) {
+        open_bins(klo, cb, mb, B0, b, nc);
+      } else {
+        pass(B0, b, klo, khi, 0, 0xFFFFFFFFu, -1, false);
+        open_window(klo, cb, mb, whole ? B0 : 1, whole ? b : 0);
+      }
     }
     return from_window(kind, amount);
   }
@@ -926,6 +971,89 @@ __global__ __launch_bounds__(kThreads, 4) void sample_finalize_kernel(SampleArgs
     if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, kmax, listed, ask_cap, asks[blockIdx.x])) return;
   }
   f.answer(rp, N, wmax, u, row, o, cuts + blockIdx.x);
+}
+
+// a slot of the filtered row: the tokens before `cut` stay
+template <int DT>
+__device__ __forceinline__ void store_filtered(typename RowType<DT>::elem* o, int V, int slot, const Slot& x, uint64_t cut,
+                                               uint32_t fill) {
+  constexpr int VE = RowType<DT>::VE;
+  Slot y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y.w[k] = 0;
+#pragma unroll
+  for (int i = 0; i < VE; ++i) {
+    const float v = slot_value<DT>(x, i);
+    const bool in = v > kNegInf && comp_of(key_of(v, RowType<DT>::kMax), (uint32_t)(slot * VE + i)) < cut;
+    if constexpr (DT == DFLASH_BF16) {
+      const uint32_t raw = (i & 1) ? x.w[i >> 1] >> 16 : x.w[i >> 1] & 0xFFFFu;
+      y.w[i >> 1] |= (in ? raw : fill) << ((i & 1) * 16);
+    } else {
+      y.w[i] = in ? x.w[i] : fill;
+    }
+  }
+  store_slot<DT>(o, V, slot, y);
+}
+
+// ---------------------------------------------------------------- short rows in one launch
+
+// A row of one slot a thread (2048 fp32 tokens, 4096 bf16) in one block: bins,
+// list and answer stay in LDS, and the filtered row is written at once.
+template <int DT>
+__global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, SampleOut o) {
+  constexpr int VE = RowType<DT>::VE;
+  constexpr float kMax = RowType<DT>::kMax;
+  __shared__ FinLds s;
+  __shared__ uint32_t next[kBins];
+  __shared__ unsigned long long cell[kBins * kCols > kThreads * VE ? kBins * kCols : kThreads * VE];  // then the list
+  __shared__ uint64_t cut;
+  BlockOps ops(s.red);
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const RowParams rp = row_params(a, row);
+  const RowRef<DT> z(a.Z, row, a.stride, a.V);
+  const double c8 = rp.c8, u = row_uniform(o, row);
+  Slot x[1] = {z.load(tid)};
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) cell[c * kBins + tid] = 0;
+  float m = kNegInf;
+#pragma unroll
+  for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[0], i));
+  m = (float)ops.max((double)fminf(m, kMax));
+  if (m == kNegInf) {
+    empty_row(row, o, &cut);
+  } else {
+    const double J = rint((double)m * c8);
+    add_cells<DT>(cell, x, J, rp);
+    __syncthreads();
+    uint32_t c, cs;
+    const unsigned long long f = read_cells(cell, tid, c);
+    cs = c;
+    double cum = tid < kTail ? (double)f * 0x1p-42 * pow2_eighth(-tid) : 0.0;
+    ops.scan(cs, cum);
+    s.cc[tid + 1] = cs;
+    s.cm[tid + 1] = cum;
+    next[tid] = cs - c;
+    if (tid == 0) {
+      s.cc[0] = 0;
+      s.cm[0] = 0.0;
+    }
+    __syncthreads();
+    uint64_t* list = reinterpret_cast<uint64_t*>(cell);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DT>(x[0], i);
+      if (v > kNegInf) list_token(next, list, c8, J, comp_of(key_of(v, kMax), (uint32_t)(tid * VE + i)));
+    }
+    __syncthreads();
+    const uint32_t kmax = key_of(m, kMax);
+    Finalize<DT, kOne> fin{s, ops, z, nullptr, list, nullptr, nullptr, 0, 1, 0, c8, rp.t8, J, tid, kmax, kBins, 0, 0, 0.0, 1, 0, 0};
+    fin.answer(rp, s.cc[kBins], fin.weight(kmax), u, row, o, &cut);
+  }
+  if (o.out) {
+    __syncthreads();
+    store_filtered<DT>(static_cast<typename RowType<DT>::elem*>(o.out) + row * o.out_stride, a.V, tid, x[0], cut, o.fill);
+  }
 }
 
 // ---------------------------------------------------------------- (3) the tokens that rows asked for
@@ -1570,25 +1698,7 @@ __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, in
 #pragma unroll
   for (int l = 0; l < NL; ++l) x[l] = z.load(s0 + l * kThreads);
 #pragma unroll
-  for (int l = 0; l < NL; ++l) {
-    const int e = (s0 + l * kThreads) * VE;
-    Slot y;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y.w[k] = 0;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float v = slot_value<DT>(x[l], i);
-      const uint32_t key = key_of(v, RowType<DT>::kMax);
-      const bool in = v > kNegInf && (((uint64_t)~key << 32) | (uint32_t)(e + i)) < cut;
-      if constexpr (DT == DFLASH_BF16) {
-        const uint32_t raw = (i & 1) ? x[l].w[i >> 1] >> 16 : x[l].w[i >> 1] & 0xFFFFu;
-        y.w[i >> 1] |= (in ? raw : fill) << ((i & 1) * 16);
-      } else {
-        y.w[i] = in ? x[l].w[i] : fill;
-      }
-    }
-    store_slot<DT>(o, a.V, s0 + l * kThreads, y);
-  }
+  for (int l = 0; l < NL; ++l) store_filtered<DT>(o, a.V, s0 + l * kThreads, x[l], cut, fill);
 }
 
 template <int DT>
@@ -1649,6 +1759,13 @@ hipError_t run_f32(const SampleArgs& a, const SampleOut& o, char* ws, const Samp
 
 hipError_t launch_sample(int32_t dtype, const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl,
                          hipStream_t st) {
+  if (pl.one) {
+    if (dtype == DFLASH_BF16)
+      launch(sample_row_kernel<DFLASH_BF16>, dim3((unsigned)a.R), dim3(kThreads), st, a, o);
+    else
+      launch(sample_row_kernel<DFLASH_F32>, dim3((unsigned)a.R), dim3(kThreads), st, a, o);
+    return hipGetLastError();
+  }
   if (dtype == DFLASH_BF16) return run_bf16(a, o, ws, pl, st);
   switch (pl.loads) {
     case 1: return run_f32<1, true>(a, o, ws, pl, st);
