@@ -238,7 +238,11 @@ static SamplePlan sample_layout(const dflash_rows& r, bool all, int loads) {
 SamplePlan sample_plan(const dflash_rows& r) {
   SamplePlan p{};
   const int slots = row_slots(r);
-  if (slots <= kSampleThreads) {  // in one launch
+  // In one launch, a block a row: short rows, in bf16 those of one slot a thread
+  // (8000 tokens: 11 us for one row against 15 in two launches, but 22 against
+  // 19 for 64 rows and 158 against 75 for 2048)
+  if (r.V <= (r.dtype == DFLASH_BF16 ? kSampleOne / 2 : kSampleOne)) {
+    p.loads = slots <= kSampleThreads ? 1 : slots <= 2 * kSampleThreads ? 2 : 4;
     p.one = true;
     p.total = align256(1);
     return p;
@@ -266,8 +270,8 @@ SamplePlan sample_plan(const dflash_rows& r) {
   if (r.R <= all_listed_rows(r)) {
     // The finish adds the segments one after another and a segment works its
     // tokens off so: one, two, four slots a thread take 42, 34, 26 us on one row
-    // of 151936, 17, 16, 22 on 32000 and 14.5, 15, 18 on 8192
-    return sample_layout(r, true, slots <= 4 * kSampleThreads ? 1 : slots <= 16 * kSampleThreads ? 2 : 4);
+    // of 151936, 17, 16, 22 on 32000
+    return sample_layout(r, true, slots <= 16 * kSampleThreads ? 2 : 4);
   }
   // the most slots a thread whose grid still has 1024 blocks (four per CU), so
   // that many rows amortise their bins

@@ -176,6 +176,7 @@ constexpr int kSampleMaxSeg = 512;   // blocks per row
 constexpr int kSampleMaxLoads = 8;
 // tokens that a segment of `loads` slots a thread lists
 constexpr int sample_cap(int loads, bool all) { return all ? kSampleThreads * 4 * loads : loads == 2 ? 256 : 64; }
+constexpr int kSampleOne = 8192;     // longest fp32 row that one block does by itself
 constexpr int kSampleAsk = 8192;     // tokens outside the lists that a row can ask for: these or an eighth
 // a segment of an fp32 row: kSampleThreads * loads slots
 struct SamplePart {

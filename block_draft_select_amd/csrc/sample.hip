@@ -906,7 +906,7 @@ __device__ __forceinline__ double row_uniform(const SampleOut& o, int64_t row) {
 // other blocks left them in memory, then scans, windows and searches).  One row
 // of 151936 fp32 takes 16 us, 256 of 262144 23 and 31 (kFirst and kSecond).
 template <int MODE>
-__global__ __launch_bounds__(kThreads, 4) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap, uint32_t ask_cap,
+__global__ __launch_bounds__(kThreads, MODE == kSecond ? 4 : 2) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap, uint32_t ask_cap,
                                                                    const SamplePart* __restrict__ parts,
                                                                    const uint64_t* __restrict__ lists,
                                                                    SampleAsk* __restrict__ asks, const uint64_t* __restrict__ asked,
@@ -997,15 +997,17 @@ __device__ __forceinline__ void store_filtered(typename RowType<DT>::elem* o, in
 
 // ---------------------------------------------------------------- short rows in one launch
 
-// A row of one slot a thread (2048 fp32 tokens, 4096 bf16) in one block: bins,
-// list and answer stay in LDS, and the filtered row is written at once.
-template <int DT>
+// A row of up to 8192 tokens in one block, NL slots a thread: bins, list and
+// answer stay in LDS, and the filtered row is written at once.  Bound by the
+// chain of steps: one row of 1024 fp32 takes 7.9 us (12.9 in two launches), 2048
+// rows 39 (82); one row of 8000 11 (15), 2048 rows 159 (180).
+template <int DT, int NL>
 __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, SampleOut o) {
   constexpr int VE = RowType<DT>::VE;
   constexpr float kMax = RowType<DT>::kMax;
   __shared__ FinLds s;
   __shared__ uint32_t next[kBins];
-  __shared__ unsigned long long cell[kBins * kCols > kThreads * VE ? kBins * kCols : kThreads * VE];  // then the list
+  __shared__ unsigned long long cell[kBins * kCols > kThreads * NL * VE ? kBins * kCols : kThreads * NL * VE];  // then the list
   __shared__ uint64_t cut;
   BlockOps ops(s.red);
   const int tid = threadIdx.x;
@@ -1013,12 +1015,16 @@ __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, S
   const RowParams rp = row_params(a, row);
   const RowRef<DT> z(a.Z, row, a.stride, a.V);
   const double c8 = rp.c8, u = row_uniform(o, row);
-  Slot x[1] = {z.load(tid)};
+  Slot x[NL];
+#pragma unroll
+  for (int l = 0; l < NL; ++l) x[l] = z.load(tid + l * kThreads);
 #pragma unroll
   for (int c = 0; c < kCols; ++c) cell[c * kBins + tid] = 0;
   float m = kNegInf;
 #pragma unroll
-  for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[0], i));
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) m = fmaxf(m, slot_value<DT>(x[l], i));
   m = (float)ops.max((double)fminf(m, kMax));
   if (m == kNegInf) {
     empty_row(row, o, &cut);
@@ -1041,10 +1047,12 @@ __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, S
     __syncthreads();
     uint64_t* list = reinterpret_cast<uint64_t*>(cell);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float v = slot_value<DT>(x[0], i);
-      if (v > kNegInf) list_token(next, list, c8, J, comp_of(key_of(v, kMax), (uint32_t)(tid * VE + i)));
-    }
+    for (int l = 0; l < NL; ++l)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float v = slot_value<DT>(x[l], i);
+        if (v > kNegInf) list_token(next, list, c8, J, comp_of(key_of(v, kMax), (uint32_t)((tid + l * kThreads) * VE + i)));
+      }
     __syncthreads();
     const uint32_t kmax = key_of(m, kMax);
     Finalize<DT, kOne> fin{s, ops, z, nullptr, list, nullptr, nullptr, 0, 1, 0, c8, rp.t8, J, tid, kmax, kBins, 0, 0, 0.0, 1, 0, 0};
@@ -1052,7 +1060,9 @@ __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, S
   }
   if (o.out) {
     __syncthreads();
-    store_filtered<DT>(static_cast<typename RowType<DT>::elem*>(o.out) + row * o.out_stride, a.V, tid, x[0], cut, o.fill);
+    typename RowType<DT>::elem* out = static_cast<typename RowType<DT>::elem*>(o.out) + row * o.out_stride;
+#pragma unroll
+    for (int l = 0; l < NL; ++l) store_filtered<DT>(out, a.V, tid + l * kThreads, x[l], cut, o.fill);
   }
 }
 
@@ -1760,17 +1770,21 @@ hipError_t run_f32(const SampleArgs& a, const SampleOut& o, char* ws, const Samp
 hipError_t launch_sample(int32_t dtype, const SampleArgs& a, const SampleOut& o, char* ws, const SamplePlan& pl,
                          hipStream_t st) {
   if (pl.one) {
+    const dim3 rows((unsigned)a.R), block(kThreads);
     if (dtype == DFLASH_BF16)
-      launch(sample_row_kernel<DFLASH_BF16>, dim3((unsigned)a.R), dim3(kThreads), st, a, o);
+      launch(sample_row_kernel<DFLASH_BF16, 1>, rows, block, st, a, o);
     else
-      launch(sample_row_kernel<DFLASH_F32>, dim3((unsigned)a.R), dim3(kThreads), st, a, o);
+      launch(pl.loads == 1   ? sample_row_kernel<DFLASH_F32, 1>
+             : pl.loads == 2 ? sample_row_kernel<DFLASH_F32, 2>
+                             : sample_row_kernel<DFLASH_F32, 4>,
+             rows, block, st, a, o);
     return hipGetLastError();
   }
   if (dtype == DFLASH_BF16) return run_bf16(a, o, ws, pl, st);
+  if (pl.all) return pl.loads == 2 ? run_f32<2, true>(a, o, ws, pl, st) : run_f32<4, true>(a, o, ws, pl, st);
   switch (pl.loads) {
-    case 1: return run_f32<1, true>(a, o, ws, pl, st);
-    case 2: return pl.all ? run_f32<2, true>(a, o, ws, pl, st) : run_f32<2, false>(a, o, ws, pl, st);
-    case 4: return pl.all ? run_f32<4, true>(a, o, ws, pl, st) : run_f32<4, false>(a, o, ws, pl, st);
+    case 2: return run_f32<2, false>(a, o, ws, pl, st);
+    case 4: return run_f32<4, false>(a, o, ws, pl, st);
     default: return run_f32<8, false>(a, o, ws, pl, st);
   }
 }
