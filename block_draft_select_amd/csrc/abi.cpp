@@ -265,8 +265,8 @@ SamplePlan sample_plan(const dflash_rows& r) {
   }
   // Up to about six million tokens every token is listed, so that the one block
   // that finishes a row needs no other and no row is read twice; beyond, lists
-  // of 8 bytes a token cost more than they save (top-p, 32 x 151936: 56 us
-  // against 90 without; 64 rows: 82 against 80; 512 x 32000: 108 against 78).
+  // of 8 bytes a token cost more than they save (top-p, 32 x 151936: 57 us
+  // against 77 without; 64 rows: 81 against 72; 512 x 32000: 98 against 77).
   if (r.R <= all_listed_rows(r)) {
     // The finish adds the segments one after another and a segment works its
     // tokens off so: one, two, four slots a thread take 42, 34, 26 us on one row
