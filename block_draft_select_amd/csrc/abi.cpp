@@ -257,7 +257,7 @@ SamplePlan sample_plan(const dflash_rows& r) {
     p.n_seg = (int)std::min<int64_t>(std::max<int64_t>(least, (1024 + r.R - 1) / std::max<int64_t>(r.R, 1)), most);
     p.n_seg = std::min(std::max(p.n_seg, 1), kSampleMaxSeg);
     p.seg_slots = (slots + p.n_seg - 1) / p.n_seg;
-    p.batch = std::max(1, 4096 / p.n_seg);
+    p.batch = std::max(1, kSampleMostParts / p.n_seg);
     const size_t rows = (size_t)std::min<int64_t>(r.R, p.batch);
     p.cuts = align256(rows * p.n_seg * sizeof(SampleValues));
     p.total = p.cuts + align256(rows * sizeof(uint64_t));
@@ -312,8 +312,8 @@ size_t rows_workspace(const dflash_rows& r) {
   if (r.dtype == DFLASH_BF16) {
     const int64_t least = (slots + kSampleMaxSegSlots - 1) / kSampleMaxSegSlots;
     const int64_t most = std::max<int64_t>(least, (slots + 4 * kSampleThreads - 1) / (4 * kSampleThreads));
-    const int64_t segs = std::min<int64_t>(std::min(r.R * most, std::max(r.R * least, 1024 + r.R)), 4096);
-    return std::max(total, align256(segs * sizeof(SampleValues)) + align256(std::min<int64_t>(r.R, 4096) * sizeof(uint64_t)));
+    const int64_t segs = std::min<int64_t>(std::min(r.R * most, std::max(r.R * least, 1024 + r.R)), kSampleMostParts);
+    return std::max(total, align256(segs * sizeof(SampleValues)) + align256(std::min<int64_t>(r.R, kSampleMostParts) * sizeof(uint64_t)));
   }
   dflash_rows few = r;
   few.R = std::min(r.R, all_listed_rows(r));

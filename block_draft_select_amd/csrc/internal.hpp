@@ -192,6 +192,7 @@ struct SamplePart {
 constexpr int kSampleItems = 6144;
 constexpr int kSampleOdd = 64;
 constexpr int kSampleMaxSegSlots = 8191;
+constexpr int kSampleMostParts = 8192;  // segments a pass over the workspace counts (12.5 KB each)
 struct SampleValues {
   uint16_t counts[kSampleItems];
   uint32_t odd[kSampleOdd];      // tokens near zero: value << 16 | place in the segment

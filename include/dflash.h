@@ -455,8 +455,8 @@ dflash_status dflash_filter(const dflash_rows* r, const void* Z, const dflash_fi
  *   lse      [R] double out
  *   lse_rest [R] double out, given exactly if t_lse is
  * K = 0 with loss NULL computes lse alone (a teacher's t_lse).  Weight 0 gives
- * 0 in all outputs.  A row in which no listed token has mass (and t_lse is
- * absent or not finite), or no student logit is unmasked, has D = 0.  NaN or
+ * 0 in all outputs.  A row whose list has no mass and no t_lse beside it, whose
+ * t_lse is infinite, or in which no student logit is unmasked, has D = 0.  NaN or
  * +inf logits make the row's outputs NaN; a masked student token with p > 0
  * makes D +inf.  x_j beyond 2^40 ln 2 are out of fp64's reach: a row whose
  * largest x_j lies below -2^40 ln 2 (every logit the type's lowest value) has
