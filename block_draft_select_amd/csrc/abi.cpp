@@ -282,10 +282,10 @@ SamplePlan sample_plan(const dflash_rows& r) {
 }
 
 // The forward pass: 2048 blocks (eight per CU) if the rows have that much, and
-// more only because a block's segment is bounded.  The gradient: eight slots
-// a thread (213 us against 278 with two at 2048 x 151936 bf16, 13.3 against
-// 14.5 at 427 blocks) unless the grid then leaves CUs idle (80 blocks: 9.0
-// against 6.4).
+// more only because a block's segment is bounded.  The gradient: as many slots a
+// thread as fill its blocks and leave four, two, one of them per CU (with 1, 2,
+// 4, 8 slots: 512 x 151936 bf16 in 93, 68, 58, 57 us; 64 x 151936 in 16, 14, 14,
+// 14; 61 x 50021 in 8.0, 8.0, 8.4, 9.7; 2048 x 1000 in 9, 10, 14, 22).
 DistillPlan distill_plan(const dflash_rows& r) {
   DistillPlan p{};
   const int slots = row_slots(r), units = (slots + kDistillUnit - 1) / kDistillUnit;
@@ -294,9 +294,10 @@ DistillPlan distill_plan(const dflash_rows& r) {
   p.n_seg = (int)std::min<int64_t>(std::max<int64_t>(want, least), units);
   p.units = (units + p.n_seg - 1) / p.n_seg;
   p.n_seg = (units + p.units - 1) / p.units;
-  for (p.grad_loads = 8;; p.grad_loads = 2) {
-    p.grad_seg = (slots + kDistillThreads * p.grad_loads - 1) / (kDistillThreads * p.grad_loads);
-    if (p.grad_loads == 2 || r.R * p.grad_seg >= 256) break;
+  for (p.grad_loads = 8;; p.grad_loads /= 2) {
+    const int per_block = kDistillThreads * p.grad_loads;
+    p.grad_seg = (slots + per_block - 1) / per_block;
+    if (p.grad_loads == 1 || (slots >= per_block / 4 * 3 && r.R * p.grad_seg >= 128 * p.grad_loads)) break;
   }
   p.total = align256((size_t)r.R * p.n_seg * sizeof(DistillPart));
   return p;

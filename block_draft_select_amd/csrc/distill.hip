@@ -433,7 +433,38 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   }
   double c = -INFINITY, p_sum = 0.0;
   float own[kPerThread];  // the listed tokens' logits of this segment, read before anything is stored (dS may be S)
-  if (!off) {
+  if (!off && a.K <= kWave) {
+    // a short list: one wave, one barrier (61 x 50021 fp32, K = 64: 11.7 us, 13.3
+    // with the block's reductions)
+    if (tid < kWave) {
+      int idx = -1;
+      const bool in = tid < a.K && listed(a, row, tid, idx);
+      const double t = in ? (double)a.t_logit[row * a.K + tid] / a.tau : -INFINITY;
+      double p;
+      if (a.t_lse) {
+        c = teacher_lse<kWave>(red, a, row);
+        p = in && c != -INFINITY ? exp(t - c) : 0.0;
+      } else {
+        c = block_max<kWave>(red, t != t ? INFINITY : t);
+        const double e = in && c != -INFINITY ? exp(t - c) : 0.0;
+        const double all = block_sum<kWave>(red, e);
+        p = in ? e / all : 0.0;
+      }
+      if (tid < a.K) {
+        seen[tid] = in ? idx : -1;
+        prob[tid] = p;
+      }
+      if (in && idx >= e0 && idx < e1) own[0] = row_value<DT>(z, idx);
+      p_sum = block_sum<kWave>(red, p);
+      if (tid == 0) {
+        red.d[0] = p_sum;
+        red.d[1] = c;
+      }
+    }
+    __syncthreads();
+    p_sum = red.d[0];
+    c = red.d[1];
+  } else if (!off) {
     c = teacher_lse<kThreads>(red, a, row);
     if (c != -INFINITY) {
 #pragma unroll
@@ -523,6 +554,17 @@ hipError_t run_grad(const DistillArgs& a, const float* grad_loss, const double* 
   return hipGetLastError();
 }
 
+template <int DT>
+hipError_t run_grad_typed(const DistillArgs& a, const float* grad_loss, const double* lse, const double* rest, void* dS,
+                          int64_t d_stride, const DistillPlan& pl, hipStream_t st) {
+  switch (pl.grad_loads) {
+    case 1: return run_grad<DT, 1>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
+    case 2: return run_grad<DT, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
+    case 4: return run_grad<DT, 4>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
+    default: return run_grad<DT, 8>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_distill(int32_t dtype, const DistillArgs& a, float* loss, double* lse, double* rest, char* ws,
@@ -536,12 +578,8 @@ hipError_t launch_distill(int32_t dtype, const DistillArgs& a, float* loss, doub
 
 hipError_t launch_distill_grad(int32_t dtype, const DistillArgs& a, const float* grad_loss, const double* lse,
                                const double* rest, void* dS, int64_t d_stride, const DistillPlan& pl, hipStream_t st) {
-  if (dtype == DFLASH_BF16) {
-    return pl.grad_loads == 2 ? run_grad<DFLASH_BF16, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st)
-                         : run_grad<DFLASH_BF16, 8>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
-  }
-  return pl.grad_loads == 2 ? run_grad<DFLASH_F32, 2>(a, grad_loss, lse, rest, dS, d_stride, pl, st)
-                       : run_grad<DFLASH_F32, 8>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
+  if (dtype == DFLASH_BF16) return run_grad_typed<DFLASH_BF16>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
+  return run_grad_typed<DFLASH_F32>(a, grad_loss, lse, rest, dS, d_stride, pl, st);
 }
 
 }  // namespace dfk

@@ -471,6 +471,22 @@ def test_distill_and_gradient(dt, with_lse, R, V, K, pad, shift):
     _check_distill(s, idx, tl, t, tau, lse, w, g, pad, shift, inplace=True)
 
 
+@pytest.mark.parametrize("dt,R,V,K", [("bf16", 260, 1000, 16), ("bf16", 260, 4003, 100), ("bf16", 300, 8195, 64), ("bf16", 520, 16411, 16),
+                                     ("f32", 300, 4099, 65), ("f32", 520, 8203, 16)])
+def test_distill_and_gradient_of_many_rows(dt, R, V, K):
+    # one, two, four and eight slots a thread in the gradient
+    import torch
+    t = dict(bf16=torch.bfloat16, f32=torch.float32)[dt]
+    rng = np.random.default_rng(R + V + K)
+    s, teacher, idx, tl = _distill_case(rng, R, V, K, dup=True, pads=True, dtype=t)
+    w = rng.uniform(0.2, 2.0, size=R).astype(np.float32)
+    w[::7] = 0.0
+    _say(f"[rows] distill {dt} R={R} V={V} K={K}")
+    for with_lse in (False, True):
+        lse = np.array([O.log_sum_exp(x.astype(np.float64)) for x in teacher]) if with_lse else None
+        _check_distill(s, idx, tl, t, 1.0, lse, w, None, pad=V % 2, inplace=with_lse)
+
+
 @pytest.mark.parametrize("with_lse", [False, True])
 def test_distill_masked_and_empty_rows(with_lse):
     import torch
