@@ -34,7 +34,8 @@
 // A bf16 row with values out of the counters' range goes the second way, in
 // one block that reads the row as often as it needs.
 //
-// sample_apply_kernel (dflash_filter) copies the kept tokens.
+// sample_apply_kernel (dflash_filter) copies the kept tokens.  Short rows of
+// either type take (1) and (2) in one launch, a block a row: sample_row_kernel.
 //
 // Counts are exact and sums do not depend on the order of the atomics: every
 // 2^((t - rint(t)) / 8) is rounded to a multiple of 2^-42 (off by 2^-43 of
@@ -138,7 +139,8 @@ __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v) {
 
 // Reductions over the block with one barrier each: successive calls alternate
 // between two buffers, so a buffer is rewritten only after the barrier of the
-// call between, which every thread reaches after it has read the buffer.
+// call between, which every thread reaches after it has read the buffer.  What
+// is equal on all lanes goes to scalar registers.
 struct Red {
   double d[2][kWaves];
   uint32_t u[2][kWaves];
@@ -158,7 +160,7 @@ struct BlockOps {
     uint32_t r = s.u[flip][0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) r = min(r, s.u[flip][w]);
-    return (int)r;
+    return (int)__builtin_amdgcn_readfirstlane(r);
   }
   // inclusive scans, in fixed order
   __device__ __forceinline__ uint32_t scan(uint32_t v) {
@@ -210,7 +212,7 @@ struct BlockOps {
     v = s.d[flip][0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) v = fmax(v, s.d[flip][w]);
-    return v;
+    return readlane_f64(v, 0);
   }
   __device__ __forceinline__ uint32_t max(uint32_t v) {
     v = ::max(v, dpp_u32<kDppRowShr1>(v, 0u));
@@ -225,7 +227,7 @@ struct BlockOps {
     v = s.u[flip][0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) v = ::max(v, s.u[flip][w]);
-    return v;
+    return __builtin_amdgcn_readfirstlane(v);
   }
   __device__ __forceinline__ uint32_t sum(uint32_t v) {
     v = wave_scan_u32(v);
@@ -235,7 +237,7 @@ struct BlockOps {
     v = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v += s.u[flip][w];
-    return v;
+    return __builtin_amdgcn_readfirstlane(v);
   }
 
 };
@@ -299,6 +301,7 @@ __device__ __forceinline__ void add_cells(unsigned long long* cells, const Slot 
   constexpr float kMax = RowType<DT>::kMax;
   const double c8 = rp.c8;
   unsigned long long* cell = cells + (threadIdx.x & (kCols - 1));
+  uint32_t tail = 0;  // counted aside: a mask of finite lowest values would queue up at one address
   if (fabs(J) <= 0x1p20) {
     // rint by adding 3 2^51, whose sum's lower word is the integer.  Tokens far
     // below the maximum are raised to 1000 bins below it: the tail all the same
@@ -312,8 +315,11 @@ __device__ __forceinline__ void add_cells(unsigned long long* cells, const Slot 
         const float v = slot_value<DT>(x[l], i);
         if (v > kNegInf) {
           const double t = (double)__builtin_amdgcn_fmed3f(v, lowest, kMax) * c8, r = t + kMagic;
-          const uint32_t b = min((uint32_t)(j - (int)(uint32_t)__double_as_longlong(r)), (uint32_t)kTail);
-          atomicAdd(&cell[b * kCols], cell_of(t - (r - kMagic)));
+          const uint32_t b = (uint32_t)(j - (int)(uint32_t)__double_as_longlong(r));
+          if (b < (uint32_t)kTail)
+            atomicAdd(&cell[b * kCols], cell_of(t - (r - kMagic)));
+          else
+            ++tail;
         }
       }
   } else {
@@ -325,9 +331,16 @@ __device__ __forceinline__ void add_cells(unsigned long long* cells, const Slot 
         if (k == e) v = slot_value<DT>(x[k / VE], k % VE);
       if (v > kNegInf) {
         const double t = (double)fminf(v, kMax) * c8, n = rint(t);
-        atomicAdd(&cell[(int)fmin(J - n, (double)kTail) * kCols], cell_of(t - n));
+        if (J - n < (double)kTail)
+          atomicAdd(&cell[(int)(J - n) * kCols], cell_of(t - n));
+        else
+          ++tail;
       }
     }
+  }
+  if (__ballot(tail != 0)) {
+    tail = wave_sum_u32(tail);
+    if (lane_id() == 0) atomicAdd(&cells[kTail * kCols + ((threadIdx.x >> 6) & (kCols - 1))], (unsigned long long)tail << kCellCount);
   }
 }
 
@@ -509,6 +522,7 @@ struct Finalize {
   double bmass;
   int b0, b1;
   uint32_t lo;
+  uint32_t seen_lo, seen_hi;  // the last pass's least and largest key
 
   // weight of a key relative to 2^(J / 8)
   __device__ __forceinline__ double weight(uint32_t key) const {
@@ -533,7 +547,8 @@ struct Finalize {
         s.to[tid] = B1 == kTail || l1 >= nb ? n_all : l1 < 0 ? 0u : upto[l1];  // the last bin: all that is left
       }
       __syncthreads();
-      const int per = n_seg <= 16 ? 5 : 4;  // log2 of the threads a segment
+      const bool lots = s.cc[B1 + 1] - s.cc[B0] > 1024u * (uint32_t)n_seg;  // then all threads on one segment after the other
+      const int per = lots ? 9 : n_seg <= 16 ? 5 : 4;  // log2 of the threads a segment
       for (int g = tid >> per; g < n_seg; g += kThreads >> per) {
         const uint64_t* list = lists + (size_t)g * cap;
         const int end = (int)s.to[g];
@@ -570,6 +585,9 @@ struct Finalize {
     if (tid == 0) s.n = 0;
     __syncthreads();
     const bool weigh = !by_index && B1 != kTail;
+    uint32_t least = 0xFFFFFFFFu, most = 0;
+    // so many tokens in one bin that equal ones may queue up at one address
+    const bool queue = (MODE == kAll || MODE == kSecond) && s.cc[B1 + 1] - s.cc[B0] > 16384u;
     each(B0, B1, [&](uint64_t c) {
       const uint32_t key = comp_key(c), idx = (uint32_t)c;
       if (key < klo || key > khi || idx < ilo || idx > ihi) return;
@@ -578,13 +596,27 @@ struct Finalize {
         if (i < (uint32_t)kThreads) s.win[i] = c;
       } else {
         const uint32_t b = (by_index ? idx - ilo : khi - key) >> sh;
-        atomicAdd(&s.cnt[b], 1u);
-        if (weigh) {
-          const double t = key_value(key) * c8;
-          atomicAdd((unsigned long long*)&s.mass[b], exp2_eighth_units(t - rint(t)));  // sums of 2^21 tokens fit 64 bits
+        least = min(least, key);
+        most = max(most, key);
+        uint32_t many = 1;
+        if (queue) {  // one addition for a wave of equal tokens
+          const uint64_t lanes = __ballot(1);
+          if (__ballot(b != (uint32_t)__builtin_amdgcn_readfirstlane(b) || key != (uint32_t)__builtin_amdgcn_readfirstlane(key)) == 0)
+            many = lane_id() == __builtin_ctzll(lanes) ? (uint32_t)__popcll(lanes) : 0u;
+        }
+        if (many) {
+          atomicAdd(&s.cnt[b], many);
+          if (weigh) {
+            const double t = key_value(key) * c8;
+            atomicAdd((unsigned long long*)&s.mass[b], many * exp2_eighth_units(t - rint(t)));  // sums of 2^21 tokens fit 64 bits
+          }
         }
       }
     });
+    if (sh >= 0 && !by_index) {
+      seen_lo = ~ops.max(~least);
+      seen_hi = ops.max(most);
+    }
     __syncthreads();
   }
 
@@ -594,7 +626,7 @@ struct Finalize {
   // (512 tokens against all: 15 thousand cycles, 6 us)
   __device__ __forceinline__ void open_window(uint32_t lo_, uint32_t hi, uint32_t base_, double bmass_, int b0_, int b1_) {
     lo = lo_, base = base_, bmass = bmass_, b0 = b0_, b1 = b1_;
-    n = min(s.n, (uint32_t)kThreads);
+    n = min((uint32_t)__builtin_amdgcn_readfirstlane(s.n), (uint32_t)kThreads);
     const bool in = tid < (int)n;
     const uint64_t mine = in ? s.win[tid] : 0;
     uint32_t from = 0, to = n, rank = 0;
@@ -678,7 +710,7 @@ struct Finalize {
       s.n = c;
     }
     __syncthreads();
-    return s.n;
+    return __builtin_amdgcn_readfirstlane(s.n);
   }
 
   __device__ __forceinline__ Cross locate(int kind, double amount) {
@@ -702,8 +734,8 @@ struct Finalize {
     if (b < b0 || b > b1) {
       uint32_t klo = b == kTail ? kKeyLowest : lowest_key(J - b, c8, t8);
       uint32_t khi = b == 0 ? kmax : lowest_key(J - b + 1.0, c8, t8) - 1u;
-      uint32_t cb = s.cc[b], nc = s.cc[b + 1] - cb;
-      double mb = s.cm[b];
+      uint32_t cb = __builtin_amdgcn_readfirstlane(s.cc[b]), nc = __builtin_amdgcn_readfirstlane(s.cc[b + 1]) - cb;
+      double mb = readlane_f64(s.cm[b], 0);
       if (nc == 0) return Cross{cb, mb, ((uint64_t)~khi) << 32, 0};  // kByWeight: nothing in the threshold's own bin
       int B0 = b;
       bool whole = true;
@@ -771,11 +803,13 @@ struct Finalize {
           q = ops.first((uint32_t)tid < n_part && (double)c1 >= amount);
         }
         nc = part_of(q, c1, m1, c, mass);
-        cb = s.before_n;
-        mb = s.before_m;
+        cb = __builtin_amdgcn_readfirstlane(s.before_n);
+        mb = readlane_f64(s.before_m, 0);
         khi -= (uint32_t)q << sh;
         if ((uint32_t)q + 1 < n_part) klo = khi - ((1u << sh) - 1u);
         if (nc == 0) return Cross{cb, mb, ((uint64_t)~khi) << 32, 0};  // kByWeight: the threshold falls between tokens
+        khi = min(khi, seen_hi);
+        klo = max(klo, seen_lo);
       }
       if (MODE == kOne && whole) {
         open_bins(klo, cb, mb, B0, b, nc);
@@ -926,7 +960,9 @@ __device__ __forceinline__ double row_uniform(const SampleOut& o, int64_t row) {
 
 // One block a row: bound by the latency of its steps (the segments' bins as
 // other blocks left them in memory, then scans, windows and searches).  One row
-// of 151936 fp32 takes 16 us, 256 of 262144 23 and 31 (kFirst and kSecond).
+// of 151936 fp32 takes 15 to 17 us, 256 of 262144 18 and 24 (kFirst and kSecond,
+// which at 128 registers keeps two blocks a CU: 1024 rows of 32000 in 70 us, 95
+// with one).
 template <int MODE>
 __global__ __launch_bounds__(kThreads, MODE == kSecond ? 4 : 2) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap, uint32_t ask_cap,
                                                                    const SamplePart* __restrict__ parts,
@@ -987,7 +1023,7 @@ __global__ __launch_bounds__(kThreads, MODE == kSecond ? 4 : 2) void sample_fina
   Finalize<DFLASH_F32, MODE> f{s, ops, RowRef<DFLASH_F32>(a.Z, row, a.stride, a.V), part, lists + (size_t)blockIdx.x * n_seg * cap,
                                MODE == kSecond ? asked + (size_t)blockIdx.x * ask_cap : nullptr,
                                MODE == kSecond ? asks + blockIdx.x : nullptr, ask_cap, n_seg, cap, rp.c8, rp.t8, J, tid, kmax, listed,
-                               0, 0, 0.0, 1, 0, 0};
+                               0, 0, 0.0, 1, 0, 0, 0, 0};
   const double wmax = f.weight(kmax);
   if constexpr (MODE == kFirst) {
     if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, kmax, listed, ask_cap, asks[blockIdx.x])) return;
@@ -1021,8 +1057,8 @@ __device__ __forceinline__ void store_filtered(typename RowType<DT>::elem* o, in
 
 // A row of up to 8192 tokens in one block, NL slots a thread: bins, list and
 // answer stay in LDS, and the filtered row is written at once.  Bound by the
-// chain of steps: one row of 1024 fp32 takes 7.9 us (12.9 in two launches), 2048
-// rows 39 (82); one row of 8000 11 (15), 2048 rows 159 (180).
+// chain of steps: one row of 1024 fp32 takes 8.1 us (12.9 in two launches), 2048
+// rows 40 (82); one row of 8000 12 (15), 2048 rows 165 (180).
 template <int DT, int NL>
 __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, SampleOut o) {
   constexpr int VE = RowType<DT>::VE;
@@ -1077,7 +1113,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, S
       }
     __syncthreads();
     const uint32_t kmax = key_of(m, kMax);
-    Finalize<DT, kOne> fin{s, ops, z, nullptr, list, nullptr, nullptr, 0, 1, 0, c8, rp.t8, J, tid, kmax, kBins, 0, 0, 0.0, 1, 0, 0};
+    Finalize<DT, kOne> fin{s, ops, z, nullptr, list, nullptr, nullptr, 0, 1, 0, c8, rp.t8, J, tid, kmax, kBins, 0, 0, 0.0, 1, 0, 0, 0, 0};
     fin.answer(rp, s.cc[kBins], fin.weight(kmax), u, row, o, &cut);
   }
   if (o.out) {
@@ -1691,7 +1727,7 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
   }
   __syncthreads();
   const uint32_t kmax = key_of(m, kMax);
-  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, 0, c8, rp.t8, J, tid, kmax, 0, 0, 0, 0.0, 1, 0, 0};
+  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, 0, c8, rp.t8, J, tid, kmax, 0, 0, 0, 0.0, 1, 0, 0, 0, 0};
   f.answer(rp, s.cc[kBins], f.weight(kmax), row_uniform(o, row), row, o, cut_out);
 }
 

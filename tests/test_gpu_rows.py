@@ -106,6 +106,8 @@ def _logits(rng, R, V, kind):
         z[rng.random(size=z.shape) < 0.7] = -3.0e38
     if kind == "shifted":
         z += 5000.0
+    if kind == "constant":
+        z[:] = z[:, :1]
     return z.astype(np.float32)
 
 
@@ -209,7 +211,7 @@ def test_sample_longest_vocabulary():
     _check_sample(np.zeros((1, 2097152), dtype=np.float32), torch.float32, [dict(top_p=0.5)], np.array([0.75]))
 
 
-@pytest.mark.parametrize("kind", ["flat", "peaked", "ties", "masked", "shifted"])
+@pytest.mark.parametrize("kind", ["flat", "peaked", "ties", "masked", "shifted", "lowest", "constant"])
 @pytest.mark.parametrize("R,V", [(260, 16003), (420, 16003), (520, 15998), (1030, 5003), (1300, 5003), (345, 40009)])
 def test_sample_f32_rows_in_long_segments(kind, R, V):
     # many fp32 rows: segments of 2, 4 and 8 slots a thread list only their
