@@ -1731,9 +1731,9 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
   f.answer(rp, s.cc[kBins], f.weight(kmax), row_uniform(o, row), row, o, cut_out);
 }
 
-// One row takes 13 us, 512 rows 30: a chain of steps whose latency counts.  Of
-// 29 thousand cycles for a row of 151936 the segments' counters take 9.5, the
-// weights 2.5, scans 3.7, a query 3 to 5 and the token's index 6 (in another
+// One row takes 13 us, 512 rows 29: a chain of steps whose latency counts.  Of
+// 25 thousand cycles for a row of 151936 the segments' counters take 7, the
+// weights 2.4, the scan 3.3, a query 3 to 5 and the token's index 6 (in another
 // block's segment).  Runs of items a thread took the weights there from 11; a
 // separate kernel for rows that have to be binned costs the others a launch (5
 // us).
