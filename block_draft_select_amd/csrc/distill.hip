@@ -137,6 +137,11 @@ __device__ __forceinline__ bool listed(const DistillArgs& a, int64_t row, int k,
   return idx >= 0 && idx < a.V;
 }
 
+// the largest t_k / tau of a list: -inf if it lies below the range, NaN above it
+__device__ __forceinline__ double in_range(double m) {
+  return m <= -kRange * kLn2 ? -INFINITY : m < kRange * kLn2 ? m : (double)NAN;
+}
+
 // the teacher's normaliser c (natural log); -inf: the teacher's row is empty
 template <int T>
 __device__ __forceinline__ double teacher_lse(Red& red, const DistillArgs& a, int64_t row) {
@@ -151,8 +156,8 @@ __device__ __forceinline__ double teacher_lse(Red& red, const DistillArgs& a, in
       const double t = (double)a.t_logit[row * a.K + k] / a.tau;
       m = t != t ? INFINITY : fmax(m, t);
     }
-  m = block_max<T>(red, m);
-  if (m == -INFINITY) return m;
+  m = in_range(block_max<T>(red, m));
+  if (!(fabs(m) < INFINITY)) return m;
   double s = 0.0;
   for (int k = threadIdx.x; k < a.K; k += T)
     if (listed(a, row, k, idx)) s += exp((double)a.t_logit[row * a.K + k] / a.tau - m);
@@ -445,7 +450,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
         c = teacher_lse<kWave>(red, a, row);
         p = in && c != -INFINITY ? exp(t - c) : 0.0;
       } else {
-        c = block_max<kWave>(red, t != t ? INFINITY : t);
+        c = in_range(block_max<kWave>(red, t != t ? INFINITY : t));
         const double e = in && c != -INFINITY ? exp(t - c) : 0.0;
         const double all = block_sum<kWave>(red, e);
         p = in ? e / all : 0.0;

@@ -460,7 +460,8 @@ dflash_status dflash_filter(const dflash_rows* r, const void* Z, const dflash_fi
  * +inf logits make the row's outputs NaN; a masked student token with p > 0
  * makes D +inf.  x_j beyond 2^40 ln 2 are out of fp64's reach: a row whose
  * largest x_j lies below -2^40 ln 2 (every logit the type's lowest value) has
- * nothing unmasked, and an x_j above 2^40 ln 2 counts as +inf. */
+ * nothing unmasked, and an x_j above 2^40 ln 2 counts as +inf; so do, without
+ * t_lse, the list's t_k / tau. */
 dflash_status dflash_distill(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
                              const float* t_logit, const double* t_lse_opt, const float* weight_opt, float* loss_opt,
                              double* lse, double* lse_rest_opt, void* ws, size_t ws_bytes, void* stream);

@@ -543,6 +543,20 @@ def test_rows_of_the_types_lowest_value(dt):
     assert torch.isnan(lse).all()
 
 
+@pytest.mark.parametrize("K", [2, 40, 100])
+def test_lists_of_the_lowest_value(K):
+    # a teacher's list that a finite mask leaves without mass, and one with some
+    import torch
+    rng = np.random.default_rng(64)
+    s, _, idx, tl = _distill_case(rng, 4, 500, K, False, False, None)
+    tl[0] = tl[2] = -3.0e38
+    tl[2, 1] = 0.5
+    tl[3] = -np.inf
+    for t in (torch.bfloat16, torch.float32):
+        _check_distill(s, idx, tl, t, 0.7, None, None, None)
+        _check_distill(s, idx, tl, t, 0.7, np.full(4, 6.0), None, None)
+
+
 def test_rows_past_32_bit_offsets():
     # two rows 2^31 elements apart
     import torch
