@@ -435,7 +435,7 @@ def _check_distill(s, idx, tl, dtype, tau, t_lse_np, weight_np, g_np, pad=0, shi
         if rest is not None:
             assert near(float(rest[i]), ref["lse_rest"]), (i, float(rest[i]), ref["lse_rest"])
         want = w * ref["loss"]
-        size = abs(w) * (1.0 + abs(ref["lse"]) + np.abs(tl[i][np.isfinite(tl[i])] / tau).max(initial=0.0))
+        size = abs(w) * (1.0 + abs(ref["lse"]) + np.abs(tl[i][np.abs(tl[i]) < 1e30] / tau).max(initial=0.0))
         assert float(loss[i]) == want or abs(float(loss[i]) - want) <= abs(want) * 2.0 ** -24 + 1e-10 * size + 2.0 ** -149, \
             (i, float(loss[i]), want)
         f = abs(w * g)
