@@ -498,7 +498,7 @@ struct Cross {
   uint32_t n;    // tokens up to and including the crossing one (kByWeight: tokens that pass)
   double cum;    // their weight
   uint64_t cut;  // a token is among them iff its (~key, index) is below this
-  uint64_t at;   // (~key, index) of the last of them (not for kByWeight)
+  uint64_t at;   // (~key, index) of the last of them (not for kByWeight); 0: none at hand (a bin that kFirst has not listed)
 };
 
 template <int DT, int MODE>
@@ -859,7 +859,9 @@ struct Finalize {
           Z = x.cum;
           cut = x.cut;
         }
-      } else if (q == 4 || x.n <= kept) {
+      } else if (q == 4 || (x.n <= kept && x.at != 0)) {
+        // (u next to 1 may cross behind the kept tokens, where kFirst need not have
+        // listed any: such a crossing counts only those before it)
         if (tid == 0) {
           o.token[row] = (int32_t)(uint32_t)x.at;
           if (o.prob) o.prob[row] = (float)(weight(comp_key(x.at)) / Z);
