@@ -1143,8 +1143,9 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, i
   __syncthreads();
   const RowRef<DT> z(a.Z, row0 + r, a.stride, a.V);
   const int s0 = seg * (kThreads * NL) + tid;
+  // a range may hold no key at all: at a tiny T values are bins apart
   const uint32_t l0 = ask.klo[0], w0 = ask.khi[0] - l0, l1 = ask.klo[1], w1 = ask.khi[1] - l1;
-  const bool two = ask.b1[1] >= 0;
+  const bool one = ask.khi[0] >= l0, two = ask.khi[1] >= l1;
   Slot x[NL];
 #pragma unroll
   for (int l = 0; l < NL; ++l) x[l] = z.load(s0 + l * kThreads);
@@ -1155,7 +1156,7 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, i
     for (int i = 0; i < VE; ++i) {
       const float v = slot_value<DT>(x[l], i);
       const uint32_t key = key_of(v, RowType<DT>::kMax);
-      hits |= (uint32_t)(v > kNegInf && (key - l0 <= w0 || (two && key - l1 <= w1))) << i;
+      hits |= (uint32_t)(v > kNegInf && ((one && key - l0 <= w0) || (two && key - l1 <= w1))) << i;
     }
     if (hits) {
       uint32_t i = atomicAdd(&n, (uint32_t)__popc(hits));

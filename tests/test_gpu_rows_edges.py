@@ -6,7 +6,7 @@ the smallest tau, and every plan of the launches.  Bars as in test_gpu_rows.
 import numpy as np
 import pytest
 
-from test_gpu_rows import _check_sample, _say
+from test_gpu_rows import _check_sample, _logits, _say
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,16 @@ def test_draw_of_the_last_token_before_a_gap(dt, R, V):
     st = [dict(top_k=5), dict(min_p=0.5), dict(top_p=0.4), dict(top_k=5, top_p=0.99)]
     u = [1.0, LAST, 7.0, 0.999]
     _check_sample(z, _type(dt), [st[i % 4] for i in range(R)], np.array([u[i // 4 % 4] for i in range(R)]), pad=1)
+
+
+@pytest.mark.parametrize("V,n", [(100003, 400), (100003, 3000)])
+def test_temperature_that_leaves_bins_without_a_value(V, n):
+    # T = 1e-7: fp32 values near 8 are 55 bins apart, so the bin of min-p's
+    # border holds no value at all; the row's end holds more equal tokens than a
+    # segment lists
+    R = 64
+    rng = np.random.default_rng(n)
+    z = np.minimum(_logits(rng, R, V, "flat"), np.float32(7.0))
+    z[:, V - 2 * n:V:2] = 8.0
+    _say(f"[rows] empty bins {V} {n}")
+    _check_sample(z, _type("f32"), [dict(T=1e-7, min_p=[0.5, 0.3, 1e-3][i % 3]) for i in range(R)], rng.random(R), pad=1)
