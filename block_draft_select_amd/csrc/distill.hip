@@ -502,6 +502,10 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   // the base are rounded once (fma), the low halves are added after
   const double c2 = kLog2e64 / a.tau, b2 = base * kLog2e64;
   const float ch = (float)c2, cl = (float)(c2 - (double)ch), bh = (float)b2, bl = (float)(b2 - (double)bh);
+  // Logits whose exponential is 0 are raised to 2^-256 of the base's (or below, by
+  // as much as rounding moves the border): a mask of finite lowest values over a
+  // small tau would leave fp32 in both products, with either sign
+  const float least = (float)fmax((b2 - 256.0 - fabs(b2) * 0x1p-22) / c2, -3.4028234663852886e38);
 #pragma unroll
   for (int l = 0; l < NL; ++l) {
     Slot y;
@@ -510,7 +514,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
       const float v = slot_value<DT>(x[l], i);
-      const float t = fmaf(v, ch, -bh) + fmaf(v, cl, -bl);
+      const float r = fmaxf(v, least), t = fmaf(r, ch, -bh) + fmaf(r, cl, -bl);
       const float g = v == kNegInf ? 0.0f : G * __builtin_amdgcn_exp2f(t);
       if constexpr (DT == DFLASH_BF16)
         y.w[i >> 1] |= bf16_round(g) << ((i & 1) * 16);

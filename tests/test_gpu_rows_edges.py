@@ -6,7 +6,8 @@ the smallest tau, and every plan of the launches.  Bars as in test_gpu_rows.
 import numpy as np
 import pytest
 
-from test_gpu_rows import _check_sample, _logits, _say
+from oracle import rows as O
+from test_gpu_rows import _check_distill, _check_sample, _distill_case, _logits, _say
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,24 @@ def test_temperature_that_leaves_bins_without_a_value(V, n):
     z[:, V - 2 * n:V:2] = 8.0
     _say(f"[rows] empty bins {V} {n}")
     _check_sample(z, _type("f32"), [dict(T=1e-7, min_p=[0.5, 0.3, 1e-3][i % 3]) for i in range(R)], rng.random(R), pad=1)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [3e-8, 3e-10, 1e-12, 1e-25])
+@pytest.mark.parametrize("with_lse", [False, True])
+def test_gradient_beside_lowest_values_at_a_small_tau(dt, tau, with_lse):
+    import torch
+    t = _type(dt)
+    rng = np.random.default_rng(71)
+    R, V, K = 4, 3001, 6
+    s, teacher, idx, tl = _distill_case(rng, R, V, K, False, False, None)
+    s, teacher, tl = s * np.float32(tau), teacher * np.float32(tau), tl * np.float32(tau)
+    gone = rng.random(size=s.shape) < 0.6
+    np.put_along_axis(gone, idx.astype(np.int64), False, 1)
+    s[gone] = float(torch.finfo(t).min)
+    s[1, gone[1]] = -np.inf
+    _say(f"[rows] lowest values at tau {tau} {dt}")
+    lse = np.array([O.log_sum_exp(x.astype(np.float64) / tau) for x in teacher]) if with_lse else None
+    g = np.full(R, tau, dtype=np.float32)
+    _check_distill(s, idx, tl, t, tau, lse, None, g)
+    _check_distill(s, idx, tl, t, tau, lse, None, g, pad=1, inplace=True)
