@@ -497,10 +497,14 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   const double p_rest = with_rest ? fmax(1.0 - p_sum, 0.0) : 0.0;
   const double A = p_sum + p_rest;
   const double base = with_rest ? rest : lse;
-  const float G = (float)(f * (with_rest ? A * exp(rest - lse) - p_rest : A));
+  // the factor; one near fp32's end leaves its power of two to the exponent, so
+  // that unlikely tokens' gradients, which fit, do not become inf times 0
+  const double G64 = f * (with_rest ? A * exp(rest - lse) - p_rest : A);
+  const int up = fabs(G64) >= 0x1p100 && fabs(G64) < INFINITY ? ilogb(G64) : 0;
+  const float G = (float)ldexp(G64, -up);
   // x_j - base in two pieces of fp32: the product s c and its difference from
   // the base are rounded once (fma), the low halves are added after
-  const double c2 = kLog2e64 / a.tau, b2 = base * kLog2e64;
+  const double c2 = kLog2e64 / a.tau, b2 = base * kLog2e64 - up;
   const float ch = (float)c2, cl = (float)(c2 - (double)ch), bh = (float)b2, bl = (float)(b2 - (double)bh);
   // Logits whose exponential is 0 are raised to 2^-256 of the base's (or below, by
   // as much as rounding moves the border): a mask of finite lowest values over a

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from oracle import rows as O
-from test_gpu_rows import _check_distill, _check_sample, _distill_case, _logits, _say
+from test_gpu_rows import _check_distill, _check_sample, _distill_case, _f64, _logits, _run_distill, _say, _tensor
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,37 @@ def test_gradient_beside_lowest_values_at_a_small_tau(dt, tau, with_lse):
     g = np.full(R, tau, dtype=np.float32)
     _check_distill(s, idx, tl, t, tau, lse, None, g)
     _check_distill(s, idx, tl, t, tau, lse, None, g, pad=1, inplace=True)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("with_lse", [False, True])
+def test_gradient_whose_factor_leaves_fp32(dt, with_lse):
+    # weight times grad_loss over tau lies beyond fp32, the gradients of unlikely tokens within
+    t = _type(dt)
+    rng = np.random.default_rng(72)
+    R, V, K, tau = 3, 2000, 5, 1e-30
+    s, teacher, idx, tl = _distill_case(rng, R, V, K, False, False, None)
+    s, tl = s * np.float32(tau * 4), tl * np.float32(tau)
+    s[:, 700:900] = -1.0
+    lse = np.array([O.log_sum_exp(x.astype(np.float64)) for x in teacher]) if with_lse else None
+    import torch
+    dev = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    v, _ = _tensor(s, t)
+    w, g = np.full(R, 1e10, dtype=np.float32), np.array([1.0, -1.0, 1e5], dtype=np.float32)
+    _, _, _, dS = _run_distill(v, dev(idx), dev(tl), tau, dev(lse), dev(w), dev(g))
+    got, zz, some_big = _f64(dS), _f64(v), False
+    for i in range(R):
+        ref = O.distill(zz[i], idx[i], tl[i], tau, None if lse is None else lse[i])
+        want = float(w[i]) * float(g[i]) * ref["grad"]
+        off = ref["p"] == 0
+        assert not np.isnan(got[i]).any() and not got[i][700:900][off[700:900]].any()
+        big = off & (np.abs(want) > 1.01 * float(torch.finfo(t).max))
+        small = off & (np.abs(want) < 0.99 * float(torch.finfo(t).max))
+        some_big |= bool(big.any())
+        assert small.any()
+        assert np.array_equal(got[i][big], np.sign(want[big]) * np.inf)
+        half = torch.finfo(t).eps / 2
+        x = zz[i] / tau
+        tt = np.minimum(np.abs(x - ref["lse"]) / np.log(2), 2.0 ** 30)
+        assert (np.abs(got[i] - want)[small] <= (np.abs(want) * (half + (tt + 4) * 2.0 ** -23))[small] + 2.0 ** -125).all()
+    assert some_big
