@@ -362,10 +362,14 @@ dflash_status check_out(const dflash_rows& r, const void* in, const void* out, i
   const uintptr_t nb = ((uintptr_t)(r.R - 1) * (r.R > 1 ? stride : 0) + r.V) * es;
   if (a < b + nb && b < a + na) {
     // rows side by side in one allocation do not meet if the strides agree
-    // and one tensor's rows lie in the other's gaps
-    const uintptr_t row = (uintptr_t)r.stride * es, d = (a < b ? b - a : a - b) % row, v = (uintptr_t)r.V * es;
-    if (r.R <= 1 || stride != r.stride || d < v || row - d < v)
-      return fail(DFLASH_ERR_INVALID_ARG, std::string(name) + " overlaps its input (equal address and stride are allowed)");
+    // and one tensor's rows lie in the other's gaps (the stride of several rows is
+    // at least V; that of one row may be 0)
+    bool apart = false;
+    if (r.R > 1 && stride == r.stride) {
+      const uintptr_t row = (uintptr_t)r.stride * es, d = (a < b ? b - a : a - b) % row, v = (uintptr_t)r.V * es;
+      apart = d >= v && row - d >= v;
+    }
+    if (!apart) return fail(DFLASH_ERR_INVALID_ARG, std::string(name) + " overlaps its input (equal address and stride are allowed)");
   }
   return DFLASH_OK;
 }

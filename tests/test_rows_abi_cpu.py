@@ -134,6 +134,19 @@ def test_overlapping_outputs_are_refused(dfl):
             assert b"overlaps" in dfl.lib.dflash_last_error()
 
 
+@pytest.mark.parametrize("stride", [0, 100, -7])
+def test_one_rows_overlapping_output_is_refused(dfl, stride):
+    # one row's stride may be anything, 0 too
+    r = _rows(dfl, R=1, stride=stride, V=100)
+    at = lambda e: ctypes.c_void_p(0x100000 + 2 * e)  # noqa: E731
+    for call, out in ((_filter, "out"), (_grad, "dS")):
+        src = {"Z" if call is _filter else "S": at(0)}
+        for e in (1, 50, -99):
+            for own in (stride, 100):
+                assert call(dfl, r, **src, **{out: at(e)}, stride=own) == 1, (e, own)
+                assert b"overlaps" in dfl.lib.dflash_last_error()
+
+
 def test_empty_calls_launch_nothing(dfl):
     r = _rows(dfl, R=0)
     assert _ws(dfl, r) == (0, 0)
