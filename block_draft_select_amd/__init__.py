@@ -8,6 +8,7 @@ library has not been built (``python block_draft_select_amd/build.py``).
 """
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -406,10 +407,13 @@ def _call(fn, device, stream, *args):
 
 
 def _filters(r, device, T, top_k, top_p, min_p, group):
-    n = -(-r.R // group) if group >= 1 else 0
+    group = operator.index(group)  # the arrays' lengths are checked against it: neither rounded nor wrapped
+    if not 1 <= group < 1 << 31:
+        raise ValueError(f"group must lie in [1, 2^31), got {group}")
+    n = -(-r.R // group)
     return dflash_filters(_vec(T, "T", torch.float32, n, device, True), _vec(top_k, "top_k", torch.int32, n, device, True),
                           _vec(top_p, "top_p", torch.float32, n, device, True),
-                          _vec(min_p, "min_p", torch.float32, n, device, True), int(group))
+                          _vec(min_p, "min_p", torch.float32, n, device, True), group)
 
 
 def dflash_sample(r, Z, u, token, ws, T=None, top_k=None, top_p=None, min_p=None, group=1, prob=None, kept=None,

@@ -177,6 +177,18 @@ def test_rows_of_tensors(dfl):
         dfl.rows(z.half())
 
 
+@pytest.mark.parametrize("group,error", [(1.5, TypeError), (9.0, TypeError), (0, ValueError), (-3, ValueError),
+                                         ((1 << 32) + 1, ValueError), (1 << 31, ValueError), (None, TypeError)])
+def test_groups_that_are_no_positive_int32_are_refused(dfl, group, error):
+    # a group that the call rounded or wrapped would read settings behind their array
+    z = torch.zeros(12, 10)
+    r = dfl.rows(z)
+    with pytest.raises(error, match="group|integer"):
+        dfl.dflash_sample(r, z, None, None, None, group=group)
+    with pytest.raises(error, match="group|integer"):
+        dfl.dflash_filter(r, z, z, None, group=group)
+
+
 def test_kernel_names(dfl):
     for i, n in enumerate(dfl.KERNELS):
         assert dfl.lib.dflash_kernel_name(i) == n.encode()
