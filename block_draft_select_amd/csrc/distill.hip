@@ -137,6 +137,12 @@ __device__ __forceinline__ bool listed(const DistillArgs& a, int64_t row, int k,
   return idx >= 0 && idx < a.V;
 }
 
+// t_k / tau of a list entry; +inf is no logit: NaN
+__device__ __forceinline__ double scaled(const DistillArgs& a, int64_t row, int k) {
+  const float t = a.t_logit[row * a.K + k];
+  return t < INFINITY ? (double)t / a.tau : (double)NAN;
+}
+
 // the largest t_k / tau of a list: -inf if it lies below the range, NaN above it
 __device__ __forceinline__ double in_range(double m) {
   return m <= -kRange * kLn2 ? -INFINITY : m < kRange * kLn2 ? m : (double)NAN;
@@ -153,14 +159,14 @@ __device__ __forceinline__ double teacher_lse(Red& red, const DistillArgs& a, in
   int idx;
   for (int k = threadIdx.x; k < a.K; k += T)
     if (listed(a, row, k, idx)) {
-      const double t = (double)a.t_logit[row * a.K + k] / a.tau;
+      const double t = scaled(a, row, k);
       m = t != t ? INFINITY : fmax(m, t);
     }
   m = in_range(block_max<T>(red, m));
   if (!(fabs(m) < INFINITY)) return m;
   double s = 0.0;
   for (int k = threadIdx.x; k < a.K; k += T)
-    if (listed(a, row, k, idx)) s += exp((double)a.t_logit[row * a.K + k] / a.tau - m);
+    if (listed(a, row, k, idx)) s += exp(scaled(a, row, k) - m);
   return m + log(block_sum<T>(red, s));
 }
 
@@ -383,7 +389,7 @@ __global__ __launch_bounds__(T) void distill_loss_kernel(DistillArgs a, int n_se
     for (int k = tid; k < a.K; k += T) {
       int idx;
       if (!listed(a, row, k, idx)) continue;
-      const double logp = (double)a.t_logit[row * a.K + k] / a.tau - c;
+      const double logp = scaled(a, row, k) - c;
       const double p = exp(logp);
       p_sum += p;
       if (p != 0.0) d += p * (logp - (double)row_value<DT>(z, idx) / a.tau + lse);
@@ -444,7 +450,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
     if (tid < kWave) {
       int idx = -1;
       const bool in = tid < a.K && listed(a, row, tid, idx);
-      const double t = in ? (double)a.t_logit[row * a.K + tid] / a.tau : -INFINITY;
+      const double t = in ? scaled(a, row, tid) : -INFINITY;
       double p;
       if (a.t_lse) {
         c = teacher_lse<kWave>(red, a, row);
@@ -478,7 +484,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
         if (k < a.K) {
           int idx;
           const bool in = listed(a, row, k, idx);
-          const double p = in ? exp((double)a.t_logit[row * a.K + k] / a.tau - c) : 0.0;
+          const double p = in ? exp(scaled(a, row, k) - c) : 0.0;
           p_sum += p;
           seen[k] = in ? idx : -1;
           prob[k] = p;

@@ -89,6 +89,7 @@ def distill(s, t_idx, t_logit, tau=1.0, t_lse=None):
     x = s / tau
     ok = (t_idx >= 0) & (t_idx < V)
     idx, t = np.asarray(t_idx)[ok].astype(np.int64), np.asarray(t_logit, dtype=np.float64)[ok] / tau
+    t = np.where(t == np.inf, np.nan, t)  # no logit: the row has no result
     lse = log_sum_exp(x)
     out = dict(lse=lse, lse_rest=None, grad=np.zeros(V), loss=0.0, p=np.zeros(V), A=0.0, p_rest=0.0)
     unlisted = np.ones(V, dtype=bool)
@@ -103,7 +104,7 @@ def distill(s, t_idx, t_logit, tau=1.0, t_lse=None):
     p = np.exp(t - c)
     pv = np.zeros(V)
     np.add.at(pv, idx, p)
-    on = p > 0
+    on = p != 0
     with np.errstate(invalid="ignore"):
         loss = float(np.sum(p[on] * (t[on] - c - x[idx[on]] + lse)))
     p_rest = 0.0

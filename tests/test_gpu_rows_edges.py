@@ -107,3 +107,21 @@ def test_gradient_whose_factor_leaves_fp32(dt, with_lse):
         tt = np.minimum(np.abs(x - ref["lse"]) / np.log(2), 2.0 ** 30)
         assert (np.abs(got[i] - want)[small] <= (np.abs(want) * (half + (tt + 4) * 2.0 ** -23))[small] + 2.0 ** -125).all()
     assert some_big
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_infinite_and_nan_teacher_logits(dt):
+    import torch
+    t = _type(dt)
+    rng = np.random.default_rng(73)
+    for K in (4, 100):
+        s, teacher, idx, tl = _distill_case(rng, 4, 700, K, False, False, None)
+        tl[1, 2], tl[2, K - 1] = np.inf, np.nan
+        dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+        v, _ = _tensor(s, t)
+        for lse in (None, dev(np.full(4, 9.0))):
+            loss, own, _, dS = _run_distill(v, dev(idx), dev(tl), 1.0, lse, None, None)
+            assert torch.isfinite(own).all()
+            for i in range(4):
+                assert bool(torch.isnan(loss[i])) == (i in (1, 2)), (K, i, float(loss[i]))
+                assert bool(torch.isnan(dS[i]).all()) == (i in (1, 2)) == bool(torch.isnan(dS[i]).any()), (K, i)

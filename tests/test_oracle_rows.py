@@ -96,3 +96,11 @@ def test_log_sum_exp_out_of_range():
     assert R.log_sum_exp(np.full(5, -3.4e38)) == -np.inf and np.isnan(R.log_sum_exp(np.array([1.0, 3e38])))
     d = R.distill(np.full(6, -3.4e38), np.array([1, 4]), np.array([0.0, 1.0]))
     assert d["loss"] == 0 and d["lse"] == -np.inf and not d["grad"].any()
+
+
+def test_distill_infinite_teacher_logit_has_no_result():
+    s = np.random.default_rng(7).normal(size=9)
+    for t_lse in (None, 4.0):
+        for bad in (np.inf, np.nan):
+            d = R.distill(s, np.array([2, 4]), np.array([bad, 0.5]), 1.0, t_lse)
+            assert np.isnan(d["loss"]) and np.isfinite(d["lse"])
