@@ -96,6 +96,25 @@ __device__ __forceinline__ double pow2_eighth(int e) {
   return ldexp(v, e >> 3);
 }
 
+// 2^t, t <= 0, to fp64's precision: by the nearest integer and the Taylor series
+// of e^(f ln 2), |f| <= 1/2, to degree 12 (truncation below 2e-16)
+__device__ __forceinline__ double exp2_full(double t) {
+  t = fmax(t, -1100.0);
+  const double n = rint(t), x = (t - n) * 0.6931471805599453;
+  double p = fma(x, scalar(1.0 / 479001600.0), 1.0 / 39916800.0);
+  p = fma(p, x, scalar(1.0 / 3628800.0));
+  p = fma(p, x, scalar(1.0 / 362880.0));
+  p = fma(p, x, scalar(1.0 / 40320.0));
+  p = fma(p, x, scalar(1.0 / 5040.0));
+  p = fma(p, x, scalar(1.0 / 720.0));
+  p = fma(p, x, scalar(1.0 / 120.0));
+  p = fma(p, x, scalar(1.0 / 24.0));
+  p = fma(p, x, scalar(1.0 / 6.0));
+  p = fma(p, x, 0.5);
+  p = fma(p, x, 1.0);
+  return ldexp(fma(p, x, 1.0), (int)n);
+}
+
 struct RowParams {
   double c8;  // 8 log2(e) / T
   double t8;  // T ln(2) / 8
@@ -265,6 +284,35 @@ __device__ __forceinline__ uint32_t lowest_key(double j, double c8, double t8) {
   return l;
 }
 
+// min-p on the logits themselves: the least key whose weight, in full precision
+// relative to the largest key's, is at least m (0: min-p is off).  As above: a
+// round of 64 lanes around zmax + T ln m, and a search of 64 lanes a round
+// otherwise (the border near zero, where keys are dense).
+__device__ __forceinline__ uint32_t least_key(double m, uint32_t kmax, double c8, double t8) {
+  if (!(m > 0.0)) return 0;
+  const double zmax = key_value(kmax), c = c8 * 0.125;
+  const double z = fmin(fmax(zmax + 8.0 * (double)__builtin_amdgcn_logf((float)m) * t8, -3.4028234663852886e38), zmax);
+  const uint32_t g = max(ord32_canon(__float_as_uint((float)z)), kKeyLowest + 32u);
+  uint32_t cand = min(g - 32u + (uint32_t)lane_id(), kmax);
+  uint64_t hit = __ballot(exp2_full((key_value(cand) - zmax) * c) >= m);
+  if (hit && !(hit & 1)) return (uint32_t)__builtin_amdgcn_readlane(cand, __builtin_ctzll(hit));
+  uint32_t l = kKeyLowest, h = kmax;  // kmax weighs 1
+  while (l < h) {
+    const uint32_t step = (h - l + 63u) / 64u;
+    cand = min(l + (uint32_t)lane_id() * step, h);
+    hit = __ballot(exp2_full((key_value(cand) - zmax) * c) >= m);
+    const int f = hit ? __builtin_ctzll(hit) : 64;
+    if (f > 0) l = min(l + (uint32_t)(f - 1) * step, h) + 1u;
+    if (f < 64) h = (uint32_t)__builtin_amdgcn_readlane(cand, f);
+    if (f == 0) break;
+  }
+  return h;
+}
+// the bin of a key at or below the row's largest
+__device__ __forceinline__ int bin_of(uint32_t key, double c8, double J) {
+  return (int)fmin(J - rint(key_value(key) * c8), (double)kTail);
+}
+
 __device__ __forceinline__ uint32_t comp_key(uint64_t c) { return ~(uint32_t)(c >> 32); }
 __device__ __forceinline__ uint64_t comp_of(uint32_t key, uint32_t index) { return ((uint64_t)~key << 32) | index; }
 
@@ -359,8 +407,7 @@ __device__ __forceinline__ unsigned long long read_cells(const unsigned long lon
 
 // a token into the list, which is in the order of its bins
 __device__ __forceinline__ void list_token(uint32_t* next, uint64_t* list, double c8, double J, uint64_t c) {
-  const int b = (int)fmin(J - rint(key_value(comp_key(c)) * c8), (double)kTail);
-  list[atomicAdd(&next[b], 1u)] = c;
+  list[atomicAdd(&next[bin_of(comp_key(c), c8, J)], 1u)] = c;
 }
 
 // Bound by instructions, about twenty a token, eleven of them fp64 (t, its bin,
@@ -493,7 +540,8 @@ struct FinLds {
   double before_m;
 };
 
-// where a running count or sum crosses a value
+// where a running count or sum crosses a value (kByWeight: where keys fall below
+// one, in fp64 as the others)
 struct Cross {
   uint32_t n;    // tokens up to and including the crossing one (kByWeight: tokens that pass)
   double cum;    // their weight
@@ -516,6 +564,7 @@ struct Finalize {
   const double c8, t8, J;
   const int tid;
   const uint32_t kmax;  // the row's largest key
+  const uint32_t kmin;  // the least that min-p keeps; 0: off
   const int listed;     // bins 0 .. listed - 1 are in the segments' lists
   // the window's tokens: rank base + 1 .. base + n, of bins b0 .. b1 (b0 > b1: part of a bin)
   uint32_t base, n;
@@ -674,7 +723,7 @@ struct Finalize {
     double w = 0.0;
     if (in) {
       const uint64_t mine = list[tid];
-      const int bin = (int)fmin(J - rint(key_value(comp_key(mine)) * c8), (double)kTail);
+      const int bin = bin_of(comp_key(mine), c8, J);
       uint32_t rank = s.cc[bin] - s.cc[b0];
       for (uint32_t j = rank, end = s.cc[bin + 1] - s.cc[b0]; j < end; ++j) rank += list[j] < mine;
       s.win[rank] = mine;
@@ -691,7 +740,7 @@ struct Finalize {
     const bool hit = in && (kind == kByCount    ? (double)(base + tid + 1) >= amount
                             : kind == kByMassGe ? s.wcum[tid] >= amount
                             : kind == kByMassGt ? s.wcum[tid] > amount
-                                                : weight(comp_key(s.win[tid])) < amount);
+                                                : (double)comp_key(s.win[tid]) < amount);
     int pos = min(ops.first(hit), (int)n);
     if (kind != kByWeight) pos = min(pos + 1, (int)n);  // pos tokens of the window are in
     Cross r;
@@ -721,7 +770,7 @@ struct Finalize {
     const bool hit = kind == kByCount    ? (double)s.cc[tid + 1] >= amount
                      : kind == kByMassGe ? s.cm[tid + 1] >= amount
                      : kind == kByMassGt ? s.cm[tid + 1] > amount
-                                         : pow2_eighth(-tid) * exp2_eighth(-0.5) <= amount;  // the bin's lowest weight
+                                         : tid >= bin_of((uint32_t)amount, c8, J);
     int b = ops.first(hit);
     if (b >= kBins) {
       b = kTail;
@@ -759,7 +808,7 @@ struct Finalize {
             if (r < (double)nc && !(kind == kByMassGe ? fma(r, w, mb) >= amount : fma(r, w, mb) > amount)) r += 1.0;
             r = fmax(r, 1.0);
           }
-          if (kind == kByWeight && weight(klo) < amount) return Cross{cb, mb, ((uint64_t)~klo) << 32, 0};
+          if (kind == kByWeight && (double)klo < amount) return Cross{cb, mb, ((uint64_t)~klo) << 32, 0};
           const Cross x{cb + (uint32_t)r, fma(r, w, mb), 0, 0};
           // the index of the r-th of them
           uint32_t left = (uint32_t)r, ilo = 0, ihi = (uint32_t)z.V - 1;
@@ -793,7 +842,7 @@ struct Finalize {
                               (kind == kByCount    ? (double)c1 >= amount
                                : kind == kByMassGe ? m1 >= amount
                                : kind == kByMassGt ? m1 > amount
-                                                   : weight(low) < amount);
+                                                   : (double)low < amount);
         int q = ops.first(part_hit);
         if (q >= (int)n_part) {  // every key passes, or rounding left the sum short of the last token
           part_of((int)n_part - 1, c1, m1, c, mass);
@@ -822,7 +871,7 @@ struct Finalize {
   }
 
   // the row's cuts and draw, once s.cc and s.cm hold its bins
-  __device__ __forceinline__ void answer(const RowParams& rp, uint32_t N, double wmax, double u, int64_t row, const SampleOut& o,
+  __device__ __forceinline__ void answer(const RowParams& rp, uint32_t N, double u, int64_t row, const SampleOut& o,
                                          uint64_t* cut_out) {
     uint32_t kept = N;
     double Z = s.cm[kBins];
@@ -840,8 +889,8 @@ struct Finalize {
         if (!(rp.p < 1.0)) continue;
         kind = kByMassGe, amount = rp.p * Z;
       } else if (q == 2) {
-        if (!(rp.m > 0.0)) continue;
-        kind = kByWeight, amount = rp.m * wmax;
+        if (kmin == 0) continue;
+        kind = kByWeight, amount = (double)kmin;
       } else if (q == 3) {
         if (tid == 0) {
           if (o.kept) o.kept[row] = (int32_t)kept;
@@ -875,8 +924,8 @@ struct Finalize {
 // The bins that a row's cuts and draw can need, from the bins' sums alone: a
 // cut or draw whose amount depends on an earlier cut inside a bin takes the
 // bins of that amount's bounds.  True if all are listed; else asks for them.
-__device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowParams& rp, uint32_t N, double wmax, bool draw,
-                                            double u, double J, uint32_t kmax, int listed, uint32_t ask_cap, SampleAsk& ask) {
+__device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowParams& rp, uint32_t N, bool draw,
+                                            double u, double J, uint32_t kmax, uint32_t kmin, int listed, uint32_t ask_cap, SampleAsk& ask) {
   const double c8 = rp.c8, t8 = rp.t8;
   constexpr double kLess = 1.0 - 0x1p-40, kMore = 1.0 + 0x1p-40;
   const int tid = threadIdx.x;
@@ -903,8 +952,8 @@ __device__ __forceinline__ bool bins_listed(FinLds& s, BlockOps& ops, const RowP
     zhi = s.cm[cut1 + 1];
     any = true;
   }
-  if (rp.m > 0.0) {
-    const int bm = min(ops.first(pow2_eighth(-tid) * exp2_eighth(-0.5) <= rp.m * wmax), kTail);
+  if (kmin != 0) {
+    const int bm = bin_of(kmin, c8, J);
     if (bm <= cut1) {
       need0 = min(need0, bm);
       need1 = max(need1, bm);
@@ -1021,16 +1070,15 @@ __global__ __launch_bounds__(kThreads, MODE == kSecond ? 4 : 2) void sample_fina
   }
   __syncthreads();
 
-  const uint32_t kmax = key_of(m, RowType<DFLASH_F32>::kMax);
+  const uint32_t kmax = key_of(m, RowType<DFLASH_F32>::kMax), kmin = least_key(rp.m, kmax, rp.c8, rp.t8);
   Finalize<DFLASH_F32, MODE> f{s, ops, RowRef<DFLASH_F32>(a.Z, row, a.stride, a.V), part, lists + (size_t)blockIdx.x * n_seg * cap,
                                MODE == kSecond ? asked + (size_t)blockIdx.x * ask_cap : nullptr,
-                               MODE == kSecond ? asks + blockIdx.x : nullptr, ask_cap, n_seg, cap, rp.c8, rp.t8, J, tid, kmax, listed,
+                               MODE == kSecond ? asks + blockIdx.x : nullptr, ask_cap, n_seg, cap, rp.c8, rp.t8, J, tid, kmax, kmin, listed,
                                0, 0, 0.0, 1, 0, 0, 0, 0};
-  const double wmax = f.weight(kmax);
   if constexpr (MODE == kFirst) {
-    if (!bins_listed(s, ops, rp, N, wmax, o.token != nullptr, u, J, kmax, listed, ask_cap, asks[blockIdx.x])) return;
+    if (!bins_listed(s, ops, rp, N, o.token != nullptr, u, J, kmax, kmin, listed, ask_cap, asks[blockIdx.x])) return;
   }
-  f.answer(rp, N, wmax, u, row, o, cuts + blockIdx.x);
+  f.answer(rp, N, u, row, o, cuts + blockIdx.x);
 }
 
 // a slot of the filtered row: the tokens before `cut` stay
@@ -1115,8 +1163,8 @@ __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, S
       }
     __syncthreads();
     const uint32_t kmax = key_of(m, kMax);
-    Finalize<DT, kOne> fin{s, ops, z, nullptr, list, nullptr, nullptr, 0, 1, 0, c8, rp.t8, J, tid, kmax, kBins, 0, 0, 0.0, 1, 0, 0, 0, 0};
-    fin.answer(rp, s.cc[kBins], fin.weight(kmax), u, row, o, &cut);
+    Finalize<DT, kOne> fin{s, ops, z, nullptr, list, nullptr, nullptr, 0, 1, 0, c8, rp.t8, J, tid, kmax, least_key(rp.m, kmax, c8, rp.t8), kBins, 0, 0, 0.0, 1, 0, 0, 0, 0};
+    fin.answer(rp, s.cc[kBins], u, row, o, &cut);
   }
   if (o.out) {
     __syncthreads();
@@ -1340,7 +1388,7 @@ struct Values {
   const int n_seg, seg_slots, tid;
   const double c;        // log2(e) / T
   const uint32_t base;
-  double tm;             // c times the largest logit
+  double m;              // the largest logit
   int n_mid;             // entries near zero
   uint32_t n_in;         // tokens in the range
 
@@ -1350,24 +1398,8 @@ struct Values {
     const float v = __uint_as_float((uint32_t)mag << 16);
     return item < kMid ? v : -v;
   }
-  // relative to the row's largest token, whose weight is exactly 1: 2^t by
-  // its nearest integer and the Taylor series of e^(f ln 2), |f| <= 1/2, to
-  // degree 12 (truncation below 2e-16)
-  __device__ __forceinline__ double weight(double v) const {
-    const double t = fmax(v * c - tm, -1100.0), n = rint(t), x = (t - n) * 0.6931471805599453;
-    double p = fma(x, scalar(1.0 / 479001600.0), 1.0 / 39916800.0);
-    p = fma(p, x, scalar(1.0 / 3628800.0));
-    p = fma(p, x, scalar(1.0 / 362880.0));
-    p = fma(p, x, scalar(1.0 / 40320.0));
-    p = fma(p, x, scalar(1.0 / 5040.0));
-    p = fma(p, x, scalar(1.0 / 720.0));
-    p = fma(p, x, scalar(1.0 / 120.0));
-    p = fma(p, x, scalar(1.0 / 24.0));
-    p = fma(p, x, scalar(1.0 / 6.0));
-    p = fma(p, x, 0.5);
-    p = fma(p, x, 1.0);
-    return ldexp(fma(p, x, 1.0), (int)n);
-  }
+  // relative to the row's largest token, whose weight is exactly 1
+  __device__ __forceinline__ double weight(double v) const { return exp2_full((v - m) * c); }
   __device__ __forceinline__ double near_value(uint32_t i) const { return key_value(comp_key(s.win[i])); }
 
   // tokens of an item
@@ -1588,7 +1620,7 @@ __device__ __forceinline__ bool finalize_values(ValLds& s, const SampleArgs& a, 
   }
   const double m = top == kMid ? f.near_value(0) : (double)f.value(top);
   if (n_low && m - 512.0 / c8 < -(double)__uint_as_float(min((base + (uint32_t)kMags) << 16, 0x7F7F0000u))) return false;
-  f.tm = m * f.c;
+  f.m = m;
   if (n_mid) {
     const uint32_t c = tid >= (int)n_mid ? 0u : comp_key(s.win[tid]) == kKeyZero ? n_zero : 1u, nc = ops.scan(c);
     const double wc = ops.scan(c ? (double)c * f.weight(f.near_value(tid)) : 0.0);
@@ -1730,8 +1762,8 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
   }
   __syncthreads();
   const uint32_t kmax = key_of(m, kMax);
-  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, 0, c8, rp.t8, J, tid, kmax, 0, 0, 0, 0.0, 1, 0, 0, 0, 0};
-  f.answer(rp, s.cc[kBins], f.weight(kmax), row_uniform(o, row), row, o, cut_out);
+  Finalize<DT, kSelf> f{s, ops, z, nullptr, nullptr, nullptr, nullptr, 0, 0, 0, c8, rp.t8, J, tid, kmax, least_key(rp.m, kmax, c8, rp.t8), 0, 0, 0, 0.0, 1, 0, 0, 0, 0};
+  f.answer(rp, s.cc[kBins], row_uniform(o, row), row, o, cut_out);
 }
 
 // One row takes 13 us, 512 rows 29: a chain of steps whose latency counts.  Of

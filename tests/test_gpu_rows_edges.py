@@ -125,3 +125,30 @@ def test_infinite_and_nan_teacher_logits(dt):
             for i in range(4):
                 assert bool(torch.isnan(loss[i])) == (i in (1, 2)), (K, i, float(loss[i]))
                 assert bool(torch.isnan(dS[i]).all()) == (i in (1, 2)) == bool(torch.isnan(dS[i]).any()), (K, i)
+
+
+@pytest.mark.parametrize("dt,R,V", [("bf16", 1, 4096), ("bf16", 1, 4104), ("bf16", 30, 50021), ("f32", 1, 1000), ("f32", 3, 8192),
+                                    ("f32", 3, 8200), ("f32", 40, 100003), ("f32", 80, 100003)])
+def test_min_p_at_weights_next_to_one(dt, R, V):
+    # T = 1e13: weights differ from 1 by 2^-43 and less, which fp64 still tells apart, on every path
+    rng = np.random.default_rng(V)
+    z = (np.round(rng.normal(size=(R, V)) * 2 * 16) / 16).astype(np.float32)
+    z[:, V // 3] = z[:, V // 2] = 16.0
+    z[:, V // 5] = 15.9375
+    st = [dict(T=1e13, min_p=1.0), dict(T=1e12, min_p=float(np.float32(1.0 - 2.0 ** -24)))]
+    _check_sample(z, _type(dt), [st[i % 2] for i in range(R)], rng.random(R))
+
+
+@pytest.mark.parametrize("dt,R,V", [("bf16", 6, 4001), ("bf16", 6, 50021), ("f32", 6, 1000), ("f32", 6, 50021), ("f32", 66, 100003)])
+def test_min_p_whose_border_lies_near_zero(dt, R, V):
+    # max 1, T = 1, min_p next to 1/e: the border lies within 1e-7 of zero, where
+    # fp32 values are dense; and borders in the tail, far below and at the maximum
+    rng = np.random.default_rng(V + 1)
+    z = rng.normal(size=(R, V)).astype(np.float32)
+    z[:, ::2] *= 10.0 ** rng.uniform(-12, -5, size=z[:, ::2].shape)
+    z = np.minimum(z, np.float32(0.9))
+    z[:, V // 3] = 1.0
+    e = float(np.exp(-1.0))
+    st = [dict(min_p=p) for p in (e, float(np.nextafter(np.float32(e), np.float32(1))), float(np.nextafter(np.float32(e), np.float32(0))),
+                                  0.03, 1e-44, 0.95)]
+    _check_sample(z, _type(dt), [st[i % 6] for i in range(R)], rng.random(R))
