@@ -503,19 +503,24 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   const double p_rest = with_rest ? fmax(1.0 - p_sum, 0.0) : 0.0;
   const double A = p_sum + p_rest;
   const double base = with_rest ? rest : lse;
-  // the factor; one near fp32's end leaves its power of two to the exponent, so
-  // that unlikely tokens' gradients, which fit, do not become inf times 0
-  const double G64 = f * (with_rest ? A * exp(rest - lse) - p_rest : A);
-  const int up = fabs(G64) >= 0x1p100 && fabs(G64) < INFINITY ? ilogb(G64) : 0;
-  const float G = (float)ldexp(G64, -up);
+  double G64 = f * (with_rest ? A * exp(rest - lse) - p_rest : A);
+  const double c2 = kLog2e64 / a.tau;
+  double b2 = base * kLog2e64;
+  // a factor near fp32's end leaves its power of two to the exponent, so that
+  // unlikely tokens' gradients, which fit, do not become inf times 0
+  if (fabs(G64) >= 0x1p100 && fabs(G64) < INFINITY) {
+    const int up = ilogb(G64);
+    G64 = ldexp(G64, -up);
+    b2 -= up;
+  }
+  const float G = (float)G64;
   // x_j - base in two pieces of fp32: the product s c and its difference from
-  // the base are rounded once (fma), the low halves are added after
-  const double c2 = kLog2e64 / a.tau, b2 = base * kLog2e64 - up;
+  // the base are rounded once (fma), the low halves are added after.  Those stay
+  // finite: logits whose exponential is 0 are raised there to 2^-256 of the base's
+  // (or below, by as much as rounding moves the border), else a mask of finite
+  // lowest values over a small tau would leave fp32 in both pieces, with either sign
   const float ch = (float)c2, cl = (float)(c2 - (double)ch), bh = (float)b2, bl = (float)(b2 - (double)bh);
-  // Logits whose exponential is 0 are raised to 2^-256 of the base's (or below, by
-  // as much as rounding moves the border): a mask of finite lowest values over a
-  // small tau would leave fp32 in both products, with either sign
-  const float least = (float)fmax((b2 - 256.0 - fabs(b2) * 0x1p-22) / c2, -3.4028234663852886e38);
+  const float least = (float)fmax((b2 - 256.0 - fabs(b2) * 0x1p-22) * kLn2 * a.tau, -3.4028234663852886e38);
 #pragma unroll
   for (int l = 0; l < NL; ++l) {
     Slot y;
@@ -524,8 +529,8 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
       const float v = slot_value<DT>(x[l], i);
-      const float r = fmaxf(v, least), t = fmaf(r, ch, -bh) + fmaf(r, cl, -bl);
-      const float g = v == kNegInf ? 0.0f : G * __builtin_amdgcn_exp2f(t);
+      const float t = fmaf(v, ch, -bh) + fmaf(fmaxf(v, least), cl, -bl);
+      const float g = G * __builtin_amdgcn_exp2f(t);  // -inf: 0
       if constexpr (DT == DFLASH_BF16)
         y.w[i >> 1] |= bf16_round(g) << ((i & 1) * 16);
       else
