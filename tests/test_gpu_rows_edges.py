@@ -1,13 +1,15 @@
 """GPU tests of the operators on logit rows at the ends of what they accept:
-uniforms next to 1, temperatures that leave bins without a value, settings of
-the smallest tau, and every plan of the launches.  Bars as in test_gpu_rows.
+uniforms next to 1, temperatures that leave bins without a value, the smallest
+tau, min-p next to its ends, and the plans of the launches.  Bars as in
+test_gpu_rows.
 """
 
 import numpy as np
 import pytest
 
 from oracle import rows as O
-from test_gpu_rows import _check_distill, _check_sample, _distill_case, _f64, _logits, _run_distill, _say, _tensor
+from test_gpu_rows import (MIX, _arr, _as_used, _check_distill, _check_sample, _distill_case, _f64, _filters, _logits,
+                           _run_distill, _say, _tensor)
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +154,143 @@ def test_min_p_whose_border_lies_near_zero(dt, R, V):
     st = [dict(min_p=p) for p in (e, float(np.nextafter(np.float32(e), np.float32(1))), float(np.nextafter(np.float32(e), np.float32(0))),
                                   0.03, 1e-44, 0.95)]
     _check_sample(z, _type(dt), [st[i % 6] for i in range(R)], rng.random(R))
+
+
+# ---------------------------------------------------------------- the launches' plans
+
+# one launch; bf16 segments; fp32 with every token listed; fp32 with the largest
+# listed, in segments of 2, 4 and 8 slots a thread
+PLANS = [("bf16", 14, 3001), ("f32", 14, 8001), ("bf16", 14, 20011), ("f32", 14, 20011), ("f32", 63, 100003), ("f32", 98, 100003),
+         ("f32", 168, 100003)]
+
+
+@pytest.mark.parametrize("dt,R,V", PLANS)
+def test_uniforms_at_their_ends_on_every_plan(dt, R, V):
+    rng = np.random.default_rng(R + V)
+    u = [0.0, -1.0, float("nan"), 1.0, 7.0, LAST, 2.0 ** -60]
+    st = [dict(), dict(top_k=5), dict(top_p=0.8), dict(T=0.5, min_p=0.2), dict(top_k=3000, top_p=0.9999), dict(T=0.0), dict(T=8.0, top_p=0.7)]
+    _say(f"[rows] u at its ends {dt} {R} x {V}")
+    z = _logits(rng, R, V, "peaked")
+    _check_sample(z, _type(dt), [st[i // 7 % 7] for i in range(R)], np.array([u[i % 7] for i in range(R)]), pad=1)
+
+
+def test_uniforms_at_their_ends_where_a_row_is_binned_by_one_block():
+    # bf16 rows with their largest logit over the counters
+    rng = np.random.default_rng(81)
+    u = [0.0, -1.0, float("nan"), 1.0, 7.0, LAST, 2.0 ** -60]
+    z = _logits(rng, 7, 20011, "peaked") + np.float32(900.0)
+    for st in (dict(), dict(top_k=5), dict(top_p=0.8, T=4.0)):
+        _check_sample(z, _type("bf16"), [st] * 7, np.array(u))
+
+
+@pytest.mark.parametrize("dt,R,V", [("bf16", 8300, 4104), ("f32", 1030, 8200), ("f32", 170, 400007)])
+def test_more_rows_than_a_pass_over_the_workspace(dt, R, V):
+    # 8192 bf16 segments a pass, 1024 fp32 rows or 4096 fp32 segments
+    import torch
+    import block_draft_select_amd as dfl
+    rng = np.random.default_rng(R)
+    t = _type(dt)
+    n = 300 if V < 10000 else 40  # the same rows over and over, every row with its own uniform and settings
+    z = _logits(rng, n, V, "peaked")[np.arange(R) % n]
+    st = [MIX[i % len(MIX)] for i in range(R)]
+    _say(f"[rows] several passes {dt} {R} x {V}")
+    u = rng.random(R)
+    _check_sample(z, t, st, u, pad=1)
+    v, _ = _tensor(z, t)
+    r = dfl.rows(v)
+    out = torch.empty_like(v)
+    kept = torch.full((R,), -7, dtype=torch.int32, device="cuda")
+    dfl.dflash_filter(r, v, out, dfl.rows_workspace(r), kept=kept, **_filters(st))
+    torch.cuda.synchronize()
+    kept = kept.cpu().numpy()
+    low = float(torch.finfo(t).min)
+    for i in range(0, R, 7 if V < 10000 else 3):
+        zz = _f64(v[i])
+        assert np.array_equal(_f64(out[i]), O.filtered(zz, low, **_as_used(st[i]))), (i, st[i])
+        assert kept[i] == O.keep(zz, **_as_used(st[i]))[0].size, (i, st[i])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_listed_tokens_at_the_types_lowest_value(dt):
+    # a student that a finite mask denies every listed token: the loss is about
+    # the mask over tau (beyond fp32: inf), the gradient ordinary
+    import torch
+    t = _type(dt)
+    low = float(torch.finfo(t).min)
+    rng = np.random.default_rng(82)
+    V = 20005
+    s = np.full((3, V), low, dtype=np.float32)
+    s[0, 100:200] = rng.normal(size=100)
+    s[1, 20004] = 0.5
+    s[2] = rng.normal(size=V)
+    s[2, 19000] = low
+    idx = np.tile(np.array([[3, 19000, 7]], dtype=np.int32), (3, 1))
+    tl = np.ones((3, 3), dtype=np.float32)
+    for with_lse in (False, True):
+        _check_distill(s, idx, tl, t, 2.0, np.full(3, 1.8) if with_lse else None, None, None)
+        dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+        v, _ = _tensor(s, t)
+        loss, lse, _, dS = _run_distill(v, dev(idx), dev(tl), 0.25, dev(np.full(3, 5.2)) if with_lse else None, None, None)
+        assert torch.isinf(loss).all() and (loss > 0).all() and torch.isfinite(lse).all() and torch.isfinite(dS).all()
+
+
+def test_gradient_at_small_tau():
+    # x = S / tau up to 2^24: beside the bars of test_gpu_rows the exponent is off
+    # by the roundings of x, lse and the products in fp64 (6 of 2^-53 |x|), and of
+    # the low pieces in fp32: theirs and the high piece's remainder, each below
+    # 2^-22 |x|, are rounded to 2^-24 of that in five places
+    import torch
+    rng = np.random.default_rng(83)
+    R, V, K = 4, 5003, 8
+    for tau in (1e-3, 1e-6):
+        for t in (torch.bfloat16, torch.float32):
+            for with_lse in (False, True):
+                s, teacher, idx, tl = _distill_case(rng, R, V, K, False, False, None)
+                v, _ = _tensor(s, t)
+                zz = _f64(v)
+                # a bulk within a few nats of the top keeps the exponentials in range
+                zz = zz.max(1, keepdims=True) * (1.0 + rng.integers(-4, 1, size=zz.shape) * float(torch.finfo(t).eps))
+                v.copy_(torch.from_numpy(zz))
+                zz = _f64(v)
+                lse_t = np.array([O.log_sum_exp(tl[i].astype(np.float64) / tau) + 0.3 for i in range(R)]) if with_lse else None
+                dev = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+                _, lse, _, dS = _run_distill(v, dev(idx), dev(tl), tau, dev(lse_t), None, None)
+                got = _f64(dS)
+                for i in range(R):
+                    ref = O.distill(zz[i], idx[i], tl[i], tau, None if lse_t is None else lse_t[i])
+                    x = zz[i] / tau
+                    big = np.abs(x).max()
+                    assert big < 2.0 ** 25
+                    assert abs(float(lse[i]) - ref["lse"]) <= 2e-11 + big * 2.0 ** -49
+                    half = torch.finfo(t).eps / 2
+                    size = (ref["A"] * np.exp(x - ref["lse"]) + ref["p"] + (0 if lse_t is None else np.where(
+                        ref["p"] > 0, 0.0, ref["p_rest"] * np.exp(np.minimum(x - ref["lse_rest"], 0.0))))) / tau
+                    d = np.abs(x - ref["lse"]) / np.log(2)
+                    tol = np.abs(ref["grad"]) * half + size * ((np.minimum(d, 126.0) + 4) * 2.0 ** -23 + 1e-10 + big * (
+                        6 * 2.0 ** -53 + 5 * 2.0 ** -46)) + 2.0 ** -125 * (1 + 1 / tau)
+                    assert (np.abs(got[i] - ref["grad"]) <= tol).all(), (tau, t, i, np.abs(got[i] - ref["grad"]).max())
+
+
+def test_per_kernel_timers_of_the_four():
+    import torch
+    import block_draft_select_amd as dfl
+    v = torch.randn(5, 20011, device="cuda")
+    r = dfl.rows(v)
+    ws, out = dfl.rows_workspace(r), torch.empty_like(v)
+    u, lse = torch.rand(5, dtype=torch.float64, device="cuda"), torch.empty(5, dtype=torch.float64, device="cuda")
+    token, loss = torch.empty(5, dtype=torch.int32, device="cuda"), torch.empty(5, device="cuda")
+    idx = torch.arange(20, dtype=torch.int32, device="cuda").view(5, 4)
+    tl = torch.randn(5, 4, device="cuda")
+    dfl.dflash_profile_enable(True)
+    try:
+        for n in range(3):
+            dfl.dflash_sample(r, v, u, token, ws, top_p=_arr([0.9] * 5, torch.float32))
+            dfl.dflash_filter(r, v, out, ws)
+            dfl.dflash_distill(r, v, idx, tl, loss, lse, ws)
+            dfl.dflash_distill_grad(r, v, idx, tl, lse, out)
+        for name in ("sample", "filter", "distill", "distill_grad"):
+            calls, ms = dfl.dflash_profile_collect(name)
+            assert calls == 3 and 0.0 < ms < 1000.0, (name, calls, ms)
+            assert dfl.dflash_profile_collect(name) == (0, 0.0)
+    finally:
+        dfl.dflash_profile_enable(False)
