@@ -238,9 +238,10 @@ static SamplePlan sample_layout(const dflash_rows& r, bool all, int loads) {
 SamplePlan sample_plan(const dflash_rows& r) {
   SamplePlan p{};
   const int slots = row_slots(r);
-  // In one launch, a block a row: short rows, in bf16 those of one slot a thread
-  // (8000 tokens: 11 us for one row against 15 in two launches, but 22 against
-  // 19 for 64 rows and 158 against 75 for 2048)
+  // In one launch, a block a row: short rows, in bf16 those of one slot a thread.
+  // Of 8000 bf16 tokens one row took 11 us so against 15 in two launches, but 64
+  // rows 22 against 19 and 2048 rows 158 against 75: the longer ones go in two,
+  // whatever R, for the sake of many rows
   if (r.V <= (r.dtype == DFLASH_BF16 ? kSampleOne / 2 : kSampleOne)) {
     p.loads = slots <= kSampleThreads ? 1 : slots <= 2 * kSampleThreads ? 2 : 4;
     p.one = true;
@@ -283,9 +284,10 @@ SamplePlan sample_plan(const dflash_rows& r) {
 
 // The forward pass: 2048 blocks (eight per CU) if the rows have that much, and
 // more only because a block's segment is bounded.  The gradient: as many slots a
-// thread as fill its blocks and leave four, two, one of them per CU (with 1, 2,
-// 4, 8 slots: 512 x 151936 bf16 in 93, 68, 58, 57 us; 64 x 151936 in 16, 14, 14,
-// 14; 61 x 50021 in 8.0, 8.0, 8.4, 9.7; 2048 x 1000 in 9, 10, 14, 22).
+// thread as fill its blocks and leave four, two, one of them per CU (the kernel's
+// median with 1, 2, 4, 8 slots over rotating inputs: 512 x 151936 bf16 in 98, 74,
+// 63, 64 us; 64 x 151936 in 18, 16, 15, 16; 61 x 50021 fp32 with K = 64 in 13.9,
+// 11.9, 11.8, 11.8; 2048 x 1000 bf16 in 9, 11, 14, 21).
 DistillPlan distill_plan(const dflash_rows& r) {
   DistillPlan p{};
   const int slots = row_slots(r), units = (slots + kDistillUnit - 1) / kDistillUnit;

@@ -47,7 +47,7 @@ constexpr double kRange = 0x1p40;
 // |v| <= h = 6.8e-4: within 1.3e-11), the first is added to the table entry's
 // exponent.  512 t is shifted by kShift so that truncation is the floor and
 // everything below 2^-960 (and -inf) ends at the range's foot.  Measured on
-// 2048 x 151936 against 64 entries and degree 3: 148 us to 160.
+// 2048 x 151936 against 64 entries and degree 3, over a few calls: 148 us to 160.
 constexpr int kTabBits = 9, kTab = 1 << kTabBits;
 constexpr double kShift = (double)kTab * 960.0;
 
@@ -217,7 +217,7 @@ __device__ __forceinline__ float largest(const Slot (&x)[N], bool& odd) {
 // A block sums a row segment of `units` times kDistillUnit slots; each of its
 // waves on its own, four slots a lane at a time, relative to the largest logit
 // so far (rounded to a power of two, so that a new one only moves exponents).
-// 2048 x 151936 bf16: 148 us, 4.2 TB/s.
+// 2048 x 151936 bf16: 154 us at best, 4.0 TB/s; 166 at the median of 24 calls.
 template <int DT, bool REST>
 __global__ __launch_bounds__(kThreads) void distill_sum_kernel(DistillArgs a, int n_seg, int units, uint32_t exp_unit,
                                                                DistillPart* __restrict__ parts) {
@@ -310,7 +310,7 @@ __device__ __forceinline__ double join_log(double m, double s) {
 }
 
 // T threads a row: a wave for short lists (no barriers; 2048 rows of K = 16 in
-// 9 us, 15 with a block each), a block for long ones, whose repeated entries
+// 10 us, 15 with a block each), a block for long ones, whose repeated entries
 // are searched for pair by pair
 template <int DT, int T, bool REST>
 __global__ __launch_bounds__(T) void distill_loss_kernel(DistillArgs a, int n_seg, const DistillPart* __restrict__ parts,
@@ -412,9 +412,9 @@ __global__ __launch_bounds__(T) void distill_loss_kernel(DistillArgs a, int n_se
 // ---------------------------------------------------------------- backward
 
 // One read and one write of the row at the memory's rate: 2048 x 151936 bf16 in
-// 213 us, 5.8 TB/s (a plain copy of 2 GiB: 4.9).  The exponentials are fp32,
-// the exponent in two pieces (off by (|t| + 4) 2^-23): the forward pass's fp64
-// terms alone take 148 us.
+// 213 to 218 us, 5.8 TB/s (torch's copy of 2 GiB: 4.9).  The exponentials are fp32,
+// the exponent in two pieces (off by (|t| + 4) 2^-23, and by the low pieces'
+// roundings, 2^-43 |x_j|): the forward pass's fp64 terms alone take 154 us.
 template <int DT, int NL, bool REST>
 __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, int n_seg, const float* __restrict__ grad_loss,
                                                                 const double* __restrict__ lse_in,
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void distill_grad_kernel(DistillArgs a, i
   double c = -INFINITY, p_sum = 0.0;
   float own[kPerThread];  // the listed tokens' logits of this segment, read before anything is stored (dS may be S)
   if (!off && a.K <= kWave) {
-    // a short list: one wave, one barrier (61 x 50021 fp32, K = 64: 11.7 us, 13.3
+    // a short list: one wave, one barrier (61 x 50021 fp32, K = 64: 11.8 us, 13.3
     // with the block's reductions)
     if (tid < kWave) {
       int idx = -1;

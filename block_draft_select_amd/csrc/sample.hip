@@ -39,8 +39,10 @@
 //
 // Counts are exact and sums do not depend on the order of the atomics: every
 // 2^((t - rint(t)) / 8) is rounded to a multiple of 2^-42 (off by 2^-43 of
-// itself) wherever it is used, and summed as an integer.  Decisions next to a
-// border need such sums: they compare running sums over the whole vocabulary.
+// itself, and by 2^-51 |z| / T as t is rounded) wherever it is used, and summed
+// as an integer.  Decisions next to a border need such sums: they compare running
+// sums over the whole vocabulary.  Only min-p asks for single weights; it takes
+// them from the logits in full precision.
 #include "rows_blocks.hpp"
 
 // t = z c8 is one rounded product wherever it is formed: fused into the
@@ -371,6 +373,9 @@ __device__ __forceinline__ void add_cells(unsigned long long* cells, const Slot 
         }
       }
   } else {
+    // |max| / T over 9e4: t's integer does not fit the sum's lower word.  Few rows
+    // have it, so the registers of a loop matter and its time does not (each token
+    // is picked by NL VE comparisons)
 #pragma unroll 1
     for (int e = 0; e < NL * VE; ++e) {
       float v = kNegInf;
@@ -411,9 +416,10 @@ __device__ __forceinline__ void list_token(uint32_t* next, uint64_t* list, doubl
 }
 
 // Bound by instructions, about twenty a token, eleven of them fp64 (t, its bin,
-// the weight): 256 x 262144 fp32 in 74 us, 3.6 TB/s; without the weight 53,
-// loads and the integer part alone 46; the one atomic a token hides behind them,
-// the list takes 10.
+// the weight): 256 x 262144 fp32 in 88 us, 3.1 TB/s.  (In a build that took 74,
+// before tokens under the bins were counted aside: 53 without the weight, 46 for
+// loads and the integer part alone, 10 for the list; the one atomic a token hides
+// behind them.)
 template <int NL, bool ALL>
 __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
                                                                SamplePart* __restrict__ parts, uint64_t* __restrict__ lists) {
@@ -764,7 +770,8 @@ struct Finalize {
 
   __device__ __forceinline__ Cross locate(int kind, double amount) {
     // a sum within 2^-44 of the value counts as equal to it: rows of equal
-    // logits meet dyadic settings exactly, and the sums round (below 2^-47)
+    // logits meet dyadic settings exactly, and sums of one weight round (below
+    // 2^-47)
     if (kind == kByMassGe) amount *= 1.0 - 0x1p-44;
     if (kind == kByMassGt) amount *= 1.0 + 0x1p-44;
     const bool hit = kind == kByCount    ? (double)s.cc[tid + 1] >= amount
@@ -1011,9 +1018,9 @@ __device__ __forceinline__ double row_uniform(const SampleOut& o, int64_t row) {
 
 // One block a row: bound by the latency of its steps (the segments' bins as
 // other blocks left them in memory, then scans, windows and searches).  One row
-// of 151936 fp32 takes 15 to 17 us, 256 of 262144 18 and 24 (kFirst and kSecond,
-// which at 128 registers keeps two blocks a CU: 1024 rows of 32000 in 70 us, 95
-// with one).
+// of 151936 fp32 takes 13 us (top-p); 256 of 262144 14 to 20 in kFirst and 20 in
+// kSecond, 1024 of 32000 26 to 35 and 13 to 34 by their settings.  kSecond at 128
+// registers keeps two blocks a CU; with one it took a third longer.
 template <int MODE>
 __global__ __launch_bounds__(kThreads, MODE == kSecond ? 4 : 2) void sample_finalize_kernel(SampleArgs a, int64_t row0, int n_seg, int cap, uint32_t ask_cap,
                                                                    const SamplePart* __restrict__ parts,
@@ -1107,8 +1114,9 @@ __device__ __forceinline__ void store_filtered(typename RowType<DT>::elem* o, in
 
 // A row of up to 8192 tokens in one block, NL slots a thread: bins, list and
 // answer stay in LDS, and the filtered row is written at once.  Bound by the
-// chain of steps: one row of 1024 fp32 takes 8.1 us (12.9 in two launches), 2048
-// rows 40 (82); one row of 8000 12 (15), 2048 rows 165 (180).
+// chain of steps: one row of 1024 fp32 takes 7.5 us (12.9 in two launches), 2048
+// of 1000 35 to 43 by their settings (82); one row of 8000 11 (15), 2048 rows 112
+// to 175 (180), as the list of four slots a thread leaves a CU one block (96 KB).
 template <int DT, int NL>
 __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, SampleOut o) {
   constexpr int VE = RowType<DT>::VE;
@@ -1176,8 +1184,8 @@ __global__ __launch_bounds__(kThreads, 4) void sample_row_kernel(SampleArgs a, S
 
 // ---------------------------------------------------------------- (3) the tokens that rows asked for
 
-// Reads the rows a second time at the memory's rate (256 x 262144 fp32: 44 us,
-// 6.1 TB/s); rows that asked for nothing are not read.
+// Reads the rows that asked a second time (256 x 262144 fp32 if all do: 44 us, 6.1
+// TB/s, the memory's rate; 26 of plain temperature, 14 of mixed requests).
 template <int NL>
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a, int64_t row0, int n_seg, uint32_t ask_cap,
                                                                  SampleAsk* __restrict__ asks, uint64_t* __restrict__ asked) {
@@ -1407,7 +1415,8 @@ struct Values {
 
   __device__ __forceinline__ ValueCross locate(int kind, double amount) {
     // a sum within 2^-44 of the value counts as equal to it: rows of equal
-    // logits meet dyadic settings exactly, and the sums round (below 2^-47)
+    // logits meet dyadic settings exactly, and sums of one weight round (below
+    // 2^-47)
     if (kind == kByMassGe) amount *= 1.0 - 0x1p-44;
     if (kind == kByMassGt) amount *= 1.0 + 0x1p-44;
     bool hit = false;
@@ -1766,7 +1775,7 @@ __device__ __forceinline__ void finalize_self(FinLds& s, const SampleArgs& a, in
   f.answer(rp, s.cc[kBins], row_uniform(o, row), row, o, cut_out);
 }
 
-// One row takes 13 us, 512 rows 29: a chain of steps whose latency counts.  Of
+// One row takes 13 us, 512 rows 30: a chain of steps whose latency counts.  Of
 // 25 thousand cycles for a row of 151936 the segments' counters take 7, the
 // weights 2.4, the scan 3.3, a query 3 to 5 and the token's index 6 (in another
 // block's segment).  Runs of items a thread took the weights there from 11; a
@@ -1784,7 +1793,8 @@ __global__ __launch_bounds__(kThreads, 4) void sample_finalize_values_kernel(Sam
 
 // ---------------------------------------------------------------- the filtered row
 
-// A copy with a comparison: 819 x 262144 bf16 in 138 us, 6.2 TB/s read and written.
+// A copy with a comparison: 819 x 262144 bf16 in 139 to 145 us, 6.1 TB/s read and
+// written.
 template <int DT, int NL>
 __global__ __launch_bounds__(kThreads) void sample_apply_kernel(SampleArgs a, int64_t row0, int n_seg,
                                                                 const uint64_t* __restrict__ cuts, uint32_t fill,

@@ -399,7 +399,13 @@ dflash_status dflash_rows_workspace_bytes(const dflash_rows* r, size_t* bytes);
  * T <= 0 or NaN is greedy: the first token of the order alone (the other
  * settings of that row are ignored); T = +inf weighs unmasked tokens alike.
  * Masked tokens (-inf, NaN) are never kept; +inf counts as the type's largest
- * finite value.  Weights, sums and their comparisons are fp64. */
+ * finite value.
+ * Precision: min_p is compared with each token's fp64 weight.  In the sums
+ * (top_p, the draw, prob) a weight is right to 2^-43 of itself and 2^-51
+ * |z_i| / T, weights below 2^-63.9 of the largest count as 0 (bf16 rows of more
+ * than 4096 tokens mostly hold weights to fp64's own rounding), and a sum within
+ * 2^-44 of a border counts as on it: a u that near to 1 takes the last kept
+ * token. */
 typedef struct dflash_filters {
   const float* T;
   const int32_t* top_k;
@@ -427,7 +433,7 @@ dflash_status dflash_sample(const dflash_rows* r, const void* Z, const dflash_fi
  * element type's lowest finite value always is).
  *   out    [R, V] in Z's type with its own row stride; out may be Z itself
  *          (same address and stride), and must not overlap it otherwise
- *   fill   rounded to Z's type
+ *   fill   rounded to Z's type (to an infinity beyond its range)
  *   kept   [R] int32 out or NULL */
 dflash_status dflash_filter(const dflash_rows* r, const void* Z, const dflash_filters* f, float fill, void* out,
                             int64_t out_stride, int32_t* kept_opt, void* ws, size_t ws_bytes, void* stream);
@@ -456,12 +462,16 @@ dflash_status dflash_filter(const dflash_rows* r, const void* Z, const dflash_fi
  *   lse_rest [R] double out, given exactly if t_lse is
  * K = 0 with loss NULL computes lse alone (a teacher's t_lse).  Weight 0 gives
  * 0 in all outputs.  A row whose list has no mass and no t_lse beside it, whose
- * t_lse is infinite, or in which no student logit is unmasked, has D = 0.  NaN or
- * +inf logits make the row's outputs NaN; a masked student token with p > 0
- * makes D +inf.  x_j beyond 2^40 ln 2 are out of fp64's reach: a row whose
+ * t_lse is infinite, or in which no student logit is unmasked, has D = 0.  Else a
+ * NaN or +inf logit of the student makes loss and lse NaN (and lse_rest, if its
+ * token is unlisted), one of the teacher's list the loss; a masked student token
+ * with p > 0 makes D +inf.  x_j beyond 2^40 ln 2 are out of fp64's reach: a row whose
  * largest x_j lies below -2^40 ln 2 (every logit the type's lowest value) has
  * nothing unmasked, and an x_j above 2^40 ln 2 counts as +inf; so do, without
- * t_lse, the list's t_k / tau. */
+ * t_lse, the list's t_k / tau.
+ * Precision: lse and lse_rest are right to 2e-11 and 2^-49 of their size (each
+ * term of their sums to 1.4e-11), the loss to that times its terms and a rounding
+ * to fp32. */
 dflash_status dflash_distill(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
                              const float* t_logit, const double* t_lse_opt, const float* weight_opt, float* loss_opt,
                              double* lse, double* lse_rest_opt, void* ws, size_t ws_bytes, void* stream);
@@ -476,6 +486,9 @@ dflash_status dflash_distill(const dflash_rows* r, const void* S, int32_t K, dou
  *   dS        [R, V] in S's type with its own row stride, written whole; may
  *             be S itself (same address and stride), and must not overlap it
  *             otherwise
+ * Precision: the exponentials are fp32, right to (|t| + 4) 2^-23 + |x_j| 2^-43 of
+ * themselves, t their exponent of two (below 2^-126: 0); a listed token's is fp64.
+ * A row whose loss is NaN comes out NaN (a masked listed token's place may not).
  * One launch, no workspace, no atomics: repeated calls give the same bits. */
 dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K, double tau, const int32_t* t_idx,
                                   const float* t_logit, const double* t_lse_opt, const float* weight_opt,
