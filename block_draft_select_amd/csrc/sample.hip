@@ -416,10 +416,11 @@ __device__ __forceinline__ void list_token(uint32_t* next, uint64_t* list, doubl
 }
 
 // Bound by instructions, about twenty a token, eleven of them fp64 (t, its bin,
-// the weight): 256 x 262144 fp32 in 88 us, 3.1 TB/s.  (In a build that took 74,
-// before tokens under the bins were counted aside: 53 without the weight, 46 for
-// loads and the integer part alone, 10 for the list; the one atomic a token hides
-// behind them.)
+// the weight): 256 x 262144 fp32 in 88 us, 3.1 TB/s.  Counting the tail aside is
+// 8 of them (80 with one atomic for either), for the sake of rows under a mask of
+// finite values (512 x 262144 masked by -1e4: a call of 193 us, 300 with it).  In a
+// build of 74 us the weight took 21, the list 10; the one atomic a token hides
+// behind them.
 template <int NL, bool ALL>
 __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a, int64_t row0, int n_seg, int cap,
                                                                SamplePart* __restrict__ parts, uint64_t* __restrict__ lists) {
