@@ -294,3 +294,124 @@ def test_per_kernel_timers_of_the_four():
             assert dfl.dflash_profile_collect(name) == (0, 0.0)
     finally:
         dfl.dflash_profile_enable(False)
+
+
+# ---------------------------------------------------------------- the largest sizes, and rows beside rows
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_most_rows_of_one_call(dt):
+    import torch
+    import block_draft_select_amd as dfl
+    t = _type(dt)
+    R, V, group = dfl.ROWS_MAX, 3, 1 << 21
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    z = torch.randn(R, V, device="cuda", generator=gen).to(t)
+    u = torch.rand(R, dtype=torch.float64, device="cuda", generator=gen)
+    r = dfl.rows(z)
+    ws = dfl.rows_workspace(r)
+    token = torch.full((R,), -7, dtype=torch.int32, device="cuda")
+    kept, T, k = torch.full_like(token, -7), _arr([1.0, 0.5], torch.float32), _arr([0, 2], torch.int32)
+    _say(f"[rows] {R} rows {dt}")
+    dfl.dflash_sample(r, z, u, token, ws, T=T, top_k=k, group=group, kept=kept)
+    val, at = torch.sort(z.double(), dim=1, descending=True, stable=True)
+    temp = T.double().repeat_interleave(group)[:, None]
+    w = torch.exp((val - val[:, :1]) / temp)
+    w[group:, 2] = 0.0
+    run = torch.cumsum(w, 1)
+    pos = (run <= u[:, None] * run[:, -1:]).sum(1)
+    assert torch.equal(token.long(), at.gather(1, pos[:, None])[:, 0])
+    assert (kept[:group] == 3).all() and (kept[group:] == 2).all()
+    out = torch.empty_like(z)
+    dfl.dflash_filter(r, z, out, ws, T=T, top_k=k, group=group)
+    want = z.clone()
+    want[group:] = want[group:].scatter(1, at[group:, 2:], torch.finfo(t).min)
+    assert torch.equal(out, want)
+    idx, tl = at[:, 1:2].to(torch.int32).contiguous(), torch.zeros(R, 1, device="cuda")
+    loss, lse, _, dS = _run_distill(z, idx, tl, 1.0, None, None, None)
+    ref = torch.logsumexp(z.double(), 1)
+    assert (lse - ref).abs().max() <= 2e-11 + 2.0 ** -46
+    d = ref - val[:, 1]
+    assert ((loss.double() - d).abs() <= d.abs() * 2.0 ** -24 + 1e-10 * (1 + ref.abs())).all()
+    x = z.double() - ref[:, None]
+    g = torch.exp(x).scatter_add(1, at[:, 1:2], torch.full((R, 1), -1.0, dtype=torch.float64, device="cuda"))
+    tol = g.abs() * (torch.finfo(t).eps / 2 + (x.abs() / np.log(2) + 4) * 2.0 ** -23) + 1e-10 * (torch.exp(x) + 1)
+    assert ((dS.double() - g).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_longest_rows_and_lists(dt):
+    import torch
+    import block_draft_select_amd as dfl
+    t = _type(dt)
+    rng = np.random.default_rng(84)
+    V, K = dfl.V_MAX, dfl.DISTILL_K_MAX
+    z = _logits(rng, 2, V, "peaked")
+    _say(f"[rows] V {V} {dt}")
+    v, _ = _tensor(z, t, 1, 1)
+    zz = _f64(v)
+    st = [dict(top_p=0.9), dict(min_p=1e-4, T=1.5)]
+    _check_sample(z, t, st, rng.random(2), pad=1, shift=1)
+    out = torch.empty(2, V + 3, dtype=t, device="cuda")[:, :V]
+    r = dfl.rows(v)
+    dfl.dflash_filter(r, v, out, dfl.rows_workspace(r), **_filters(st))
+    got = _f64(out)
+    for i in range(2):
+        assert np.array_equal(got[i], O.filtered(zz[i], float(torch.finfo(t).min), **_as_used(st[i]))), i
+    s, teacher, idx, tl = _distill_case(rng, 2, V, K, True, True, None)
+    lse = np.array([O.log_sum_exp(x.astype(np.float64)) for x in teacher])
+    _check_distill(s, idx, tl, t, 1.0, lse, None, None, pad=1, shift=1)
+    _check_distill(s, idx, tl, t, 1.0, None, None, None, inplace=True)
+
+
+@pytest.mark.parametrize("dt,R,V", [("bf16", 5, 1000), ("f32", 5, 1000), ("bf16", 5, 30001), ("f32", 5, 30001)])
+def test_outputs_in_the_gaps_between_the_rows(dt, R, V):
+    # input and output rows alternate in one allocation
+    import torch
+    import block_draft_select_amd as dfl
+    t = _type(dt)
+    rng = np.random.default_rng(85)
+    both = torch.zeros(R, 2 * V + 1, dtype=t, device="cuda")
+    v, out = both[:, :V], both[:, V:2 * V]
+    s, _, idx, tl = _distill_case(rng, R, V, 5, False, False, None)
+    v.copy_(torch.from_numpy(s))
+    zz = _f64(v)
+    r = dfl.rows(v)
+    st = [dict(top_k=7), dict(top_p=0.5), dict(min_p=0.2), dict(), dict(T=0.0)]
+    dfl.dflash_filter(r, v, out, dfl.rows_workspace(r), **_filters(st))
+    got = _f64(out)
+    for i in range(R):
+        assert np.array_equal(got[i], O.filtered(zz[i], float(torch.finfo(t).min), **_as_used(st[i]))), i
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    _, _, _, alone = _run_distill(v.contiguous(), dev(idx), dev(tl), 1.0, None, None, None)
+    _run_distill(v, dev(idx), dev(tl), 1.0, None, None, None, out)
+    assert torch.equal(out, alone) and np.array_equal(_f64(v), zz) and not both[:, 2 * V].any()
+
+
+def test_samples_and_filters_on_two_streams_at_once():
+    # each call with a workspace of its own
+    import torch
+    import block_draft_select_amd as dfl
+    rng = np.random.default_rng(86)
+    for dt, R, V in (("bf16", 20, 50021), ("f32", 20, 50021), ("f32", 70, 100003)):
+        z = torch.from_numpy(_logits(rng, R, V, "peaked")).cuda().to(_type(dt))
+        u = torch.rand(R, dtype=torch.float64, device="cuda")
+        f = _filters([MIX[i % len(MIX)] for i in range(R)])
+        r = dfl.rows(z)
+        ws = [dfl.rows_workspace(r) for _ in range(3)]
+        token = [torch.full((R,), -7, dtype=torch.int32, device="cuda") for _ in range(3)]
+        out = [torch.empty_like(z) for _ in range(3)]
+        side = [None, torch.cuda.Stream(), torch.cuda.Stream()]
+
+        def call(i):
+            dfl.dflash_sample(r, z, u, token[i], ws[i], stream=side[i], **f)
+            dfl.dflash_filter(r, z, out[i], ws[i], stream=side[i], **f)
+
+        call(0)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            call(1)
+            call(2)
+        torch.cuda.synchronize()
+        for i in (1, 2):
+            assert torch.equal(token[0], token[i]) and torch.equal(out[0], out[i]), (dt, R, i)
