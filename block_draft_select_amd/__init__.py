@@ -21,12 +21,13 @@ BF16 = 1
 K_MAX, L_MAX, R_MAX, V_MAX, CHUNK = 16, 16, 256, 2097152, 4096
 STATIC_SCRATCH_BYTES = 8 << 20
 ROWS_MAX, DISTILL_K_MAX = 4194304, 1024
+LOGPROBS_M_MAX, TOP_MAX, H_MAX = 1024, 32, 65536
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = 0, 1, 2, 3, 4
 
 KERNELS = ("topk", "gate", "scores", "trace", "stats", "finalize", "cycle_stream", "cycle_scores",
            "cycle_finalize", "conv2tap", "trace_viterbi", "topk_merge", "shard_stats", "shard_finalize", "sample",
-           "filter", "distill", "distill_grad")
+           "filter", "distill", "distill_grad", "quant_i8", "linear_i8", "logprobs", "logprobs_grad")
 
 
 class dflash_dims(ctypes.Structure):
@@ -46,6 +47,11 @@ class dflash_filters(ctypes.Structure):
                 ("min_p", ctypes.c_void_p), ("group", ctypes.c_int32)]
 
 
+class dflash_linear(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("xq_stride", ctypes.c_int64), ("wq_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("N", ctypes.c_int32), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 class DFlashError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(f"{message} (status {status})")
@@ -59,6 +65,7 @@ def _load():
     P, I32, U64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64, ctypes.c_size_t
     I64, F64 = ctypes.c_int64, ctypes.c_double
     D, W, F = ctypes.POINTER(dflash_dims), ctypes.POINTER(dflash_rows), ctypes.POINTER(dflash_filters)
+    L = ctypes.POINTER(dflash_linear)
     sig = {
         "dflash_abi_version": (I32, []),
         "dflash_status_string": (ctypes.c_char_p, [I32]),
@@ -84,6 +91,10 @@ def _load():
         "dflash_filter": (I32, [W, P, F, ctypes.c_float, P, I64, P, P, SZ, P]),
         "dflash_distill": (I32, [W, P, I32, F64, P, P, P, P, P, P, P, P, SZ, P]),
         "dflash_distill_grad": (I32, [W, P, I32, F64, P, P, P, P, P, P, P, P, I64, P]),
+        "dflash_logprobs": (I32, [W, P, P, I32, I32, P, P, P, P, I32, P, P, P, SZ, P]),
+        "dflash_logprobs_grad": (I32, [W, P, P, I32, I32, P, P, P, P, P, P, I64, P]),
+        "dflash_quant_i8": (I32, [W, P, P, I64, P, P]),
+        "dflash_linear_i8": (I32, [L, P, P, P, P, P, P]),
         "dflash_read_probe": (I32, [P, SZ, P, P]),
         "dflash_copy_probe": (I32, [P, P, SZ, P]),
         "dflash_kernel_name": (ctypes.c_char_p, [I32]),
@@ -406,11 +417,15 @@ def _call(fn, device, stream, *args):
             _check(fn(*args, stream.cuda_stream))
 
 
-def _filters(r, device, T, top_k, top_p, min_p, group):
+def _groups(r, group):
     group = operator.index(group)  # the arrays' lengths are checked against it: neither rounded nor wrapped
     if not 1 <= group < 1 << 31:
         raise ValueError(f"group must lie in [1, 2^31), got {group}")
-    n = -(-r.R // group)
+    return group, -(-r.R // group)
+
+
+def _filters(r, device, T, top_k, top_p, min_p, group):
+    group, n = _groups(r, group)
     return dflash_filters(_vec(T, "T", torch.float32, n, device, True), _vec(top_k, "top_k", torch.int32, n, device, True),
                           _vec(top_p, "top_p", torch.float32, n, device, True),
                           _vec(min_p, "min_p", torch.float32, n, device, True), group)
@@ -473,6 +488,108 @@ def dflash_distill_grad(r, S, t_idx, t_logit, lse, dS, tau=1.0, t_lse=None, weig
           _vec(t_lse, "t_lse", torch.float64, r.R, dev, True), _vec(weight, "weight", torch.float32, r.R, dev, True),
           _vec(grad_loss, "grad_loss", torch.float32, r.R, dev, True), _vec(lse, "lse", torch.float64, r.R, dev),
           _vec(lse_rest, "lse_rest", torch.float64, r.R, dev, True), pd, sd)
+
+
+def _given(r, tok, values, name, device):
+    if tok is None and values is None:
+        return 0, None, None
+    if tok is None or values is None or tok.shape != values.shape or tok.dim() < 1:
+        raise ValueError(f"tok and {name} must be given together, with one shape [R, M]")
+    M = tok.shape[-1] if r.R == 0 or tok.numel() != r.R else 1  # [R] as well as [R, 1]
+    return M, _vec(tok, "tok", torch.int32, r.R * M, device), _vec(values, name, torch.float32, r.R * M, device)
+
+
+def dflash_logprobs(r, Z, tok, logp, norm, ws, T=None, group=1, entropy=None, top_idx=None, top_logp=None, stream=None):
+    """Log probabilities ``logp`` of the tokens ``tok`` [R, M] (both None: M =
+    0) in the rows ``Z``, ``norm`` [R, 2] for the gradient, and, if given,
+    ``entropy`` [R] and the largest alternatives ``top_idx``, ``top_logp``
+    [R, N].  ``T``: a temperature per ``group`` rows (None: 1)."""
+    dev = Z.device
+    group, n = _groups(r, group)
+    M, pk, pl = _given(r, tok, logp, "logp", dev)
+    N, pi, pv = 0, None, None
+    if top_idx is not None or top_logp is not None:
+        if top_idx is None or top_logp is None or top_idx.shape != top_logp.shape or top_idx.dim() < 1:
+            raise ValueError("top_idx and top_logp must be given together, with one shape [R, N]")
+        N = top_idx.shape[-1]
+        pi, pv = _vec(top_idx, "top_idx", torch.int32, r.R * N, dev), _vec(top_logp, "top_logp", torch.float32, r.R * N, dev)
+    _call(lib.dflash_logprobs, dev, stream, r, _row_tensor(Z, "Z", r, dev, r.stride)[0],
+          _vec(T, "T", torch.float32, n, dev, True), group, M, pk, pl, _vec(norm, "norm", torch.float32, 2 * r.R, dev),
+          _vec(entropy, "entropy", torch.float32, r.R, dev, True), N, pi, pv, _vec(ws, "ws", torch.uint8, None, dev),
+          ws.numel())
+
+
+def dflash_logprobs_grad(r, Z, tok, grad_logp, norm, dZ, T=None, group=1, entropy=None, grad_entropy=None, stream=None):
+    """The gradient of dflash_logprobs's ``logp`` and ``entropy`` with respect
+    to ``Z`` into ``dZ`` (may be ``Z``)."""
+    dev = Z.device
+    group, n = _groups(r, group)
+    M, pk, pg = _given(r, tok, grad_logp, "grad_logp", dev)
+    pd, sd = _row_tensor(dZ, "dZ", r, dev)
+    _call(lib.dflash_logprobs_grad, dev, stream, r, _row_tensor(Z, "Z", r, dev, r.stride)[0],
+          _vec(T, "T", torch.float32, n, dev, True), group, M, pk, pg,
+          _vec(grad_entropy, "grad_entropy", torch.float32, r.R, dev, True), _vec(norm, "norm", torch.float32, 2 * r.R, dev),
+          _vec(entropy, "entropy", torch.float32, r.R, dev, True), pd, sd)
+
+
+# ------------------------------------------------------------------ rows in 8 bits
+
+def i8_rows(R, H, device="cuda"):
+    """An int8 tensor [R, H] whose rows lie as the 8-bit operators take them:
+    a multiple of 16 bytes apart, from a 16-byte aligned address on."""
+    return torch.empty(R, -(-H // 16) * 16, dtype=torch.int8, device=device)[:, :H]
+
+
+def _i8(t, name, rows_, H, device, stride=None):
+    """Pointer and row stride of an int8 tensor of ``rows_`` rows of H."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows_ or t.shape[1] != H:
+        raise ValueError(f"{name} must have the shape [{rows_}, {H}], got {list(t.shape)}")
+    if H > 1 and t.stride(1) != 1:
+        raise ValueError(f"the elements of a row of {name} must be adjacent")
+    st = t.stride(0) if rows_ > 1 else -(-H // 16) * 16
+    if stride is not None and rows_ > 1 and st != stride:
+        raise ValueError(f"{name} must have the row stride {stride}, got {st}")
+    if t.get_device() != device.index:
+        _on(t, name, device)
+    if rows_ and t.storage_offset() + (rows_ - 1) * st + -(-H // 16) * 16 > t.untyped_storage().nbytes():
+        raise ValueError(f"the last row of {name} must lie in a multiple of 16 bytes (i8_rows makes such tensors)")
+    return t.data_ptr(), st
+
+
+def dflash_quant_i8(r, X, q, scale, stream=None):
+    """The rows ``X`` (described by ``r = rows(X)``) as 8-bit integers ``q``
+    [R, H] (``i8_rows``) with the scales ``scale`` [R]."""
+    dev = X.device
+    pq, sq = _i8(q, "q", r.R, r.V, dev)
+    _call(lib.dflash_quant_i8, dev, stream, r, _row_tensor(X, "X", r, dev, r.stride)[0], pq, sq,
+          _vec(scale, "scale", torch.float32, r.R, dev))
+
+
+def linear_i8(xq, wq, y):
+    """A ``dflash_linear`` value describing ``y`` [..., N] = ``xq`` [R, H] times
+    ``wq`` [N, H]."""
+    ry = rows(y)
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError(f"xq and wq must have the shapes [R, H] and [N, H], got {list(xq.shape)} and {list(wq.shape)}")
+    if ry.R != xq.shape[0] or ry.V != wq.shape[0]:
+        raise ValueError(f"y must hold {xq.shape[0]} rows of {wq.shape[0]}, got {ry.R} of {ry.V}")
+    pitch = -(-xq.shape[1] // 16) * 16
+    return dflash_linear(ry.R, xq.stride(0) if xq.shape[0] > 1 else pitch, wq.stride(0) if wq.shape[0] > 1 else pitch,
+                         ry.stride, ry.V, xq.shape[1], ry.dtype)
+
+
+def dflash_linear_i8(d, xq, xs, wq, ws, y, stream=None):
+    """``y`` = the 8-bit rows ``xq`` (scales ``xs``) times ``wq`` (scales
+    ``ws``), as ``d = linear_i8(xq, wq, y)`` describes them."""
+    dev = xq.device
+    ry = dflash_rows(d.R, d.y_stride, d.N, d.dtype)
+    _call(lib.dflash_linear_i8, dev, stream, d, _i8(xq, "xq", d.R, d.H, dev, d.xq_stride)[0],
+          _vec(xs, "xs", torch.float32, d.R, dev), _i8(wq, "wq", d.N, d.H, dev, d.wq_stride)[0],
+          _vec(ws, "ws", torch.float32, d.N, dev), _row_tensor(y, "y", ry, dev, d.y_stride)[0])
 
 
 def dflash_workspace_init(ws, stream=None):

@@ -110,7 +110,8 @@ hipError_t timed(int kernel, hipStream_t st, F f) {
     }
   }
   const bool on_stream = kernel == DFLASH_KERNEL_TOPK || kernel == DFLASH_KERNEL_SAMPLE ||
-                         kernel == DFLASH_KERNEL_FILTER || kernel == DFLASH_KERNEL_DISTILL;
+                         kernel == DFLASH_KERNEL_FILTER || kernel == DFLASH_KERNEL_DISTILL ||
+                         kernel == DFLASH_KERNEL_LOGPROBS;
   if (a && b) {
     if (on_stream) {
       hipEventRecord(a, st);
@@ -305,6 +306,40 @@ DistillPlan distill_plan(const dflash_rows& r) {
   return p;
 }
 
+// dflash_logprobs: a wave a row of up to four slots a lane; else a block a row,
+// or as many segments as give 2048 blocks (eight per CU), joined by a second launch
+static int logprobs_units(const dflash_rows& r) {
+  return (row_slots(r) + kLogprobsThreads * kLogprobsUnit - 1) / (kLogprobsThreads * kLogprobsUnit);
+}
+
+LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
+  LogprobsPlan p{};
+  const int slots = row_slots(r), units = logprobs_units(r);
+  p.threads = slots <= 64 * kLogprobsUnit ? 64 : kLogprobsThreads;
+  const int64_t want = (kLogprobsBlocks + std::max<int64_t>(r.R, 1) - 1) / std::max<int64_t>(r.R, 1);
+  p.n_seg = (int)std::min<int64_t>(std::min<int64_t>(want, units), kLogprobsMaxSeg);
+  const int per = (units + p.n_seg - 1) / p.n_seg;
+  p.n_seg = (units + per - 1) / per;
+  p.seg_slots = per * kLogprobsThreads * kLogprobsUnit;
+  const DistillPlan d = distill_plan(r);
+  p.grad_loads = d.grad_loads;
+  p.grad_seg = d.grad_seg;
+  if (p.n_seg > 1) {
+    p.lists = align256((size_t)r.R * p.n_seg * sizeof(LogprobsPart));
+    p.total = p.lists + align256((size_t)r.R * p.n_seg * N * sizeof(uint64_t));
+  }
+  return p;
+}
+
+// a bound over all plans of at most R rows: several segments are taken only while they number under 2048 + R < 4096
+static size_t logprobs_workspace(const dflash_rows& r) {
+  const int64_t most = std::min(logprobs_units(r), kLogprobsMaxSeg);
+  if (most <= 1) return 0;
+  const int64_t few = std::min<int64_t>(r.R, kLogprobsBlocks - 1);
+  const size_t segs = (size_t)std::min(few * most, kLogprobsBlocks + few);
+  return align256(segs * sizeof(LogprobsPart)) + align256(segs * DFLASH_TOP_MAX * sizeof(uint64_t));
+}
+
 // Workspace for these rows, or fewer of their length: plans of fewer rows split
 // them further, so this is a bound over all of them that grows with R
 size_t rows_workspace(const dflash_rows& r) {
@@ -312,6 +347,7 @@ size_t rows_workspace(const dflash_rows& r) {
   const int slots = row_slots(r), units = (slots + kDistillUnit - 1) / kDistillUnit;
   const int64_t least_units = (units + kDistillMaxUnits - 1) / kDistillMaxUnits;
   size_t total = align256((size_t)std::min(r.R * units, std::max(r.R * least_units, 2048 + r.R)) * sizeof(DistillPart));
+  total = std::max(total, logprobs_workspace(r));
   if (r.dtype == DFLASH_BF16) {
     const int64_t least = (slots + kSampleMaxSegSlots - 1) / kSampleMaxSegSlots;
     const int64_t most = std::max<int64_t>(least, (slots + 4 * kSampleThreads - 1) / (4 * kSampleThreads));
@@ -404,6 +440,67 @@ dflash_status check_distill(const dflash_rows* r, const void* S, int32_t K, doub
   if (!lse) return fail(DFLASH_ERR_INVALID_ARG, "lse is NULL");
   if ((t_lse != nullptr) != (lse_rest != nullptr))
     return fail(DFLASH_ERR_INVALID_ARG, "lse_rest must be given exactly if t_lse is");
+  return DFLASH_OK;
+}
+
+dflash_status check_logprobs(const dflash_rows* r, const void* Z, int32_t group, int32_t M, const int32_t* tok,
+                             const float* logp, const char* logp_name, const float* norm) {
+  if (group < 1) return fail(DFLASH_ERR_INVALID_ARG, "group must be >= 1");
+  if (M < 0 || M > DFLASH_LOGPROBS_M_MAX) return fail(DFLASH_ERR_INVALID_ARG, "M must be in [0, DFLASH_LOGPROBS_M_MAX]");
+  if (r->R == 0) return DFLASH_OK;
+  if (dflash_status s = check_elem(*r, Z, "Z")) return s;
+  if (M > 0)
+    if (dflash_status s = check_ptrs({{tok, "tok", false}, {logp, logp_name, false}})) return s;
+  if (!norm) return fail(DFLASH_ERR_INVALID_ARG, "norm is NULL");
+  return DFLASH_OK;
+}
+
+// bytes that rows of `width` bytes reach over (2^62 if that is more)
+uintptr_t span(int64_t rows, int64_t stride, int64_t width) {
+  constexpr int64_t kMost = INT64_C(1) << 62;
+  if (rows <= 1) return (uintptr_t)width;
+  return (uintptr_t)(stride > (kMost - width) / (rows - 1) ? kMost : (rows - 1) * stride + width);
+}
+
+bool meet(const void* a, uintptr_t na, const void* b, uintptr_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// an array of `rows` 8-bit rows of H values
+dflash_status check_i8(const void* p, int64_t rows, int64_t stride, int64_t H, const char* name) {
+  if (rows > 1 && (stride < H || stride % 16))
+    return fail(DFLASH_ERR_INVALID_ARG, std::string(name) + "'s stride must be a multiple of 16 and at least H");
+  if (rows > 1 && stride > (INT64_C(1) << 40)) return fail(DFLASH_ERR_UNSUPPORTED, std::string(name) + "'s stride is above 2^40 bytes");
+  if (rows == 0) return DFLASH_OK;
+  return check_ptrs({{p, name, true}});
+}
+
+dflash_status check_linear(const dflash_linear* d, const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
+                           const void* Y) {
+  if (!d) return fail(DFLASH_ERR_INVALID_ARG, "linear is NULL");
+  if (d->R < 0) return fail(DFLASH_ERR_INVALID_ARG, "R must not be negative");
+  if (d->N < 1) return fail(DFLASH_ERR_INVALID_ARG, "N must be >= 1");
+  if (d->H < 1) return fail(DFLASH_ERR_INVALID_ARG, "H must be >= 1");
+  if (d->dtype != DFLASH_F32 && d->dtype != DFLASH_BF16) return fail(DFLASH_ERR_INVALID_ARG, "unknown dtype");
+  if (d->R > DFLASH_ROWS_MAX) return fail(DFLASH_ERR_UNSUPPORTED, "R above DFLASH_ROWS_MAX");
+  if (d->N > DFLASH_V_MAX) return fail(DFLASH_ERR_UNSUPPORTED, "N above DFLASH_V_MAX");
+  if (d->H > DFLASH_H_MAX) return fail(DFLASH_ERR_UNSUPPORTED, "H above DFLASH_H_MAX");
+  if (d->R > 1 && d->y_stride < d->N) return fail(DFLASH_ERR_INVALID_ARG, "Y's stride must be at least N");
+  if (d->R > 1 && d->y_stride > (INT64_C(1) << 40)) return fail(DFLASH_ERR_UNSUPPORTED, "Y's stride is above 2^40 elements");
+  // a launch holds fewer than 2^32 threads
+  if (dfk::linear_blocks(d->R, d->N, d->H) >= (INT64_C(1) << 32) / 512)
+    return fail(DFLASH_ERR_UNSUPPORTED, "R * N too large for one launch");
+  if (dflash_status s = check_i8(xq, d->R, d->xq_stride, d->H, "xq")) return s;
+  if (d->R == 0) return DFLASH_OK;
+  if (dflash_status s = check_i8(wq, d->N, d->wq_stride, d->H, "wq")) return s;
+  if (dflash_status s = check_ptrs({{xs, "xs", false}, {ws, "ws", false}, {Y, "Y", false}})) return s;
+  const int64_t es = (int64_t)logit_bytes(d->dtype), width = ((int64_t)d->H + 15) / 16 * 16;
+  if (reinterpret_cast<uintptr_t>(Y) % es) return fail(DFLASH_ERR_INVALID_ARG, "Y is not aligned to its elements");
+  const uintptr_t ny = span(d->R, d->y_stride * es, d->N * es);
+  if (meet(Y, ny, xq, span(d->R, d->xq_stride, width)) || meet(Y, ny, wq, span(d->N, d->wq_stride, width)) ||
+      meet(Y, ny, xs, d->R * 4) || meet(Y, ny, ws, d->N * 4))
+    return fail(DFLASH_ERR_INVALID_ARG, "Y overlaps an input");
   return DFLASH_OK;
 }
 
@@ -872,6 +969,89 @@ dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K
   }
 }
 
+dflash_status dflash_logprobs(const dflash_rows* r, const void* Z, const float* T_opt, int32_t group, int32_t M,
+                              const int32_t* tok, float* logp, float* norm, float* entropy_opt, int32_t N,
+                              int32_t* top_idx, float* top_logp, void* ws, size_t ws_bytes, void* stream) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_rows(r)) return s;
+    if (dflash_status s = check_logprobs(r, Z, group, M, tok, logp, "logp", norm)) return s;
+    if (N < 0 || N > DFLASH_TOP_MAX) return fail(DFLASH_ERR_INVALID_ARG, "N must be in [0, DFLASH_TOP_MAX]");
+    if (r->R == 0) return DFLASH_OK;
+    if (N > 0)
+      if (dflash_status s = check_ptrs({{top_idx, "top_idx", false}, {top_logp, "top_logp", false}})) return s;
+    const dfk::LogprobsPlan p = dfk::logprobs_plan(*r, N);
+    if (p.total > 0)
+      if (dflash_status s = check_rows_ws(p.total, ws, ws_bytes)) return s;
+    hipStream_t st = (hipStream_t)stream;
+    const dfk::LogprobsArgs a{Z, r->R, r->stride, r->V, group, T_opt, M, N, tok};
+    const dfk::LogprobsOut o{logp, norm, entropy_opt, top_idx, top_logp};
+    return hip_status(timed(DFLASH_KERNEL_LOGPROBS, st, [&] {
+      return dfk::launch_logprobs(r->dtype, a, o, static_cast<char*>(ws), p, st);
+    }), "logprobs launch");
+  } catch (...) {
+    return fail(DFLASH_ERR_HIP, "internal error");
+  }
+}
+
+dflash_status dflash_logprobs_grad(const dflash_rows* r, const void* Z, const float* T_opt, int32_t group, int32_t M,
+                                   const int32_t* tok, const float* grad_logp, const float* grad_entropy_opt,
+                                   const float* norm, const float* entropy_opt, void* dZ, int64_t dz_stride,
+                                   void* stream) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_rows(r)) return s;
+    if (dflash_status s = check_logprobs(r, Z, group, M, tok, grad_logp, "grad_logp", norm)) return s;
+    if (r->R == 0) return DFLASH_OK;
+    if (grad_entropy_opt && !entropy_opt) return fail(DFLASH_ERR_INVALID_ARG, "grad_entropy needs entropy");
+    if (dflash_status s = check_out(*r, Z, dZ, dz_stride, "dZ")) return s;
+    hipStream_t st = (hipStream_t)stream;
+    const dfk::LogprobsArgs a{Z, r->R, r->stride, r->V, group, T_opt, M, 0, tok};
+    return hip_status(timed(DFLASH_KERNEL_LOGPROBS_GRAD, st, [&] {
+      return dfk::launch_logprobs_grad(r->dtype, a, grad_logp, grad_entropy_opt, norm, entropy_opt, dZ, dz_stride,
+                                       dfk::logprobs_plan(*r, 0), st);
+    }), "logprobs gradient launch");
+  } catch (...) {
+    return fail(DFLASH_ERR_HIP, "internal error");
+  }
+}
+
+dflash_status dflash_quant_i8(const dflash_rows* r, const void* X, int8_t* q, int64_t q_stride, float* scale,
+                              void* stream) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_rows(r)) return s;
+    if (dflash_status s = check_i8(q, r->R, q_stride, r->V, "q")) return s;
+    if (r->R == 0) return DFLASH_OK;
+    if (dflash_status s = check_elem(*r, X, "X")) return s;
+    if (dflash_status s = check_ptrs({{scale, "scale", false}})) return s;
+    const int64_t es = (int64_t)logit_bytes(r->dtype);
+    if (meet(X, span(r->R, r->stride * es, r->V * es), q, span(r->R, q_stride, r->V)))
+      return fail(DFLASH_ERR_INVALID_ARG, "q overlaps X");
+    hipStream_t st = (hipStream_t)stream;
+    const dfk::QuantArgs a{X, r->R, r->stride, r->V, q, q_stride, scale};
+    return hip_status(timed(DFLASH_KERNEL_QUANT_I8, st, [&] { return dfk::launch_quant_i8(r->dtype, a, st); }),
+                      "quantisation launch");
+  } catch (...) {
+    return fail(DFLASH_ERR_HIP, "internal error");
+  }
+}
+
+dflash_status dflash_linear_i8(const dflash_linear* d, const int8_t* xq, const float* xs, const int8_t* wq,
+                               const float* ws, void* Y, void* stream) {
+  try {
+    g_err.clear();
+    if (dflash_status s = check_linear(d, xq, xs, wq, ws, Y)) return s;
+    if (d->R == 0) return DFLASH_OK;
+    hipStream_t st = (hipStream_t)stream;
+    const dfk::LinearArgs a{d->R, d->xq_stride, d->wq_stride, d->y_stride, d->N, d->H, xq, xs, wq, ws, Y};
+    return hip_status(timed(DFLASH_KERNEL_LINEAR_I8, st, [&] { return dfk::launch_linear_i8(d->dtype, a, st); }),
+                      "8-bit product launch");
+  } catch (...) {
+    return fail(DFLASH_ERR_HIP, "internal error");
+  }
+}
+
 dflash_status dflash_read_probe(const void* buf, size_t bytes, uint32_t* sink, void* stream) {
   try {
     g_err.clear();
@@ -899,7 +1079,8 @@ const char* dflash_kernel_name(int32_t kernel) {
                                                    "cycle_stream", "cycle_scores", "cycle_finalize", "conv2tap",
                                                    "trace_viterbi", "topk_merge", "shard_stats",
                                                    "shard_finalize", "sample", "filter", "distill",
-                                                   "distill_grad"};
+                                                   "distill_grad", "quant_i8", "linear_i8", "logprobs",
+                                                   "logprobs_grad"};
   return (kernel >= 0 && kernel < DFLASH_KERNEL_COUNT) ? names[kernel] : "";
 }
 

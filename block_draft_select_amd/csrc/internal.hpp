@@ -267,6 +267,65 @@ hipError_t launch_distill(int32_t dtype, const DistillArgs& a, float* loss, doub
                           const DistillPlan& pl, hipStream_t st);
 hipError_t launch_distill_grad(int32_t dtype, const DistillArgs& a, const float* grad_loss, const double* lse,
                                const double* lse_rest, void* dS, int64_t d_stride, const DistillPlan& pl, hipStream_t st);
+// dflash_logprobs: a block streams seg_slots slots of a row; the gradient as dflash_distill's
+constexpr int kLogprobsThreads = 256;
+constexpr int kLogprobsUnit = 4;       // slots a thread loads at a time
+constexpr int kLogprobsMaxSeg = 256;   // segments of a row: one a thread of the join
+constexpr int kLogprobsBlocks = 2048;  // eight a CU
+struct LogprobsPart {
+  double M, s, h;  // reference (a power of two), sums of 2^t and 2^t t over the segment
+  float m;         // its largest logit
+};
+struct LogprobsArgs {
+  const void* Z;
+  int64_t R, stride;
+  int32_t V, group;
+  const float* T;  // or null
+  int32_t M, N;
+  const int32_t* tok;
+};
+struct LogprobsOut {
+  float* logp;
+  float* norm;
+  float* entropy;  // or null
+  int32_t* top_idx;
+  float* top_logp;
+};
+struct LogprobsPlan {
+  int threads, n_seg, seg_slots;
+  int grad_loads, grad_seg;
+  size_t lists, total;
+};
+LogprobsPlan logprobs_plan(const dflash_rows& r, int N);
+hipError_t launch_logprobs(int32_t dtype, const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl,
+                           hipStream_t st);
+hipError_t launch_logprobs_grad(int32_t dtype, const LogprobsArgs& a, const float* g_logp, const float* g_ent,
+                                const float* norm, const float* entropy, void* dZ, int64_t d_stride,
+                                const LogprobsPlan& pl, hipStream_t st);
+
+// ---- rows in 8 bits ----
+struct QuantArgs {
+  const void* X;
+  int64_t R, stride;
+  int32_t H;
+  int8_t* q;
+  int64_t q_stride;
+  float* scale;
+};
+hipError_t launch_quant_i8(int32_t dtype, const QuantArgs& a, hipStream_t st);
+struct LinearArgs {
+  int64_t R, xq_stride, wq_stride, y_stride;
+  int32_t N, H;
+  const int8_t* xq;
+  const float* xs;
+  const int8_t* wq;
+  const float* ws;
+  void* y;
+};
+// blocks of the launch (a block has at most 512 threads)
+int64_t linear_blocks(int64_t R, int32_t N, int32_t H);
+hipError_t launch_linear_i8(int32_t dtype, const LinearArgs& a, hipStream_t st);
+
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t st);
 // device address and size of the library's static scratch on the current
 // device (looked up once per device)

@@ -1,0 +1,607 @@
+// dflash_logprobs and dflash_logprobs_grad: log probabilities of given tokens
+// of a row of logits, its entropy and its largest alternatives; the gradient
+// of the first two.
+//
+// With m = max z, c = log2 e / T and any reference M,
+//   t_j = z_j c - M,  s = sum_j 2^t_j,  h = sum_j 2^t_j t_j:
+//   log sum_j e^((z_j - m) / T) = ln 2 (log2 s + M - m c),
+//   entropy                     = ln 2 (log2 s - h / s).
+// t_j is one fma, right to half a step of itself however large M is, so the
+// terms that count (t near 0) are right to 2^-23; a thread sums 16 or 32 of
+// them in fp32 and adds that to fp64.  M is a whole number, so that a larger
+// one scales the sums exactly.  It is m c rounded, to half a step of fp32: a row
+// with |m| c beyond 2^30, where that step nears fp32's exponents (all of it the
+// type's lowest value, or T below 1e-8), is summed again from z_j - m.
+//
+// The alternatives take nothing from the streaming loop but three maxima a
+// thread: of the 64 bytes a thread loads at a time (a piece), the two largest
+// maxima with their places and the third.  The N-th largest of the threads'
+// maxima bounds the N-th largest logit from below, so only pieces whose maximum
+// reaches it are read again: about N of them.
+#include "rows_blocks.hpp"
+
+namespace dfk {
+
+namespace {
+
+constexpr double kLog2e64 = 1.4426950408889634;
+constexpr double kLn2 = 0.6931471805599453;
+constexpr int kU = kLogprobsUnit;  // slots of a piece
+constexpr int kPieces = 512;       // pieces that are read again
+constexpr int kCap = 512;          // tokens of those that are ranked
+constexpr float kHuge = 0x1p30f;   // |m| c beyond this, whose rounding 2^t may not hold: from z - m
+
+// log2 e over a row's temperature, which lies in [1e-30, 1e30]; 0, below or NaN: 1
+__device__ __forceinline__ double row_scale(const float* T, int group, int64_t row) {
+  const float t = T ? T[row / group] : 1.0f;
+  return t > 0.0f ? kLog2e64 / fmin(fmax((double)t, 1e-30), 1e30) : kLog2e64;
+}
+
+template <int T>
+struct Shared {
+  float tm[T];                 // the threads' maxima
+  uint64_t key[kCap];          // value and inverted index of tokens that may be alternatives
+  uint32_t piece[kPieces];     // thread | piece << 8
+  float wave_m[T / kWave];
+  double wave_s[T / kWave], wave_h[T / kWave];
+  uint32_t n_piece, n_key;
+  float tau;
+  uint64_t least;
+  uint64_t top[DFLASH_TOP_MAX];
+};
+
+__device__ __forceinline__ uint64_t token_key(float v, int idx) {
+  return ((uint64_t)ord32_canon(__float_as_uint(v)) << 32) | (uint32_t)~idx;
+}
+__device__ __forceinline__ int key_token(uint64_t k) { return (int)~(uint32_t)k; }
+__device__ __forceinline__ float key_value(uint64_t k) { return __uint_as_float(unord32((uint32_t)(k >> 32))); }
+
+// what a row, or a segment of one, has come to
+struct Sums {
+  float m;      // the largest logit; -inf: nothing unmasked; NaN: a NaN or +inf among them
+  double M;     // the sums' reference
+  double s, h;
+};
+
+__device__ __forceinline__ double reference(float m, float c) {
+  return rint((double)fminf(fmaxf(m * c, -kHuge), kHuge));
+}
+
+// s and h from reference `from` to a larger one
+__device__ __forceinline__ void rebase(double from, double to, double& s, double& h) {
+  const double d = from - to;  // a whole number
+  s = ldexp(s, (int)fmax(d, -4000.0));
+  h = ldexp(h, (int)fmax(d, -4000.0));
+  h = s > 0.0 ? fma(d, s, h) : 0.0;
+}
+
+// the N largest keys of sh.key[0 .. n), in order, to sh.top; the others of sh.top are 0
+template <int T>
+__device__ void rank_keys(Shared<T>& sh, int n, int N) {
+  if (threadIdx.x < DFLASH_TOP_MAX) sh.top[threadIdx.x] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += T) {
+    const uint64_t k = sh.key[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += sh.key[j] > k;
+    if (rank < N) sh.top[rank] = k;
+  }
+  __syncthreads();
+}
+
+// The N largest tokens of a segment with no bound on how many tie: slots in the
+// order of their index, the tokens above the N-th best so far join it.  One more
+// pass over the segment.
+template <int DT, int T>
+__device__ __noinline__ void top_by_scan(Shared<T>& sh, const RowRef<DT> z, int s0, int s1, int N) {
+  constexpr int VE = RowType<DT>::VE;
+  const int tid = threadIdx.x;
+  __syncthreads();
+  if (tid == 0) sh.n_key = 0, sh.least = 0;
+  __syncthreads();
+  for (int b = s0; b < s1; b += T) {
+    const Slot x = z.load(b + tid < s1 ? b + tid : z.slots());
+    uint64_t least = sh.least;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float v = slot_value<DT>(x, i);
+      any |= v > kNegInf && token_key(v, (b + tid) * VE + i) > least;
+    }
+    if (!__syncthreads_or(any)) continue;
+#pragma unroll 1
+    for (int i = 0; i < VE; ++i) {
+      // at most T new keys beside the N kept
+      float v = slot_value<DT>(x, 0);
+#pragma unroll
+      for (int q = 1; q < VE; ++q)
+        if (i == q) v = slot_value<DT>(x, q);
+      const uint64_t k = token_key(v, (b + tid) * VE + i);
+      least = sh.least;
+      const bool hit = v > kNegInf && k > least;
+      if (!__syncthreads_or(hit)) continue;
+      if (hit) sh.key[atomicAdd(&sh.n_key, 1u)] = k;
+      __syncthreads();
+      const int n = (int)sh.n_key;
+      rank_keys(sh, n, N);
+      if (tid < N) sh.key[tid] = sh.top[tid];
+      if (tid == 0) {
+        sh.n_key = (uint32_t)min(n, N);
+        if (n >= N) sh.least = sh.top[N - 1];
+      }
+      __syncthreads();
+    }
+  }
+  rank_keys(sh, (int)sh.n_key, N);
+}
+
+// The N largest tokens of the segment to sh.top.  m1, m2, m3: the largest maxima of
+// this thread's pieces, u1 and u2 where the first two are.
+template <int DT, int T>
+__device__ __forceinline__ void top_of_segment(Shared<T>& sh, const RowRef<DT>& z, int s0, int s1, int N, float m1, float m2,
+                                               float m3, int u1, int u2) {
+  constexpr int VE = RowType<DT>::VE;
+  const int tid = threadIdx.x;
+  sh.tm[tid] = m1;
+  if (tid == 0) sh.n_piece = 0, sh.n_key = 0, sh.tau = kNegInf;
+  __syncthreads();
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < T; j += 4) {
+    const float4 o = *reinterpret_cast<const float4*>(&sh.tm[j]);
+    rank += (o.x > m1 || (o.x == m1 && j < tid)) + (o.y > m1 || (o.y == m1 && j + 1 < tid)) +
+            (o.z > m1 || (o.z == m1 && j + 2 < tid)) + (o.w > m1 || (o.w == m1 && j + 3 < tid));
+  }
+  if (rank == N - 1) sh.tau = m1;
+  __syncthreads();
+  const float tau = sh.tau;
+  auto note = [&](int u) {
+    const uint32_t at = atomicAdd(&sh.n_piece, 1u);
+    if (at < (uint32_t)kPieces) sh.piece[at] = (uint32_t)tid | (uint32_t)u << 8;
+  };
+  const int n_unit = (s1 - s0 + T * kU - 1) / (T * kU);
+  if (m1 >= tau && m1 > kNegInf) {
+    if (m3 >= tau && m3 > kNegInf) {
+      for (int u = 0; u < n_unit; ++u) {
+        note(u);
+        if (*(volatile uint32_t*)&sh.n_piece > (uint32_t)kPieces) break;  // too many: the scan below
+      }
+    } else {
+      note(u1);
+      if (m2 >= tau && m2 > kNegInf) note(u2);
+    }
+  }
+  __syncthreads();
+  const int n_piece = (int)sh.n_piece;
+  bool full = n_piece > kPieces;
+  if (!full) {
+    for (int i = tid; i < n_piece * kU; i += T) {
+      const uint32_t p = sh.piece[i / kU];
+      const int slot = s0 + ((int)(p >> 8) * kU + i % kU) * T + (int)(p & 255u);
+      if (slot >= s1) continue;
+      const Slot x = z.load(slot);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) {
+        const float v = slot_value<DT>(x, q);
+        if (v >= tau && v > kNegInf) {
+          const uint32_t at = atomicAdd(&sh.n_key, 1u);
+          if (at < (uint32_t)kCap) sh.key[at] = token_key(v, slot * VE + q);
+        }
+      }
+    }
+    __syncthreads();
+    full = sh.n_key > (uint32_t)kCap;
+  }
+  if (full)
+    top_by_scan<DT, T>(sh, z, s0, s1, N);
+  else
+    rank_keys(sh, (int)sh.n_key, N);
+}
+
+// streams slots s0 .. s1 - 1 of a row
+template <int DT, int T, bool ENT, bool TOP>
+__device__ __forceinline__ Sums sum_segment(Shared<T>& sh, const RowRef<DT>& z, int s0, int s1, float c, int N) {
+  constexpr int VE = RowType<DT>::VE;
+  const int tid = threadIdx.x;
+  float m1 = kNegInf, m2 = kNegInf, m3 = kNegInf, Mf = -kHuge;
+  int u1 = 0, u2 = 0, u = 0;
+  double s = 0.0, h = 0.0;
+  bool any_odd = false;
+#pragma unroll 1
+  for (int b = s0; b < s1; b += T * kU, ++u) {
+    Slot x[kU];
+#pragma unroll
+    for (int l = 0; l < kU; ++l) {
+      const int slot = b + l * T + tid;
+      x[l] = z.template load<true>(slot < s1 ? slot : z.slots());
+    }
+    bool odd;
+    const float m = largest<DT>(x, odd);
+    any_odd |= odd;
+    if (TOP) {
+      const bool a1 = m > m1, a2 = m > m2;
+      m3 = a2 ? m2 : fmaxf(m3, m);
+      m2 = a1 ? m1 : a2 ? m : m2;
+      u2 = a1 ? u1 : a2 ? u : u2;
+      u1 = a1 ? u : u1;
+    }
+    if (m > m1) {
+      m1 = m;
+      const float to = (float)reference(m, c);
+      rebase((double)Mf, (double)to, s, h);
+      Mf = to;
+    }
+    float ps[kU], ph[kU];
+#pragma unroll
+    for (int l = 0; l < kU; ++l) {
+      ps[l] = ph[l] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float t = fmaf(slot_value<DT>(x[l], i), c, -Mf);
+        const float e = __builtin_amdgcn_exp2f(t);
+        ps[l] += e;
+        if (ENT) ph[l] = fmaf(e, t, ph[l]);
+      }
+    }
+    float us = (ps[0] + ps[1]) + (ps[2] + ps[3]), uh = (ph[0] + ph[1]) + (ph[2] + ph[3]);
+    if (ENT && uh != uh) {  // a masked token: 0 times -inf
+      uh = 0.0f;
+#pragma unroll
+      for (int l = 0; l < kU; ++l)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          const float t = fmaf(slot_value<DT>(x[l], i), c, -Mf);
+          const float e = __builtin_amdgcn_exp2f(t);
+          uh = fmaf(e, fmaxf(t, -256.0f), uh);
+        }
+    }
+    s += (double)us;
+    if (ENT) h += (double)uh;
+  }
+  // over the block: the largest logit, then sums at its reference
+  float bm = wave_max_dpp_f32(any_odd ? INFINITY : m1);
+  if constexpr (T > kWave) {
+    if ((tid & 63) == 0) sh.wave_m[tid >> 6] = bm;
+    __syncthreads();
+    bm = sh.wave_m[0];
+#pragma unroll
+    for (int w = 1; w < T / kWave; ++w) bm = fmaxf(bm, sh.wave_m[w]);
+  }
+  Sums r{};
+  if (bm == INFINITY) {
+    r.m = NAN;
+    return r;
+  }
+  r.m = bm;
+  if (bm > kNegInf) {
+    r.M = reference(bm, c);
+    if (m1 > kNegInf) rebase((double)Mf, r.M, s, h); else s = h = 0.0;
+    r.s = wave_sum_dpp_f64(s);
+    if (ENT) r.h = wave_sum_dpp_f64(h);
+    if constexpr (T > kWave) {
+      if ((tid & 63) == 0) sh.wave_s[tid >> 6] = r.s, sh.wave_h[tid >> 6] = r.h;
+      __syncthreads();
+      r.s = r.h = 0.0;
+#pragma unroll
+      for (int w = 0; w < T / kWave; ++w) r.s += sh.wave_s[w], r.h += sh.wave_h[w];
+    }
+  }
+  if (TOP) top_of_segment<DT, T>(sh, z, s0, s1, N, m1, m2, m3, u1, u2);
+  return r;
+}
+
+// The sums of a row whose |m| c leaves fp32, from z - m (reference m c): one more pass over the row
+template <int DT, int T>
+__device__ __noinline__ void sum_far(Shared<T>& sh, const RowRef<DT> z, float m, double c, double& s, double& h) {
+  constexpr int VE = RowType<DT>::VE;
+  const int tid = threadIdx.x;
+  s = h = 0.0;
+  for (int b = tid; b < z.slots(); b += T) {
+    const Slot x = z.load(b);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const double t = fmax(((double)slot_value<DT>(x, i) - (double)m) * c, -2000.0), e = exp2(t);
+      s += e;
+      h = fma(e, t, h);
+    }
+  }
+  s = wave_sum_dpp_f64(s);
+  h = wave_sum_dpp_f64(h);
+  if constexpr (T > kWave) {
+    __syncthreads();
+    if ((tid & 63) == 0) sh.wave_s[tid >> 6] = s, sh.wave_h[tid >> 6] = h;
+    __syncthreads();
+    s = h = 0.0;
+#pragma unroll
+    for (int w = 0; w < T / kWave; ++w) s += sh.wave_s[w], h += sh.wave_h[w];
+  }
+}
+
+// a row's outputs from its sums and its alternatives (sh.top)
+template <int DT, int T>
+__device__ __forceinline__ void write_row(Shared<T>& sh, const LogprobsArgs& a, const LogprobsOut& o, int64_t row, Sums r, double c) {
+  const int tid = threadIdx.x;
+  const RowRef<DT> z(a.Z, row, a.stride, a.V);
+  double l = 0.0, ent = 0.0;
+  if (r.m > kNegInf) {
+    double off = r.M - (double)r.m * (double)(float)c;
+    if (!(fabsf(r.m) * (float)c < kHuge)) {
+      sum_far<DT, T>(sh, z, r.m, c, r.s, r.h);
+      off = 0.0;
+    }
+    const double ls = log2(r.s);
+    l = kLn2 * (ls + off);
+    ent = fmax(kLn2 * (ls - r.h / r.s), 0.0);
+  } else if (r.m != r.m) {
+    l = ent = NAN;
+  }
+  if (tid == 0) {
+    o.norm[2 * row] = r.m;
+    o.norm[2 * row + 1] = (float)l;
+    if (o.entropy) o.entropy[row] = (float)ent;
+  }
+  const double per = c * kLn2;  // 1 / T
+  for (int k = tid; k < a.M; k += T) {
+    const int t = a.tok[row * a.M + k];
+    float v = 0.0f;
+    if (t >= 0 && t < a.V) v = r.m == kNegInf ? kNegInf : (float)(((double)row_value<DT>(z, t) - (double)r.m) * per - l);
+    o.logp[row * a.M + k] = v;
+  }
+  if (tid < a.N) {
+    const uint64_t k = r.m > kNegInf ? sh.top[tid] : 0;
+    o.top_idx[row * a.N + tid] = k ? key_token(k) : -1;
+    o.top_logp[row * a.N + tid] =
+        r.m != r.m ? NAN : k ? (float)(((double)key_value(k) - (double)r.m) * per - l) : kNegInf;
+  }
+}
+
+// One row, or one segment of it, a block: streams it once.
+template <int DT, int T, bool ENT, bool TOP>
+__global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, LogprobsOut o, int n_seg, int seg_slots,
+                                                     LogprobsPart* __restrict__ parts, uint64_t* __restrict__ lists) {
+  __shared__ Shared<T> sh;
+  const int seg = blockIdx.x % n_seg;
+  const int64_t row = blockIdx.x / n_seg;
+  const RowRef<DT> z(a.Z, row, a.stride, a.V);
+  const double c = row_scale(a.T, a.group, row);
+  const int s0 = seg * seg_slots, s1 = min(s0 + seg_slots, z.slots());
+  const Sums r = sum_segment<DT, T, ENT, TOP>(sh, z, s0, s1, (float)c, a.N);
+  if (n_seg == 1) {
+    write_row<DT, T>(sh, a, o, row, r, c);
+  } else {
+    if (threadIdx.x == 0) parts[blockIdx.x] = LogprobsPart{r.M, r.s, r.h, r.m};
+    if (TOP && threadIdx.x < a.N) lists[(int64_t)blockIdx.x * a.N + threadIdx.x] = r.m == r.m && r.m > kNegInf ? sh.top[threadIdx.x] : 0;
+  }
+}
+
+// joins a row's segments
+template <int DT, int T>
+__global__ __launch_bounds__(T) void logprobs_join_kernel(LogprobsArgs a, LogprobsOut o, int n_seg,
+                                                          const LogprobsPart* __restrict__ parts,
+                                                          const uint64_t* __restrict__ lists) {
+  __shared__ Shared<T> sh;
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const double c = row_scale(a.T, a.group, row);
+  const LogprobsPart* part = parts + row * n_seg;
+  // at most T segments
+  LogprobsPart p{0.0, 0.0, 0.0, kNegInf};
+  if (tid < n_seg) p = part[tid];
+  float bm = wave_max_dpp_f32(p.m != p.m ? INFINITY : p.m);
+  if ((tid & 63) == 0) sh.wave_m[tid >> 6] = bm;
+  __syncthreads();
+  bm = sh.wave_m[0];
+#pragma unroll
+  for (int w = 1; w < T / kWave; ++w) bm = fmaxf(bm, sh.wave_m[w]);
+  Sums r{};
+  r.m = bm == INFINITY ? NAN : bm;
+  if (r.m > kNegInf) {
+    r.M = reference(r.m, (float)c);
+    if (p.m > kNegInf) rebase(p.M, r.M, p.s, p.h);
+    r.s = wave_sum_dpp_f64(p.s);
+    r.h = wave_sum_dpp_f64(p.h);
+    if ((tid & 63) == 0) sh.wave_s[tid >> 6] = r.s, sh.wave_h[tid >> 6] = r.h;
+    __syncthreads();
+    r.s = r.h = 0.0;
+#pragma unroll
+    for (int w = 0; w < T / kWave; ++w) r.s += sh.wave_s[w], r.h += sh.wave_h[w];
+  }
+  if (a.N > 0 && r.m > kNegInf) {
+    // the N-th largest of the segments' best bounds the row's N-th from below;
+    // lists are in order, and at most N of them reach it with at most N tokens each
+    const uint64_t* list = lists + row * n_seg * a.N;
+    sh.key[tid] = tid < n_seg ? list[(int64_t)tid * a.N] : 0;
+    if (tid == 0) sh.least = 1, sh.n_key = 0;
+    __syncthreads();
+    const uint64_t mine = sh.key[tid];
+    int rank = 0;
+    for (int j = 0; j < n_seg; ++j) rank += sh.key[j] > mine;
+    if (mine && rank == a.N - 1) sh.least = mine;
+    __syncthreads();
+    const uint64_t least = sh.least;
+    // N rounds: the k-th of every list still at or above the bound, ranked with
+    // the N best so far
+    if (tid < DFLASH_TOP_MAX) sh.top[tid] = 0;
+    int k = 0;
+    uint64_t next = tid < n_seg ? mine : 0;
+    for (; k < a.N; ++k) {
+      const bool in = next >= least && next;
+      if (!__syncthreads_or(in)) break;
+      if (in) {
+        const uint32_t at = atomicAdd(&sh.n_key, 1u);
+        if (at < (uint32_t)kCap) sh.key[at] = next;
+        next = k + 1 < a.N ? list[(int64_t)tid * a.N + k + 1] : 0;
+      } else {
+        next = 0;
+      }
+      __syncthreads();
+      if (sh.n_key > (uint32_t)(kCap - T)) {
+        const int n = (int)sh.n_key;
+        rank_keys(sh, n, a.N);
+        if (tid < a.N) sh.key[tid] = sh.top[tid];
+        if (tid == 0) sh.n_key = (uint32_t)min(n, a.N);
+        __syncthreads();
+      }
+    }
+    __syncthreads();
+    rank_keys(sh, (int)sh.n_key, a.N);
+  }
+  write_row<DT, T>(sh, a, o, row, r, c);
+}
+
+// ---------------------------------------------------------------- backward
+
+struct GradRed {
+  double d[kLogprobsThreads / kWave];
+};
+
+// dz_j = p_j (a0 + a1 log2 p_j) + (the given token's own gradients) / T, with
+//   a0 = -(sum g + g_H H) / T,  a1 = -g_H ln 2 / T.
+// One read and one write of the row.
+template <int DT, int NL>
+__global__ __launch_bounds__(kLogprobsThreads) void logprobs_grad_kernel(LogprobsArgs a, const float* __restrict__ g_logp,
+                                                                         const float* __restrict__ g_ent,
+                                                                         const float* __restrict__ norm,
+                                                                         const float* __restrict__ entropy, void* dZ,
+                                                                         int64_t d_stride, int n_seg) {
+  using E = typename RowType<DT>::elem;
+  constexpr int VE = RowType<DT>::VE, T = kLogprobsThreads;
+  constexpr int kPerThread = DFLASH_LOGPROBS_M_MAX / T;
+  __shared__ int tok[DFLASH_LOGPROBS_M_MAX];
+  __shared__ float grad[DFLASH_LOGPROBS_M_MAX];
+  __shared__ GradRed red;
+  const int tid = threadIdx.x, seg = blockIdx.x % n_seg;
+  const int64_t row = blockIdx.x / n_seg;
+  const RowRef<DT> z(a.Z, row, a.stride, a.V);
+  E* o = static_cast<E*>(dZ) + row * d_stride;
+  const int s0 = seg * (T * NL), e0 = s0 * VE, e1 = e0 + T * NL * VE;
+  const double c = row_scale(a.T, a.group, row), per = c * kLn2;
+  const float m = norm[2 * row], l = norm[2 * row + 1];
+  const double gh = g_ent ? (double)g_ent[row] : 0.0;
+
+  // the given tokens of the row, and the sum of their gradients
+  double A = 0.0;
+  bool some = gh != 0.0;
+  float own[kPerThread];
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int k = j * T + tid;
+    if (j * T < a.M && k < a.M) {
+      const int t = a.tok[row * a.M + k];
+      const bool in = t >= 0 && t < a.V;
+      const float g = in ? g_logp[row * a.M + k] : 0.0f;
+      tok[k] = in ? t : -1;
+      grad[k] = g;
+      some |= g != 0.0f;
+      A += (double)g;
+      if (in && t >= e0 && t < e1) own[j] = row_value<DT>(z, t);
+    }
+  }
+  A = wave_sum_dpp_f64(A);
+  if ((tid & 63) == 0) red.d[tid >> 6] = A;
+  some = __syncthreads_or(some);
+  A = red.d[0];
+#pragma unroll
+  for (int w = 1; w < T / kWave; ++w) A += red.d[w];
+  if (!some || m == kNegInf) {  // no gradient comes in, or nothing is unmasked
+#pragma unroll
+    for (int q = 0; q < NL; ++q) store_slot<DT>(o, a.V, s0 + q * T + tid, Slot{{0, 0, 0, 0}});
+    return;
+  }
+  Slot x[NL];
+#pragma unroll
+  for (int q = 0; q < NL; ++q) x[q] = z.template load<true>(s0 + q * T + tid);
+  const double H = g_ent ? (double)entropy[row] : 0.0;
+  double a0 = -(A + gh * H) * per, a1 = -gh * kLn2 * per;
+  if (m != m) a0 = NAN;
+  // factors near fp32's end leave their power of two to the exponent, so that
+  // unlikely tokens' gradients, which fit, do not become inf times 0
+  const double big = fmax(fabs(a0), 256.0 * fabs(a1));
+  const int up = big >= 0x1p100 && big < INFINITY ? ilogb(big) : 0;
+  const float f0 = (float)ldexp(a0, -up), f1 = (float)ldexp(a1, -up), fup = (float)up;
+  // log2 p in two pieces of fp32 (-inf: NaN at times, which the maximum below replaces)
+  const double l2 = (double)l * kLog2e64;
+  const float ch = (float)c, cl = (float)(c - (double)ch), lh = (float)l2, ll = (float)(l2 - (double)lh);
+  __syncthreads();  // every given token's logit is read (dZ may be Z)
+#pragma unroll
+  for (int q = 0; q < NL; ++q) {
+    Slot y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y.w[k] = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float d = slot_value<DT>(x[q], i) - m;
+      const float t = fmaxf(fmaf(d, ch, -lh) + fmaf(d, cl, -ll), -256.0f);
+      const float g = __builtin_amdgcn_exp2f(t + fup) * fmaf(f1, t, f0);
+      if constexpr (DT == DFLASH_BF16)
+        y.w[i >> 1] |= bf16_round(g) << ((i & 1) * 16);
+      else
+        y.w[i] = __float_as_uint(g);
+    }
+    store_slot<DT>(o, a.V, s0 + q * T + tid, y);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int k = j * T + tid;
+    if (j * T < a.M && k < a.M && tok[k] >= e0 && tok[k] < e1) {
+      double g = 0.0;  // every entry of this token, in order
+      for (int q = 0; q < a.M; ++q)
+        if (tok[q] == tok[k]) g += (double)grad[q];
+      const double lp = ((double)own[j] - (double)m) * per - (double)l;
+      const double p = exp(lp);
+      const double d = p > 0.0 ? p * (a0 + a1 * kLog2e64 * lp) : m != m ? (double)NAN : 0.0;
+      o[tok[k]] = to_elem<DT>((float)(d + g * per));
+    }
+  }
+}
+
+template <int DT, int T, bool ENT, bool TOP>
+hipError_t run(const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl, hipStream_t st) {
+  LogprobsPart* parts = reinterpret_cast<LogprobsPart*>(ws);
+  uint64_t* lists = reinterpret_cast<uint64_t*>(ws + pl.lists);
+  launch(logprobs_kernel<DT, T, ENT, TOP>, dim3((unsigned)(a.R * pl.n_seg)), dim3(T), st, a, o, pl.n_seg, pl.seg_slots, parts, lists);
+  if (pl.n_seg > 1)
+    launch(logprobs_join_kernel<DT, kLogprobsThreads>, dim3((unsigned)a.R), dim3(kLogprobsThreads), st, a, o, pl.n_seg,
+           (const LogprobsPart*)parts, (const uint64_t*)lists);
+  return hipGetLastError();
+}
+
+template <int DT, int T>
+hipError_t run_threads(const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl, hipStream_t st) {
+  if (a.N > 0) return o.entropy ? run<DT, T, true, true>(a, o, ws, pl, st) : run<DT, T, false, true>(a, o, ws, pl, st);
+  return o.entropy ? run<DT, T, true, false>(a, o, ws, pl, st) : run<DT, T, false, false>(a, o, ws, pl, st);
+}
+
+template <int DT>
+hipError_t run_typed(const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl, hipStream_t st) {
+  return pl.threads == kWave ? run_threads<DT, kWave>(a, o, ws, pl, st) : run_threads<DT, kLogprobsThreads>(a, o, ws, pl, st);
+}
+
+template <int DT>
+hipError_t run_grad(const LogprobsArgs& a, const float* g_logp, const float* g_ent, const float* norm, const float* entropy,
+                    void* dZ, int64_t d_stride, const LogprobsPlan& pl, hipStream_t st) {
+  const dim3 grid((unsigned)(a.R * pl.grad_seg)), block(kLogprobsThreads);
+  switch (pl.grad_loads) {
+    case 1: launch(logprobs_grad_kernel<DT, 1>, grid, block, st, a, g_logp, g_ent, norm, entropy, dZ, d_stride, pl.grad_seg); break;
+    case 2: launch(logprobs_grad_kernel<DT, 2>, grid, block, st, a, g_logp, g_ent, norm, entropy, dZ, d_stride, pl.grad_seg); break;
+    case 4: launch(logprobs_grad_kernel<DT, 4>, grid, block, st, a, g_logp, g_ent, norm, entropy, dZ, d_stride, pl.grad_seg); break;
+    default: launch(logprobs_grad_kernel<DT, 8>, grid, block, st, a, g_logp, g_ent, norm, entropy, dZ, d_stride, pl.grad_seg);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_logprobs(int32_t dtype, const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl,
+                           hipStream_t st) {
+  return dtype == DFLASH_BF16 ? run_typed<DFLASH_BF16>(a, o, ws, pl, st) : run_typed<DFLASH_F32>(a, o, ws, pl, st);
+}
+
+hipError_t launch_logprobs_grad(int32_t dtype, const LogprobsArgs& a, const float* g_logp, const float* g_ent, const float* norm,
+                                const float* entropy, void* dZ, int64_t d_stride, const LogprobsPlan& pl, hipStream_t st) {
+  return dtype == DFLASH_BF16 ? run_grad<DFLASH_BF16>(a, g_logp, g_ent, norm, entropy, dZ, d_stride, pl, st)
+                              : run_grad<DFLASH_F32>(a, g_logp, g_ent, norm, entropy, dZ, d_stride, pl, st);
+}
+
+}  // namespace dfk

@@ -28,7 +28,10 @@
  * dflash_conv2tap is the drafter's two-tap dynamic convolution, upstream of
  * the context vectors h.  Around the cycle: dflash_sample and dflash_filter
  * (top-k, top-p, min-p on any logit rows), dflash_distill and
- * dflash_distill_grad (the drafter's loss against a teacher's top logits).
+ * dflash_distill_grad (the drafter's loss against a teacher's top logits),
+ * dflash_logprobs and dflash_logprobs_grad (log probabilities of given
+ * tokens, entropy and top alternatives), dflash_quant_i8 and
+ * dflash_linear_i8 (logits from hidden vectors and a head in 8 bits).
  *
  * Conventions for every entry point:
  *   - Every array argument is a DEVICE pointer owned by the caller; the
@@ -85,6 +88,9 @@ extern "C" {
 #define DFLASH_CHUNK 4096    /* tokens per first-level item of the residual draw */
 #define DFLASH_ROWS_MAX 4194304  /* rows of one call on a dflash_rows */
 #define DFLASH_DISTILL_K_MAX 1024 /* listed teacher tokens per row */
+#define DFLASH_LOGPROBS_M_MAX 1024 /* given tokens per row */
+#define DFLASH_TOP_MAX 32    /* alternatives per row */
+#define DFLASH_H_MAX 65536   /* products per sum of dflash_linear_i8 */
 #define DFLASH_STATIC_SCRATCH_BYTES (8u << 20) /* the library's own scratch per GPU (dflash_cycle_static) */
 
 typedef int32_t dflash_status;
@@ -360,10 +366,11 @@ dflash_status dflash_conv2tap(const dflash_dims* d, const void* x, const void* x
                               void* stream);
 
 /* ---- rows of vocabulary logits ------------------------------------------
- * Four operators around the cycle that take any set of logit rows: the
- * filters a serving request asks for (dflash_sample, dflash_filter) and the
- * drafter's training loss (dflash_distill, dflash_distill_grad).  The
- * conventions above hold except that
+ * Operators around the cycle that take any set of logit rows: the filters a
+ * serving request asks for (dflash_sample, dflash_filter), the drafter's
+ * training loss (dflash_distill, dflash_distill_grad), and what a client or a
+ * policy's loss wants to know of a row (dflash_logprobs,
+ * dflash_logprobs_grad).  The conventions above hold except that
  *   - rows may have any length, any stride and any element-aligned address
  *     (16-byte aligned rows whose stride is a multiple of 16 bytes are the
  *     fastest);
@@ -379,7 +386,7 @@ typedef struct dflash_rows {
   int32_t dtype;  /* DFLASH_F32 | DFLASH_BF16 */
 } dflash_rows;
 
-/* Bytes of workspace any of the four needs for these rows, or for fewer of the
+/* Bytes of workspace any of them needs for these rows, or for fewer of the
  * same V and dtype (host only, pure; grows with R).  The contents need no
  * initialisation; calls that overlap in time, and captured graphs whose
  * replays may, must not share a workspace. */
@@ -495,6 +502,92 @@ dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K
                                   const float* grad_loss_opt, const double* lse, const double* lse_rest_opt, void* dS,
                                   int64_t ds_stride, void* stream);
 
+/* Log probabilities of given tokens, the row's entropy and its largest
+ * alternatives.  With x_j = z_j / T, m = max z and l = log sum_j
+ * e^((z_j - m) / T):
+ *   log p_j = (z_j - m) / T - l,   H = -sum_j p_j log p_j.
+ *   T        [ceil(R / group)] float or NULL (ones): the temperature of `group`
+ *            consecutive rows, clamped into [1e-30, 1e30]; 0, negative or NaN
+ *            counts as 1 (a greedy request reports its logits as they are)
+ *   tok      [R, M] int32, M in 0..DFLASH_LOGPROBS_M_MAX; a token may come
+ *            several times, an id outside [0, V) is padding
+ *   logp     [R, M] float out: log p of them (padding: 0)
+ *   norm     [R, 2] float out: m and l, what the gradient needs
+ *   entropy  [R] float out or NULL
+ *   top_idx  [R, N] int32 out, N in 0..DFLASH_TOP_MAX: the N largest logits'
+ *            tokens, by logit descending, then index ascending (-0 equal to +0)
+ *   top_logp [R, N] float out: their log p; what a row has fewer unmasked
+ *            tokens than N leaves -1 and -inf
+ * A masked token (-inf) has log p -inf and no part in the sums.  A row with
+ * nothing unmasked has log p -inf, H 0 and norm (-inf, 0).  A row with a NaN or
+ * +inf logit has NaN throughout, its alternatives -1 (padding stays 0).  Finite
+ * lowest values are logits like any other.
+ * Precision: l, log p and H are right to 2^-21 and 2^-23 of their size (the sums'
+ * terms to 2^-22, added in fp32 up to 32 at a time and in fp64 beyond). */
+dflash_status dflash_logprobs(const dflash_rows* r, const void* Z, const float* T_opt, int32_t group, int32_t M,
+                              const int32_t* tok, float* logp, float* norm, float* entropy_opt, int32_t N,
+                              int32_t* top_idx, float* top_logp, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient: of sum_k grad_logp_k log p_{tok_k} + grad_entropy H in each row,
+ *   dZ_j = (1 / T) (sum_k grad_logp_k ([tok_k = j] - p_j) - grad_entropy p_j (log p_j + H)),
+ * with the arguments of the forward call and what it wrote (norm, and entropy
+ * where grad_entropy is given).
+ *   grad_logp    [R, M] float (padding's is not read)
+ *   grad_entropy [R] float or NULL (zeros)
+ *   dZ           [R, V] in Z's type with its own row stride, written whole; may
+ *                be Z itself (same address and stride), and must not overlap it
+ *                otherwise
+ * A row whose incoming gradients are all 0, or with nothing unmasked, gets zeros
+ * (its Z counts for nothing); a row with NaN in norm gets NaN.
+ * Precision: p_j is right to (|log2 p_j| + 4) 2^-23 of itself (below 2^-126: 0); a
+ * given token's gradient is computed in fp64.  One launch, no workspace, no
+ * atomics: repeated calls give the same bits. */
+dflash_status dflash_logprobs_grad(const dflash_rows* r, const void* Z, const float* T_opt, int32_t group, int32_t M,
+                                   const int32_t* tok, const float* grad_logp, const float* grad_entropy_opt,
+                                   const float* norm, const float* entropy_opt, void* dZ, int64_t dz_stride,
+                                   void* stream);
+
+/* ---- rows in 8 bits -----------------------------------------------------
+ * Where the rows of logits come from: hidden vectors times a vocabulary head
+ * (or any other linear map of the drafter), both in 8-bit integers with one
+ * scale a row, so that the head, the largest thing a step reads, takes half of
+ * bf16's bytes.  An 8-bit row of H values lies in H bytes rounded up to a
+ * multiple of 16, of any contents behind the H (they belong to the array, the
+ * last row's too); rows start at multiples of 16 bytes. */
+
+/* Rows in 8 bits: scale = max |x| / 127 (nearest fp32), q = x / scale to the
+ * nearest integer, ties to even (beyond 127, where a subnormal scale was rounded
+ * down: 127).  A row of zeros, or whose scale is 0, has q = 0 and scale 0; a row
+ * with a NaN or an infinity q = 0 and scale NaN, which makes its products NaN.
+ *   r      R rows of V = H values (H up to DFLASH_V_MAX)
+ *   X      [R, H];  q [R, H] int8 out, rows q_stride bytes apart (a multiple
+ *          of 16, at least H), 16-byte aligned; what lies between rows stays
+ *   scale  [R] float out
+ * The weights of a head are rows like any other: one scale a token of the
+ * vocabulary.  One launch, no workspace. */
+dflash_status dflash_quant_i8(const dflash_rows* r, const void* X, int8_t* q, int64_t q_stride, float* scale,
+                              void* stream);
+
+typedef struct dflash_linear {
+  int64_t R;         /* rows of xq and Y (tokens), 0..DFLASH_ROWS_MAX */
+  int64_t xq_stride; /* bytes between rows of xq, a multiple of 16, >= H (any value if R <= 1) */
+  int64_t wq_stride; /* bytes between rows of wq, a multiple of 16, >= H (any value if N = 1) */
+  int64_t y_stride;  /* elements between rows of Y, >= N (any value if R <= 1) */
+  int32_t N;         /* rows of wq, columns of Y (channels), 1..DFLASH_V_MAX */
+  int32_t H;         /* values of an 8-bit row, 1..DFLASH_H_MAX */
+  int32_t dtype;     /* of Y: DFLASH_F32 | DFLASH_BF16 */
+} dflash_linear;
+
+/* The product of two sets of 8-bit rows:
+ *   Y[r, n] = xs[r] * ws[n] * sum_k xq[r, k] wq[n, k].
+ *   xq [R, H] int8, xs [R] float;  wq [N, H] int8, ws [N] float;  Y [R, N] out,
+ *   any element-aligned address; it must not overlap the inputs
+ * The sum is exact (int32; -128 may occur); it is rounded to fp32, multiplied by
+ * xs, then by ws, each rounded to fp32, and rounded to Y's type.  R = 0 is an
+ * empty call.  One launch, no workspace; may be captured into a HIP graph. */
+dflash_status dflash_linear_i8(const dflash_linear* d, const int8_t* xq, const float* xs, const int8_t* wq,
+                               const float* ws, void* Y, void* stream);
+
 /* ---- measurement helpers (not part of the method) ---------------------- */
 
 /* Stream-read `bytes` (multiple of 16, 16-byte aligned) of `buf` once: the
@@ -530,7 +623,11 @@ enum {
   DFLASH_KERNEL_FILTER = 15,        /* dflash_filter (all of its launches) */
   DFLASH_KERNEL_DISTILL = 16,       /* dflash_distill (both launches) */
   DFLASH_KERNEL_DISTILL_GRAD = 17,  /* dflash_distill_grad */
-  DFLASH_KERNEL_COUNT = 18
+  DFLASH_KERNEL_QUANT_I8 = 18,      /* dflash_quant_i8 */
+  DFLASH_KERNEL_LINEAR_I8 = 19,     /* dflash_linear_i8 */
+  DFLASH_KERNEL_LOGPROBS = 20,      /* dflash_logprobs (one launch or two) */
+  DFLASH_KERNEL_LOGPROBS_GRAD = 21, /* dflash_logprobs_grad */
+  DFLASH_KERNEL_COUNT = 22
 };
 
 /* Name of a kernel identifier ("" if out of range). */

@@ -18,8 +18,9 @@ that a reader can check each step against the pages by eye:
   drafter's block representations.
 * ``oracle.viterbi`` -- the global max-sum path through the candidate
   lattice (a variant of the greedy trace).
-* ``oracle.rows``    -- filters and draws on logit rows, and distillation from
-  a teacher's top logits.
+* ``oracle.rows``    -- filters and draws on logit rows, distillation from a
+  teacher's top logits, log probabilities with entropy and alternatives.
+* ``oracle.i8``      -- rows in 8-bit integers and their product.
 
 Pinned by ``tests/test_oracle_*.py`` against known-answer vectors, closed
 forms, brute-force enumeration and chi-square tests (see each function's
@@ -33,3 +34,4 @@ from . import dflash  # noqa: F401
 from . import conv  # noqa: F401
 from . import viterbi  # noqa: F401
 from . import rows  # noqa: F401
+from . import i8  # noqa: F401

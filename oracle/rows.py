@@ -118,3 +118,60 @@ def distill(s, t_idx, t_logit, tau=1.0, t_lse=None):
         g = g - np.where(unlisted, p_rest * np.exp(x - rest), 0.0)
     out.update(grad=g / tau, loss=loss, p=pv, A=A, p_rest=p_rest)
     return out
+
+
+def temperature(T):
+    """What a row's temperature counts as: 0, negative or NaN as 1, others within [1e-30, 1e30]."""
+    T = float(T)
+    return min(max(T, 1e-30), 1e30) if T > 0 else 1.0
+
+
+def distribution(z, T=1.0):
+    """(m, l, log p [V], H) of one row: m = max z, l = log sum e^((z - m) / T).
+    Nothing unmasked: (-inf, 0, all -inf, 0); a NaN or +inf logit: all NaN."""
+    z = np.asarray(z, dtype=np.float64)
+    if np.isnan(z).any() or (z == np.inf).any():
+        return np.nan, np.nan, np.full(z.shape, np.nan), np.nan
+    m = z.max()
+    if m == -np.inf:
+        return -np.inf, 0.0, np.full(z.shape, -np.inf), 0.0
+    with np.errstate(over="ignore", under="ignore"):
+        x = (z - m) / temperature(T)
+        e = np.exp(x)
+        l = float(np.log(e.sum()))
+        logp = x - l
+        p = e / e.sum()
+    return m, l, logp, float(-np.sum(p[p > 0] * logp[p > 0]))
+
+
+def logprobs(z, tok, N=0, T=1.0):
+    """One row's log probabilities of the tokens ``tok`` (0 for one outside the
+    vocabulary), (m, l), entropy, and the N largest tokens with theirs."""
+    z = np.asarray(z, dtype=np.float64)
+    m, l, logp, H = distribution(z, T)
+    given = np.array([logp[t] if 0 <= t < z.size else 0.0 for t in np.asarray(tok, dtype=np.int64)])
+    idx, top = np.full(N, -1, dtype=np.int64), np.full(N, np.nan if np.isnan(m) else -np.inf)
+    if not np.isnan(m):
+        o = order(z)[:N]
+        idx[:o.size], top[:o.size] = o, logp[o]
+    return dict(logp=given, norm=(m, l), entropy=H, top_idx=idx, top_logp=top)
+
+
+def logprobs_grad(z, tok, g_logp, g_entropy, norm, entropy, T=1.0):
+    """The gradient of sum_k g_logp_k log p_{tok_k} + g_entropy H in one row's
+    logits, from (m, l) and H as the forward pass left them."""
+    z = np.asarray(z, dtype=np.float64)
+    tok, g = np.asarray(tok, dtype=np.int64), np.asarray(g_logp, dtype=np.float64)
+    on = (tok >= 0) & (tok < z.size)
+    tok, g = tok[on], g[on]
+    m, l = (float(v) for v in norm)
+    if m == -np.inf or (not np.any(g != 0) and g_entropy == 0):
+        return np.zeros(z.shape)
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        logp = (z - m) / temperature(T) - l
+        p = np.exp(logp)
+        d = -g.sum() * p
+        if g_entropy != 0:
+            d = d - g_entropy * np.where(p > 0, p * (logp + entropy), 0.0)
+    np.add.at(d, tok, g)
+    return np.full(z.shape, np.nan) if np.isnan(m) else d / temperature(T)
