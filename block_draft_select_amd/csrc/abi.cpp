@@ -471,7 +471,8 @@ bool meet(const void* a, uintptr_t na, const void* b, uintptr_t nb) {
 dflash_status check_i8(const void* p, int64_t rows, int64_t stride, int64_t H, const char* name) {
   if (rows > 1 && (stride < H || stride % 16))
     return fail(DFLASH_ERR_INVALID_ARG, std::string(name) + "'s stride must be a multiple of 16 and at least H");
-  if (rows > 1 && stride > (INT64_C(1) << 40)) return fail(DFLASH_ERR_UNSUPPORTED, std::string(name) + "'s stride is above 2^40 bytes");
+  if (rows > 1 && stride > DFLASH_I8_STRIDE_MAX)
+    return fail(DFLASH_ERR_UNSUPPORTED, std::string(name) + "'s stride is above DFLASH_I8_STRIDE_MAX");
   if (rows == 0) return DFLASH_OK;
   return check_ptrs({{p, name, true}});
 }

@@ -91,6 +91,7 @@ extern "C" {
 #define DFLASH_LOGPROBS_M_MAX 1024 /* given tokens per row */
 #define DFLASH_TOP_MAX 32    /* alternatives per row */
 #define DFLASH_H_MAX 65536   /* products per sum of dflash_linear_i8 */
+#define DFLASH_I8_STRIDE_MAX 16777216 /* bytes between 8-bit rows */
 #define DFLASH_STATIC_SCRATCH_BYTES (8u << 20) /* the library's own scratch per GPU (dflash_cycle_static) */
 
 typedef int32_t dflash_status;
@@ -553,7 +554,8 @@ dflash_status dflash_logprobs_grad(const dflash_rows* r, const void* Z, const fl
  * scale a row, so that the head, the largest thing a step reads, takes half of
  * bf16's bytes.  An 8-bit row of H values lies in H bytes rounded up to a
  * multiple of 16, of any contents behind the H (they belong to the array, the
- * last row's too); rows start at multiples of 16 bytes. */
+ * last row's too); rows start at multiples of 16 bytes, at most
+ * DFLASH_I8_STRIDE_MAX apart. */
 
 /* Rows in 8 bits: scale = max |x| / 127 (nearest fp32), q = x / scale to the
  * nearest integer, ties to even (beyond 127, where a subnormal scale was rounded
