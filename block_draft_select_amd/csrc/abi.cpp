@@ -308,22 +308,28 @@ DistillPlan distill_plan(const dflash_rows& r) {
 
 // dflash_logprobs: a wave a row of up to four slots a lane; else a block a row,
 // or as many segments as give 2048 blocks (eight per CU), joined by a second launch
-static int logprobs_units(const dflash_rows& r) {
-  return (row_slots(r) + kLogprobsThreads * kLogprobsUnit - 1) / (kLogprobsThreads * kLogprobsUnit);
-}
+static int logprobs_units(const dflash_rows& r) { return (row_slots(r) + kLogprobsThreads - 1) / kLogprobsThreads; }
 
 LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
   LogprobsPlan p{};
   const int slots = row_slots(r), units = logprobs_units(r);
-  p.threads = slots <= 64 * kLogprobsUnit ? 64 : kLogprobsThreads;
-  const int64_t want = (kLogprobsBlocks + std::max<int64_t>(r.R, 1) - 1) / std::max<int64_t>(r.R, 1);
-  p.n_seg = (int)std::min<int64_t>(std::min<int64_t>(want, units), kLogprobsMaxSeg);
-  const int per = (units + p.n_seg - 1) / p.n_seg;
-  p.n_seg = (units + per - 1) / per;
-  p.seg_slots = per * kLogprobsThreads * kLogprobsUnit;
   const DistillPlan d = distill_plan(r);
   p.grad_loads = d.grad_loads;
   p.grad_seg = d.grad_seg;
+  p.n_seg = 1;
+  p.seg_slots = slots;
+  p.unit = 4;
+  if (slots <= 64 * p.unit) {
+    p.threads = 64;
+    return p;
+  }
+  p.threads = kLogprobsThreads;
+  const int64_t want = (kLogprobsBlocks + std::max<int64_t>(r.R, 1) - 1) / std::max<int64_t>(r.R, 1);
+  p.n_seg = (int)std::min<int64_t>(std::min<int64_t>(want, units), kLogprobsMaxSeg);
+  const int per = (units + p.n_seg - 1) / p.n_seg;  // slots a thread
+  p.n_seg = (units + per - 1) / per;
+  p.seg_slots = per * kLogprobsThreads;
+  if (per < 4) p.unit = 1;
   if (p.n_seg > 1) {
     p.lists = align256((size_t)r.R * p.n_seg * sizeof(LogprobsPart));
     p.total = p.lists + align256((size_t)r.R * p.n_seg * N * sizeof(uint64_t));

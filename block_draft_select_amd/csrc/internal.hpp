@@ -269,7 +269,6 @@ hipError_t launch_distill_grad(int32_t dtype, const DistillArgs& a, const float*
                                const double* lse_rest, void* dS, int64_t d_stride, const DistillPlan& pl, hipStream_t st);
 // dflash_logprobs: a block streams seg_slots slots of a row; the gradient as dflash_distill's
 constexpr int kLogprobsThreads = 256;
-constexpr int kLogprobsUnit = 4;       // slots a thread loads at a time
 constexpr int kLogprobsMaxSeg = 256;   // segments of a row: one a thread of the join
 constexpr int kLogprobsBlocks = 2048;  // eight a CU
 struct LogprobsPart {
@@ -293,6 +292,7 @@ struct LogprobsOut {
 };
 struct LogprobsPlan {
   int threads, n_seg, seg_slots;
+  int unit;  // slots a thread loads at a time
   int grad_loads, grad_seg;
   size_t lists, total;
 };

@@ -14,10 +14,10 @@
 // type's lowest value, or T below 1e-8), is summed again from z_j - m.
 //
 // The alternatives take nothing from the streaming loop but three maxima a
-// thread: of the 64 bytes a thread loads at a time (a piece), the two largest
-// maxima with their places and the third.  The N-th largest of the threads'
-// maxima bounds the N-th largest logit from below, so only pieces whose maximum
-// reaches it are read again: about N of them.
+// thread: of the slots a thread loads at a time (a piece), the two largest maxima
+// with their places and the third.  A bound that N threads' maxima reach bounds
+// the N-th largest logit from below, so only pieces whose maximum reaches it
+// are read again: little more than N of them.
 #include "rows_blocks.hpp"
 
 namespace dfk {
@@ -26,9 +26,9 @@ namespace {
 
 constexpr double kLog2e64 = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
-constexpr int kU = kLogprobsUnit;  // slots of a piece
 constexpr int kPieces = 512;       // pieces that are read again
-constexpr int kCap = 512;          // tokens of those that are ranked
+constexpr int kCap = 1024;         // tokens of those that are ranked; of as many lists of the join
+static_assert(kCap >= DFLASH_TOP_MAX * DFLASH_TOP_MAX && kPieces >= kLogprobsMaxSeg, "the join's lists");
 constexpr float kHuge = 0x1p30f;   // |m| c beyond this, whose rounding 2^t may not hold: from z - m
 
 // log2 e over a row's temperature, which lies in [1e-30, 1e30]; 0, below or NaN: 1
@@ -39,13 +39,12 @@ __device__ __forceinline__ double row_scale(const float* T, int group, int64_t r
 
 template <int T>
 struct Shared {
-  float tm[T];                 // the threads' maxima
+  uint32_t tm[T];              // the threads' maxima, as ordered keys
   uint64_t key[kCap];          // value and inverted index of tokens that may be alternatives
   uint32_t piece[kPieces];     // thread | piece << 8
   float wave_m[T / kWave];
   double wave_s[T / kWave], wave_h[T / kWave];
-  uint32_t n_piece, n_key;
-  float tau;
+  uint32_t n_piece, n_key, tau;
   uint64_t least;
   uint64_t top[DFLASH_TOP_MAX];
 };
@@ -55,6 +54,60 @@ __device__ __forceinline__ uint64_t token_key(float v, int idx) {
 }
 __device__ __forceinline__ int key_token(uint64_t k) { return (int)~(uint32_t)k; }
 __device__ __forceinline__ float key_value(uint64_t k) { return __uint_as_float(unord32((uint32_t)(k >> 32))); }
+
+// a thread's largest logit; whether one is NaN or +inf (then both are any value);
+// low: the most negative logit, or any if there is none below zero
+template <int DT, int N>
+__device__ __forceinline__ float largest(const Slot (&x)[N], bool& odd, float& low) {
+  if constexpr (DT == DFLASH_BF16) {
+    // signed and unsigned maxima of the raw patterns, two a word: the signed one
+    // is the largest logit unless all are negative (then the unsigned minimum
+    // is), and a NaN of either sign stands over its infinity
+    uint32_t hi = 0x80008000u, up = 0;
+#pragma unroll
+    for (int l = 0; l < N; ++l)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        hi = smax_i16x2(hi, x[l].w[d]);
+        up = max_u16x2(up, x[l].w[d]);
+      }
+    const int h = max((int)(int16_t)(hi & 0xFFFFu), (int)(int16_t)(hi >> 16));
+    const uint32_t u = max(up & 0xFFFFu, up >> 16);
+    odd = h >= 0x7F80 || u > 0xFF80u;
+    low = __uint_as_float(u << 16);
+    uint32_t best = (uint32_t)h;
+    if (h < 0) {
+      uint32_t lo = 0xFFFFFFFFu;
+#pragma unroll
+      for (int l = 0; l < N; ++l)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) lo = min_u16x2(lo, x[l].w[d]);
+      best = min(lo & 0xFFFFu, lo >> 16);
+    }
+    return __uint_as_float(best << 16);
+  } else {
+    int hi = INT32_MIN;
+    uint32_t up = 0;
+#pragma unroll
+    for (int l = 0; l < N; ++l)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        hi = max(hi, (int)x[l].w[d]);
+        up = max(up, x[l].w[d]);
+      }
+    odd = hi >= 0x7F800000 || up > 0xFF800000u;
+    low = __uint_as_float(up);
+    uint32_t best = (uint32_t)hi;
+    if (hi < 0) {
+      best = 0xFFFFFFFFu;
+#pragma unroll
+      for (int l = 0; l < N; ++l)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) best = min(best, x[l].w[d]);
+    }
+    return __uint_as_float(best);
+  }
+}
 
 // what a row, or a segment of one, has come to
 struct Sums {
@@ -83,6 +136,7 @@ __device__ void rank_keys(Shared<T>& sh, int n, int N) {
   for (int i = threadIdx.x; i < n; i += T) {
     const uint64_t k = sh.key[i];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) rank += sh.key[j] > k;
     if (rank < N) sh.top[rank] = k;
   }
@@ -135,55 +189,68 @@ __device__ __noinline__ void top_by_scan(Shared<T>& sh, const RowRef<DT> z, int 
   rank_keys(sh, (int)sh.n_key, N);
 }
 
+__device__ __forceinline__ uint32_t value_key(float v) { return ord32_canon(__float_as_uint(v)); }
+constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // of -inf
+
 // The N largest tokens of the segment to sh.top.  m1, m2, m3: the largest maxima of
 // this thread's pieces, u1 and u2 where the first two are.
-template <int DT, int T>
+template <int DT, int T, int U>
 __device__ __forceinline__ void top_of_segment(Shared<T>& sh, const RowRef<DT>& z, int s0, int s1, int N, float m1, float m2,
                                                float m3, int u1, int u2) {
   constexpr int VE = RowType<DT>::VE;
   const int tid = threadIdx.x;
-  sh.tm[tid] = m1;
-  if (tid == 0) sh.n_piece = 0, sh.n_key = 0, sh.tau = kNegInf;
+  const uint32_t k1 = value_key(m1), k2 = value_key(m2), k3 = value_key(m3);
+  sh.tm[tid] = k1;
+  if (tid == 0) sh.n_piece = 0, sh.n_key = 0;
   __syncthreads();
-  int rank = 0;
-#pragma unroll 4
-  for (int j = 0; j < T; j += 4) {
-    const float4 o = *reinterpret_cast<const float4*>(&sh.tm[j]);
-    rank += (o.x > m1 || (o.x == m1 && j < tid)) + (o.y > m1 || (o.y == m1 && j + 1 < tid)) +
-            (o.z > m1 || (o.z == m1 && j + 2 < tid)) + (o.w > m1 || (o.w == m1 && j + 3 < tid));
+  if (tid < kWave) {
+    // from the highest bit on the largest value that N maxima reach, or one that few more reach
+    uint32_t k[T / kWave], t = 0;
+#pragma unroll
+    for (int q = 0; q < T / kWave; ++q) k[q] = sh.tm[q * kWave + tid];
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t c = t | 1u << bit;
+      int n = 0;
+#pragma unroll
+      for (int q = 0; q < T / kWave; ++q) n += __popcll(__ballot(k[q] >= c));
+      if (n >= N) {
+        t = c;
+        if (n <= N + 4) break;
+      }
+    }
+    if (tid == 0) sh.tau = max(t, kMaskedKey + 1);
   }
-  if (rank == N - 1) sh.tau = m1;
   __syncthreads();
-  const float tau = sh.tau;
+  const uint32_t tau = sh.tau;
   auto note = [&](int u) {
     const uint32_t at = atomicAdd(&sh.n_piece, 1u);
     if (at < (uint32_t)kPieces) sh.piece[at] = (uint32_t)tid | (uint32_t)u << 8;
   };
-  const int n_unit = (s1 - s0 + T * kU - 1) / (T * kU);
-  if (m1 >= tau && m1 > kNegInf) {
-    if (m3 >= tau && m3 > kNegInf) {
+  const int n_unit = (s1 - s0 + T * U - 1) / (T * U);
+  if (k1 >= tau) {
+    if (k3 >= tau) {
       for (int u = 0; u < n_unit; ++u) {
         note(u);
         if (*(volatile uint32_t*)&sh.n_piece > (uint32_t)kPieces) break;  // too many: the scan below
       }
     } else {
       note(u1);
-      if (m2 >= tau && m2 > kNegInf) note(u2);
+      if (k2 >= tau) note(u2);
     }
   }
   __syncthreads();
   const int n_piece = (int)sh.n_piece;
   bool full = n_piece > kPieces;
   if (!full) {
-    for (int i = tid; i < n_piece * kU; i += T) {
-      const uint32_t p = sh.piece[i / kU];
-      const int slot = s0 + ((int)(p >> 8) * kU + i % kU) * T + (int)(p & 255u);
+    for (int i = tid; i < n_piece * U; i += T) {
+      const uint32_t p = sh.piece[i / U];
+      const int slot = s0 + ((int)(p >> 8) * U + i % U) * T + (int)(p & 255u);
       if (slot >= s1) continue;
       const Slot x = z.load(slot);
 #pragma unroll
       for (int q = 0; q < VE; ++q) {
         const float v = slot_value<DT>(x, q);
-        if (v >= tau && v > kNegInf) {
+        if (value_key(v) >= tau) {
           const uint32_t at = atomicAdd(&sh.n_key, 1u);
           if (at < (uint32_t)kCap) sh.key[at] = token_key(v, slot * VE + q);
         }
@@ -198,25 +265,88 @@ __device__ __forceinline__ void top_of_segment(Shared<T>& sh, const RowRef<DT>& 
     rank_keys(sh, (int)sh.n_key, N);
 }
 
-// streams slots s0 .. s1 - 1 of a row
-template <int DT, int T, bool ENT, bool TOP>
-__device__ __forceinline__ Sums sum_segment(Shared<T>& sh, const RowRef<DT>& z, int s0, int s1, float c, int N) {
+// adds the terms of U slots to s and h
+template <int DT, bool ENT, bool MASKED, int U>
+__device__ __forceinline__ void add_terms(Slot (&x)[U], float c, float M, double& s, double& h) {
   constexpr int VE = RowType<DT>::VE;
+  float ps[U], ph[U];
+#pragma unroll
+  for (int l = 0; l < U; ++l) {
+    ps[l] = ph[l] = 0.0f;
+    if (MASKED) {  // or the compiler takes the words apart before it branches here, into twice the registers
+#pragma unroll
+      for (int d = 0; d < 4; ++d) asm volatile("" : "+v"(x[l].w[d]));
+    }
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const float t = fmaf(slot_value<DT>(x[l], i), c, -M);
+      const float e = __builtin_amdgcn_exp2f(t);
+      ps[l] += e;
+      if (ENT) ph[l] = fmaf(e, MASKED ? fmaxf(t, -256.0f) : t, ph[l]);  // 0 times -inf
+    }
+    asm volatile("" : "+v"(ps[l]), "+v"(ph[l]));  // slot by slot: else all terms are kept at once, and spill
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int w = 1; w < U; w *= 2)
+#pragma unroll
+    for (int l = 0; l < U; l += 2 * w) ps[l] += ps[l + w], ph[l] += ph[l + w];
+  s += (double)ps[0];
+  if (ENT) h += (double)ph[0];
+}
+
+// A slot whose elements' order does not matter: the last one of a row comes as the 16
+// bytes that end with the row, what the slot before it holds of them masked;
+// slots from s1 on are masked.  Rows of at least one whole slot.
+template <int DT>
+__device__ __forceinline__ Slot load_unordered(const RowRef<DT>& z, int slot, int s1) {
+  constexpr int VE = RowType<DT>::VE;
+  const int e = slot * VE, at = min(e, z.V - VE);
+  const u32x4_any v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(z.p + at));
+  Slot s{{v.x, v.y, v.z, v.w}};
+  const int drop = slot < s1 ? e - at : VE;  // elements that do not belong here
+  if (drop > 0) {
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+      if (i < drop) {
+        if constexpr (DT == DFLASH_BF16)
+          s.w[i >> 1] = (i & 1) ? (s.w[i >> 1] & 0x0000FFFFu) | 0xFF800000u : (s.w[i >> 1] & 0xFFFF0000u) | 0x0000FF80u;
+        else
+          s.w[i] = 0xFF800000u;
+      }
+  }
+  return s;
+}
+
+// streams slots s0 .. s1 - 1 of a row
+template <int DT, int T, int U, bool ENT, bool TOP>
+__device__ __forceinline__ Sums sum_segment(Shared<T>& sh, const RowRef<DT>& z, int s0, int s1, float c, int N) {
   const int tid = threadIdx.x;
   float m1 = kNegInf, m2 = kNegInf, m3 = kNegInf, Mf = -kHuge;
   int u1 = 0, u2 = 0, u = 0;
   double s = 0.0, h = 0.0;
   bool any_odd = false;
 #pragma unroll 1
-  for (int b = s0; b < s1; b += T * kU, ++u) {
-    Slot x[kU];
+  for (int b = s0; b < s1; b += T * U, ++u) {
+    Slot x[U];
+    if (b + T * U <= s1 && (b + T * U) * RowType<DT>::VE <= z.V) {
 #pragma unroll
-    for (int l = 0; l < kU; ++l) {
-      const int slot = b + l * T + tid;
-      x[l] = z.template load<true>(slot < s1 ? slot : z.slots());
+      for (int l = 0; l < U; ++l) {
+        const u32x4_any v =
+            __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(z.p + (b + l * T + tid) * RowType<DT>::VE));
+        x[l] = Slot{{v.x, v.y, v.z, v.w}};
+      }
+    } else if (T > kWave || z.V >= RowType<DT>::VE) {
+#pragma unroll
+      for (int l = 0; l < U; ++l) x[l] = load_unordered<DT>(z, b + l * T + tid, s1);
+    } else {
+      x[0] = z.load(tid);
+#pragma unroll
+      for (int l = 1; l < U; ++l) x[l] = Slot{{RowType<DT>::kMasked, RowType<DT>::kMasked, RowType<DT>::kMasked, RowType<DT>::kMasked}};
     }
     bool odd;
-    const float m = largest<DT>(x, odd);
+    float low;
+    const float m = largest<DT>(x, odd, low);
     any_odd |= odd;
     if (TOP) {
       const bool a1 = m > m1, a2 = m > m2;
@@ -231,32 +361,10 @@ __device__ __forceinline__ Sums sum_segment(Shared<T>& sh, const RowRef<DT>& z, 
       rebase((double)Mf, (double)to, s, h);
       Mf = to;
     }
-    float ps[kU], ph[kU];
-#pragma unroll
-    for (int l = 0; l < kU; ++l) {
-      ps[l] = ph[l] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float t = fmaf(slot_value<DT>(x[l], i), c, -Mf);
-        const float e = __builtin_amdgcn_exp2f(t);
-        ps[l] += e;
-        if (ENT) ph[l] = fmaf(e, t, ph[l]);
-      }
-    }
-    float us = (ps[0] + ps[1]) + (ps[2] + ps[3]), uh = (ph[0] + ph[1]) + (ph[2] + ph[3]);
-    if (ENT && uh != uh) {  // a masked token: 0 times -inf
-      uh = 0.0f;
-#pragma unroll
-      for (int l = 0; l < kU; ++l)
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          const float t = fmaf(slot_value<DT>(x[l], i), c, -Mf);
-          const float e = __builtin_amdgcn_exp2f(t);
-          uh = fmaf(e, fmaxf(t, -256.0f), uh);
-        }
-    }
-    s += (double)us;
-    if (ENT) h += (double)uh;
+    if (ENT && __any(!(fmaf(low, c, -Mf) > -3e38f)))  // masked, or so low that t leaves fp32
+      add_terms<DT, ENT, true>(x, c, Mf, s, h);
+    else
+      add_terms<DT, ENT, false>(x, c, Mf, s, h);
   }
   // over the block: the largest logit, then sums at its reference
   float bm = wave_max_dpp_f32(any_odd ? INFINITY : m1);
@@ -286,7 +394,7 @@ __device__ __forceinline__ Sums sum_segment(Shared<T>& sh, const RowRef<DT>& z, 
       for (int w = 0; w < T / kWave; ++w) r.s += sh.wave_s[w], r.h += sh.wave_h[w];
     }
   }
-  if (TOP) top_of_segment<DT, T>(sh, z, s0, s1, N, m1, m2, m3, u1, u2);
+  if (TOP) top_of_segment<DT, T, U>(sh, z, s0, s1, N, m1, m2, m3, u1, u2);
   return r;
 }
 
@@ -356,8 +464,8 @@ __device__ __forceinline__ void write_row(Shared<T>& sh, const LogprobsArgs& a, 
 }
 
 // One row, or one segment of it, a block: streams it once.
-template <int DT, int T, bool ENT, bool TOP>
-__global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, LogprobsOut o, int n_seg, int seg_slots,
+template <int DT, int T, int U, bool ENT, bool TOP>
+__global__ __launch_bounds__(T, 8) void logprobs_kernel(LogprobsArgs a, LogprobsOut o, int n_seg, int seg_slots,
                                                      LogprobsPart* __restrict__ parts, uint64_t* __restrict__ lists) {
   __shared__ Shared<T> sh;
   const int seg = blockIdx.x % n_seg;
@@ -365,7 +473,7 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, LogprobsOut
   const RowRef<DT> z(a.Z, row, a.stride, a.V);
   const double c = row_scale(a.T, a.group, row);
   const int s0 = seg * seg_slots, s1 = min(s0 + seg_slots, z.slots());
-  const Sums r = sum_segment<DT, T, ENT, TOP>(sh, z, s0, s1, (float)c, a.N);
+  const Sums r = sum_segment<DT, T, U, ENT, TOP>(sh, z, s0, s1, (float)c, a.N);
   if (n_seg == 1) {
     write_row<DT, T>(sh, a, o, row, r, c);
   } else {
@@ -407,41 +515,27 @@ __global__ __launch_bounds__(T) void logprobs_join_kernel(LogprobsArgs a, Logpro
     for (int w = 0; w < T / kWave; ++w) r.s += sh.wave_s[w], r.h += sh.wave_h[w];
   }
   if (a.N > 0 && r.m > kNegInf) {
-    // the N-th largest of the segments' best bounds the row's N-th from below;
-    // lists are in order, and at most N of them reach it with at most N tokens each
+    // the N-th largest of the segments' best bounds the row's N-th from below: only
+    // the lists of those N segments can hold one, what of them reaches it is ranked
     const uint64_t* list = lists + row * n_seg * a.N;
     sh.key[tid] = tid < n_seg ? list[(int64_t)tid * a.N] : 0;
-    if (tid == 0) sh.least = 1, sh.n_key = 0;
+    if (tid == 0) sh.least = 1, sh.n_key = 0, sh.n_piece = 0;
     __syncthreads();
     const uint64_t mine = sh.key[tid];
     int rank = 0;
+#pragma unroll 4
     for (int j = 0; j < n_seg; ++j) rank += sh.key[j] > mine;
-    if (mine && rank == a.N - 1) sh.least = mine;
+    if (mine && rank < a.N) {
+      sh.piece[rank] = (uint32_t)tid;
+      atomicMax(&sh.n_piece, (uint32_t)rank + 1);
+      if (rank == a.N - 1) sh.least = mine;
+    }
     __syncthreads();
     const uint64_t least = sh.least;
-    // N rounds: the k-th of every list still at or above the bound, ranked with
-    // the N best so far
-    if (tid < DFLASH_TOP_MAX) sh.top[tid] = 0;
-    int k = 0;
-    uint64_t next = tid < n_seg ? mine : 0;
-    for (; k < a.N; ++k) {
-      const bool in = next >= least && next;
-      if (!__syncthreads_or(in)) break;
-      if (in) {
-        const uint32_t at = atomicAdd(&sh.n_key, 1u);
-        if (at < (uint32_t)kCap) sh.key[at] = next;
-        next = k + 1 < a.N ? list[(int64_t)tid * a.N + k + 1] : 0;
-      } else {
-        next = 0;
-      }
-      __syncthreads();
-      if (sh.n_key > (uint32_t)(kCap - T)) {
-        const int n = (int)sh.n_key;
-        rank_keys(sh, n, a.N);
-        if (tid < a.N) sh.key[tid] = sh.top[tid];
-        if (tid == 0) sh.n_key = (uint32_t)min(n, a.N);
-        __syncthreads();
-      }
+    const int n = (int)sh.n_piece * a.N;
+    for (int i = tid; i < n; i += T) {
+      const uint64_t k = list[(int64_t)sh.piece[i / a.N] * a.N + i % a.N];
+      if (k >= least) sh.key[atomicAdd(&sh.n_key, 1u)] = k;
     }
     __syncthreads();
     rank_keys(sh, (int)sh.n_key, a.N);
@@ -556,26 +650,28 @@ __global__ __launch_bounds__(kLogprobsThreads) void logprobs_grad_kernel(Logprob
   }
 }
 
-template <int DT, int T, bool ENT, bool TOP>
+template <int DT, int T, int U, bool ENT, bool TOP>
 hipError_t run(const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl, hipStream_t st) {
   LogprobsPart* parts = reinterpret_cast<LogprobsPart*>(ws);
   uint64_t* lists = reinterpret_cast<uint64_t*>(ws + pl.lists);
-  launch(logprobs_kernel<DT, T, ENT, TOP>, dim3((unsigned)(a.R * pl.n_seg)), dim3(T), st, a, o, pl.n_seg, pl.seg_slots, parts, lists);
+  launch(logprobs_kernel<DT, T, U, ENT, TOP>, dim3((unsigned)(a.R * pl.n_seg)), dim3(T), st, a, o, pl.n_seg, pl.seg_slots, parts,
+         lists);
   if (pl.n_seg > 1)
     launch(logprobs_join_kernel<DT, kLogprobsThreads>, dim3((unsigned)a.R), dim3(kLogprobsThreads), st, a, o, pl.n_seg,
            (const LogprobsPart*)parts, (const uint64_t*)lists);
   return hipGetLastError();
 }
 
-template <int DT, int T>
-hipError_t run_threads(const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl, hipStream_t st) {
-  if (a.N > 0) return o.entropy ? run<DT, T, true, true>(a, o, ws, pl, st) : run<DT, T, false, true>(a, o, ws, pl, st);
-  return o.entropy ? run<DT, T, true, false>(a, o, ws, pl, st) : run<DT, T, false, false>(a, o, ws, pl, st);
+template <int DT, int T, int U>
+hipError_t run_sized(const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl, hipStream_t st) {
+  if (a.N > 0) return o.entropy ? run<DT, T, U, true, true>(a, o, ws, pl, st) : run<DT, T, U, false, true>(a, o, ws, pl, st);
+  return o.entropy ? run<DT, T, U, true, false>(a, o, ws, pl, st) : run<DT, T, U, false, false>(a, o, ws, pl, st);
 }
 
 template <int DT>
 hipError_t run_typed(const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl, hipStream_t st) {
-  return pl.threads == kWave ? run_threads<DT, kWave>(a, o, ws, pl, st) : run_threads<DT, kLogprobsThreads>(a, o, ws, pl, st);
+  if (pl.threads == kWave) return run_sized<DT, kWave, 4>(a, o, ws, pl, st);
+  return pl.unit == 1 ? run_sized<DT, kLogprobsThreads, 1>(a, o, ws, pl, st) : run_sized<DT, kLogprobsThreads, 4>(a, o, ws, pl, st);
 }
 
 template <int DT>

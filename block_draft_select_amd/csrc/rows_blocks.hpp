@@ -117,48 +117,6 @@ __device__ __forceinline__ float row_value(const RowRef<DT>& z, int i) {
     return __uint_as_float(z.p[i]);
 }
 
-// a thread's largest logit; whether one is NaN or +inf
-template <int DT, int N>
-__device__ __forceinline__ float largest(const Slot (&x)[N], bool& odd) {
-  float m = kNegInf;
-  odd = false;
-  if constexpr (DT == DFLASH_BF16) {
-    // signed and unsigned maxima of the raw patterns, two a word: the signed one
-    // is the largest logit unless all are negative (then the unsigned minimum
-    // is), and a NaN of either sign stands over its infinity
-    uint32_t hi = 0x80008000u, up = 0;
-#pragma unroll
-    for (int l = 0; l < N; ++l)
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        hi = smax_i16x2(hi, x[l].w[d]);
-        up = max_u16x2(up, x[l].w[d]);
-      }
-    const int h = max((int)(int16_t)(hi & 0xFFFFu), (int)(int16_t)(hi >> 16));
-    odd = h >= 0x7F80 || max(up & 0xFFFFu, up >> 16) > 0xFF80u;
-    uint32_t best = (uint32_t)h;
-    if (h < 0) {
-      uint32_t lo = 0xFFFFFFFFu;
-#pragma unroll
-      for (int l = 0; l < N; ++l)
-#pragma unroll
-        for (int d = 0; d < 4; ++d) lo = min_u16x2(lo, x[l].w[d]);
-      best = min(lo & 0xFFFFu, lo >> 16);
-    }
-    m = __uint_as_float(best << 16);
-  } else {
-#pragma unroll
-    for (int l = 0; l < N; ++l)
-#pragma unroll
-      for (int i = 0; i < RowType<DT>::VE; ++i) {
-        const float v = slot_value<DT>(x[l], i);
-        m = fmaxf(m, v);
-        odd |= !(v < INFINITY);
-      }
-  }
-  return m;
-}
-
 // fp32 -> bf16, nearest even (NaN stays NaN)
 __device__ __forceinline__ uint32_t bf16_round(float x) {
   const uint32_t u = __float_as_uint(x);
