@@ -324,12 +324,15 @@ LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
     return p;
   }
   p.threads = kLogprobsThreads;
-  const int64_t want = (kLogprobsBlocks + std::max<int64_t>(r.R, 1) - 1) / std::max<int64_t>(r.R, 1);
+  const int64_t want = std::max<int64_t>(kLogprobsBlocks / std::max<int64_t>(r.R, 1), 1);
   p.n_seg = (int)std::min<int64_t>(std::min<int64_t>(want, units), kLogprobsMaxSeg);
-  const int per = (units + p.n_seg - 1) / p.n_seg;  // slots a thread
+  int per = (units + p.n_seg - 1) / p.n_seg;  // slots a thread
+  if (per < 4)
+    p.unit = 1;
+  else
+    per = (per + 3) / 4 * 4;
   p.n_seg = (units + per - 1) / per;
   p.seg_slots = per * kLogprobsThreads;
-  if (per < 4) p.unit = 1;
   if (p.n_seg > 1) {
     p.lists = align256((size_t)r.R * p.n_seg * sizeof(LogprobsPart));
     p.total = p.lists + align256((size_t)r.R * p.n_seg * N * sizeof(uint64_t));
@@ -337,12 +340,11 @@ LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
   return p;
 }
 
-// a bound over all plans of at most R rows: several segments are taken only while they number under 2048 + R < 4096
+// a bound over all plans of at most R rows: several segments are taken only while they number at most 2048
 static size_t logprobs_workspace(const dflash_rows& r) {
   const int64_t most = std::min(logprobs_units(r), kLogprobsMaxSeg);
   if (most <= 1) return 0;
-  const int64_t few = std::min<int64_t>(r.R, kLogprobsBlocks - 1);
-  const size_t segs = (size_t)std::min(few * most, kLogprobsBlocks + few);
+  const size_t segs = (size_t)std::min<int64_t>(r.R * most, kLogprobsBlocks);
   return align256(segs * sizeof(LogprobsPart)) + align256(segs * DFLASH_TOP_MAX * sizeof(uint64_t));
 }
 

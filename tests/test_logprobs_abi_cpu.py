@@ -75,7 +75,7 @@ def test_a_workspace_serves_fewer_rows_too(dfl, dtype, V):
         last = n
         for N in (0, 1, 32):
             # the most rows and the longest need none: one launch
-            if R < 2048 and V > 8192:
+            if R <= 1024 and V > 8192:
                 assert _fwd(dfl, r, N=N, n=0) == 3
                 assert int(dfl.lib.dflash_last_error().split(b"need ")[1].split()[0]) <= n, (R, V)
 
