@@ -6,6 +6,8 @@
 // channels of one token.  Lane l of either operand holds the 16 bytes
 // 16 (l / 16) .. of row l % 16 and of 64 bytes of k.  Only the tokens' side is
 // cleared past the row's end: what the weights hold there is multiplied by zero.
+#include <type_traits>
+
 #include "rows_blocks.hpp"
 
 namespace dfk {
@@ -13,6 +15,29 @@ namespace dfk {
 namespace {
 
 typedef int v4i32 __attribute__((ext_vector_type(4)));
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// 16 values to a row of any element-aligned address, each rounded to the type
+template <int DT>
+__device__ __forceinline__ void store16(void* y, int64_t at, const float (&v)[16]) {
+  using E = typename RowType<DT>::elem;
+  constexpr int VE = RowType<DT>::VE;
+  E* p = static_cast<E*>(y) + at;
+#pragma unroll
+  for (int q = 0; q < 16 / VE; ++q) {
+    u32x4_any o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      if constexpr (DT == DFLASH_BF16)
+        o[d] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[q * 8 + 2 * d], v[q * 8 + 2 * d + 1]}), bf16x2));
+      else
+        o[d] = __float_as_uint(v[q * 4 + d]);
+    }
+    *reinterpret_cast<u32x4_any*>(p + q * VE) = o;
+  }
+}
 
 // Few tokens: 16 channels and 16 MT tokens a block, its four waves split k.
 // Each wave has eight steps of 64 bytes in flight.
@@ -100,11 +125,10 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // An array of 8-bit rows from `row` on as a buffer: loads behind its end give 0,
-// so neither rows nor pieces of k need a clamp (`last`: rows from there on; strides stay
-// below 2^24, and a block uses 256 rows at most)
+// so neither rows nor pieces of k need a clamp (strides are at most 2^22, and a
+// block reaches over 256 rows)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const int8_t* p, int64_t row, int64_t rows, int64_t stride, int H) {
-  const int64_t last = min(rows - 1 - row, (int64_t)511);
-  const int64_t bytes = min(last * stride, (int64_t)0x7FFF0000) + (H + 15) / 16 * 16;
+  const int64_t bytes = min(rows - 1 - row, (int64_t)255) * stride + (H + 15) / 16 * 16;
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p) + row * stride, 0, (int)bytes, 0x00027000);
 }
 
@@ -115,142 +139,167 @@ __device__ __forceinline__ void load_to_lds16(__amdgpu_buffer_rsrc_t b, int lane
 #endif
 }
 
-__device__ __forceinline__ v4i32 load16(__amdgpu_buffer_rsrc_t b, int lane_offset, int offset) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  return __builtin_bit_cast(v4i32, __builtin_amdgcn_raw_buffer_load_b128(b, lane_offset, offset, 0));
-#else
-  return v4i32{};
-#endif
+// vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N <= 63, "the field");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
 }
 
-// Many tokens: a block of four waves owns 256 channels and 16 TT tokens, each wave
-// 64 channels of all its tokens.  The weights go from global memory straight
-// into the wave's registers (no other wave of the block needs them), two
-// stages of 128 bytes of k ahead; the tokens' rows go straight into a ring of
-// three LDS stages that the waves share.  So LDS moves one KB a wave for every four matrix
-// instructions, half of what it can.
-// A stage in LDS: 128-byte rows, the 16-byte piece c of row r at place c ^ (r % 8), so that
-// the eight rows that are read at once lie in different banks.
-// The rows of the A operand are dealt out so that a lane ends up with 16
-// neighbouring channels: row i of tile c is channel 16 (i / 4) + 4 c + i % 4.
+// Many tokens: a block of eight waves owns 256 channels and 32 TT tokens, a wave 64
+// channels and 16 TT tokens.  Stages of 64 bytes of k go from global memory straight
+// into a ring of NB in LDS, four lanes to a row's 64 bytes.  (Loading the weights
+// straight into the operand's registers puts neighbouring lanes in
+// different rows: 38 bytes a nanosecond and CU against 100 this way, and 1490 us
+// against 1235 at 1152 x 4096 x 262144.)
+// A stage in LDS: rows of 64 bytes, piece c of row r at place c ^ (r / 2 % 4), so that
+// the eight rows that are read at once lie in different banks.  The channels' rows are
+// dealt out so that a lane ends up with 16 neighbouring channels: row i of tile c
+// is channel 16 (i / 4) + 4 c + i % 4.
+// All waves of a CU meet at the one barrier a stage has, so nothing may wait behind
+// it: the operands that a stage begins with are read in the stage before, which is
+// why a stage has landed one barrier before its turn.
 constexpr int kTileCh = 256;
 
+template <int TT>
+struct LinearTile {
+  static constexpr int BM = 32 * TT, ROWS = kTileCh + BM, SBYTES = ROWS * 64;
+  static constexpr int NB = 163840 / SBYTES > 6 ? 6 : 163840 / SBYTES;
+  static constexpr int XI = 2 * TT;  // loads of a stage's token rows, 16 rows each
+  static constexpr int LO = 2 + XI / 8, HI = 2 + (XI + 7) / 8;  // a wave's loads a stage: HI for the first XI % 8 waves
+  static_assert(NB >= 4, "a stage in use, one landed, one refilling, one in flight");
+};
+
 template <int DT, int TT>
-__global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a, int n_rt, int n_ct) {
-  constexpr int BM = 16 * TT, NB = 3;
-  constexpr int XL = TT / 2;           // loads of a stage's token rows a wave: 8 rows each
-  constexpr int PER_STAGE = XL + 8;    // and of weights
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[NB * BM * 128];
+__global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n_rt, int n_ct) {
+  using L = LinearTile<TT>;
+  constexpr int NB = L::NB, SB = L::SBYTES, G = TT / 2;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[NB * SB];
   // ids with the same value mod 8 run on one XCD: the row tiles of a channel tile follow one another there
   const int grp = blockIdx.x / (8 * n_rt), rem = blockIdx.x - grp * 8 * n_rt;
   const int rt = rem >> 3, ct = grp * 8 + (rem & 7);
   if (ct >= n_ct) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  // the last waves step back to whole tiles: some channels are computed twice, alike (N >= 64)
-  const int ch0 = min(ct * kTileCh + wave * 64, a.N - 64);
-  const int64_t row0 = (int64_t)rt * BM;
-  const int n_st = (a.H + 127) / 128;
+  const int wc = wave & 3, wm = wave >> 2;
+  // the last tiles step back to whole ones: some channels are computed twice, alike (N >= 64)
+  const int chb = min(ct * kTileCh, a.N - 64);
+  const int64_t row0 = (int64_t)rt * L::BM;
+  const int n_st = (a.H + 63) / 64;
 
   const int i16 = lane & 15, g4 = lane >> 4;
   const int w_stride = (int)a.wq_stride, x_stride = (int)a.xq_stride;
-  const __amdgpu_buffer_rsrc_t wb = rows_buffer(a.wq, ch0, a.N, a.wq_stride, a.H);
+  const __amdgpu_buffer_rsrc_t wb = rows_buffer(a.wq, chb, a.N, a.wq_stride, a.H);
   const __amdgpu_buffer_rsrc_t xb = rows_buffer(a.xq, row0, a.R, a.xq_stride, a.H);
-  const int wo = ((i16 >> 2) * 16 + (i16 & 3)) * w_stride + g4 * 16;
-  const int xo = (lane >> 3) * x_stride + ((lane & 7) ^ (lane >> 3)) * 16;  // place l % 8 of a row holds this piece
-  auto load_x = [&](int s) {
-    unsigned char* to = lds + (s % NB) * (BM * 128) + wave * XL * 1024;
-#pragma unroll
-    for (int i = 0; i < XL; ++i) load_to_lds16(xb, xo, 8 * (wave * XL + i) * x_stride + s * 128, to + i * 1024);
+  const int piece = ((lane & 3) ^ (lane >> 3 & 3)) * 16;  // place l % 4 of row l / 4 holds this piece
+  const int wo = ((lane >> 4) * 16 + (lane >> 2 & 3)) * w_stride + piece;
+  const int xo = (lane >> 2) * x_stride + piece;
+  // the wave's i-th load of stage s
+  auto load = [&](int s, int buf, int i) __attribute__((always_inline)) {
+    unsigned char* to = lds + buf * SB;
+    if (i < 2) {
+      const int j = wave * 2 + i;  // 16 rows: tile j % 4 of wave j / 4's channels
+      const int ch = min(ct * kTileCh + (j >> 2) * 64, a.N - 64) - chb;
+      load_to_lds16(wb, wo, (ch + 4 * (j & 3)) * w_stride + s * 64, to + j * 1024);
+    } else {
+      const int j = wave + 8 * (i - 2);
+      if (j < L::XI) load_to_lds16(xb, xo, 16 * j * x_stride + s * 64, to + (16 + j) * 1024);
+    }
   };
-  v4i32 wv[2][2][4];  // [stage parity][64-byte step][tile]
-  auto load_w = [&](int s, int ks, v4i32(&to)[4]) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) to[t] = load16(wb, wo, 4 * t * w_stride + s * 128 + ks * 64);
+  // until this wave's loads of all but the last n stages are done
+  auto wait = [&](auto n) __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    if (L::LO == L::HI || wave < L::XI % 8)
+      wait_loads<L::HI * decltype(n)::value>();
+    else
+      wait_loads<L::LO * decltype(n)::value>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // the tokens' bytes behind the rows' end, in a stage that holds such
+  auto clear = [&](int s, int buf) __attribute__((always_inline)) {
+    if (s * 64 + 64 > a.H) {
+      const int valid = a.H - s * 64;
+      uint32_t* p = reinterpret_cast<uint32_t*>(lds + buf * SB + kTileCh * 64);
+#pragma unroll 1
+      for (int q = tid; q < L::BM * 16; q += 512) {  // words
+        const int n = valid - (((q >> 2) & 3) ^ ((q >> 5) & 3)) * 16 - (q & 3) * 4;
+        if (n < 4) p[q] = n <= 0 ? 0u : p[q] & ((1u << (8 * n)) - 1u);
+      }
+      lds_barrier();
+    }
   };
 
-  v4i32 acc[TT][4];
+  const int fo = i16 * 64 + ((g4 ^ (i16 >> 1 & 3)) * 16);
+  const unsigned char* wf = lds + wc * 4096 + fo;
+  const unsigned char* xf = lds + kTileCh * 64 + wm * (TT * 1024) + fo;
+  v4i32 acc[TT][4], wv[2][4], xv[2][2];
 #pragma unroll
   for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[t][c] = (v4i32){0, 0, 0, 0};
-  int fo[2];
-#pragma unroll
-  for (int ks = 0; ks < 2; ++ks) fo[ks] = i16 * 128 + ((4 * ks + g4) ^ (lane & 7)) * 16;
 
-  auto stage = [&](int s, v4i32(&ws)[2][4]) {
-    // this wave's loads of stage s are done when only those of s + 1 remain
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070 | (PER_STAGE & 15) | ((PER_STAGE >> 4) << 14));  // vmcnt(PER_STAGE) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    unsigned char* st = lds + (s % NB) * (BM * 128);
-    if (s * 128 + 128 > a.H) {  // the rows end in this stage, or before it: clear the tokens' bytes behind the end
-      const int valid = a.H - s * 128;
-#pragma unroll 1
-      for (int q = tid; q < BM * 32; q += 256) {  // words
-        const int n = valid - (((q >> 2) & 7) ^ ((q >> 5) & 7)) * 16 - (q & 3) * 4;
-        uint32_t* p = reinterpret_cast<uint32_t*>(st) + q;
-        if (n < 4) *p = n <= 0 ? 0u : *p & ((1u << (8 * n)) - 1u);
-      }
-      lds_barrier();
-    }
-    load_x(s + 2);  // into the buffer that stage s - 1 used
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+  for (int s = 0; s < NB - 1; ++s) {
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const v4i32 xv = *reinterpret_cast<const v4i32*>(st + t * 2048 + fo[ks]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[t][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ws[ks][c], xv, acc[t][c], 0, 0, 0);
-      }
-      // left to itself the scheduler loads the next weights before these are used, into registers that it then spills
-      __builtin_amdgcn_sched_barrier(0);
-      load_w(s + 2, ks, ws[ks]);
-    }
-  };
-
-  // in the order that the waits count
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    load_x(s);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) load_w(s, ks, wv[s][ks]);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < L::HI; ++i) load(s, s, i);
   }
+  wait(std::integral_constant<int, NB - 2>{});
+  clear(0, 0);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) wv[0][c] = *reinterpret_cast<const v4i32*>(wf + c * 1024);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) xv[0][t] = *reinterpret_cast<const v4i32*>(xf + t * 1024);
+
+  int buf = 0;  // of stage s
+  auto stage = [&](int s, auto parity) __attribute__((always_inline)) {
+    constexpr int P = decltype(parity)::value;
+    const int next = buf + 1 == NB ? 0 : buf + 1, refill = buf == 0 ? NB - 1 : buf - 1;
+    // stage s + 1 has landed, and no wave reads stage s - 1 any more
+    wait(std::integral_constant<int, NB - 3>{});
+    clear(s + 1, next);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      constexpr int kX0 = P * G;  // pairs of token tiles so far, mod 2
+      const int cur = (kX0 + g) & 1;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        xv[cur ^ 1][t] = *reinterpret_cast<const v4i32*>(g + 1 < G ? xf + buf * SB + (2 * g + 2 + t) * 1024 : xf + next * SB + t * 1024);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c * G / 4 == g) wv[P ^ 1][c] = *reinterpret_cast<const v4i32*>(wf + next * SB + c * 1024);
+#pragma unroll
+      for (int i = 0; i < L::HI; ++i)
+        if (i * G / L::HI == g) load(s + NB - 1, refill, i);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc[2 * g + t][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[P][c], xv[cur][t], acc[2 * g + t][c], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    buf = next;
+  };
   // an odd last stage takes one behind the end with it, whose tokens are cleared
   for (int s = 0; s < n_st; s += 2) {
-    stage(s, wv[0]);
-    stage(s + 1, wv[1]);
+    stage(s, std::integral_constant<int, 0>{});
+    stage(s + 1, std::integral_constant<int, 1>{});
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no transfer outlives the loop
 
-  using E = typename RowType<DT>::elem;
-  const int ch = ch0 + g4 * 16;
+  const int ch = min(ct * kTileCh + wc * 64, a.N - 64) + g4 * 16;
   float sc[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) sc[j] = a.ws[ch + j];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    const int64_t row = row0 + t * 16 + i16;
-    if (row >= a.R) continue;
-    const float xs = a.xs[row];
-    E* y = static_cast<E*>(a.y) + row * a.y_stride + ch;
-    E v[16];
+    const int64_t row = row0 + (wm * TT + t) * 16 + i16;
+    if (row < a.R) {
+      const float xs = a.xs[row];
+      float v[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = to_elem<DT>((float)acc[t][j >> 2][j & 3] * xs * sc[j]);
-    constexpr int VE = RowType<DT>::VE;
-#pragma unroll
-    for (int q = 0; q < 16 / VE; ++q) {
-      u32x4_any o;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        if constexpr (DT == DFLASH_BF16)
-          o[d] = (uint32_t)v[q * 8 + 2 * d] | (uint32_t)v[q * 8 + 2 * d + 1] << 16;
-        else
-          o[d] = v[q * 4 + d];
-      }
-      *reinterpret_cast<u32x4_any*>(y + q * VE) = o;
+      for (int j = 0; j < 16; ++j) v[j] = (float)acc[t][j >> 2][j & 3] * xs * sc[j];
+      store16<DT>(a.y, row * a.y_stride + ch, v);
     }
   }
 }
@@ -258,14 +307,14 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a, int n
 template <int DT, int TT>
 hipError_t run_tile(const LinearArgs& a, hipStream_t st) {
   const int n_ct = (a.N + kTileCh - 1) / kTileCh;
-  const int n_rt = (int)((a.R + 16 * TT - 1) / (16 * TT));
-  launch(linear_tile_kernel<DT, TT>, dim3((unsigned)((int64_t)((n_ct + 7) / 8) * 8 * n_rt)), dim3(256), st, a, n_rt, n_ct);
+  const int n_rt = (int)((a.R + 32 * TT - 1) / (32 * TT));
+  launch(linear_tile_kernel<DT, TT>, dim3((unsigned)((int64_t)((n_ct + 7) / 8) * 8 * n_rt)), dim3(512), st, a, n_rt, n_ct);
   return hipGetLastError();
 }
 
 struct LinearPlan {
   int few;   // 16-token tiles of the few-tokens kernel, or 0
-  int tile;  // of the tile kernel
+  int tile;  // TT of the tile kernel
   int64_t blocks;
 };
 
@@ -275,8 +324,10 @@ LinearPlan linear_plan(int64_t R, int32_t N) {
     p.few = R <= 16 ? 1 : 2;
     p.blocks = (int64_t)((N + 15) / 16) * ((R + 16 * p.few - 1) / (16 * p.few));
   } else {
-    p.tile = R <= 64 ? 4 : 8;
-    p.blocks = (int64_t)((N + kTileCh * 8 - 1) / (kTileCh * 8)) * 8 * ((R + 16 * p.tile - 1) / (16 * p.tile));
+    // the tile that covers the tokens with the least over; the larger one of two that do
+    p.tile = R <= 64 ? 2 : R <= 128 ? 4 : 8;
+    if (p.tile == 8 && (R + 191) / 192 * 192 < (R + 255) / 256 * 256) p.tile = 6;
+    p.blocks = (int64_t)((N + kTileCh * 8 - 1) / (kTileCh * 8)) * 8 * ((R + 32 * p.tile - 1) / (32 * p.tile));
   }
   return p;
 }
@@ -286,7 +337,12 @@ hipError_t run_typed(const LinearArgs& a, hipStream_t st) {
   const LinearPlan p = linear_plan(a.R, a.N);
   if (p.few == 1) return run_few<DT, 1>(a, st);
   if (p.few == 2) return run_few<DT, 2>(a, st);
-  return p.tile == 4 ? run_tile<DT, 4>(a, st) : run_tile<DT, 8>(a, st);
+  switch (p.tile) {
+    case 2: return run_tile<DT, 2>(a, st);
+    case 4: return run_tile<DT, 4>(a, st);
+    case 6: return run_tile<DT, 6>(a, st);
+    default: return run_tile<DT, 8>(a, st);
+  }
 }
 
 }  // namespace

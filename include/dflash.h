@@ -91,7 +91,7 @@ extern "C" {
 #define DFLASH_LOGPROBS_M_MAX 1024 /* given tokens per row */
 #define DFLASH_TOP_MAX 32    /* alternatives per row */
 #define DFLASH_H_MAX 65536   /* products per sum of dflash_linear_i8 */
-#define DFLASH_I8_STRIDE_MAX 16777216 /* bytes between 8-bit rows */
+#define DFLASH_I8_STRIDE_MAX 4194304 /* bytes between 8-bit rows */
 #define DFLASH_STATIC_SCRATCH_BYTES (8u << 20) /* the library's own scratch per GPU (dflash_cycle_static) */
 
 typedef int32_t dflash_status;

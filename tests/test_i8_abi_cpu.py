@@ -50,7 +50,7 @@ def test_bad_quant_calls(dfl):
     (dict(null=True), 1), (dict(R=-1), 1), (dict(N=0), 1), (dict(H=0), 1), (dict(dtype=2), 1), (dict(R=4194305), 2),
     (dict(N=2097153, y_stride=2097153), 2), (dict(H=65537, xq_stride=65552, wq_stride=65552), 2), (dict(xq_stride=96), 1),
     (dict(xq_stride=104), 1), (dict(wq_stride=96), 1), (dict(wq_stride=120), 1), (dict(xq_stride=-112), 1), (dict(y_stride=49), 1),
-    (dict(y_stride=(1 << 40) + 1), 2), (dict(xq_stride=1 << 41), 2), (dict(wq_stride=1 << 41), 2), (dict(xq=None), 1), (dict(xs=None), 1),
+    (dict(y_stride=(1 << 40) + 1), 2), (dict(xq_stride=(1 << 22) + 16), 2), (dict(wq_stride=1 << 41), 2), (dict(xq=None), 1), (dict(xs=None), 1),
     (dict(wq=None), 1), (dict(ws=None), 1), (dict(Y=None), 1), (dict(xq=OFF8), 1), (dict(wq=OFF8), 1), (dict(Y=ODD), 1),
     (dict(R=4194304, N=2097152, y_stride=2097152), 2),
 ])
