@@ -19,14 +19,14 @@ typedef int v4i32 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// 16 values to a row of any element-aligned address, each rounded to the type
-template <int DT>
-__device__ __forceinline__ void store16(void* y, int64_t at, const float (&v)[16]) {
+// NV values to a row of any element-aligned address, each rounded to the type
+template <int DT, int NV>
+__device__ __forceinline__ void store_values(void* y, int64_t at, const float (&v)[NV]) {
   using E = typename RowType<DT>::elem;
   constexpr int VE = RowType<DT>::VE;
   E* p = static_cast<E*>(y) + at;
 #pragma unroll
-  for (int q = 0; q < 16 / VE; ++q) {
+  for (int q = 0; q < NV / VE; ++q) {
     u32x4_any o;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
@@ -37,6 +37,49 @@ __device__ __forceinline__ void store16(void* y, int64_t at, const float (&v)[16
     }
     *reinterpret_cast<u32x4_any*>(p + q * VE) = o;
   }
+}
+
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+
+// four of them
+template <int DT>
+__device__ __forceinline__ void store4(typename RowType<DT>::elem* p, const float (&v)[4]) {
+  if constexpr (DT == DFLASH_BF16)
+    *reinterpret_cast<u32x2_any*>(p) = u32x2_any{__builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[0], v[1]}), bf16x2)),
+                                                 __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[2], v[3]}), bf16x2))};
+  else
+    *reinterpret_cast<u32x4_any*>(p) = u32x4_any{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+}
+
+// Workgroup barrier for LDS hand-offs only: __syncthreads() would also wait for
+// every global load in flight
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // vmcnt 63 (no wait), expcnt 7, lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// An array of 8-bit rows from `row` on as a buffer: loads behind its end give 0,
+// so neither rows nor pieces of k need a clamp (strides are at most 2^22, and a
+// block reaches over 256 rows)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const int8_t* p, int64_t row, int64_t rows, int64_t stride, int H) {
+  const int64_t bytes = min(rows - 1 - row, (int64_t)255) * stride + (H + 15) / 16 * 16;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p) + row * stride, 0, (int)bytes, 0x00027000);
+}
+
+// 16 bytes a lane from a buffer straight into LDS, at 16 l past the wave's address
+__device__ __forceinline__ void load_to_lds16(__amdgpu_buffer_rsrc_t b, int lane_offset, int offset, unsigned char* l) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, l, 16, lane_offset, offset, 0, 0);
+#endif
+}
+
+// vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N <= 63, "the field");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
 }
 
 // Few tokens: 16 channels and 16 MT tokens a block, its four waves split k.
@@ -115,35 +158,124 @@ hipError_t run_few(const LinearArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Workgroup barrier for LDS hand-offs only: __syncthreads() would also wait for
-// every global load in flight
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // vmcnt 63 (no wait), expcnt 7, lgkmcnt 0
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
+// Few tokens and many channels: the tokens' rows stay in LDS, and each of a CU's eight
+// waves streams the weights of 16 channels at a time through a ring of its own
+// there, 128 bytes of k a step; no wave waits for another.  Rows of 128 bytes (of
+// the ring) and of whole 128 bytes (of the tokens) hold piece c of row r at place
+// c ^ (r % 8).  What lies behind a token row's end is zero.
+template <int DT, int MT, int XBYTES>
+__global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
+  constexpr int D = (163840 - XBYTES) / 8 / 2048;  // steps in a wave's ring
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[XBYTES + 8 * D * 2048];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int steps = (a.H + 127) / 128, pitch = steps * 128;
+  const int n_group = (a.N + 15) / 16, stride = (int)gridDim.x * 8;
+  int group = (int)blockIdx.x + (int)gridDim.x * wave;  // neighbouring blocks read neighbouring rows
+  const int total = group < n_group ? ((n_group - 1 - group) / stride + 1) * steps : 0;
 
-// An array of 8-bit rows from `row` on as a buffer: loads behind its end give 0,
-// so neither rows nor pieces of k need a clamp (strides are at most 2^22, and a
-// block reaches over 256 rows)
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const int8_t* p, int64_t row, int64_t rows, int64_t stride, int H) {
-  const int64_t bytes = min(rows - 1 - row, (int64_t)255) * stride + (H + 15) / 16 * 16;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p) + row * stride, 0, (int)bytes, 0x00027000);
-}
+  unsigned char* ring = lds + XBYTES + wave * (D * 2048);
+  const int w_stride = (int)a.wq_stride;
+  const int wo = (lane >> 3) * w_stride + ((lane & 7) ^ (lane >> 3)) * 16;
+  int load_group = group, load_step = 0, load_slot = 0;
+  __amdgpu_buffer_rsrc_t wb = rows_buffer(a.wq, (int64_t)min(group, n_group - 1) * 16, a.N, a.wq_stride, a.H);
+  // the next step; behind the last one, the last group's rows again, which no one reads
+  auto load = [&]() __attribute__((always_inline)) {
+    load_to_lds16(wb, wo, load_step * 128, ring + load_slot * 2048);
+    load_to_lds16(wb, wo, load_step * 128 + 8 * w_stride, ring + load_slot * 2048 + 1024);
+    load_slot = load_slot + 1 == D ? 0 : load_slot + 1;
+    if (++load_step == steps) {
+      load_step = 0;
+      load_group += stride;
+      if (load_group < n_group) wb = rows_buffer(a.wq, (int64_t)load_group * 16, a.N, a.wq_stride, a.H);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) load();
 
-// 16 bytes a lane from a buffer straight into LDS, at 16 l past the wave's address
-__device__ __forceinline__ void load_to_lds16(__amdgpu_buffer_rsrc_t b, int lane_offset, int offset, unsigned char* l) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, l, 16, lane_offset, offset, 0, 0);
-#endif
-}
+  const int chunks = (a.H + 15) / 16, places = steps * 8;
+  for (int q = tid; q < MT * 16 * places; q += 512) {
+    const int r = q / places, c = q - r * places;
+    v4i32 v = {0, 0, 0, 0};
+    if (r < a.R && c < chunks) {
+      v = *reinterpret_cast<const v4i32*>(a.xq + r * a.xq_stride + c * 16);
+      const int valid = a.H - c * 16;
+      if (valid < 16) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int n = valid - 4 * d;
+          v[d] = n <= 0 ? 0 : n >= 4 ? v[d] : (int)((uint32_t)v[d] & ((1u << (8 * n)) - 1u));
+        }
+      }
+    }
+    *reinterpret_cast<v4i32*>(lds + r * pitch + (c ^ (r & 7)) * 16) = v;
+  }
+  __syncthreads();
 
-// vmcnt(N) lgkmcnt(0)
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(N >= 0 && N <= 63, "the field");
-  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+  const int i16 = lane & 15, g4 = lane >> 4;
+  int fo[2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) fo[ks] = ((4 * ks + g4) ^ (i16 & 7)) * 16;
+  v4i32 acc[MT];
+  float xs[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    acc[m] = (v4i32){0, 0, 0, 0};
+    xs[m] = a.xs[min(m * 16 + i16, (int)a.R - 1)];
+  }
+  typedef const float __attribute__((address_space(4))) * Scales;
+  const Scales ws = (Scales)(uintptr_t)a.ws;
+  int step = 0, slot = 0;
+#pragma unroll 1
+  for (int q = 0; q < total; ++q) {
+    asm volatile("" ::: "memory");
+    wait_loads<2 * (D - 2)>();  // this step's are done when only those of the D - 2 after it remain
+    asm volatile("" ::: "memory");
+    v4i32 wv[2], xv[2][MT];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      wv[ks] = *reinterpret_cast<const v4i32*>(ring + slot * 2048 + i16 * 128 + fo[ks]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xv[ks][m] = *reinterpret_cast<const v4i32*>(lds + (m * 16 + i16) * pitch + step * 128 + fo[ks]);
+    }
+    load();  // into the slot that the step before used
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[ks], xv[ks][m], acc[m], 0, 0, 0);
+    slot = slot + 1 == D ? 0 : slot + 1;
+    if (++step < steps) continue;
+    step = 0;
+    const int ch = group * 16 + g4 * 4;
+    // the channels' scales through scalar loads: a vector load's wait would drain the ring
+    float sc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) v[g] = ws[min(group * 16 + g * 4 + j, a.N - 1)];
+      sc[j] = g4 < 2 ? (g4 == 0 ? v[0] : v[1]) : g4 == 2 ? v[2] : v[3];
+    }
+    group += stride;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = m * 16 + i16;
+      if (row < a.R) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = (float)acc[m][j] * xs[m] * sc[j];
+        typename RowType<DT>::elem* y = static_cast<typename RowType<DT>::elem*>(a.y) + row * a.y_stride + ch;
+        if (ch + 4 <= a.N) {
+          store4<DT>(y, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (ch + j < a.N) y[j] = to_elem<DT>(v[j]);
+        }
+      }
+      acc[m] = (v4i32){0, 0, 0, 0};
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no transfer outlives the wave
 }
 
 // Many tokens: a block of eight waves owns 256 channels and 32 TT tokens, a wave 64
@@ -299,9 +431,23 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = (float)acc[t][j >> 2][j & 3] * xs * sc[j];
-      store16<DT>(a.y, row * a.y_stride + ch, v);
+      store_values<DT>(a.y, row * a.y_stride + ch, v);
     }
   }
+}
+
+template <int DT, int MT, int XBYTES>
+hipError_t run_stream(const LinearArgs& a, hipStream_t st) {
+  const int want = ((a.N + 15) / 16 + 7) / 8;  // a block a CU, or fewer if the channels do not give each wave some
+  launch(linear_stream_kernel<DT, MT, XBYTES>, dim3((unsigned)(want < 256 ? want : 256)), dim3(512), st, a);
+  return hipGetLastError();
+}
+
+template <int DT, int MT>
+hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
+  if (bytes <= 32768) return run_stream<DT, MT, 32768>(a, st);
+  if (bytes <= 65536) return run_stream<DT, MT, 65536>(a, st);
+  return run_stream<DT, MT, 98304>(a, st);
 }
 
 template <int DT, int TT>
@@ -313,14 +459,23 @@ hipError_t run_tile(const LinearArgs& a, hipStream_t st) {
 }
 
 struct LinearPlan {
-  int few;   // 16-token tiles of the few-tokens kernel, or 0
-  int tile;  // TT of the tile kernel
+  int few;     // 16-token tiles of the few-tokens kernel, or 0
+  int stream;  // of the streaming kernel, or 0
+  int tile;    // TT of the tile kernel
   int64_t blocks;
 };
 
-LinearPlan linear_plan(int64_t R, int32_t N) {
+constexpr int kStreamBytes = 98304;
+
+int stream_bytes(int tiles, int32_t H) { return tiles * 16 * ((H + 127) / 128 * 128); }
+
+LinearPlan linear_plan(int64_t R, int32_t N, int32_t H) {
   LinearPlan p{};
-  if (R <= 32 || N < 64) {
+  const int tiles = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  if (R <= 64 && N >= 16384 && stream_bytes(tiles, H) <= kStreamBytes) {
+    p.stream = tiles;
+    p.blocks = 256;
+  } else if (R <= 32 || N < 64) {
     p.few = R <= 16 ? 1 : 2;
     p.blocks = (int64_t)((N + 15) / 16) * ((R + 16 * p.few - 1) / (16 * p.few));
   } else {
@@ -334,7 +489,13 @@ LinearPlan linear_plan(int64_t R, int32_t N) {
 
 template <int DT>
 hipError_t run_typed(const LinearArgs& a, hipStream_t st) {
-  const LinearPlan p = linear_plan(a.R, a.N);
+  const LinearPlan p = linear_plan(a.R, a.N, a.H);
+  switch (p.stream) {
+    case 0: break;
+    case 1: return run_stream_sized<DT, 1>(a, stream_bytes(1, a.H), st);
+    case 2: return run_stream_sized<DT, 2>(a, stream_bytes(2, a.H), st);
+    default: return run_stream_sized<DT, 4>(a, stream_bytes(4, a.H), st);
+  }
   if (p.few == 1) return run_few<DT, 1>(a, st);
   if (p.few == 2) return run_few<DT, 2>(a, st);
   switch (p.tile) {
@@ -347,7 +508,7 @@ hipError_t run_typed(const LinearArgs& a, hipStream_t st) {
 
 }  // namespace
 
-int64_t linear_blocks(int64_t R, int32_t N, int32_t) { return linear_plan(R, N).blocks; }
+int64_t linear_blocks(int64_t R, int32_t N, int32_t H) { return linear_plan(R, N, H).blocks; }
 
 hipError_t launch_linear_i8(int32_t dtype, const LinearArgs& a, hipStream_t st) {
   return dtype == DFLASH_BF16 ? run_typed<DFLASH_BF16>(a, st) : run_typed<DFLASH_F32>(a, st);

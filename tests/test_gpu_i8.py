@@ -157,6 +157,14 @@ def test_linear_sizes(dt, R, N, H):
     check_linear(R, N, H, dt, seed=R, full=True)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("R,N,H", [(1, 16400, 200), (1, 70001, 63), (5, 16999, 4097), (16, 16385, 8192), (17, 20001, 1003), (32, 16384, 2048),
+                                   (33, 30011, 129), (40, 16417, 1000), (64, 17000, 2048), (64, 140000, 16)])
+def test_linear_few_tokens_many_channels(dt, R, N, H):
+    _say(f"[i8] linear {dt} {R} x {N} x {H}")
+    check_linear(R, N, H, dt, seed=R + N, gaps=(16 * (H % 2), 16 * (N % 2)), pad=N % 3, shift=R % 4)
+
+
 def test_linear_special_scales():
     R, N = 20, 40
     xs, ws = np.ones(R), np.ones(N)
