@@ -544,18 +544,20 @@ def _i8(t, name, rows_, H, device, stride=None):
     """Pointer and row stride of an int8 tensor of ``rows_`` rows of H."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int8:
+    if t.dtype is not torch.int8:
         raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows_ or t.shape[1] != H:
+    if t.shape != (rows_, H):
         raise ValueError(f"{name} must have the shape [{rows_}, {H}], got {list(t.shape)}")
-    if H > 1 and t.stride(1) != 1:
+    st, step = t.stride()
+    if step != 1 and H > 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent")
-    st = t.stride(0) if rows_ > 1 else -(-H // 16) * 16
-    if stride is not None and rows_ > 1 and st != stride:
+    if rows_ <= 1:
+        st = -(-H // 16) * 16
+    elif stride is not None and st != stride:
         raise ValueError(f"{name} must have the row stride {stride}, got {st}")
     if t.get_device() != device.index:
         _on(t, name, device)
-    if rows_ and t.storage_offset() + (rows_ - 1) * st + -(-H // 16) * 16 > t.untyped_storage().nbytes():
+    if H % 16 and rows_ and t.storage_offset() + (rows_ - 1) * st + -(-H // 16) * 16 > t.untyped_storage().nbytes():
         raise ValueError(f"the last row of {name} must lie in a multiple of 16 bytes (i8_rows makes such tensors)")
     return t.data_ptr(), st
 
@@ -586,10 +588,11 @@ def dflash_linear_i8(d, xq, xs, wq, ws, y, stream=None):
     """``y`` = the 8-bit rows ``xq`` (scales ``xs``) times ``wq`` (scales
     ``ws``), as ``d = linear_i8(xq, wq, y)`` describes them."""
     dev = xq.device
-    ry = dflash_rows(d.R, d.y_stride, d.N, d.dtype)
+    if y.shape != (d.R, d.N) or y.stride() != (d.y_stride, 1) or _ROWS_DTYPE.get(y.dtype) != d.dtype or y.get_device() != dev.index:
+        _row_tensor(y, "y", dflash_rows(d.R, d.y_stride, d.N, d.dtype), dev, d.y_stride)  # other forms of the same rows, or what is wrong
     _call(lib.dflash_linear_i8, dev, stream, d, _i8(xq, "xq", d.R, d.H, dev, d.xq_stride)[0],
           _vec(xs, "xs", torch.float32, d.R, dev), _i8(wq, "wq", d.N, d.H, dev, d.wq_stride)[0],
-          _vec(ws, "ws", torch.float32, d.N, dev), _row_tensor(y, "y", ry, dev, d.y_stride)[0])
+          _vec(ws, "ws", torch.float32, d.N, dev), y.data_ptr())
 
 
 def dflash_workspace_init(ws, stream=None):

@@ -6,6 +6,7 @@
 // channels of one token.  Lane l of either operand holds the 16 bytes
 // 16 (l / 16) .. of row l % 16 and of 64 bytes of k.  Only the tokens' side is
 // cleared past the row's end: what the weights hold there is multiplied by zero.
+#include <algorithm>
 #include <type_traits>
 
 #include "rows_blocks.hpp"
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int steps = (a.H + 127) / 128, pitch = steps * 128;
   const int n_group = (a.N + 15) / 16, stride = (int)gridDim.x * 8;
-  int group = (int)blockIdx.x + (int)gridDim.x * wave;  // neighbouring blocks read neighbouring rows
+  int group = (int)blockIdx.x * 8 + wave;  // a block's waves read neighbouring rows
   const int total = group < n_group ? ((n_group - 1 - group) / stride + 1) * steps : 0;
 
   unsigned char* ring = lds + XBYTES + wave * (D * 2048);
@@ -469,20 +470,46 @@ constexpr int kStreamBytes = 98304;
 
 int stream_bytes(int tiles, int32_t H) { return tiles * 16 * ((H + 127) / 128 * 128); }
 
+// The streaming kernel wherever its tokens fit and the channels give half of its waves
+// 16; else the least of the others' times in nanoseconds, fitted to them over 322
+// shapes from 1 x 100 x 64 to 2048 x 151936 x 512.  The few-tokens kernel: a start, and
+// the most of a round trip to memory for every eight steps of a wave, its loads at 38
+// bytes a CU, and what a block costs.  The tiles: a start, and rounds of 256 blocks at a time a stage
+// that grows with the tile, or the weights at half of the memory's rate (a quarter of
+// the rounds' time once more, as they do not overlap in whole).
 LinearPlan linear_plan(int64_t R, int32_t N, int32_t H) {
   LinearPlan p{};
   const int tiles = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   if (R <= 64 && N >= 16384 && stream_bytes(tiles, H) <= kStreamBytes) {
     p.stream = tiles;
     p.blocks = 256;
-  } else if (R <= 32 || N < 64) {
-    p.few = R <= 16 ? 1 : 2;
-    p.blocks = (int64_t)((N + 15) / 16) * ((R + 16 * p.few - 1) / (16 * p.few));
-  } else {
-    // the tile that covers the tokens with the least over; the larger one of two that do
-    p.tile = R <= 64 ? 2 : R <= 128 ? 4 : 8;
-    if (p.tile == 8 && (R + 191) / 192 * 192 < (R + 255) / 256 * 256) p.tile = 6;
-    p.blocks = (int64_t)((N + kTileCh * 8 - 1) / (kTileCh * 8)) * 8 * ((R + 32 * p.tile - 1) / (32 * p.tile));
+    return p;
+  }
+  const int64_t st = (H + 63) / 64;
+  double least = 1e300;
+  for (int mt = 1; mt <= 4; mt *= 2) {
+    const int64_t blocks = (int64_t)((N + 15) / 16) * ((R + 16 * mt - 1) / (16 * mt));
+    const double rounds = (double)((blocks + 255) / 256);
+    const double t = 4000.0 + std::max({900.0 * (double)((st + 31) / 32), rounds * (double)((1 + mt) * 1024 * st) / 38.0,
+                                        rounds * (500.0 + 900.0 * mt)});
+    if (t <= least) {
+      least = t;
+      p.few = mt;
+      p.blocks = blocks;
+    }
+  }
+  if (N < 64) return p;
+  for (int tt = 2; tt <= 8; tt += 2) {
+    const int64_t blocks = (int64_t)((N + kTileCh - 1) / kTileCh) * ((R + 32 * tt - 1) / (32 * tt));
+    const double stage = tt == 2 ? 290.0 : tt == 4 ? 360.0 : tt == 6 ? 475.0 : 590.0;
+    const double work = (double)((blocks + 255) / 256 * st) * stage, read = (double)N * H / 3700.0;
+    const double t = 3500.0 + std::max(work, read) + work / 4;
+    if (t < least) {
+      least = t;
+      p.few = 0;
+      p.tile = tt;
+      p.blocks = (int64_t)((N + kTileCh * 8 - 1) / (kTileCh * 8)) * 8 * ((R + 32 * tt - 1) / (32 * tt));
+    }
   }
   return p;
 }
@@ -498,6 +525,7 @@ hipError_t run_typed(const LinearArgs& a, hipStream_t st) {
   }
   if (p.few == 1) return run_few<DT, 1>(a, st);
   if (p.few == 2) return run_few<DT, 2>(a, st);
+  if (p.few == 4) return run_few<DT, 4>(a, st);
   switch (p.tile) {
     case 2: return run_tile<DT, 2>(a, st);
     case 4: return run_tile<DT, 4>(a, st);
