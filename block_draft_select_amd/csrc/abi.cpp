@@ -306,10 +306,15 @@ DistillPlan distill_plan(const dflash_rows& r) {
   return p;
 }
 
-// dflash_logprobs: a wave a row of up to four slots a lane; else a block a row,
-// or as many segments as give 2048 blocks (eight per CU), joined by a second launch
 static int logprobs_units(const dflash_rows& r) { return (row_slots(r) + kLogprobsThreads - 1) / kLogprobsThreads; }
 
+// dflash_logprobs: a wave a row of up to four slots a lane; else a block a row in
+// one launch, or a row's segments over 2048 blocks (eight a CU) and a launch that
+// joins them.  One launch is the better one for many rows (1024 x 50021 bf16 with 20 alternatives: 35 us, 42 in
+// segments) and for short ones; few long rows need more CUs than rows (one of
+// 151936: 14 us, 19 in one launch; 32: 17, 21).  Finding alternatives takes every segment 5 us, so
+// with them segments end at 64 rows (100 x 151936: 22 us in one launch, 32 in
+// segments), without them later (288 x 151936: 29 and 23).
 LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
   LogprobsPlan p{};
   const int slots = row_slots(r), units = logprobs_units(r);
@@ -323,8 +328,17 @@ LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
     p.threads = 64;
     return p;
   }
+  const bool split = N == 0         ? r.R <= 320 && slots >= 4096
+                     : slots > 65536 ? r.R < 256
+                                     : r.R < 64 && slots > 16384;
+  if (!split) {
+    // all rows on the card at once, and at least two slots a thread
+    p.threads = r.R > 512 ? 256 : r.R > 256 ? 512 : 1024;
+    while (p.threads > 256 && slots < 2 * p.threads) p.threads /= 2;
+    return p;
+  }
   p.threads = kLogprobsThreads;
-  const int64_t want = std::max<int64_t>(kLogprobsBlocks / std::max<int64_t>(r.R, 1), 1);
+  const int64_t want = std::max<int64_t>(kLogprobsBlocks / r.R, 1);
   p.n_seg = (int)std::min<int64_t>(std::min<int64_t>(want, units), kLogprobsMaxSeg);
   int per = (units + p.n_seg - 1) / p.n_seg;  // slots a thread
   if (per < 4)

@@ -39,9 +39,10 @@ __device__ __forceinline__ double row_scale(const float* T, int group, int64_t r
 
 template <int T>
 struct Shared {
-  uint32_t tm[T];              // the threads' maxima, as ordered keys
-  uint64_t key[kCap];          // value and inverted index of tokens that may be alternatives
-  uint32_t piece[kPieces];     // thread | piece << 8
+  static constexpr int kMaxima = T < 256 ? T : 256;  // of T / kMaxima neighbouring threads each
+  uint32_t tm[kMaxima];        // as ordered keys
+  uint64_t key[kCap > T + DFLASH_TOP_MAX ? kCap : T + DFLASH_TOP_MAX];  // value and inverted index of tokens that may be alternatives
+  uint32_t piece[kPieces];     // thread | piece << 10
   float wave_m[T / kWave];
   double wave_s[T / kWave], wave_h[T / kWave];
   uint32_t n_piece, n_key, tau;
@@ -200,19 +201,23 @@ __device__ __forceinline__ void top_of_segment(Shared<T>& sh, const RowRef<DT>& 
   constexpr int VE = RowType<DT>::VE;
   const int tid = threadIdx.x;
   const uint32_t k1 = value_key(m1), k2 = value_key(m2), k3 = value_key(m3);
-  sh.tm[tid] = k1;
+  constexpr int kMaxima = Shared<T>::kMaxima, kShare = T / kMaxima;
+  uint32_t shared_max = k1;
+#pragma unroll
+  for (int w = 1; w < kShare; w *= 2) shared_max = max(shared_max, (uint32_t)__shfl_xor(shared_max, w));
+  if (tid % kShare == 0) sh.tm[tid / kShare] = shared_max;
   if (tid == 0) sh.n_piece = 0, sh.n_key = 0;
   __syncthreads();
   if (tid < kWave) {
     // from the highest bit on the largest value that N maxima reach, or one that few more reach
-    uint32_t k[T / kWave], t = 0;
+    uint32_t k[kMaxima / kWave], t = 0;
 #pragma unroll
-    for (int q = 0; q < T / kWave; ++q) k[q] = sh.tm[q * kWave + tid];
+    for (int q = 0; q < kMaxima / kWave; ++q) k[q] = sh.tm[q * kWave + tid];
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t c = t | 1u << bit;
       int n = 0;
 #pragma unroll
-      for (int q = 0; q < T / kWave; ++q) n += __popcll(__ballot(k[q] >= c));
+      for (int q = 0; q < kMaxima / kWave; ++q) n += __popcll(__ballot(k[q] >= c));
       if (n >= N) {
         t = c;
         if (n <= N + 4) break;
@@ -224,7 +229,7 @@ __device__ __forceinline__ void top_of_segment(Shared<T>& sh, const RowRef<DT>& 
   const uint32_t tau = sh.tau;
   auto note = [&](int u) {
     const uint32_t at = atomicAdd(&sh.n_piece, 1u);
-    if (at < (uint32_t)kPieces) sh.piece[at] = (uint32_t)tid | (uint32_t)u << 8;
+    if (at < (uint32_t)kPieces) sh.piece[at] = (uint32_t)tid | (uint32_t)u << 10;
   };
   const int n_unit = (s1 - s0 + T * U - 1) / (T * U);
   if (k1 >= tau) {
@@ -244,7 +249,7 @@ __device__ __forceinline__ void top_of_segment(Shared<T>& sh, const RowRef<DT>& 
   if (!full) {
     for (int i = tid; i < n_piece * U; i += T) {
       const uint32_t p = sh.piece[i / U];
-      const int slot = s0 + ((int)(p >> 8) * U + i % U) * T + (int)(p & 255u);
+      const int slot = s0 + ((int)(p >> 10) * U + i % U) * T + (int)(p & 1023u);
       if (slot >= s1) continue;
       const Slot x = z.load(slot);
 #pragma unroll
@@ -425,11 +430,26 @@ __device__ __noinline__ void sum_far(Shared<T>& sh, const RowRef<DT> z, float m,
   }
 }
 
+// a thread's first given token: read before the row is, as one load waits for the other
+struct Given {
+  int t;    // -1: none, or padding
+  float v;  // its logit
+};
+template <int DT>
+__device__ __forceinline__ Given first_given(const LogprobsArgs& a, const RowRef<DT>& z, int64_t row) {
+  Given g{-1, 0.0f};
+  if ((int)threadIdx.x < a.M) {
+    const int t = a.tok[row * a.M + threadIdx.x];
+    if (t >= 0 && t < a.V) g = Given{t, row_value<DT>(z, t)};
+  }
+  return g;
+}
+
 // a row's outputs from its sums and its alternatives (sh.top)
 template <int DT, int T>
-__device__ __forceinline__ void write_row(Shared<T>& sh, const LogprobsArgs& a, const LogprobsOut& o, int64_t row, Sums r, double c) {
+__device__ __forceinline__ void write_row(Shared<T>& sh, const LogprobsArgs& a, const LogprobsOut& o, const RowRef<DT>& z, int64_t row,
+                                          Sums r, double c, Given first) {
   const int tid = threadIdx.x;
-  const RowRef<DT> z(a.Z, row, a.stride, a.V);
   double l = 0.0, ent = 0.0;
   if (r.m > kNegInf) {
     double off = r.M - (double)r.m * (double)(float)c;
@@ -450,10 +470,12 @@ __device__ __forceinline__ void write_row(Shared<T>& sh, const LogprobsArgs& a, 
   }
   const double per = c * kLn2;  // 1 / T
   for (int k = tid; k < a.M; k += T) {
-    const int t = a.tok[row * a.M + k];
-    float v = 0.0f;
-    if (t >= 0 && t < a.V) v = r.m == kNegInf ? kNegInf : (float)(((double)row_value<DT>(z, t) - (double)r.m) * per - l);
-    o.logp[row * a.M + k] = v;
+    Given g = first;
+    if (k != tid) {
+      g.t = a.tok[row * a.M + k];
+      if (g.t < 0 || g.t >= a.V) g.t = -1; else g.v = row_value<DT>(z, g.t);
+    }
+    o.logp[row * a.M + k] = g.t < 0 ? 0.0f : r.m == kNegInf ? kNegInf : (float)(((double)g.v - (double)r.m) * per - l);
   }
   if (tid < a.N) {
     const uint64_t k = r.m > kNegInf ? sh.top[tid] : 0;
@@ -472,10 +494,11 @@ __global__ __launch_bounds__(T, 8) void logprobs_kernel(LogprobsArgs a, Logprobs
   const int64_t row = blockIdx.x / n_seg;
   const RowRef<DT> z(a.Z, row, a.stride, a.V);
   const double c = row_scale(a.T, a.group, row);
+  const Given first = n_seg == 1 ? first_given<DT>(a, z, row) : Given{-1, 0.0f};
   const int s0 = seg * seg_slots, s1 = min(s0 + seg_slots, z.slots());
   const Sums r = sum_segment<DT, T, U, ENT, TOP>(sh, z, s0, s1, (float)c, a.N);
   if (n_seg == 1) {
-    write_row<DT, T>(sh, a, o, row, r, c);
+    write_row<DT, T>(sh, a, o, z, row, r, c, first);
   } else {
     if (threadIdx.x == 0) parts[blockIdx.x] = LogprobsPart{r.M, r.s, r.h, r.m};
     if (TOP && threadIdx.x < a.N) lists[(int64_t)blockIdx.x * a.N + threadIdx.x] = r.m == r.m && r.m > kNegInf ? sh.top[threadIdx.x] : 0;
@@ -495,6 +518,10 @@ __global__ __launch_bounds__(T) void logprobs_join_kernel(LogprobsArgs a, Logpro
   // at most T segments
   LogprobsPart p{0.0, 0.0, 0.0, kNegInf};
   if (tid < n_seg) p = part[tid];
+  const uint64_t* list = lists + row * n_seg * a.N;
+  const uint64_t mine = a.N > 0 && tid < n_seg ? list[(int64_t)tid * a.N] : 0;  // its segment's best
+  const RowRef<DT> z(a.Z, row, a.stride, a.V);
+  const Given first = first_given<DT>(a, z, row);
   float bm = wave_max_dpp_f32(p.m != p.m ? INFINITY : p.m);
   if ((tid & 63) == 0) sh.wave_m[tid >> 6] = bm;
   __syncthreads();
@@ -517,11 +544,9 @@ __global__ __launch_bounds__(T) void logprobs_join_kernel(LogprobsArgs a, Logpro
   if (a.N > 0 && r.m > kNegInf) {
     // the N-th largest of the segments' best bounds the row's N-th from below: only
     // the lists of those N segments can hold one, what of them reaches it is ranked
-    const uint64_t* list = lists + row * n_seg * a.N;
-    sh.key[tid] = tid < n_seg ? list[(int64_t)tid * a.N] : 0;
+    sh.key[tid] = mine;
     if (tid == 0) sh.least = 1, sh.n_key = 0, sh.n_piece = 0;
     __syncthreads();
-    const uint64_t mine = sh.key[tid];
     int rank = 0;
 #pragma unroll 4
     for (int j = 0; j < n_seg; ++j) rank += sh.key[j] > mine;
@@ -540,7 +565,7 @@ __global__ __launch_bounds__(T) void logprobs_join_kernel(LogprobsArgs a, Logpro
     __syncthreads();
     rank_keys(sh, (int)sh.n_key, a.N);
   }
-  write_row<DT, T>(sh, a, o, row, r, c);
+  write_row<DT, T>(sh, a, o, z, row, r, c, first);
 }
 
 // ---------------------------------------------------------------- backward
@@ -671,6 +696,8 @@ hipError_t run_sized(const LogprobsArgs& a, const LogprobsOut& o, char* ws, cons
 template <int DT>
 hipError_t run_typed(const LogprobsArgs& a, const LogprobsOut& o, char* ws, const LogprobsPlan& pl, hipStream_t st) {
   if (pl.threads == kWave) return run_sized<DT, kWave, 4>(a, o, ws, pl, st);
+  if (pl.threads == 512) return run_sized<DT, 512, 4>(a, o, ws, pl, st);
+  if (pl.threads == 1024) return run_sized<DT, 1024, 4>(a, o, ws, pl, st);
   return pl.unit == 1 ? run_sized<DT, kLogprobsThreads, 1>(a, o, ws, pl, st) : run_sized<DT, kLogprobsThreads, 4>(a, o, ws, pl, st);
 }
 
