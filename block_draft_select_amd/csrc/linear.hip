@@ -7,7 +7,6 @@
 // 16 (l / 16) .. of row l % 16 and of 64 bytes of k.  Only the tokens' side is
 // cleared past the row's end: what the weights hold there is multiplied by zero.
 #include <algorithm>
-#include <type_traits>
 
 #include "rows_blocks.hpp"
 
@@ -279,154 +278,14 @@ __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no transfer outlives the wave
 }
 
-// Many tokens: a block of eight waves owns 256 channels and 32 TT tokens, a wave 64
-// channels and 16 TT tokens.  Stages of 64 bytes of k go from global memory straight
-// into a ring of NB in LDS, four lanes to a row's 64 bytes.  (Loading the weights
-// straight into the operand's registers puts neighbouring lanes in
-// different rows: 38 bytes a nanosecond and CU against 100 this way, and 1490 us
-// against 1235 at 1152 x 4096 x 262144.)
-// A stage in LDS: rows of 64 bytes, piece c of row r at place c ^ (r / 2 % 4), so that
-// the eight rows that are read at once lie in different banks.  The channels' rows are
-// dealt out so that a lane ends up with 16 neighbouring channels: row i of tile c
-// is channel 16 (i / 4) + 4 c + i % 4.
-// All waves of a CU meet at the one barrier a stage has, so nothing may wait behind
-// it: the operands that a stage begins with are read in the stage before, which is
-// why a stage has landed one barrier before its turn.
-constexpr int kTileCh = 256;
-
-template <int TT>
-struct LinearTile {
-  static constexpr int BM = 32 * TT, ROWS = kTileCh + BM, SBYTES = ROWS * 64;
-  static constexpr int NB = 163840 / SBYTES > 6 ? 6 : 163840 / SBYTES;
-  static constexpr int XI = 2 * TT;  // loads of a stage's token rows, 16 rows each
-  static constexpr int LO = 2 + XI / 8, HI = 2 + (XI + 7) / 8;  // a wave's loads a stage: HI for the first XI % 8 waves
-  static_assert(NB >= 4, "a stage in use, one landed, one refilling, one in flight");
-};
-
+// a lane's 16 channels from ch on of the tokens row, row + 16, ..
 template <int DT, int TT>
-__global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n_rt, int n_ct) {
-  using L = LinearTile<TT>;
-  constexpr int NB = L::NB, SB = L::SBYTES, G = TT / 2;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[NB * SB];
-  // ids with the same value mod 8 run on one XCD: the row tiles of a channel tile follow one another there
-  const int grp = blockIdx.x / (8 * n_rt), rem = blockIdx.x - grp * 8 * n_rt;
-  const int rt = rem >> 3, ct = grp * 8 + (rem & 7);
-  if (ct >= n_ct) return;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int wc = wave & 3, wm = wave >> 2;
-  // the last tiles step back to whole ones: some channels are computed twice, alike (N >= 64)
-  const int chb = min(ct * kTileCh, a.N - 64);
-  const int64_t row0 = (int64_t)rt * L::BM;
-  const int n_st = (a.H + 63) / 64;
-
-  const int i16 = lane & 15, g4 = lane >> 4;
-  const int w_stride = (int)a.wq_stride, x_stride = (int)a.xq_stride;
-  const __amdgpu_buffer_rsrc_t wb = rows_buffer(a.wq, chb, a.N, a.wq_stride, a.H);
-  const __amdgpu_buffer_rsrc_t xb = rows_buffer(a.xq, row0, a.R, a.xq_stride, a.H);
-  const int piece = ((lane & 3) ^ (lane >> 3 & 3)) * 16;  // place l % 4 of row l / 4 holds this piece
-  const int wo = ((lane >> 4) * 16 + (lane >> 2 & 3)) * w_stride + piece;
-  const int xo = (lane >> 2) * x_stride + piece;
-  // the wave's i-th load of stage s
-  auto load = [&](int s, int buf, int i) __attribute__((always_inline)) {
-    unsigned char* to = lds + buf * SB;
-    if (i < 2) {
-      const int j = wave * 2 + i;  // 16 rows: tile j % 4 of wave j / 4's channels
-      const int ch = min(ct * kTileCh + (j >> 2) * 64, a.N - 64) - chb;
-      load_to_lds16(wb, wo, (ch + 4 * (j & 3)) * w_stride + s * 64, to + j * 1024);
-    } else {
-      const int j = wave + 8 * (i - 2);
-      if (j < L::XI) load_to_lds16(xb, xo, 16 * j * x_stride + s * 64, to + (16 + j) * 1024);
-    }
-  };
-  // until this wave's loads of all but the last n stages are done
-  auto wait = [&](auto n) __attribute__((always_inline)) {
-    asm volatile("" ::: "memory");
-    if (L::LO == L::HI || wave < L::XI % 8)
-      wait_loads<L::HI * decltype(n)::value>();
-    else
-      wait_loads<L::LO * decltype(n)::value>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-  // the tokens' bytes behind the rows' end, in a stage that holds such
-  auto clear = [&](int s, int buf) __attribute__((always_inline)) {
-    if (s * 64 + 64 > a.H) {
-      const int valid = a.H - s * 64;
-      uint32_t* p = reinterpret_cast<uint32_t*>(lds + buf * SB + kTileCh * 64);
-#pragma unroll 1
-      for (int q = tid; q < L::BM * 16; q += 512) {  // words
-        const int n = valid - (((q >> 2) & 3) ^ ((q >> 5) & 3)) * 16 - (q & 3) * 4;
-        if (n < 4) p[q] = n <= 0 ? 0u : p[q] & ((1u << (8 * n)) - 1u);
-      }
-      lds_barrier();
-    }
-  };
-
-  const int fo = i16 * 64 + ((g4 ^ (i16 >> 1 & 3)) * 16);
-  const unsigned char* wf = lds + wc * 4096 + fo;
-  const unsigned char* xf = lds + kTileCh * 64 + wm * (TT * 1024) + fo;
-  v4i32 acc[TT][4], wv[2][4], xv[2][2];
-#pragma unroll
-  for (int t = 0; t < TT; ++t)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[t][c] = (v4i32){0, 0, 0, 0};
-
-#pragma unroll
-  for (int s = 0; s < NB - 1; ++s) {
-#pragma unroll
-    for (int i = 0; i < L::HI; ++i) load(s, s, i);
-  }
-  wait(std::integral_constant<int, NB - 2>{});
-  clear(0, 0);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) wv[0][c] = *reinterpret_cast<const v4i32*>(wf + c * 1024);
-#pragma unroll
-  for (int t = 0; t < 2; ++t) xv[0][t] = *reinterpret_cast<const v4i32*>(xf + t * 1024);
-
-  int buf = 0;  // of stage s
-  auto stage = [&](int s, auto parity) __attribute__((always_inline)) {
-    constexpr int P = decltype(parity)::value;
-    const int next = buf + 1 == NB ? 0 : buf + 1, refill = buf == 0 ? NB - 1 : buf - 1;
-    // stage s + 1 has landed, and no wave reads stage s - 1 any more
-    wait(std::integral_constant<int, NB - 3>{});
-    clear(s + 1, next);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      constexpr int kX0 = P * G;  // pairs of token tiles so far, mod 2
-      const int cur = (kX0 + g) & 1;
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        xv[cur ^ 1][t] = *reinterpret_cast<const v4i32*>(g + 1 < G ? xf + buf * SB + (2 * g + 2 + t) * 1024 : xf + next * SB + t * 1024);
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c * G / 4 == g) wv[P ^ 1][c] = *reinterpret_cast<const v4i32*>(wf + next * SB + c * 1024);
-#pragma unroll
-      for (int i = 0; i < L::HI; ++i)
-        if (i * G / L::HI == g) load(s + NB - 1, refill, i);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          acc[2 * g + t][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[P][c], xv[cur][t], acc[2 * g + t][c], 0, 0, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    buf = next;
-  };
-  // an odd last stage takes one behind the end with it, whose tokens are cleared
-  for (int s = 0; s < n_st; s += 2) {
-    stage(s, std::integral_constant<int, 0>{});
-    stage(s + 1, std::integral_constant<int, 1>{});
-  }
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no transfer outlives the loop
-
-  const int ch = min(ct * kTileCh + wc * 64, a.N - 64) + g4 * 16;
+__device__ __forceinline__ void store_tile(const LinearArgs& a, const v4i32 (&acc)[TT][4], int ch, int64_t row) {
   float sc[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) sc[j] = a.ws[ch + j];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t row = row0 + (wm * TT + t) * 16 + i16;
+  for (int t = 0; t < TT; ++t, row += 16) {
     if (row < a.R) {
       const float xs = a.xs[row];
       float v[16];
@@ -449,6 +308,146 @@ hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
   if (bytes <= 32768) return run_stream<DT, MT, 32768>(a, st);
   if (bytes <= 65536) return run_stream<DT, MT, 65536>(a, st);
   return run_stream<DT, MT, 98304>(a, st);
+}
+
+// Many tokens: a block of eight waves owns 256 channels and 32 TT tokens, a wave 64
+// channels and 16 TT tokens.  Stages of 128 bytes of k go from global memory straight
+// into a ring of NB in LDS, eight lanes to a row's cache line.  (Loading the
+// weights straight into the operand's registers puts neighbouring lanes in different
+// rows: 38 bytes a nanosecond and CU against 125 this way, 100 with 64 bytes of a
+// row; 1152 x 4096 x 262144 took 1490 us so, 1280 with stages of 64 bytes, 1250 with these.)
+// A stage in LDS: rows of 128 bytes, piece c of row r at place c ^ (r % 8), so that the
+// eight rows that are read at once lie in different banks.  The channels' rows are
+// dealt out so that a lane ends up with 16 neighbouring channels: row i of tile c is
+// channel 16 (i / 4) + 4 c + i % 4.
+// A stage is waited for late in the one before it, at a barrier of its own, so that
+// the operands it begins with are read before it begins and the loads of the stages
+// behind it stay in flight.  What bounds it: the clock, which the card lowers to 1.5
+// to 1.7 GHz under this load (a stage of 256 tokens takes 1.4 times its products' cycles).
+constexpr int kTileCh = 256;
+
+template <int DT, int TT>
+__global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n_rt, int n_ct) {
+  constexpr int BM = 32 * TT, SB = (kTileCh + BM) * 128, NB = 163840 / SB, G = TT / 2;
+  constexpr int PER = (kTileCh + BM) / 64;  // a wave's loads a stage, 8 rows each
+  static_assert(NB >= 2, "a stage in use, one landing");
+  constexpr int LG = NB == 2 ? (2 * G + 3) / 4 : 2 * G - 1;  // groups that bring loads: early ones if they have to land in this stage
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[NB * SB];
+  // ids with the same value mod 8 run on one XCD: the row tiles of a channel tile follow one another there
+  const int grp = blockIdx.x / (8 * n_rt), rem = blockIdx.x - grp * 8 * n_rt;
+  const int rt = rem >> 3, ct = grp * 8 + (rem & 7);
+  if (ct >= n_ct) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wc = wave & 3, wm = wave >> 2;
+  // the last tiles step back to whole ones: some channels are computed twice, alike (N >= 64)
+  const int chb = min(ct * kTileCh, a.N - 64);
+  const int64_t row0 = (int64_t)rt * BM;
+  const int n_st = (a.H + 127) / 128;
+
+  const int i16 = lane & 15, g4 = lane >> 4;
+  const int w_stride = (int)a.wq_stride, x_stride = (int)a.xq_stride;
+  const __amdgpu_buffer_rsrc_t wb = rows_buffer(a.wq, chb, a.N, a.wq_stride, a.H);
+  const __amdgpu_buffer_rsrc_t xb = rows_buffer(a.xq, row0, a.R, a.xq_stride, a.H);
+  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;  // place l % 8 of row l / 8 holds this piece
+  const int wo = ((lane >> 5) * 16 + (lane >> 3 & 3)) * w_stride + piece;
+  const int xo = (lane >> 3) * x_stride + piece;
+  const int chw = min(ct * kTileCh + (wave >> 1) * 64, a.N - 64) - chb;
+  // the wave's i-th load of stage s
+  auto load = [&](int s, int buf, int i) __attribute__((always_inline)) {
+    unsigned char* to = lds + buf * SB;
+    if (i < 4) {  // rows 8 (j % 2) .. of tile j / 2 of 64 channels, a pair of waves each
+      const int j = (wave & 1) * 4 + i;
+      load_to_lds16(wb, wo, (chw + 32 * (j & 1) + 4 * (j >> 1)) * w_stride + s * 128, to + (wave * 4 + i) * 1024);
+    } else {
+      const int j = wave * (TT / 2) + i - 4;
+      load_to_lds16(xb, xo, 8 * j * x_stride + s * 128, to + (32 + j) * 1024);
+    }
+  };
+  auto barrier = [&]() __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // the tokens' bytes behind the rows' end, in a stage that holds such
+  auto clear = [&](int s, int buf) __attribute__((always_inline)) {
+    if (s * 128 + 128 > a.H) {
+      const int valid = a.H - s * 128;
+      uint32_t* p = reinterpret_cast<uint32_t*>(lds + buf * SB + kTileCh * 128);
+#pragma unroll 1
+      for (int q = tid; q < BM * 32; q += 512) {  // words
+        const int n = valid - (((q >> 2) & 7) ^ ((q >> 5) & 7)) * 16 - (q & 3) * 4;
+        if (n < 4) p[q] = n <= 0 ? 0u : p[q] & ((1u << (8 * n)) - 1u);
+      }
+      lds_barrier();
+    }
+  };
+
+  int fo[2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) fo[ks] = i16 * 128 + ((4 * ks + g4) ^ (i16 & 7)) * 16;
+  const unsigned char* wf = lds + wc * 8192;
+  const unsigned char* xf = lds + kTileCh * 128 + wm * (TT * 2048);
+  v4i32 acc[TT][4], wv[2][4], xv[2][2];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[t][c] = (v4i32){0, 0, 0, 0};
+
+#pragma unroll
+  for (int s = 0; s < NB - 1; ++s) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) load(s, s, i);
+  }
+  asm volatile("" ::: "memory");
+  wait_loads<PER * (NB - 2)>();
+  barrier();
+  clear(0, 0);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) wv[0][c] = *reinterpret_cast<const v4i32*>(wf + c * 2048 + fo[0]);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) xv[0][t] = *reinterpret_cast<const v4i32*>(xf + t * 2048 + fo[0]);
+
+  int buf = 0;
+#pragma unroll 1
+  for (int s = 0; s < n_st; ++s) {
+    const int next = buf + 1 == NB ? 0 : buf + 1, refill = buf == 0 ? NB - 1 : buf - 1;
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads are done
+    barrier();                           // and all waves': stage s - 1 may go
+#pragma unroll
+    for (int g = 0; g < 2 * G; ++g) {
+      const int ks = g / G;
+      __builtin_amdgcn_sched_barrier(0);
+      if (g == 2 * G - 1) {
+        asm volatile("" ::: "memory");
+        wait_loads<PER * (NB - 2)>();  // stage s + 1 has landed
+        barrier();
+        if (s + 1 < n_st) clear(s + 1, next);
+      }
+      const unsigned char* from = g + 1 < 2 * G ? xf + buf * SB + ((g + 1) % G) * 4096 + fo[(g + 1) / G % 2] : xf + next * SB + fo[0];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) xv[(g + 1) & 1][t] = *reinterpret_cast<const v4i32*>(from + t * 2048);
+      if (g == G - 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) wv[1][c] = *reinterpret_cast<const v4i32*>(wf + buf * SB + c * 2048 + fo[1]);
+      }
+      if (g == 2 * G - 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) wv[0][c] = *reinterpret_cast<const v4i32*>(wf + next * SB + c * 2048 + fo[0]);
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i * LG / PER == g) load(s + NB - 1, refill, i);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc[g % G * 2 + t][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[ks][c], xv[g & 1][t], acc[g % G * 2 + t][c], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    buf = next;
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no transfer outlives the loop
+  store_tile<DT, TT>(a, acc, min(ct * kTileCh + wc * 64, a.N - 64) + g4 * 16, row0 + wm * TT * 16 + i16);
 }
 
 template <int DT, int TT>
@@ -499,9 +498,9 @@ LinearPlan linear_plan(int64_t R, int32_t N, int32_t H) {
     }
   }
   if (N < 64) return p;
-  for (int tt = 2; tt <= 8; tt += 2) {
+  for (int tt = 2; tt <= 8; tt *= 2) {
     const int64_t blocks = (int64_t)((N + kTileCh - 1) / kTileCh) * ((R + 32 * tt - 1) / (32 * tt));
-    const double stage = tt == 2 ? 290.0 : tt == 4 ? 360.0 : tt == 6 ? 475.0 : 590.0;
+    const double stage = tt == 2 ? 250.0 : tt == 4 ? 330.0 : 590.0;
     const double work = (double)((blocks + 255) / 256 * st) * stage, read = (double)N * H / 3700.0;
     const double t = 3500.0 + std::max(work, read) + work / 4;
     if (t < least) {
@@ -529,7 +528,6 @@ hipError_t run_typed(const LinearArgs& a, hipStream_t st) {
   switch (p.tile) {
     case 2: return run_tile<DT, 2>(a, st);
     case 4: return run_tile<DT, 4>(a, st);
-    case 6: return run_tile<DT, 6>(a, st);
     default: return run_tile<DT, 8>(a, st);
   }
 }
