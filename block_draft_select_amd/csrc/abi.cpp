@@ -308,13 +308,17 @@ DistillPlan distill_plan(const dflash_rows& r) {
 
 static int logprobs_units(const dflash_rows& r) { return (row_slots(r) + kLogprobsThreads - 1) / kLogprobsThreads; }
 
-// dflash_logprobs: a wave a row of up to four slots a lane; else a block a row in
-// one launch, or a row's segments over 2048 blocks (eight a CU) and a launch that
-// joins them.  One launch is the better one for many rows (1024 x 50021 bf16 with 20 alternatives: 35 us, 42 in
-// segments) and for short ones; few long rows need more CUs than rows (one of
-// 151936: 14 us, 19 in one launch; 32: 17, 21).  Finding alternatives takes every segment 5 us, so
-// with them segments end at 64 rows (100 x 151936: 22 us in one launch, 32 in
-// segments), without them later (288 x 151936: 29 and 23).
+// dflash_logprobs: a wave a row of up to four slots a lane; else a block a row in one
+// launch, or a row's segments over 2048 blocks (eight a CU) and a launch that joins
+// them.  One launch is the better one for many rows (1024 x 50021 bf16 with 20
+// alternatives: 35 us, 42 in segments) and for short ones; few long rows need more CUs
+// than rows (one of 151936: 14 us, 19 in one launch; 32: 17, 21).  Finding alternatives
+// takes every segment 5 us, so with them segments end at 64 rows (100 x 151936: 20 us in
+// one launch, 21 in segments) or at 128 of more than 65536 slots (128 x 600000 fp32: 62,
+// 78), without them later (288 x 151936: 29 and 23).  Rows a little beyond one a CU leave
+// most CUs idle behind the first: three segments a row share them (288 x 151936 bf16 with
+// 20 alternatives and entropies: 31.5 us, 34.5; 360: 35.6, 34.7; fp32, which computes
+// less per byte: 43.8, 41.8).
 LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
   LogprobsPlan p{};
   const int slots = row_slots(r), units = logprobs_units(r);
@@ -328,9 +332,10 @@ LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
     p.threads = 64;
     return p;
   }
-  const bool split = N == 0         ? r.R <= 320 && slots >= 4096
-                     : slots > 65536 ? r.R < 256
-                                     : r.R < 64 && slots > 16384;
+  const bool shared = N > 0 && r.dtype == DFLASH_BF16 && r.R > 256 && r.R <= 341 && slots > 16384;
+  const bool split = shared || (N == 0         ? r.R <= 320 && slots >= 4096
+                                : slots > 65536 ? r.R < 128
+                                                : r.R < 64 && slots > 16384);
   if (!split) {
     // all rows on the card at once, and at least two slots a thread
     p.threads = r.R > 512 ? 256 : r.R > 256 ? 512 : 1024;
@@ -338,7 +343,7 @@ LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
     return p;
   }
   p.threads = kLogprobsThreads;
-  const int64_t want = std::max<int64_t>(kLogprobsBlocks / r.R, 1);
+  const int64_t want = shared ? 3 : std::max<int64_t>(kLogprobsBlocks / r.R, 1);
   p.n_seg = (int)std::min<int64_t>(std::min<int64_t>(want, units), kLogprobsMaxSeg);
   int per = (units + p.n_seg - 1) / p.n_seg;  // slots a thread
   if (per < 4)
@@ -1049,8 +1054,10 @@ dflash_status dflash_quant_i8(const dflash_rows* r, const void* X, int8_t* q, in
     if (dflash_status s = check_elem(*r, X, "X")) return s;
     if (dflash_status s = check_ptrs({{scale, "scale", false}})) return s;
     const int64_t es = (int64_t)logit_bytes(r->dtype);
-    if (meet(X, span(r->R, r->stride * es, r->V * es), q, span(r->R, q_stride, r->V)))
-      return fail(DFLASH_ERR_INVALID_ARG, "q overlaps X");
+    const uintptr_t nx = span(r->R, r->stride * es, r->V * es), nq = span(r->R, q_stride, r->V);
+    if (meet(X, nx, q, nq)) return fail(DFLASH_ERR_INVALID_ARG, "q overlaps X");
+    if (meet(scale, r->R * 4, X, nx) || meet(scale, r->R * 4, q, nq))
+      return fail(DFLASH_ERR_INVALID_ARG, "scale overlaps X or q");
     hipStream_t st = (hipStream_t)stream;
     const dfk::QuantArgs a{X, r->R, r->stride, r->V, q, q_stride, scale};
     return hip_status(timed(DFLASH_KERNEL_QUANT_I8, st, [&] { return dfk::launch_quant_i8(r->dtype, a, st); }),
@@ -1067,7 +1074,9 @@ dflash_status dflash_linear_i8(const dflash_linear* d, const int8_t* xq, const f
     if (dflash_status s = check_linear(d, xq, xs, wq, ws, Y)) return s;
     if (d->R == 0) return DFLASH_OK;
     hipStream_t st = (hipStream_t)stream;
-    const dfk::LinearArgs a{d->R, d->xq_stride, d->wq_stride, d->y_stride, d->N, d->H, xq, xs, wq, ws, Y};
+    // one row's stride may be anything
+    const dfk::LinearArgs a{d->R, d->R > 1 ? d->xq_stride : 0, d->N > 1 ? d->wq_stride : 0, d->y_stride, d->N, d->H,
+                            xq, xs, wq, ws, Y};
     return hip_status(timed(DFLASH_KERNEL_LINEAR_I8, st, [&] { return dfk::launch_linear_i8(d->dtype, a, st); }),
                       "8-bit product launch");
   } catch (...) {

@@ -174,6 +174,108 @@ def test_linear_special_scales():
         check_linear(R, N, 100, dt, scales=(xs, ws))
 
 
+@pytest.mark.parametrize("R,N", [(1, 48), (20, 300), (130, 1000), (300, 2000)])
+def test_the_longest_rows(R, N):
+    # sums of 65536 products of -128 and -128 stay below 2^31
+    _say(f"[i8] linear f32 {R} x {N} x 65536")
+    check_linear(R, N, 65536, "f32", seed=R, full=True)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("R,N,H,strides", [
+    (9, 100, 100, (112, 112, 1 << 28)), (9, 16400, 100, (112, 112, 1 << 28)), (300, 300, 64, (64, 64, 1 << 23)),
+    (530, 600, 200, (1 << 22, 1 << 22, 600)), (20, 600, 200, (1 << 22, 1 << 22, 600)), (20, 16400, 200, (1 << 22, 1 << 18, 16401))])
+def test_products_beyond_32_bit_offsets(dt, R, N, H, strides):
+    # the last rows of the result, of the tokens or of the weights begin 2^31 elements and more behind the first
+    import torch
+    import block_draft_select_amd as dfl
+    rng = np.random.default_rng(R + N)
+    xq, wq = rng.integers(-127, 128, size=(R, H)), rng.integers(-127, 128, size=(N, H))
+    pitch = -(-H // 16) * 16
+    xs, ws = np.exp(rng.normal(size=R)).astype(np.float32), np.exp(rng.normal(size=N)).astype(np.float32)
+
+    def far(rows, stride, width, a, dtype):
+        t = torch.empty((rows - 1) * stride + width, dtype=dtype, device="cuda").as_strided((rows, a.shape[1]), (stride, 1))
+        t.copy_(torch.from_numpy(a).to(dtype))
+        return t
+
+    tx, tw = far(R, strides[0], pitch, xq, torch.int8), far(N, strides[1], pitch, wq, torch.int8)
+    y = far(R, strides[2], N, np.full((R, N), 777.0), _type(dt))
+    _say(f"[i8] linear {dt} {R} x {N} x {H}, rows {strides} apart")
+    dfl.dflash_linear_i8(dfl.linear_i8(tx, tw, y), tx, torch.from_numpy(xs).cuda(), tw, torch.from_numpy(ws).cuda(), y)
+    torch.cuda.synchronize()
+    want = O.product(xq, xs, wq, ws)
+    assert np.array_equal(y.float().cpu().numpy(), O.to_bf16(want) if dt == "bf16" else want)
+
+
+def test_quant_beyond_32_bit_offsets():
+    import torch
+    import block_draft_select_amd as dfl
+    R, H = 20, 1003
+    rng = np.random.default_rng(8)
+    x = torch.empty((R - 1) * (1 << 27) + H, dtype=torch.bfloat16, device="cuda").as_strided((R, H), (1 << 27, 1))
+    x.copy_(torch.from_numpy(rng.normal(size=(R, H))).to(x.dtype))
+    near, q, qn = x.contiguous(), dfl.i8_rows(R, H), dfl.i8_rows(R, H)
+    s, sn = torch.empty(R, device="cuda"), torch.empty(R, device="cuda")
+    dfl.dflash_quant_i8(dfl.rows(x), x, q, s)
+    dfl.dflash_quant_i8(dfl.rows(near), near, qn, sn)
+    far = torch.empty(2000 * (1 << 21), dtype=torch.int8, device="cuda").view(2000, 1 << 21)[:, :H]
+    many = near.repeat(100, 1)
+    sm = torch.empty(2000, device="cuda")
+    dfl.dflash_quant_i8(dfl.rows(many), many, far, sm)
+    torch.cuda.synchronize()
+    assert torch.equal(q, qn) and torch.equal(s, sn)
+    assert torch.equal(far, qn.repeat(100, 1)) and torch.equal(sm, sn.repeat(100))
+
+
+@pytest.mark.parametrize("R,N,H", [(3, 400, 300), (5, 40000, 300), (40, 20000, 1000), (300, 3000, 500)])
+def test_products_on_two_streams_and_in_a_graph(R, N, H):
+    import torch
+    import block_draft_select_amd as dfl
+    ins = []
+    for k in range(2):
+        x, w = dfl.i8_rows(R, H), dfl.i8_rows(N, H)
+        h, m = torch.randn(R, H, device="cuda").bfloat16(), torch.randn(N, H, device="cuda").bfloat16()
+        xs, ws, y = torch.empty(R, device="cuda"), torch.empty(N, device="cuda"), torch.empty(R, N, device="cuda")
+        ins.append((h, m, x, xs, w, ws, y))
+
+    def step(i):
+        h, m, x, xs, w, ws, y = i
+        dfl.dflash_quant_i8(dfl.rows(h), h, x, xs)
+        dfl.dflash_quant_i8(dfl.rows(m), m, w, ws)
+        dfl.dflash_linear_i8(dfl.linear_i8(x, w, y), x, xs, w, ws, y)
+
+    wants = []
+    for i in ins:
+        step(i)
+        torch.cuda.synchronize()
+        wants.append(i[-1].clone())
+        q = [[O.quantise(r) for r in t.float().cpu().numpy()] for t in (i[0], i[1][:50])]
+        want = O.product(*[np.stack([a[j] for a in b]) if j == 0 else np.array([a[j] for a in b]) for b in q for j in (0, 1)])
+        assert np.array_equal(i[-1][:, :50].cpu().numpy(), want)
+        i[-1].zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                step(ins[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert torch.equal(ins[k][-1], wants[k])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(ins[0])
+    for k in range(4):
+        ins[0][0].copy_(torch.randn(R, H, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = ins[0][-1].clone()
+        step(ins[0])
+        torch.cuda.synchronize()
+        assert torch.equal(got, ins[0][-1])
+
+
 def test_empty_product():
     import torch
     import block_draft_select_amd as dfl
@@ -219,6 +321,7 @@ def test_hidden_vectors_to_log_probabilities():
     want = O.to_bf16(O.product(np.stack([q for q, _ in hq]), np.array([s for _, s in hq]), np.stack([q for q, _ in hw]),
                                np.array([s for _, s in hw])))
     assert np.array_equal(U.view(-1, V).float().cpu().numpy(), want)
+    # l is below 9 and E|t| below 13: 9 2^-24 + 13 ln2 1.5 2^-24 + 12 2^-24 < 4e-6, eleven times the second for the entropy
     for i in range(B * L):
         o = RO.logprobs(want[i], [int(tok[i])], 5)
         assert 0 <= int(tok[i]) < V and top[i].tolist() == o["top_idx"].tolist()

@@ -192,9 +192,10 @@ def test_long_rows(dt, kind, V, N):
 
 
 @pytest.mark.parametrize("kind", ["flat", "ties", "constant", "down", "odd", "masked"])
-@pytest.mark.parametrize("dt,R,V", [("bf16", 2050, 20000), ("f32", 2050, 9001), ("bf16", 300, 30011), ("f32", 1030, 20000)])
+@pytest.mark.parametrize("dt,R,V", [("bf16", 2050, 20000), ("f32", 2050, 9001), ("bf16", 300, 30011), ("f32", 1030, 20000),
+                                    ("bf16", 300, 140011), ("f32", 129, 270001), ("bf16", 40, 140011)])
 def test_many_rows(dt, R, V, kind):
-    # one block a row, and two segments; the oracle looks at some of the rows
+    # one block a row, and segments of rows; the oracle looks at some of the rows
     rng = np.random.default_rng(R + V)
     z = np.tile(logits(rng, 25, V, kind), (R // 25 + 1, 1))[:R]
     _say(f"[logprobs] {dt} {R} x {V} {kind}")
@@ -414,6 +415,76 @@ def test_grad_against_differences_of_the_forward(dt):
             num = (value(zz[i] + 1e-5 * u) - value(zz[i] - 1e-5 * u)) / 2e-5
             bar = float(np.sum(np.abs(dd[i] * u)) * (EPS[dt] + 32 * 2.0 ** -23)) + 1e-6
             assert abs(num - float(np.dot(dd[i], u))) <= bar
+
+
+# ---------------------------------------------------------------- far rows, streams
+
+
+@pytest.mark.parametrize("dt,V,R,stride", [("bf16", 5003, 18, (1 << 27) + 3), ("f32", 140011, 18, 1 << 27), ("bf16", 9, 66, 1 << 25)])
+def test_rows_beyond_32_bit_offsets(dt, V, R, stride):
+    # the last rows begin 2^31 elements and more behind the first
+    import torch
+    import block_draft_select_amd as dfl
+    rng = np.random.default_rng(V)
+    z = logits(rng, R, V, "peaked")
+    far = torch.empty((R - 1) * stride + V, dtype=_type(dt), device="cuda").as_strided((R, V), (stride, 1))
+    far.copy_(torch.from_numpy(z).to(far.dtype))
+    near = far.contiguous()
+    tok, g = _gpu_arr(tokens(rng, R, V, 3), torch.int32), _gpu_arr(rng.normal(size=(R, 3)), torch.float32)
+    ge = _gpu_arr(rng.normal(size=R), torch.float32)
+    _say(f"[logprobs] {R} rows of {V} {dt}, {stride} apart")
+    o, p = forward(far, tok, 9), forward(near, tok, 9)
+    for n in o:
+        assert torch.equal(o[n], p[n]), n
+    want = torch.empty_like(near)
+    dfl.dflash_logprobs_grad(dfl.rows(near), near, tok, g, p["norm"], want, entropy=p["entropy"], grad_entropy=ge)
+    dfl.dflash_logprobs_grad(dfl.rows(far), far, tok, g, o["norm"], far, entropy=o["entropy"], grad_entropy=ge)
+    torch.cuda.synchronize()
+    assert torch.equal(far, want)
+
+
+def test_one_row_of_any_stride():
+    import torch
+    import block_draft_select_amd as dfl
+    z = torch.randn(1, 4001, device="cuda").bfloat16()
+    tok = torch.tensor([[17]], dtype=torch.int32, device="cuda")
+    want = forward(z, tok, 4)
+    for stride in (0, -9, 1 << 40):  # 2^40 is the largest that any call takes
+        got = forward(z.as_strided((1, 4001), (max(stride, 0), 1)), tok, 4)
+        r = dfl.dflash_rows(1, stride, 4001, dfl.BF16)
+        norm, logp = torch.empty(1, 2, device="cuda"), torch.empty(1, 1, device="cuda")
+        dfl.dflash_logprobs(r, z, tok, logp, norm, dfl.rows_workspace(dfl.rows(z)))
+        assert torch.equal(got["norm"], want["norm"]) and torch.equal(norm, want["norm"]) and torch.equal(logp, want["logp"])
+
+
+def test_calls_on_two_streams_at_once():
+    import torch
+    import block_draft_select_amd as dfl
+    rng = np.random.default_rng(3)
+    R, V = 24, 151936
+    ins, wants = [], []
+    for _ in range(2):
+        v, _ = _tensor(logits(rng, R, V, "peaked"), torch.bfloat16)
+        tok, g = _gpu_arr(tokens(rng, R, V, 2), torch.int32), _gpu_arr(rng.normal(size=(R, 2)), torch.float32)
+        o = forward(v, tok, 20)
+        d = torch.empty_like(v)
+        dfl.dflash_logprobs_grad(dfl.rows(v), v, tok, g, o["norm"], d)
+        ins.append((v, tok, g, torch.empty_like(v), dfl.rows_workspace(dfl.rows(v))))
+        wants.append((o, d))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    for _ in range(5):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                v, tok, g, d, ws = ins[k]
+                got[k] = forward(v, tok, 20, ws=ws)
+                dfl.dflash_logprobs_grad(dfl.rows(v), v, tok, g, got[k]["norm"], d)
+    torch.cuda.synchronize()
+    for k in range(2):
+        for n in wants[k][0]:
+            assert torch.equal(got[k][n], wants[k][0][n]), (k, n)
+        assert torch.equal(ins[k][3], wants[k][1])
 
 
 # ---------------------------------------------------------------- graphs

@@ -44,6 +44,8 @@ def test_bad_quant_calls(dfl):
     for at in (0x10000, 0x10000 + 500, 0x10000 - 300):
         assert _quant(dfl, r, q=ctypes.c_void_p(at // 16 * 16)) == 1
         assert b"overlaps" in dfl.lib.dflash_last_error()
+    for kw in (dict(X=ctypes.c_void_p(0x50000), scale=ctypes.c_void_p(0x50000 + 596)), dict(q=ctypes.c_void_p(0x50000), scale=ctypes.c_void_p(0x50000 - 8))):
+        assert _quant(dfl, r, **kw) == 1 and b"scale overlaps" in dfl.lib.dflash_last_error()
 
 
 @pytest.mark.parametrize("kw,status", [
