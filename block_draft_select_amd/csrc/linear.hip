@@ -411,15 +411,15 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
 #pragma unroll 1
   for (int s = 0; s < n_st; ++s) {
     const int next = buf + 1 == NB ? 0 : buf + 1, refill = buf == 0 ? NB - 1 : buf - 1;
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads are done
-    barrier();                           // and all waves': stage s - 1 may go
+    // The refilled stage s - 1 is read no more: the wait before its barrier was for LDS reads
+    // too, and all of them had been issued by then
 #pragma unroll
     for (int g = 0; g < 2 * G; ++g) {
       const int ks = g / G;
       __builtin_amdgcn_sched_barrier(0);
       if (g == 2 * G - 1) {
         asm volatile("" ::: "memory");
-        wait_loads<PER * (NB - 2)>();  // stage s + 1 has landed
+        wait_loads<PER * (NB - 2)>();  // stage s + 1 has landed, and stage s is read
         barrier();
         if (s + 1 < n_st) clear(s + 1, next);
       }
