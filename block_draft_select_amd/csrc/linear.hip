@@ -82,8 +82,18 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
 }
 
+// Weights whose rows are a multiple of 4096 bytes apart begin in the same memory channels,
+// all of them: blocks that go through k in step then read from a few channels at a time.
+// There each begins at a place of its own (sums of integers have no order); elsewhere
+// that gains nothing, and costs where rows are 2048 bytes apart (1 x 151936 x 2048: 57 us,
+// 53; 1 x 100000 x 4096: 79, 85).
+bool shifted(const LinearArgs& a) { return a.wq_stride % 4096 == 0; }
+
 // Few tokens: 16 channels and 16 MT tokens a block, its four waves split k.
-// Each wave has eight steps of 64 bytes in flight.
+// Each wave has eight steps of 64 bytes in flight.  The operands go straight to registers,
+// neighbouring lanes in different rows: at 30 to 40 bytes a nanosecond and CU that is the
+// slowest way to read, but the one that starts first (1 x 2048 x 2048: 7 us of call, the
+// kernel 3; 1 x 65536 x 8192 with one round after another: 96 us, 5.6 TB/s).
 template <int DT, int MT>
 __global__ __launch_bounds__(256) void linear_few_kernel(LinearArgs a) {
   constexpr int U = 8;
@@ -163,7 +173,9 @@ hipError_t run_few(const LinearArgs& a, hipStream_t st) {
 // there, 128 bytes of k a step; no wave waits for another.  Rows of 128 bytes (of
 // the ring) and of whole 128 bytes (of the tokens) hold piece c of row r at place
 // c ^ (r % 8).  What lies behind a token row's end is zero.
-template <int DT, int MT, int XBYTES>
+// Bound by the weights' bytes: 2048 x 151936 in 53 us for one token (5.9 TB/s of the 7.0 that
+// a read reaches), 59 for 16, 64 for 32, where the tiles below take 66, 69 and 72.
+template <int DT, int MT, int XBYTES, bool SHIFT>
 __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
   constexpr int D = (163840 - XBYTES) / 8 / 2048;  // steps in a wave's ring
   __shared__ __attribute__((aligned(1024))) unsigned char lds[XBYTES + 8 * D * 2048];
@@ -176,15 +188,16 @@ __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
   unsigned char* ring = lds + XBYTES + wave * (D * 2048);
   const int w_stride = (int)a.wq_stride;
   const int wo = (lane >> 3) * w_stride + ((lane & 7) ^ (lane >> 3)) * 16;
-  int load_group = group, load_step = 0, load_slot = 0;
+  const int rot = SHIFT ? (wave * 3 + (int)blockIdx.x) % steps : 0;  // the step that a group begins with
+  int load_group = group, load_step = rot, load_slot = 0;
   __amdgpu_buffer_rsrc_t wb = rows_buffer(a.wq, (int64_t)min(group, n_group - 1) * 16, a.N, a.wq_stride, a.H);
   // the next step; behind the last one, the last group's rows again, which no one reads
   auto load = [&]() __attribute__((always_inline)) {
     load_to_lds16(wb, wo, load_step * 128, ring + load_slot * 2048);
     load_to_lds16(wb, wo, load_step * 128 + 8 * w_stride, ring + load_slot * 2048 + 1024);
     load_slot = load_slot + 1 == D ? 0 : load_slot + 1;
-    if (++load_step == steps) {
-      load_step = 0;
+    if (++load_step == steps) load_step = 0;
+    if (load_step == rot) {
       load_group += stride;
       if (load_group < n_group) wb = rows_buffer(a.wq, (int64_t)load_group * 16, a.N, a.wq_stride, a.H);
     }
@@ -224,7 +237,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
   }
   typedef const float __attribute__((address_space(4))) * Scales;
   const Scales ws = (Scales)(uintptr_t)a.ws;
-  int step = 0, slot = 0;
+  int step = rot, slot = 0;
 #pragma unroll 1
   for (int q = 0; q < total; ++q) {
     asm volatile("" ::: "memory");
@@ -243,8 +256,8 @@ __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[ks], xv[ks][m], acc[m], 0, 0, 0);
     slot = slot + 1 == D ? 0 : slot + 1;
-    if (++step < steps) continue;
-    step = 0;
+    if (++step == steps) step = 0;
+    if (step != rot) continue;
     const int ch = group * 16 + g4 * 4;
     // the channels' scales through scalar loads: a vector load's wait would drain the ring
     float sc[4];
@@ -299,7 +312,11 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, const v4i32 (&ac
 template <int DT, int MT, int XBYTES>
 hipError_t run_stream(const LinearArgs& a, hipStream_t st) {
   const int want = ((a.N + 15) / 16 + 7) / 8;  // a block a CU, or fewer if the channels do not give each wave some
-  launch(linear_stream_kernel<DT, MT, XBYTES>, dim3((unsigned)(want < 256 ? want : 256)), dim3(512), st, a);
+  const dim3 grid((unsigned)(want < 256 ? want : 256)), block(512);
+  if (shifted(a))
+    launch(linear_stream_kernel<DT, MT, XBYTES, true>, grid, block, st, a);
+  else
+    launch(linear_stream_kernel<DT, MT, XBYTES, false>, grid, block, st, a);
   return hipGetLastError();
 }
 
@@ -315,18 +332,24 @@ hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
 // into a ring of NB in LDS, eight lanes to a row's cache line.  (Loading the
 // weights straight into the operand's registers puts neighbouring lanes in different
 // rows: 38 bytes a nanosecond and CU against 125 this way, 100 with 64 bytes of a
-// row; 1152 x 4096 x 262144 took 1490 us so, 1280 with stages of 64 bytes, 1250 with these.)
+// row; 1152 x 4096 x 262144 took 1490 us so, 1234 with stages of 64 bytes, 1202 with these.)
 // A stage in LDS: rows of 128 bytes, piece c of row r at place c ^ (r % 8), so that the
 // eight rows that are read at once lie in different banks.  The channels' rows are
 // dealt out so that a lane ends up with 16 neighbouring channels: row i of tile c is
 // channel 16 (i / 4) + 4 c + i % 4.
+// Rows that all begin in the same places of memory: few row tiles begin with a stage of
+// their own, where the tokens fit into half an XCD's L2 (64 x 65536 x 8192: 97 us, 132 all
+// with the first; 2048 x 65536 x 4096, tokens of 8 MiB: 560, 510).
 // A stage is waited for late in the one before it, at a barrier of its own, so that
 // the operands it begins with are read before it begins and the loads of the stages
-// behind it stay in flight.  What bounds it: the clock, which the card lowers to 1.5
-// to 1.7 GHz under this load (a stage of 256 tokens takes 1.4 times its products' cycles).
+// behind it stay in flight.  What bounds it: with many tokens a stage's LDS traffic and
+// its products each take half of its time, at a clock that the load pulls down to 2.0 GHz
+// (1152 x 4096 x 262144: 2060 TOP/s, the matrix cores busy for 51 %); with fewer, that 594 tiles
+// of 151936 channels make three rounds of 256 CUs (128 tokens: 87 us, 256: 112, the bytes 50
+// and 57).
 constexpr int kTileCh = 256;
 
-template <int DT, int TT>
+template <int DT, int TT, bool SHIFT>
 __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n_rt, int n_ct) {
   constexpr int BM = 32 * TT, SB = (kTileCh + BM) * 128, NB = 163840 / SB, G = TT / 2;
   constexpr int PER = (kTileCh + BM) / 64;  // a wave's loads a stage, 8 rows each
@@ -352,8 +375,12 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
   const int wo = ((lane >> 5) * 16 + (lane >> 3 & 3)) * w_stride + piece;
   const int xo = (lane >> 3) * x_stride + piece;
   const int chw = min(ct * kTileCh + (wave >> 1) * 64, a.N - 64) - chb;
+  // where the row's stage number s lies
+  const int rot = SHIFT ? (ct >> 3) * 5 % n_st : 0;
+  auto place = [&](int s) __attribute__((always_inline)) { return !SHIFT ? s : s + rot < n_st ? s + rot : s + rot - n_st; };
   // the wave's i-th load of stage s
   auto load = [&](int s, int buf, int i) __attribute__((always_inline)) {
+    s = place(s);
     unsigned char* to = lds + buf * SB;
     if (i < 4) {  // rows 8 (j % 2) .. of tile j / 2 of 64 channels, a pair of waves each
       const int j = (wave & 1) * 4 + i;
@@ -401,7 +428,7 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
   asm volatile("" ::: "memory");
   wait_loads<PER * (NB - 2)>();
   barrier();
-  clear(0, 0);
+  clear(place(0), 0);
 #pragma unroll
   for (int c = 0; c < 4; ++c) wv[0][c] = *reinterpret_cast<const v4i32*>(wf + c * 2048 + fo[0]);
 #pragma unroll
@@ -421,7 +448,7 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
         asm volatile("" ::: "memory");
         wait_loads<PER * (NB - 2)>();  // stage s + 1 has landed, and stage s is read
         barrier();
-        if (s + 1 < n_st) clear(s + 1, next);
+        if (s + 1 < n_st) clear(place(s + 1), next);
       }
       const unsigned char* from = g + 1 < 2 * G ? xf + buf * SB + ((g + 1) % G) * 4096 + fo[(g + 1) / G % 2] : xf + next * SB + fo[0];
 #pragma unroll
@@ -454,7 +481,11 @@ template <int DT, int TT>
 hipError_t run_tile(const LinearArgs& a, hipStream_t st) {
   const int n_ct = (a.N + kTileCh - 1) / kTileCh;
   const int n_rt = (int)((a.R + 32 * TT - 1) / (32 * TT));
-  launch(linear_tile_kernel<DT, TT>, dim3((unsigned)((int64_t)((n_ct + 7) / 8) * 8 * n_rt)), dim3(512), st, a, n_rt, n_ct);
+  const dim3 grid((unsigned)((int64_t)((n_ct + 7) / 8) * 8 * n_rt)), block(512);
+  if (shifted(a) && a.R * a.H <= (1 << 21))
+    launch(linear_tile_kernel<DT, TT, true>, grid, block, st, a, n_rt, n_ct);
+  else
+    launch(linear_tile_kernel<DT, TT, false>, grid, block, st, a, n_rt, n_ct);
   return hipGetLastError();
 }
 
@@ -470,8 +501,10 @@ constexpr int kStreamBytes = 98304;
 int stream_bytes(int tiles, int32_t H) { return tiles * 16 * ((H + 127) / 128 * 128); }
 
 // The streaming kernel wherever its tokens fit and the channels give half of its waves
-// 16; else the least of the others' times in nanoseconds, fitted to them over 322
-// shapes from 1 x 100 x 64 to 2048 x 151936 x 512.  The few-tokens kernel: a start, and
+// 16 (with cold weights within 20 % of the best of 159 shapes: 16 x 24000 x 1024: 10 us, the
+// few-tokens kernel 8.5; 16 x 151936 x 512: 18, tiles 24); else the least of the others' times
+// in nanoseconds, fitted to them over 405 shapes from 1 x 100 x 64 to 2048 x 151936 x 512 (1.3 %
+// above the best one on average, 18 % at most but for 1152 x 151936 x 64, all output).  The few-tokens kernel: a start, and
 // the most of a round trip to memory for every eight steps of a wave, its loads at 38
 // bytes a CU, and what a block costs.  The tiles: a start, and rounds of 256 blocks at a time a stage
 // that grows with the tile, or the weights at half of the memory's rate (a quarter of

@@ -165,6 +165,16 @@ def test_linear_few_tokens_many_channels(dt, R, N, H):
     check_linear(R, N, H, dt, seed=R + N, gaps=(16 * (H % 2), 16 * (N % 2)), pad=N % 3, shift=R % 4)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("R,N,H,pitch", [(1, 17000, 4001, 4096), (20, 40000, 4096, 4096), (40, 16500, 900, 4096), (64, 5003, 4001, 4096),
+                                         (200, 9001, 4001, 4096), (256, 17001, 4096, 4096), (512, 4999, 4001, 4096), (64, 9000, 8100, 8192),
+                                         (130, 20011, 100, 4096)])
+def test_weights_a_multiple_of_4096_apart(dt, R, N, H, pitch):
+    # blocks begin in other places of k there
+    _say(f"[i8] linear {dt} {R} x {N} x {H}, weights {pitch} apart")
+    check_linear(R, N, H, dt, seed=R + N, gaps=(16, pitch - -(-H // 16) * 16), pad=N % 3)
+
+
 def test_linear_special_scales():
     R, N = 20, 40
     xs, ws = np.ones(R), np.ones(N)
