@@ -486,6 +486,8 @@ __device__ __forceinline__ void write_row(Shared<T>& sh, const LogprobsArgs& a, 
 }
 
 // One row, or one segment of it, a block: streams it once.
+// Eight waves a SIMD hide the loads, four of which a thread has in flight; bound by issue
+// slots with the entropy (2048 x 151936 bf16: 116 us, 5.4 TB/s; a read alone reaches 7.0).
 template <int DT, int T, int U, bool ENT, bool TOP>
 __global__ __launch_bounds__(T, 8) void logprobs_kernel(LogprobsArgs a, LogprobsOut o, int n_seg, int seg_slots,
                                                      LogprobsPart* __restrict__ parts, uint64_t* __restrict__ lists) {
@@ -576,7 +578,8 @@ struct GradRed {
 
 // dz_j = p_j (a0 + a1 log2 p_j) + (the given token's own gradients) / T, with
 //   a0 = -(sum g + g_H H) / T,  a1 = -g_H ln 2 / T.
-// One read and one write of the row.
+// One read and one write of the row, NL slots a thread as in the distillation's gradient.
+// Bound by memory: 2048 x 151936 bf16 in 217 us, 5.75 TB/s.
 template <int DT, int NL>
 __global__ __launch_bounds__(kLogprobsThreads) void logprobs_grad_kernel(LogprobsArgs a, const float* __restrict__ g_logp,
                                                                          const float* __restrict__ g_ent,

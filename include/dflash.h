@@ -523,8 +523,12 @@ dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K
  * nothing unmasked has log p -inf, H 0 and norm (-inf, 0).  A row with a NaN or
  * +inf logit has NaN throughout, its alternatives -1 (padding stays 0).  Finite
  * lowest values are logits like any other.
- * Precision: l, log p and H are right to 2^-21 and 2^-23 of their size (the sums'
- * terms to 2^-22, added in fp32 up to 32 at a time and in fp64 beyond). */
+ * Precision: with t the exponent of two of a term over the largest one (|t| at most
+ * log2 V + 1/2 on average over p), a term is right to (1.04 |t| + 12) 2^-24 of itself; l
+ * and log p to its average over p (2.1e-6 at most), H to that of its product with |log p + H|
+ * and 7.7 |t| 2^-24; each is rounded once.  The alternatives' order is exact.
+ * One launch, or two with ws (dflash_rows_workspace_bytes); may be captured into a HIP
+ * graph; repeated calls give the same bits. */
 dflash_status dflash_logprobs(const dflash_rows* r, const void* Z, const float* T_opt, int32_t group, int32_t M,
                               const int32_t* tok, float* logp, float* norm, float* entropy_opt, int32_t N,
                               int32_t* top_idx, float* top_logp, void* ws, size_t ws_bytes, void* stream);
