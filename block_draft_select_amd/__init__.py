@@ -372,11 +372,13 @@ def _row_tensor(t, name, r, device, stride=None):
     stride it must have)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() == 2 and t.stride(1) == 1 and t.shape[0] > 1:  # the usual case without the walk over dimensions
-        own_R, own_V, own_stride, own_dtype = t.shape[0], t.shape[1], t.stride(0), _ROWS_DTYPE.get(t.dtype)
-    else:
-        own = rows(t)
-        own_R, own_V, own_stride, own_dtype = own.R, own.V, own.stride, own.dtype
+    if t.dim() == 2:  # the usual case without the walk over dimensions
+        (n, V), (st, step) = t.shape, t.stride()
+        if (step == 1 and n == r.R and V == r.V and n > 0 and (n == 1 or stride is None or st == stride)
+                and _ROWS_DTYPE.get(t.dtype) == r.dtype and t.get_device() == device.index):
+            return t.data_ptr(), st if n > 1 else V
+    own = rows(t)
+    own_R, own_V, own_stride, own_dtype = own.R, own.V, own.stride, own.dtype
     if own_R != r.R or own_V != r.V or own_dtype != r.dtype:
         raise ValueError(f"{name} must hold {r.R} rows of {r.V} logits of the rows' dtype")
     if stride is not None and own_R > 1 and own_stride != stride:
@@ -403,21 +405,31 @@ def _vec(t, name, dtype, numel, device, optional=False):
     _on(t, name, device)
 
 
+# the current stream's handle without the stream object around it, which takes 1 us of a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call(fn, device, stream, *args):
     """Call an entry point on ``stream`` (None: the current stream of the
     tensors' device), with that device current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device.index)
+        raw = _raw_stream(device.index)
     elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the rows are on {device}")
+    else:
+        raw = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream.cuda_stream))
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream))
+            status = fn(*args, raw)
+    if status:
+        _check(status)
 
 
 def _groups(r, group):
+    if group == 1 and type(group) is int:
+        return 1, r.R
     group = operator.index(group)  # the arrays' lengths are checked against it: neither rounded nor wrapped
     if not 1 <= group < 1 << 31:
         raise ValueError(f"group must lie in [1, 2^31), got {group}")
