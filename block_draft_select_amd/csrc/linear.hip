@@ -92,8 +92,8 @@ bool shifted(const LinearArgs& a) { return a.wq_stride % 4096 == 0; }
 // Few tokens: 16 channels and 16 MT tokens a block, its four waves split k.
 // Each wave has eight steps of 64 bytes in flight.  The operands go straight to registers,
 // neighbouring lanes in different rows: at 30 to 40 bytes a nanosecond and CU that is the
-// slowest way to read, but the one that starts first (1 x 2048 x 2048: 7 us of call, the
-// kernel 3; 1 x 65536 x 8192 with one round after another: 96 us, 5.6 TB/s).
+// slowest way to read, but the one that starts first (1 x 2048 x 2048: the 6.5 us of host
+// time that a call takes; 1 x 65536 x 8192, one round of blocks after another: 96 us, 5.6 TB/s).
 template <int DT, int MT>
 __global__ __launch_bounds__(256) void linear_few_kernel(LinearArgs a) {
   constexpr int U = 8;
