@@ -342,7 +342,9 @@ hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
 // with the first; 2048 x 65536 x 4096, tokens of 8 MiB: 560, 510).
 // A stage is waited for late in the one before it, at a barrier of its own, so that
 // the operands it begins with are read before it begins and the loads of the stages
-// behind it stay in flight.  What bounds it: with many tokens a stage's LDS traffic and
+// behind it stay in flight.  By then its own rows are read too: the ring of two takes the
+// weights of the stage after next into their place at once (1152 x 4096 x 262144: 1220 us,
+// 1255 with all loads a little later; rings of three and four lose 2 %).  What bounds it: with many tokens a stage's LDS traffic and
 // its products each take half of its time, at a clock that the load pulls down to 2.0 GHz
 // (1152 x 4096 x 262144: 2060 TOP/s, the matrix cores busy for 51 %); with fewer, that 594 tiles
 // of 151936 channels make three rounds of 256 CUs (128 tokens: 87 us, 256: 112, the bytes 50
@@ -353,6 +355,7 @@ template <int DT, int TT, bool SHIFT>
 __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n_rt, int n_ct) {
   constexpr int BM = 32 * TT, SB = (kTileCh + BM) * 128, NB = 163840 / SB, G = TT / 2;
   constexpr int PER = (kTileCh + BM) / 64;  // a wave's loads a stage, 8 rows each
+  constexpr int E = NB == 2 ? 4 : 0;  // loads that go out behind the stage's own barrier, into its place
   static_assert(NB >= 2, "a stage in use, one landing");
   constexpr int LG = NB == 2 ? (2 * G + 3) / 4 : 2 * G - 1;  // groups that bring loads: early ones if they have to land in this stage
   __shared__ __attribute__((aligned(1024))) unsigned char lds[NB * SB];
@@ -425,8 +428,10 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
 #pragma unroll
     for (int i = 0; i < PER; ++i) load(s, s, i);
   }
+#pragma unroll
+  for (int i = 0; i < E; ++i) load(NB - 1, NB - 1, i);
   asm volatile("" ::: "memory");
-  wait_loads<PER * (NB - 2)>();
+  wait_loads<PER * (NB - 2) + E>();
   barrier();
   clear(place(0), 0);
 #pragma unroll
@@ -449,6 +454,8 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
         wait_loads<PER * (NB - 2)>();  // stage s + 1 has landed, and stage s is read
         barrier();
         if (s + 1 < n_st) clear(place(s + 1), next);
+#pragma unroll
+        for (int i = 0; i < E; ++i) load(s + NB, buf, i);
       }
       const unsigned char* from = g + 1 < 2 * G ? xf + buf * SB + ((g + 1) % G) * 4096 + fo[(g + 1) / G % 2] : xf + next * SB + fo[0];
 #pragma unroll
@@ -462,8 +469,8 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
         for (int c = 0; c < 4; ++c) wv[0][c] = *reinterpret_cast<const v4i32*>(wf + next * SB + c * 2048 + fo[0]);
       }
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i * LG / PER == g) load(s + NB - 1, refill, i);
+      for (int i = E; i < PER; ++i)
+        if ((i - E) * LG / PER == g) load(s + NB - 1, refill, i);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
