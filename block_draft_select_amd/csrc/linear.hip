@@ -332,7 +332,7 @@ hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
 // into a ring of NB in LDS, eight lanes to a row's cache line.  (Loading the
 // weights straight into the operand's registers puts neighbouring lanes in different
 // rows: 38 bytes a nanosecond and CU against 125 this way, 100 with 64 bytes of a
-// row; 1152 x 4096 x 262144 took 1490 us so, 1234 with stages of 64 bytes, 1202 with these.)
+// row; 1152 x 4096 x 262144 took 1490 us so, 1234 with stages of 64 bytes.)
 // A stage in LDS: rows of 128 bytes, piece c of row r at place c ^ (r % 8), so that the
 // eight rows that are read at once lie in different banks.  The channels' rows are
 // dealt out so that a lane ends up with 16 neighbouring channels: row i of tile c is
@@ -343,12 +343,12 @@ hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
 // A stage is waited for late in the one before it, at a barrier of its own, so that
 // the operands it begins with are read before it begins and the loads of the stages
 // behind it stay in flight.  By then its own rows are read too: the ring of two takes the
-// weights of the stage after next into their place at once (1152 x 4096 x 262144: 1220 us,
-// 1255 with all loads a little later; rings of three and four lose 2 %).  What bounds it: with many tokens a stage's LDS traffic and
-// its products each take half of its time, at a clock that the load pulls down to 2.0 GHz
-// (1152 x 4096 x 262144: 2060 TOP/s, the matrix cores busy for 51 %); with fewer, that 594 tiles
-// of 151936 channels make three rounds of 256 CUs (128 tokens: 87 us, 256: 112, the bytes 50
-// and 57).
+// weights of the stage after next into their place at once (1152 x 4096 x 262144: 1134 us,
+// 1202 with all loads a little later; rings of three and four lose 2 % by it).
+// What bounds it: with many tokens a stage's LDS traffic and its products each take 0.6
+// of its time, at a clock that the load pulls down to 2.0 GHz (1152 x 4096 x 262144: 2180
+// TOP/s, the matrix cores busy for 59 %); with fewer, that 594 tiles of 151936 channels make
+// three rounds of 256 CUs (128 tokens: 87 us, 256: 111, the bytes 50 and 57).
 constexpr int kTileCh = 256;
 
 template <int DT, int TT, bool SHIFT>
