@@ -494,6 +494,16 @@ bool meet(const void* a, uintptr_t na, const void* b, uintptr_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// whether rows of logits share memory with one of these arrays (those that are NULL have none)
+struct Small { const void* p; int64_t bytes; };
+bool rows_meet(const dflash_rows& r, const void* Z, int64_t stride, std::initializer_list<Small> others) {
+  const int64_t es = (int64_t)logit_bytes(r.dtype);
+  const uintptr_t n = span(r.R, stride * es, r.V * es);
+  for (const Small& o : others)
+    if (o.p && o.bytes > 0 && meet(Z, n, o.p, (uintptr_t)o.bytes)) return true;
+  return false;
+}
+
 // an array of `rows` 8-bit rows of H values
 dflash_status check_i8(const void* p, int64_t rows, int64_t stride, int64_t H, const char* name) {
   if (rows > 1 && (stride < H || stride % 16))
@@ -1011,6 +1021,9 @@ dflash_status dflash_logprobs(const dflash_rows* r, const void* Z, const float* 
     const dfk::LogprobsPlan p = dfk::logprobs_plan(*r, N);
     if (p.total > 0)
       if (dflash_status s = check_rows_ws(p.total, ws, ws_bytes)) return s;
+    if (rows_meet(*r, Z, r->stride, {{logp, r->R * M * 4}, {norm, r->R * 8}, {entropy_opt, r->R * 4}, {top_idx, r->R * N * 4},
+                                     {top_logp, r->R * N * 4}}))
+      return fail(DFLASH_ERR_INVALID_ARG, "an output overlaps Z");
     hipStream_t st = (hipStream_t)stream;
     const dfk::LogprobsArgs a{Z, r->R, r->stride, r->V, group, T_opt, M, N, tok};
     const dfk::LogprobsOut o{logp, norm, entropy_opt, top_idx, top_logp};
@@ -1033,6 +1046,9 @@ dflash_status dflash_logprobs_grad(const dflash_rows* r, const void* Z, const fl
     if (r->R == 0) return DFLASH_OK;
     if (grad_entropy_opt && !entropy_opt) return fail(DFLASH_ERR_INVALID_ARG, "grad_entropy needs entropy");
     if (dflash_status s = check_out(*r, Z, dZ, dz_stride, "dZ")) return s;
+    if (rows_meet(*r, dZ, dz_stride, {{T_opt, ((r->R - 1) / group + 1) * 4}, {tok, r->R * M * 4}, {grad_logp, r->R * M * 4},
+                                      {grad_entropy_opt, r->R * 4}, {norm, r->R * 8}, {entropy_opt, r->R * 4}}))
+      return fail(DFLASH_ERR_INVALID_ARG, "dZ overlaps an input");
     hipStream_t st = (hipStream_t)stream;
     const dfk::LogprobsArgs a{Z, r->R, r->stride, r->V, group, T_opt, M, 0, tok};
     return hip_status(timed(DFLASH_KERNEL_LOGPROBS_GRAD, st, [&] {

@@ -527,6 +527,7 @@ dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K
  * log2 V + 1/2 on average over p), a term is right to (1.04 |t| + 12) 2^-24 of itself; l
  * and log p to its average over p (2.1e-6 at most), H to that of its product with |log p + H|
  * and 7.7 |t| 2^-24; each is rounded once.  The alternatives' order is exact.
+ * Z is read only and must not overlap an output.
  * One launch, or two with ws (dflash_rows_workspace_bytes); may be captured into a HIP
  * graph; repeated calls give the same bits. */
 dflash_status dflash_logprobs(const dflash_rows* r, const void* Z, const float* T_opt, int32_t group, int32_t M,
@@ -541,7 +542,7 @@ dflash_status dflash_logprobs(const dflash_rows* r, const void* Z, const float* 
  *   grad_entropy [R] float or NULL (zeros)
  *   dZ           [R, V] in Z's type with its own row stride, written whole; may
  *                be Z itself (same address and stride), and must not overlap it
- *                otherwise
+ *                otherwise, nor the other arrays
  * A row whose incoming gradients are all 0, or with nothing unmasked, gets zeros
  * (its Z counts for nothing); a row with NaN in norm gets NaN.
  * Precision: p_j is right to (|log2 p_j| + 4) 2^-23 of itself (below 2^-126: 0); a

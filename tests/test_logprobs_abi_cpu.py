@@ -88,6 +88,21 @@ def test_overlapping_gradients_are_refused(dfl):
         assert b"overlaps" in dfl.lib.dflash_last_error()
 
 
+@pytest.mark.parametrize("at", [0, 100, 3 * 240 - 42, -4])
+def test_outputs_over_their_rows_are_refused(dfl, at):
+    # 3 rows of 100 bf16 logits, 240 bytes apart: 680 bytes
+    r = _rows(dfl, R=3, stride=120, V=100)
+    rows_, there, away = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100000 + at), ctypes.c_void_p(0x7000000000)
+    out = dict(Z=rows_, tok=away, logp=away, norm=away, top=away, top_logp=away)
+    for name in ("logp", "norm", "ent", "top", "top_logp"):
+        assert _fwd(dfl, r, **{**out, name: there}) == 1, name
+        assert b"overlaps Z" in dfl.lib.dflash_last_error()
+    given = dict(Z=away, dZ=rows_, stride=120, tok=away, g=away, norm=away, ge=away, ent=away)
+    for name in ("T", "tok", "g", "norm", "ge", "ent"):
+        assert _grad(dfl, r, **{**given, name: there}) == 1, name
+        assert b"dZ overlaps" in dfl.lib.dflash_last_error()
+
+
 def test_empty_calls_launch_nothing(dfl):
     r = _rows(dfl, R=0)
     assert _fwd(dfl, r, Z=None, tok=None, logp=None, norm=None, top=None, top_logp=None, ws=None, n=0) == 0
