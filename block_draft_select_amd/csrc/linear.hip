@@ -293,7 +293,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
 
 // A wave's 64 channels from ch on of 16 TT tokens from row on, by way of 16 rows of LDS of its
 // own: neighbouring lanes then write one row's line (16 rows' pieces of 16 bytes in an
-// instruction, as the products leave them, write 2.5 TB/s).
+// instruction, as the products leave them, take 82 us at 1883 x 64 x 53594, these 72).
 // All scales are here before the first store: a load between stores waits for them.
 template <int DT, int TT>
 __device__ __forceinline__ void store_tile(const LinearArgs& a, const v4i32 (&acc)[TT][4], int ch, int64_t row, unsigned char* buf) {
@@ -365,9 +365,9 @@ hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
 // weights of the stage after next into their place at once (1152 x 4096 x 262144: 1134 us,
 // 1202 with all loads a little later; rings of three and four lose 2 % by it).
 // What bounds it: with many tokens a stage's LDS traffic and its products each take 0.6
-// of its time, at a clock that the load pulls down to 2.0 GHz (1152 x 4096 x 262144: 2180
-// TOP/s, the matrix cores busy for 59 %); with fewer, that 594 tiles of 151936 channels make
-// three rounds of 256 CUs (128 tokens: 87 us, 256: 111, the bytes 50 and 57).
+// of its time, at a clock that the load pulls down to 1.9 GHz (1152 x 4096 x 262144: 1103 us,
+// 2245 TOP/s, the matrix cores busy for 62 %); with fewer, that 594 tiles of 151936 channels
+// make three rounds of 256 CUs (128 tokens: 86 us, 256: 110, the bytes 50 and 57).
 constexpr int kTileCh = 256;
 
 template <int DT, int TT, bool SHIFT>
