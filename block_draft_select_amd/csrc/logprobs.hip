@@ -634,33 +634,45 @@ __global__ __launch_bounds__(kLogprobsThreads) void logprobs_grad_kernel(Logprob
 #pragma unroll
   for (int q = 0; q < NL; ++q) x[q] = z.template load<true>(s0 + q * T + tid);
   const double H = g_ent ? (double)entropy[row] : 0.0;
-  double a0 = -(A + gh * H) * per, a1 = -gh * kLn2 * per;
-  if (m != m) a0 = NAN;
-  // factors near fp32's end leave their power of two to the exponent, so that
-  // unlikely tokens' gradients, which fit, do not become inf times 0
-  const double big = fmax(fabs(a0), 256.0 * fabs(a1));
-  const int up = big >= 0x1p100 && big < INFINITY ? ilogb(big) : 0;
-  const float f0 = (float)ldexp(a0, -up), f1 = (float)ldexp(a1, -up), fup = (float)up;
+  const double b0 = m != m ? (double)NAN : -(A + gh * H), a0 = b0 * per, a1 = -gh * kLn2 * per;
   // log2 p in two pieces of fp32 (-inf: NaN at times, which the maximum below replaces)
   const double l2 = (double)l * kLog2e64;
   const float ch = (float)c, cl = (float)(c - (double)ch), lh = (float)l2, ll = (float)(l2 - (double)lh);
   __syncthreads();  // every given token's logit is read (dZ may be Z)
+  auto slots = [&](auto from_t) __attribute__((always_inline)) {
 #pragma unroll
-  for (int q = 0; q < NL; ++q) {
-    Slot y;
+    for (int q = 0; q < NL; ++q) {
+      Slot y;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y.w[k] = 0;
+      for (int k = 0; k < 4; ++k) y.w[k] = 0;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const float d = slot_value<DT>(x[q], i) - m;
-      const float t = fmaxf(fmaf(d, ch, -lh) + fmaf(d, cl, -ll), -256.0f);
-      const float g = __builtin_amdgcn_exp2f(t + fup) * fmaf(f1, t, f0);
-      if constexpr (DT == DFLASH_BF16)
-        y.w[i >> 1] |= bf16_round(g) << ((i & 1) * 16);
-      else
-        y.w[i] = __float_as_uint(g);
+      for (int i = 0; i < VE; ++i) {
+        const float d = slot_value<DT>(x[q], i) - m;
+        const float g = from_t(fmaf(d, ch, -lh) + fmaf(d, cl, -ll));
+        if constexpr (DT == DFLASH_BF16)
+          y.w[i >> 1] |= bf16_round(g) << ((i & 1) * 16);
+        else
+          y.w[i] = __float_as_uint(g);
+      }
+      store_slot<DT>(o, a.V, s0 + q * T + tid, y);
+      __builtin_amdgcn_sched_barrier(0);  // slot by slot: else the two paths below take a block's registers a CU more
     }
-    store_slot<DT>(o, a.V, s0 + q * T + tid, y);
+  };
+  const double big = fmax(fabs(a0), 256.0 * fabs(a1));
+  if (big >= 0x1p60 && big < INFINITY) {
+    // factors that fp32 may not hold are multiplied in fp64, by the power of two of t's whole part
+    // as well: unlikely tokens' gradients may fit fp32, those of masked ones are 0 (a factor is below 2^250)
+    slots([&](float t) {
+      t = fmaxf(t, -1000.0f);
+      const float n = rintf(t);
+      return (float)ldexp((double)__builtin_amdgcn_exp2f(t - n) * fma(a1, (double)t, a0), (int)n);
+    });
+  } else {
+    const float f0 = (float)a0, f1 = (float)a1;
+    slots([&](float t) {
+      t = fmaxf(t, -256.0f);
+      return __builtin_amdgcn_exp2f(t) * fmaf(f1, t, f0);
+    });
   }
   __syncthreads();
 #pragma unroll
@@ -672,8 +684,10 @@ __global__ __launch_bounds__(kLogprobsThreads) void logprobs_grad_kernel(Logprob
         if (tok[q] == tok[k]) g += (double)grad[q];
       const double lp = ((double)own[j] - (double)m) * per - (double)l;
       const double p = exp(lp);
-      const double d = p > 0.0 ? p * (a0 + a1 * kLog2e64 * lp) : m != m ? (double)NAN : 0.0;
-      o[tok[k]] = to_elem<DT>((float)(d + g * per));
+      // all that may cancel comes before 1 / T: a token with p = 1 has exactly 0
+      if (p > 0.0) g += p * (b0 - gh * lp);
+      if (m != m) g = NAN;
+      o[tok[k]] = to_elem<DT>((float)(g * per));
     }
   }
 }

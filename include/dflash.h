@@ -545,7 +545,8 @@ dflash_status dflash_logprobs(const dflash_rows* r, const void* Z, const float* 
  *                otherwise, nor the other arrays
  * A row whose incoming gradients are all 0, or with nothing unmasked, gets zeros
  * (its Z counts for nothing); a row with NaN in norm gets NaN.
- * Precision: p_j is right to (|log2 p_j| + 4) 2^-23 of itself (below 2^-126: 0); a
+ * Precision: p_j is right to (|log2 p_j| + 4) 2^-23 of itself (below 2^-126: 0, unless
+ * the row's factors, the gradients' sum or that of the entropy over T, reach 2^60); a
  * given token's gradient is computed in fp64.  One launch, no workspace, no
  * atomics: repeated calls give the same bits. */
 dflash_status dflash_logprobs_grad(const dflash_rows* r, const void* Z, const float* T_opt, int32_t group, int32_t M,
