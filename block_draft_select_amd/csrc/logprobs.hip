@@ -9,9 +9,9 @@
 // t_j is one fma, right to half a step of itself however large M is, so the
 // terms that count (t near 0) are right to 2^-23; a thread sums 16 or 32 of
 // them in fp32 and adds that to fp64.  M is a whole number, so that a larger
-// one scales the sums exactly.  It is m c rounded, to half a step of fp32: a row
-// with |m| c beyond 2^30, where that step nears fp32's exponents (all of it the
-// type's lowest value, or T below 1e-8), is summed again from z_j - m.
+// one scales the sums exactly: m c rounded, so that no t is above 1/2.  Beyond 2^24
+// fp32 holds no such number: a row with |m| c there (all of it the type's lowest
+// value, or T below 1e-6) is summed again from z_j - m.
 //
 // The alternatives take nothing from the streaming loop but three maxima a
 // thread: of the slots a thread loads at a time (a piece), the two largest maxima
@@ -29,7 +29,7 @@ constexpr double kLn2 = 0.6931471805599453;
 constexpr int kPieces = 512;       // pieces that are read again
 constexpr int kCap = 1024;         // tokens of those that are ranked; of as many lists of the join
 static_assert(kCap >= DFLASH_TOP_MAX * DFLASH_TOP_MAX && kPieces >= kLogprobsMaxSeg, "the join's lists");
-constexpr float kHuge = 0x1p30f;   // |m| c beyond this, whose rounding 2^t may not hold: from z - m
+constexpr float kHuge = 0x1p24f;   // |m| c beyond this, which fp32 does not hold to 1/2: from z - m
 
 // log2 e over a row's temperature, which lies in [1e-30, 1e30]; 0, below or NaN: 1
 __device__ __forceinline__ double row_scale(const float* T, int group, int64_t row) {
@@ -118,7 +118,7 @@ struct Sums {
 };
 
 __device__ __forceinline__ double reference(float m, float c) {
-  return rint((double)fminf(fmaxf(m * c, -kHuge), kHuge));
+  return rint(fmin(fmax((double)m * (double)c, -(double)kHuge), (double)kHuge));
 }
 
 // s and h from reference `from` to a larger one
@@ -403,19 +403,31 @@ __device__ __forceinline__ Sums sum_segment(Shared<T>& sh, const RowRef<DT>& z, 
   return r;
 }
 
-// The sums of a row whose |m| c leaves fp32, from z - m (reference m c): one more pass over the row
+// The sums of a row whose |m| c is beyond kHuge, from z - m (reference m c): one more pass over the
+// row, of which most slots have nothing to add where c is that large (2048 x 151936 bf16 at T =
+// 1e-6: 252 us, 1340 with every exponential, 116 at T = 1; one such row: 22, 190 and 10).
 template <int DT, int T>
 __device__ __noinline__ void sum_far(Shared<T>& sh, const RowRef<DT> z, float m, double c, double& s, double& h) {
-  constexpr int VE = RowType<DT>::VE;
+  constexpr int VE = RowType<DT>::VE, U = 2;
   const int tid = threadIdx.x;
   s = h = 0.0;
-  for (int b = tid; b < z.slots(); b += T) {
-    const Slot x = z.load(b);
+#pragma unroll 1
+  for (int b = tid; b < z.slots(); b += T * U) {
+    Slot x[U];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const double t = fmax(((double)slot_value<DT>(x, i) - (double)m) * c, -2000.0), e = exp2(t);
-      s += e;
-      h = fma(e, t, h);
+    for (int l = 0; l < U; ++l) x[l] = z.load(b + l * T);
+#pragma unroll
+    for (int l = 0; l < U; ++l) {
+      float top = slot_value<DT>(x[l], 0);
+#pragma unroll
+      for (int i = 1; i < VE; ++i) top = fmaxf(top, slot_value<DT>(x[l], i));
+      if (!(((double)top - (double)m) * c > -1100.0)) continue;  // 2^t is 0
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const double t = fmax(((double)slot_value<DT>(x[l], i) - (double)m) * c, -2000.0), e = exp2(t);
+        s += e;
+        h = fma(e, t, h);
+      }
     }
   }
   s = wave_sum_dpp_f64(s);

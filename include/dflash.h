@@ -526,7 +526,8 @@ dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K
  * Precision: with t the exponent of two of a term over the largest one (|t| at most
  * log2 V + 1/2 on average over p), a term is right to (1.04 |t| + 12) 2^-24 of itself; l
  * and log p to its average over p (2.1e-6 at most), H to that of its product with |log p + H|
- * and 7.7 |t| 2^-24; each is rounded once.  The alternatives' order is exact.
+ * and 7.7 |t| 2^-24; each is rounded once.  The alternatives' order is exact.  A row whose
+ * |m| log2 e / T reaches 2^24 (T of 1e-6 and less, or m a type's lowest value) is read twice.
  * Z is read only and must not overlap an output.
  * One launch, or two with ws (dflash_rows_workspace_bytes); may be captured into a HIP
  * graph; repeated calls give the same bits. */
