@@ -8,6 +8,7 @@
 // cleared past the row's end: what the weights hold there is multiplied by zero.
 #include <algorithm>
 
+#include "linear_loads.hpp"
 #include "rows_blocks.hpp"
 
 namespace dfk {
@@ -60,18 +61,15 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// An array of 8-bit rows from `row` on as a buffer: loads behind its end give 0,
-// so neither rows nor pieces of k need a clamp (strides are at most 2^22, and a
-// block reaches over 256 rows)
+// An array of 8-bit rows from `row` on as a buffer
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const int8_t* p, int64_t row, int64_t rows, int64_t stride, int H) {
-  const int64_t bytes = min(rows - 1 - row, (int64_t)255) * stride + (H + 15) / 16 * 16;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p) + row * stride, 0, (int)bytes, 0x00027000);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p) + row * stride, 0, buffer_bytes(row, rows, stride, H), 0x00027000);
 }
 
 // 16 bytes a lane from a buffer straight into LDS, at 16 l past the wave's address
-__device__ __forceinline__ void load_to_lds16(__amdgpu_buffer_rsrc_t b, int lane_offset, int offset, unsigned char* l) {
+__device__ __forceinline__ void load_to_lds16(__amdgpu_buffer_rsrc_t b, int offset, unsigned char* l) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, l, 16, lane_offset, offset, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, l, 16, offset, 0, 0, 0);
 #endif
 }
 
@@ -177,7 +175,7 @@ hipError_t run_few(const LinearArgs& a, hipStream_t st) {
 // a read reaches), 59 for 16, 64 for 32, where the tiles below take 66, 69 and 72.
 template <int DT, int MT, int XBYTES, bool SHIFT>
 __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
-  constexpr int D = (163840 - XBYTES) / 8 / 2048;  // steps in a wave's ring
+  constexpr int D = (kLdsBytes - XBYTES) / 8 / 2048;  // steps in a wave's ring
   __shared__ __attribute__((aligned(1024))) unsigned char lds[XBYTES + 8 * D * 2048];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int steps = (a.H + 127) / 128, pitch = steps * 128;
@@ -187,14 +185,14 @@ __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
 
   unsigned char* ring = lds + XBYTES + wave * (D * 2048);
   const int w_stride = (int)a.wq_stride;
-  const int wo = (lane >> 3) * w_stride + ((lane & 7) ^ (lane >> 3)) * 16;
+  const int wo[2] = {stream_channel(lane, 0) * w_stride + load_piece(lane), stream_channel(lane, 1) * w_stride + load_piece(lane)};
   const int rot = SHIFT ? (wave * 3 + (int)blockIdx.x) % steps : 0;  // the step that a group begins with
   int load_group = group, load_step = rot, load_slot = 0;
   __amdgpu_buffer_rsrc_t wb = rows_buffer(a.wq, (int64_t)min(group, n_group - 1) * 16, a.N, a.wq_stride, a.H);
   // the next step; behind the last one, the last group's rows again, which no one reads
   auto load = [&]() __attribute__((always_inline)) {
-    load_to_lds16(wb, wo, load_step * 128, ring + load_slot * 2048);
-    load_to_lds16(wb, wo, load_step * 128 + 8 * w_stride, ring + load_slot * 2048 + 1024);
+    load_to_lds16(wb, wo[0] + load_step * 128, ring + load_slot * 2048);
+    load_to_lds16(wb, wo[1] + load_step * 128, ring + load_slot * 2048 + 1024);
     load_slot = load_slot + 1 == D ? 0 : load_slot + 1;
     if (++load_step == steps) load_step = 0;
     if (load_step == rot) {
@@ -368,14 +366,11 @@ hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
 // of its time, at a clock that the load pulls down to 1.9 GHz (1152 x 4096 x 262144: 1103 us,
 // 2245 TOP/s, the matrix cores busy for 62 %); with fewer, that 594 tiles of 151936 channels
 // make three rounds of 256 CUs (128 tokens: 86 us, 256: 110, the bytes 50 and 57).
-constexpr int kTileCh = 256;
-
 template <int DT, int TT, bool SHIFT>
 __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n_rt, int n_ct) {
-  constexpr int BM = 32 * TT, SB = (kTileCh + BM) * 128, NB = 163840 / SB, G = TT / 2;
-  constexpr int PER = (kTileCh + BM) / 64;  // a wave's loads a stage, 8 rows each
+  using L = TileLoads<TT>;
+  constexpr int BM = L::BM, SB = L::SB, NB = L::NB, PER = L::PER, G = TT / 2;
   constexpr int E = NB == 2 ? 4 : 0;  // loads that go out behind the stage's own barrier, into its place
-  static_assert(NB >= 2, "a stage in use, one landing");
   constexpr int LG = NB == 2 ? (2 * G + 3) / 4 : 2 * G - 1;  // groups that bring loads: early ones if they have to land in this stage
   __shared__ __attribute__((aligned(1024))) unsigned char lds[NB * SB];
   // ids with the same value mod 8 run on one XCD: the row tiles of a channel tile follow one another there
@@ -393,24 +388,17 @@ __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n
   const int w_stride = (int)a.wq_stride, x_stride = (int)a.xq_stride;
   const __amdgpu_buffer_rsrc_t wb = rows_buffer(a.wq, chb, a.N, a.wq_stride, a.H);
   const __amdgpu_buffer_rsrc_t xb = rows_buffer(a.xq, row0, a.R, a.xq_stride, a.H);
-  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;  // place l % 8 of row l / 8 holds this piece
-  const int wo = ((lane >> 5) * 16 + (lane >> 3 & 3)) * w_stride + piece;
-  const int xo = (lane >> 3) * x_stride + piece;
   const int chw = min(ct * kTileCh + (wave >> 1) * 64, a.N - 64) - chb;
-  // where the row's stage number s lies
+  int lo[PER];  // of the wave's loads, in the first stage
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    lo[i] = (i < 4 ? (chw + tile_channel(wave, lane, i)) * w_stride : tile_token<TT>(wave, lane, i) * x_stride) + load_piece(lane);
   const int rot = SHIFT ? (ct >> 3) * 5 % n_st : 0;
-  auto place = [&](int s) __attribute__((always_inline)) { return !SHIFT ? s : s + rot < n_st ? s + rot : s + rot - n_st; };
+  auto place = [&](int s) __attribute__((always_inline)) { return SHIFT ? tile_stage(s, rot, n_st) : s; };
   // the wave's i-th load of stage s
   auto load = [&](int s, int buf, int i) __attribute__((always_inline)) {
-    s = place(s);
-    unsigned char* to = lds + buf * SB;
-    if (i < 4) {  // rows 8 (j % 2) .. of tile j / 2 of 64 channels, a pair of waves each
-      const int j = (wave & 1) * 4 + i;
-      load_to_lds16(wb, wo, (chw + 32 * (j & 1) + 4 * (j >> 1)) * w_stride + s * 128, to + (wave * 4 + i) * 1024);
-    } else {
-      const int j = wave * (TT / 2) + i - 4;
-      load_to_lds16(xb, xo, 8 * j * x_stride + s * 128, to + (32 + j) * 1024);
-    }
+    unsigned char* to = lds + buf * SB + (i < 4 ? wave * 4 + i : 32 + wave * (TT / 2) + i - 4) * 1024;
+    load_to_lds16(i < 4 ? wb : xb, lo[i] + place(s) * 128, to);
   };
   auto barrier = [&]() __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
