@@ -316,8 +316,10 @@ static int logprobs_units(const dflash_rows& r) { return (row_slots(r) + kLogpro
 // takes every segment 5 us, so with them segments end at 64 rows (100 x 151936: 20 us in
 // one launch, 21 in segments) or at 128 of more than 65536 slots (128 x 600000 fp32: 62,
 // 78), without them later (288 x 151936: 29 and 23).  Rows a little beyond one a CU leave
-// most CUs idle behind the first: three segments a row share them (288 x 151936 bf16 with
-// 20 alternatives and entropies: 31.5 us, 34.5; 360: 35.6, 34.7; fp32, which computes
+// most CUs idle behind the first: three segments a row share them, as long as those are four
+// a CU (bf16 with 20 alternatives and entropies, in segments and in one launch: 257 rows of
+// 131080 28.2 us, 30.6, of 151936 30.0, 33.2, of 600000 73.9, 93.3; 341 rows 30.0, 32.1; 31.9, 34.5;
+// 79.1, 98.3; 341 of 2097152 240, 297; 360 of 151936 35.6, 34.7; 288 of them in fp32, which computes
 // less per byte: 43.8, 41.8).
 LogprobsPlan logprobs_plan(const dflash_rows& r, int N) {
   LogprobsPlan p{};

@@ -272,7 +272,7 @@ constexpr int kLogprobsThreads = 256;
 constexpr int kLogprobsMaxSeg = 256;   // segments of a row: one a thread of the join
 constexpr int kLogprobsBlocks = 2048;  // eight a CU
 struct LogprobsPart {
-  double M, s, h;  // reference (a power of two), sums of 2^t and 2^t t over the segment
+  double M, s, h;  // reference (a whole exponent of two), sums of 2^t and 2^t t over the segment
   float m;         // its largest logit
 };
 struct LogprobsArgs {

@@ -22,10 +22,8 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // NV values to a row of any element-aligned address, each rounded to the type
 template <int DT, int NV>
-__device__ __forceinline__ void store_values(void* y, int64_t at, const float (&v)[NV]) {
-  using E = typename RowType<DT>::elem;
+__device__ __forceinline__ void store_values(typename RowType<DT>::elem* p, const float (&v)[NV]) {
   constexpr int VE = RowType<DT>::VE;
-  E* p = static_cast<E*>(y) + at;
 #pragma unroll
   for (int q = 0; q < NV / VE; ++q) {
     u32x4_any o;
@@ -83,15 +81,15 @@ __device__ __forceinline__ void wait_loads() {
 // Weights whose rows are a multiple of 4096 bytes apart begin in the same memory channels,
 // all of them: blocks that go through k in step then read from a few channels at a time.
 // There each begins at a place of its own (sums of integers have no order); elsewhere
-// that gains nothing, and costs where rows are 2048 bytes apart (1 x 151936 x 2048: 57 us,
-// 53; 1 x 100000 x 4096: 79, 85).
+// that gains nothing, and costs where rows are 2048 bytes apart (1 x 2048 x 151936: 57 us,
+// 53; 1 x 4096 x 100000: 79, 85).
 bool shifted(const LinearArgs& a) { return a.wq_stride % 4096 == 0; }
 
 // Few tokens: 16 channels and 16 MT tokens a block, its four waves split k.
 // Each wave has eight steps of 64 bytes in flight.  The operands go straight to registers,
 // neighbouring lanes in different rows: at 30 to 40 bytes a nanosecond and CU that is the
 // slowest way to read, but the one that starts first (1 x 2048 x 2048: the 6.5 us of host
-// time that a call takes; 1 x 65536 x 8192, one round of blocks after another: 96 us, 5.6 TB/s).
+// time that a call takes; 1 x 8192 x 65536, one round of blocks after another: 96 us, 5.6 TB/s).
 template <int DT, int MT>
 __global__ __launch_bounds__(256) void linear_few_kernel(LinearArgs a) {
   constexpr int U = 8;
@@ -171,7 +169,7 @@ hipError_t run_few(const LinearArgs& a, hipStream_t st) {
 // there, 128 bytes of k a step; no wave waits for another.  Rows of 128 bytes (of
 // the ring) and of whole 128 bytes (of the tokens) hold piece c of row r at place
 // c ^ (r % 8).  What lies behind a token row's end is zero.
-// Bound by the weights' bytes: 2048 x 151936 in 53 us for one token (5.9 TB/s of the 7.0 that
+// Bound by the weights' bytes: 2048 x 151936 in 53.5 us for one token (5.8 TB/s of the 7.0 that
 // a read reaches), 59 for 16, 64 for 32, where the tiles below take 66, 69 and 72.
 template <int DT, int MT, int XBYTES, bool SHIFT>
 __global__ __launch_bounds__(512, 2) void linear_stream_kernel(LinearArgs a) {
@@ -314,7 +312,7 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, const v4i32 (&ac
     float v[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = (float)acc[t][j >> 2][j & 3] * xs[t] * sc[j];
-    store_values<DT>(reinterpret_cast<E*>(put), 0, v);
+    store_values<DT>(reinterpret_cast<E*>(put), v);
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int k = 0; k < 16 / ROWS; ++k) {
@@ -355,17 +353,20 @@ hipError_t run_stream_sized(const LinearArgs& a, int bytes, hipStream_t st) {
 // dealt out so that a lane ends up with 16 neighbouring channels: row i of tile c is
 // channel 16 (i / 4) + 4 c + i % 4.
 // Rows that all begin in the same places of memory: few row tiles begin with a stage of
-// their own, where the tokens fit into half an XCD's L2 (64 x 65536 x 8192: 97 us, 132 all
-// with the first; 2048 x 65536 x 4096, tokens of 8 MiB: 560, 510).
+// their own, where the tokens fit into half an XCD's L2 (64 x 8192 x 65536: 97 us, 132 all
+// with the first; 2048 x 4096 x 65536, tokens of 8 MiB: 560, 510).
 // A stage is waited for late in the one before it, at a barrier of its own, so that
 // the operands it begins with are read before it begins and the loads of the stages
 // behind it stay in flight.  By then its own rows are read too: the ring of two takes the
 // weights of the stage after next into their place at once (1152 x 4096 x 262144: 1134 us,
 // 1202 with all loads a little later; rings of three and four lose 2 % by it).
 // What bounds it: with many tokens a stage's LDS traffic and its products each take 0.6
-// of its time, at a clock that the load pulls down to 1.9 GHz (1152 x 4096 x 262144: 1103 us,
-// 2245 TOP/s, the matrix cores busy for 62 %); with fewer, that 594 tiles of 151936 channels
-// make three rounds of 256 CUs (128 tokens: 86 us, 256: 110, the bytes 50 and 57).
+// of its time, at a clock that the load pulls down to 1.9 GHz (1152 x 4096 x 262144: 1100 to
+// 1130 us, 2190 to 2250 TOP/s, the matrix cores busy for 62 %).  With fewer, a tile's first
+// round trip and its stores, which nothing covers where a block is alone on its CU, and weights at
+// half of the memory's rate (256 tokens of 2048 times 151936 channels: 110 us, the bytes 57;
+// its 1188 tiles of 16 stages are 4.6 rounds of 256 CUs); for 128 tokens also that 594 tiles
+// make three rounds where 2.3 would do (86 us, the bytes 50).
 template <int DT, int TT, bool SHIFT>
 __global__ __launch_bounds__(512, 2) void linear_tile_kernel(LinearArgs a, int n_rt, int n_ct) {
   using L = TileLoads<TT>;
@@ -516,10 +517,10 @@ constexpr int kStreamBytes = 98304;
 int stream_bytes(int tiles, int32_t H) { return tiles * 16 * ((H + 127) / 128 * 128); }
 
 // The streaming kernel wherever its tokens fit and the channels give half of its waves
-// 16 (with cold weights within 20 % of the best of 159 shapes: 16 x 24000 x 1024: 10 us, the
-// few-tokens kernel 8.5; 16 x 151936 x 512: 18, tiles 24); else the least of the others' times
-// in nanoseconds, fitted to them over 405 shapes from 1 x 100 x 64 to 2048 x 151936 x 512 (1.3 %
-// above the best one on average, 18 % at most but for 1152 x 151936 x 64, all output).  The few-tokens kernel: a start, and
+// 16 (with cold weights within 20 % of the best of 159 shapes: 16 x 1024 x 24000: 10 us, the
+// few-tokens kernel 8.5; 16 x 512 x 151936: 18, tiles 24); else the least of the others' times
+// in nanoseconds, fitted to them over 405 shapes from 1 x 64 x 100 to 2048 x 512 x 151936 (1.3 %
+// above the best one on average, 18 % at most but for 1152 x 64 x 151936, all output).  The few-tokens kernel: a start, and
 // the most of a round trip to memory for every eight steps of a wave, its loads at 38
 // bytes a CU, and what a block costs.  The tiles: a start, and rounds of 256 blocks at a time a stage
 // that grows with the tile, or the weights at half of the memory's rate (a quarter of

@@ -87,7 +87,7 @@ __device__ __forceinline__ void store_bytes(int8_t* q, int V, int slot, uint2 b)
   }
 }
 
-// slots past the row's end read as -inf
+// a slot of the row, 0 past its end
 template <int DT>
 __device__ __forceinline__ Slot load_or_zero(const RowRef<DT>& z, int slot) {
   constexpr int VE = RowType<DT>::VE;

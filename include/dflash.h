@@ -593,7 +593,7 @@ typedef struct dflash_linear {
  *   any element-aligned address; it must not overlap the inputs
  * The sum is exact (int32; -128 may occur); it is rounded to fp32, multiplied by
  * xs, then by ws, each rounded to fp32, and rounded to Y's type.  R = 0 is an
- * empty call.  One launch, no workspace; may be captured into a HIP graph. */
+ * empty call; R * N of some 2^39 and more, which no launch holds, is unsupported.  One launch, no workspace; may be captured into a HIP graph. */
 dflash_status dflash_linear_i8(const dflash_linear* d, const int8_t* xq, const float* xs, const int8_t* wq,
                                const float* ws, void* Y, void* stream);
 
