@@ -527,7 +527,7 @@ dflash_status dflash_distill_grad(const dflash_rows* r, const void* S, int32_t K
  * log2 V + 1/2 on average over p), a term is right to (1.04 |t| + 12) 2^-24 of itself; l
  * and log p to its average over p (2.1e-6 at most), H to that of its product with |log p + H|
  * and 7.7 |t| 2^-24; each is rounded once.  The alternatives' order is exact.  A row whose
- * |m| log2 e / T reaches 2^24 (T of 1e-6 and less, or m a type's lowest value) is read twice.
+ * |m| log2 e / T reaches 2^24 (m = 12 at T = 1e-6, or a type's lowest value) is read twice.
  * Z is read only and must not overlap an output.
  * One launch, or two with ws (dflash_rows_workspace_bytes); may be captured into a HIP
  * graph; repeated calls give the same bits. */
@@ -593,7 +593,8 @@ typedef struct dflash_linear {
  *   any element-aligned address; it must not overlap the inputs
  * The sum is exact (int32; -128 may occur); it is rounded to fp32, multiplied by
  * xs, then by ws, each rounded to fp32, and rounded to Y's type.  R = 0 is an
- * empty call; R * N of some 2^39 and more, which no launch holds, is unsupported.  One launch, no workspace; may be captured into a HIP graph. */
+ * empty call; R * N of some 2^39 and more, which no launch holds, is
+ * unsupported.  One launch, no workspace; may be captured into a HIP graph. */
 dflash_status dflash_linear_i8(const dflash_linear* d, const int8_t* xq, const float* xs, const int8_t* wq,
                                const float* ws, void* Y, void* stream);
 
